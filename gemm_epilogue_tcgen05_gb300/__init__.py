@@ -14,7 +14,9 @@ form :func:`fused_linear_gelu_host`), :func:`fused_qkv_rope`,
 the deferred-scale chain :func:`fused_linear_residual_gamma` and
 :func:`fused_linear_rms_rowscale`, :func:`fused_linear_cross_entropy`,
 :func:`fused_linear_quant`, and the backward epilogues
-:func:`fused_dgrad_gelu` and :func:`fused_swiglu_bwd`.
+:func:`fused_dgrad_gelu` and :func:`fused_swiglu_bwd`; for the attention behind
+the QKV projections :func:`paged_kv_append`, :func:`attention_prefill` and
+:func:`attention_decode`.
 """
 from __future__ import annotations
 
@@ -31,7 +33,7 @@ HEADER = os.path.join(ROOT, "include", "fused_linear.h")
 
 FL_OK, FL_ERR_INVALID_ARG, FL_ERR_UNSUPPORTED, FL_ERR_ALIGNMENT, FL_ERR_WORKSPACE, FL_ERR_CUDA, \
     FL_ERR_TIMEOUT, FL_ERR_ARCH = range(8)
-FL_F32, FL_BF16 = 0, 1
+FL_F32, FL_BF16, FL_E4M3 = 0, 1, 2
 FL_GELU_ERF, FL_GELU_TANH = 0, 1
 
 _lib = None
@@ -78,6 +80,16 @@ def load() -> ctypes.CDLL:
     lib.fl_linear_gelu_host_buffer_bytes.restype = SZ
     lib.fused_linear_quant.argtypes = [P, P, P, P, P, P, I, I, I, I64, I64, I64, I64, I, P]
     lib.fused_linear_quant.restype = I
+    lib.paged_kv_append.argtypes = [P] * 11 + [I] * 7 + [I64] * 5 + [I, I, P]
+    lib.paged_kv_append.restype = I
+    lib.attention_decode.argtypes = [P] * 8 + [I] * 7 + [I64] * 5 + [F, I, P, SZ, P]
+    lib.attention_decode.restype = I
+    lib.fl_attention_decode_workspace_bytes.argtypes = []
+    lib.fl_attention_decode_workspace_bytes.restype = SZ
+    lib.attention_prefill.argtypes = [P] * 7 + [I] * 6 + [I64] * 4 + [F, I, I, P, SZ, P]
+    lib.attention_prefill.restype = I
+    lib.fl_attention_prefill_workspace_bytes.argtypes = [I, I, I]
+    lib.fl_attention_prefill_workspace_bytes.restype = SZ
     lib.fl_cross_entropy_workspace_bytes.argtypes = [I, I]
     lib.fl_cross_entropy_workspace_bytes.restype = SZ
     lib.fl_rms_partials_per_row.argtypes = [I]
@@ -550,6 +562,186 @@ def fused_swiglu_bwd(dO, Wd, G, U, dGU=None, stream=None):
     return dGU
 
 
+HEAD_DIM = 128
+
+
+def _kv_rows(t, name, scale, sname):
+    """Checks K or V rows: bf16 without scales, or E4M3 bytes (uint8) with fp32 [rows, n_kv_heads] scales."""
+    if t.dtype == torch.bfloat16:
+        if scale is not None:
+            raise ValueError(f"{sname}: bf16 rows have no scales")
+    elif t.dtype != torch.uint8 or scale is None:
+        raise ValueError(f"{name}: expected bf16 rows, or uint8 (E4M3) rows with {sname}")
+    ld = _mat(t, name, t.dtype)
+    if t.shape[1] % HEAD_DIM != 0:
+        raise ValueError(f"{name}: expected [rows, n_kv_heads * {HEAD_DIM}]")
+    lds = 0
+    if scale is not None:
+        lds = _mat(scale, sname, torch.float32)
+        if tuple(scale.shape) != (t.shape[0], t.shape[1] // HEAD_DIM):
+            raise ValueError(f"{sname}: expected [rows, n_kv_heads]")
+    return ld, lds
+
+
+def _kv_pair(K, V, k_scale, v_scale):
+    ld, lds = _kv_rows(K, "K", k_scale, "k_scale")
+    if V.dtype != K.dtype or V.shape != K.shape or (ld, lds) != _kv_rows(V, "V", v_scale, "v_scale"):
+        raise ValueError("K and V (and their scales) must share type, shape and leading dimension")
+    return ld, lds
+
+
+def _ints(t, name, device):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or (t.numel() > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected a contiguous int32 vector on {device}")
+    return t.numel()
+
+
+def _cache(k_pages, v_pages, page_table, seq_lens, ks, vs):
+    """Checks the paged cache; returns (n_kv_heads, page_size, num_pages, max_pages, ldt, page_pitch, scale_pitch)."""
+    dev, shape = k_pages.device, k_pages.shape
+    if k_pages.dtype not in (torch.bfloat16, torch.uint8) or not k_pages.is_cuda or len(shape) != 4 or \
+            shape[3] != HEAD_DIM:
+        raise ValueError(f"k_pages: expected bf16 or uint8 (E4M3) [num_pages, n_kv_heads, page_size, {HEAD_DIM}]")
+    n_pages, n_kv, page, _ = shape
+    pitch = k_pages.stride(0) if n_pages > 1 else n_kv * page * HEAD_DIM
+    for t in (k_pages, v_pages):
+        if t.dtype != k_pages.dtype or t.shape != shape or t.device != dev:
+            raise ValueError("k_pages and v_pages must share type, shape and device")
+        if n_pages and (t.stride()[1:] != (page * HEAD_DIM, HEAD_DIM, 1) or (n_pages > 1 and t.stride(0) != pitch)):
+            raise ValueError("k_pages and v_pages: expected contiguous pages with one shared pitch")
+    spitch = 0
+    if k_pages.dtype == torch.uint8:
+        if ks is None or vs is None:
+            raise ValueError("an E4M3 cache needs k_page_scale and v_page_scale")
+        spitch = ks.stride(0) if n_pages > 1 else n_kv * page
+        for t in (ks, vs):
+            if t.dtype != torch.float32 or t.shape != shape[:3] or t.device != dev or \
+                    (n_pages and (t.stride()[1:] != (page, 1) or (n_pages > 1 and t.stride(0) != spitch))):
+                raise ValueError("k_page_scale and v_page_scale: expected fp32 [num_pages, n_kv_heads, page_size] "
+                                 "with contiguous pages and one shared pitch")
+    elif ks is not None or vs is not None:
+        raise ValueError("a bf16 cache has no scales")
+    batch = _ints(seq_lens, "seq_lens", dev)
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev or \
+            page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table: expected int32 [batch, max_pages] with unit column stride")
+    max_pages = page_table.shape[1]
+    ldt = page_table.stride(0) if batch > 1 else max_pages
+    return n_kv, page, n_pages, max_pages, ldt, pitch, spitch
+
+
+def _on_device(*tensors):
+    """All tensors on one device; calls run there whatever the current device is."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one device")
+    return torch.cuda.device(dev)
+
+
+def paged_kv_append(K, V, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None,
+                    k_page_scale=None, v_page_scale=None, stream=None):
+    """Puts K/V rows [T, n_kv_heads * 128] into the pages of a cache [num_pages, n_kv_heads, page_size, 128].
+
+    The rows of sequence b (cu_seqlens[b] .. cu_seqlens[b + 1] - 1; without cu_seqlens row b alone) become its
+    last tokens: seq_lens holds the lengths after the call.  bf16 rows go into a bf16 cache as they are and into
+    an E4M3 cache (uint8 pages with fp32 page scales) quantised with one scale per (token, kv head); uint8 rows
+    with k_scale and v_scale (as fused_qkv_rope_fp8kv returns them) go into an E4M3 cache as they are."""
+    ld, lds = _kv_pair(K, V, k_scale, v_scale)
+    n_kv, page, n_pages, max_pages, ldt, pitch, spitch = _cache(k_pages, v_pages, page_table, seq_lens, k_page_scale,
+                                                               v_page_scale)
+    T, batch = K.shape[0], seq_lens.numel()
+    if K.shape[1] != n_kv * HEAD_DIM:
+        raise ValueError("the rows must have the cache's n_kv_heads")
+    if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", K.device) != batch + 1:
+        raise ValueError("cu_seqlens must have batch + 1 entries")
+    with _on_device(K, V, k_pages, k_scale, v_scale):
+        st = load().paged_kv_append(_ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), _ptr(k_pages), _ptr(v_pages),
+                                    _ptr(k_page_scale), _ptr(v_page_scale), _ptr(page_table), _ptr(seq_lens),
+                                    _ptr(cu_seqlens), T, batch, n_kv, HEAD_DIM, page, n_pages, max_pages, ld, lds, ldt,
+                                    pitch, spitch, FL_E4M3 if K.dtype == torch.uint8 else FL_BF16,
+                                    FL_E4M3 if k_pages.dtype == torch.uint8 else FL_BF16, _stream(stream))
+    _check("paged_kv_append", st)
+
+
+def attention_decode_workspace(device=None) -> torch.Tensor:
+    """A zero-filled workspace for attention_decode calls of any shape (one for each set of calls that may overlap)."""
+    return torch.zeros(load().fl_attention_decode_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
+
+
+def attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale=None, v_page_scale=None, scale=None,
+                     O=None, workspace=None, stream=None):
+    """Attention of one new token per sequence, Q bf16 [batch, n_heads * 128], over the paged cache.
+
+    scale: of the logits, 1 / sqrt(128) by default.  Returns O bf16 [batch, n_heads * 128]."""
+    n_kv, page, n_pages, max_pages, ldt, pitch, spitch = _cache(k_pages, v_pages, page_table, seq_lens, k_page_scale,
+                                                               v_page_scale)
+    batch, width = Q.shape
+    ldq = _mat(Q, "Q", torch.bfloat16)
+    if width % HEAD_DIM != 0 or batch != seq_lens.numel():
+        raise ValueError("Q: expected [batch, n_heads * 128]")
+    if O is None:
+        O = torch.empty((batch, width), dtype=torch.bfloat16, device=Q.device)
+    ldo = _mat(O, "O", torch.bfloat16)
+    if O.shape != Q.shape:
+        raise ValueError("O must have Q's shape")
+    if workspace is None:
+        workspace = attention_decode_workspace(Q.device)
+    with _on_device(Q, k_pages, O, workspace):
+        st = load().attention_decode(_ptr(Q), _ptr(k_pages), _ptr(v_pages), _ptr(k_page_scale), _ptr(v_page_scale),
+                                     _ptr(page_table), _ptr(seq_lens), _ptr(O), batch, width // HEAD_DIM, n_kv,
+                                     HEAD_DIM, page, n_pages, max_pages, ldq, ldo, ldt, pitch, spitch,
+                                     HEAD_DIM ** -0.5 if scale is None else scale,
+                                     FL_E4M3 if k_pages.dtype == torch.uint8 else FL_BF16, _ptr(workspace),
+                                     workspace.numel(), _stream(stream))
+    _check("attention_decode", st)
+    return O
+
+
+def attention_prefill_workspace(rows: int, n_kv_heads: int, fp8: bool, device=None) -> torch.Tensor:
+    """A zero-filled workspace for attention_prefill calls of up to `rows` rows."""
+    n = load().fl_attention_prefill_workspace_bytes(int(rows), int(n_kv_heads), FL_E4M3 if fp8 else FL_BF16)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def attention_prefill(Q, K, V, cu_seqlens=None, seq_len: int = 0, k_scale=None, v_scale=None, causal: bool = True,
+                      scale=None, O=None, workspace=None, stream=None):
+    """Attention over whole prompts, Q bf16 [M, n_heads * 128], K and V [M, n_kv_heads * 128] bf16 or uint8 (E4M3
+    codes with fp32 [M, n_kv_heads] scales, as fused_qkv_rope_fp8kv returns them).
+
+    Sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; without cu_seqlens the rows are sequences of
+    seq_len tokens laid end to end (0: one sequence).  Rows of O in no sequence stay as they were.  scale: of the
+    logits, 1 / sqrt(128) by default.  Returns O bf16 [M, n_heads * 128]."""
+    ldkv, lds = _kv_pair(K, V, k_scale, v_scale)
+    M, width = Q.shape
+    _mat(Q, "Q", torch.bfloat16)
+    if width % HEAD_DIM != 0 or K.shape[0] != M:
+        raise ValueError("Q: expected [M, n_heads * 128] with as many rows as K and V")
+    n_kv, kv_width = K.shape[1] // HEAD_DIM, K.shape[1]
+    batch = 0 if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", Q.device) - 1
+    if batch < 0:
+        raise ValueError("cu_seqlens must have batch + 1 entries")
+    fp8 = K.dtype == torch.uint8
+    if O is None:
+        O = (torch.empty if cu_seqlens is None else torch.zeros)((M, width), dtype=torch.bfloat16, device=Q.device)
+    _mat(O, "O", torch.bfloat16)
+    if O.shape != Q.shape:
+        raise ValueError("O must have Q's shape")
+    if workspace is None:
+        workspace = attention_prefill_workspace(M, n_kv, fp8, Q.device)
+    if M == 1:
+        ldkv, lds = kv_width, n_kv
+    with _on_device(Q, K, V, O, workspace, k_scale, v_scale):
+        st = load().attention_prefill(_ptr(Q), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), _ptr(cu_seqlens),
+                                      _ptr(O), M, batch, width // HEAD_DIM, n_kv, HEAD_DIM, seq_len or max(M, 1),
+                                      _ld(Q, width, width), ldkv, lds, _ld(O, width, width),
+                                      HEAD_DIM ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                      FL_E4M3 if fp8 else FL_BF16, _ptr(workspace), workspace.numel(),
+                                      _stream(stream))
+    _check("attention_prefill", st)
+    return O
+
+
 def device_status(stream=None) -> int:
     """Synchronises the stream; returns (and clears) the device-wide failure code."""
     return load().fl_device_status(_stream(stream))
@@ -557,7 +749,7 @@ def device_status(stream=None) -> int:
 
 def check_device_status(workspace=None, stream=None) -> int:
     """Synchronises the stream; returns (and clears) the failure code recorded in `workspace`
-    (a workspace of the RMSNorm + FP8 or cross-entropy calls); None: the device-wide word."""
+    (a workspace of the RMSNorm + FP8, cross-entropy or attention calls); None: the device-wide word."""
     return load().fl_check_device_status(_ptr(workspace), _stream(stream))
 
 

@@ -1,4 +1,4 @@
-"""Builds libfusedlinear.so (sm_103a) in-tree from csrc/*.cu.
+"""Builds libfusedlinear.so (sm_103a) in-tree from csrc/*.cu and attention/*.cu.
 
 Each translation unit is compiled by its own nvcc process in parallel, then
 linked into one shared library next to this file.  Nothing is installed.
@@ -14,6 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+ATTENTION = os.path.join(HERE, "attention")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfusedlinear.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -28,15 +29,16 @@ def _nvcc() -> str:
 
 def _flags():
     return ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-                   "-I", os.path.join(ROOT, "include"), "-I", CSRC]
+                   "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", ATTENTION]
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+    return [os.path.join(d, f) for d in (CSRC, ATTENTION) for f in sorted(os.listdir(d)) if f.endswith(".cu")]
 
 
 def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "fused_linear.h")]
+    return [os.path.join(d, f) for d in (CSRC, ATTENTION) for f in os.listdir(d)] + [
+        os.path.join(ROOT, "include", "fused_linear.h")]
 
 
 def up_to_date() -> bool:

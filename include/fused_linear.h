@@ -1,9 +1,11 @@
 /* fused_linear.h — C ABI of the GB300 (sm_103a) fused Linear + epilogue library.
  *
- * Every entry point computes a Linear layer Y = X W^T (+ b) on the tcgen05
+ * Every fused_* entry point computes a Linear layer Y = X W^T (+ b) on the tcgen05
  * tensor cores, keeps the fp32 accumulator tile in tensor memory, and applies
  * the memory-bound tail ("epilogue") to that tile before anything is written
- * to HBM; no intermediate tensor is materialised.
+ * to HBM; no intermediate tensor is materialised.  Three more (paged_kv_append,
+ * attention_prefill, attention_decode) take what the QKV projections write: they
+ * put keys and values into a paged cache and compute the attention over them.
  *
  * Conventions shared by all entry points
  *   - Matrices are row-major.  X is [M, K] with leading dimension ldx (in
@@ -61,7 +63,7 @@ typedef enum fl_status {
     FL_ERR_ARCH = 7           /* the current device is not sm_103 */
 } fl_status;
 
-enum { FL_F32 = 0, FL_BF16 = 1 };
+enum { FL_F32 = 0, FL_BF16 = 1, FL_E4M3 = 2 };
 enum { FL_GELU_ERF = 0, FL_GELU_TANH = 1 };
 
 /* Linear + bias + GELU.
@@ -294,6 +296,80 @@ FL_API int fused_dgrad_gelu(const void* dZ, const void* W, const void* H, void* 
 FL_API int fused_swiglu_bwd(const void* dO, const void* Wd, const void* G, const void* U, void* dGU,
                             int M, int N, int K, int64_t ldo_in, int64_t ldw, int64_t ldgu, int64_t ldout,
                             void* stream);
+
+/* ---------------------------------------------------------------- attention
+ * The paged cache that paged_kv_append fills and attention_decode reads:
+ *   k_pages, v_pages   [num_pages] blocks `page_pitch` elements apart, each
+ *                      [n_kv_heads][page_size][128], bf16 (FL_BF16) or E4M3 bytes (FL_E4M3);
+ *   k_page_scale, v_page_scale  E4M3 only: [num_pages] blocks `scale_pitch` floats apart, each
+ *                      [n_kv_heads][page_size] fp32, one scale per (token, kv head);
+ *   page_table         int32, row b `ldt` entries behind row b - 1, max_pages entries each: entry i is
+ *                      the page of positions [i*page_size, (i+1)*page_size) of sequence b.  Sequences
+ *                      may share pages (a common prefix); entries behind a sequence's length are not
+ *                      used;
+ *   seq_lens           int32 [batch], tokens in the cache.
+ * page_size is any number >= 1 (a multiple of 8 streams best), offsets are 64-bit.  All of these live
+ * on the device, so a captured graph can be replayed as the sequences grow.  head_dim must be 128
+ * (FL_ERR_UNSUPPORTED otherwise).  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes
+ * them.  Scale, table, length and offset pointers need 4-byte alignment, the others 16. */
+
+/* Rows of keys and values into the cache.
+ * K, V [T, n_kv_heads*128], pitch ldkv elements: bf16 (row_dtype FL_BF16) or E4M3 bytes (FL_E4M3) with
+ * k_scale, v_scale [T, lds] fp32.  The rows of sequence b are cu_seqlens[b] .. cu_seqlens[b+1] - 1
+ * (int32 [batch + 1]) and become its LAST tokens: seq_lens holds the lengths after the call, so the
+ * same array goes to attention_decode.  cu_seqlens NULL: row b is the one new token of sequence b (T
+ * may not exceed batch).  Rows outside every sequence (behind cu_seqlens[batch]) are ignored, and so
+ * is a row whose position or page is outside the table or the cache (attention_decode reports
+ * those).  Two rows of one call must not meet in one slot.
+ * Rows and cache of one type are moved as they are; bf16 rows into an E4M3 cache (cache_dtype
+ * FL_E4M3) are quantised with one scale per (token, kv head) as fused_qkv_rope_fp8kv does:
+ * s = max|y| / 448, codes E4M3(y / s) (nearest even), a head of zeros has s = 0.  E4M3 rows into a
+ * bf16 cache: FL_ERR_UNSUPPORTED. */
+FL_API int paged_kv_append(const void* K, const void* V, const float* k_scale, const float* v_scale,
+                           void* k_pages, void* v_pages, float* k_page_scale, float* v_page_scale,
+                           const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_seqlens,
+                           int T, int batch, int n_kv_heads, int head_dim, int page_size, int num_pages,
+                           int max_pages, int64_t ldkv, int64_t lds, int64_t ldt, int64_t page_pitch,
+                           int64_t scale_pitch, int row_dtype, int cache_dtype, void* stream);
+
+/* Attention of one new token per sequence over the paged cache.
+ *   O[b, h] = sum_j p_j V[j] / sum_j p_j,  p_j = exp(scale * Q[b, h] . K[j] - max),  j < seq_lens[b],
+ * query head h reading kv head h / (n_heads / n_kv_heads).  Q, O [batch, n_heads*128] bf16 (Q already
+ * rotated); n_heads a multiple of n_kv_heads; scale > 0.  Sums and the softmax's state are fp32.
+ * A sequence of length 0 gets zeros.  A negative length, one beyond max_pages * page_size, or a page
+ * outside [0, num_pages) among the entries in use: the sequence's rows are NaN and
+ * fl_check_device_status(workspace) returns FL_ERR_INVALID_ARG once.  Nothing behind a sequence's
+ * length is read into the result, whatever it holds.
+ * workspace: fl_attention_decode_workspace_bytes() bytes, 256-byte aligned, zero-filled before first
+ * use; calls of any shape may follow one another with it, two calls that may overlap on the GPU need
+ * one each. */
+FL_API int attention_decode(const void* Q, const void* k_pages, const void* v_pages, const float* k_page_scale,
+                            const float* v_page_scale, const int32_t* page_table, const int32_t* seq_lens, void* O,
+                            int batch, int n_heads, int n_kv_heads, int head_dim, int page_size, int num_pages,
+                            int max_pages, int64_t ldq, int64_t ldo, int64_t ldt, int64_t page_pitch,
+                            int64_t scale_pitch, float scale, int cache_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+FL_API size_t fl_attention_decode_workspace_bytes(void);
+
+/* Attention over whole prompts.
+ *   O[i, h] = sum_j p_ij V[j] / sum_j p_ij,  p_ij = exp(scale * Q[i, h] . K[j] - max),
+ * over the keys j of row i's own sequence, with `causal` those at or before i.  Q, O [M, n_heads*128]
+ * bf16; K, V [M, n_kv_heads*128], pitch ldkv elements, bf16 (kv_dtype FL_BF16) or E4M3 bytes
+ * (FL_E4M3) with k_scale, v_scale [M, lds] fp32, as fused_qkv_rope and fused_qkv_rope_fp8kv write them.
+ * Sequence b is rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32 [batch + 1] on the device, not
+ * decreasing, in [0, M]); cu_seqlens NULL: the rows are sequences of seq_len tokens laid end to end,
+ * the last one possibly shorter (batch is ignored).  Rows of O in no sequence stay as they were.
+ * Rows of another sequence, or masked ones of the own, never reach a result, whatever they hold.
+ * Softmax state and sums are fp32; the weights p_ij (times the scale of V) are rounded to bf16 for the
+ * tensor cores.
+ * workspace: fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype) bytes, 256-byte aligned, its
+ * first 512 bytes zero-filled before first use; two calls that may overlap on the GPU need one each. */
+FL_API int attention_prefill(const void* Q, const void* K, const void* V, const float* k_scale,
+                             const float* v_scale, const int32_t* cu_seqlens, void* O, int M, int batch,
+                             int n_heads, int n_kv_heads, int head_dim, int seq_len, int64_t ldq, int64_t ldkv,
+                             int64_t lds, int64_t ldo, float scale, int causal, int kv_dtype, void* workspace,
+                             size_t workspace_bytes, void* stream);
+FL_API size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, int kv_dtype);
 
 /* fused_linear_gelu (bf16) on HOST buffers: copies in, GEMM + epilogue, copies out.
  *   X [M,K], W [N,K], b [N] (nullable) and Y [M,N] are contiguous bf16 arrays in host
