@@ -59,6 +59,12 @@ __device__ __forceinline__ void sequence_rows(const int* cu, int b, int seq_len,
   }
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
   uint32_t h;
   asm("{\n\t.reg .b32 t;\n\tcvt.rn.f16x2.e4m3x2 t, %1;\n\tmov.b32 %0, t;\n\t}" : "=r"(h) : "h"(static_cast<uint16_t>(code)));

@@ -1,0 +1,563 @@
+// Attention of one new token per sequence over a paged key-value cache.
+//
+//   o_h = sum_j p_j v_j / sum_j p_j,  p_j = 2^(x_j - m),  x_j = scale * log2(e) * q_h . k_j
+//
+// What bounds it: the cache is read once, 4 * 128 * group multiply-adds for every 256 (E4M3) or 512 (bf16)
+// bytes, so it runs at the memory's rate as long as enough loads are in flight and nothing else keeps a warp
+// from issuing the next ones.
+//
+// Split.  The work is cut into units of 64 tokens of one (sequence, kv head); every sequence has at least one.
+// CTA i of G takes units [i T / G, (i + 1) T / G) in the order (sequence, kv head, unit), so every CTA streams
+// the same number of bytes whatever the lengths are, and a captured launch adapts to them.  A (sequence, kv
+// head) that lies in one CTA is finished there; one that is cut writes (m, l, o) of each piece to the workspace,
+// and the last CTA to arrive joins the pieces in the order of the CTAs (the result does not depend on which
+// came last).
+//
+// Inside a CTA each of four warps streams its own tokens, 16 at a time, through its own ring of cp.async
+// stages: no barrier in the loop, and the ring runs on over the end of a sequence.  Both products run on the
+// tensor cores with the tokens on the M side, S^T = K Q^T and O^T = V^T P^T (m16n8k16: 8 query heads of a group
+// in the N columns, two column tiles for groups above 8), so a small group wastes little.  The assignment of
+// cache columns to MMA k-indexes is free as long as both operands agree: each lane takes 16 consecutive bytes
+// of a row, and the query's fragments are loaded in the same order.  V^T needs two tokens of one dimension in a
+// register: bytes of two rows interleaved by prmt.  Chunks of 16 bytes are permuted inside a row (xor with bits
+// of the row) so that no quarter warp meets a bank twice.
+//
+// E4M3: codes become fp16 exactly (cvt.f16x2.e4m3x2); a query head is scaled by a power of two to fp16's upper
+// range, where its bf16 values are exact down to 2^-29 of the largest; the scales stay in fp32: K's multiplies
+// the logit, V's enters the weight as 2^(x_j + log2 vs_j - m').  m' is the running maximum of that exponent, so
+// weights lie in [0, 2^15] and are rounded to fp16 (2^-11).
+// bf16: weights are split into two bf16 terms (hi + lo, 2^-16) so that the product is as exact as the inputs.
+//
+// The maxima m and m' rise only when a logit passes them by more than 8 (2^8 fits every type used): then the
+// sums are rescaled.  That takes one vote in most steps instead of six shuffles and a rescale of O.
+#pragma once
+#include "attention_common.h"
+
+namespace fl {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecSub = 16;                    // tokens of one warp's step
+constexpr int kDecUnit = kDecWarps * kDecSub;  // tokens of one unit of work
+constexpr int kDecMaxCtas = 640;
+constexpr int kDecPartFloats = 16 * (kHeadDim + 3);  // (o[128], m, m', l) of up to 16 heads
+constexpr float kDecNone = -3e38f;             // a maximum over nothing: any finite logit passes it
+constexpr float kDecLazy = 8.f;
+constexpr float kDecLift = 7.f;                // E4M3: weights are lifted by 2^7 in fp16
+
+struct DecodeParams {
+  CacheView c;
+  const __nv_bfloat16* Q;
+  __nv_bfloat16* O;
+  long long ldq, ldo;
+  int group, chunks, chunk_heads;  // query heads of a kv head, cut into `chunks` of `chunk_heads` (<= 8 NT)
+  int page_shift;                  // log2(page_size), -1 if it is no power of two
+  float scale_log2;
+  int* status;
+  unsigned* counters;              // [kDecMaxCtas], by the first CTA of a cut (sequence, kv head)
+  float* parts;                    // [kDecMaxCtas][2][kDecPartFloats]
+};
+
+template <bool FP8, int NT>
+struct DecodeTraits {
+  static constexpr int kRowBytes = FP8 ? 128 : 256;
+  static constexpr int kTile = kDecSub * kRowBytes;
+  static constexpr int kStage = 2 * kTile + (FP8 ? 2 * kDecSub * 4 : 0);
+  static constexpr int kStages = FP8 ? 5 : 3;
+  static constexpr int kMerge = kDecWarps * 8 * kHeadDim * 4;
+  static constexpr int kSmem = kDecWarps * kStages * kStage + kMerge + kDecWarps * 8 * NT * 3 * 4 + 128;
+};
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A run of units of one (sequence, head chunk): tokens [t0, t1).
+struct DecodeSeg {
+  int b, h, t0, t1, units;
+  int n_units, len;  // of the whole sequence
+  bool bad;          // its length is outside the table
+};
+
+__device__ __forceinline__ int decode_units(int len, long long capacity, bool& bad) {
+  bad = len < 0 || len > capacity;
+  return bad || len == 0 ? 1 : (len - 1) / kDecUnit + 1;
+}
+
+template <bool FP8, int NT>
+__global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using T = DecodeTraits<FP8, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + kDecWarps * T::kStages * T::kStage);
+  float* stats = merge + T::kMerge / 4;  // [3][warp][8 NT]: m, m', l
+  long long* plan = reinterpret_cast<long long*>(stats + kDecWarps * 8 * NT * 3);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int heads_v = p.c.n_kv * p.chunks;  // independent (kv head, chunk) pairs of a sequence
+  const long long capacity = static_cast<long long>(p.c.max_pages) * p.c.page_size;
+  const int G = gridDim.x, cta = blockIdx.x;
+
+  // ---- plan: total units, and where this CTA's first unit lies
+  auto block_scan = [&](int b0, int& mine, long long& before) -> long long {  // of 128 sequences from b0
+    const int b = b0 + tid;
+    bool bad;
+    mine = b < p.c.batch ? decode_units(__ldg(p.c.lens + b), capacity, bad) : 0;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) plan[warp] = x;
+    __syncthreads();
+    long long sum = 0;
+    before = x - mine;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (w < warp) before += plan[w];
+      sum += plan[w];
+    }
+    return sum;
+  };
+  int mine;
+  long long before, total = 0;
+  for (int b0 = 0; b0 < p.c.batch; b0 += kDecThreads) total += block_scan(b0, mine, before);
+  total *= heads_v;
+  const long long u0 = total * cta / G, u1 = total * (cta + 1) / G;
+  if (u0 == u1) return;
+  {
+    long long base = 0;
+    for (int b0 = 0;; b0 += kDecThreads) {
+      // one block of sequences: the scan above still stands
+      const long long sum = p.c.batch > kDecThreads ? block_scan(b0, mine, before) : total / heads_v;
+      const long long lo = (base + before) * heads_v;
+      if (mine > 0 && u0 >= lo && u0 < lo + static_cast<long long>(mine) * heads_v) {
+        plan[8] = b0 + tid;
+        plan[9] = u0 - lo;
+      }
+      base += sum;
+      if (base * heads_v > u0) break;
+    }
+    __syncthreads();
+  }
+  long long left = u1 - u0;
+  auto begin_seg = [&](DecodeSeg& s, int tile, long long units_left) {
+    if (tile == 0 && s.h == 0) s.len = __ldg(p.c.lens + s.b);
+    s.n_units = decode_units(s.len, capacity, s.bad);
+    s.units = static_cast<int>(min(static_cast<long long>(s.n_units - tile), units_left));
+    const int end = s.bad ? 0 : s.len;
+    s.t0 = tile * kDecUnit;
+    s.t1 = static_cast<int>(min(static_cast<long long>(end), (static_cast<long long>(tile) + s.units) * kDecUnit));
+  };
+  auto next_seg = [&](DecodeSeg& s, long long units_left) {
+    if (++s.h == heads_v) {
+      s.h = 0;
+      ++s.b;
+    }
+    begin_seg(s, 0, units_left);
+  };
+  DecodeSeg seg;
+  long long seg_first;  // first unit of this (sequence, head) in the whole order
+  {
+    seg.b = static_cast<int>(plan[8]);
+    const long long in = plan[9];
+    seg.len = __ldg(p.c.lens + seg.b);
+    bool bad;
+    const int n = decode_units(seg.len, capacity, bad);
+    seg.h = static_cast<int>(in / n);
+    const int tile = static_cast<int>(in - static_cast<long long>(seg.h) * n);
+    seg_first = u0 - tile;
+    begin_seg(seg, tile, left);
+  }
+
+  // ---- producer side of this warp's ring
+  DecodeSeg ps = seg;
+  long long p_left = left;
+  int pt = ps.t0 + warp * kDecSub, entry = 0, p_stage = 0;
+  uint32_t bad_steps = 0;  // stages whose page-table entry is outside the cache
+  const bool one_page = (p.c.page_size & (kDecSub - 1)) == 0;  // a step's 16 tokens lie in one page
+  auto page_of = [&](int pos) { return p.page_shift >= 0 ? pos >> p.page_shift : pos / p.c.page_size; };
+  auto settle = [&]() {  // moves on to this warp's next step and fetches its page-table entry
+    while (pt >= ps.t1) {
+      p_left -= ps.units;
+      if (p_left <= 0) return;
+      next_seg(ps, p_left);
+      pt = ps.t0 + warp * kDecSub;
+    }
+    const int pos = one_page ? pt : min(pt + (lane & 15), ps.t1 - 1);
+    entry = __ldg(p.c.table + ps.b * p.c.ldt + page_of(pos));
+  };
+  const uint32_t ring = smem_u32(smem) + warp * T::kStages * T::kStage;
+  auto issue = [&]() {
+    if (p_left > 0) {
+      constexpr int kChunks = T::kRowBytes / 16, kRowsPer = 32 / kChunks;
+      const uint32_t dst = ring + p_stage * T::kStage;
+      const int kvh = ps.h / p.chunks;
+      const int mypos = one_page ? pt : min(pt + (lane & 15), ps.t1 - 1);
+      const int slot = mypos - page_of(mypos) * p.c.page_size;
+      const bool ok = static_cast<unsigned>(entry) < static_cast<unsigned>(p.c.num_pages);
+      bad_steps = (bad_steps & ~(1u << p_stage)) | (ok ? 0u : 1u << p_stage);
+      const int c = lane % kChunks;
+#pragma unroll
+      for (int i = 0; i < kDecSub / kRowsPer; ++i) {
+        const int row = lane / kChunks + i * kRowsPer;
+        int page = entry, s = slot + row;
+        bool there = ok && pt + row < ps.t1;
+        if (!one_page) {
+          page = __shfl_sync(~0u, entry, row);
+          s = __shfl_sync(~0u, slot, row);
+          there = pt + row < ps.t1 && static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
+        }
+        const long long at =
+            there ? page * p.c.page_pitch + (static_cast<long long>(kvh) * p.c.page_size + s) * kHeadDim : 0;
+        const long long byte = at * (FP8 ? 1 : 2) + c * 16;
+        cp_async_16_or_zero(dst + row * T::kRowBytes + ((c ^ ((row & 1) << 2)) << 4),
+                            static_cast<const uint8_t*>(p.c.k) + byte, there);
+        cp_async_16_or_zero(dst + T::kTile + row * T::kRowBytes + ((c ^ (row & 6)) << 4),
+                            static_cast<const uint8_t*>(p.c.v) + byte, there);
+      }
+      if (FP8) {  // lanes 0..15 K's scales, 16..31 V's
+        const int row = lane & 15;
+        const bool there = ok && pt + row < ps.t1;
+        const int s = one_page ? slot + row : slot;
+        const long long at = there ? entry * p.c.scale_pitch + static_cast<long long>(kvh) * p.c.page_size + s : 0;
+        cp_async_4_or_zero(dst + 2 * T::kTile + lane * 4, (lane < 16 ? p.c.ks : p.c.vs) + at, there);
+      }
+      pt += kDecUnit;
+      settle();
+    }
+    cp_async_commit();
+    p_stage = p_stage + 1 == T::kStages ? 0 : p_stage + 1;
+  };
+  settle();
+#pragma unroll
+  for (int i = 0; i < T::kStages - 1; ++i) issue();
+  int stage = 0;
+
+  for (;;) {
+    // ---- this segment's query fragments (B operand: head g of the column tile, dimensions in the cache's order)
+    const int kvh = seg.h / p.chunks, chunk = seg.h - kvh * p.chunks;
+    const int head0 = kvh * p.group + chunk * p.chunk_heads;
+    const int n_heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+    uint32_t qf[NT][16];
+    float fac[NT][2];  // of heads 2q, 2q + 1 of the column tile
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool has = nt * 8 + g < n_heads;
+      const __nv_bfloat16* src = p.Q + seg.b * p.ldq + static_cast<long long>(head0 + nt * 8 + g) * kHeadDim;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = FP8 ? ((i >> 1) * 4 + q) * 16 + (i & 1) * 8 : (i * 4 + q) * 8;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (has) w = __ldg(reinterpret_cast<const uint4*>(src + d));
+        qf[nt][i * 4] = w.x, qf[nt][i * 4 + 1] = w.y, qf[nt][i * 4 + 2] = w.z, qf[nt][i * 4 + 3] = w.w;
+      }
+      float f = p.scale_log2;
+      if (FP8) {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a = fmaxf(a, fmaxf(fabsf(bf16_lo(qf[nt][i])), fabsf(bf16_hi(qf[nt][i]))));
+        a = fmaxf(a, __shfl_xor_sync(~0u, a, 1));
+        a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
+        // 2^e that takes the largest value to [2^14, 2^15); values that are not finite stay what they are
+        const int ex = static_cast<int>(__float_as_uint(a) >> 23);
+        const int up = ex == 255 ? 127 : min(max(268 - ex, 1), 253);
+        const float lift = __uint_as_float(static_cast<uint32_t>(up) << 23);
+        f *= __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) qf[nt][i] = pack_f16x2(bf16_lo(qf[nt][i]) * lift, bf16_hi(qf[nt][i]) * lift);
+      }
+      fac[nt][0] = __shfl_sync(~0u, f, q * 8);
+      fac[nt][1] = __shfl_sync(~0u, f, q * 8 + 4);
+    }
+    bool bad = seg.bad;
+    float o[NT][8][4];
+    float m[NT][2], mv[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][t][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[nt][i] = mv[nt][i] = kDecNone, l[nt][i] = 0.f;
+    }
+
+    for (int t = seg.t0 + warp * kDecSub; t < seg.t1; t += kDecUnit) {
+      cp_async_wait<T::kStages - 2>();
+      __syncwarp();
+      const uint32_t kb = ring + stage * T::kStage, vb = kb + T::kTile;
+      // ---- S^T = K Q^T: 16 tokens x 8 heads, k = 128
+      float s[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][0][i] = s[nt][1][i] = 0.f;
+      const uint32_t kr0 = kb + g * T::kRowBytes, kr1 = kr0 + 8 * T::kRowBytes;
+      const int sw = (g & 1) << 2;
+#pragma unroll
+      for (int ci = 0; ci < T::kRowBytes / 64; ++ci) {
+        const uint32_t off = ((ci * 4 + q) ^ sw) << 4;
+        const uint4 x = ld_shared_v4(kr0 + off), y = ld_shared_v4(kr1 + off);
+        const uint32_t xr[4] = {x.x, x.y, x.z, x.w}, yr[4] = {y.x, y.y, y.z, y.w};
+        if (FP8) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t a0 = e4m3x2_to_f16x2(xr[u] & 0xFFFFu), a2 = e4m3x2_to_f16x2(xr[u] >> 16);
+            const uint32_t a1 = e4m3x2_to_f16x2(yr[u] & 0xFFFFu), a3 = e4m3x2_to_f16x2(yr[u] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816<true>(s[nt][u & 1], a0, a1, a2, a3, qf[nt][ci * 8 + u * 2], qf[nt][ci * 8 + u * 2 + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816<false>(s[nt][u], xr[u * 2], yr[u * 2], xr[u * 2 + 1], yr[u * 2 + 1], qf[nt][ci * 4 + u * 2],
+                               qf[nt][ci * 4 + u * 2 + 1]);
+        }
+      }
+      // ---- softmax: lane (g, q) holds tokens g, g + 8 of heads 2q, 2q + 1
+      float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+      if (FP8) {
+        const float* sc = reinterpret_cast<const float*>(smem + (kb - smem_u32(smem)) + 2 * T::kTile);
+        ks[0] = sc[g], ks[1] = sc[g + 8];
+        lv[0] = lg2(sc[16 + g]), lv[1] = lg2(sc[24 + g]);
+      }
+      float x[NT][4];
+      bool rise = false;
+      const bool cut = t + kDecSub > seg.t1;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = (s[nt][0][i] + s[nt][1][i]) * fac[nt][i & 1];
+          if (FP8) v *= ks[i >> 1];
+          if (cut && t + g + (i >> 1) * 8 >= seg.t1) v = -INFINITY;
+          x[nt][i] = v;
+          rise |= v > m[nt][i & 1] + kDecLazy;
+          if (FP8) rise |= v + lv[i >> 1] > mv[nt][i & 1] + kDecLazy;
+        }
+      if (__any_sync(~0u, rise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float a = fmaxf(m[nt][i], fmaxf(x[nt][i], x[nt][i + 2]));
+            float b = FP8 ? fmaxf(mv[nt][i], fmaxf(x[nt][i] + lv[0], x[nt][i + 2] + lv[1])) : 0.f;
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              a = fmaxf(a, __shfl_xor_sync(~0u, a, d));
+              if (FP8) b = fmaxf(b, __shfl_xor_sync(~0u, b, d));
+            }
+            const float down = ex2(m[nt][i] - a), down_o = FP8 ? ex2(mv[nt][i] - b) : down;
+            m[nt][i] = a;
+            mv[nt][i] = b;
+            l[nt][i] *= down;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[nt][d][i] *= down_o, o[nt][d][i + 2] *= down_o;
+          }
+      }
+      uint32_t pf[NT][2], pl[NT][2];  // P^T (B operand: tokens 2q, 2q + 1 | + 8 of head g)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = ex2(x[nt][i] - m[nt][i & 1]);
+          l[nt][i & 1] += e;
+          w[i] = FP8 ? ex2((x[nt][i] + lv[i >> 1]) - (mv[nt][i & 1] - kDecLift)) : e;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (FP8) {
+            pf[nt][i] = transpose8x8(pack_f16x2(w[i * 2], w[i * 2 + 1]));
+          } else {
+            const uint32_t hi = pack_bf16x2(w[i * 2], w[i * 2 + 1]);
+            pf[nt][i] = transpose8x8(hi);
+            pl[nt][i] = transpose8x8(pack_bf16x2(w[i * 2] - bf16_lo(hi), w[i * 2 + 1] - bf16_hi(hi)));
+          }
+        }
+      }
+      // ---- O^T += V^T P^T: lane (g, q) brings tokens 2q, 2q + 1, 2q + 8, 2q + 9 of 16 dimensions
+      const uint32_t vr = vb + 2 * q * T::kRowBytes;
+#pragma unroll
+      for (int half = 0; half < T::kRowBytes / 128; ++half) {
+        const uint32_t off = ((half * 8 + g) ^ (2 * q)) << 4;
+        uint32_t v[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint4 y = ld_shared_v4(vr + ((r & 1) + (r >> 1) * 8) * T::kRowBytes + off);
+          v[r][0] = y.x, v[r][1] = y.y, v[r][2] = y.z, v[r][3] = y.w;
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (FP8) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t lo = __byte_perm(v[0][w], v[1][w], u ? 0x7362 : 0x5140);
+              const uint32_t hi = __byte_perm(v[2][w], v[3][w], u ? 0x7362 : 0x5140);
+              const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xFFFFu), a1 = e4m3x2_to_f16x2(lo >> 16);
+              const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xFFFFu), a3 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816<true>(o[nt][w * 2 + u], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            }
+          } else {
+            const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+            const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816<false>(o[nt][half * 4 + w], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+              mma_16816<false>(o[nt][half * 4 + w], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+            }
+          }
+        }
+      }
+      bad |= (bad_steps >> stage & 1u) != 0;
+      __syncwarp();
+      stage = stage + 1 == T::kStages ? 0 : stage + 1;
+      issue();
+    }
+
+    // ---- the CTA's four pieces become one: finished here, or a part of a cut (sequence, head)
+    const long long last_unit = seg_first + seg.n_units - 1;
+    const int c_first = static_cast<int>(((seg_first + 1) * G - 1) / total);
+    const int c_last = static_cast<int>(((last_unit + 1) * G - 1) / total);
+    const bool whole = c_first == c_last;
+    float* part = p.parts + (static_cast<long long>(cta) * 2 + (cta == c_first ? 1 : 0)) * kDecPartFloats;
+    const bool spoiled = __any_sync(~0u, bad);
+    if (spoiled && lane == 0 && atomicCAS(p.status + ST_CODE, 0, static_cast<int>(FL_ERR_INVALID_ARG)) == 0)
+      p.status[ST_DETAIL] = seg.b;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      // o[nt][t][i]: head 2q + (i & 1), dimension 16 g + 2 t + (i >> 1) (E4M3), or for bf16 with t = 4 half + w
+      // dimension 64 half + 8 g + 2 w + (i >> 1).  Chunks of 4 dimensions, permuted by q against bank conflicts.
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float sum = l[nt][i];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        float* row = merge + (warp * 8 + 2 * q + i) * kHeadDim;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int chunk4 = FP8 ? g * 4 + c : (c >> 1) * 16 + g * 2 + (c & 1);
+          *reinterpret_cast<float4*>(row + ((chunk4 ^ q) << 2)) =
+              make_float4(o[nt][c * 2][i], o[nt][c * 2][i + 2], o[nt][c * 2 + 1][i], o[nt][c * 2 + 1][i + 2]);
+        }
+        if (g == 0) {
+          float* st = stats + warp * 8 * NT + nt * 8 + 2 * q + i;
+          st[0] = m[nt][i];
+          st[kDecWarps * 8 * NT] = FP8 ? mv[nt][i] - kDecLift : m[nt][i];
+          st[2 * kDecWarps * 8 * NT] = spoiled ? NAN : sum;
+        }
+      }
+      __syncthreads();
+      for (int h = 0; h < 8 && nt * 8 + h < n_heads; ++h) {
+        const float* st = stats + nt * 8 + h;
+        float M = kDecNone, MV = kDecNone, L = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          M = fmaxf(M, st[w * 8 * NT]);
+          MV = fmaxf(MV, st[(kDecWarps + w) * 8 * NT]);
+        }
+        const int at = ((((tid >> 2) ^ (h >> 1)) << 2) | (tid & 3));
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          L += st[(2 * kDecWarps + w) * 8 * NT] * ex2(st[w * 8 * NT] - M);
+          acc += merge[(w * 8 + h) * kHeadDim + at] * ex2(st[(kDecWarps + w) * 8 * NT] - MV);
+        }
+        if (whole) {
+          const float r = seg.len == 0 ? 0.f : acc * (ex2(MV - M) / L);
+          p.O[seg.b * p.ldo + static_cast<long long>(head0 + nt * 8 + h) * kHeadDim + tid] = __float2bfloat16_rn(r);
+        } else {
+          float* dst = part + (nt * 8 + h) * (kHeadDim + 3);
+          __stcg(dst + tid, acc);
+          if (tid < 3) __stcg(dst + kHeadDim + tid, tid == 0 ? M : tid == 1 ? MV : L);
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      // every CTA of the cut that has units arrives once; with fewer units than CTAs each of them is one unit
+      const unsigned want = static_cast<unsigned>(total >= G ? c_last - c_first + 1 : seg.n_units);
+      if (tid == 0) {
+        const unsigned n = atomicAdd(p.counters + c_first, 1u);
+        if (n + 1 == want) p.counters[c_first] = 0;
+        plan[0] = n + 1 == want;
+      }
+      __syncthreads();
+      if (plan[0] != 0) {
+        __threadfence();
+        auto src = [&](int c, int h) {
+          return p.parts + (static_cast<long long>(c) * 2 + (c == c_first)) * kDecPartFloats + h * (kHeadDim + 3);
+        };
+        auto has = [&](int c) { return total >= G || total * c / G != total * (c + 1) / G; };
+        for (int h = 0; h < n_heads; ++h) {
+          float M = kDecNone, MV = kDecNone, L = 0.f, acc = 0.f;
+          for (int c = c_first; c <= c_last; ++c) {
+            if (!has(c)) continue;
+            const float* s = src(c, h);
+            const float pm = __ldcg(s + kHeadDim), pmv = __ldcg(s + kHeadDim + 1);
+            const float nm = fmaxf(M, pm), nmv = fmaxf(MV, pmv);
+            L = L * ex2(M - nm) + __ldcg(s + kHeadDim + 2) * ex2(pm - nm);
+            acc = acc * ex2(MV - nmv) + __ldcg(s + tid) * ex2(pmv - nmv);
+            M = nm;
+            MV = nmv;
+          }
+          const float r = acc * (ex2(MV - M) / L);
+          p.O[seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + tid] = __float2bfloat16_rn(r);
+        }
+      }
+      __syncthreads();
+    }
+    left -= seg.units;
+    if (left <= 0) return;
+    seg_first += seg.n_units;
+    next_seg(seg, left);
+  }
+}
+
+}  // namespace fl
