@@ -563,80 +563,120 @@ def fused_swiglu_bwd(dO, Wd, G, U, dGU=None, stream=None):
 
 
 HEAD_DIM = 128
+_BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+
+# The attention calls are made once per layer and token, so their checks are written for few Python steps:
+# a device is an index, pointers go to ctypes as plain integers, and the device is switched only where the
+# tensors are not on the current one.
 
 
-def _kv_rows(t, name, scale, sname):
-    """Checks K or V rows: bf16 without scales, or E4M3 bytes (uint8) with fp32 [rows, n_kv_heads] scales."""
-    if t.dtype == torch.bfloat16:
-        if scale is not None:
-            raise ValueError(f"{sname}: bf16 rows have no scales")
-    elif t.dtype != torch.uint8 or scale is None:
-        raise ValueError(f"{name}: expected bf16 rows, or uint8 (E4M3) rows with {sname}")
-    ld = _mat(t, name, t.dtype)
-    if t.shape[1] % HEAD_DIM != 0:
-        raise ValueError(f"{name}: expected [rows, n_kv_heads * {HEAD_DIM}]")
-    lds = 0
-    if scale is not None:
-        lds = _mat(scale, sname, torch.float32)
-        if tuple(scale.shape) != (t.shape[0], t.shape[1] // HEAD_DIM):
-            raise ValueError(f"{sname}: expected [rows, n_kv_heads]")
-    return ld, lds
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _kv_pair(K, V, k_scale, v_scale):
-    ld, lds = _kv_rows(K, "K", k_scale, "k_scale")
-    if V.dtype != K.dtype or V.shape != K.shape or (ld, lds) != _kv_rows(V, "V", v_scale, "v_scale"):
-        raise ValueError("K and V (and their scales) must share type, shape and leading dimension")
-    return ld, lds
+def _on(dev, call, args, stream):
+    """Runs call(*args, stream) on device `dev` (an index) and its current stream, or on the stream given."""
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    if stream is not None:
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+    with torch.cuda.device(dev):
+        return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
 
 
-def _ints(t, name, device):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or (t.numel() > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: expected a contiguous int32 vector on {device}")
+def _kv_pair(K, V, k_scale, v_scale, dev):
+    """Checks K and V rows: bf16 without scales, or E4M3 bytes (uint8) with fp32 [rows, n_kv_heads] scales; returns
+    (rows, width, leading dimension, that of the scales, type)."""
+    shape, dt, lds = K.shape, K.dtype, 0
+    if len(shape) != 2 or V.shape != shape or V.dtype != dt or K.get_device() != dev or V.get_device() != dev:
+        raise ValueError("K and V: expected two 2-D tensors of one shape and type on the call's device")
+    rows, width = shape
+    (ld, one), sv = K.stride(), V.stride()
+    if width % HEAD_DIM or ((one != 1 or sv[1] != 1) and width > 1) or (rows > 1 and sv[0] != ld):
+        raise ValueError(f"K and V: expected [rows, n_kv_heads * {HEAD_DIM}] with unit column stride and one pitch")
+    if rows <= 1:
+        ld = width
+    if dt is _BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("bf16 rows have no scales")
+        return rows, width, ld, 0, FL_BF16
+    if dt is not _U8 or k_scale is None or v_scale is None:
+        raise ValueError("K and V: expected bf16 rows, or uint8 (E4M3) rows with k_scale and v_scale")
+    heads = width // HEAD_DIM
+    for t in (k_scale, v_scale):
+        if t.dtype is not _F32 or t.shape != (rows, heads) or t.get_device() != dev or \
+                (heads > 1 and t.stride(1) != 1):
+            raise ValueError("k_scale and v_scale: expected fp32 [rows, n_kv_heads] with unit column stride")
+    lds = k_scale.stride(0) if rows > 1 else heads
+    if rows > 1 and v_scale.stride(0) != lds:
+        raise ValueError("k_scale and v_scale must share one leading dimension")
+    return rows, width, ld, lds, FL_E4M3
+
+
+def _ints(t, name, dev):
+    if t.dtype is not _I32 or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 vector on the call's device")
     return t.numel()
 
 
-def _cache(k_pages, v_pages, page_table, seq_lens, ks, vs):
-    """Checks the paged cache; returns (n_kv_heads, page_size, num_pages, max_pages, ldt, page_pitch, scale_pitch)."""
-    dev, shape = k_pages.device, k_pages.shape
-    if k_pages.dtype not in (torch.bfloat16, torch.uint8) or not k_pages.is_cuda or len(shape) != 4 or \
-            shape[3] != HEAD_DIM:
-        raise ValueError(f"k_pages: expected bf16 or uint8 (E4M3) [num_pages, n_kv_heads, page_size, {HEAD_DIM}]")
+def _cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
+    """Checks the paged cache; returns (batch, n_kv_heads, page_size, num_pages, max_pages, ldt, page_pitch,
+    scale_pitch, type)."""
+    shape, dt = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or shape[3] != HEAD_DIM or (dt is not _BF16 and dt is not _U8) or v_pages.shape != shape or \
+            v_pages.dtype is not dt or k_pages.get_device() != dev or v_pages.get_device() != dev:
+        raise ValueError(f"k_pages and v_pages: expected two bf16 or uint8 (E4M3) tensors [num_pages, n_kv_heads, "
+                         f"page_size, {HEAD_DIM}] on the call's device")
     n_pages, n_kv, page, _ = shape
-    pitch = k_pages.stride(0) if n_pages > 1 else n_kv * page * HEAD_DIM
-    for t in (k_pages, v_pages):
-        if t.dtype != k_pages.dtype or t.shape != shape or t.device != dev:
-            raise ValueError("k_pages and v_pages must share type, shape and device")
-        if n_pages and (t.stride()[1:] != (page * HEAD_DIM, HEAD_DIM, 1) or (n_pages > 1 and t.stride(0) != pitch)):
-            raise ValueError("k_pages and v_pages: expected contiguous pages with one shared pitch")
+    pitch = n_kv * page * HEAD_DIM
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        if n_pages > 1:
+            pitch = k_pages.stride(0)
+        for t in (k_pages, v_pages):
+            if n_pages and (t.stride()[1:] != (page * HEAD_DIM, HEAD_DIM, 1) or (n_pages > 1 and t.stride(0) != pitch)):
+                raise ValueError("k_pages and v_pages: expected contiguous pages with one shared pitch")
     spitch = 0
-    if k_pages.dtype == torch.uint8:
+    if dt is _U8:
         if ks is None or vs is None:
             raise ValueError("an E4M3 cache needs k_page_scale and v_page_scale")
-        spitch = ks.stride(0) if n_pages > 1 else n_kv * page
+        spitch = n_kv * page if n_pages <= 1 or ks.is_contiguous() else ks.stride(0)
         for t in (ks, vs):
-            if t.dtype != torch.float32 or t.shape != shape[:3] or t.device != dev or \
-                    (n_pages and (t.stride()[1:] != (page, 1) or (n_pages > 1 and t.stride(0) != spitch))):
+            if t.dtype is not _F32 or t.shape != shape[:3] or t.get_device() != dev or not (
+                    t.is_contiguous() and spitch == n_kv * page or
+                    t.stride()[1:] == (page, 1) and (n_pages <= 1 or t.stride(0) == spitch)):
                 raise ValueError("k_page_scale and v_page_scale: expected fp32 [num_pages, n_kv_heads, page_size] "
                                  "with contiguous pages and one shared pitch")
     elif ks is not None or vs is not None:
         raise ValueError("a bf16 cache has no scales")
     batch = _ints(seq_lens, "seq_lens", dev)
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev or \
-            page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table: expected int32 [batch, max_pages] with unit column stride")
+    if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.get_device() != dev or \
+            page_table.shape[0] != batch:
+        raise ValueError("page_table: expected int32 [batch, max_pages] on the call's device")
     max_pages = page_table.shape[1]
-    ldt = page_table.stride(0) if batch > 1 else max_pages
-    return n_kv, page, n_pages, max_pages, ldt, pitch, spitch
+    ldt, one = page_table.stride()
+    if one != 1 and max_pages > 1:
+        raise ValueError("page_table: expected unit column stride")
+    return (batch, n_kv, page, n_pages, max_pages, ldt if batch > 1 else max_pages, pitch, spitch,
+            FL_E4M3 if dt is _U8 else FL_BF16)
 
 
-def _on_device(*tensors):
-    """All tensors on one device; calls run there whatever the current device is."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on one device")
-    return torch.cuda.device(dev)
+def _query(t, name, dev):
+    """Checks Q or O, bf16 [rows, n_heads * 128]; returns (rows, width, leading dimension)."""
+    if t.dtype is not _BF16 or t.dim() != 2 or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a 2-D bf16 tensor on the call's device")
+    rows, width = t.shape
+    ld, one = t.stride()
+    if width % HEAD_DIM or (one != 1 and width > 1):
+        raise ValueError(f"{name}: expected [rows, n_heads * {HEAD_DIM}] with unit column stride")
+    return rows, width, ld if rows > 1 else width
+
+
+def _space(t, dev):
+    if t.dtype is not _U8 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor on the call's device")
+    return t.numel()
 
 
 def paged_kv_append(K, V, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None,
@@ -647,21 +687,20 @@ def paged_kv_append(K, V, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
     last tokens: seq_lens holds the lengths after the call.  bf16 rows go into a bf16 cache as they are and into
     an E4M3 cache (uint8 pages with fp32 page scales) quantised with one scale per (token, kv head); uint8 rows
     with k_scale and v_scale (as fused_qkv_rope_fp8kv returns them) go into an E4M3 cache as they are."""
-    ld, lds = _kv_pair(K, V, k_scale, v_scale)
-    n_kv, page, n_pages, max_pages, ldt, pitch, spitch = _cache(k_pages, v_pages, page_table, seq_lens, k_page_scale,
-                                                               v_page_scale)
-    T, batch = K.shape[0], seq_lens.numel()
-    if K.shape[1] != n_kv * HEAD_DIM:
+    dev = K.get_device()
+    T, width, ld, lds, rows_dt = _kv_pair(K, V, k_scale, v_scale, dev)
+    batch, n_kv, page, n_pages, max_pages, ldt, pitch, spitch, dt = _cache(k_pages, v_pages, page_table, seq_lens,
+                                                                          k_page_scale, v_page_scale, dev)
+    if width != n_kv * HEAD_DIM:
         raise ValueError("the rows must have the cache's n_kv_heads")
-    if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", K.device) != batch + 1:
+    if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", dev) != batch + 1:
         raise ValueError("cu_seqlens must have batch + 1 entries")
-    with _on_device(K, V, k_pages, k_scale, v_scale):
-        st = load().paged_kv_append(_ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), _ptr(k_pages), _ptr(v_pages),
-                                    _ptr(k_page_scale), _ptr(v_page_scale), _ptr(page_table), _ptr(seq_lens),
-                                    _ptr(cu_seqlens), T, batch, n_kv, HEAD_DIM, page, n_pages, max_pages, ld, lds, ldt,
-                                    pitch, spitch, FL_E4M3 if K.dtype == torch.uint8 else FL_BF16,
-                                    FL_E4M3 if k_pages.dtype == torch.uint8 else FL_BF16, _stream(stream))
-    _check("paged_kv_append", st)
+    st = _on(dev, load().paged_kv_append,
+             (K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), k_pages.data_ptr(), v_pages.data_ptr(),
+              _addr(k_page_scale), _addr(v_page_scale), page_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens),
+              T, batch, n_kv, HEAD_DIM, page, n_pages, max_pages, ld, lds, ldt, pitch, spitch, rows_dt, dt), stream)
+    if st:
+        _check("paged_kv_append", st)
 
 
 def attention_decode_workspace(device=None) -> torch.Tensor:
@@ -674,27 +713,26 @@ def attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale=Non
     """Attention of one new token per sequence, Q bf16 [batch, n_heads * 128], over the paged cache.
 
     scale: of the logits, 1 / sqrt(128) by default.  Returns O bf16 [batch, n_heads * 128]."""
-    n_kv, page, n_pages, max_pages, ldt, pitch, spitch = _cache(k_pages, v_pages, page_table, seq_lens, k_page_scale,
-                                                               v_page_scale)
-    batch, width = Q.shape
-    ldq = _mat(Q, "Q", torch.bfloat16)
-    if width % HEAD_DIM != 0 or batch != seq_lens.numel():
-        raise ValueError("Q: expected [batch, n_heads * 128]")
+    dev = Q.get_device()
+    rows, width, ldq = _query(Q, "Q", dev)
+    batch, n_kv, page, n_pages, max_pages, ldt, pitch, spitch, dt = _cache(k_pages, v_pages, page_table, seq_lens,
+                                                                          k_page_scale, v_page_scale, dev)
+    if rows != batch:
+        raise ValueError("Q: expected one row for each sequence")
     if O is None:
-        O = torch.empty((batch, width), dtype=torch.bfloat16, device=Q.device)
-    ldo = _mat(O, "O", torch.bfloat16)
-    if O.shape != Q.shape:
+        O = torch.empty((rows, width), dtype=_BF16, device=Q.device)
+    o_rows, o_width, ldo = _query(O, "O", dev)
+    if o_rows != rows or o_width != width:
         raise ValueError("O must have Q's shape")
     if workspace is None:
         workspace = attention_decode_workspace(Q.device)
-    with _on_device(Q, k_pages, O, workspace):
-        st = load().attention_decode(_ptr(Q), _ptr(k_pages), _ptr(v_pages), _ptr(k_page_scale), _ptr(v_page_scale),
-                                     _ptr(page_table), _ptr(seq_lens), _ptr(O), batch, width // HEAD_DIM, n_kv,
-                                     HEAD_DIM, page, n_pages, max_pages, ldq, ldo, ldt, pitch, spitch,
-                                     HEAD_DIM ** -0.5 if scale is None else scale,
-                                     FL_E4M3 if k_pages.dtype == torch.uint8 else FL_BF16, _ptr(workspace),
-                                     workspace.numel(), _stream(stream))
-    _check("attention_decode", st)
+    st = _on(dev, load().attention_decode,
+             (Q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale),
+              page_table.data_ptr(), seq_lens.data_ptr(), O.data_ptr(), batch, width // HEAD_DIM, n_kv, HEAD_DIM, page,
+              n_pages, max_pages, ldq, ldo, ldt, pitch, spitch, HEAD_DIM ** -0.5 if scale is None else scale, dt,
+              workspace.data_ptr(), _space(workspace, dev)), stream)
+    if st:
+        _check("attention_decode", st)
     return O
 
 
@@ -710,35 +748,31 @@ def attention_prefill(Q, K, V, cu_seqlens=None, seq_len: int = 0, k_scale=None, 
     codes with fp32 [M, n_kv_heads] scales, as fused_qkv_rope_fp8kv returns them).
 
     Sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; without cu_seqlens the rows are sequences of
-    seq_len tokens laid end to end (0: one sequence).  Rows of O in no sequence stay as they were.  scale: of the
-    logits, 1 / sqrt(128) by default.  Returns O bf16 [M, n_heads * 128]."""
-    ldkv, lds = _kv_pair(K, V, k_scale, v_scale)
-    M, width = Q.shape
-    _mat(Q, "Q", torch.bfloat16)
-    if width % HEAD_DIM != 0 or K.shape[0] != M:
-        raise ValueError("Q: expected [M, n_heads * 128] with as many rows as K and V")
-    n_kv, kv_width = K.shape[1] // HEAD_DIM, K.shape[1]
-    batch = 0 if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", Q.device) - 1
+    seq_len tokens laid end to end (0: one sequence).  Rows of O in no sequence stay as they were (zeros where O
+    is allocated here).  scale: of the logits, 1 / sqrt(128) by default.  Returns O bf16 [M, n_heads * 128]."""
+    dev = Q.get_device()
+    M, width, ldq = _query(Q, "Q", dev)
+    rows, kv_width, ldkv, lds, dt = _kv_pair(K, V, k_scale, v_scale, dev)
+    if rows != M:
+        raise ValueError("Q, K and V must have the same number of rows")
+    n_kv = kv_width // HEAD_DIM
+    batch = 0 if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", dev) - 1
     if batch < 0:
         raise ValueError("cu_seqlens must have batch + 1 entries")
-    fp8 = K.dtype == torch.uint8
     if O is None:
-        O = (torch.empty if cu_seqlens is None else torch.zeros)((M, width), dtype=torch.bfloat16, device=Q.device)
-    _mat(O, "O", torch.bfloat16)
-    if O.shape != Q.shape:
+        O = (torch.empty if cu_seqlens is None else torch.zeros)((M, width), dtype=_BF16, device=Q.device)
+    o_rows, o_width, ldo = _query(O, "O", dev)
+    if o_rows != M or o_width != width:
         raise ValueError("O must have Q's shape")
     if workspace is None:
-        workspace = attention_prefill_workspace(M, n_kv, fp8, Q.device)
-    if M == 1:
-        ldkv, lds = kv_width, n_kv
-    with _on_device(Q, K, V, O, workspace, k_scale, v_scale):
-        st = load().attention_prefill(_ptr(Q), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), _ptr(cu_seqlens),
-                                      _ptr(O), M, batch, width // HEAD_DIM, n_kv, HEAD_DIM, seq_len or max(M, 1),
-                                      _ld(Q, width, width), ldkv, lds, _ld(O, width, width),
-                                      HEAD_DIM ** -0.5 if scale is None else scale, 1 if causal else 0,
-                                      FL_E4M3 if fp8 else FL_BF16, _ptr(workspace), workspace.numel(),
-                                      _stream(stream))
-    _check("attention_prefill", st)
+        workspace = attention_prefill_workspace(M, n_kv, dt == FL_E4M3, Q.device)
+    st = _on(dev, load().attention_prefill,
+             (Q.data_ptr(), K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens),
+              O.data_ptr(), M, batch, width // HEAD_DIM, n_kv, HEAD_DIM, seq_len or max(M, 1), ldq, ldkv, lds, ldo,
+              HEAD_DIM ** -0.5 if scale is None else scale, 1 if causal else 0, dt, workspace.data_ptr(),
+              _space(workspace, dev)), stream)
+    if st:
+        _check("attention_prefill", st)
     return O
 
 

@@ -40,7 +40,7 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecSub = 16;                    // tokens of one warp's step
 constexpr int kDecUnit = kDecWarps * kDecSub;  // tokens of one unit of work
 constexpr int kDecMaxCtas = 640;
-constexpr int kDecPartFloats = 16 * (kHeadDim + 3);  // (o[128], m, m', l) of up to 16 heads
+constexpr int kDecPartFloats = 16 * (kHeadDim + 4);  // o[16][128], then (m, m', l, 0) of up to 16 heads
 constexpr float kDecNone = -3e38f;             // a maximum over nothing: any finite logit passes it
 constexpr float kDecLazy = 8.f;
 constexpr float kDecLift = 7.f;                // E4M3: weights are lifted by 2^7 in fp16
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int heads_v = p.c.n_kv * p.chunks;  // independent (kv head, chunk) pairs of a sequence
   const long long capacity = static_cast<long long>(p.c.max_pages) * p.c.page_size;
-  const int G = gridDim.x, cta = blockIdx.x;
+  const int cta = blockIdx.x;
 
   // ---- plan: total units, and where this CTA's first unit lies
   auto block_scan = [&](int b0, int& mine, long long& before) -> long long {  // of 128 sequences from b0
@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
   long long before, total = 0;
   for (int b0 = 0; b0 < p.c.batch; b0 += kDecThreads) total += block_scan(b0, mine, before);
   total *= heads_v;
+  const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // each has a unit at least
+  if (cta >= G) return;
   const long long u0 = total * cta / G, u1 = total * (cta + 1) / G;
-  if (u0 == u1) return;
   {
     long long base = 0;
     for (int b0 = 0;; b0 += kDecThreads) {
@@ -461,10 +462,12 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
     }
 
     // ---- the CTA's four pieces become one: finished here, or a part of a cut (sequence, head)
-    const long long last_unit = seg_first + seg.n_units - 1;
-    const int c_first = static_cast<int>(((seg_first + 1) * G - 1) / total);
-    const int c_last = static_cast<int>(((last_unit + 1) * G - 1) / total);
-    const bool whole = c_first == c_last;
+    const bool whole = seg_first >= u0 && seg_first + seg.n_units <= u1;
+    int c_first = cta, c_last = cta;  // the CTAs that share it
+    if (!whole) {
+      c_first = static_cast<int>(((seg_first + 1) * G - 1) / total);
+      c_last = static_cast<int>(((seg_first + seg.n_units) * G - 1) / total);
+    }
     float* part = p.parts + (static_cast<long long>(cta) * 2 + (cta == c_first ? 1 : 0)) * kDecPartFloats;
     const bool spoiled = __any_sync(~0u, bad);
     if (spoiled && lane == 0 && atomicCAS(p.status + ST_CODE, 0, static_cast<int>(FL_ERR_INVALID_ARG)) == 0)
@@ -511,9 +514,9 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
           const float r = seg.len == 0 ? 0.f : acc * (ex2(MV - M) / L);
           p.O[seg.b * p.ldo + static_cast<long long>(head0 + nt * 8 + h) * kHeadDim + tid] = __float2bfloat16_rn(r);
         } else {
-          float* dst = part + (nt * 8 + h) * (kHeadDim + 3);
-          __stcg(dst + tid, acc);
-          if (tid < 3) __stcg(dst + kHeadDim + tid, tid == 0 ? M : tid == 1 ? MV : L);
+          __stcg(part + (nt * 8 + h) * kHeadDim + tid, acc);
+          if (tid == 0)
+            __stcg(reinterpret_cast<float4*>(part + 16 * kHeadDim) + nt * 8 + h, make_float4(M, MV, L, 0.f));
         }
       }
       __syncthreads();
@@ -521,34 +524,55 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
     if (!whole) {
       __threadfence();
       __syncthreads();
-      // every CTA of the cut that has units arrives once; with fewer units than CTAs each of them is one unit
-      const unsigned want = static_cast<unsigned>(total >= G ? c_last - c_first + 1 : seg.n_units);
       if (tid == 0) {
-        const unsigned n = atomicAdd(p.counters + c_first, 1u);
-        if (n + 1 == want) p.counters[c_first] = 0;
-        plan[0] = n + 1 == want;
+        const unsigned n = atomicAdd(p.counters + c_first, 1u), want = static_cast<unsigned>(c_last - c_first);
+        if (n == want) p.counters[c_first] = 0;
+        plan[0] = n == want;
       }
       __syncthreads();
-      if (plan[0] != 0) {
+      if (plan[0] != 0) {  // the last to arrive: a warp joins a head, lane i weighs piece i, then holds 4 dimensions
         __threadfence();
-        auto src = [&](int c, int h) {
-          return p.parts + (static_cast<long long>(c) * 2 + (c == c_first)) * kDecPartFloats + h * (kHeadDim + 3);
-        };
-        auto has = [&](int c) { return total >= G || total * c / G != total * (c + 1) / G; };
-        for (int h = 0; h < n_heads; ++h) {
-          float M = kDecNone, MV = kDecNone, L = 0.f, acc = 0.f;
-          for (int c = c_first; c <= c_last; ++c) {
-            if (!has(c)) continue;
-            const float* s = src(c, h);
-            const float pm = __ldcg(s + kHeadDim), pmv = __ldcg(s + kHeadDim + 1);
-            const float nm = fmaxf(M, pm), nmv = fmaxf(MV, pmv);
-            L = L * ex2(M - nm) + __ldcg(s + kHeadDim + 2) * ex2(pm - nm);
-            acc = acc * ex2(MV - nmv) + __ldcg(s + tid) * ex2(pmv - nmv);
+        auto src = [&](int c) { return p.parts + (static_cast<long long>(c) * 2 + (c == c_first)) * kDecPartFloats; };
+        for (int h = warp; h < n_heads; h += kDecWarps) {
+          float M = kDecNone, MV = kDecNone, L = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c0 = c_first; c0 <= c_last; c0 += 32) {
+            const int n = min(32, c_last - c0 + 1);
+            float4 st = make_float4(kDecNone, kDecNone, 0.f, 0.f);
+            if (lane < n) st = __ldcg(reinterpret_cast<const float4*>(src(c0 + lane) + 16 * kHeadDim) + h);
+            float nm = fmaxf(M, st.x), nmv = fmaxf(MV, st.y);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+              nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, d));
+              nmv = fmaxf(nmv, __shfl_xor_sync(~0u, nmv, d));
+            }
+            float sum = st.z * ex2(st.x - nm);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            L = L * ex2(M - nm) + sum;
+            const float w = lane < n ? ex2(st.y - nmv) : 0.f, old = ex2(MV - nmv);
+            acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
             M = nm;
             MV = nmv;
+            for (int i0 = 0; i0 < n; i0 += 8) {
+              float4 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(src(c0 + i0 + i) + h * kHeadDim) + lane);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl_sync(~0u, w, i0 + i);
+                acc.x += v[i].x * wi, acc.y += v[i].y * wi, acc.z += v[i].z * wi, acc.w += v[i].w * wi;
+              }
+            }
           }
-          const float r = acc * (ex2(MV - M) / L);
-          p.O[seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + tid] = __float2bfloat16_rn(r);
+          const float r = ex2(MV - M) / L;
+          uint2 out;
+          out.x = pack_bf16x2(acc.x * r, acc.y * r);
+          out.y = pack_bf16x2(acc.z * r, acc.w * r);
+          *reinterpret_cast<uint2*>(p.O + seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + lane * 4) = out;
         }
       }
       __syncthreads();
