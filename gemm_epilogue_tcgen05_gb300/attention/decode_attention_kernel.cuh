@@ -6,14 +6,15 @@
 // bytes, so it runs at the memory's rate as long as enough loads are in flight and nothing else keeps a warp
 // from issuing the next ones.
 //
-// Split.  The work is cut into units of 64 tokens of one (sequence, kv head); every sequence has at least one.
+// Split.  The work is cut into units of 64 (bf16) or 128 (E4M3) tokens of one (sequence, kv head); every sequence has at least one.
 // CTA i of G takes units [i T / G, (i + 1) T / G) in the order (sequence, kv head, unit), so every CTA streams
 // the same number of bytes whatever the lengths are, and a captured launch adapts to them.  A (sequence, kv
 // head) that lies in one CTA is finished there; one that is cut writes (m, l, o) of each piece to the workspace,
 // and the last CTA to arrive joins the pieces in the order of the CTAs (the result does not depend on which
 // came last).
 //
-// Inside a CTA each of four warps streams its own tokens, 16 at a time, through its own ring of cp.async
+// Inside a CTA each of four warps streams its own tokens, 16 (bf16) or 32 (E4M3, two independent tiles: the
+// conversions make a step longer) at a time, through its own ring of cp.async
 // stages: no barrier in the loop, and the ring runs on over the end of a sequence.  Both products run on the
 // tensor cores with the tokens on the M side, S^T = K Q^T and O^T = V^T P^T (m16n8k16: 8 query heads of a group
 // in the N columns, two column tiles for groups above 8), so a small group wastes little.  The assignment of
@@ -37,8 +38,6 @@ namespace fl {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecSub = 16;                    // tokens of one warp's step
-constexpr int kDecUnit = kDecWarps * kDecSub;  // tokens of one unit of work
 constexpr int kDecMaxCtas = 640;
 constexpr int kDecPartFloats = 16 * (kHeadDim + 4);  // o[16][128], then (m, m', l, 0) of up to 16 heads
 constexpr float kDecNone = -3e38f;             // a maximum over nothing: any finite logit passes it
@@ -61,11 +60,18 @@ struct DecodeParams {
 template <bool FP8, int NT>
 struct DecodeTraits {
   static constexpr int kRowBytes = FP8 ? 128 : 256;
-  static constexpr int kTile = kDecSub * kRowBytes;
-  static constexpr int kStage = 2 * kTile + (FP8 ? 2 * kDecSub * 4 : 0);
-  static constexpr int kStages = FP8 ? 5 : 3;
-  static constexpr int kMerge = kDecWarps * 8 * kHeadDim * 4;
-  static constexpr int kSmem = kDecWarps * kStages * kStage + kMerge + kDecWarps * 8 * NT * 3 * 4 + 128;
+  static constexpr int kSubs = FP8 ? 2 : 1;          // 16-token tiles of one warp's step
+  static constexpr int kStep = 16 * kSubs;
+  static constexpr int kUnit = kDecWarps * kStep;    // tokens of one unit of work
+  static constexpr int kTile = kStep * kRowBytes;
+  static constexpr int kStage = 2 * kTile + (FP8 ? 2 * kStep * 4 : 0);
+  // CTAs on an SM and stages of a warp's ring.  Measured (64 sequences of 2048-8192 tokens, E4M3): 2 x 3 stages
+  // 106 us, 3 x 2 111 us; (24 sequences of 5-4096 tokens | 3 of 15000-32768, bf16): 2 x 3 29.7 | 87.6 us, 3 x 2
+  // 25.0 | 89.0 us.  Two column tiles need the registers of 3 CTAs.
+  static constexpr int kCtas = !FP8 && NT == 1 ? 3 : 2;
+  static constexpr int kStages = kCtas == 3 ? 2 : 3;
+  static constexpr int kMerge = kDecWarps * 4 * kHeadDim * 4;  // four heads at a time
+  static constexpr int kSmem = kDecWarps * kStages * kStage + kMerge + kDecWarps * 4 * 16 + 128;
 };
 
 __device__ __forceinline__ float lg2(float x) {
@@ -119,28 +125,32 @@ struct DecodeSeg {
   bool bad;          // its length is outside the table
 };
 
+template <int UNIT>
 __device__ __forceinline__ int decode_units(int len, long long capacity, bool& bad) {
   bad = len < 0 || len > capacity;
-  return bad || len == 0 ? 1 : (len - 1) / kDecUnit + 1;
+  return bad || len == 0 ? 1 : (len - 1) / UNIT + 1;
 }
 
 template <bool FP8, int NT>
-__global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) attention_decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = DecodeTraits<FP8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem + kDecWarps * T::kStages * T::kStage);
-  float* stats = merge + T::kMerge / 4;  // [3][warp][8 NT]: m, m', l
-  long long* plan = reinterpret_cast<long long*>(stats + kDecWarps * 8 * NT * 3);
+  float4* stats = reinterpret_cast<float4*>(merge + T::kMerge / 4);  // [warp][4 heads]: m, m', l
+  long long* plan = reinterpret_cast<long long*>(stats + kDecWarps * 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int heads_v = p.c.n_kv * p.chunks;  // independent (kv head, chunk) pairs of a sequence
   const long long capacity = static_cast<long long>(p.c.max_pages) * p.c.page_size;
   const int cta = blockIdx.x;
 
+  griddep_wait();  // launched as a dependent: nothing is read before the kernel in front has finished
+  griddep_launch_dependents();
+
   // ---- plan: total units, and where this CTA's first unit lies
   auto block_scan = [&](int b0, int& mine, long long& before) -> long long {  // of 128 sequences from b0
     const int b = b0 + tid;
     bool bad;
-    mine = b < p.c.batch ? decode_units(__ldg(p.c.lens + b), capacity, bad) : 0;
+    mine = b < p.c.batch ? decode_units<T::kUnit>(__ldg(p.c.lens + b), capacity, bad) : 0;
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -184,11 +194,11 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
   long long left = u1 - u0;
   auto begin_seg = [&](DecodeSeg& s, int tile, long long units_left) {
     if (tile == 0 && s.h == 0) s.len = __ldg(p.c.lens + s.b);
-    s.n_units = decode_units(s.len, capacity, s.bad);
+    s.n_units = decode_units<T::kUnit>(s.len, capacity, s.bad);
     s.units = static_cast<int>(min(static_cast<long long>(s.n_units - tile), units_left));
     const int end = s.bad ? 0 : s.len;
-    s.t0 = tile * kDecUnit;
-    s.t1 = static_cast<int>(min(static_cast<long long>(end), (static_cast<long long>(tile) + s.units) * kDecUnit));
+    s.t0 = tile * T::kUnit;
+    s.t1 = static_cast<int>(min(static_cast<long long>(end), (static_cast<long long>(tile) + s.units) * T::kUnit));
   };
   auto next_seg = [&](DecodeSeg& s, long long units_left) {
     if (++s.h == heads_v) {
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
     const long long in = plan[9];
     seg.len = __ldg(p.c.lens + seg.b);
     bool bad;
-    const int n = decode_units(seg.len, capacity, bad);
+    const int n = decode_units<T::kUnit>(seg.len, capacity, bad);
     seg.h = static_cast<int>(in / n);
     const int tile = static_cast<int>(in - static_cast<long long>(seg.h) * n);
     seg_first = u0 - tile;
@@ -214,18 +224,25 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
   // ---- producer side of this warp's ring
   DecodeSeg ps = seg;
   long long p_left = left;
-  int pt = ps.t0 + warp * kDecSub, entry = 0, p_stage = 0;
+  int pt = ps.t0 + warp * T::kStep, entry = 0, p_stage = 0;
   uint32_t bad_steps = 0;  // stages whose page-table entry is outside the cache
-  const bool one_page = (p.c.page_size & (kDecSub - 1)) == 0;  // a step's 16 tokens lie in one page
+  bool fresh = true;
+  const bool one_page = (p.c.page_size & (T::kStep - 1)) == 0;  // a step's 16 tokens lie in one page
   auto page_of = [&](int pos) { return p.page_shift >= 0 ? pos >> p.page_shift : pos / p.c.page_size; };
   auto settle = [&]() {  // moves on to this warp's next step and fetches its page-table entry
     while (pt >= ps.t1) {
       p_left -= ps.units;
       if (p_left <= 0) return;
       next_seg(ps, p_left);
-      pt = ps.t0 + warp * kDecSub;
+      pt = ps.t0 + warp * T::kStep;
+      fresh = true;
     }
-    const int pos = one_page ? pt : min(pt + (lane & 15), ps.t1 - 1);
+    if (fresh) {  // the query rows of the segment that begins, into L2
+      fresh = false;
+      const char* row = reinterpret_cast<const char*>(p.Q + ps.b * p.ldq + static_cast<long long>(ps.h / p.chunks) * p.group * kHeadDim);
+      if (lane < 2 * p.group) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + lane * 128));
+    }
+    const int pos = one_page ? pt : min(pt + (lane & (T::kStep - 1)), ps.t1 - 1);
     entry = __ldg(p.c.table + ps.b * p.c.ldt + page_of(pos));
   };
   const uint32_t ring = smem_u32(smem) + warp * T::kStages * T::kStage;
@@ -233,43 +250,51 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
     if (p_left > 0) {
       constexpr int kChunks = T::kRowBytes / 16, kRowsPer = 32 / kChunks;
       const uint32_t dst = ring + p_stage * T::kStage;
-      const int kvh = ps.h / p.chunks;
-      const int mypos = one_page ? pt : min(pt + (lane & 15), ps.t1 - 1);
-      const int slot = mypos - page_of(mypos) * p.c.page_size;
+      const int kvh = ps.h / p.chunks, rows = ps.t1 - pt;
       const bool ok = static_cast<unsigned>(entry) < static_cast<unsigned>(p.c.num_pages);
       bad_steps = (bad_steps & ~(1u << p_stage)) | (ok ? 0u : 1u << p_stage);
-      const int c = lane % kChunks;
+      const int mypos = one_page ? pt : min(pt + (lane & (T::kStep - 1)), ps.t1 - 1);
+      const int slot = mypos - page_of(mypos) * p.c.page_size, mypage = ok ? entry : 0;
+      const int c = lane % kChunks, row0 = lane / kChunks;
+      const long long cell = static_cast<long long>(kvh) * p.c.page_size + slot;
+      if (one_page) {
+        const long long byte = (mypage * p.c.page_pitch + (cell + row0) * kHeadDim) * (FP8 ? 1 : 2) + c * 16;
+        const uint8_t* ksrc = static_cast<const uint8_t*>(p.c.k) + byte;
+        const uint8_t* vsrc = static_cast<const uint8_t*>(p.c.v) + byte;
 #pragma unroll
-      for (int i = 0; i < kDecSub / kRowsPer; ++i) {
-        const int row = lane / kChunks + i * kRowsPer;
-        int page = entry, s = slot + row;
-        bool there = ok && pt + row < ps.t1;
-        if (!one_page) {
-          page = __shfl_sync(~0u, entry, row);
-          s = __shfl_sync(~0u, slot, row);
-          there = pt + row < ps.t1 && static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
+        for (int i = 0; i < T::kStep / kRowsPer; ++i) {
+          const int row = row0 + i * kRowsPer;
+          const bool there = ok && row < rows;
+          cp_async_16_or_zero(dst + row * T::kRowBytes + ((c ^ ((row & 1) << 2)) << 4), ksrc + i * 512, there);
+          cp_async_16_or_zero(dst + T::kTile + row * T::kRowBytes + ((c ^ (row & 6)) << 4), vsrc + i * 512, there);
         }
-        const long long at =
-            there ? page * p.c.page_pitch + (static_cast<long long>(kvh) * p.c.page_size + s) * kHeadDim : 0;
-        const long long byte = at * (FP8 ? 1 : 2) + c * 16;
-        cp_async_16_or_zero(dst + row * T::kRowBytes + ((c ^ ((row & 1) << 2)) << 4),
-                            static_cast<const uint8_t*>(p.c.k) + byte, there);
-        cp_async_16_or_zero(dst + T::kTile + row * T::kRowBytes + ((c ^ (row & 6)) << 4),
-                            static_cast<const uint8_t*>(p.c.v) + byte, there);
+      } else {
+#pragma unroll
+        for (int i = 0; i < T::kStep / kRowsPer; ++i) {
+          const int row = row0 + i * kRowsPer;
+          const int page = __shfl_sync(~0u, ok ? entry : -1, row), s = __shfl_sync(~0u, slot, row);
+          const bool there = page >= 0 && row < rows;
+          const long long at = max(page, 0) * p.c.page_pitch + (static_cast<long long>(kvh) * p.c.page_size + s) * kHeadDim;
+          const long long byte = at * (FP8 ? 1 : 2) + c * 16;
+          cp_async_16_or_zero(dst + row * T::kRowBytes + ((c ^ ((row & 1) << 2)) << 4),
+                              static_cast<const uint8_t*>(p.c.k) + byte, there);
+          cp_async_16_or_zero(dst + T::kTile + row * T::kRowBytes + ((c ^ (row & 6)) << 4),
+                              static_cast<const uint8_t*>(p.c.v) + byte, there);
+        }
       }
-      if (FP8) {  // lanes 0..15 K's scales, 16..31 V's
-        const int row = lane & 15;
-        const bool there = ok && pt + row < ps.t1;
-        const int s = one_page ? slot + row : slot;
-        const long long at = there ? entry * p.c.scale_pitch + static_cast<long long>(kvh) * p.c.page_size + s : 0;
-        cp_async_4_or_zero(dst + 2 * T::kTile + lane * 4, (lane < 16 ? p.c.ks : p.c.vs) + at, there);
+      if (FP8) {  // lane = row of the step
+        const bool there = ok && lane < rows;
+        const long long at = mypage * p.c.scale_pitch + cell + (one_page ? lane : 0);
+        cp_async_4_or_zero(dst + 2 * T::kTile + lane * 4, p.c.ks + at, there);
+        cp_async_4_or_zero(dst + 2 * T::kTile + 128 + lane * 4, p.c.vs + at, there);
       }
-      pt += kDecUnit;
+      pt += T::kUnit;
       settle();
     }
     cp_async_commit();
     p_stage = p_stage + 1 == T::kStages ? 0 : p_stage + 1;
   };
+  int cut_b[2] = {0, 0}, cut_h[2] = {0, 0}, cut_first[2] = {-1, -1}, cut_last[2] = {-1, -1};
   settle();
 #pragma unroll
   for (int i = 0; i < T::kStages - 1; ++i) issue();
@@ -324,56 +349,62 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
       for (int i = 0; i < 2; ++i) m[nt][i] = mv[nt][i] = kDecNone, l[nt][i] = 0.f;
     }
 
-    for (int t = seg.t0 + warp * kDecSub; t < seg.t1; t += kDecUnit) {
+    for (int t = seg.t0 + warp * T::kStep; t < seg.t1; t += T::kUnit) {
       cp_async_wait<T::kStages - 2>();
       __syncwarp();
       const uint32_t kb = ring + stage * T::kStage, vb = kb + T::kTile;
-      // ---- S^T = K Q^T: 16 tokens x 8 heads, k = 128
-      float s[NT][2][4];
+      // ---- S^T = K Q^T: tiles of 16 tokens x 8 heads, k = 128
+      float s[NT][T::kSubs][2][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][0][i] = s[nt][1][i] = 0.f;
-      const uint32_t kr0 = kb + g * T::kRowBytes, kr1 = kr0 + 8 * T::kRowBytes;
+        for (int i = 0; i < T::kSubs * 8; ++i) s[nt][i >> 3][(i >> 2) & 1][i & 3] = 0.f;
+      const uint32_t kr = kb + g * T::kRowBytes;
       const int sw = (g & 1) << 2;
 #pragma unroll
-      for (int ci = 0; ci < T::kRowBytes / 64; ++ci) {
-        const uint32_t off = ((ci * 4 + q) ^ sw) << 4;
-        const uint4 x = ld_shared_v4(kr0 + off), y = ld_shared_v4(kr1 + off);
-        const uint32_t xr[4] = {x.x, x.y, x.z, x.w}, yr[4] = {y.x, y.y, y.z, y.w};
-        if (FP8) {
+      for (int ci = 0; ci < T::kRowBytes / 64; ++ci)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t a0 = e4m3x2_to_f16x2(xr[u] & 0xFFFFu), a2 = e4m3x2_to_f16x2(xr[u] >> 16);
-            const uint32_t a1 = e4m3x2_to_f16x2(yr[u] & 0xFFFFu), a3 = e4m3x2_to_f16x2(yr[u] >> 16);
+        for (int sub = 0; sub < T::kSubs; ++sub) {
+          const uint32_t at = kr + sub * 16 * T::kRowBytes + (((ci * 4 + q) ^ sw) << 4);
+          const uint4 x = ld_shared_v4(at), y = ld_shared_v4(at + 8 * T::kRowBytes);
+          const uint32_t xr[4] = {x.x, x.y, x.z, x.w}, yr[4] = {y.x, y.y, y.z, y.w};
+          if (FP8) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816<true>(s[nt][u & 1], a0, a1, a2, a3, qf[nt][ci * 8 + u * 2], qf[nt][ci * 8 + u * 2 + 1]);
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t a0 = e4m3x2_to_f16x2(xr[u] & 0xFFFFu), a2 = e4m3x2_to_f16x2(xr[u] >> 16);
+              const uint32_t a1 = e4m3x2_to_f16x2(yr[u] & 0xFFFFu), a3 = e4m3x2_to_f16x2(yr[u] >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_16816<true>(s[nt][sub][u & 1], a0, a1, a2, a3, qf[nt][ci * 8 + u * 2], qf[nt][ci * 8 + u * 2 + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_16816<false>(s[nt][sub][u], xr[u * 2], yr[u * 2], xr[u * 2 + 1], yr[u * 2 + 1],
+                                 qf[nt][ci * 4 + u * 2], qf[nt][ci * 4 + u * 2 + 1]);
           }
-        } else {
+        }
+      // ---- softmax: lane (g, q) holds tokens g, g + 8 of each tile for heads 2q, 2q + 1
+      float ks[T::kSubs * 2], lv[T::kSubs * 2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816<false>(s[nt][u], xr[u * 2], yr[u * 2], xr[u * 2 + 1], yr[u * 2 + 1], qf[nt][ci * 4 + u * 2],
-                               qf[nt][ci * 4 + u * 2 + 1]);
+      for (int r = 0; r < T::kSubs * 2; ++r) {
+        ks[r] = 1.f, lv[r] = 0.f;
+        if (FP8) {
+          const float* sc = reinterpret_cast<const float*>(smem + (kb - smem_u32(smem)) + 2 * T::kTile);
+          ks[r] = sc[g + r * 8];
+          lv[r] = lg2(sc[T::kStep + g + r * 8]);
         }
       }
-      // ---- softmax: lane (g, q) holds tokens g, g + 8 of heads 2q, 2q + 1
-      float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
-      if (FP8) {
-        const float* sc = reinterpret_cast<const float*>(smem + (kb - smem_u32(smem)) + 2 * T::kTile);
-        ks[0] = sc[g], ks[1] = sc[g + 8];
-        lv[0] = lg2(sc[16 + g]), lv[1] = lg2(sc[24 + g]);
-      }
-      float x[NT][4];
+      float x[NT][T::kSubs * 4];  // [tile][token half][head]
       bool rise = false;
-      const bool cut = t + kDecSub > seg.t1;
+      const bool cut = t + T::kStep > seg.t1;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = (s[nt][0][i] + s[nt][1][i]) * fac[nt][i & 1];
+        for (int i = 0; i < T::kSubs * 4; ++i) {
+          float v = (s[nt][i >> 2][0][i & 3] + s[nt][i >> 2][1][i & 3]) * fac[nt][i & 1];
           if (FP8) v *= ks[i >> 1];
           if (cut && t + g + (i >> 1) * 8 >= seg.t1) v = -INFINITY;
           x[nt][i] = v;
@@ -385,8 +416,12 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float a = fmaxf(m[nt][i], fmaxf(x[nt][i], x[nt][i + 2]));
-            float b = FP8 ? fmaxf(mv[nt][i], fmaxf(x[nt][i] + lv[0], x[nt][i + 2] + lv[1])) : 0.f;
+            float a = m[nt][i], b = mv[nt][i];
+#pragma unroll
+            for (int r = 0; r < T::kSubs * 2; ++r) {
+              a = fmaxf(a, x[nt][r * 2 + i]);
+              if (FP8) b = fmaxf(b, x[nt][r * 2 + i] + lv[r]);
+            }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
               a = fmaxf(a, __shfl_xor_sync(~0u, a, d));
@@ -400,57 +435,61 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
             for (int d = 0; d < 8; ++d) o[nt][d][i] *= down_o, o[nt][d][i + 2] *= down_o;
           }
       }
-      uint32_t pf[NT][2], pl[NT][2];  // P^T (B operand: tokens 2q, 2q + 1 | + 8 of head g)
+      uint32_t pf[NT][T::kSubs][2], pl[NT][T::kSubs][2];  // P^T (B operand: tokens 2q, 2q + 1 | + 8 of head g)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+        float w[T::kSubs * 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < T::kSubs * 4; ++i) {
           const float e = ex2(x[nt][i] - m[nt][i & 1]);
           l[nt][i & 1] += e;
           w[i] = FP8 ? ex2((x[nt][i] + lv[i >> 1]) - (mv[nt][i & 1] - kDecLift)) : e;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int r = 0; r < T::kSubs * 2; ++r) {
           if (FP8) {
-            pf[nt][i] = transpose8x8(pack_f16x2(w[i * 2], w[i * 2 + 1]));
+            pf[nt][r >> 1][r & 1] = transpose8x8(pack_f16x2(w[r * 2], w[r * 2 + 1]));
           } else {
-            const uint32_t hi = pack_bf16x2(w[i * 2], w[i * 2 + 1]);
-            pf[nt][i] = transpose8x8(hi);
-            pl[nt][i] = transpose8x8(pack_bf16x2(w[i * 2] - bf16_lo(hi), w[i * 2 + 1] - bf16_hi(hi)));
+            const uint32_t hi = pack_bf16x2(w[r * 2], w[r * 2 + 1]);
+            pf[nt][r >> 1][r & 1] = transpose8x8(hi);
+            pl[nt][r >> 1][r & 1] = transpose8x8(pack_bf16x2(w[r * 2] - bf16_lo(hi), w[r * 2 + 1] - bf16_hi(hi)));
           }
         }
       }
       // ---- O^T += V^T P^T: lane (g, q) brings tokens 2q, 2q + 1, 2q + 8, 2q + 9 of 16 dimensions
-      const uint32_t vr = vb + 2 * q * T::kRowBytes;
 #pragma unroll
-      for (int half = 0; half < T::kRowBytes / 128; ++half) {
-        const uint32_t off = ((half * 8 + g) ^ (2 * q)) << 4;
-        uint32_t v[4][4];
+      for (int sub = 0; sub < T::kSubs; ++sub) {
+        const uint32_t vr = vb + (sub * 16 + 2 * q) * T::kRowBytes;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint4 y = ld_shared_v4(vr + ((r & 1) + (r >> 1) * 8) * T::kRowBytes + off);
-          v[r][0] = y.x, v[r][1] = y.y, v[r][2] = y.z, v[r][3] = y.w;
-        }
+        for (int half = 0; half < T::kRowBytes / 128; ++half) {
+          const uint32_t off = ((half * 8 + g) ^ (2 * q)) << 4;
+          uint32_t v[4][4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (FP8) {
+          for (int r = 0; r < 4; ++r) {
+            const uint4 y = ld_shared_v4(vr + ((r & 1) + (r >> 1) * 8) * T::kRowBytes + off);
+            v[r][0] = y.x, v[r][1] = y.y, v[r][2] = y.z, v[r][3] = y.w;
+          }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t lo = __byte_perm(v[0][w], v[1][w], u ? 0x7362 : 0x5140);
-              const uint32_t hi = __byte_perm(v[2][w], v[3][w], u ? 0x7362 : 0x5140);
-              const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xFFFFu), a1 = e4m3x2_to_f16x2(lo >> 16);
-              const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xFFFFu), a3 = e4m3x2_to_f16x2(hi >> 16);
+          for (int w = 0; w < 4; ++w) {
+            if (FP8) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_16816<true>(o[nt][w * 2 + u], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-            }
-          } else {
-            const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-            const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t lo = __byte_perm(v[0][w], v[1][w], u ? 0x7362 : 0x5140);
+                const uint32_t hi = __byte_perm(v[2][w], v[3][w], u ? 0x7362 : 0x5140);
+                const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xFFFFu), a1 = e4m3x2_to_f16x2(lo >> 16);
+                const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xFFFFu), a3 = e4m3x2_to_f16x2(hi >> 16);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_16816<false>(o[nt][half * 4 + w], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-              mma_16816<false>(o[nt][half * 4 + w], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_16816<true>(o[nt][w * 2 + u], a0, a1, a2, a3, pf[nt][sub][0], pf[nt][sub][1]);
+              }
+            } else {
+              const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+              const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_16816<false>(o[nt][half * 4 + w], a0, a1, a2, a3, pf[nt][sub][0], pf[nt][sub][1]);
+                mma_16816<false>(o[nt][half * 4 + w], a0, a1, a2, a3, pl[nt][sub][0], pl[nt][sub][1]);
+              }
             }
           }
         }
@@ -472,115 +511,126 @@ __global__ void __launch_bounds__(kDecThreads) attention_decode_kernel(const __g
     const bool spoiled = __any_sync(~0u, bad);
     if (spoiled && lane == 0 && atomicCAS(p.status + ST_CODE, 0, static_cast<int>(FL_ERR_INVALID_ARG)) == 0)
       p.status[ST_DETAIL] = seg.b;
+    // o[nt][t][i]: head 2q + (i & 1), dimension 16 g + 2 t + (i >> 1) (E4M3), or for bf16 with t = 4 half + w
+    // dimension 64 half + 8 g + 2 w + (i >> 1).  Chunks of 4 dimensions, permuted by q against bank conflicts.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      // o[nt][t][i]: head 2q + (i & 1), dimension 16 g + 2 t + (i >> 1) (E4M3), or for bf16 with t = 4 half + w
-      // dimension 64 half + 8 g + 2 w + (i >> 1).  Chunks of 4 dimensions, permuted by q against bank conflicts.
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float sum = l[nt][i];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        float* row = merge + (warp * 8 + 2 * q + i) * kHeadDim;
+        float* row = merge + (warp * 4 + q) * kHeadDim;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int chunk4 = FP8 ? g * 4 + c : (c >> 1) * 16 + g * 2 + (c & 1);
           *reinterpret_cast<float4*>(row + ((chunk4 ^ q) << 2)) =
               make_float4(o[nt][c * 2][i], o[nt][c * 2][i + 2], o[nt][c * 2 + 1][i], o[nt][c * 2 + 1][i + 2]);
         }
-        if (g == 0) {
-          float* st = stats + warp * 8 * NT + nt * 8 + 2 * q + i;
-          st[0] = m[nt][i];
-          st[kDecWarps * 8 * NT] = FP8 ? mv[nt][i] - kDecLift : m[nt][i];
-          st[2 * kDecWarps * 8 * NT] = spoiled ? NAN : sum;
-        }
-      }
-      __syncthreads();
-      for (int h = 0; h < 8 && nt * 8 + h < n_heads; ++h) {
-        const float* st = stats + nt * 8 + h;
-        float M = kDecNone, MV = kDecNone, L = 0.f, acc = 0.f;
+        if (g == 0)
+          stats[warp * 4 + q] = make_float4(m[nt][i], FP8 ? mv[nt][i] - kDecLift : m[nt][i], spoiled ? NAN : sum, 0.f);
+        __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          M = fmaxf(M, st[w * 8 * NT]);
-          MV = fmaxf(MV, st[(kDecWarps + w) * 8 * NT]);
-        }
-        const int at = ((((tid >> 2) ^ (h >> 1)) << 2) | (tid & 3));
+        for (int j = 0; j < 4; ++j) {
+          const int h = nt * 8 + 2 * j + i;
+          if (h >= n_heads) break;
+          float M = kDecNone, MV = kDecNone, L = 0.f, acc = 0.f;
+          float4 st[kDecWarps];
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          L += st[(2 * kDecWarps + w) * 8 * NT] * ex2(st[w * 8 * NT] - M);
-          acc += merge[(w * 8 + h) * kHeadDim + at] * ex2(st[(kDecWarps + w) * 8 * NT] - MV);
-        }
-        if (whole) {
-          const float r = seg.len == 0 ? 0.f : acc * (ex2(MV - M) / L);
-          p.O[seg.b * p.ldo + static_cast<long long>(head0 + nt * 8 + h) * kHeadDim + tid] = __float2bfloat16_rn(r);
-        } else {
-          __stcg(part + (nt * 8 + h) * kHeadDim + tid, acc);
-          if (tid == 0)
-            __stcg(reinterpret_cast<float4*>(part + 16 * kHeadDim) + nt * 8 + h, make_float4(M, MV, L, 0.f));
-        }
-      }
-      __syncthreads();
-    }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned n = atomicAdd(p.counters + c_first, 1u), want = static_cast<unsigned>(c_last - c_first);
-        if (n == want) p.counters[c_first] = 0;
-        plan[0] = n == want;
-      }
-      __syncthreads();
-      if (plan[0] != 0) {  // the last to arrive: a warp joins a head, lane i weighs piece i, then holds 4 dimensions
-        __threadfence();
-        auto src = [&](int c) { return p.parts + (static_cast<long long>(c) * 2 + (c == c_first)) * kDecPartFloats; };
-        for (int h = warp; h < n_heads; h += kDecWarps) {
-          float M = kDecNone, MV = kDecNone, L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c0 = c_first; c0 <= c_last; c0 += 32) {
-            const int n = min(32, c_last - c0 + 1);
-            float4 st = make_float4(kDecNone, kDecNone, 0.f, 0.f);
-            if (lane < n) st = __ldcg(reinterpret_cast<const float4*>(src(c0 + lane) + 16 * kHeadDim) + h);
-            float nm = fmaxf(M, st.x), nmv = fmaxf(MV, st.y);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-              nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, d));
-              nmv = fmaxf(nmv, __shfl_xor_sync(~0u, nmv, d));
-            }
-            float sum = st.z * ex2(st.x - nm);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-            L = L * ex2(M - nm) + sum;
-            const float w = lane < n ? ex2(st.y - nmv) : 0.f, old = ex2(MV - nmv);
-            acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-            M = nm;
-            MV = nmv;
-            for (int i0 = 0; i0 < n; i0 += 8) {
-              float4 v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i0 + i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(src(c0 + i0 + i) + h * kHeadDim) + lane);
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float wi = __shfl_sync(~0u, w, i0 + i);
-                acc.x += v[i].x * wi, acc.y += v[i].y * wi, acc.z += v[i].z * wi, acc.w += v[i].w * wi;
-              }
-            }
+          for (int w = 0; w < kDecWarps; ++w) {
+            st[w] = stats[w * 4 + j];
+            M = fmaxf(M, st[w].x);
+            MV = fmaxf(MV, st[w].y);
           }
-          const float r = ex2(MV - M) / L;
-          uint2 out;
-          out.x = pack_bf16x2(acc.x * r, acc.y * r);
-          out.y = pack_bf16x2(acc.z * r, acc.w * r);
-          *reinterpret_cast<uint2*>(p.O + seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + lane * 4) = out;
+          const int at = (((tid >> 2) ^ j) << 2) | (tid & 3);
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) {
+            L += st[w].z * ex2(st[w].x - M);
+            acc += merge[(w * 4 + j) * kHeadDim + at] * ex2(st[w].y - MV);
+          }
+          if (whole) {
+            const float r = seg.len == 0 ? 0.f : acc * (ex2(MV - M) / L);
+            p.O[seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + tid] = __float2bfloat16_rn(r);
+          } else {
+            __stcg(part + h * kHeadDim + tid, acc);
+            if (tid == 0) __stcg(reinterpret_cast<float4*>(part + 16 * kHeadDim) + h, make_float4(M, MV, L, 0.f));
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
+    if (!whole) {  // at most two of a CTA's segments are cut: its first and its last
+      if (cta == c_first) cut_b[1] = seg.b, cut_h[1] = seg.h, cut_first[1] = c_first, cut_last[1] = c_last;
+      else cut_b[0] = seg.b, cut_h[0] = seg.h, cut_first[0] = c_first, cut_last[0] = c_last;
     }
     left -= seg.units;
-    if (left <= 0) return;
+    if (left <= 0) break;
     seg_first += seg.n_units;
     next_seg(seg, left);
+  }
+
+  // ---- pieces of cut (sequence, head) pairs: the CTA that arrives last joins them
+  if (cut_first[0] < 0 && cut_first[1] < 0) return;
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    plan[tid] = 0;
+    const int first = tid == 0 ? cut_first[0] : cut_first[1], last = tid == 0 ? cut_last[0] : cut_last[1];
+    if (first >= 0 && atomicAdd(p.counters + first, 1u) == static_cast<unsigned>(last - first)) {
+      p.counters[first] = 0;
+      plan[tid] = 1;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (plan[k] == 0) continue;
+    __threadfence();
+    const int c_first = cut_first[k], c_last = cut_last[k];
+    const int kvh = cut_h[k] / p.chunks, chunk = cut_h[k] - kvh * p.chunks;
+    const int head0 = kvh * p.group + chunk * p.chunk_heads;
+    const int n_heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+    auto src = [&](int c) { return p.parts + (static_cast<long long>(c) * 2 + (c == c_first)) * kDecPartFloats; };
+    for (int h = warp; h < n_heads; h += kDecWarps) {  // lane i weighs piece i, then holds 4 dimensions
+      float M = kDecNone, MV = kDecNone, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c0 = c_first; c0 <= c_last; c0 += 32) {
+        const int n = min(32, c_last - c0 + 1);
+        float4 st = make_float4(kDecNone, kDecNone, 0.f, 0.f);
+        if (lane < n) st = __ldcg(reinterpret_cast<const float4*>(src(c0 + lane) + 16 * kHeadDim) + h);
+        float nm = fmaxf(M, st.x), nmv = fmaxf(MV, st.y);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, d));
+          nmv = fmaxf(nmv, __shfl_xor_sync(~0u, nmv, d));
+        }
+        float sum = st.z * ex2(st.x - nm);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        L = L * ex2(M - nm) + sum;
+        const float w = lane < n ? ex2(st.y - nmv) : 0.f, old = ex2(MV - nmv);
+        acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+        M = nm;
+        MV = nmv;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+          float4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(src(c0 + i0 + i) + h * kHeadDim) + lane);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float wi = __shfl_sync(~0u, w, i0 + i);
+            acc.x += v[i].x * wi, acc.y += v[i].y * wi, acc.z += v[i].z * wi, acc.w += v[i].w * wi;
+          }
+        }
+      }
+      const float r = ex2(MV - M) / L;
+      uint2 out;
+      out.x = pack_bf16x2(acc.x * r, acc.y * r);
+      out.y = pack_bf16x2(acc.z * r, acc.w * r);
+      *reinterpret_cast<uint2*>(p.O + cut_b[k] * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + lane * 4) = out;
+    }
   }
 }
 

@@ -12,9 +12,19 @@ int launch_decode(const DecodeParams& p, const DeviceInfo& di, cudaStream_t s) {
   using T = DecodeTraits<FP8, NT>;
   const void* fn = reinterpret_cast<const void*>(&attention_decode_kernel<FP8, NT>);
   if (!ensure_smem_attr(fn, di.device, T::kSmem)) return FL_ERR_CUDA;
-  const int grid = 2 * di.num_sms < kDecMaxCtas ? 2 * di.num_sms : kDecMaxCtas;
-  attention_decode_kernel<FP8, NT><<<grid, kDecThreads, T::kSmem, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+  const int grid = T::kCtas * di.num_sms < kDecMaxCtas ? T::kCtas * di.num_sms : kDecMaxCtas;
+  // programmatic dependent launch: only the launch itself overlaps the kernel in front (griddep_wait)
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = T::kSmem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_decode_kernel<FP8, NT>, p) == cudaSuccess ? FL_OK : FL_ERR_CUDA;
 }
 
 }  // namespace
