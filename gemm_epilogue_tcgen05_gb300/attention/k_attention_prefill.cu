@@ -1,79 +1,55 @@
-// attention_prefill: attention over whole prompts, packed one behind the other.
-//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale * q_i . k_j - max_j), over the keys j of i's own
-//   sequence (causal: j <= i).
-// One warp takes one (row, query head) and walks the keys once with the running maximum and sum; a lane
-// holds 4 of the 128 dimensions.
-#include "attention_common.h"
+// attention_prefill: argument checks, tensor maps and launch (the kernel: prefill_attention_kernel.cuh).
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "prefill_attention_kernel.cuh"
 
 namespace fl {
 namespace {
 
-struct PrefillParams {
-  const __nv_bfloat16* Q;
-  const void* K;
-  const void* V;
-  const float* ks;
-  const float* vs;
-  const int* cu;
-  __nv_bfloat16* O;
-  long long ldq, ldkv, lds, ldo;
-  int M, batch, n_heads, group, seq_len, causal;
-  float scale;
-};
+// 3-D tiled map over Q [rows][heads][128] bf16 with a row pitch of ld elements.
+bool encode_q(CUtensorMap* map, const void* base, int heads, int rows, int64_t ld, int hp, int tq) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(hp), static_cast<cuuint32_t>(tq)}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
-template <bool FP8>
-__device__ __forceinline__ float4 load4(const void* base, long long i) {
-  if (FP8) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + i);
-    return make_float4(e4m3_to_f32(w & 255u), e4m3_to_f32((w >> 8) & 255u), e4m3_to_f32((w >> 16) & 255u),
-                       e4m3_to_f32(w >> 24));
-  }
-  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i);
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+template <class Kernel, class... Args>
+bool launch_dependent(Kernel* kernel, int grid, int threads, int smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait in the kernels
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(128) attention_prefill_kernel(const PrefillParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (item >= static_cast<long long>(p.M) * p.n_heads) return;
-  const int r = static_cast<int>(item / p.n_heads), head = static_cast<int>(item % p.n_heads), kvh = head / p.group;
-  int first = 0, last = 0;
-  for (int b = 0; b < p.batch; ++b) {
-    sequence_rows(p.cu, b, p.seq_len, p.M, first, last);
-    if (r >= first && r < last) break;
-  }
-  if (r < first || r >= last) return;  // a row of no sequence stays as it is
-  const int end = p.causal ? r + 1 : last;
-  const float4 q = load4<false>(p.Q, r * p.ldq + head * kHeadDim + lane * 4);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = first; j < end; ++j) {
-    const long long at = j * p.ldkv + kvh * kHeadDim + lane * 4;
-    const float4 k = load4<FP8>(p.K, at), v = load4<FP8>(p.V, at);
-    float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    float vs = 1.f;
-    if (FP8) {
-      s *= p.ks[j * p.lds + kvh];
-      vs = p.vs[j * p.lds + kvh];
-    }
-    s *= p.scale;
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-    const float a = expf(m - ref), w = expf(s - ref);
-    m = mn;
-    l = l * a + w;
-    o.x = o.x * a + w * vs * v.x;
-    o.y = o.y * a + w * vs * v.y;
-    o.z = o.z * a + w * vs * v.z;
-    o.w = o.w * a + w * vs * v.w;
-  }
-  const float inv = 1.f / l;
-  uint2 w;
-  w.x = pack_bf16x2(o.x * inv, o.y * inv);
-  w.y = pack_bf16x2(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(p.O + r * p.ldo + head * kHeadDim + lane * 4) = w;
+int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di, cudaStream_t s) {
+  using T = PrefillTraits<FP8>;
+  const void* fn = reinterpret_cast<const void*>(&attention_prefill_kernel<FP8>);
+  if (!ensure_smem_attr(fn, di.device, T::kSmem)) return FL_ERR_CUDA;
+  const int grid = tiles < di.num_sms ? static_cast<int>(tiles) : di.num_sms;
+  return launch_dependent(attention_prefill_kernel<FP8>, grid, kPreThreads, T::kSmem, s, p) ? FL_OK : FL_ERR_CUDA;
 }
 
 }  // namespace
@@ -112,18 +88,62 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   if (workspace == nullptr || workspace_bytes < fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype))
     return FL_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & (kWsStatusBytes - 1)) != 0) return FL_ERR_ALIGNMENT;
-  const long long items = static_cast<long long>(M) * n_heads;
-  if ((items + 3) / 4 > 0x7FFFFFFFll) return FL_ERR_UNSUPPORTED;
   DeviceInfo di;
   const int st = current_device(&di);
   if (st != FL_OK) return st;
-  if (cu_seqlens == nullptr) batch = (M - 1) / seq_len + 1;
-  const PrefillParams p{static_cast<const __nv_bfloat16*>(Q), K, V, k_scale, v_scale, cu_seqlens,
-                        static_cast<__nv_bfloat16*>(O), ldq, ldkv, lds, ldo, M, batch, n_heads,
-                        n_heads / n_kv_heads, seq_len, causal, scale};
-  const int grid = static_cast<int>((items + 3) / 4);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (fp8) attention_prefill_kernel<true><<<grid, 128, 0, s>>>(p);
-  else attention_prefill_kernel<false><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+
+  PrefillParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.group = n_heads / n_kv_heads;
+  // heads of a tile: the largest part of the group that leaves room for two tokens
+  p.hp = p.group < 64 ? p.group : 64;
+  while (p.group % p.hp != 0) --p.hp;
+  p.tq = kPreTile / p.hp;
+  p.pairs = n_heads / p.hp;
+  p.batch = cu_seqlens == nullptr ? (M - 1) / seq_len + 1 : batch;
+  p.seq_len = seq_len;
+  const long long per_cta = 2 * p.tq;
+  const long long blocks = cu_seqlens == nullptr
+                               ? (M / seq_len) * ((seq_len - 1) / per_cta + 1) + (M % seq_len + per_cta - 1) / per_cta
+                               : M / per_cta + batch;  // an upper bound: the lengths are on the device
+  const int kv_w = static_cast<int>(kv_width);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const void* k16 = K;
+  const void* v16 = V;
+  int64_t ld16 = ldkv;
+  if (fp8) {
+    __nv_bfloat16* kw = reinterpret_cast<__nv_bfloat16*>(ws + 2 * kWsStatusBytes);
+    __nv_bfloat16* vw = kw + static_cast<size_t>(M) * kv_width;
+    k16 = kw, v16 = vw, ld16 = kv_width;
+  }
+  if (!encode_q(&p.map_q, Q, n_heads, M, ldq, p.hp, p.tq) ||
+      !encode_2d(&p.map_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k16, kv_width, M, ld16, 64, kPreTile,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&p.map_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, v16, kv_width, M, ld16, 64, kPreTile,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return FL_ERR_CUDA;
+  p.V = static_cast<const __nv_bfloat16*>(v16);
+  p.ldv = ld16;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.lds = lds;
+  p.cu = cu_seqlens;
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.ldo = ldo;
+  p.M = M;
+  p.causal = causal != 0;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.status = reinterpret_cast<int*>(ws);
+  p.timeout_ns = wait_timeout_ns();
+  if (fp8) {
+    const long long work = (2ll * M * (kv_w / 16) + 255) / 256;
+    const int grid = work < 8ll * di.num_sms ? static_cast<int>(work) : 8 * di.num_sms;
+    if (!launch_dependent(e4m3_rows_to_bf16_kernel, grid, 256, 0, s, static_cast<const uint8_t*>(K),
+                          static_cast<const uint8_t*>(V), static_cast<long long>(ldkv), M, kv_w,
+                          static_cast<__nv_bfloat16*>(const_cast<void*>(k16)),
+                          static_cast<__nv_bfloat16*>(const_cast<void*>(v16))))
+      return FL_ERR_CUDA;
+  }
+  return fp8 ? launch_prefill<true>(p, blocks * p.pairs, di, s) : launch_prefill<false>(p, blocks * p.pairs, di, s);
 }

@@ -1,0 +1,692 @@
+// Attention over whole prompts, packed one behind the other, on the tcgen05 tensor cores.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(x_ij - m_i),  x_ij = scale * log2(e) * q_i . k_j
+//
+// What bounds it: 4 * 128 multiply-adds for every (query, key, head) on the tensor cores, and one exponential
+// for each of the same on the special-function units; HBM traffic is small beside both.
+//
+// Tile.  A CTA works on two query tiles of 128 rows at once against one stream of 128-key tiles of K and V.  The
+// rows of a query tile are (token, head) pairs: the hp query heads that share a kv head lie side by side, so a
+// tile holds 128 / hp consecutive tokens.  Short prompts fill their tiles and the causal diagonal cuts off less.
+// While one query tile is in its softmax the tensor cores work for the other one:
+//   S_s = Q_s K^T (TMEM, 128 columns each)  ->  softmax in registers, one thread a row  ->  P_s as bf16 over S_s
+//   (TMEM)  ->  O_s += P_s V (A from TMEM, V as stored: MN-major B; TMEM, 128 columns each).  512 columns in all.
+//
+// Warps 0-3 and 4-7: softmax of query tile 0 and 1 and its output.  Warp 8: one thread issues the MMAs.  Warp 9:
+// one thread issues the TMA loads (Q by a 3-D map over (dimension, head, row); K and V into one ring of 32 KB
+// stages).  Warp 10: which tile comes next; the scales of E4M3 keys and values.  Warp 11: V rows in masked tiles.
+// One persistent CTA on each SM; the next tile's loads, its first products and the last one's output overlap.
+//
+// The row maximum is only raised when a logit passes it by more than 2^8 (in the weights); then the thread that
+// owns the row scales its O in TMEM, which is complete by the time S of the next key tile is (one commit covers
+// all products before it), so no hand-over is needed.
+//
+// Work: tile (sequence, block of tokens, kv head) by falling block index, so the longest come first whatever the
+// sequences' lengths are; CTA c takes ranks c, 2 G - 1 - c, 2 G + c, ...
+//
+// Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
+// values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
+//
+// E4M3: a first kernel turns the codes of K and V into bf16 (exact) in the workspace; their scales stay fp32:
+// K's multiplies the logits, V's the weights before these are rounded to bf16.
+#pragma once
+#include <climits>
+
+#include "attention_common.h"
+
+namespace fl {
+
+constexpr int kPreThreads = 384;
+constexpr int kPreTile = 128;                      // query rows of a tile, and keys of a tile
+constexpr int kPreTileBytes = kPreTile * kHeadDim * 2;
+constexpr int kPreRing = 4;                        // tile descriptors
+constexpr float kPreNone = -3e38f;                 // a maximum over nothing: any finite logit passes it
+constexpr float kPreLazy = 8.f;
+
+// Where a wait gave up (recorded in the workspace's status record).
+enum : int {
+  W_PRE_TILE_FULL = 20, W_PRE_TILE_EMPTY = 21, W_PRE_Q_EMPTY = 22, W_PRE_Q_FULL = 23, W_PRE_KV_EMPTY = 24,
+  W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29, W_PRE_SCALE_FULL = 30,
+  W_PRE_SCALE_EMPTY = 31
+};
+
+struct alignas(128) PrefillParams {
+  CUtensorMap map_q;  // Q [M][n_heads][128] bf16, box {64, hp, tq}
+  CUtensorMap map_k;  // K [M][n_kv * 128] bf16, box {64, 128}
+  CUtensorMap map_v;
+  const __nv_bfloat16* V;  // the rows map_v covers
+  long long ldv;
+  const float* ks;  // E4M3: scales [M][lds]
+  const float* vs;
+  long long lds;
+  const int* cu;
+  __nv_bfloat16* O;
+  long long ldo;
+  int M, batch, seq_len, causal;
+  int group, hp, tq;       // query heads of a kv head; heads and tokens of a query tile
+  int pairs;               // head packs of a token block: n_kv * group / hp
+  float scale_log2;
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+template <bool FP8>
+struct PrefillTraits {
+  static constexpr int kStages = FP8 ? 4 : 5;
+  static constexpr int kBars = 1024;
+  static constexpr int kScales = FP8 ? 2 * 2 * kPreTile * 4 : 0;
+  static constexpr int kSmem = 2 * kPreTileBytes + kStages * kPreTileBytes + kScales + kBars + 1024 /*alignment*/;
+};
+
+// One unit of work.
+struct PrefillTile {
+  int row0, len;   // the sequence's first row and length
+  int tok0;        // first token of query tile 0 (query tile 1: + tq)
+  int n0, n1;      // key tiles that query tiles 0 and 1 meet
+  int head0, kvh;
+  int spoiled;     // set by warp 11: V holds values that are not finite in a masked tile
+};
+
+struct PrefillBars {
+  uint64_t tile_full[kPreRing], tile_empty[kPreRing];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[5], kv_empty[5], v_ok[5];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t sc_full[2], sc_empty[2];
+  uint64_t drain;
+  PrefillTile tile[kPreRing];
+  int abort_flag;
+  uint32_t tmem;
+};
+static_assert(sizeof(PrefillBars) <= 1024, "barrier block");
+
+// D[tmem] (+)= A[tmem] * B: A bf16 pairs packed along K in tensor memory.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tma_load_3d(const void* map, uint64_t* bar, uint32_t dst, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// A wait of all lanes of a warp: they go on, or give up, together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where) {
+  return __all_sync(~0u, mbar_wait(bar, parity, w, where));
+}
+// Two fp32 lanes in one 64-bit register.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const __grid_constant__ PrefillParams p) {
+  using T = PrefillTraits<FP8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * kPreTileBytes;
+  float* scales = reinterpret_cast<float*>(smem + (2 + T::kStages) * kPreTileBytes);  // [2][K | V][128]
+  PrefillBars& bar = *reinterpret_cast<PrefillBars*>(smem + (2 + T::kStages) * kPreTileBytes + T::kScales);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = gridDim.x, cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPreRing; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 11);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
+      mbar_init(&bar.sc_full[i], 32), mbar_init(&bar.sc_empty[i], 8);
+    }
+    for (int i = 0; i < T::kStages; ++i)
+      mbar_init(&bar.kv_full[i], 1), mbar_init(&bar.kv_empty[i], 2), mbar_init(&bar.v_ok[i], 1);
+    mbar_init(&bar.drain, 1);
+    bar.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.map_q);
+    tma_prefetch_desc(&p.map_k);
+    tma_prefetch_desc(&p.map_v);
+  }
+  if (warp == 8) {
+    tmem_alloc(&bar.tmem, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bar.tmem);
+  const WaitCtx wc{&bar.abort_flag, p.status, p.timeout_ns};
+
+  // The tile that descriptor k (counted per CTA) describes; false when there is none or a wait gave up.
+  auto get_tile = [&](int k, PrefillTile& t) -> bool {
+    if (!mbar_wait(&bar.tile_full[k % kPreRing], (k / kPreRing) & 1, wc, W_PRE_TILE_FULL)) return false;
+    const volatile PrefillTile& s = bar.tile[k % kPreRing];
+    t.row0 = s.row0, t.len = s.len, t.tok0 = s.tok0, t.n0 = s.n0, t.n1 = s.n1, t.head0 = s.head0, t.kvh = s.kvh;
+    return t.len > 0;
+  };
+  auto first_masked = [&](const PrefillTile& t) { return p.causal ? (t.tok0 + 1) / kPreTile : t.len / kPreTile; };
+
+  if (warp == 10) {
+    // ================================================================ tiles, and the scales of E4M3 K and V
+    const int tpc = 2 * p.tq;
+    auto blocks_of = [&](int b) {
+      int first, last;
+      sequence_rows(p.cu, b, p.seq_len, p.M, first, last);
+      return last > first ? (last - first - 1) / tpc + 1 : 0;
+    };
+    int mine = 0, tier = 0;
+    if (lane < p.batch) mine = blocks_of(lane);
+    // sum over the sequences of max(0, blocks - j): blocks with an index of at least j
+    auto at_least = [&](int j) -> int {
+      int n = max(0, mine - j);
+      for (int b = lane + 32; b < p.batch; b += 32) n += max(0, blocks_of(b) - j);
+      return __reduce_add_sync(~0u, n);
+    };
+    {
+      int n = mine;
+      for (int b = lane + 32; b < p.batch; b += 32) n = max(n, blocks_of(b));
+      tier = __reduce_max_sync(~0u, n);
+    }
+    int above = 0, upto = 0;  // blocks of higher tiers, and with this tier's
+    auto produce = [&](int k) -> bool {
+      if (!warp_wait(&bar.tile_empty[k % kPreRing], ((k / kPreRing) & 1) ^ 1, wc, W_PRE_TILE_EMPTY)) return false;
+      const long long rank = static_cast<long long>(k) * G + ((k & 1) ? G - 1 - cta : cta);
+      const int block = static_cast<int>(min(rank / p.pairs, static_cast<long long>(INT_MAX)));
+      const int pair = static_cast<int>(rank - static_cast<long long>(block) * p.pairs);
+      while (tier > 0 && upto <= block) {
+        above = upto;
+        upto = at_least(--tier);
+      }
+      PrefillTile t = {};
+      if (upto > block) {  // the (block - above)-th sequence that reaches this tier
+        int skip = block - above, seq = -1;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+          const bool reaches = b0 + lane < p.batch && (b0 == 0 ? mine : blocks_of(b0 + lane)) > tier;
+          const unsigned who = __ballot_sync(~0u, reaches);
+          const int n = __popc(who);
+          if (skip < n) {
+            seq = b0 + __fns(who, 0, skip + 1);
+            break;
+          }
+          skip -= n;
+        }
+        int first, last;
+        sequence_rows(p.cu, seq, p.seq_len, p.M, first, last);
+        t.row0 = first;
+        t.len = last - first;
+        t.tok0 = tier * tpc;
+        const int packs = p.group / p.hp;
+        t.kvh = pair / packs;
+        t.head0 = t.kvh * p.group + (pair - t.kvh * packs) * p.hp;
+        const int all = (t.len - 1) / kPreTile + 1;
+        // tokens [tok0, tok0 + tq) and [tok0 + tq, tok0 + 2 tq), cut off at the sequence's end
+        t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
+        t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
+      }
+      if (lane == 0) {
+        bar.tile[k % kPreRing] = t;
+        mbar_arrive(&bar.tile_full[k % kPreRing]);
+      }
+      __syncwarp();
+      return t.len > 0;
+    };
+    bool more = produce(0);
+    if (!FP8) {
+      for (int k = 1; more; ++k) more = produce(k);
+    } else {
+      int k = 0, sc = 0;
+      bool next = more && produce(1);
+      while (more) {
+        const PrefillTile t = bar.tile[k % kPreRing];
+        const int n = max(t.n0, t.n1);
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i, ++sc) {
+          float a[4], b[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int pos = i * kPreTile + c * 32 + lane;
+            a[c] = b[c] = 0.f;
+            if (pos < t.len) {
+              const long long at = static_cast<long long>(t.row0 + pos) * p.lds + t.kvh;
+              a[c] = __ldg(p.ks + at), b[c] = __ldg(p.vs + at);
+            }
+          }
+          ok = warp_wait(&bar.sc_empty[sc & 1], ((sc >> 1) & 1) ^ 1, wc, W_PRE_SCALE_EMPTY);
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            scales[(sc & 1) * 256 + c * 32 + lane] = a[c];
+            scales[(sc & 1) * 256 + 128 + c * 32 + lane] = b[c];
+          }
+          mbar_arrive(&bar.sc_full[sc & 1]);
+        }
+        ++k;
+        more = ok && next;
+        next = more && produce(k + 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ================================================================ TMA loads
+    if (lane == 0) {
+      int stage = 0, fill = 0, q_uses[2] = {0, 0}, issued = 0;
+      bool ok = true;
+      PrefillTile t;
+      for (int k = 0; ok && get_tile(k, t); ++k) {
+        mbar_arrive(&bar.tile_empty[k % kPreRing]);
+        const int n = max(t.n0, t.n1);
+        auto load_q = [&](int s) {
+          if ((s ? t.n1 : t.n0) == 0) return;
+          if (!mbar_wait(&bar.q_empty[s], (q_uses[s] & 1) ^ 1, wc, W_PRE_Q_EMPTY)) {
+            ok = false;
+            return;
+          }
+          ++q_uses[s];
+          mbar_arrive_expect_tx(&bar.q_full[s], static_cast<uint32_t>(p.hp * p.tq * kHeadDim * 2));
+          const uint32_t dst = q_smem + s * kPreTileBytes;
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(&p.map_q, &bar.q_full[s], dst + h * (kPreTileBytes / 2), h * 64, t.head0,
+                        t.row0 + t.tok0 + s * p.tq);
+        };
+        auto load_kv = [&](const CUtensorMap* map, int i) {
+          if (!ok || !mbar_wait(&bar.kv_empty[stage], (fill & 1) ^ 1, wc, W_PRE_KV_EMPTY)) {
+            ok = false;
+            return;
+          }
+          mbar_arrive_expect_tx(&bar.kv_full[stage], kPreTileBytes);
+          uint8_t* dst = smem + (2 + stage) * kPreTileBytes;
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d(map, &bar.kv_full[stage], dst + h * (kPreTileBytes / 2), t.kvh * kHeadDim + h * 64,
+                        t.row0 + i * kPreTile);
+          ++issued;
+          if (++stage == T::kStages) stage = 0, ++fill;
+        };
+        load_q(0);
+        load_kv(&p.map_k, 0);
+        if (ok) load_q(1);
+        load_kv(&p.map_v, 0);
+        for (int i = 1; i < n && ok; ++i) {
+          load_kv(&p.map_k, i);
+          load_kv(&p.map_v, i);
+        }
+      }
+      if (bar.abort_flag) {  // leave no copy in flight
+        for (int s = 0; s < 2; ++s)
+          if (q_uses[s] > 0) mbar_wait_quiet(&bar.q_full[s], (q_uses[s] - 1) & 1, p.timeout_ns);
+        for (int i = max(0, issued - T::kStages); i < issued; ++i)
+          mbar_wait_quiet(&bar.kv_full[i % T::kStages], (i / T::kStages) & 1, p.timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ================================================================ MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile), idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true);
+      int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+      uint32_t v_phase = 0;
+      int kv = 0;  // index into the sequence K0 V0 K1 V1 ... of loads
+      auto qk = [&](int s, int at, bool last) {  // S_s = Q_s K^T with K in ring slot `at`
+        const uint32_t a = q_smem + s * kPreTileBytes, b = kv_smem + (at % T::kStages) * kPreTileBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t ad = sdesc_k_sw128(a + h * (kPreTileBytes / 2)), bd = sdesc_k_sw128(b + h * (kPreTileBytes / 2));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_bf16(tmem + s * kPreTile, ad + k * 2, bd + k * 2, idesc_qk, (h | k) != 0);
+        }
+        mma_commit(&bar.s_full[s]);
+        if (last) mma_commit(&bar.q_empty[s]);
+      };
+      auto pv = [&](int s, int at, bool first) {  // O_s (+)= P_s V with V in ring slot `at`
+        const uint64_t bd = sdesc_mn_sw128(kv_smem + (at % T::kStages) * kPreTileBytes, kPreTileBytes / 2);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_ts(tmem + 256 + s * kHeadDim, tmem + s * kPreTile + k * 8, bd + k * 128, idesc_pv, !(first && k == 0));
+      };
+      auto kv_wait = [&](int at) {
+        return mbar_wait(&bar.kv_full[at % T::kStages], (at / T::kStages) & 1, wc, W_PRE_KV_FULL);
+      };
+      auto q_wait = [&](int s) {
+        const bool ok = mbar_wait(&bar.q_full[s], q_uses[s] & 1, wc, W_PRE_Q_FULL);
+        ++q_uses[s];
+        return ok;
+      };
+      PrefillTile t, u;
+      bool ok = get_tile(0, t);
+      if (ok) {
+        mbar_arrive(&bar.tile_empty[0]);
+        ok = kv_wait(0);
+        for (int s = 0; s < 2 && ok; ++s)
+          if ((s ? t.n1 : t.n0) > 0) {
+            ok = q_wait(s);
+            if (ok) qk(s, 0, (s ? t.n1 : t.n0) == 1);
+          }
+        if (ok) mma_commit(&bar.kv_empty[0]);
+      }
+      for (int k = 0; ok; ++k) {
+        const int n = max(t.n0, t.n1), mask0 = first_masked(t);
+        bool more = false;
+        for (int i = 0; i < n && ok; ++i) {
+          const int v_at = kv + 1, k_at = kv + 2;
+          const bool last = i == n - 1;
+          if (last) {
+            more = get_tile(k + 1, u);
+            if (more) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
+          }
+          ok = kv_wait(v_at);
+          if (ok && i >= mask0) {
+            const int st = v_at % T::kStages;
+            ok = mbar_wait(&bar.v_ok[st], (v_phase >> st) & 1, wc, W_PRE_V);
+            v_phase ^= 1u << st;
+          }
+          bool have_k = false;
+          for (int s = 0; s < 2 && ok; ++s) {
+            const int ns = s ? t.n1 : t.n0;
+            if (i < ns) {
+              ok = mbar_wait(&bar.p_full[s], p_uses[s] & 1, wc, W_PRE_P);
+              ++p_uses[s];
+              if (!ok) break;
+              tc_fence_after();
+              pv(s, v_at, i == 0);
+              if (i == ns - 1) mma_commit(&bar.o_full[s]);
+            }
+            const int un = s ? u.n1 : u.n0;
+            if (last ? more && un > 0 : i + 1 < ns) {
+              if (!have_k) ok = kv_wait(k_at);
+              have_k = true;
+              if (ok && last) ok = q_wait(s);
+              if (ok) qk(s, k_at, last ? un == 1 : i + 1 == ns - 1);
+            }
+          }
+          if (!ok) break;
+          mma_commit(&bar.kv_empty[v_at % T::kStages]);
+          if (have_k) mma_commit(&bar.kv_empty[k_at % T::kStages]);
+          kv += 2;
+        }
+        if (!more) break;
+        t = u;
+      }
+      mma_commit(&bar.drain);  // nothing of this CTA's products or their arrivals is left behind
+      mbar_wait_quiet(&bar.drain, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ================================================================ V of masked tiles: finite values only
+    PrefillTile t;
+    int kv = 0;
+    bool ok = true;
+    for (int k = 0; ok && __all_sync(~0u, get_tile(k, t)); ++k) {
+      const int n = max(t.n0, t.n1);
+      const int mask0 = first_masked(t);
+      // Every fill of the ring passes here in order (a parity says nothing about older or newer phases), so
+      // a stage is only free once this warp has seen it, too.
+      for (int i = 0; i < 2 * n; ++i, ++kv) {
+        const int st = kv % T::kStages;
+        if (!(ok = warp_wait(&bar.kv_full[st], (kv / T::kStages) & 1, wc, W_PRE_KV_FULL))) break;
+        if ((i & 1) == 0 || (i >> 1) < mask0) {
+          if (lane == 0) mbar_arrive(&bar.kv_empty[st]);
+          continue;
+        }
+        const uint32_t base = kv_smem + st * kPreTileBytes + lane * 16;
+        uint32_t seen = 0;
+#pragma unroll 8
+        for (int c = 0; c < kPreTileBytes / 512; ++c) {
+          const uint4 w = ld_shared_v4(base + c * 512);
+          // an exponent of all ones carries into the sign's place
+          seen |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                  ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+        }
+        if (__any_sync(~0u, (seen & 0x80008000u) != 0)) {
+          if (lane == 0) bar.tile[k % kPreRing].spoiled = 1;
+          auto clean = [](uint32_t w) {
+            const uint32_t bad = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+            return w & ~((bad >> 15) * 0xFFFFu);
+          };
+          for (int c = 0; c < kPreTileBytes / 512; ++c) {
+            const uint4 w = ld_shared_v4(base + c * 512);
+            st_shared_v4(base + c * 512, clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_ok[st]), mbar_arrive(&bar.kv_empty[st]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.tile_empty[k % kPreRing]);
+    }
+  } else {
+    // ================================================================ softmax of query tile s, and its output
+    const int s = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tmem = tmem + lanes + s * kPreTile, o_tmem = tmem + lanes + 256 + s * kHeadDim;
+    const int row_tok = row / p.hp, row_head = row - row_tok * p.hp;
+    const bool row_used = row_tok < p.tq;
+    const float c = p.scale_log2;
+    int s_uses = 0, o_uses = 0, sc = 0;
+    bool ok = true;
+    PrefillTile t;
+    for (int k = 0; ok && __all_sync(~0u, get_tile(k, t)); ++k) {
+      const int ns = s ? t.n1 : t.n0, n = FP8 ? max(t.n0, t.n1) : ns, first = t.tok0 + s * p.tq;
+      const int tok = first + row_tok;
+      const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
+      const int clear = p.causal ? first : t.len - 1;              // last key that every row sees
+      float m = kPreNone;
+      uint64_t l0 = 0, l1 = 0;
+      for (int i = 0; i < n; ++i) {
+        if (FP8) {
+          if (!(ok = warp_wait(&bar.sc_full[sc & 1], (sc >> 1) & 1, wc, W_PRE_SCALE_FULL))) break;
+        }
+        if (i < ns) {
+          if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
+          ++s_uses;
+          tc_fence_after();
+          uint32_t x[4][32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tmem_ld32(s_tmem + j * 32, x[j]);
+          tmem_ld_wait();
+          const float4* ks = reinterpret_cast<const float4*>(scales + (sc & 1) * 256);
+          if (FP8) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float4 f = ks[j];
+              uint32_t* y = &x[j >> 3][(j & 7) * 4];
+              float a, b;
+              f2_split(f2_mul(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), f2(f.x, f.y)), a, b);
+              y[0] = __float_as_uint(a), y[1] = __float_as_uint(b);
+              f2_split(f2_mul(f2(__uint_as_float(y[2]), __uint_as_float(y[3])), f2(f.z, f.w)), a, b);
+              y[2] = __float_as_uint(a), y[3] = __float_as_uint(b);
+            }
+          }
+          const bool masked = i * kPreTile + kPreTile - 1 > clear;
+          const int cols = lim - i * kPreTile;  // columns up to this one count
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (j > cols) x[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+          }
+          float mx[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(x[j][0]);
+#pragma unroll
+          for (int j = 1; j < 31; j += 2)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              mx[h] = fmaxf(mx[h], fmaxf(__uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1])));
+#pragma unroll
+          for (int h = 0; h < 4; ++h) mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const bool rise = top > m + kPreLazy;
+          if (__any_sync(~0u, rise)) {
+            const float up = rise ? top : m, down = ex2(m - up);
+            m = up;
+            l0 = f2_mul(l0, f2(down, down)), l1 = f2_mul(l1, f2(down, down));
+            if (i > 0) {  // O of the key tiles before is complete: S of this one was committed behind it
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                uint32_t o[16];
+                tmem_ld16(o_tmem + j * 16, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < 16; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * down);
+                tmem_st16(o_tmem + j * 16, o);
+              }
+            }
+          }
+          const uint64_t c2 = f2(c, c), m2 = f2(-m, -m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[16];
+#pragma unroll
+            for (int h = 0; h < 16; h += 2) {
+              float a, b, d, e;
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), c2, m2), a, b);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m2), d, e);
+              a = ex2(a), b = ex2(b), d = ex2(d), e = ex2(e);
+              l0 = f2_add(l0, f2(a, b)), l1 = f2_add(l1, f2(d, e));
+              if (FP8) {
+                const float4 f = ks[32 + j * 8 + (h >> 1)];
+                f2_split(f2_mul(f2(a, b), f2(f.x, f.y)), a, b);
+                f2_split(f2_mul(f2(d, e), f2(f.z, f.w)), d, e);
+                if (masked) {  // a scale behind the mask may be anything
+                  const int col = j * 32 + h * 2;
+                  a = col > cols ? 0.f : a, b = col + 1 > cols ? 0.f : b;
+                  d = col + 2 > cols ? 0.f : d, e = col + 3 > cols ? 0.f : e;
+                }
+              }
+              w[h] = pack_bf16x2(a, b), w[h + 1] = pack_bf16x2(d, e);
+            }
+            tmem_st16(s_tmem + j * 16, w);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full[s]);
+        }
+        if (FP8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.sc_empty[sc & 1]);
+          ++sc;
+        }
+      }
+      if (!ok) break;
+      if (ns > 0) {
+        if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
+        ++o_uses;
+        tc_fence_after();
+        float a, b, d, e;
+        f2_split(l0, a, b);
+        f2_split(l1, d, e);
+        const float inv = 1.f / ((a + b) + (d + e));
+        const bool there = row_used && tok < t.len;
+        const bool spoiled = *reinterpret_cast<volatile int*>(&bar.tile[k % kPreRing].spoiled) != 0;
+        const int from = first_masked(t) * kPreTile;
+        __nv_bfloat16* dst = p.O + static_cast<long long>(t.row0 + tok) * p.ldo +
+                             static_cast<long long>(t.head0 + row_head) * kHeadDim;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[32];
+          tmem_ld32(o_tmem + j * 32, o);
+          tmem_ld_wait();
+          if (!there) continue;
+          if (spoiled) {  // values that were taken out for the rows that do not see them
+            for (int pos = from; pos <= lim; ++pos) {
+              const __nv_bfloat16* v = p.V + static_cast<long long>(t.row0 + pos) * p.ldv +
+                                       static_cast<long long>(t.kvh) * kHeadDim + j * 32;
+#pragma unroll
+              for (int h = 0; h < 32; ++h) {
+                const float y = __bfloat162float(v[h]);
+                if (!isfinite(y)) o[h] = __float_as_uint(__uint_as_float(o[h]) + y);
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(o[h * 8]) * inv, __uint_as_float(o[h * 8 + 1]) * inv);
+            w.y = pack_bf16x2(__uint_as_float(o[h * 8 + 2]) * inv, __uint_as_float(o[h * 8 + 3]) * inv);
+            w.z = pack_bf16x2(__uint_as_float(o[h * 8 + 4]) * inv, __uint_as_float(o[h * 8 + 5]) * inv);
+            w.w = pack_bf16x2(__uint_as_float(o[h * 8 + 6]) * inv, __uint_as_float(o[h * 8 + 7]) * inv);
+            *reinterpret_cast<uint4*>(dst + j * 32 + h * 8) = w;
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.tile_empty[k % kPreRing]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// E4M3 codes of K and V to bf16 (exact), [rows][width] each, 16 codes a thread.
+__global__ void __launch_bounds__(256) e4m3_rows_to_bf16_kernel(const uint8_t* K, const uint8_t* V, long long ld, int rows,
+                                                                int width, __nv_bfloat16* K16, __nv_bfloat16* V16) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int per_row = width / 16;
+  const long long n = static_cast<long long>(rows) * per_row;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < 2 * n;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const bool second = i >= n;
+    const long long j = second ? i - n : i, r = j / per_row;
+    const int c = static_cast<int>(j - r * per_row) * 16;
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>((second ? V : K) + r * ld + c));
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(in[k >> 1] >> ((k & 1) * 16))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      out[k] = pack_bf16x2(f.x, f.y);
+    }
+    uint4* dst = reinterpret_cast<uint4*>((second ? V16 : K16) + r * width + c);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+}
+
+}  // namespace fl
