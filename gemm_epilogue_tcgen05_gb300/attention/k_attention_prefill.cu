@@ -1,6 +1,7 @@
 // attention_prefill: argument checks, tensor maps and launch (the kernel: prefill_attention_kernel.cuh).
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "prefill_attention_kernel.cuh"
@@ -48,6 +49,14 @@ int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di
   using T = PrefillTraits<FP8>;
   const void* fn = reinterpret_cast<const void*>(&attention_prefill_kernel<FP8>);
   if (!ensure_smem_attr(fn, di.device, T::kSmem)) return FL_ERR_CUDA;
+  // the warps share out the registers of the launch: with any other number of them the kernel would not start
+  static std::atomic<int> regs{0};
+  if (regs.load() == 0) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, fn) != cudaSuccess) return FL_ERR_CUDA;
+    regs.store(a.numRegs);
+  }
+  if (regs.load() != kPreRegs) return FL_ERR_UNSUPPORTED;
   const int grid = tiles < di.num_sms ? static_cast<int>(tiles) : di.num_sms;
   return launch_dependent(attention_prefill_kernel<FP8>, grid, kPreThreads, T::kSmem, s, p) ? FL_OK : FL_ERR_CUDA;
 }

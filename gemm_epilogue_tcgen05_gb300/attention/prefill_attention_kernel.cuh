@@ -37,6 +37,10 @@
 namespace fl {
 
 constexpr int kPreThreads = 384;
+// Registers of a thread at launch (the launch checks that the compiler used exactly these), of the softmax
+// warps and of the other four: 384 * 168 = 256 * 200 + 128 * 104.
+constexpr int kPreRegs = 168, kPreRegsSoftmax = 200, kPreRegsOther = 104;
+static_assert(kPreThreads * kPreRegs == 256 * kPreRegsSoftmax + 128 * kPreRegsOther, "register split");
 constexpr int kPreTile = 128;                      // query rows of a tile, and keys of a tile
 constexpr int kPreTileBytes = kPreTile * kHeadDim * 2;
 constexpr int kPreRing = 4;                        // tile descriptors
@@ -124,6 +128,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_load_3d(const void* map, uint64_t* bar, uint32_t dst, int x, int y, int z) {
   asm volatile(
@@ -132,9 +144,26 @@ __device__ __forceinline__ void tma_load_3d(const void* map, uint64_t* bar, uint
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// A bounded wait that reads the clock only now and then: reading it takes longer than most of these waits.
+__device__ __forceinline__ bool pre_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*w.abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > w.timeout_ns) {
+        *w.abort_flag = 1;
+        record_failure(w.status, where, static_cast<int>(parity));
+        return false;
+      }
+    }
+  }
+}
 // A wait of all lanes of a warp: they go on, or give up, together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where) {
-  return __all_sync(~0u, mbar_wait(bar, parity, w, where));
+  return __all_sync(~0u, pre_wait(bar, parity, w, where));
 }
 // Two fp32 lanes in one 64-bit register.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
@@ -201,13 +230,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 
   // The tile that descriptor k (counted per CTA) describes; false when there is none or a wait gave up.
   auto get_tile = [&](int k, PrefillTile& t) -> bool {
-    if (!mbar_wait(&bar.tile_full[k % kPreRing], (k / kPreRing) & 1, wc, W_PRE_TILE_FULL)) return false;
+    if (!pre_wait(&bar.tile_full[k % kPreRing], (k / kPreRing) & 1, wc, W_PRE_TILE_FULL)) return false;
     const volatile PrefillTile& s = bar.tile[k % kPreRing];
     t.row0 = s.row0, t.len = s.len, t.tok0 = s.tok0, t.n0 = s.n0, t.n1 = s.n1, t.head0 = s.head0, t.kvh = s.kvh;
     return t.len > 0;
   };
   auto first_masked = [&](const PrefillTile& t) { return p.causal ? (t.tok0 + 1) / kPreTile : t.len / kPreTile; };
 
+  if (warp >= 8) {
+  fewer_registers<kPreRegsOther>();
   if (warp == 10) {
     // ================================================================ tiles, and the scales of E4M3 K and V
     const int tpc = 2 * p.tq;
@@ -318,7 +349,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         const int n = max(t.n0, t.n1);
         auto load_q = [&](int s) {
           if ((s ? t.n1 : t.n0) == 0) return;
-          if (!mbar_wait(&bar.q_empty[s], (q_uses[s] & 1) ^ 1, wc, W_PRE_Q_EMPTY)) {
+          if (!pre_wait(&bar.q_empty[s], (q_uses[s] & 1) ^ 1, wc, W_PRE_Q_EMPTY)) {
             ok = false;
             return;
           }
@@ -330,7 +361,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
                         t.row0 + t.tok0 + s * p.tq);
         };
         auto load_kv = [&](const CUtensorMap* map, int i) {
-          if (!ok || !mbar_wait(&bar.kv_empty[stage], (fill & 1) ^ 1, wc, W_PRE_KV_EMPTY)) {
+          if (!ok || !pre_wait(&bar.kv_empty[stage], (fill & 1) ^ 1, wc, W_PRE_KV_EMPTY)) {
             ok = false;
             return;
           }
@@ -384,10 +415,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           mma_bf16_ts(tmem + 256 + s * kHeadDim, tmem + s * kPreTile + k * 8, bd + k * 128, idesc_pv, !(first && k == 0));
       };
       auto kv_wait = [&](int at) {
-        return mbar_wait(&bar.kv_full[at % T::kStages], (at / T::kStages) & 1, wc, W_PRE_KV_FULL);
+        return pre_wait(&bar.kv_full[at % T::kStages], (at / T::kStages) & 1, wc, W_PRE_KV_FULL);
       };
       auto q_wait = [&](int s) {
-        const bool ok = mbar_wait(&bar.q_full[s], q_uses[s] & 1, wc, W_PRE_Q_FULL);
+        const bool ok = pre_wait(&bar.q_full[s], q_uses[s] & 1, wc, W_PRE_Q_FULL);
         ++q_uses[s];
         return ok;
       };
@@ -416,14 +447,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           ok = kv_wait(v_at);
           if (ok && i >= mask0) {
             const int st = v_at % T::kStages;
-            ok = mbar_wait(&bar.v_ok[st], (v_phase >> st) & 1, wc, W_PRE_V);
+            ok = pre_wait(&bar.v_ok[st], (v_phase >> st) & 1, wc, W_PRE_V);
             v_phase ^= 1u << st;
           }
           bool have_k = false;
           for (int s = 0; s < 2 && ok; ++s) {
             const int ns = s ? t.n1 : t.n0;
             if (i < ns) {
-              ok = mbar_wait(&bar.p_full[s], p_uses[s] & 1, wc, W_PRE_P);
+              ok = pre_wait(&bar.p_full[s], p_uses[s] & 1, wc, W_PRE_P);
               ++p_uses[s];
               if (!ok) break;
               tc_fence_after();
@@ -494,7 +525,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.tile_empty[k % kPreRing]);
     }
+  }
   } else {
+    more_registers<kPreRegsSoftmax>();
     // ================================================================ softmax of query tile s, and its output
     const int s = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
