@@ -165,6 +165,11 @@ __device__ __forceinline__ bool pre_wait(uint64_t* bar, uint32_t parity, const W
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where) {
   return __all_sync(~0u, pre_wait(bar, parity, w, where));
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 // Two fp32 lanes in one 64-bit register.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -392,91 +397,111 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     __syncwarp();
   } else if (warp == 8) {
     // ================================================================ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile), idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true);
-      int q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
-      uint32_t v_phase = 0;
-      int kv = 0;  // index into the sequence K0 V0 K1 V1 ... of loads
-      auto qk = [&](int s, int at, bool last) {  // S_s = Q_s K^T with K in ring slot `at`
-        const uint32_t a = q_smem + s * kPreTileBytes, b = kv_smem + (at % T::kStages) * kPreTileBytes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t ad = sdesc_k_sw128(a + h * (kPreTileBytes / 2)), bd = sdesc_k_sw128(b + h * (kPreTileBytes / 2));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(tmem + s * kPreTile, ad + k * 2, bd + k * 2, idesc_qk, (h | k) != 0);
-        }
-        mma_commit(&bar.s_full[s]);
-        if (last) mma_commit(&bar.q_empty[s]);
-      };
-      auto pv = [&](int s, int at, bool first) {  // O_s (+)= P_s V with V in ring slot `at`
-        const uint64_t bd = sdesc_mn_sw128(kv_smem + (at % T::kStages) * kPreTileBytes, kPreTileBytes / 2);
+    // The whole warp walks the loop, so that descriptors stay in uniform registers, and one elected lane issues.
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile), idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true);
+    constexpr uint32_t kStep16 = kPreTileBytes / 16;  // one tile in descriptor units
+    const bool one = elect_one();
+    const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem),
+                   v_desc = sdesc_mn_sw128(kv_smem, kPreTileBytes / 2);
+    uint32_t q_phase = 0, p_phase = 0, v_phase = 0, kv_phase = 0;  // a bit for each barrier
+    int slot = 0;                                                  // ring slot of the next K or V tile
+    auto kv_wait = [&](int at) {
+      const bool ok = warp_wait(&bar.kv_full[at], (kv_phase >> at) & 1, wc, W_PRE_KV_FULL);
+      kv_phase ^= 1u << at;
+      return ok;
+    };
+    auto next_slot = [&]() {
+      const int at = slot;
+      slot = slot + 1 == T::kStages ? 0 : slot + 1;
+      return at;
+    };
+    auto q_wait = [&](int s) {
+      const bool ok = warp_wait(&bar.q_full[s], (q_phase >> s) & 1, wc, W_PRE_Q_FULL);
+      q_phase ^= 1u << s;
+      return ok;
+    };
+    auto qk = [&](int s, int at, bool last) {  // S_s = Q_s K^T with K in ring slot `at`
+      if (one) {
+        const uint64_t ad = q_desc + s * kStep16, bd = k_desc + at * kStep16;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_bf16_ts(tmem + 256 + s * kHeadDim, tmem + s * kPreTile + k * 8, bd + k * 128, idesc_pv, !(first && k == 0));
-      };
-      auto kv_wait = [&](int at) {
-        return pre_wait(&bar.kv_full[at % T::kStages], (at / T::kStages) & 1, wc, W_PRE_KV_FULL);
-      };
-      auto q_wait = [&](int s) {
-        const bool ok = pre_wait(&bar.q_full[s], q_uses[s] & 1, wc, W_PRE_Q_FULL);
-        ++q_uses[s];
-        return ok;
-      };
-      PrefillTile t, u;
-      bool ok = get_tile(0, t);
-      if (ok) {
-        mbar_arrive(&bar.tile_empty[0]);
-        ok = kv_wait(0);
-        for (int s = 0; s < 2 && ok; ++s)
-          if ((s ? t.n1 : t.n0) > 0) {
-            ok = q_wait(s);
-            if (ok) qk(s, 0, (s ? t.n1 : t.n0) == 1);
-          }
-        if (ok) mma_commit(&bar.kv_empty[0]);
+          mma_bf16(tmem + s * kPreTile, ad + (k >> 2) * (kStep16 / 2) + (k & 3) * 2,
+                   bd + (k >> 2) * (kStep16 / 2) + (k & 3) * 2, idesc_qk, k != 0);
+        mma_commit(&bar.s_full[s]);
+        if (last) mma_commit(&bar.q_empty[s]);
       }
-      for (int k = 0; ok; ++k) {
-        const int n = max(t.n0, t.n1), mask0 = first_masked(t);
-        bool more = false;
-        for (int i = 0; i < n && ok; ++i) {
-          const int v_at = kv + 1, k_at = kv + 2;
-          const bool last = i == n - 1;
-          if (last) {
-            more = get_tile(k + 1, u);
-            if (more) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
-          }
-          ok = kv_wait(v_at);
-          if (ok && i >= mask0) {
-            const int st = v_at % T::kStages;
-            ok = pre_wait(&bar.v_ok[st], (v_phase >> st) & 1, wc, W_PRE_V);
-            v_phase ^= 1u << st;
-          }
-          bool have_k = false;
-          for (int s = 0; s < 2 && ok; ++s) {
-            const int ns = s ? t.n1 : t.n0;
-            if (i < ns) {
-              ok = pre_wait(&bar.p_full[s], p_uses[s] & 1, wc, W_PRE_P);
-              ++p_uses[s];
-              if (!ok) break;
-              tc_fence_after();
-              pv(s, v_at, i == 0);
-              if (i == ns - 1) mma_commit(&bar.o_full[s]);
-            }
-            const int un = s ? u.n1 : u.n0;
-            if (last ? more && un > 0 : i + 1 < ns) {
-              if (!have_k) ok = kv_wait(k_at);
-              have_k = true;
-              if (ok && last) ok = q_wait(s);
-              if (ok) qk(s, k_at, last ? un == 1 : i + 1 == ns - 1);
-            }
-          }
-          if (!ok) break;
-          mma_commit(&bar.kv_empty[v_at % T::kStages]);
-          if (have_k) mma_commit(&bar.kv_empty[k_at % T::kStages]);
-          kv += 2;
+      __syncwarp();
+    };
+    auto pv = [&](int s, int at, bool first, bool last) {  // O_s (+)= P_s V with V in ring slot `at`
+      if (one) {
+        const uint64_t bd = v_desc + at * kStep16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_ts(tmem + 256 + s * kHeadDim, tmem + s * kPreTile + k * 8, bd + k * 128, idesc_pv, !first || k != 0);
+        if (last) mma_commit(&bar.o_full[s]);
+      }
+      __syncwarp();
+    };
+    PrefillTile t, u = {};
+    bool ok = __all_sync(~0u, get_tile(0, t));
+    if (ok) {
+      if (one) mbar_arrive(&bar.tile_empty[0]);
+      const int at = next_slot();
+      ok = kv_wait(at);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int ns = s ? t.n1 : t.n0;
+        if (ok && ns > 0) {
+          ok = q_wait(s);
+          if (ok) qk(s, at, ns == 1);
         }
-        if (!more) break;
-        t = u;
       }
+      if (ok && one) mma_commit(&bar.kv_empty[at]);
+    }
+    for (int k = 0; ok; ++k) {
+      const int n = max(t.n0, t.n1), mask0 = first_masked(t);
+      bool more = false;
+      for (int i = 0; i < n && ok; ++i) {
+        const bool last = i == n - 1;
+        if (last) {
+          more = __all_sync(~0u, get_tile(k + 1, u));
+          if (more && one) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
+        }
+        const int v_at = next_slot();
+        ok = kv_wait(v_at);
+        if (ok && i >= mask0) {
+          ok = warp_wait(&bar.v_ok[v_at], (v_phase >> v_at) & 1, wc, W_PRE_V);
+          v_phase ^= 1u << v_at;
+        }
+        const bool next = !last || more;  // another key tile, of this unit of work or the next
+        int k_at = 0;
+        if (ok && next) {
+          k_at = next_slot();
+          ok = kv_wait(k_at);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int ns = s ? t.n1 : t.n0, un = s ? u.n1 : u.n0;
+          if (ok && i < ns) {
+            ok = warp_wait(&bar.p_full[s], (p_phase >> s) & 1, wc, W_PRE_P);
+            p_phase ^= 1u << s;
+            tc_fence_after();
+            if (ok) pv(s, v_at, i == 0, i == ns - 1);
+          }
+          if (ok && (last ? more && un > 0 : i + 1 < ns)) {
+            if (last) ok = q_wait(s);
+            if (ok) qk(s, k_at, last ? un == 1 : i + 1 == ns - 1);
+          }
+        }
+        if (ok && one) {
+          mma_commit(&bar.kv_empty[v_at]);
+          if (next) mma_commit(&bar.kv_empty[k_at]);
+        }
+      }
+      if (!more) break;
+      t = u;
+    }
+    if (one) {
       mma_commit(&bar.drain);  // nothing of this CTA's products or their arrivals is left behind
       mbar_wait_quiet(&bar.drain, 0, p.timeout_ns);
     }
