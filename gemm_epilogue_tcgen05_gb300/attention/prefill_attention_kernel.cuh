@@ -13,8 +13,8 @@
 //   (TMEM)  ->  O_s += P_s V (A from TMEM, V as stored: MN-major B; TMEM, 128 columns each).  512 columns in all.
 //
 // Warps 0-3 and 4-7: softmax of query tile 0 and 1 and its output.  Warp 8: one thread issues the MMAs.  Warp 9:
-// one thread issues the TMA loads (Q by a 3-D map over (dimension, head, row); K and V into one ring of 32 KB
-// stages).  Warp 10: which tile comes next; the scales of E4M3 keys and values.  Warp 11: V rows in masked tiles.
+// one thread issues the TMA loads (Q by a 3-D map over (dimension, head, row); a V tile and the K tile behind it
+// into one of two 64 KB stages).  Warp 10: which tile comes next; the scales of E4M3 keys and values.  Warp 11: V rows in masked tiles.
 // One persistent CTA on each SM; the next tile's loads, its first products and the last one's output overlap.
 //
 // The row maximum is only raised when a logit passes it by more than 2^8 (in the weights); then the thread that
@@ -76,10 +76,10 @@ struct alignas(128) PrefillParams {
 
 template <bool FP8>
 struct PrefillTraits {
-  static constexpr int kStages = FP8 ? 4 : 5;
+  static constexpr int kStages = 2;  // of a V tile and the next K tile, 64 KB
   static constexpr int kBars = 1024;
   static constexpr int kScales = FP8 ? 2 * 2 * kPreTile * 4 : 0;
-  static constexpr int kSmem = 2 * kPreTileBytes + kStages * kPreTileBytes + kScales + kBars + 1024 /*alignment*/;
+  static constexpr int kSmem = (2 + 2 * kStages) * kPreTileBytes + kScales + kBars + 1024 /*alignment*/;
 };
 
 // One unit of work.
@@ -94,7 +94,7 @@ struct PrefillTile {
 struct PrefillBars {
   uint64_t tile_full[kPreRing], tile_empty[kPreRing];
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[5], kv_empty[5], v_ok[5];
+  uint64_t kv_full[2], kv_empty[2], v_ok[2];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t sc_full[2], sc_empty[2];
   uint64_t drain;
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * kPreTileBytes;
-  float* scales = reinterpret_cast<float*>(smem + (2 + T::kStages) * kPreTileBytes);  // [2][K | V][128]
-  PrefillBars& bar = *reinterpret_cast<PrefillBars*>(smem + (2 + T::kStages) * kPreTileBytes + T::kScales);
+  float* scales = reinterpret_cast<float*>(smem + (2 + 2 * T::kStages) * kPreTileBytes);  // [2][K | V][128]
+  PrefillBars& bar = *reinterpret_cast<PrefillBars*>(smem + (2 + 2 * T::kStages) * kPreTileBytes + T::kScales);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = gridDim.x, cta = blockIdx.x;
 
@@ -346,52 +346,54 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   } else if (warp == 9) {
     // ================================================================ TMA loads
     if (lane == 0) {
-      int stage = 0, fill = 0, q_uses[2] = {0, 0}, issued = 0;
+      int fills = 0, q_uses[2] = {0, 0};
       bool ok = true;
-      PrefillTile t;
-      for (int k = 0; ok && get_tile(k, t); ++k) {
-        mbar_arrive(&bar.tile_empty[k % kPreRing]);
-        const int n = max(t.n0, t.n1);
-        auto load_q = [&](int s) {
-          if ((s ? t.n1 : t.n0) == 0) return;
-          if (!pre_wait(&bar.q_empty[s], (q_uses[s] & 1) ^ 1, wc, W_PRE_Q_EMPTY)) {
-            ok = false;
-            return;
-          }
+      PrefillTile t, u;
+      auto load_q = [&](const PrefillTile& t) {
+        for (int s = 0; s < 2 && ok; ++s) {
+          if ((s ? t.n1 : t.n0) == 0) continue;
+          ok = pre_wait(&bar.q_empty[s], (q_uses[s] & 1) ^ 1, wc, W_PRE_Q_EMPTY);
+          if (!ok) return;
           ++q_uses[s];
           mbar_arrive_expect_tx(&bar.q_full[s], static_cast<uint32_t>(p.hp * p.tq * kHeadDim * 2));
-          const uint32_t dst = q_smem + s * kPreTileBytes;
           for (int h = 0; h < 2; ++h)
-            tma_load_3d(&p.map_q, &bar.q_full[s], dst + h * (kPreTileBytes / 2), h * 64, t.head0,
+            tma_load_3d(&p.map_q, &bar.q_full[s], q_smem + s * kPreTileBytes + h * (kPreTileBytes / 2), h * 64, t.head0,
                         t.row0 + t.tok0 + s * p.tq);
-        };
-        auto load_kv = [&](const CUtensorMap* map, int i) {
-          if (!ok || !pre_wait(&bar.kv_empty[stage], (fill & 1) ^ 1, wc, W_PRE_KV_EMPTY)) {
-            ok = false;
-            return;
-          }
-          mbar_arrive_expect_tx(&bar.kv_full[stage], kPreTileBytes);
-          uint8_t* dst = smem + (2 + stage) * kPreTileBytes;
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d(map, &bar.kv_full[stage], dst + h * (kPreTileBytes / 2), t.kvh * kHeadDim + h * 64,
-                        t.row0 + i * kPreTile);
-          ++issued;
-          if (++stage == T::kStages) stage = 0, ++fill;
-        };
-        load_q(0);
-        load_kv(&p.map_k, 0);
-        if (ok) load_q(1);
-        load_kv(&p.map_v, 0);
-        for (int i = 1; i < n && ok; ++i) {
-          load_kv(&p.map_k, i);
-          load_kv(&p.map_v, i);
         }
+      };
+      // one stage: key tile vi of a unit's V, and key tile ki of the same or the next unit's K (either may be absent)
+      auto load_kv = [&](const PrefillTile* v, int vi, const PrefillTile* k, int ki) {
+        const int st = fills & 1;
+        if (!ok || !(ok = pre_wait(&bar.kv_empty[st], ((fills >> 1) & 1) ^ 1, wc, W_PRE_KV_EMPTY))) return;
+        mbar_arrive_expect_tx(&bar.kv_full[st], ((v != nullptr) + (k != nullptr)) * kPreTileBytes);
+        uint8_t* dst = smem + (2 + 2 * st) * kPreTileBytes;
+        for (int h = 0; h < 2 && v != nullptr; ++h)
+          tma_load_2d(&p.map_v, &bar.kv_full[st], dst + h * (kPreTileBytes / 2), v->kvh * kHeadDim + h * 64,
+                      v->row0 + vi * kPreTile);
+        for (int h = 0; h < 2 && k != nullptr; ++h)
+          tma_load_2d(&p.map_k, &bar.kv_full[st], dst + kPreTileBytes + h * (kPreTileBytes / 2),
+                      k->kvh * kHeadDim + h * 64, k->row0 + ki * kPreTile);
+        ++fills;
+      };
+      bool more = get_tile(0, t);
+      if (more) {
+        load_kv(nullptr, 0, &t, 0);
+        load_q(t);
+      }
+      for (int k = 0; more && ok; ++k) {
+        mbar_arrive(&bar.tile_empty[k % kPreRing]);
+        const int n = max(t.n0, t.n1);
+        for (int i = 0; i + 1 < n; ++i) load_kv(&t, i, &t, i + 1);
+        more = get_tile(k + 1, u);
+        load_kv(&t, n - 1, more ? &u : nullptr, 0);
+        if (more) load_q(u);
+        t = u;
       }
       if (bar.abort_flag) {  // leave no copy in flight
         for (int s = 0; s < 2; ++s)
           if (q_uses[s] > 0) mbar_wait_quiet(&bar.q_full[s], (q_uses[s] - 1) & 1, p.timeout_ns);
-        for (int i = max(0, issued - T::kStages); i < issued; ++i)
-          mbar_wait_quiet(&bar.kv_full[i % T::kStages], (i / T::kStages) & 1, p.timeout_ns);
+        for (int i = max(0, fills - T::kStages); i < fills; ++i)
+          mbar_wait_quiet(&bar.kv_full[i & 1], (i >> 1) & 1, p.timeout_ns);
       }
     }
     __syncwarp();
@@ -401,28 +403,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile), idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true);
     constexpr uint32_t kStep16 = kPreTileBytes / 16;  // one tile in descriptor units
     const bool one = elect_one();
-    const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem),
+    const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem + kPreTileBytes),
                    v_desc = sdesc_mn_sw128(kv_smem, kPreTileBytes / 2);
-    uint32_t q_phase = 0, p_phase = 0, v_phase = 0, kv_phase = 0;  // a bit for each barrier
-    int slot = 0;                                                  // ring slot of the next K or V tile
-    auto kv_wait = [&](int at) {
-      const bool ok = warp_wait(&bar.kv_full[at], (kv_phase >> at) & 1, wc, W_PRE_KV_FULL);
-      kv_phase ^= 1u << at;
+    uint32_t q_phase = 0, p_phase = 0, v_phase = 0;  // a bit for each barrier
+    uint32_t uses = 0;                               // stages waited for: the next one is (uses & 1)
+    auto stage_wait = [&]() {
+      const bool ok = warp_wait(&bar.kv_full[uses & 1], (uses >> 1) & 1, wc, W_PRE_KV_FULL);
+      ++uses;
       return ok;
-    };
-    auto next_slot = [&]() {
-      const int at = slot;
-      slot = slot + 1 == T::kStages ? 0 : slot + 1;
-      return at;
     };
     auto q_wait = [&](int s) {
       const bool ok = warp_wait(&bar.q_full[s], (q_phase >> s) & 1, wc, W_PRE_Q_FULL);
       q_phase ^= 1u << s;
       return ok;
     };
-    auto qk = [&](int s, int at, bool last) {  // S_s = Q_s K^T with K in ring slot `at`
+    auto qk = [&](int s, int st, bool last) {  // S_s = Q_s K^T
       if (one) {
-        const uint64_t ad = q_desc + s * kStep16, bd = k_desc + at * kStep16;
+        const uint64_t ad = q_desc + s * kStep16, bd = k_desc + st * (2 * kStep16);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           mma_bf16(tmem + s * kPreTile, ad + (k >> 2) * (kStep16 / 2) + (k & 3) * 2,
@@ -432,9 +429,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       }
       __syncwarp();
     };
-    auto pv = [&](int s, int at, bool first, bool last) {  // O_s (+)= P_s V with V in ring slot `at`
+    auto pv = [&](int s, int st, bool first, bool last) {  // O_s (+)= P_s V
       if (one) {
-        const uint64_t bd = v_desc + at * kStep16;
+        const uint64_t bd = v_desc + st * (2 * kStep16);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           mma_bf16_ts(tmem + 256 + s * kHeadDim, tmem + s * kPreTile + k * 8, bd + k * 128, idesc_pv, !first || k != 0);
@@ -446,38 +443,30 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     bool ok = __all_sync(~0u, get_tile(0, t));
     if (ok) {
       if (one) mbar_arrive(&bar.tile_empty[0]);
-      const int at = next_slot();
-      ok = kv_wait(at);
+      ok = stage_wait();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int ns = s ? t.n1 : t.n0;
         if (ok && ns > 0) {
           ok = q_wait(s);
-          if (ok) qk(s, at, ns == 1);
+          if (ok) qk(s, 0, ns == 1);
         }
       }
-      if (ok && one) mma_commit(&bar.kv_empty[at]);
+      if (ok && one) mma_commit(&bar.kv_empty[0]);
+      ok = ok && stage_wait();
     }
+    // The queue behind the tensor cores holds about three instructions (some 190 cycles), so between two products
+    // stands one wait at most: the one for a P before its PV, the one for the next stage before the second QK.
     for (int k = 0; ok; ++k) {
       const int n = max(t.n0, t.n1), mask0 = first_masked(t);
-      bool more = false;
+      const bool more = __all_sync(~0u, get_tile(k + 1, u));
+      if (more && one) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
       for (int i = 0; i < n && ok; ++i) {
-        const bool last = i == n - 1;
-        if (last) {
-          more = __all_sync(~0u, get_tile(k + 1, u));
-          if (more && one) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
-        }
-        const int v_at = next_slot();
-        ok = kv_wait(v_at);
-        if (ok && i >= mask0) {
-          ok = warp_wait(&bar.v_ok[v_at], (v_phase >> v_at) & 1, wc, W_PRE_V);
-          v_phase ^= 1u << v_at;
-        }
-        const bool next = !last || more;  // another key tile, of this unit of work or the next
-        int k_at = 0;
-        if (ok && next) {
-          k_at = next_slot();
-          ok = kv_wait(k_at);
+        const bool last = i == n - 1, next = !last || more;  // another key tile, of this unit of work or the next
+        const int st = (uses - 1) & 1;
+        if (i >= mask0) {
+          ok = warp_wait(&bar.v_ok[st], (v_phase >> st) & 1, wc, W_PRE_V);
+          v_phase ^= 1u << st;
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -486,17 +475,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             ok = warp_wait(&bar.p_full[s], (p_phase >> s) & 1, wc, W_PRE_P);
             p_phase ^= 1u << s;
             tc_fence_after();
-            if (ok) pv(s, v_at, i == 0, i == ns - 1);
+            if (ok) pv(s, st, i == 0, i == ns - 1);
           }
+          if (s == 1 && next && ok) ok = stage_wait();
           if (ok && (last ? more && un > 0 : i + 1 < ns)) {
             if (last) ok = q_wait(s);
-            if (ok) qk(s, k_at, last ? un == 1 : i + 1 == ns - 1);
+            if (ok) qk(s, st, last ? un == 1 : i + 1 == ns - 1);
           }
         }
-        if (ok && one) {
-          mma_commit(&bar.kv_empty[v_at]);
-          if (next) mma_commit(&bar.kv_empty[k_at]);
-        }
+        if (ok && one) mma_commit(&bar.kv_empty[st]);
       }
       if (!more) break;
       t = u;
@@ -509,21 +496,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   } else if (warp == 11) {
     // ================================================================ V of masked tiles: finite values only
     PrefillTile t;
-    int kv = 0;
+    int fills = 1;  // the first holds a K tile only
     bool ok = true;
     for (int k = 0; ok && __all_sync(~0u, get_tile(k, t)); ++k) {
+      if (k == 0) {
+        if (!(ok = warp_wait(&bar.kv_full[0], 0, wc, W_PRE_KV_FULL))) break;
+        if (lane == 0) mbar_arrive(&bar.kv_empty[0]);
+      }
       const int n = max(t.n0, t.n1);
       const int mask0 = first_masked(t);
       // Every fill of the ring passes here in order (a parity says nothing about older or newer phases), so
       // a stage is only free once this warp has seen it, too.
-      for (int i = 0; i < 2 * n; ++i, ++kv) {
-        const int st = kv % T::kStages;
-        if (!(ok = warp_wait(&bar.kv_full[st], (kv / T::kStages) & 1, wc, W_PRE_KV_FULL))) break;
-        if ((i & 1) == 0 || (i >> 1) < mask0) {
+      for (int i = 0; i < n; ++i, ++fills) {
+        const int st = fills & 1;
+        if (!(ok = warp_wait(&bar.kv_full[st], (fills >> 1) & 1, wc, W_PRE_KV_FULL))) break;
+        if (i < mask0) {
           if (lane == 0) mbar_arrive(&bar.kv_empty[st]);
           continue;
         }
-        const uint32_t base = kv_smem + st * kPreTileBytes + lane * 16;
+        const uint32_t base = kv_smem + st * 2 * kPreTileBytes + lane * 16;
         uint32_t seen = 0;
 #pragma unroll 8
         for (int c = 0; c < kPreTileBytes / 512; ++c) {
