@@ -1,6 +1,7 @@
 // attention_prefill: argument checks, tensor maps and launch (the kernel: prefill_attention_kernel.cuh).
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -8,6 +9,8 @@
 
 namespace fl {
 namespace {
+
+constexpr int64_t kL2Share = 32 << 20;  // keys and values of the heads worked off together
 
 // 3-D tiled map over Q [rows][heads][128] bf16 with a row pitch of ld elements.
 bool encode_q(CUtensorMap* map, const void* base, int heads, int rows, int64_t ld, int hp, int tq) {
@@ -110,6 +113,10 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   while (p.group % p.hp != 0) --p.hp;
   p.tq = kPreTile / p.hp;
   p.pairs = n_heads / p.hp;
+  const int64_t kv_bytes = static_cast<int64_t>(M) * kHeadDim * 4;  // of one kv head, as bf16
+  const int64_t at_once = std::max<int64_t>(kL2Share / kv_bytes, 1);
+  const int64_t groups = (n_kv_heads + at_once - 1) / at_once;
+  p.pairs_at_once = static_cast<int>((n_kv_heads + groups - 1) / groups) * (p.group / p.hp);
   p.batch = cu_seqlens == nullptr ? (M - 1) / seq_len + 1 : batch;
   p.seq_len = seq_len;
   const long long per_cta = 2 * p.tq;
@@ -144,6 +151,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   p.causal = causal != 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.status = reinterpret_cast<int*>(ws);
+  p.work = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);
   p.timeout_ns = wait_timeout_ns();
   if (fp8) {
     const long long work = (2ll * M * (kv_w / 16) + 255) / 256;

@@ -14,7 +14,7 @@
 //
 // Warps 0-3 and 4-7: softmax of query tile 0 and 1 and its output.  Warp 8: one thread issues the MMAs.  Warp 9:
 // one thread issues the TMA loads (Q by a 3-D map over (dimension, head, row); a V tile and the K tile behind it
-// into one of two 64 KB stages).  Warp 10: which tile comes next; the scales of E4M3 keys and values.  Warp 11: V rows in masked tiles.
+// into one of two 64 KB stages).  Warp 10: which tile comes next.  Warp 11: V rows in masked tiles.
 // One persistent CTA on each SM; the next tile's loads, its first products and the last one's output overlap.
 //
 // The row maximum is only raised when a logit passes it by more than 2^8 (in the weights); then the thread that
@@ -22,13 +22,18 @@
 // all products before it), so no hand-over is needed.
 //
 // Work: tile (sequence, block of tokens, kv head) by falling block index, so the longest come first whatever the
-// sequences' lengths are; CTA c takes ranks c, 2 G - 1 - c, 2 G + c, ...
+// sequences' lengths are (without the causal mask by falling length), each taken by the CTA that is free next
+// (an atomic counter, one tile ahead).  Neighbouring ranks are the heads of one
+// block: K and V are met again by every block of the sequence, and the keys and values of all heads of all
+// sequences can be more than the L2 holds.  So the heads are worked off in groups whose keys and values are at
+// most 32 MB.
 //
 // Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
 //
 // E4M3: a first kernel turns the codes of K and V into bf16 (exact) in the workspace; their scales stay fp32:
-// K's multiplies the logits, V's the weights before these are rounded to bf16.
+// K's multiplies the logits, V's the weights before these are rounded to bf16.  (Scaled values rounded to bf16 would
+// need no work here, but add their error to that of the weights.)
 #pragma once
 #include <climits>
 
@@ -43,15 +48,14 @@ constexpr int kPreRegs = 168, kPreRegsSoftmax = 200, kPreRegsOther = 104;
 static_assert(kPreThreads * kPreRegs == 256 * kPreRegsSoftmax + 128 * kPreRegsOther, "register split");
 constexpr int kPreTile = 128;                      // query rows of a tile, and keys of a tile
 constexpr int kPreTileBytes = kPreTile * kHeadDim * 2;
-constexpr int kPreRing = 4;                        // tile descriptors
+constexpr int kPreRing = 3;                        // tile descriptors
 constexpr float kPreNone = -3e38f;                 // a maximum over nothing: any finite logit passes it
 constexpr float kPreLazy = 8.f;
 
 // Where a wait gave up (recorded in the workspace's status record).
 enum : int {
   W_PRE_TILE_FULL = 20, W_PRE_TILE_EMPTY = 21, W_PRE_Q_EMPTY = 22, W_PRE_Q_FULL = 23, W_PRE_KV_EMPTY = 24,
-  W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29, W_PRE_SCALE_FULL = 30,
-  W_PRE_SCALE_EMPTY = 31
+  W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29, W_PRE_SCALE = 30
 };
 
 struct alignas(128) PrefillParams {
@@ -69,8 +73,10 @@ struct alignas(128) PrefillParams {
   int M, batch, seq_len, causal;
   int group, hp, tq;       // query heads of a kv head; heads and tokens of a query tile
   int pairs;               // head packs of a token block: n_kv * group / hp
+  int pairs_at_once;       // of which this many are worked off before the next ones begin
   float scale_log2;
   int* status;
+  unsigned* work;          // [0] ranks given out beyond the first of each CTA, [1] CTAs that found none left
   unsigned long long timeout_ns;
 };
 
@@ -78,7 +84,9 @@ template <bool FP8>
 struct PrefillTraits {
   static constexpr int kStages = 2;  // of a V tile and the next K tile, 64 KB
   static constexpr int kBars = 1024;
-  static constexpr int kScales = FP8 ? 2 * 2 * kPreTile * 4 : 0;
+  // E4M3: for each query tile two buffers of K's and V's scales (four runs of 32 + 4), and a factor for each row
+  static constexpr int kScaleRun = 36, kScaleSet = 4 * kScaleRun;
+  static constexpr int kScales = FP8 ? 2 * (4 * kScaleSet + kPreTile) * 4 : 0;
   static constexpr int kSmem = (2 + 2 * kStages) * kPreTileBytes + kScales + kBars + 1024 /*alignment*/;
 };
 
@@ -96,7 +104,7 @@ struct PrefillBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[2], kv_empty[2], v_ok[2];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t sc_full[2], sc_empty[2];
+  uint64_t sc_full[2];
   uint64_t drain;
   PrefillTile tile[kPreRing];
   int abort_flag;
@@ -126,6 +134,55 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Shapes of 16 lanes: x16 of 16x256b is 128 columns (a thread t has columns 8 k + 2 (t % 4) + {0, 1} of lanes t / 4 and
+// t / 4 + 8 in registers 4 k .. 4 k + 3), x16 of 16x128b 64 columns (column 4 k + t % 4 of the same lanes).
+__device__ __forceinline__ void tmem_ld_16x256b_x16(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+      "%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,"
+      "%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+      "}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
+      "};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b_x16(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31,%32"
+      "};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 template <int N>
@@ -211,7 +268,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.sc_full[i], 32), mbar_init(&bar.sc_empty[i], 8);
+      mbar_init(&bar.sc_full[i], 4);
     }
     for (int i = 0; i < T::kStages; ++i)
       mbar_init(&bar.kv_full[i], 1), mbar_init(&bar.kv_empty[i], 2), mbar_init(&bar.v_ok[i], 1);
@@ -245,54 +302,85 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   if (warp >= 8) {
   fewer_registers<kPreRegsOther>();
   if (warp == 10) {
-    // ================================================================ tiles, and the scales of E4M3 K and V
+    // ================================================================ tiles
     const int tpc = 2 * p.tq;
-    auto blocks_of = [&](int b) {
+    // Tiers: sequences have blocks [0, blocks) of tpc tokens.  Causal: block j costs about j, tier j is block j of
+    // each sequence that has one.  Full mask: a block costs as much as its sequence has key tiles, tier j is all
+    // blocks of the sequences with j + 1 key tiles.
+    auto length_of = [&](int b) {
       int first, last;
       sequence_rows(p.cu, b, p.seq_len, p.M, first, last);
-      return last > first ? (last - first - 1) / tpc + 1 : 0;
+      return last - first;
     };
-    int mine = 0, tier = 0;
-    if (lane < p.batch) mine = blocks_of(lane);
-    // sum over the sequences of max(0, blocks - j): blocks with an index of at least j
-    auto at_least = [&](int j) -> int {
-      int n = max(0, mine - j);
-      for (int b = lane + 32; b < p.batch; b += 32) n += max(0, blocks_of(b) - j);
-      return __reduce_add_sync(~0u, n);
+    auto tiers_of = [&](int len) { return len > 0 ? (len - 1) / (p.causal ? tpc : kPreTile) + 1 : 0; };
+    auto blocks_in = [&](int len, int tier) {  // a sequence's blocks in a tier
+      if (p.causal) return tiers_of(len) > tier ? 1 : 0;
+      return tiers_of(len) == tier + 1 ? (len - 1) / tpc + 1 : 0;
     };
-    {
-      int n = mine;
-      for (int b = lane + 32; b < p.batch; b += 32) n = max(n, blocks_of(b));
-      tier = __reduce_max_sync(~0u, n);
-    }
-    int above = 0, upto = 0;  // blocks of higher tiers, and with this tier's
-    auto produce = [&](int k) -> bool {
-      if (!warp_wait(&bar.tile_empty[k % kPreRing], ((k / kPreRing) & 1) ^ 1, wc, W_PRE_TILE_EMPTY)) return false;
-      const long long rank = static_cast<long long>(k) * G + ((k & 1) ? G - 1 - cta : cta);
-      const int block = static_cast<int>(min(rank / p.pairs, static_cast<long long>(INT_MAX)));
-      const int pair = static_cast<int>(rank - static_cast<long long>(block) * p.pairs);
+    const int mine = lane < p.batch ? length_of(lane) : 0;
+    auto over_sequences = [&](auto&& f, bool take_max) -> int {
+      int n = f(mine);
+      for (int b = lane + 32; b < p.batch; b += 32) {
+        const int x = f(length_of(b));
+        n = take_max ? max(n, x) : n + x;
+      }
+      return take_max ? __reduce_max_sync(~0u, n) : __reduce_add_sync(~0u, n);
+    };
+    const int tiers = over_sequences(tiers_of, true);
+    const long long blocks = over_sequences([&](int len) { return len > 0 ? (len - 1) / tpc + 1 : 0; }, false);
+    int tier = tiers, above = 0, upto = 0;  // blocks of higher tiers, and with this tier's
+    int pair0 = 0, n_pairs = min(p.pairs, p.pairs_at_once);  // the group of heads
+    long long rank0 = 0;                                     // its first rank
+    bool more = true, long_before = false;
+    for (int k = 0; more; ++k) {
+      if (!warp_wait(&bar.tile_empty[k % kPreRing], ((k / kPreRing) & 1) ^ 1, wc, W_PRE_TILE_EMPTY)) break;
+      // behind a long tile the next one is only taken once the tile before it is done: it goes to who is free
+      if (k >= 2 && long_before &&
+          !warp_wait(&bar.tile_empty[(k - 2) % kPreRing], ((k - 2) / kPreRing) & 1, wc, W_PRE_TILE_EMPTY))
+        break;
+      unsigned taken = 0;
+      if (k > 0 && lane == 0) taken = atomicAdd(p.work, 1u);
+      const long long rank = k == 0 ? cta : static_cast<long long>(G) + __shfl_sync(~0u, taken, 0);
+      while (rank >= rank0 + blocks * n_pairs && pair0 + n_pairs < p.pairs) {  // on to the next group
+        rank0 += blocks * n_pairs;
+        pair0 += n_pairs;
+        n_pairs = min(p.pairs - pair0, p.pairs_at_once);
+        tier = tiers, above = 0, upto = 0;
+      }
+      const long long block = (rank - rank0) / n_pairs;
+      const int pair = pair0 + static_cast<int>((rank - rank0) % n_pairs);
       while (tier > 0 && upto <= block) {
         above = upto;
-        upto = at_least(--tier);
+        --tier;
+        upto += over_sequences([&](int len) { return blocks_in(len, tier); }, false);
       }
       PrefillTile t = {};
-      if (upto > block) {  // the (block - above)-th sequence that reaches this tier
-        int skip = block - above, seq = -1;
+      more = upto > block;
+      if (more) {  // the sequence that holds the (block - above)-th block of this tier
+        int skip = static_cast<int>(block - above), seq = 0, in = 0;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
-          const bool reaches = b0 + lane < p.batch && (b0 == 0 ? mine : blocks_of(b0 + lane)) > tier;
-          const unsigned who = __ballot_sync(~0u, reaches);
-          const int n = __popc(who);
-          if (skip < n) {
-            seq = b0 + __fns(who, 0, skip + 1);
+          const int len = b0 == 0 ? mine : b0 + lane < p.batch ? length_of(b0 + lane) : 0;
+          const int have = blocks_in(len, tier);
+          int sum = have;  // inclusive sum over the lanes
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += y;
+          }
+          const unsigned who = __ballot_sync(~0u, sum > skip);
+          if (who != 0) {
+            const int src = __ffs(who) - 1;
+            seq = b0 + src;
+            in = skip - __shfl_sync(~0u, sum - have, src);
             break;
           }
-          skip -= n;
+          skip -= __shfl_sync(~0u, sum, 31);
         }
         int first, last;
         sequence_rows(p.cu, seq, p.seq_len, p.M, first, last);
         t.row0 = first;
         t.len = last - first;
-        t.tok0 = tier * tpc;
+        t.tok0 = (p.causal ? tier : in) * tpc;
         const int packs = p.group / p.hp;
         t.kvh = pair / packs;
         t.head0 = t.kvh * p.group + (pair - t.kvh * packs) * p.hp;
@@ -300,48 +388,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         // tokens [tok0, tok0 + tq) and [tok0 + tq, tok0 + 2 tq), cut off at the sequence's end
         t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
         t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
+        long_before = max(t.n0, t.n1) >= 4;
+      } else if (lane == 0 && atomicAdd(p.work + 1, 1u) == static_cast<unsigned>(G) - 1) {
+        p.work[0] = 0;  // every CTA has come to the end: ready for the next launch
+        p.work[1] = 0;
       }
       if (lane == 0) {
         bar.tile[k % kPreRing] = t;
         mbar_arrive(&bar.tile_full[k % kPreRing]);
       }
       __syncwarp();
-      return t.len > 0;
-    };
-    bool more = produce(0);
-    if (!FP8) {
-      for (int k = 1; more; ++k) more = produce(k);
-    } else {
-      int k = 0, sc = 0;
-      bool next = more && produce(1);
-      while (more) {
-        const PrefillTile t = bar.tile[k % kPreRing];
-        const int n = max(t.n0, t.n1);
-        bool ok = true;
-        for (int i = 0; i < n && ok; ++i, ++sc) {
-          float a[4], b[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int pos = i * kPreTile + c * 32 + lane;
-            a[c] = b[c] = 0.f;
-            if (pos < t.len) {
-              const long long at = static_cast<long long>(t.row0 + pos) * p.lds + t.kvh;
-              a[c] = __ldg(p.ks + at), b[c] = __ldg(p.vs + at);
-            }
-          }
-          ok = warp_wait(&bar.sc_empty[sc & 1], ((sc >> 1) & 1) ^ 1, wc, W_PRE_SCALE_EMPTY);
-          if (!ok) break;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            scales[(sc & 1) * 256 + c * 32 + lane] = a[c];
-            scales[(sc & 1) * 256 + 128 + c * 32 + lane] = b[c];
-          }
-          mbar_arrive(&bar.sc_full[sc & 1]);
-        }
-        ++k;
-        more = ok && next;
-        next = more && produce(k + 1);
-      }
     }
   } else if (warp == 9) {
     // ================================================================ TMA loads
@@ -459,10 +515,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     // stands one wait at most: the one for a P before its PV, the one for the next stage before the second QK.
     for (int k = 0; ok; ++k) {
       const int n = max(t.n0, t.n1), mask0 = first_masked(t);
-      const bool more = __all_sync(~0u, get_tile(k + 1, u));
-      if (more && one) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
+      bool more = false;
       for (int i = 0; i < n && ok; ++i) {
-        const bool last = i == n - 1, next = !last || more;  // another key tile, of this unit of work or the next
+        const bool last = i == n - 1;
+        if (last) {
+          more = __all_sync(~0u, get_tile(k + 1, u));
+          if (more && one) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
+        }
+        const bool next = !last || more;  // another key tile, of this unit of work or the next
         const int st = (uses - 1) & 1;
         if (i >= mask0) {
           ok = warp_wait(&bar.v_ok[st], (v_phase >> st) & 1, wc, W_PRE_V);
@@ -551,21 +611,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const int row_tok = row / p.hp, row_head = row - row_tok * p.hp;
     const bool row_used = row_tok < p.tq;
     const float c = p.scale_log2;
-    int s_uses = 0, o_uses = 0, sc = 0;
+    // E4M3 (see below): this thread's four rows, 8 apart, and its place in a run of scales
+    int tok4[4];
+    float* sets = scales + s * (4 * T::kScaleSet + kPreTile);
+    float* row_factor = sets + 4 * T::kScaleSet;
+    int sc_uses = 0;
+    if (FP8) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) tok4[r] = ((warp & 3) * 32 + (lane >> 2) + r * 8) / p.hp;
+    }
+    int s_uses = 0, o_uses = 0;
     bool ok = true;
     PrefillTile t;
     for (int k = 0; ok && __all_sync(~0u, get_tile(k, t)); ++k) {
-      const int ns = s ? t.n1 : t.n0, n = FP8 ? max(t.n0, t.n1) : ns, first = t.tok0 + s * p.tq;
+      const int n = s ? t.n1 : t.n0, first = t.tok0 + s * p.tq;
       const int tok = first + row_tok;
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int clear = p.causal ? first : t.len - 1;              // last key that every row sees
-      float m = kPreNone;
-      uint64_t l0 = 0, l1 = 0;
-      for (int i = 0; i < n; ++i) {
-        if (FP8) {
-          if (!(ok = warp_wait(&bar.sc_full[sc & 1], (sc >> 1) & 1, wc, W_PRE_SCALE_FULL))) break;
-        }
-        if (i < ns) {
+      float inv = 0.f;
+      if (!FP8) {
+        // ---- bf16: one thread a row
+        float m = kPreNone;
+        uint64_t l0 = 0, l1 = 0;
+        for (int i = 0; i < n; ++i) {
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
@@ -573,22 +641,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmem_ld32(s_tmem + j * 32, x[j]);
           tmem_ld_wait();
-          const float4* ks = reinterpret_cast<const float4*>(scales + (sc & 1) * 256);
-          if (FP8) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float4 f = ks[j];
-              uint32_t* y = &x[j >> 3][(j & 7) * 4];
-              float a, b;
-              f2_split(f2_mul(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), f2(f.x, f.y)), a, b);
-              y[0] = __float_as_uint(a), y[1] = __float_as_uint(b);
-              f2_split(f2_mul(f2(__uint_as_float(y[2]), __uint_as_float(y[3])), f2(f.z, f.w)), a, b);
-              y[2] = __float_as_uint(a), y[3] = __float_as_uint(b);
-            }
-          }
-          const bool masked = i * kPreTile + kPreTile - 1 > clear;
-          const int cols = lim - i * kPreTile;  // columns up to this one count
-          if (masked) {
+          if (i * kPreTile + kPreTile - 1 > clear) {
+            const int cols = lim - i * kPreTile;  // columns up to this one count
 #pragma unroll
             for (int j = 0; j < 128; ++j)
               if (j > cols) x[j >> 5][j & 31] = __float_as_uint(-INFINITY);
@@ -632,16 +686,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m2), d, e);
               a = ex2(a), b = ex2(b), d = ex2(d), e = ex2(e);
               l0 = f2_add(l0, f2(a, b)), l1 = f2_add(l1, f2(d, e));
-              if (FP8) {
-                const float4 f = ks[32 + j * 8 + (h >> 1)];
-                f2_split(f2_mul(f2(a, b), f2(f.x, f.y)), a, b);
-                f2_split(f2_mul(f2(d, e), f2(f.z, f.w)), d, e);
-                if (masked) {  // a scale behind the mask may be anything
-                  const int col = j * 32 + h * 2;
-                  a = col > cols ? 0.f : a, b = col + 1 > cols ? 0.f : b;
-                  d = col + 2 > cols ? 0.f : d, e = col + 3 > cols ? 0.f : e;
-                }
-              }
               w[h] = pack_bf16x2(a, b), w[h + 1] = pack_bf16x2(d, e);
             }
             tmem_st16(s_tmem + j * 16, w);
@@ -651,21 +695,167 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.p_full[s]);
         }
-        if (FP8) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.sc_empty[sc & 1]);
-          ++sc;
-        }
-      }
-      if (!ok) break;
-      if (ns > 0) {
-        if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
-        ++o_uses;
-        tc_fence_after();
         float a, b, d, e;
         f2_split(l0, a, b);
         f2_split(l1, d, e);
-        const float inv = 1.f / ((a + b) + (d + e));
+        inv = 1.f / ((a + b) + (d + e));
+      } else {
+        // ---- E4M3: each key has a scale, and a thread that held a whole row would read all 128 of them from
+        // shared memory twice (that alone took as long as the products).  In the 16x256b shape a lane holds
+        // columns 8 k + 2 (lane % 4) + {0, 1} of four rows (lane / 4 + 8 r): 32 scales serve four rows.
+        const int col = threadIdx.x & 127;  // the column whose scales this thread fetches
+        auto fetch = [&](int i, float& a, float& b) {
+          const int pos = i * kPreTile + col;
+          a = b = 0.f;
+          if (pos < t.len) {
+            const long long at = static_cast<long long>(t.row0 + pos) * p.lds + t.kvh;
+            a = __ldg(p.ks + at), b = __ldg(p.vs + at);
+          }
+        };
+        auto publish = [&](int i, float a, float b) {
+          float* to = sets + (i & 1) * 2 * T::kScaleSet + ((col >> 1) & 3) * T::kScaleRun + (col >> 3) * 2 + (col & 1);
+          to[0] = a;
+          to[T::kScaleSet] = b;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.sc_full[s]);
+          const bool done = warp_wait(&bar.sc_full[s], sc_uses & 1, wc, W_PRE_SCALE);
+          ++sc_uses;
+          return done;
+        };
+        float m[4], next_k = 0.f, next_v = 0.f;
+        uint64_t l[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = kPreNone, l[r] = 0;
+        if (n > 0) {
+          fetch(0, next_k, next_v);
+          ok = publish(0, next_k, next_v);
+        }
+        for (int i = 0; i < n && ok; ++i) {
+          if (i + 1 < n) fetch(i + 1, next_k, next_v);
+          if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
+          ++s_uses;
+          tc_fence_after();
+          uint32_t x[2][64];  // [rows r = 2 h, 2 h + 1][4 k + 2 (r & 1) + column]
+          tmem_ld_16x256b_x16(s_tmem, x[0]);
+          tmem_ld_16x256b_x16(s_tmem + (16u << 16), x[1]);
+          tmem_ld_wait();
+          const float4* kf = reinterpret_cast<const float4*>(sets + (i & 1) * 2 * T::kScaleSet + (lane & 3) * T::kScaleRun);
+          const float4* vf = kf + T::kScaleSet / 4;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 f = kf[j];
+            const uint64_t f0 = f2(f.x, f.y), f1 = f2(f.z, f.w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t* y = &x[h][j * 8 + q * 2];
+                float a, b;
+                f2_split(f2_mul(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), q < 2 ? f0 : f1), a, b);
+                y[0] = __float_as_uint(a), y[1] = __float_as_uint(b);
+              }
+          }
+          const bool masked = i * kPreTile + kPreTile - 1 > clear;
+          int cols[4];  // columns up to these count; counted from this lane's first
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            cols[r] = (p.causal ? min(first + tok4[r], t.len - 1) : t.len - 1) - i * kPreTile - 2 * (lane & 3);
+          if (masked) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if ((j >> 2) * 8 + (j & 1) > cols[h * 2 + ((j >> 1) & 1)]) x[h][j] = __float_as_uint(-INFINITY);
+          }
+          float top[4];
+          bool rise = false;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              mx = fmaxf(mx, fmaxf(__uint_as_float(x[r >> 1][j * 4 + (r & 1) * 2]),
+                                   __uint_as_float(x[r >> 1][j * 4 + (r & 1) * 2 + 1])));
+            top[r] = mx * c;
+            rise |= top[r] > m[r] + kPreLazy;
+          }
+          if (__any_sync(~0u, rise)) {
+            float down[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float a = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+              a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
+              const float up = a > m[r] + kPreLazy ? a : m[r];
+              down[r] = ex2(m[r] - up);
+              m[r] = up;
+              l[r] = f2_mul(l[r], f2(down[r], down[r]));
+            }
+            if (i > 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  uint32_t o[16];
+                  const uint32_t at = o_tmem + (static_cast<uint32_t>(h * 16) << 16) + j * 32;
+                  tmem_ld_16x256b_x4(at, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int q = 0; q < 16; ++q)
+                    o[q] = __float_as_uint(__uint_as_float(o[q]) * down[h * 2 + ((q >> 1) & 1)]);
+                  tmem_st_16x256b_x4(at, o);
+                }
+            }
+          }
+          const uint64_t c2 = f2(c, c);
+          uint32_t w[2][32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 f = vf[j];
+            const uint64_t f0 = f2(f.x, f.y), f1 = f2(f.z, f.w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {  // columns of k = 2 j + (q >> 1), row 2 h + (q & 1)
+                const int r = h * 2 + (q & 1);
+                float a, b;
+                f2_split(f2_fma(f2(__uint_as_float(x[h][j * 8 + q * 2]), __uint_as_float(x[h][j * 8 + q * 2 + 1])), c2,
+                                f2(-m[r], -m[r])), a, b);
+                a = ex2(a), b = ex2(b);
+                l[r] = f2_add(l[r], f2(a, b));
+                f2_split(f2_mul(f2(a, b), q < 2 ? f0 : f1), a, b);
+                if (masked) {  // a scale behind the mask may be anything
+                  const int at = (j * 2 + (q >> 1)) * 8;
+                  a = at > cols[r] ? 0.f : a, b = at + 1 > cols[r] ? 0.f : b;
+                }
+                w[h][j * 4 + q] = pack_bf16x2(a, b);
+              }
+          }
+          tmem_st_16x128b_x16(s_tmem, w[0]);
+          tmem_st_16x128b_x16(s_tmem + (16u << 16), w[1]);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full[s]);
+          if (i + 1 < n) ok = publish(i + 1, next_k, next_v);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float a, b;
+          f2_split(l[r], a, b);
+          a += b;
+          a += __shfl_xor_sync(~0u, a, 1);
+          a += __shfl_xor_sync(~0u, a, 2);
+          if ((lane & 3) == 0) row_factor[(warp & 3) * 32 + (lane >> 2) + r * 8] = 1.f / a;
+        }
+        __syncwarp();
+        inv = row_factor[row];
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
+        ++o_uses;
+        tc_fence_after();
         const bool there = row_used && tok < t.len;
         const bool spoiled = *reinterpret_cast<volatile int*>(&bar.tile[k % kPreRing].spoiled) != 0;
         const int from = first_masked(t) * kPreTile;
