@@ -136,25 +136,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Shapes of 16 lanes: x16 of 16x256b is 128 columns (a thread t has columns 8 k + 2 (t % 4) + {0, 1} of lanes t / 4 and
-// t / 4 + 8 in registers 4 k .. 4 k + 3), x16 of 16x128b 64 columns (column 4 k + t % 4 of the same lanes).
-__device__ __forceinline__ void tmem_ld_16x256b_x16(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
-      "%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,"
-      "%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
-      "}, [%64];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr));
-}
+// Shapes of 16 lanes: x4 of 16x256b is 32 columns (thread t has columns 8 k + 2 (t % 4) + {0, 1} of lanes t / 4 and
+// t / 4 + 8 in registers 4 k .. 4 k + 3), x4 of 16x128b 16 columns (column 4 k + t % 4 of the same lanes).
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
@@ -173,17 +156,10 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_16x128b_x16(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {"
-      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-      "%29,%30,%31,%32"
-      "};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -615,6 +591,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     int tok4[4];
     float* sets = scales + s * (4 * T::kScaleSet + kPreTile);
     float* row_factor = sets + 4 * T::kScaleSet;
+    const uint32_t sets_smem = smem_u32(sets) + (lane & 3) * (T::kScaleRun * 4);
     int sc_uses = 0;
     if (FP8) {
 #pragma unroll
@@ -735,103 +712,109 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
-          uint32_t x[2][64];  // [rows r = 2 h, 2 h + 1][4 k + 2 (r & 1) + column]
-          tmem_ld_16x256b_x16(s_tmem, x[0]);
-          tmem_ld_16x256b_x16(s_tmem + (16u << 16), x[1]);
-          tmem_ld_wait();
-          const float4* kf = reinterpret_cast<const float4*>(sets + (i & 1) * 2 * T::kScaleSet + (lane & 3) * T::kScaleRun);
-          const float4* vf = kf + T::kScaleSet / 4;
+          const uint32_t kf = sets_smem + (i & 1) * (2 * T::kScaleSet * 4), vf = kf + T::kScaleSet * 4;
+          const bool masked = i * kPreTile + kPreTile - 1 > clear;
+          const uint64_t c2 = f2(c, c);
+          // Two rows at a time: half the registers, and half the code in the instruction cache.
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t half = static_cast<uint32_t>(h * 16) << 16;
+            uint32_t x[4][16];  // [32 columns][4 k + 2 row + column]
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 f = kf[j];
-            const uint64_t f0 = f2(f.x, f.y), f1 = f2(f.z, f.w);
+            for (int j = 0; j < 4; ++j) tmem_ld_16x256b_x4(s_tmem + half + j * 32, x[j]);
+            tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int j = 0; j < 8; ++j) {
+              const uint4 f = ld_shared_v4(kf + j * 16);
+              const uint64_t f0 = f2(__uint_as_float(f.x), __uint_as_float(f.y)),
+                             f1 = f2(__uint_as_float(f.z), __uint_as_float(f.w));
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                uint32_t* y = &x[h][j * 8 + q * 2];
+                uint32_t* y = &x[j >> 1][(j & 1) * 8 + q * 2];
                 float a, b;
                 f2_split(f2_mul(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), q < 2 ? f0 : f1), a, b);
                 y[0] = __float_as_uint(a), y[1] = __float_as_uint(b);
               }
-          }
-          const bool masked = i * kPreTile + kPreTile - 1 > clear;
-          int cols[4];  // columns up to these count; counted from this lane's first
+            }
+            int cols[2];  // columns up to these count; counted from this lane's first
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            cols[r] = (p.causal ? min(first + tok4[r], t.len - 1) : t.len - 1) - i * kPreTile - 2 * (lane & 3);
-          if (masked) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int r = 0; r < 2; ++r)
+              cols[r] = (p.causal ? min(first + tok4[r], t.len - 1) : t.len - 1) - i * kPreTile - 2 * (lane & 3);
+            if (masked) {
 #pragma unroll
               for (int j = 0; j < 64; ++j)
-                if ((j >> 2) * 8 + (j & 1) > cols[h * 2 + ((j >> 1) & 1)]) x[h][j] = __float_as_uint(-INFINITY);
-          }
-          float top[4];
-          bool rise = false;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              mx = fmaxf(mx, fmaxf(__uint_as_float(x[r >> 1][j * 4 + (r & 1) * 2]),
-                                   __uint_as_float(x[r >> 1][j * 4 + (r & 1) * 2 + 1])));
-            top[r] = mx * c;
-            rise |= top[r] > m[r] + kPreLazy;
-          }
-          if (__any_sync(~0u, rise)) {
-            float down[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float a = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-              a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
-              const float up = a > m[r] + kPreLazy ? a : m[r];
-              down[r] = ex2(m[r] - up);
-              m[r] = up;
-              l[r] = f2_mul(l[r], f2(down[r], down[r]));
+                if ((j >> 2) * 8 + (j & 1) > cols[(j >> 1) & 1]) x[j >> 4][j & 15] = __float_as_uint(-INFINITY);
             }
-            if (i > 0) {
+            float top[2];
+            bool rise = false;
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+            for (int r = 0; r < 2; ++r) {
+              float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
+              for (int j = 0; j < 16; ++j)
+                mx[j & 1] = fmaxf(mx[j & 1], fmaxf(__uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2]),
+                                                   __uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2 + 1])));
+              top[r] = fmaxf(mx[0], mx[1]) * c;
+              rise |= top[r] > m[r] + kPreLazy;
+            }
+            if (__any_sync(~0u, rise)) {
+              float down[2];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                float a = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+                a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
+                const float up = a > m[r] + kPreLazy ? a : m[r];
+                down[r] = ex2(m[r] - up);
+                m[r] = up;
+                l[r] = f2_mul(l[r], f2(down[r], down[r]));
+              }
+              if (i > 0) {
+#pragma unroll 1
                 for (int j = 0; j < 4; ++j) {
                   uint32_t o[16];
-                  const uint32_t at = o_tmem + (static_cast<uint32_t>(h * 16) << 16) + j * 32;
-                  tmem_ld_16x256b_x4(at, o);
+                  tmem_ld_16x256b_x4(o_tmem + half + j * 32, o);
                   tmem_ld_wait();
 #pragma unroll
-                  for (int q = 0; q < 16; ++q)
-                    o[q] = __float_as_uint(__uint_as_float(o[q]) * down[h * 2 + ((q >> 1) & 1)]);
-                  tmem_st_16x256b_x4(at, o);
+                  for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * down[(q >> 1) & 1]);
+                  tmem_st_16x256b_x4(o_tmem + half + j * 32, o);
                 }
+              }
+            }
+            const uint64_t m2[2] = {f2(-m[0], -m[0]), f2(-m[1], -m[1])};
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+              uint32_t w[8];
+#pragma unroll
+              for (int j = jj * 2; j < jj * 2 + 2; ++j) {
+                const uint4 f = ld_shared_v4(vf + j * 16);
+                const uint64_t f0 = f2(__uint_as_float(f.x), __uint_as_float(f.y)),
+                               f1 = f2(__uint_as_float(f.z), __uint_as_float(f.w));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // columns of k = 2 j + (q >> 1), row q & 1
+                  const uint32_t* y = &x[jj][(j & 1) * 8 + q * 2];
+                  float a, b;
+                  f2_split(f2_fma(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, m2[q & 1]), a, b);
+                  a = ex2(a), b = ex2(b);
+                  l[q & 1] = f2_add(l[q & 1], f2(a, b));
+                  f2_split(f2_mul(f2(a, b), q < 2 ? f0 : f1), a, b);
+                  if (masked) {  // a scale behind the mask may be anything
+                    const int at = (j * 2 + (q >> 1)) * 8;
+                    a = at > cols[q & 1] ? 0.f : a, b = at + 1 > cols[q & 1] ? 0.f : b;
+                  }
+                  w[(j & 1) * 4 + q] = pack_bf16x2(a, b);
+                }
+              }
+              tmem_st_16x128b_x4(s_tmem + half + jj * 16, w);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {  // the other two rows' turn (and back)
+              const float m_r = m[r];
+              const uint64_t l_r = l[r];
+              const int tok_r = tok4[r];
+              m[r] = m[r + 2], l[r] = l[r + 2], tok4[r] = tok4[r + 2];
+              m[r + 2] = m_r, l[r + 2] = l_r, tok4[r + 2] = tok_r;
             }
           }
-          const uint64_t c2 = f2(c, c);
-          uint32_t w[2][32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 f = vf[j];
-            const uint64_t f0 = f2(f.x, f.y), f1 = f2(f.z, f.w);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {  // columns of k = 2 j + (q >> 1), row 2 h + (q & 1)
-                const int r = h * 2 + (q & 1);
-                float a, b;
-                f2_split(f2_fma(f2(__uint_as_float(x[h][j * 8 + q * 2]), __uint_as_float(x[h][j * 8 + q * 2 + 1])), c2,
-                                f2(-m[r], -m[r])), a, b);
-                a = ex2(a), b = ex2(b);
-                l[r] = f2_add(l[r], f2(a, b));
-                f2_split(f2_mul(f2(a, b), q < 2 ? f0 : f1), a, b);
-                if (masked) {  // a scale behind the mask may be anything
-                  const int at = (j * 2 + (q >> 1)) * 8;
-                  a = at > cols[r] ? 0.f : a, b = at + 1 > cols[r] ? 0.f : b;
-                }
-                w[h][j * 4 + q] = pack_bf16x2(a, b);
-              }
-          }
-          tmem_st_16x128b_x16(s_tmem, w[0]);
-          tmem_st_16x128b_x16(s_tmem + (16u << 16), w[1]);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
