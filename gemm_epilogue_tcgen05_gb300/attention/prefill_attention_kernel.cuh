@@ -87,7 +87,11 @@ struct PrefillTraits {
   // E4M3: for each query tile two buffers of K's and V's scales (four runs of 32 + 4), and a factor for each row
   static constexpr int kScaleRun = 36, kScaleSet = 4 * kScaleRun;
   static constexpr int kScales = FP8 ? 2 * (4 * kScaleSet + kPreTile) * 4 : 0;
-  static constexpr int kSmem = (2 + 2 * kStages) * kPreTileBytes + kScales + kBars + 1024 /*alignment*/;
+  // output on its way from a row per thread to whole lines: 32 rows of kOutCols columns for each softmax warp
+  static constexpr int kOutCols = FP8 ? 32 : 64;
+  static constexpr int kOut = 8 * 32 * kOutCols * 2;
+  static constexpr int kSmem = (2 + 2 * kStages) * kPreTileBytes + kOut + kScales + kBars + 1024 /*alignment*/;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
 // One unit of work.
@@ -234,8 +238,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * kPreTileBytes;
-  float* scales = reinterpret_cast<float*>(smem + (2 + 2 * T::kStages) * kPreTileBytes);  // [2][K | V][128]
-  PrefillBars& bar = *reinterpret_cast<PrefillBars*>(smem + (2 + 2 * T::kStages) * kPreTileBytes + T::kScales);
+  constexpr int kOutAt = (2 + 2 * T::kStages) * kPreTileBytes;
+  float* scales = reinterpret_cast<float*>(smem + kOutAt + T::kOut);
+  PrefillBars& bar = *reinterpret_cast<PrefillBars*>(smem + kOutAt + T::kOut + T::kScales);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = gridDim.x, cta = blockIdx.x;
 
@@ -584,8 +589,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const int s = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tmem = tmem + lanes + s * kPreTile, o_tmem = tmem + lanes + 256 + s * kHeadDim;
-    const int row_tok = row / p.hp, row_head = row - row_tok * p.hp;
-    const bool row_used = row_tok < p.tq;
+    const uint32_t hp_inverse = 65536u / p.hp + 1;  // row / hp = row * hp_inverse >> 16 for rows below 128
+    const int row_tok = row / p.hp;
     const float c = p.scale_log2;
     // E4M3 (see below): this thread's four rows, 8 apart, and its place in a run of scales
     int tok4[4];
@@ -839,37 +844,53 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
         tc_fence_after();
-        const bool there = row_used && tok < t.len;
         const bool spoiled = *reinterpret_cast<volatile int*>(&bar.tile[k % kPreRing].spoiled) != 0;
         const int from = first_masked(t) * kPreTile;
-        __nv_bfloat16* dst = p.O + static_cast<long long>(t.row0 + tok) * p.ldo +
-                             static_cast<long long>(t.head0 + row_head) * kHeadDim;
+        // A thread has a row; lines of global memory want a few rows each, all of 128 bytes.  So 16-byte pieces go
+        // through shared memory, piece j of row r at place j ^ (r's low bits).  (Stored straight from the row's
+        // thread, each instruction touched 32 lines: 4000 cycles a tile.)
+        constexpr int kPieces = T::kOutCols / 8, kRowsPer = 32 / kPieces, kSwizzle = kPieces - 1;
+        const uint32_t out = smem_u32(smem) + kOutAt + warp * (32 * T::kOutCols * 2);
+        const int piece = lane % kPieces;
+        __nv_bfloat16* dst = p.O + static_cast<long long>(t.row0) * p.ldo + static_cast<long long>(t.head0) * kHeadDim +
+                             piece * 8;
+#pragma unroll 1
+        for (int j = 0; j < kHeadDim; j += T::kOutCols) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t o[32];
-          tmem_ld32(o_tmem + j * 32, o);
-          tmem_ld_wait();
-          if (!there) continue;
-          if (spoiled) {  // values that were taken out for the rows that do not see them
-            for (int pos = from; pos <= lim; ++pos) {
-              const __nv_bfloat16* v = p.V + static_cast<long long>(t.row0 + pos) * p.ldv +
-                                       static_cast<long long>(t.kvh) * kHeadDim + j * 32;
+          for (int h = 0; h < T::kOutCols; h += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_tmem + j + h, o);
+            tmem_ld_wait();
+            if (spoiled) {  // values that were taken out for the rows that do not see them
+              for (int pos = from; pos <= lim; ++pos) {
+                const __nv_bfloat16* v = p.V + static_cast<long long>(t.row0 + pos) * p.ldv +
+                                         static_cast<long long>(t.kvh) * kHeadDim + j + h;
 #pragma unroll
-              for (int h = 0; h < 32; ++h) {
-                const float y = __bfloat162float(v[h]);
-                if (!isfinite(y)) o[h] = __float_as_uint(__uint_as_float(o[h]) + y);
+                for (int q = 0; q < 32; ++q) {
+                  const float y = __bfloat162float(v[q]);
+                  if (!isfinite(y)) o[q] = __float_as_uint(__uint_as_float(o[q]) + y);
+                }
               }
             }
-          }
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(o[h * 8]) * inv, __uint_as_float(o[h * 8 + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(o[h * 8 + 2]) * inv, __uint_as_float(o[h * 8 + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(o[h * 8 + 4]) * inv, __uint_as_float(o[h * 8 + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(o[h * 8 + 6]) * inv, __uint_as_float(o[h * 8 + 7]) * inv);
-            *reinterpret_cast<uint4*>(dst + j * 32 + h * 8) = w;
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(o[q * 8 + e * 2]) * inv, __uint_as_float(o[q * 8 + e * 2 + 1]) * inv);
+              st_shared_v4(out + lane * (T::kOutCols * 2) + (((h >> 3) + q) ^ (lane & kSwizzle)) * 16, w[0], w[1], w[2], w[3]);
+            }
           }
+          __syncwarp();
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += kRowsPer) {
+            const int r = r0 + lane / kPieces, at = (warp & 3) * 32 + r;
+            const int at_tok = static_cast<int>((at * hp_inverse) >> 16), at_head = at - at_tok * p.hp;
+            const uint4 w = ld_shared_v4(out + r * (T::kOutCols * 2) + (piece ^ (r & kSwizzle)) * 16);
+            if (at_tok < p.tq && first + at_tok < t.len)
+              *reinterpret_cast<uint4*>(dst + static_cast<long long>(first + at_tok) * p.ldo + at_head * kHeadDim + j) = w;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       }
