@@ -123,6 +123,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   const long long blocks = cu_seqlens == nullptr
                                ? (M / seq_len) * ((seq_len - 1) / per_cta + 1) + (M % seq_len + per_cta - 1) / per_cta
                                : M / per_cta + batch;  // an upper bound: the lengths are on the device
+  if (blocks * p.pairs > (1ll << 30)) return FL_ERR_UNSUPPORTED;
   const int kv_w = static_cast<int>(kv_width);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const void* k16 = K;

@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const int mine = lane < p.batch ? length_of(lane) : 0;
     auto over_sequences = [&](auto&& f, bool take_max) -> int {
       int n = f(mine);
+#pragma unroll 1
       for (int b = lane + 32; b < p.batch; b += 32) {
         const int x = f(length_of(b));
         n = take_max ? max(n, x) : n + x;
@@ -308,10 +309,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       return take_max ? __reduce_max_sync(~0u, n) : __reduce_add_sync(~0u, n);
     };
     const int tiers = over_sequences(tiers_of, true);
-    const long long blocks = over_sequences([&](int len) { return len > 0 ? (len - 1) / tpc + 1 : 0; }, false);
-    int tier = tiers, above = 0, upto = 0;  // blocks of higher tiers, and with this tier's
+    const unsigned blocks = over_sequences([&](int len) { return len > 0 ? (len - 1) / tpc + 1 : 0; }, false);
+    int tier = tiers;
+    unsigned above = 0, upto = 0;                            // blocks of higher tiers, and with this tier's
     int pair0 = 0, n_pairs = min(p.pairs, p.pairs_at_once);  // the group of heads
-    long long rank0 = 0;                                     // its first rank
+    unsigned rank0 = 0;                                      // its first rank (the launch keeps ranks below 2^30)
     bool more = true, long_before = false;
     for (int k = 0; more; ++k) {
       if (!warp_wait(&bar.tile_empty[k % kPreRing], ((k / kPreRing) & 1) ^ 1, wc, W_PRE_TILE_EMPTY)) break;
@@ -321,15 +323,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         break;
       unsigned taken = 0;
       if (k > 0 && lane == 0) taken = atomicAdd(p.work, 1u);
-      const long long rank = k == 0 ? cta : static_cast<long long>(G) + __shfl_sync(~0u, taken, 0);
+      const unsigned rank = k == 0 ? cta : G + __shfl_sync(~0u, taken, 0);
       while (rank >= rank0 + blocks * n_pairs && pair0 + n_pairs < p.pairs) {  // on to the next group
         rank0 += blocks * n_pairs;
         pair0 += n_pairs;
         n_pairs = min(p.pairs - pair0, p.pairs_at_once);
         tier = tiers, above = 0, upto = 0;
       }
-      const long long block = (rank - rank0) / n_pairs;
-      const int pair = pair0 + static_cast<int>((rank - rank0) % n_pairs);
+      const unsigned block = (rank - rank0) / n_pairs;
+      const int pair = pair0 + static_cast<int>(rank - rank0 - block * n_pairs);
       while (tier > 0 && upto <= block) {
         above = upto;
         --tier;
@@ -339,6 +341,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       more = upto > block;
       if (more) {  // the sequence that holds the (block - above)-th block of this tier
         int skip = static_cast<int>(block - above), seq = 0, in = 0;
+#pragma unroll 1
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
           const int len = b0 == 0 ? mine : b0 + lane < p.batch ? length_of(b0 + lane) : 0;
           const int have = blocks_in(len, tier);
@@ -444,15 +447,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
                    v_desc = sdesc_mn_sw128(kv_smem, kPreTileBytes / 2);
     uint32_t q_phase = 0, p_phase = 0, v_phase = 0;  // a bit for each barrier
     uint32_t uses = 0;                               // stages waited for: the next one is (uses & 1)
+    // Lanes wait on their own and agree once a step: after a wait that gave up, what is still issued works on the
+    // CTA's own memory and its results are not used.
+    bool ok = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, int where) { ok = pre_wait(b, parity, wc, where) && ok; };
     auto stage_wait = [&]() {
-      const bool ok = warp_wait(&bar.kv_full[uses & 1], (uses >> 1) & 1, wc, W_PRE_KV_FULL);
+      wait(&bar.kv_full[uses & 1], (uses >> 1) & 1, W_PRE_KV_FULL);
       ++uses;
-      return ok;
     };
     auto q_wait = [&](int s) {
-      const bool ok = warp_wait(&bar.q_full[s], (q_phase >> s) & 1, wc, W_PRE_Q_FULL);
+      wait(&bar.q_full[s], (q_phase >> s) & 1, W_PRE_Q_FULL);
       q_phase ^= 1u << s;
-      return ok;
+    };
+    auto p_wait = [&](int s) {
+      wait(&bar.p_full[s], (p_phase >> s) & 1, W_PRE_P);
+      p_phase ^= 1u << s;
+      tc_fence_after();
     };
     auto qk = [&](int s, int st, bool last) {  // S_s = Q_s K^T
       if (one) {
@@ -477,27 +487,43 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       __syncwarp();
     };
     PrefillTile t, u = {};
-    bool ok = __all_sync(~0u, get_tile(0, t));
-    if (ok) {
+    bool more = __all_sync(~0u, get_tile(0, t));
+    if (more) {
       if (one) mbar_arrive(&bar.tile_empty[0]);
-      ok = stage_wait();
+      stage_wait();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int ns = s ? t.n1 : t.n0;
-        if (ok && ns > 0) {
-          ok = q_wait(s);
-          if (ok) qk(s, 0, ns == 1);
+        if (ns > 0) {
+          q_wait(s);
+          qk(s, 0, ns == 1);
         }
       }
-      if (ok && one) mma_commit(&bar.kv_empty[0]);
-      ok = ok && stage_wait();
+      if (one) mma_commit(&bar.kv_empty[0]);
+      stage_wait();
     }
     // The queue behind the tensor cores holds about three instructions (some 190 cycles), so between two products
     // stands one wait at most: the one for a P before its PV, the one for the next stage before the second QK.
-    for (int k = 0; ok; ++k) {
+    for (int k = 0; more && (ok = __all_sync(~0u, ok)); ++k) {
       const int n = max(t.n0, t.n1), mask0 = first_masked(t);
-      bool more = false;
-      for (int i = 0; i < n && ok; ++i) {
+      const int plain = min(min(t.n0, t.n1) - 1, mask0);  // steps without a mask that both query tiles go on behind
+      int i = 0;
+#pragma unroll 1
+      for (; i < plain; ++i) {
+        const int st = (uses - 1) & 1;
+        p_wait(0);
+        pv(0, st, i == 0, false);
+        qk(0, st, i + 2 == t.n0);
+        p_wait(1);
+        pv(1, st, i == 0, false);
+        stage_wait();
+        qk(1, st, i + 2 == t.n1);
+        if (one) mma_commit(&bar.kv_empty[st]);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+      }
+#pragma unroll 1
+      for (; i < n && ok; ++i) {
         const bool last = i == n - 1;
         if (last) {
           more = __all_sync(~0u, get_tile(k + 1, u));
@@ -506,27 +532,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         const bool next = !last || more;  // another key tile, of this unit of work or the next
         const int st = (uses - 1) & 1;
         if (i >= mask0) {
-          ok = warp_wait(&bar.v_ok[st], (v_phase >> st) & 1, wc, W_PRE_V);
+          wait(&bar.v_ok[st], (v_phase >> st) & 1, W_PRE_V);
           v_phase ^= 1u << st;
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int ns = s ? t.n1 : t.n0, un = s ? u.n1 : u.n0;
-          if (ok && i < ns) {
-            ok = warp_wait(&bar.p_full[s], (p_phase >> s) & 1, wc, W_PRE_P);
-            p_phase ^= 1u << s;
-            tc_fence_after();
-            if (ok) pv(s, st, i == 0, i == ns - 1);
+          if (i < ns) {
+            p_wait(s);
+            pv(s, st, i == 0, i == ns - 1);
           }
-          if (s == 1 && next && ok) ok = stage_wait();
-          if (ok && (last ? more && un > 0 : i + 1 < ns)) {
-            if (last) ok = q_wait(s);
-            if (ok) qk(s, st, last ? un == 1 : i + 1 == ns - 1);
+          if (s == 1 && next) stage_wait();
+          if (last ? more && un > 0 : i + 1 < ns) {
+            if (last) q_wait(s);
+            qk(s, st, last ? un == 1 : i + 1 == ns - 1);
           }
         }
-        if (ok && one) mma_commit(&bar.kv_empty[st]);
+        if (one) mma_commit(&bar.kv_empty[st]);
+        ok = __all_sync(~0u, ok);
       }
-      if (!more) break;
       t = u;
     }
     if (one) {
@@ -570,6 +594,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             const uint32_t bad = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
             return w & ~((bad >> 15) * 0xFFFFu);
           };
+#pragma unroll 1
           for (int c = 0; c < kPreTileBytes / 512; ++c) {
             const uint4 w = ld_shared_v4(base + c * 512);
             st_shared_v4(base + c * 512, clean(w.x), clean(w.y), clean(w.z), clean(w.w));
@@ -861,17 +886,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             uint32_t o[32];
             tmem_ld32(o_tmem + j + h, o);
             tmem_ld_wait();
-            if (spoiled) {  // values that were taken out for the rows that do not see them
-              for (int pos = from; pos <= lim; ++pos) {
-                const __nv_bfloat16* v = p.V + static_cast<long long>(t.row0 + pos) * p.ldv +
-                                         static_cast<long long>(t.kvh) * kHeadDim + j + h;
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                  const float y = __bfloat162float(v[q]);
-                  if (!isfinite(y)) o[q] = __float_as_uint(__uint_as_float(o[q]) + y);
-                }
-              }
-            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t w[4];
@@ -893,6 +907,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           __syncwarp();
         }
         tc_fence_before();
+        if (spoiled && row_tok < p.tq && tok < t.len) {
+          // Values of V that are not finite were taken out for the rows that do not see them.  The others get their
+          // sum (infinite or NaN), whatever the finite rest is.
+          const __nv_bfloat16* v = p.V + static_cast<long long>(t.row0) * p.ldv + static_cast<long long>(t.kvh) * kHeadDim;
+          __nv_bfloat16* mine = p.O + static_cast<long long>(t.row0 + tok) * p.ldo +
+                                static_cast<long long>(t.head0 + row - row_tok * p.hp) * kHeadDim;
+#pragma unroll 1
+          for (int d = 0; d < kHeadDim; ++d) {
+            float sum = 0.f;
+#pragma unroll 1
+            for (int pos = from; pos <= lim; ++pos) {
+              const float y = __bfloat162float(v[static_cast<long long>(pos) * p.ldv + d]);
+              if (!isfinite(y)) sum += y;
+            }
+            if (!isfinite(sum)) mine[d] = __float2bfloat16_rn(sum);
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.tile_empty[k % kPreRing]);
