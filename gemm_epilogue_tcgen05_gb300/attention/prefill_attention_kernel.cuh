@@ -207,6 +207,11 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
   return one != 0;
 }
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 // Two fp32 lanes in one 64-bit register.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -580,15 +585,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           continue;
         }
         const uint32_t base = kv_smem + st * 2 * kPreTileBytes + lane * 16;
-        uint32_t seen = 0;
+        uint32_t seen[4] = {0, 0, 0, 0};  // sums of 0 * v: NaN once a v is not finite
 #pragma unroll 8
         for (int c = 0; c < kPreTileBytes / 512; ++c) {
           const uint4 w = ld_shared_v4(base + c * 512);
-          // an exponent of all ones carries into the sign's place
-          seen |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                  ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+          seen[0] = bf16x2_fma(w.x, 0, seen[0]), seen[1] = bf16x2_fma(w.y, 0, seen[1]);
+          seen[2] = bf16x2_fma(w.z, 0, seen[2]), seen[3] = bf16x2_fma(w.w, 0, seen[3]);
         }
-        if (__any_sync(~0u, (seen & 0x80008000u) != 0)) {
+        if (__any_sync(~0u, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7FFF7FFFu) != 0)) {
           if (lane == 0) bar.tile[k % kPreRing].spoiled = 1;
           auto clean = [](uint32_t w) {
             const uint32_t bad = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
