@@ -207,6 +207,11 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
   return one != 0;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           for (int j = 1; j < 31; j += 2)
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-              mx[h] = fmaxf(mx[h], fmaxf(__uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1])));
+              mx[h] = max3(mx[h], __uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1]));
 #pragma unroll
           for (int h = 0; h < 4; ++h) mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
@@ -724,6 +729,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           }
         };
         auto publish = [&](int i, float a, float b) {
+          // Where rows mask keys their weight is zero, and a scale of V that is not finite must not meet it: such a
+          // key counts as one whose values are not finite (see the end of the tile).
+          if (!isfinite(b) && i >= first_masked(t)) {
+            b = 0.f;
+            *reinterpret_cast<volatile int*>(&bar.tile[k % kPreRing].spoiled) = 1;
+          }
           float* to = sets + (i & 1) * 2 * T::kScaleSet + ((col >> 1) & 3) * T::kScaleRun + (col >> 3) * 2 + (col & 1);
           to[0] = a;
           to[T::kScaleSet] = b;
@@ -786,8 +797,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                mx[j & 1] = fmaxf(mx[j & 1], fmaxf(__uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2]),
-                                                   __uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2 + 1])));
+                mx[j & 1] = max3(mx[j & 1], __uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2]),
+                                 __uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2 + 1]));
               top[r] = fmaxf(mx[0], mx[1]) * c;
               rise |= top[r] > m[r] + kPreLazy;
             }
@@ -831,10 +842,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
                   a = ex2(a), b = ex2(b);
                   l[q & 1] = f2_add(l[q & 1], f2(a, b));
                   f2_split(f2_mul(f2(a, b), q < 2 ? f0 : f1), a, b);
-                  if (masked) {  // a scale behind the mask may be anything
-                    const int at = (j * 2 + (q >> 1)) * 8;
-                    a = at > cols[q & 1] ? 0.f : a, b = at + 1 > cols[q & 1] ? 0.f : b;
-                  }
                   w[(j & 1) * 4 + q] = pack_bf16x2(a, b);
                 }
               }
@@ -881,8 +888,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         constexpr int kPieces = T::kOutCols / 8, kRowsPer = 32 / kPieces, kSwizzle = kPieces - 1;
         const uint32_t out = smem_u32(smem) + kOutAt + warp * (32 * T::kOutCols * 2);
         const int piece = lane % kPieces;
-        __nv_bfloat16* dst = p.O + static_cast<long long>(t.row0) * p.ldo + static_cast<long long>(t.head0) * kHeadDim +
-                             piece * 8;
+        // rows lane / kPieces, + kRowsPer, ... of the warp's: their token and head step by step
+        const int r_first = lane / kPieces, at_first = (warp & 3) * 32 + r_first;
+        const int tok_first = static_cast<int>((at_first * hp_inverse) >> 16), head_first = at_first - tok_first * p.hp;
+        const int d_tok = kRowsPer / p.hp, d_head = kRowsPer - d_tok * p.hp;
+        const long long d_off = d_tok * p.ldo + d_head * kHeadDim, d_wrap = p.ldo - static_cast<long long>(p.hp) * kHeadDim;
+        const int toks = min(p.tq, t.len - first);
+        __nv_bfloat16* dst = p.O + static_cast<long long>(t.row0 + first + tok_first) * p.ldo +
+                             static_cast<long long>(t.head0 + head_first) * kHeadDim + piece * 8;
 #pragma unroll 1
         for (int j = 0; j < kHeadDim; j += T::kOutCols) {
 #pragma unroll
@@ -900,13 +913,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             }
           }
           __syncwarp();
+          __nv_bfloat16* to = dst + j;
+          int at_tok = tok_first, at_head = head_first;
 #pragma unroll
           for (int r0 = 0; r0 < 32; r0 += kRowsPer) {
-            const int r = r0 + lane / kPieces, at = (warp & 3) * 32 + r;
-            const int at_tok = static_cast<int>((at * hp_inverse) >> 16), at_head = at - at_tok * p.hp;
+            const int r = r_first + r0;
             const uint4 w = ld_shared_v4(out + r * (T::kOutCols * 2) + (piece ^ (r & kSwizzle)) * 16);
-            if (at_tok < p.tq && first + at_tok < t.len)
-              *reinterpret_cast<uint4*>(dst + static_cast<long long>(first + at_tok) * p.ldo + at_head * kHeadDim + j) = w;
+            if (at_tok < toks) *reinterpret_cast<uint4*>(to) = w;
+            at_tok += d_tok, at_head += d_head, to += d_off;
+            if (at_head >= p.hp) at_head -= p.hp, ++at_tok, to += d_wrap;
           }
           __syncwarp();
         }
@@ -922,7 +937,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             float sum = 0.f;
 #pragma unroll 1
             for (int pos = from; pos <= lim; ++pos) {
-              const float y = __bfloat162float(v[static_cast<long long>(pos) * p.ldv + d]);
+              float y = __bfloat162float(v[static_cast<long long>(pos) * p.ldv + d]);
+              if (FP8) y *= p.vs[static_cast<long long>(t.row0 + pos) * p.lds + t.kvh];
               if (!isfinite(y)) sum += y;
             }
             if (!isfinite(sum)) mine[d] = __float2bfloat16_rn(sum);

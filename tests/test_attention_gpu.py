@@ -111,6 +111,22 @@ def test_prefill_masked_values_of_the_own_sequence(which, bad, fp8):
         assert seen.isnan().all()
 
 
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("at", [5, 127, 128, 210, 299])
+def test_prefill_masked_scales_of_the_own_sequence(which, bad, at):
+    """The same for a scale that is not finite: rows before it do not meet it, rows behind a NaN one do."""
+    n = 300
+    q, k, v, ks, vs = prompt(n, 4, 1, True, seed=9)
+    (ks if which == "k" else vs)[at] = bad
+    out = fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs)
+    check_prefill(q[:at], k[:at], v[:at], ks[:at], vs[:at], [at], out[:at], True)
+    if bad != bad:
+        assert out[at:].isnan().all()
+    elif which == "v":  # an infinite scale of K gives logits of both signs: weight 0 or NaN
+        assert not out[at:].isfinite().all(-1).any()
+
+
 def test_prefill_peaked_and_flat_rows():
     """Logits of many hundreds (the running maximum jumps late) and of one value."""
     for std, seed in ((60.0, 10), (0.0, 11)):
