@@ -116,6 +116,11 @@ struct PrefillBars {
 };
 static_assert(sizeof(PrefillBars) <= 1024, "barrier block");
 
+struct PreWait {
+  int* abort_flag;      // shared memory: where the first wait gave up, 0 while none has
+  uint32_t timeout_ns;  // at most 2^32 - 1: 4 seconds
+};
+
 // D[tmem] (+)= A[tmem] * B: A bf16 pairs packed along K in tensor memory.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -181,25 +186,24 @@ __device__ __forceinline__ void tma_load_3d(const void* map, uint64_t* bar, uint
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// A bounded wait that reads the clock only now and then: reading it takes longer than most of these waits.
-__device__ __forceinline__ bool pre_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*w.abort_flag) return false;
-      const uint64_t now = global_timer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > w.timeout_ns) {
-        *w.abort_flag = 1;
-        record_failure(w.status, where, static_cast<int>(parity));
-        return false;
-      }
-    }
+// A bounded wait that looks at the clock only now and then (reading it takes longer than most of these waits).  One
+// that gives up leaves its place in the abort flag, which is recorded at the end: there are many waits, and
+// instructions come from a cache that this kernel overflows.
+__device__ __forceinline__ bool pre_wait(uint64_t* bar, uint32_t parity, const PreWait& w, int where) {
+  uint32_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255u) != 255u) continue;
+    uint32_t now;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+    t0 = i < 256u ? now : t0;
+    if (now - t0 > w.timeout_ns) atomicCAS(w.abort_flag, 0, where);
+    if (*const_cast<volatile int*>(w.abort_flag) != 0) return false;
   }
+  return true;
 }
 // A wait of all lanes of a warp: they go on, or give up, together.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int where) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const PreWait& w, int where) {
   return __all_sync(~0u, pre_wait(bar, parity, w, where));
 }
 __device__ __forceinline__ bool elect_one() {
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bar.tmem);
-  const WaitCtx wc{&bar.abort_flag, p.status, p.timeout_ns};
+  const PreWait wc{&bar.abort_flag, static_cast<uint32_t>(min(p.timeout_ns, 0xFFFFFFFFull))};
 
   // The tile that descriptor k (counted per CTA) describes; false when there is none or a wait gave up.
   auto get_tile = [&](int k, PrefillTile& t) -> bool {
@@ -303,25 +307,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       sequence_rows(p.cu, b, p.seq_len, p.M, first, last);
       return last - first;
     };
-    auto tiers_of = [&](int len) { return len > 0 ? (len - 1) / (p.causal ? tpc : kPreTile) + 1 : 0; };
-    auto blocks_in = [&](int len, int tier) {  // a sequence's blocks in a tier
-      if (p.causal) return tiers_of(len) > tier ? 1 : 0;
-      return tiers_of(len) == tier + 1 ? (len - 1) / tpc + 1 : 0;
-    };
-    const int mine = lane < p.batch ? length_of(lane) : 0;
-    auto over_sequences = [&](auto&& f, bool take_max) -> int {
-      int n = f(mine);
+    const int tier_len = p.causal ? tpc : kPreTile;
+    auto tiers_of = [&](int len) { return len > 0 ? (len - 1) / tier_len + 1 : 0; };
+    int mine = 0, tiers = 0;
+    unsigned blocks = 0;
 #pragma unroll 1
-      for (int b = lane + 32; b < p.batch; b += 32) {
-        const int x = f(length_of(b));
-        n = take_max ? max(n, x) : n + x;
-      }
-      return take_max ? __reduce_max_sync(~0u, n) : __reduce_add_sync(~0u, n);
-    };
-    const int tiers = over_sequences(tiers_of, true);
-    const unsigned blocks = over_sequences([&](int len) { return len > 0 ? (len - 1) / tpc + 1 : 0; }, false);
-    int tier = tiers;
-    unsigned above = 0, upto = 0;                            // blocks of higher tiers, and with this tier's
+    for (int b = lane; b < p.batch; b += 32) {
+      const int len = length_of(b);
+      if (b == lane) mine = len;
+      tiers = max(tiers, tiers_of(len));
+      blocks += len > 0 ? (len - 1) / tpc + 1 : 0;
+    }
+    tiers = __reduce_max_sync(~0u, tiers);
+    blocks = __reduce_add_sync(~0u, blocks);
+    int tier = tiers - 1;
+    unsigned above = 0;                                      // blocks of higher tiers
     int pair0 = 0, n_pairs = min(p.pairs, p.pairs_at_once);  // the group of heads
     unsigned rank0 = 0;                                      // its first rank (the launch keeps ranks below 2^30)
     bool more = true, long_before = false;
@@ -338,38 +338,41 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         rank0 += blocks * n_pairs;
         pair0 += n_pairs;
         n_pairs = min(p.pairs - pair0, p.pairs_at_once);
-        tier = tiers, above = 0, upto = 0;
+        tier = tiers - 1, above = 0;
       }
       const unsigned block = (rank - rank0) / n_pairs;
       const int pair = pair0 + static_cast<int>(rank - rank0 - block * n_pairs);
-      while (tier > 0 && upto <= block) {
-        above = upto;
-        --tier;
-        upto += over_sequences([&](int len) { return blocks_in(len, tier); }, false);
-      }
-      PrefillTile t = {};
-      more = upto > block;
-      if (more) {  // the sequence that holds the (block - above)-th block of this tier
-        int skip = static_cast<int>(block - above), seq = 0, in = 0;
+      // the tier, and in it the sequence, that holds this block: `in` of it
+      int seq = -1, in = 0;
 #pragma unroll 1
-        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      while (tier >= 0) {
+        unsigned upto = above;
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.batch && seq < 0; b0 += 32) {
           const int len = b0 == 0 ? mine : b0 + lane < p.batch ? length_of(b0 + lane) : 0;
-          const int have = blocks_in(len, tier);
-          int sum = have;  // inclusive sum over the lanes
+          const int reach = tiers_of(len);
+          const unsigned have = p.causal ? reach > tier : reach == tier + 1 ? (len - 1) / tpc + 1 : 0;
+          unsigned sum = have;  // inclusive sum over the lanes
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(~0u, sum, o);
+            const unsigned y = __shfl_up_sync(~0u, sum, o);
             if (lane >= o) sum += y;
           }
-          const unsigned who = __ballot_sync(~0u, sum > skip);
+          const unsigned who = __ballot_sync(~0u, upto + sum > block);
           if (who != 0) {
             const int src = __ffs(who) - 1;
             seq = b0 + src;
-            in = skip - __shfl_sync(~0u, sum - have, src);
-            break;
+            in = static_cast<int>(block - upto - __shfl_sync(~0u, sum - have, src));
           }
-          skip -= __shfl_sync(~0u, sum, 31);
+          upto += __shfl_sync(~0u, sum, 31);
         }
+        if (seq >= 0) break;
+        above = upto;
+        --tier;
+      }
+      PrefillTile t = {};
+      more = seq >= 0;
+      if (more) {
         int first, last;
         sequence_rows(p.cu, seq, p.seq_len, p.M, first, last);
         t.row0 = first;
@@ -396,52 +399,53 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   } else if (warp == 9) {
     // ================================================================ TMA loads
     if (lane == 0) {
-      int fills = 0, q_uses[2] = {0, 0};
-      bool ok = true;
-      PrefillTile t, u;
-      auto load_q = [&](const PrefillTile& t) {
-        for (int s = 0; s < 2 && ok; ++s) {
-          if ((s ? t.n1 : t.n0) == 0) continue;
-          ok = pre_wait(&bar.q_empty[s], (q_uses[s] & 1) ^ 1, wc, W_PRE_Q_EMPTY);
-          if (!ok) return;
-          ++q_uses[s];
-          mbar_arrive_expect_tx(&bar.q_full[s], static_cast<uint32_t>(p.hp * p.tq * kHeadDim * 2));
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d(&p.map_q, &bar.q_full[s], q_smem + s * kPreTileBytes + h * (kPreTileBytes / 2), h * 64, t.head0,
-                        t.row0 + t.tok0 + s * p.tq);
-        }
-      };
-      // one stage: key tile vi of a unit's V, and key tile ki of the same or the next unit's K (either may be absent)
-      auto load_kv = [&](const PrefillTile* v, int vi, const PrefillTile* k, int ki) {
+      int fills = 0;
+      PrefillTile t = {}, next = {};
+      uint32_t q_phase = 0;  // a bit for each query tile
+      bool q_used[2] = {false, false}, ok = true, more = get_tile(0, next);
+      // Stage after stage: key tile i of the current unit's V (none before the first unit), and the K tile behind it,
+      // of the same unit or, at its end, the first of the next one, whose queries follow.
+#pragma unroll 1
+      for (int k = -1, i = 0, n = 1; ok; ++i) {
+        const bool last = i == n - 1;
+        if (k >= 0 && last) more = get_tile(k + 1, next);
+        const bool has_v = k >= 0, has_k = !last || more;
+        if (!has_v && !has_k) break;
         const int st = fills & 1;
-        if (!ok || !(ok = pre_wait(&bar.kv_empty[st], ((fills >> 1) & 1) ^ 1, wc, W_PRE_KV_EMPTY))) return;
-        mbar_arrive_expect_tx(&bar.kv_full[st], ((v != nullptr) + (k != nullptr)) * kPreTileBytes);
-        uint8_t* dst = smem + (2 + 2 * st) * kPreTileBytes;
-        for (int h = 0; h < 2 && v != nullptr; ++h)
-          tma_load_2d(&p.map_v, &bar.kv_full[st], dst + h * (kPreTileBytes / 2), v->kvh * kHeadDim + h * 64,
-                      v->row0 + vi * kPreTile);
-        for (int h = 0; h < 2 && k != nullptr; ++h)
-          tma_load_2d(&p.map_k, &bar.kv_full[st], dst + kPreTileBytes + h * (kPreTileBytes / 2),
-                      k->kvh * kHeadDim + h * 64, k->row0 + ki * kPreTile);
+        if (!(ok = pre_wait(&bar.kv_empty[st], ((fills >> 1) & 1) ^ 1, wc, W_PRE_KV_EMPTY))) break;
+        mbar_arrive_expect_tx(&bar.kv_full[st], (has_v + has_k) * kPreTileBytes);
         ++fills;
-      };
-      bool more = get_tile(0, t);
-      if (more) {
-        load_kv(nullptr, 0, &t, 0);
-        load_q(t);
-      }
-      for (int k = 0; more && ok; ++k) {
-        mbar_arrive(&bar.tile_empty[k % kPreRing]);
-        const int n = max(t.n0, t.n1);
-        for (int i = 0; i + 1 < n; ++i) load_kv(&t, i, &t, i + 1);
-        more = get_tile(k + 1, u);
-        load_kv(&t, n - 1, more ? &u : nullptr, 0);
-        if (more) load_q(u);
-        t = u;
+        const int v_row = t.row0 + i * kPreTile, v_col = t.kvh * kHeadDim;
+        const int k_row = last ? next.row0 : v_row + kPreTile, k_col = last ? next.kvh * kHeadDim : v_col;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint8_t* to = smem + (2 + 2 * st) * kPreTileBytes + h * (kPreTileBytes / 2);
+          if (has_v) tma_load_2d(&p.map_v, &bar.kv_full[st], to, v_col + h * 64, v_row);
+          if (has_k) tma_load_2d(&p.map_k, &bar.kv_full[st], to + kPreTileBytes, k_col + h * 64, k_row);
+        }
+        if (!last) continue;
+        if (!more) break;
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          if ((s ? next.n1 : next.n0) == 0) continue;
+          if (!(ok = pre_wait(&bar.q_empty[s], ((q_phase >> s) & 1) ^ 1, wc, W_PRE_Q_EMPTY))) break;
+          q_phase ^= 1u << s;
+          q_used[0] |= s == 0, q_used[1] |= s == 1;
+          mbar_arrive_expect_tx(&bar.q_full[s], static_cast<uint32_t>(p.hp * p.tq * kHeadDim * 2));
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(&p.map_q, &bar.q_full[s], q_smem + s * kPreTileBytes + h * (kPreTileBytes / 2), h * 64, next.head0,
+                        next.row0 + next.tok0 + s * p.tq);
+        }
+        mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
+        t = next;
+        ++k;
+        i = -1;
+        n = max(t.n0, t.n1);
       }
       if (bar.abort_flag) {  // leave no copy in flight
-        for (int s = 0; s < 2; ++s)
-          if (q_uses[s] > 0) mbar_wait_quiet(&bar.q_full[s], (q_uses[s] - 1) & 1, p.timeout_ns);
+        if (q_used[0]) mbar_wait_quiet(&bar.q_full[0], (q_phase & 1) ^ 1, p.timeout_ns);
+        if (q_used[1]) mbar_wait_quiet(&bar.q_full[1], ((q_phase >> 1) & 1) ^ 1, p.timeout_ns);
         for (int i = max(0, fills - T::kStages); i < fills; ++i)
           mbar_wait_quiet(&bar.kv_full[i & 1], (i >> 1) & 1, p.timeout_ns);
       }
@@ -953,6 +957,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && bar.abort_flag != 0) record_failure(p.status, bar.abort_flag, 0);
 }
 
 // E4M3 codes of K and V to bf16 (exact), [rows][width] each, 16 codes a thread.
