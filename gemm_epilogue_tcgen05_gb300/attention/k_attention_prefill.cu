@@ -33,12 +33,12 @@ bool encode_q(CUtensorMap* map, const void* base, int heads, int rows, int64_t l
 }
 
 template <class Kernel, class... Args>
-bool launch_dependent(Kernel* kernel, int grid, int threads, int smem, cudaStream_t s, const Args&... args) {
+bool launch_dependent(Kernel* kernel, dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait in the kernels
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -70,9 +70,10 @@ int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di
 extern "C" size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, int kv_dtype) {
   using namespace fl;
   if (M < 0 || n_kv_heads < 0) return 0;
-  // the status record, and the E4M3 codes of K and V as bf16
-  return 2 * kWsStatusBytes +
-         (kv_dtype == FL_E4M3 ? static_cast<size_t>(M) * n_kv_heads * kHeadDim * 2 * sizeof(__nv_bfloat16) : 0);
+  // the status record and the work counters; for E4M3 also K and V as fp16, and two powers for each key tile (kept at
+  // its first row)
+  const size_t rows = static_cast<size_t>(M) * n_kv_heads;
+  return 2 * kWsStatusBytes + (kv_dtype == FL_E4M3 ? rows * (kHeadDim * 2 * sizeof(__half) + sizeof(float2)) : 0);
 }
 
 extern "C" int attention_prefill(const void* Q, const void* K, const void* V, const float* k_scale,
@@ -124,14 +125,14 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
                                ? (M / seq_len) * ((seq_len - 1) / per_cta + 1) + (M % seq_len + per_cta - 1) / per_cta
                                : M / per_cta + batch;  // an upper bound: the lengths are on the device
   if (blocks * p.pairs > (1ll << 30)) return FL_ERR_UNSUPPORTED;
-  const int kv_w = static_cast<int>(kv_width);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const void* k16 = K;
   const void* v16 = V;
   int64_t ld16 = ldkv;
   if (fp8) {
-    __nv_bfloat16* kw = reinterpret_cast<__nv_bfloat16*>(ws + 2 * kWsStatusBytes);
-    __nv_bfloat16* vw = kw + static_cast<size_t>(M) * kv_width;
+    __half* kw = reinterpret_cast<__half*>(ws + 2 * kWsStatusBytes);
+    __half* vw = kw + static_cast<size_t>(M) * kv_width;
+    p.powers = reinterpret_cast<const float2*>(vw + static_cast<size_t>(M) * kv_width);
     k16 = kw, v16 = vw, ld16 = kv_width;
   }
   if (!encode_q(&p.map_q, Q, n_heads, M, ldq, p.hp, p.tq) ||
@@ -142,9 +143,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
     return FL_ERR_CUDA;
   p.V = static_cast<const __nv_bfloat16*>(v16);
   p.ldv = ld16;
-  p.ks = k_scale;
-  p.vs = v_scale;
-  p.lds = lds;
+  p.n_kv = n_kv_heads;
   p.cu = cu_seqlens;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.ldo = ldo;
@@ -155,12 +154,15 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   p.work = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);
   p.timeout_ns = wait_timeout_ns();
   if (fp8) {
-    const long long work = (2ll * M * (kv_w / 16) + 255) / 256;
-    const int grid = work < 8ll * di.num_sms ? static_cast<int>(work) : 8 * di.num_sms;
-    if (!launch_dependent(e4m3_rows_to_bf16_kernel, grid, 256, 0, s, static_cast<const uint8_t*>(K),
-                          static_cast<const uint8_t*>(V), static_cast<long long>(ldkv), M, kv_w,
-                          static_cast<__nv_bfloat16*>(const_cast<void*>(k16)),
-                          static_cast<__nv_bfloat16*>(const_cast<void*>(v16))))
+    if (n_kv_heads > 65535) return FL_ERR_UNSUPPORTED;
+    const int key_tiles = cu_seqlens == nullptr
+                              ? M / seq_len * ((seq_len - 1) / kPreTile + 1) + (M % seq_len + kPreTile - 1) / kPreTile
+                              : static_cast<int>(std::min<long long>(static_cast<long long>(M) / kPreTile + batch, M));
+    if (!launch_dependent(e4m3_tiles_to_f16_kernel, dim3(key_tiles, n_kv_heads), 256, 0, s,
+                          static_cast<const uint8_t*>(K), static_cast<const uint8_t*>(V), k_scale, v_scale,
+                          static_cast<long long>(ldkv), static_cast<long long>(lds), cu_seqlens, p.batch, seq_len, M,
+                          n_kv_heads, static_cast<__half*>(const_cast<void*>(k16)),
+                          static_cast<__half*>(const_cast<void*>(v16)), const_cast<float2*>(p.powers)))
       return FL_ERR_CUDA;
   }
   return fp8 ? launch_prefill<true>(p, blocks * p.pairs, di, s) : launch_prefill<false>(p, blocks * p.pairs, di, s);

@@ -31,9 +31,13 @@
 // Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
 //
-// E4M3: a first kernel turns the codes of K and V into bf16 (exact) in the workspace; their scales stay fp32:
-// K's multiplies the logits, V's the weights before these are rounded to bf16.  (Scaled values rounded to bf16 would
-// need no work here, but add their error to that of the weights.)
+// E4M3: a first kernel turns codes times scales into fp16, for each key tile of a sequence and head with the powers of
+// two 2^-a (K) and 2^-b (V) that bring its largest possible value to [2^12, 2^14): 11 bits for all that is above
+// 2^-26 of it, where scales applied here would cost two multiplications for each (query, key) and shared-memory reads
+// that the tensor cores need for themselves (147 us for 4 x 2048 tokens of 32 heads; XXX us so).  The queries become
+// fp16 in place, each row with a power of two of its own (8-bit values in 11 bits: exact down to 2^-28 of the row's
+// largest).  2^a joins the factor of the logits; V's tiles meet in O at the common power 2^E: weights are
+// 2^(x - m + 7 + b - E) in fp16, at most 2^15, and E rises with a rescale like m.
 #pragma once
 #include <climits>
 
@@ -51,11 +55,12 @@ constexpr int kPreTileBytes = kPreTile * kHeadDim * 2;
 constexpr int kPreRing = 3;                        // tile descriptors
 constexpr float kPreNone = -3e38f;                 // a maximum over nothing: any finite logit passes it
 constexpr float kPreLazy = 8.f;
+constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted by 2^7 in fp16
 
 // Where a wait gave up (recorded in the workspace's status record).
 enum : int {
   W_PRE_TILE_FULL = 20, W_PRE_TILE_EMPTY = 21, W_PRE_Q_EMPTY = 22, W_PRE_Q_FULL = 23, W_PRE_KV_EMPTY = 24,
-  W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29, W_PRE_SCALE = 30
+  W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29, W_PRE_Q_READY = 30
 };
 
 struct alignas(128) PrefillParams {
@@ -64,9 +69,8 @@ struct alignas(128) PrefillParams {
   CUtensorMap map_v;
   const __nv_bfloat16* V;  // the rows map_v covers
   long long ldv;
-  const float* ks;  // E4M3: scales [M][lds]
-  const float* vs;
-  long long lds;
+  const float2* powers;  // E4M3: [first row of a key tile][n_kv]: 2^a of K, b of V
+  int n_kv;
   const int* cu;
   __nv_bfloat16* O;
   long long ldo;
@@ -84,13 +88,10 @@ template <bool FP8>
 struct PrefillTraits {
   static constexpr int kStages = 2;  // of a V tile and the next K tile, 64 KB
   static constexpr int kBars = 1024;
-  // E4M3: for each query tile two buffers of K's and V's scales (four runs of 32 + 4), and a factor for each row
-  static constexpr int kScaleRun = 36, kScaleSet = 4 * kScaleRun;
-  static constexpr int kScales = FP8 ? 2 * (4 * kScaleSet + kPreTile) * 4 : 0;
   // output on its way from a row per thread to whole lines: 32 rows of kOutCols columns for each softmax warp
-  static constexpr int kOutCols = FP8 ? 32 : 64;
+  static constexpr int kOutCols = 64;
   static constexpr int kOut = 8 * 32 * kOutCols * 2;
-  static constexpr int kSmem = (2 + 2 * kStages) * kPreTileBytes + kOut + kScales + kBars + 1024 /*alignment*/;
+  static constexpr int kSmem = (2 + 2 * kStages) * kPreTileBytes + kOut + kBars + 1024 /*alignment*/;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -108,7 +109,7 @@ struct PrefillBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[2], kv_empty[2], v_ok[2];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t sc_full[2];
+  uint64_t q_ready[2];  // E4M3: the queries are fp16
   uint64_t drain;
   PrefillTile tile[kPreRing];
   int abort_flag;
@@ -144,31 +145,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-// Shapes of 16 lanes: x4 of 16x256b is 32 columns (thread t has columns 8 k + 2 (t % 4) + {0, 1} of lanes t / 4 and
-// t / 4 + 8 in registers 4 k .. 4 k + 3), x4 of 16x128b 16 columns (column 4 k + t % 4 of the same lanes).
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
-      "}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {"
-      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
-      "};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -216,9 +192,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+// Two values times zero, plus c: NaN for one that is not finite.
+template <bool F16>
+__device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t c) {
   uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  if (F16) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
+  else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 // Two fp32 lanes in one 64-bit register.
@@ -253,8 +242,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * kPreTileBytes;
   constexpr int kOutAt = (2 + 2 * T::kStages) * kPreTileBytes;
-  float* scales = reinterpret_cast<float*>(smem + kOutAt + T::kOut);
-  PrefillBars& bar = *reinterpret_cast<PrefillBars*>(smem + kOutAt + T::kOut + T::kScales);
+  PrefillBars& bar = *reinterpret_cast<PrefillBars*>(smem + kOutAt + T::kOut);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = gridDim.x, cta = blockIdx.x;
 
@@ -263,7 +251,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.sc_full[i], 4);
+      mbar_init(&bar.q_ready[i], 4);
     }
     for (int i = 0; i < T::kStages; ++i)
       mbar_init(&bar.kv_full[i], 1), mbar_init(&bar.kv_empty[i], 2), mbar_init(&bar.v_ok[i], 1);
@@ -454,7 +442,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   } else if (warp == 8) {
     // ================================================================ MMA issue
     // The whole warp walks the loop, so that descriptors stay in uniform registers, and one elected lane issues.
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile), idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true);
+    constexpr uint32_t kTypes = FP8 ? (1u << 7) | (1u << 10) : 0u;  // of A and B: bf16, or without these bits fp16
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile) & ~kTypes,
+                       idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true) & ~kTypes;
     constexpr uint32_t kStep16 = kPreTileBytes / 16;  // one tile in descriptor units
     const bool one = elect_one();
     const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem + kPreTileBytes),
@@ -470,7 +460,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       ++uses;
     };
     auto q_wait = [&](int s) {
-      wait(&bar.q_full[s], (q_phase >> s) & 1, W_PRE_Q_FULL);
+      wait(FP8 ? &bar.q_ready[s] : &bar.q_full[s], (q_phase >> s) & 1, FP8 ? W_PRE_Q_READY : W_PRE_Q_FULL);
       q_phase ^= 1u << s;
     };
     auto p_wait = [&](int s) {
@@ -598,13 +588,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll 8
         for (int c = 0; c < kPreTileBytes / 512; ++c) {
           const uint4 w = ld_shared_v4(base + c * 512);
-          seen[0] = bf16x2_fma(w.x, 0, seen[0]), seen[1] = bf16x2_fma(w.y, 0, seen[1]);
-          seen[2] = bf16x2_fma(w.z, 0, seen[2]), seen[3] = bf16x2_fma(w.w, 0, seen[3]);
+          seen[0] = times_zero<FP8>(w.x, seen[0]), seen[1] = times_zero<FP8>(w.y, seen[1]);
+          seen[2] = times_zero<FP8>(w.z, seen[2]), seen[3] = times_zero<FP8>(w.w, seen[3]);
         }
         if (__any_sync(~0u, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7FFF7FFFu) != 0)) {
           if (lane == 0) bar.tile[k % kPreRing].spoiled = 1;
-          auto clean = [](uint32_t w) {
-            const uint32_t bad = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+          auto clean = [](uint32_t w) {  // an exponent of all ones carries into the sign's place
+            constexpr uint32_t kExp = FP8 ? 0x7C007C00u : 0x7F807F80u, kOne = FP8 ? 0x04000400u : 0x00800080u;
+            const uint32_t bad = ((w & kExp) + kOne) & 0x80008000u;
             return w & ~((bad >> 15) * 0xFFFFu);
           };
 #pragma unroll 1
@@ -630,30 +621,58 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const uint32_t hp_inverse = 65536u / p.hp + 1;  // row / hp = row * hp_inverse >> 16 for rows below 128
     const int row_tok = row / p.hp;
     const float c = p.scale_log2;
-    // E4M3 (see below): this thread's four rows, 8 apart, and its place in a run of scales
-    int tok4[4];
-    float* sets = scales + s * (4 * T::kScaleSet + kPreTile);
-    float* row_factor = sets + 4 * T::kScaleSet;
-    const uint32_t sets_smem = smem_u32(sets) + (lane & 3) * (T::kScaleRun * 4);
-    int sc_uses = 0;
-    if (FP8) {
+    int q_uses = 0;
+    float q_factor = c;  // of this row's logits
+    // E4M3: the queries of a tile to fp16, each row times the power of two that takes its largest value to [2^14, 2^15)
+    auto convert_queries = [&](const PrefillTile& t) -> bool {
+      if ((s ? t.n1 : t.n0) == 0) return true;
+      if (!warp_wait(&bar.q_full[s], q_uses & 1, wc, W_PRE_Q_FULL)) return false;
+      ++q_uses;
+      const uint32_t at = q_smem + s * kPreTileBytes + row * 128;
+      uint4 v[16];
+      uint32_t top = 0;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) tok4[r] = ((warp & 3) * 32 + (lane >> 2) + r * 8) / p.hp;
-    }
+      for (int j = 0; j < 16; ++j) {
+        v[j] = ld_shared_v4(at + (j >> 3) * (kPreTileBytes / 2) + (((j & 7) ^ (row & 7)) << 4));
+        top = bf16x2_max(top, bf16x2_max(bf16x2_max(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
+                                         bf16x2_max(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
+      }
+      const int ex = static_cast<int>(max(top >> 16, top & 0xFFFFu) >> 7);
+      const int up = ex == 255 ? 127 : min(max(268 - ex, 1), 253);
+      const float lift = __uint_as_float(static_cast<uint32_t>(up) << 23);
+      q_factor = c * __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        auto half2 = [&](uint32_t w) { return pack_f16x2(bf16_lo(w) * lift, bf16_hi(w) * lift); };
+        st_shared_v4(at + (j >> 3) * (kPreTileBytes / 2) + (((j & 7) ^ (row & 7)) << 4), half2(v[j].x), half2(v[j].y),
+                     half2(v[j].z), half2(v[j].w));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_ready[s]);
+      return true;
+    };
     int s_uses = 0, o_uses = 0;
     bool ok = true;
-    PrefillTile t;
-    for (int k = 0; ok && __all_sync(~0u, get_tile(k, t)); ++k) {
+    PrefillTile t = {}, next;
+    for (int k = -1; ok; ++k) {  // unit -1 is there for what precedes the first one
       const int n = s ? t.n1 : t.n0, first = t.tok0 + s * p.tq;
       const int tok = first + row_tok;
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int clear = p.causal ? first : t.len - 1;              // last key that every row sees
-      float inv = 0.f;
-      if (!FP8) {
-        // ---- bf16: one thread a row
-        float m = kPreNone;
-        uint64_t l0 = 0, l1 = 0;
-        for (int i = 0; i < n; ++i) {
+      float m = kPreNone, l = 0.f;
+      const float my_factor = q_factor;
+      float E = 0.f;
+      float2 power = make_float2(1.f, 0.f);  // E4M3: 2^a and b of this step's key tile
+      const float2* powers = p.powers + static_cast<long long>(t.row0) * p.n_kv + t.kvh;
+      if (FP8 && n > 0) {
+        power = __ldg(powers);
+        E = power.y + 2.f;
+      }
+      for (int i = 0; i < n; ++i) {
+          float2 power_next = power;
+          if (FP8 && i + 1 < n) power_next = __ldg(powers + static_cast<long long>(i + 1) * kPreTile * p.n_kv);
+          const float f = FP8 ? my_factor * power.x : c;
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
@@ -677,12 +696,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               mx[h] = max3(mx[h], __uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1]));
 #pragma unroll
           for (int h = 0; h < 4; ++h) mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
           const bool rise = top > m + kPreLazy;
-          if (__any_sync(~0u, rise)) {
-            const float up = rise ? top : m, down = ex2(m - up);
+          if (__any_sync(~0u, rise) || (FP8 && power.y > E)) {
+            const float up = rise ? top : m;
+            float down = ex2(m - up);
             m = up;
-            l0 = f2_mul(l0, f2(down, down)), l1 = f2_mul(l1, f2(down, down));
+            l *= down;
+            if (FP8 && power.y > E) {
+              down *= ex2(E - power.y - 2.f);
+              E = power.y + 2.f;
+            }
             if (i > 0) {  // O of the key tiles before is complete: S of this one was committed behind it
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -695,191 +719,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               }
             }
           }
-          const uint64_t c2 = f2(c, c), m2 = f2(-m, -m);
+          const float lift = FP8 ? kPreLift + power.y - E : 0.f;  // weights are larger by 2^lift
+          const uint64_t f2f = f2(f, f), m2 = f2(lift - m, lift - m);
+          uint64_t l0 = 0, l1 = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t w[16];
 #pragma unroll
             for (int h = 0; h < 16; h += 2) {
               float a, b, d, e;
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), c2, m2), a, b);
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m2), d, e);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), f2f, m2), a, b);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), f2f, m2), d, e);
               a = ex2(a), b = ex2(b), d = ex2(d), e = ex2(e);
               l0 = f2_add(l0, f2(a, b)), l1 = f2_add(l1, f2(d, e));
-              w[h] = pack_bf16x2(a, b), w[h + 1] = pack_bf16x2(d, e);
+              w[h] = FP8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+              w[h + 1] = FP8 ? pack_f16x2(d, e) : pack_bf16x2(d, e);
             }
             tmem_st16(s_tmem + j * 16, w);
           }
+          float a, b, d, e;
+          f2_split(l0, a, b);
+          f2_split(l1, d, e);
+          l += FP8 ? ((a + b) + (d + e)) * ex2(-lift) : (a + b) + (d + e);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.p_full[s]);
-        }
-        float a, b, d, e;
-        f2_split(l0, a, b);
-        f2_split(l1, d, e);
-        inv = 1.f / ((a + b) + (d + e));
-      } else {
-        // ---- E4M3: each key has a scale, and a thread that held a whole row would read all 128 of them from
-        // shared memory twice (that alone took as long as the products).  In the 16x256b shape a lane holds
-        // columns 8 k + 2 (lane % 4) + {0, 1} of four rows (lane / 4 + 8 r): 32 scales serve four rows.
-        const int col = threadIdx.x & 127;  // the column whose scales this thread fetches
-        auto fetch = [&](int i, float& a, float& b) {
-          const int pos = i * kPreTile + col;
-          a = b = 0.f;
-          if (pos < t.len) {
-            const long long at = static_cast<long long>(t.row0 + pos) * p.lds + t.kvh;
-            a = __ldg(p.ks + at), b = __ldg(p.vs + at);
-          }
-        };
-        auto publish = [&](int i, float a, float b) {
-          // Where rows mask keys their weight is zero, and a scale of V that is not finite must not meet it: such a
-          // key counts as one whose values are not finite (see the end of the tile).
-          if (!isfinite(b) && i >= first_masked(t)) {
-            b = 0.f;
-            *reinterpret_cast<volatile int*>(&bar.tile[k % kPreRing].spoiled) = 1;
-          }
-          float* to = sets + (i & 1) * 2 * T::kScaleSet + ((col >> 1) & 3) * T::kScaleRun + (col >> 3) * 2 + (col & 1);
-          to[0] = a;
-          to[T::kScaleSet] = b;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.sc_full[s]);
-          const bool done = warp_wait(&bar.sc_full[s], sc_uses & 1, wc, W_PRE_SCALE);
-          ++sc_uses;
-          return done;
-        };
-        float m[4], next_k = 0.f, next_v = 0.f;
-        uint64_t l[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m[r] = kPreNone, l[r] = 0;
-        if (n > 0) {
-          fetch(0, next_k, next_v);
-          ok = publish(0, next_k, next_v);
-        }
-        for (int i = 0; i < n && ok; ++i) {
-          if (i + 1 < n) fetch(i + 1, next_k, next_v);
-          if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
-          ++s_uses;
-          tc_fence_after();
-          const uint32_t kf = sets_smem + (i & 1) * (2 * T::kScaleSet * 4), vf = kf + T::kScaleSet * 4;
-          const bool masked = i * kPreTile + kPreTile - 1 > clear;
-          const uint64_t c2 = f2(c, c);
-          // Two rows at a time: half the registers, and half the code in the instruction cache.
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t half = static_cast<uint32_t>(h * 16) << 16;
-            uint32_t x[4][16];  // [32 columns][4 k + 2 row + column]
-#pragma unroll
-            for (int j = 0; j < 4; ++j) tmem_ld_16x256b_x4(s_tmem + half + j * 32, x[j]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 f = ld_shared_v4(kf + j * 16);
-              const uint64_t f0 = f2(__uint_as_float(f.x), __uint_as_float(f.y)),
-                             f1 = f2(__uint_as_float(f.z), __uint_as_float(f.w));
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t* y = &x[j >> 1][(j & 1) * 8 + q * 2];
-                float a, b;
-                f2_split(f2_mul(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), q < 2 ? f0 : f1), a, b);
-                y[0] = __float_as_uint(a), y[1] = __float_as_uint(b);
-              }
-            }
-            int cols[2];  // columns up to these count; counted from this lane's first
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              cols[r] = (p.causal ? min(first + tok4[r], t.len - 1) : t.len - 1) - i * kPreTile - 2 * (lane & 3);
-            if (masked) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j)
-                if ((j >> 2) * 8 + (j & 1) > cols[(j >> 1) & 1]) x[j >> 4][j & 15] = __float_as_uint(-INFINITY);
-            }
-            float top[2];
-            bool rise = false;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                mx[j & 1] = max3(mx[j & 1], __uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2]),
-                                 __uint_as_float(x[j >> 2][(j & 3) * 4 + r * 2 + 1]));
-              top[r] = fmaxf(mx[0], mx[1]) * c;
-              rise |= top[r] > m[r] + kPreLazy;
-            }
-            if (__any_sync(~0u, rise)) {
-              float down[2];
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                float a = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-                a = fmaxf(a, __shfl_xor_sync(~0u, a, 2));
-                const float up = a > m[r] + kPreLazy ? a : m[r];
-                down[r] = ex2(m[r] - up);
-                m[r] = up;
-                l[r] = f2_mul(l[r], f2(down[r], down[r]));
-              }
-              if (i > 0) {
-#pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                  uint32_t o[16];
-                  tmem_ld_16x256b_x4(o_tmem + half + j * 32, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * down[(q >> 1) & 1]);
-                  tmem_st_16x256b_x4(o_tmem + half + j * 32, o);
-                }
-              }
-            }
-            const uint64_t m2[2] = {f2(-m[0], -m[0]), f2(-m[1], -m[1])};
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              uint32_t w[8];
-#pragma unroll
-              for (int j = jj * 2; j < jj * 2 + 2; ++j) {
-                const uint4 f = ld_shared_v4(vf + j * 16);
-                const uint64_t f0 = f2(__uint_as_float(f.x), __uint_as_float(f.y)),
-                               f1 = f2(__uint_as_float(f.z), __uint_as_float(f.w));
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {  // columns of k = 2 j + (q >> 1), row q & 1
-                  const uint32_t* y = &x[jj][(j & 1) * 8 + q * 2];
-                  float a, b;
-                  f2_split(f2_fma(f2(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, m2[q & 1]), a, b);
-                  a = ex2(a), b = ex2(b);
-                  l[q & 1] = f2_add(l[q & 1], f2(a, b));
-                  f2_split(f2_mul(f2(a, b), q < 2 ? f0 : f1), a, b);
-                  w[(j & 1) * 4 + q] = pack_bf16x2(a, b);
-                }
-              }
-              tmem_st_16x128b_x4(s_tmem + half + jj * 16, w);
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {  // the other two rows' turn (and back)
-              const float m_r = m[r];
-              const uint64_t l_r = l[r];
-              const int tok_r = tok4[r];
-              m[r] = m[r + 2], l[r] = l[r + 2], tok4[r] = tok4[r + 2];
-              m[r + 2] = m_r, l[r + 2] = l_r, tok4[r + 2] = tok_r;
-            }
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_full[s]);
-          if (i + 1 < n) ok = publish(i + 1, next_k, next_v);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float a, b;
-          f2_split(l[r], a, b);
-          a += b;
-          a += __shfl_xor_sync(~0u, a, 1);
-          a += __shfl_xor_sync(~0u, a, 2);
-          if ((lane & 3) == 0) row_factor[(warp & 3) * 32 + (lane >> 2) + r * 8] = 1.f / a;
-        }
-        __syncwarp();
-        inv = row_factor[row];
-        __syncwarp();
+          power = power_next;
       }
       if (!ok) break;
+      const bool have = __all_sync(~0u, get_tile(k + 1, next));
+      if (FP8 && have && !(ok = convert_queries(next))) break;  // before the output: the products behind it wait for them
+      const float inv = (FP8 ? ex2(E - kPreLift) : 1.f) / l;
       if (n > 0) {
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
@@ -941,8 +812,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             float sum = 0.f;
 #pragma unroll 1
             for (int pos = from; pos <= lim; ++pos) {
-              float y = __bfloat162float(v[static_cast<long long>(pos) * p.ldv + d]);
-              if (FP8) y *= p.vs[static_cast<long long>(t.row0 + pos) * p.lds + t.kvh];
+              const __nv_bfloat16 raw = v[static_cast<long long>(pos) * p.ldv + d];
+              const float y = FP8 ? __half2float(__ushort_as_half(__bfloat16_as_ushort(raw))) : __bfloat162float(raw);
               if (!isfinite(y)) sum += y;
             }
             if (!isfinite(sum)) mine[d] = __float2bfloat16_rn(sum);
@@ -950,7 +821,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.tile_empty[k % kPreRing]);
+      if (k >= 0 && lane == 0) mbar_arrive(&bar.tile_empty[k % kPreRing]);
+      if (!have) break;
+      t = next;
     }
   }
   tc_fence_before();
@@ -960,19 +833,69 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   if (threadIdx.x == 0 && bar.abort_flag != 0) record_failure(p.status, bar.abort_flag, 0);
 }
 
-// E4M3 codes of K and V to bf16 (exact), [rows][width] each, 16 codes a thread.
-__global__ void __launch_bounds__(256) e4m3_rows_to_bf16_kernel(const uint8_t* K, const uint8_t* V, long long ld, int rows,
-                                                                int width, __nv_bfloat16* K16, __nv_bfloat16* V16) {
+// E4M3 codes and scales of K and V to fp16 for the kernel above.  One CTA takes a key tile (128 rows of a sequence,
+// from its first) of one kv head: the largest finite scale among them gives 2^a (K) or b (V), then each 16 codes of a
+// thread become code * (scale * 2^-a).  Bound by memory: 2 bytes in and 4 out for each K and V value.
+__global__ void __launch_bounds__(256) e4m3_tiles_to_f16_kernel(const uint8_t* K, const uint8_t* V, const float* ks,
+                                                               const float* vs, long long ld, long long lds, const int* cu,
+                                                               int batch, int seq_len, int M, int n_kv, __half* K16,
+                                                               __half* V16, float2* powers) {
   griddep_wait();
   griddep_launch_dependents();
-  const int per_row = width / 16;
-  const long long n = static_cast<long long>(rows) * per_row;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < 2 * n;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const bool second = i >= n;
-    const long long j = second ? i - n : i, r = j / per_row;
-    const int c = static_cast<int>(j - r * per_row) * 16;
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>((second ? V : K) + r * ld + c));
+  __shared__ int found[2];  // first row and rows of this tile
+  __shared__ uint32_t top[2];
+  const int tid = threadIdx.x, lane = tid & 31, kvh = blockIdx.y;
+  if (tid == 0) found[1] = 0;
+  if (tid < 2) top[tid] = 0;
+  __syncthreads();
+  if (tid < 32) {  // the sequence that holds key tile blockIdx.x
+    int skip = static_cast<int>(blockIdx.x);
+    for (int b0 = 0; b0 < batch; b0 += 32) {
+      int first = 0, last = 0;
+      if (b0 + lane < batch) sequence_rows(cu, b0 + lane, seq_len, M, first, last);
+      const int have = last > first ? (last - first - 1) / kPreTile + 1 : 0;
+      int sum = have;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const unsigned who = __ballot_sync(~0u, sum > skip);
+      if (who != 0) {
+        if (lane == __ffs(who) - 1) {
+          found[0] = first + (skip - (sum - have)) * kPreTile;
+          found[1] = min(kPreTile, last - found[0]);
+        }
+        break;
+      }
+      skip -= __shfl_sync(~0u, sum, 31);
+    }
+  }
+  __syncthreads();
+  const int row0 = found[0], rows = found[1];
+  if (rows == 0) return;
+  {  // threads 0 .. 127 the scales of K, 128 .. 255 those of V
+    const int r = tid & 127;
+    float x = r < rows ? fabsf((tid < 128 ? ks : vs)[static_cast<long long>(row0 + r) * lds + kvh]) : 0.f;
+    const uint32_t bits = __reduce_max_sync(~0u, x < INFINITY ? __float_as_uint(x) : 0u);
+    if (lane == 0) atomicMax(&top[tid >> 7], bits);
+  }
+  __syncthreads();
+  int e[2];  // 448 * scale * 2^-e is below 2^14
+#pragma unroll
+  for (int i = 0; i < 2; ++i) e[i] = top[i] == 0 ? 0 : min(max(static_cast<int>(top[i] >> 23) - 127 - 4, -120), 120);
+  if (tid == 0)
+    powers[static_cast<long long>(row0) * n_kv + kvh] =
+        make_float2(__uint_as_float(static_cast<uint32_t>(127 + e[0]) << 23), static_cast<float>(e[1]));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // 32 rows at a time, 8 threads a row; K first, then V
+    const bool second = i >= 4;
+    const int r = (i & 3) * 32 + (tid >> 3), c = (tid & 7) * 16;
+    if (r >= rows) continue;
+    const long long row = row0 + r;
+    const float s = (second ? vs : ks)[row * lds + kvh] *
+                    __uint_as_float(static_cast<uint32_t>(127 - e[second ? 1 : 0]) << 23);
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>((second ? V : K) + row * ld + kvh * kHeadDim + c));
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t out[8];
 #pragma unroll
@@ -980,9 +903,9 @@ __global__ void __launch_bounds__(256) e4m3_rows_to_bf16_kernel(const uint8_t* K
       uint32_t h;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(in[k >> 1] >> ((k & 1) * 16))));
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      out[k] = pack_bf16x2(f.x, f.y);
+      out[k] = pack_f16x2(f.x * s, f.y * s);
     }
-    uint4* dst = reinterpret_cast<uint4*>((second ? V16 : K16) + r * width + c);
+    uint4* dst = reinterpret_cast<uint4*>((second ? V16 : K16) + (row * n_kv + kvh) * kHeadDim + c);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
     dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }

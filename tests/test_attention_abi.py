@@ -86,7 +86,7 @@ def test_prefill_checks(lib, status, changes):
 def test_workspace_sizes(lib):
     n = lib.fl_attention_prefill_workspace_bytes
     assert n(100, 2, fl.FL_BF16) >= 512
-    assert n(100, 2, fl.FL_E4M3) - n(100, 2, fl.FL_BF16) == 100 * 2 * 128 * 2 * 2  # K and V as bf16
+    assert n(100, 2, fl.FL_E4M3) - n(100, 2, fl.FL_BF16) >= 100 * 2 * 128 * 2 * 2  # K and V in 16 bits
     assert n(1 << 22, 16, fl.FL_E4M3) > 1 << 32
     assert n(-1, 2, fl.FL_BF16) == 0
     assert lib.fl_attention_decode_workspace_bytes() % 256 == 0
