@@ -874,6 +874,15 @@ __global__ void __launch_bounds__(256) e4m3_tiles_to_f16_kernel(const uint8_t* K
   __syncthreads();
   const int row0 = found[0], rows = found[1];
   if (rows == 0) return;
+  uint4 codes[8];  // 32 rows at a time, 8 threads a row; K first, then V; on their way while the scales are compared
+  float scale[8];
+  const int c = (tid & 7) * 16;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = min((i & 3) * 32 + (tid >> 3), rows - 1);
+    codes[i] = __ldg(reinterpret_cast<const uint4*>((i >= 4 ? V : K) + (row0 + r) * ld + kvh * kHeadDim + c));
+    scale[i] = __ldg((i >= 4 ? vs : ks) + (row0 + r) * lds + kvh);
+  }
   {  // threads 0 .. 127 the scales of K, 128 .. 255 those of V
     const int r = tid & 127;
     float x = r < rows ? fabsf((tid < 128 ? ks : vs)[static_cast<long long>(row0 + r) * lds + kvh]) : 0.f;
@@ -888,14 +897,13 @@ __global__ void __launch_bounds__(256) e4m3_tiles_to_f16_kernel(const uint8_t* K
     powers[static_cast<long long>(row0) * n_kv + kvh] =
         make_float2(__uint_as_float(static_cast<uint32_t>(127 + e[0]) << 23), static_cast<float>(e[1]));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // 32 rows at a time, 8 threads a row; K first, then V
+  for (int i = 0; i < 8; ++i) {
     const bool second = i >= 4;
-    const int r = (i & 3) * 32 + (tid >> 3), c = (tid & 7) * 16;
+    const int r = (i & 3) * 32 + (tid >> 3);
     if (r >= rows) continue;
     const long long row = row0 + r;
-    const float s = (second ? vs : ks)[row * lds + kvh] *
-                    __uint_as_float(static_cast<uint32_t>(127 - e[second ? 1 : 0]) << 23);
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>((second ? V : K) + row * ld + kvh * kHeadDim + c));
+    const float s = scale[i] * __uint_as_float(static_cast<uint32_t>(127 - e[second ? 1 : 0]) << 23);
+    const uint4 w = codes[i];
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t out[8];
 #pragma unroll
