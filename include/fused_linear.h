@@ -311,7 +311,7 @@ FL_API int fused_swiglu_bwd(const void* dO, const void* Wd, const void* G, const
  * page_size is any number >= 1 (a multiple of 8 streams best), offsets are 64-bit.  All of these live
  * on the device, so a captured graph can be replayed as the sequences grow.  head_dim must be 128
  * (FL_ERR_UNSUPPORTED otherwise).  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes
- * them.  Scale, table, length and offset pointers need 4-byte alignment, the others 16. */
+ * them, with scales that are not negative.  Scale, table, length and offset pointers need 4-byte alignment, the others 16. */
 
 /* Rows of keys and values into the cache.
  * K, V [T, n_kv_heads*128], pitch ldkv elements: bf16 (row_dtype FL_BF16) or E4M3 bytes (FL_E4M3) with
@@ -360,10 +360,13 @@ FL_API size_t fl_attention_decode_workspace_bytes(void);
  * decreasing, in [0, M]); cu_seqlens NULL: the rows are sequences of seq_len tokens laid end to end,
  * the last one possibly shorter (batch is ignored).  Rows of O in no sequence stay as they were.
  * Rows of another sequence, or masked ones of the own, never reach a result, whatever they hold.
- * Softmax state and sums are fp32; the weights p_ij (times the scale of V) are rounded to bf16 for the
- * tensor cores.
+ * Softmax state and sums are fp32; the weights p_ij are rounded to bf16 for the tensor cores.  With E4M3
+ * keys and values the products run in fp16 instead: codes times scales and the weights are rounded to 11
+ * bits, with a power of two of its own for each query row and for each 128 keys of a sequence and head
+ * (what is below 2^-26 of the largest there loses bits).
  * workspace: fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype) bytes, 256-byte aligned, its
- * first 512 bytes zero-filled before first use; two calls that may overlap on the GPU need one each. */
+ * first 512 bytes zero-filled before first use (and again after FL_ERR_TIMEOUT); two calls that may
+ * overlap on the GPU need one each.  One kernel; E4M3 runs a second one in front. */
 FL_API int attention_prefill(const void* Q, const void* K, const void* V, const float* k_scale,
                              const float* v_scale, const int32_t* cu_seqlens, void* O, int M, int batch,
                              int n_heads, int n_kv_heads, int head_dim, int seq_len, int64_t ldq, int64_t ldkv,

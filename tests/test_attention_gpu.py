@@ -220,6 +220,25 @@ def test_prefill_same_results_every_time():
         assert torch.equal(first, fl.attention_prefill(q, k, v, seq_len=700, k_scale=ks, v_scale=vs))
 
 
+def test_prefill_wait_that_runs_out():
+    """With a limit of a microsecond a wait behind a unit of work of some hundred microseconds gives up: the call
+    ends, the status record says so, and after zeroing it the workspace serves again."""
+    n = 32768
+    q, k, v = (randn(n, D, seed=s) for s in (51, 52, 53))
+    ws = fl.attention_prefill_workspace(n, 1, False)
+    try:
+        fl.set_wait_timeout_ns(1000)
+        fl.attention_prefill(q, k, v, workspace=ws)
+        status = fl.check_device_status(ws)
+    finally:
+        fl.set_wait_timeout_ns(0)
+    assert status == fl.FL_ERR_TIMEOUT
+    ws[:512] = 0
+    out = fl.attention_prefill(q[:700], k[:700], v[:700], workspace=ws)
+    check_prefill(q[:700], k[:700], v[:700], None, None, [700], out, True)
+    assert fl.check_device_status(ws) == fl.FL_OK
+
+
 # ---------------------------------------------------------------- decode
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("lens,heads,kv,page", [
