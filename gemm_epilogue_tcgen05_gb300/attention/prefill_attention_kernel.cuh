@@ -170,10 +170,10 @@ __device__ __forceinline__ bool pre_wait(uint64_t* bar, uint32_t parity, const P
   uint32_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
-    if ((i & 255u) != 255u) continue;
+    if ((i & 15u) != 15u) continue;
     uint32_t now;
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
-    t0 = i < 256u ? now : t0;
+    t0 = i < 16u ? now : t0;
     if (now - t0 > w.timeout_ns) atomicCAS(w.abort_flag, 0, where);
     if (*const_cast<volatile int*>(w.abort_flag) != 0) return false;
   }
@@ -297,15 +297,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       return last - first;
     };
     const int tier_len = p.causal ? tpc : kPreTile;
-    auto tiers_of = [&](int len) { return len > 0 ? (len - 1) / tier_len + 1 : 0; };
-    int mine = 0, tiers = 0;
+    auto measure = [&](int b, int& reach, int& count) {  // tiers of a sequence, and its blocks
+      const int len = b < p.batch ? length_of(b) : 0;
+      reach = len > 0 ? (len - 1) / tier_len + 1 : 0;
+      count = len > 0 ? (len - 1) / tpc + 1 : 0;
+    };
+    int my_reach = 0, my_count = 0, tiers = 0;  // of sequence `lane`
     unsigned blocks = 0;
 #pragma unroll 1
     for (int b = lane; b < p.batch; b += 32) {
-      const int len = length_of(b);
-      if (b == lane) mine = len;
-      tiers = max(tiers, tiers_of(len));
-      blocks += len > 0 ? (len - 1) / tpc + 1 : 0;
+      int reach, count;
+      measure(b, reach, count);
+      if (b == lane) my_reach = reach, my_count = count;
+      tiers = max(tiers, reach);
+      blocks += count;
     }
     tiers = __reduce_max_sync(~0u, tiers);
     blocks = __reduce_add_sync(~0u, blocks);
@@ -338,22 +343,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         unsigned upto = above;
 #pragma unroll 1
         for (int b0 = 0; b0 < p.batch && seq < 0; b0 += 32) {
-          const int len = b0 == 0 ? mine : b0 + lane < p.batch ? length_of(b0 + lane) : 0;
-          const int reach = tiers_of(len);
-          const unsigned have = p.causal ? reach > tier : reach == tier + 1 ? (len - 1) / tpc + 1 : 0;
-          unsigned sum = have;  // inclusive sum over the lanes
+          int reach = my_reach, count = my_count;
+          if (b0 > 0) measure(b0 + lane, reach, count);
+          const unsigned have = p.causal ? reach > tier : reach == tier + 1 ? count : 0;
+          const unsigned all = __reduce_add_sync(~0u, have);
+          if (block < upto + all) {
+            unsigned sum = have;  // inclusive sum over the lanes
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned y = __shfl_up_sync(~0u, sum, o);
-            if (lane >= o) sum += y;
-          }
-          const unsigned who = __ballot_sync(~0u, upto + sum > block);
-          if (who != 0) {
-            const int src = __ffs(who) - 1;
+            for (int o = 1; o < 32; o <<= 1) {
+              const unsigned y = __shfl_up_sync(~0u, sum, o);
+              if (lane >= o) sum += y;
+            }
+            const int src = __ffs(__ballot_sync(~0u, upto + sum > block)) - 1;
             seq = b0 + src;
             in = static_cast<int>(block - upto - __shfl_sync(~0u, sum - have, src));
           }
-          upto += __shfl_sync(~0u, sum, 31);
+          upto += all;
         }
         if (seq >= 0) break;
         above = upto;

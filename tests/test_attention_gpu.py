@@ -221,11 +221,12 @@ def test_prefill_same_results_every_time():
 
 
 def test_prefill_wait_that_runs_out():
-    """With a limit of a microsecond a wait behind a unit of work of some hundred microseconds gives up: the call
-    ends, the status record says so, and after zeroing it the workspace serves again."""
-    n = 32768
-    q, k, v = (randn(n, D, seed=s) for s in (51, 52, 53))
-    ws = fl.attention_prefill_workspace(n, 1, False)
+    """With a limit of a microsecond the wait for a unit of work of some hundred microseconds (two heads of 65536
+    tokens give every CTA three) gives up: the call ends, the status record says so, and after zeroing it the
+    workspace serves again."""
+    n = 65536
+    q, k, v = (randn(n, 2 * D, seed=s) for s in (51, 52, 53))
+    ws = fl.attention_prefill_workspace(n, 2, False)
     try:
         fl.set_wait_timeout_ns(1000)
         fl.attention_prefill(q, k, v, workspace=ws)
