@@ -703,9 +703,16 @@ def paged_kv_append(K, V, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
         _check("paged_kv_append", st)
 
 
+def _fresh(n: int, head: int, device) -> torch.Tensor:
+    """A workspace of n bytes, its first `head` bytes (status and counters; the rest is written before it is read) zero."""
+    t = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    t[:head].zero_()
+    return t
+
+
 def attention_decode_workspace(device=None) -> torch.Tensor:
-    """A zero-filled workspace for attention_decode calls of any shape (one for each set of calls that may overlap)."""
-    return torch.zeros(load().fl_attention_decode_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
+    """A workspace for attention_decode calls of any shape (one for each set of calls that may overlap)."""
+    return _fresh(load().fl_attention_decode_workspace_bytes(), 4096, device)
 
 
 def attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale=None, v_page_scale=None, scale=None,
@@ -737,9 +744,9 @@ def attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale=Non
 
 
 def attention_prefill_workspace(rows: int, n_kv_heads: int, fp8: bool, device=None) -> torch.Tensor:
-    """A zero-filled workspace for attention_prefill calls of up to `rows` rows."""
+    """A workspace for attention_prefill calls of up to `rows` rows."""
     n = load().fl_attention_prefill_workspace_bytes(int(rows), int(n_kv_heads), FL_E4M3 if fp8 else FL_BF16)
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return _fresh(n, 512, device)
 
 
 def attention_prefill(Q, K, V, cu_seqlens=None, seq_len: int = 0, k_scale=None, v_scale=None, causal: bool = True,

@@ -8,6 +8,7 @@
 namespace fl {
 
 constexpr int kHeadDim = 128;  // the width the QKV projections of this library write
+constexpr int kMaxHeads = 1 << 16;
 
 // The E4M3 or bf16 cache: k_pages and v_pages are [num_pages] blocks `page_pitch` elements apart, each
 // [n_kv_heads][page_size][128]; the scales are [num_pages] blocks `scale_pitch` floats apart, each

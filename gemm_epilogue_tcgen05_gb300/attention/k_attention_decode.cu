@@ -48,6 +48,7 @@ extern "C" int attention_decode(const void* Q, const void* k_pages, const void* 
   if (batch == 0 || n_heads == 0) return FL_OK;
   if (n_kv_heads == 0 || n_heads % n_kv_heads != 0) return FL_ERR_INVALID_ARG;
   if (head_dim != kHeadDim) return FL_ERR_UNSUPPORTED;
+  if (n_heads > kMaxHeads) return FL_ERR_UNSUPPORTED;
   if (Q == nullptr || O == nullptr) return FL_ERR_INVALID_ARG;
   const int64_t width = static_cast<int64_t>(n_heads) * kHeadDim;
   if (batch > 1 && (ldq < width || ldo < width)) return FL_ERR_INVALID_ARG;

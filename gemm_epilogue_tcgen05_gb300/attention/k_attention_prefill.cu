@@ -89,6 +89,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   if (M == 0 || n_heads == 0 || (cu_seqlens != nullptr && batch == 0)) return FL_OK;
   if (n_kv_heads == 0 || n_heads % n_kv_heads != 0) return FL_ERR_INVALID_ARG;
   if (head_dim != kHeadDim) return FL_ERR_UNSUPPORTED;
+  if (n_heads > kMaxHeads) return FL_ERR_UNSUPPORTED;
   if (Q == nullptr || K == nullptr || V == nullptr || O == nullptr) return FL_ERR_INVALID_ARG;
   if (fp8 && (k_scale == nullptr || v_scale == nullptr)) return FL_ERR_INVALID_ARG;
   const int64_t width = static_cast<int64_t>(n_heads) * kHeadDim, kv_width = static_cast<int64_t>(n_kv_heads) * kHeadDim;

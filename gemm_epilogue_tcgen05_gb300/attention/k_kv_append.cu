@@ -154,6 +154,7 @@ extern "C" int paged_kv_append(const void* K, const void* V, const float* k_scal
   if ((row_dtype != FL_BF16 && !rows8) || (cache_dtype != FL_BF16 && !cache8)) return FL_ERR_INVALID_ARG;
   if (T == 0 || batch == 0 || n_kv_heads == 0) return FL_OK;
   if (head_dim != kHeadDim || (rows8 && !cache8)) return FL_ERR_UNSUPPORTED;
+  if (n_kv_heads > kMaxHeads) return FL_ERR_UNSUPPORTED;
   if (cu_seqlens == nullptr && T > batch) return FL_ERR_INVALID_ARG;
   if (K == nullptr || V == nullptr || (rows8 && (k_scale == nullptr || v_scale == nullptr))) return FL_ERR_INVALID_ARG;
   if (T > 1 && (ldkv < static_cast<int64_t>(n_kv_heads) * kHeadDim || (rows8 && lds < n_kv_heads)))

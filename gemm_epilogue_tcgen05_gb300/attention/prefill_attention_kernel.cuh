@@ -102,7 +102,7 @@ struct PrefillTile {
   int tok0;        // first token of query tile 0 (query tile 1: + tq)
   int n0, n1;      // key tiles that query tiles 0 and 1 meet
   int head0, kvh;
-  int spoiled;     // set by warp 11: V holds values that are not finite in a masked tile
+  int bad_lo, bad_hi;  // set by warp 11: first and last key of masked tiles whose V is not finite (none: hi < 0)
 };
 
 struct PrefillBars {
@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         --tier;
       }
       PrefillTile t = {};
+      t.bad_lo = INT_MAX, t.bad_hi = -1;
       more = seq >= 0;
       if (more) {
         int first, last;
@@ -598,16 +599,26 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           seen[2] = times_zero<FP8>(w.z, seen[2]), seen[3] = times_zero<FP8>(w.w, seen[3]);
         }
         if (__any_sync(~0u, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7FFF7FFFu) != 0)) {
-          if (lane == 0) bar.tile[k % kPreRing].spoiled = 1;
-          auto clean = [](uint32_t w) {  // an exponent of all ones carries into the sign's place
+          int lo = INT_MAX, hi = -1;
+          bool bad_chunk = false;
+          auto clean = [&](uint32_t w) {  // an exponent of all ones carries into the sign's place
             constexpr uint32_t kExp = FP8 ? 0x7C007C00u : 0x7F807F80u, kOne = FP8 ? 0x04000400u : 0x00800080u;
             const uint32_t bad = ((w & kExp) + kOne) & 0x80008000u;
+            bad_chunk |= bad != 0;
             return w & ~((bad >> 15) * 0xFFFFu);
           };
 #pragma unroll 1
           for (int c = 0; c < kPreTileBytes / 512; ++c) {
             const uint4 w = ld_shared_v4(base + c * 512);
+            bad_chunk = false;
             st_shared_v4(base + c * 512, clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+            const int pos = i * kPreTile + (c & 31) * 4 + (lane >> 3);  // half a key's values are 128 bytes
+            if (bad_chunk && pos < t.len) lo = min(lo, pos), hi = max(hi, pos);
+          }
+          lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
+          if (lane == 0) {
+            PrefillTile& to = bar.tile[k % kPreRing];
+            to.bad_lo = min(to.bad_lo, lo), to.bad_hi = max(to.bad_hi, hi);
           }
           fence_async_smem();
         }
@@ -761,8 +772,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
         tc_fence_after();
-        const bool spoiled = *reinterpret_cast<volatile int*>(&bar.tile[k % kPreRing].spoiled) != 0;
-        const int from = first_masked(t) * kPreTile;
+        const volatile PrefillTile& said = bar.tile[k % kPreRing];
+        const int bad_lo = said.bad_lo, bad_hi = said.bad_hi;
         // A thread has a row; lines of global memory want a few rows each, all of 128 bytes.  So 16-byte pieces go
         // through shared memory, piece j of row r at place j ^ (r's low bits).  (Stored straight from the row's
         // thread, each instruction touched 32 lines: 4000 cycles a tile.)
@@ -807,7 +818,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           __syncwarp();
         }
         tc_fence_before();
-        if (spoiled && row_tok < p.tq && tok < t.len) {
+        if (bad_lo <= min(bad_hi, lim) && row_tok < p.tq && tok < t.len) {
           // Values of V that are not finite were taken out for the rows that do not see them.  The others get their
           // sum (infinite or NaN), whatever the finite rest is.
           const __nv_bfloat16* v = p.V + static_cast<long long>(t.row0) * p.ldv + static_cast<long long>(t.kvh) * kHeadDim;
@@ -817,7 +828,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           for (int d = 0; d < kHeadDim; ++d) {
             float sum = 0.f;
 #pragma unroll 1
-            for (int pos = from; pos <= lim; ++pos) {
+            for (int pos = bad_lo; pos <= min(bad_hi, lim); ++pos) {
               const __nv_bfloat16 raw = v[static_cast<long long>(pos) * p.ldv + d];
               const float y = FP8 ? __half2float(__ushort_as_half(__bfloat16_as_ushort(raw))) : __bfloat162float(raw);
               if (!isfinite(y)) sum += y;

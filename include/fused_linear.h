@@ -310,7 +310,8 @@ FL_API int fused_swiglu_bwd(const void* dO, const void* Wd, const void* G, const
  *   seq_lens           int32 [batch], tokens in the cache.
  * page_size is any number >= 1 (a multiple of 8 streams best), offsets are 64-bit.  All of these live
  * on the device, so a captured graph can be replayed as the sequences grow.  head_dim must be 128
- * (FL_ERR_UNSUPPORTED otherwise).  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes
+ * and head counts at most 65536 (FL_ERR_UNSUPPORTED otherwise).  Outputs may not overlap K, V or the
+ * cache.  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes
  * them, with scales that are not negative.  Scale, table, length and offset pointers need 4-byte alignment, the others 16. */
 
 /* Rows of keys and values into the cache.
@@ -340,8 +341,8 @@ FL_API int paged_kv_append(const void* K, const void* V, const float* k_scale, c
  * outside [0, num_pages) among the entries in use: the sequence's rows are NaN and
  * fl_check_device_status(workspace) returns FL_ERR_INVALID_ARG once.  Nothing behind a sequence's
  * length is read into the result, whatever it holds.
- * workspace: fl_attention_decode_workspace_bytes() bytes, 256-byte aligned, zero-filled before first
- * use; calls of any shape may follow one another with it, two calls that may overlap on the GPU need
+ * workspace: fl_attention_decode_workspace_bytes() bytes, 256-byte aligned, its first 4096 bytes
+ * zero-filled before first use; calls of any shape may follow one another with it, two calls that may overlap on the GPU need
  * one each. */
 FL_API int attention_decode(const void* Q, const void* k_pages, const void* v_pages, const float* k_page_scale,
                             const float* v_page_scale, const int32_t* page_table, const int32_t* seq_lens, void* O,

@@ -41,7 +41,8 @@ FP8_CACHE = dict(kps=A, vps=A, spitch=32, cache=2)
 @pytest.mark.parametrize("status,changes", [
     (INVALID, dict(T=-1)), (INVALID, dict(batch=-1)), (INVALID, dict(n_kv=-1)), (INVALID, dict(page=0)),
     (INVALID, dict(pages=-1)), (INVALID, dict(max_pages=-1)), (INVALID, dict(row=0)), (INVALID, dict(cache=3)),
-    (UNSUPPORTED, dict(head_dim=64)), (UNSUPPORTED, dict(row=2, ks=A, vs=A, lds=2)), (INVALID, dict(K=None)),
+    (UNSUPPORTED, dict(head_dim=64)),
+    (UNSUPPORTED, dict(n_kv=65537)), (UNSUPPORTED, dict(row=2, ks=A, vs=A, lds=2)), (INVALID, dict(K=None)),
     (INVALID, dict(V=None)), (INVALID, dict(kp=None)), (INVALID, dict(vp=None)), (INVALID, dict(table=None)),
     (INVALID, dict(lens=None)), (INVALID, dict(cu=None)), (INVALID, dict(ldkv=248)), (INVALID, dict(ldt=4)),
     (INVALID, dict(pitch=16 * 256 - 8)), (INVALID, dict(cache=2)), (INVALID, dict(FP8_CACHE, spitch=31)),
@@ -58,7 +59,8 @@ def test_append_checks(lib, status, changes):
     (INVALID, dict(batch=-1)), (INVALID, dict(heads=-1)), (INVALID, dict(n_kv=-2)), (INVALID, dict(page=0)),
     (INVALID, dict(pages=-1)), (INVALID, dict(max_pages=-1)), (INVALID, dict(cache=0)), (INVALID, dict(scale=F(0.0))),
     (INVALID, dict(scale=F(-1.0))), (INVALID, dict(scale=F(float("nan")))), (INVALID, dict(scale=F(float("inf")))),
-    (INVALID, dict(n_kv=0)), (INVALID, dict(n_kv=3)), (UNSUPPORTED, dict(head_dim=64)), (INVALID, dict(Q=None)),
+    (INVALID, dict(n_kv=0)), (INVALID, dict(n_kv=3)), (UNSUPPORTED, dict(head_dim=64)),
+    (UNSUPPORTED, dict(heads=131072)), (INVALID, dict(Q=None)),
     (INVALID, dict(O=None)), (INVALID, dict(kp=None)), (INVALID, dict(table=None)), (INVALID, dict(lens=None)),
     (INVALID, dict(ldq=1016)), (INVALID, dict(ldo=1016)), (INVALID, dict(ldt=4)), (INVALID, dict(pitch=4088)),
     (INVALID, dict(cache=2)), (INVALID, dict(FP8_CACHE, spitch=30)), (ALIGNMENT, dict(Q=P(0x10004))),
@@ -72,7 +74,7 @@ def test_decode_checks(lib, status, changes):
 @pytest.mark.parametrize("status,changes", [
     (INVALID, dict(M=-1)), (INVALID, dict(batch=-1)), (INVALID, dict(heads=-8)), (INVALID, dict(n_kv=-1)),
     (INVALID, dict(cu=None)), (INVALID, dict(kv=0)), (INVALID, dict(scale=F(0.0))), (INVALID, dict(n_kv=3)),
-    (INVALID, dict(n_kv=0)), (UNSUPPORTED, dict(head_dim=256)), (INVALID, dict(Q=None)), (INVALID, dict(K=None)),
+    (INVALID, dict(n_kv=0)), (UNSUPPORTED, dict(head_dim=256)), (UNSUPPORTED, dict(heads=131072)), (INVALID, dict(Q=None)), (INVALID, dict(K=None)),
     (INVALID, dict(V=None)), (INVALID, dict(O=None)), (INVALID, dict(kv=2)), (INVALID, dict(ldq=1016)),
     (INVALID, dict(ldo=1016)), (INVALID, dict(ldkv=248)), (INVALID, dict(kv=2, ks=A, vs=A, lds=1)),
     (ALIGNMENT, dict(Q=P(0x10008))), (ALIGNMENT, dict(ldkv=260)), (ALIGNMENT, dict(ldo=1028)),
