@@ -565,9 +565,9 @@ def fused_swiglu_bwd(dO, Wd, G, U, dGU=None, stream=None):
 HEAD_DIM = 128
 _BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 
-# The attention calls are made once per layer and token, so their checks are written for few Python steps:
-# a device is an index, pointers go to ctypes as plain integers, and the device is switched only where the
-# tensors are not on the current one.
+# The attention calls are made once per layer and token, so their checks are written for few Python steps: a device
+# is an index, pointers go to ctypes as plain integers, a contiguous tensor is asked for nothing further, and the
+# device is switched only where the tensors are not on the current one.
 
 
 def _addr(t):
@@ -578,26 +578,32 @@ def _on(dev, call, args, stream):
     """Runs call(*args, stream) on device `dev` (an index) and its current stream, or on the stream given."""
     if dev < 0:
         raise ValueError("expected CUDA tensors")
-    if stream is not None:
-        stream = stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+        return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     with torch.cuda.device(dev):
-        return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+        return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+
+
+def _pitch(a, b, rows, width, what):
+    """The shared leading dimension of two [rows, width] tensors with unit column stride."""
+    if a.is_contiguous() and b.is_contiguous():
+        return width
+    (ld, one), (ld_b, one_b) = a.stride(), b.stride()
+    if width > 1 and (one != 1 or one_b != 1) or rows > 1 and ld != ld_b:
+        raise ValueError(f"{what}: expected unit column stride and one shared pitch")
+    return ld if rows > 1 else width
 
 
 def _kv_pair(K, V, k_scale, v_scale, dev):
     """Checks K and V rows: bf16 without scales, or E4M3 bytes (uint8) with fp32 [rows, n_kv_heads] scales; returns
     (rows, width, leading dimension, that of the scales, type)."""
-    shape, dt, lds = K.shape, K.dtype, 0
-    if len(shape) != 2 or V.shape != shape or V.dtype != dt or K.get_device() != dev or V.get_device() != dev:
-        raise ValueError("K and V: expected two 2-D tensors of one shape and type on the call's device")
+    shape, dt = K.shape, K.dtype
+    if len(shape) != 2 or shape[1] % HEAD_DIM or V.shape != shape or V.dtype is not dt or V.get_device() != dev or \
+            K.get_device() != dev:
+        raise ValueError(f"K and V: expected two tensors [rows, n_kv_heads * {HEAD_DIM}] of one type on the call's "
+                         "device")
     rows, width = shape
-    (ld, one), sv = K.stride(), V.stride()
-    if width % HEAD_DIM or ((one != 1 or sv[1] != 1) and width > 1) or (rows > 1 and sv[0] != ld):
-        raise ValueError(f"K and V: expected [rows, n_kv_heads * {HEAD_DIM}] with unit column stride and one pitch")
-    if rows <= 1:
-        ld = width
+    ld = _pitch(K, V, rows, width, "K and V")
     if dt is _BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("bf16 rows have no scales")
@@ -605,14 +611,10 @@ def _kv_pair(K, V, k_scale, v_scale, dev):
     if dt is not _U8 or k_scale is None or v_scale is None:
         raise ValueError("K and V: expected bf16 rows, or uint8 (E4M3) rows with k_scale and v_scale")
     heads = width // HEAD_DIM
-    for t in (k_scale, v_scale):
-        if t.dtype is not _F32 or t.shape != (rows, heads) or t.get_device() != dev or \
-                (heads > 1 and t.stride(1) != 1):
-            raise ValueError("k_scale and v_scale: expected fp32 [rows, n_kv_heads] with unit column stride")
-    lds = k_scale.stride(0) if rows > 1 else heads
-    if rows > 1 and v_scale.stride(0) != lds:
-        raise ValueError("k_scale and v_scale must share one leading dimension")
-    return rows, width, ld, lds, FL_E4M3
+    if k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or k_scale.shape != (rows, heads) or \
+            v_scale.shape != (rows, heads) or k_scale.get_device() != dev or v_scale.get_device() != dev:
+        raise ValueError("k_scale and v_scale: expected fp32 [rows, n_kv_heads] on the call's device")
+    return rows, width, ld, _pitch(k_scale, v_scale, rows, heads, "k_scale and v_scale"), FL_E4M3
 
 
 def _ints(t, name, dev):
@@ -621,55 +623,69 @@ def _ints(t, name, dev):
     return t.numel()
 
 
+def _page_pitch(a, b, shape, per_page, what):
+    """The shared pitch of two page arrays whose pages are contiguous blocks of per_page elements."""
+    if a.is_contiguous() and b.is_contiguous():
+        return per_page
+    n, pitch = shape[0], a.stride(0) if shape[0] > 1 else per_page
+    inner, size = [], 1
+    for d in reversed(shape[1:]):
+        inner.insert(0, size)
+        size *= d
+    for t in (a, b):
+        if n and (t.stride()[1:] != tuple(inner) or (n > 1 and t.stride(0) != pitch)):
+            raise ValueError(f"{what}: expected contiguous pages with one shared pitch")
+    return pitch
+
+
 def _cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
     """Checks the paged cache; returns (batch, n_kv_heads, page_size, num_pages, max_pages, ldt, page_pitch,
     scale_pitch, type)."""
     shape, dt = k_pages.shape, k_pages.dtype
-    if len(shape) != 4 or shape[3] != HEAD_DIM or (dt is not _BF16 and dt is not _U8) or v_pages.shape != shape or \
-            v_pages.dtype is not dt or k_pages.get_device() != dev or v_pages.get_device() != dev:
-        raise ValueError(f"k_pages and v_pages: expected two bf16 or uint8 (E4M3) tensors [num_pages, n_kv_heads, "
-                         f"page_size, {HEAD_DIM}] on the call's device")
+    if len(shape) != 4 or shape[3] != HEAD_DIM or v_pages.shape != shape or v_pages.dtype is not dt or \
+            k_pages.get_device() != dev or v_pages.get_device() != dev:
+        raise ValueError(f"k_pages and v_pages: expected two tensors [num_pages, n_kv_heads, page_size, {HEAD_DIM}] "
+                         "of one type on the call's device")
     n_pages, n_kv, page, _ = shape
-    pitch = n_kv * page * HEAD_DIM
-    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
-        if n_pages > 1:
-            pitch = k_pages.stride(0)
-        for t in (k_pages, v_pages):
-            if n_pages and (t.stride()[1:] != (page * HEAD_DIM, HEAD_DIM, 1) or (n_pages > 1 and t.stride(0) != pitch)):
-                raise ValueError("k_pages and v_pages: expected contiguous pages with one shared pitch")
-    spitch = 0
+    pitch = _page_pitch(k_pages, v_pages, shape, n_kv * page * HEAD_DIM, "k_pages and v_pages")
+    spitch, kind = 0, FL_BF16
     if dt is _U8:
+        kind = FL_E4M3
         if ks is None or vs is None:
             raise ValueError("an E4M3 cache needs k_page_scale and v_page_scale")
-        spitch = n_kv * page if n_pages <= 1 or ks.is_contiguous() else ks.stride(0)
-        for t in (ks, vs):
-            if t.dtype is not _F32 or t.shape != shape[:3] or t.get_device() != dev or not (
-                    t.is_contiguous() and spitch == n_kv * page or
-                    t.stride()[1:] == (page, 1) and (n_pages <= 1 or t.stride(0) == spitch)):
-                raise ValueError("k_page_scale and v_page_scale: expected fp32 [num_pages, n_kv_heads, page_size] "
-                                 "with contiguous pages and one shared pitch")
+        if ks.dtype is not _F32 or vs.dtype is not _F32 or ks.shape != shape[:3] or vs.shape != shape[:3] or \
+                ks.get_device() != dev or vs.get_device() != dev:
+            raise ValueError("k_page_scale and v_page_scale: expected fp32 [num_pages, n_kv_heads, page_size] on the "
+                             "call's device")
+        spitch = _page_pitch(ks, vs, shape[:3], n_kv * page, "k_page_scale and v_page_scale")
+    elif dt is not _BF16:
+        raise ValueError("k_pages and v_pages: expected bf16 or uint8 (E4M3)")
     elif ks is not None or vs is not None:
         raise ValueError("a bf16 cache has no scales")
-    batch = _ints(seq_lens, "seq_lens", dev)
-    if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.get_device() != dev or \
-            page_table.shape[0] != batch:
+    batch, t_shape = _ints(seq_lens, "seq_lens", dev), page_table.shape
+    if page_table.dtype is not _I32 or len(t_shape) != 2 or t_shape[0] != batch or page_table.get_device() != dev:
         raise ValueError("page_table: expected int32 [batch, max_pages] on the call's device")
-    max_pages = page_table.shape[1]
-    ldt, one = page_table.stride()
-    if one != 1 and max_pages > 1:
-        raise ValueError("page_table: expected unit column stride")
-    return (batch, n_kv, page, n_pages, max_pages, ldt if batch > 1 else max_pages, pitch, spitch,
-            FL_E4M3 if dt is _U8 else FL_BF16)
+    ldt = max_pages = t_shape[1]
+    if not page_table.is_contiguous():
+        ldt, one = page_table.stride()
+        if one != 1 and max_pages > 1:
+            raise ValueError("page_table: expected unit column stride")
+        if batch <= 1:
+            ldt = max_pages
+    return batch, n_kv, page, n_pages, max_pages, ldt, pitch, spitch, kind
 
 
 def _query(t, name, dev):
     """Checks Q or O, bf16 [rows, n_heads * 128]; returns (rows, width, leading dimension)."""
-    if t.dtype is not _BF16 or t.dim() != 2 or t.get_device() != dev:
-        raise ValueError(f"{name}: expected a 2-D bf16 tensor on the call's device")
-    rows, width = t.shape
+    shape = t.shape
+    if t.dtype is not _BF16 or len(shape) != 2 or shape[1] % HEAD_DIM or t.get_device() != dev:
+        raise ValueError(f"{name}: expected bf16 [rows, n_heads * {HEAD_DIM}] on the call's device")
+    rows, width = shape
+    if t.is_contiguous():
+        return rows, width, width
     ld, one = t.stride()
-    if width % HEAD_DIM or (one != 1 and width > 1):
-        raise ValueError(f"{name}: expected [rows, n_heads * {HEAD_DIM}] with unit column stride")
+    if one != 1 and width > 1:
+        raise ValueError(f"{name}: expected unit column stride")
     return rows, width, ld if rows > 1 else width
 
 
