@@ -7,8 +7,8 @@
 // from issuing the next ones.
 //
 // Split.  The work is cut into units of 64 (bf16) or 128 (E4M3) tokens of one (sequence, kv head); every sequence has at least one.
-// CTA i of G takes units [i T / G, (i + 1) T / G) in the order (sequence, kv head, unit), so every CTA streams
-// the same number of bytes whatever the lengths are, and a captured launch adapts to them.  A (sequence, kv
+// The CTAs take runs of units in the order (sequence, kv head, unit) that differ by one unit at most, so every CTA
+// streams the same number of bytes whatever the lengths are, and a captured launch adapts to them.  A (sequence, kv
 // head) that lies in one CTA is finished there; one that is cut writes (m, l, o) of each piece to the workspace,
 // and the last CTA to arrive joins the pieces in the order of the CTAs (the result does not depend on which
 // came last).
@@ -51,6 +51,7 @@ struct DecodeParams {
   long long ldq, ldo;
   int group, chunks, chunk_heads;  // query heads of a kv head, cut into `chunks` of `chunk_heads` (<= 8 NT)
   int page_shift;                  // log2(page_size), -1 if it is no power of two
+  bool small;                      // batch <= 128 and no count can pass 31 bits
   float scale_log2;
   int* status;
   unsigned* counters;              // [kDecMaxCtas], by the first CTA of a cut (sequence, kv head)
@@ -146,42 +147,78 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
   griddep_wait();  // launched as a dependent: nothing is read before the kernel in front has finished
   griddep_launch_dependents();
 
-  // ---- plan: total units, and where this CTA's first unit lies
-  auto block_scan = [&](int b0, int& mine, long long& before) -> long long {  // of 128 sequences from b0
-    const int b = b0 + tid;
-    bool bad;
-    mine = b < p.c.batch ? decode_units<T::kUnit>(__ldg(p.c.lens + b), capacity, bad) : 0;
-    long long x = mine;
+  // ---- plan: total units, and where this CTA's first unit lies.  CTA i of G starts at unit i * share + min(i, more).
+  long long total = 0, share, more, u0, seg_first;  // seg_first: first unit of this (sequence, head) in the whole order
+  int G, tile;                                      // tile: the CTA's first unit, inside its (sequence, head)
+  DecodeSeg seg;
+  bool odd;
+  if (p.small) {  // at most 128 sequences, all counts in 32 bits: each warp finds its way alone, without a barrier
+    int len[4], mine[4], last[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(~0u, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) plan[warp] = x;
-    __syncthreads();
-    long long sum = 0;
-    before = x - mine;
+    for (int k = 0; k < 4; ++k) len[k] = k * 32 + lane < p.c.batch ? __ldg(p.c.lens + k * 32 + lane) : 0;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      if (w < warp) before += plan[w];
-      sum += plan[w];
+    for (int k = 0; k < 4; ++k)
+      last[k] = mine[k] = k * 32 + lane < p.c.batch ? decode_units<T::kUnit>(len[k], capacity, odd) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int y = __shfl_up_sync(~0u, last[k], o);
+        if (lane >= o) last[k] += y;
+      }
+    int sum[5] = {0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k + 1] = sum[k] + __shfl_sync(~0u, last[k], 31);
+    const unsigned all = static_cast<unsigned>(sum[4]) * heads_v;
+    G = static_cast<int>(min(gridDim.x, all));  // each has a unit at least
+    if (cta >= G) return;
+    const unsigned each = all / G, rest = all - each * G, first = each * cta + min(static_cast<unsigned>(cta), rest);
+    const int at = static_cast<int>(first / heads_v);
+    total = all, share = each, more = rest, u0 = first;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (at < sum[k] || at >= sum[k + 1]) continue;  // the same for all lanes
+      const int who = __ffs(__ballot_sync(~0u, at < sum[k] + last[k])) - 1;
+      const int n = __shfl_sync(~0u, mine[k], who), before = sum[k] + __shfl_sync(~0u, last[k], who) - n;
+      const int in = static_cast<int>(first - static_cast<unsigned>(before) * heads_v);
+      seg.b = k * 32 + who;
+      seg.len = __shfl_sync(~0u, len[k], who);
+      seg.h = in / n;
+      tile = in - seg.h * n;
     }
-    return sum;
-  };
-  int mine;
-  long long before, total = 0;
-  for (int b0 = 0; b0 < p.c.batch; b0 += kDecThreads) total += block_scan(b0, mine, before);
-  total *= heads_v;
-  const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // each has a unit at least
-  if (cta >= G) return;
-  const long long u0 = total * cta / G, u1 = total * (cta + 1) / G;
-  {
+  } else {
+    int mine;
+    long long before;
+    auto block_scan = [&](int b0) -> long long {  // of 128 sequences from b0
+      const int b = b0 + tid;
+      mine = b < p.c.batch ? decode_units<T::kUnit>(__ldg(p.c.lens + b), capacity, odd) : 0;
+      long long x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) plan[warp] = x;
+      __syncthreads();
+      long long sum = 0;
+      before = x - mine;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        if (w < warp) before += plan[w];
+        sum += plan[w];
+      }
+      return sum;
+    };
+    for (int b0 = 0; b0 < p.c.batch; b0 += kDecThreads) total += block_scan(b0);
+    total *= heads_v;
+    G = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    if (cta >= G) return;
+    share = total / G, more = total - share * G;
+    u0 = share * cta + min(static_cast<long long>(cta), more);
     long long base = 0;
     for (int b0 = 0;; b0 += kDecThreads) {
-      // one block of sequences: the scan above still stands
-      const long long sum = p.c.batch > kDecThreads ? block_scan(b0, mine, before) : total / heads_v;
-      const long long lo = (base + before) * heads_v;
+      const long long sum = block_scan(b0), lo = (base + before) * heads_v;
       if (mine > 0 && u0 >= lo && u0 < lo + static_cast<long long>(mine) * heads_v) {
         plan[8] = b0 + tid;
         plan[9] = u0 - lo;
@@ -190,7 +227,18 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
       if (base * heads_v > u0) break;
     }
     __syncthreads();
+    seg.b = static_cast<int>(plan[8]);
+    seg.len = __ldg(p.c.lens + seg.b);
+    const int n = decode_units<T::kUnit>(seg.len, capacity, odd);
+    seg.h = static_cast<int>(plan[9] / n);
+    tile = static_cast<int>(plan[9] - static_cast<long long>(seg.h) * n);
   }
+  const long long u1 = u0 + share + (cta < more ? 1 : 0);
+  seg_first = u0 - tile;
+  auto cta_of = [&](long long u) {  // the CTA that has unit u
+    const long long longer = more * (share + 1);
+    return static_cast<int>(u < longer ? u / (share + 1) : more + (u - longer) / share);
+  };
   long long left = u1 - u0;
   auto begin_seg = [&](DecodeSeg& s, int tile, long long units_left) {
     if (tile == 0 && s.h == 0) s.len = __ldg(p.c.lens + s.b);
@@ -207,19 +255,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
     }
     begin_seg(s, 0, units_left);
   };
-  DecodeSeg seg;
-  long long seg_first;  // first unit of this (sequence, head) in the whole order
-  {
-    seg.b = static_cast<int>(plan[8]);
-    const long long in = plan[9];
-    seg.len = __ldg(p.c.lens + seg.b);
-    bool bad;
-    const int n = decode_units<T::kUnit>(seg.len, capacity, bad);
-    seg.h = static_cast<int>(in / n);
-    const int tile = static_cast<int>(in - static_cast<long long>(seg.h) * n);
-    seg_first = u0 - tile;
-    begin_seg(seg, tile, left);
-  }
+  begin_seg(seg, tile, left);
 
   // ---- producer side of this warp's ring
   DecodeSeg ps = seg;
@@ -504,8 +540,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
     const bool whole = seg_first >= u0 && seg_first + seg.n_units <= u1;
     int c_first = cta, c_last = cta;  // the CTAs that share it
     if (!whole) {
-      c_first = static_cast<int>(((seg_first + 1) * G - 1) / total);
-      c_last = static_cast<int>(((seg_first + seg.n_units) * G - 1) / total);
+      if (seg_first < u0) c_first = cta_of(seg_first);
+      if (seg_first + seg.n_units > u1) c_last = cta_of(seg_first + seg.n_units - 1);
     }
     float* part = p.parts + (static_cast<long long>(cta) * 2 + (cta == c_first ? 1 : 0)) * kDecPartFloats;
     const bool spoiled = __any_sync(~0u, bad);

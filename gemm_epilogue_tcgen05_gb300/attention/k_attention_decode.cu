@@ -1,4 +1,7 @@
 // attention_decode: argument checks and launch (the kernel and its design: decode_attention_kernel.cuh).
+#include <algorithm>
+#include <cstdint>
+
 #include "decode_attention_kernel.cuh"
 
 namespace fl {
@@ -72,6 +75,9 @@ extern "C" int attention_decode(const void* Q, const void* k_pages, const void* 
   p.chunks = (p.group + 15) / 16;
   p.chunk_heads = (p.group + p.chunks - 1) / p.chunks;
   p.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(page_size)) : -1;
+  // units of all lengths that the table allows (64 tokens at least), for all heads
+  const int64_t longest = std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, INT32_MAX) / 64 + 1;
+  p.small = batch <= 128 && longest * batch < (int64_t{1} << 31) / (static_cast<int64_t>(n_kv_heads) * p.chunks);
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int*>(ws);
