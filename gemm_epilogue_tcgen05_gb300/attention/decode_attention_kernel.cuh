@@ -71,8 +71,8 @@ struct DecodeTraits {
   // 25.0 | 89.0 us.  Two column tiles need the registers of 3 CTAs.
   static constexpr int kCtas = !FP8 && NT == 1 ? 3 : 2;
   static constexpr int kStages = kCtas == 3 ? 2 : 3;
-  static constexpr int kMerge = kDecWarps * 4 * kHeadDim * 4;  // four heads at a time
-  static constexpr int kSmem = kDecWarps * kStages * kStage + kMerge + kDecWarps * 4 * 16 + 128;
+  static_assert(kStage >= NT * 8 * kHeadDim * 4, "a stage takes a warp's piece");
+  static constexpr int kSmem = kDecWarps * kStages * kStage + kDecWarps * NT * 8 * 16 + 128;
 };
 
 __device__ __forceinline__ float lg2(float x) {
@@ -136,14 +136,19 @@ template <bool FP8, int NT>
 __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) attention_decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = DecodeTraits<FP8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* merge = reinterpret_cast<float*>(smem + kDecWarps * T::kStages * T::kStage);
-  float4* stats = reinterpret_cast<float4*>(merge + T::kMerge / 4);  // [warp][4 heads]: m, m', l
-  long long* plan = reinterpret_cast<long long*>(stats + kDecWarps * 4);
+  float4* stats = reinterpret_cast<float4*>(smem + kDecWarps * T::kStages * T::kStage);  // [warp][head]: m, m', l, stage
+  long long* plan = reinterpret_cast<long long*>(stats + kDecWarps * NT * 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int heads_v = p.c.n_kv * p.chunks;  // independent (kv head, chunk) pairs of a sequence
   const long long capacity = static_cast<long long>(p.c.max_pages) * p.c.page_size;
   const int cta = blockIdx.x;
 
+  // Only hints go out before the kernel in front has finished: they bring the address translations (plan done after
+  // 1900 instead of 2400 cycles).  Planning on lengths that may be old and fetching the first keys with it was slower.
+  if (tid < p.c.batch) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.c.lens + tid));
+    if (p.c.max_pages > 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.c.table + tid * p.c.ldt));
+  }
   griddep_wait();  // launched as a dependent: nothing is read before the kernel in front has finished
   griddep_launch_dependents();
 
@@ -547,8 +552,10 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
     const bool spoiled = __any_sync(~0u, bad);
     if (spoiled && lane == 0 && atomicCAS(p.status + ST_CODE, 0, static_cast<int>(FL_ERR_INVALID_ARG)) == 0)
       p.status[ST_DETAIL] = seg.b;
+    // The ring always has a stage that is neither read nor on its way, the next to be filled: the warp's piece goes there.
     // o[nt][t][i]: head 2q + (i & 1), dimension 16 g + 2 t + (i >> 1) (E4M3), or for bf16 with t = 4 half + w
     // dimension 64 half + 8 g + 2 w + (i >> 1).  Chunks of 4 dimensions, permuted by q against bank conflicts.
+    const int own = (warp * T::kStages + p_stage) * T::kStage;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -556,7 +563,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
         float sum = l[nt][i];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        float* row = merge + (warp * 4 + q) * kHeadDim;
+        const int h = nt * 8 + 2 * q + i;
+        float* row = reinterpret_cast<float*>(smem + own) + h * kHeadDim;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int chunk4 = FP8 ? g * 4 + c : (c >> 1) * 16 + g * 2 + (c & 1);
@@ -564,36 +572,40 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
               make_float4(o[nt][c * 2][i], o[nt][c * 2][i + 2], o[nt][c * 2 + 1][i], o[nt][c * 2 + 1][i + 2]);
         }
         if (g == 0)
-          stats[warp * 4 + q] = make_float4(m[nt][i], FP8 ? mv[nt][i] - kDecLift : m[nt][i], spoiled ? NAN : sum, 0.f);
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int h = nt * 8 + 2 * j + i;
-          if (h >= n_heads) break;
-          float M = kDecNone, MV = kDecNone, L = 0.f, acc = 0.f;
-          float4 st[kDecWarps];
-#pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) {
-            st[w] = stats[w * 4 + j];
-            M = fmaxf(M, st[w].x);
-            MV = fmaxf(MV, st[w].y);
-          }
-          const int at = (((tid >> 2) ^ j) << 2) | (tid & 3);
-#pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) {
-            L += st[w].z * ex2(st[w].x - M);
-            acc += merge[(w * 4 + j) * kHeadDim + at] * ex2(st[w].y - MV);
-          }
-          if (whole) {
-            const float r = seg.len == 0 ? 0.f : acc * (ex2(MV - M) / L);
-            p.O[seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + tid] = __float2bfloat16_rn(r);
-          } else {
-            __stcg(part + h * kHeadDim + tid, acc);
-            if (tid == 0) __stcg(reinterpret_cast<float4*>(part + 16 * kHeadDim) + h, make_float4(M, MV, L, 0.f));
-          }
-        }
-        __syncthreads();
+          stats[warp * NT * 8 + h] = make_float4(m[nt][i], FP8 ? mv[nt][i] - kDecLift : m[nt][i], spoiled ? NAN : sum,
+                                                 __int_as_float(own));
       }
+    __syncthreads();
+    for (int h = warp; h < n_heads; h += kDecWarps) {  // a warp joins whole heads, a lane 4 dimensions
+      float4 st[kDecWarps], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float M = kDecNone, MV = kDecNone, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        st[w] = stats[w * NT * 8 + h];
+        M = fmaxf(M, st[w].x);
+        MV = fmaxf(MV, st[w].y);
+      }
+      const int at = h * kHeadDim + ((lane ^ ((h >> 1) & 3)) << 2);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + __float_as_int(st[w].w)) + at);
+        const float f = ex2(st[w].y - MV);
+        L += st[w].z * ex2(st[w].x - M);
+        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+      }
+      if (whole) {
+        const float r = ex2(MV - M) / L;
+        uint2 out;
+        out.x = pack_bf16x2(acc.x * r, acc.y * r);
+        out.y = pack_bf16x2(acc.z * r, acc.w * r);
+        if (seg.len == 0) out = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(p.O + seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + lane * 4) = out;
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + h * kHeadDim) + lane, acc);
+        if (lane == 0) __stcg(reinterpret_cast<float4*>(part + 16 * kHeadDim) + h, make_float4(M, MV, L, 0.f));
+      }
+    }
+    __syncthreads();
     if (!whole) {  // at most two of a CTA's segments are cut: its first and its last
       if (cta == c_first) cut_b[1] = seg.b, cut_h[1] = seg.h, cut_first[1] = c_first, cut_last[1] = c_last;
       else cut_b[0] = seg.b, cut_h[0] = seg.h, cut_first[0] = c_first, cut_last[0] = c_last;
