@@ -618,9 +618,9 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
 
   // ---- pieces of cut (sequence, head) pairs: the CTA that arrives last joins them
   if (cut_first[0] < 0 && cut_first[1] < 0) return;
-  __threadfence();
   __syncthreads();
   if (tid < 2) {
+    __threadfence();  // for the whole CTA: the others' stores are behind the barrier
     plan[tid] = 0;
     const int first = tid == 0 ? cut_first[0] : cut_first[1], last = tid == 0 ? cut_last[0] : cut_last[1];
     if (first >= 0 && atomicAdd(p.counters + first, 1u) == static_cast<unsigned>(last - first)) {
@@ -645,6 +645,15 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
         const int n = min(32, c_last - c0 + 1);
         float4 st = make_float4(kDecNone, kDecNone, 0.f, 0.f);
         if (lane < n) st = __ldcg(reinterpret_cast<const float4*>(src(c0 + lane) + 16 * kHeadDim) + h);
+        float4 v[8];
+        auto fetch = [&](int i0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(src(c0 + i0 + i) + h * kHeadDim) + lane);
+          }
+        };
+        fetch(0);  // before their weights are known
         float nm = fmaxf(M, st.x), nmv = fmaxf(MV, st.y);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
@@ -660,12 +669,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
         M = nm;
         MV = nmv;
         for (int i0 = 0; i0 < n; i0 += 8) {
-          float4 v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(src(c0 + i0 + i) + h * kHeadDim) + lane);
-          }
+          if (i0 > 0) fetch(i0);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float wi = __shfl_sync(~0u, w, i0 + i);
