@@ -31,13 +31,10 @@
 // Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
 //
-// E4M3: a first kernel turns codes times scales into fp16, for each key tile of a sequence and head with the powers of
-// two 2^-a (K) and 2^-b (V) that bring its largest possible value to [2^12, 2^14): 11 bits for all that is above
-// 2^-26 of it, where scales applied here would cost two multiplications for each (query, key) and shared-memory reads
-// that the tensor cores need for themselves (146 us for 4 x 2048 tokens, 32 query and 8 kv heads; 125 us so).  The queries become
-// fp16 in place, each row with a power of two of its own (8-bit values in 11 bits: exact down to 2^-28 of the row's
-// largest).  2^a joins the factor of the logits; V's tiles meet in O at the common power 2^E: weights are
-// 2^(x - m + 7 + b - E) in fp16, at most 2^15, and E rises with a rescale like m.
+// E4M3: a first kernel writes codes times scales as bf16, 8 bits where the codes carry 4.  Measured for 4 x 2048
+// tokens, 32 query and 8 kv heads: 311 us with the scales in the softmax (two multiplications and two shared-memory
+// reads for each query and key, reads that the tensor cores need for themselves), 123 us with fp16 products (11 bits,
+// but powers of two for each key tile against fp16's range, and queries that become fp16, too); 109 us so.
 #pragma once
 #include <climits>
 
@@ -56,12 +53,11 @@ constexpr int kPreRing = 3;                        // tile descriptors
 constexpr float kPreNone = -3e38f;                 // a maximum over nothing: any finite logit passes it
 constexpr float kPreLazy = 8.f;
 constexpr uint64_t kPreDrainNs = 1000000000;       // for copies and products in flight, whatever the limit of the waits
-constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted by 2^7 in fp16
 
 // Where a wait gave up (recorded in the workspace's status record).
 enum : int {
   W_PRE_TILE_FULL = 20, W_PRE_TILE_EMPTY = 21, W_PRE_Q_EMPTY = 22, W_PRE_Q_FULL = 23, W_PRE_KV_EMPTY = 24,
-  W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29, W_PRE_Q_READY = 30
+  W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29
 };
 
 struct alignas(128) PrefillParams {
@@ -70,8 +66,6 @@ struct alignas(128) PrefillParams {
   CUtensorMap map_v;
   const __nv_bfloat16* V;  // the rows map_v covers
   long long ldv;
-  const float2* powers;  // E4M3: [first row of a key tile][n_kv]: 2^a of K, b of V
-  int n_kv;
   const int* cu;
   __nv_bfloat16* O;
   long long ldo;
@@ -85,7 +79,6 @@ struct alignas(128) PrefillParams {
   unsigned long long timeout_ns;
 };
 
-template <bool FP8>
 struct PrefillTraits {
   static constexpr int kStages = 2;  // of a V tile and the next K tile, 64 KB
   static constexpr int kBars = 1024;
@@ -110,7 +103,6 @@ struct PrefillBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[2], kv_empty[2], v_ok[2];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_ready[2];  // E4M3: the queries are fp16
   uint64_t drain;
   PrefillTile tile[kPreRing];
   int abort_flag;
@@ -194,21 +186,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 // Two values times zero, plus c: NaN for one that is not finite.
-template <bool F16>
 __device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t c) {
   uint32_t r;
-  if (F16) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
-  else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
   return r;
 }
 // Two fp32 lanes in one 64-bit register.
@@ -236,9 +216,8 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <bool FP8>
 __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const __grid_constant__ PrefillParams p) {
-  using T = PrefillTraits<FP8>;
+  using T = PrefillTraits;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_smem = smem_u32(smem), kv_smem = q_smem + 2 * kPreTileBytes;
@@ -252,7 +231,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.q_ready[i], 4);
     }
     for (int i = 0; i < T::kStages; ++i)
       mbar_init(&bar.kv_full[i], 1), mbar_init(&bar.kv_empty[i], 2), mbar_init(&bar.v_ok[i], 1);
@@ -449,9 +427,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   } else if (warp == 8) {
     // ================================================================ MMA issue
     // The whole warp walks the loop, so that descriptors stay in uniform registers, and one elected lane issues.
-    constexpr uint32_t kTypes = FP8 ? (1u << 7) | (1u << 10) : 0u;  // of A and B: bf16, or without these bits fp16
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile) & ~kTypes,
-                       idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true) & ~kTypes;
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile), idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true);
     constexpr uint32_t kStep16 = kPreTileBytes / 16;  // one tile in descriptor units
     const bool one = elect_one();
     const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem + kPreTileBytes),
@@ -467,7 +443,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       ++uses;
     };
     auto q_wait = [&](int s) {
-      wait(FP8 ? &bar.q_ready[s] : &bar.q_full[s], (q_phase >> s) & 1, FP8 ? W_PRE_Q_READY : W_PRE_Q_FULL);
+      wait(&bar.q_full[s], (q_phase >> s) & 1, W_PRE_Q_FULL);
       q_phase ^= 1u << s;
     };
     auto p_wait = [&](int s) {
@@ -595,14 +571,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll 8
         for (int c = 0; c < kPreTileBytes / 512; ++c) {
           const uint4 w = ld_shared_v4(base + c * 512);
-          seen[0] = times_zero<FP8>(w.x, seen[0]), seen[1] = times_zero<FP8>(w.y, seen[1]);
-          seen[2] = times_zero<FP8>(w.z, seen[2]), seen[3] = times_zero<FP8>(w.w, seen[3]);
+          seen[0] = times_zero(w.x, seen[0]), seen[1] = times_zero(w.y, seen[1]);
+          seen[2] = times_zero(w.z, seen[2]), seen[3] = times_zero(w.w, seen[3]);
         }
         if (__any_sync(~0u, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7FFF7FFFu) != 0)) {
           int lo = INT_MAX, hi = -1;
           bool bad_chunk = false;
           auto clean = [&](uint32_t w) {  // an exponent of all ones carries into the sign's place
-            constexpr uint32_t kExp = FP8 ? 0x7C007C00u : 0x7F807F80u, kOne = FP8 ? 0x04000400u : 0x00800080u;
+            constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
             const uint32_t bad = ((w & kExp) + kOne) & 0x80008000u;
             bad_chunk |= bad != 0;
             return w & ~((bad >> 15) * 0xFFFFu);
@@ -638,37 +614,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const uint32_t hp_inverse = 65536u / p.hp + 1;  // row / hp = row * hp_inverse >> 16 for rows below 128
     const int row_tok = row / p.hp;
     const float c = p.scale_log2;
-    int q_uses = 0;
-    float q_factor = c;  // of this row's logits
-    // E4M3: the queries of a tile to fp16, each row times the power of two that takes its largest value to [2^14, 2^15)
-    auto convert_queries = [&](const PrefillTile& t) -> bool {
-      if ((s ? t.n1 : t.n0) == 0) return true;
-      if (!warp_wait(&bar.q_full[s], q_uses & 1, wc, W_PRE_Q_FULL)) return false;
-      ++q_uses;
-      const uint32_t at = q_smem + s * kPreTileBytes + row * 128;
-      uint4 v[16];
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        v[j] = ld_shared_v4(at + (j >> 3) * (kPreTileBytes / 2) + (((j & 7) ^ (row & 7)) << 4));
-        top = bf16x2_max(top, bf16x2_max(bf16x2_max(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
-                                         bf16x2_max(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
-      }
-      const int ex = static_cast<int>(max(top >> 16, top & 0xFFFFu) >> 7);
-      const int up = ex == 255 ? 127 : min(max(268 - ex, 1), 253);
-      const float lift = __uint_as_float(static_cast<uint32_t>(up) << 23);
-      q_factor = c * __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        auto half2 = [&](uint32_t w) { return pack_f16x2(bf16_lo(w) * lift, bf16_hi(w) * lift); };
-        st_shared_v4(at + (j >> 3) * (kPreTileBytes / 2) + (((j & 7) ^ (row & 7)) << 4), half2(v[j].x), half2(v[j].y),
-                     half2(v[j].z), half2(v[j].w));
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.q_ready[s]);
-      return true;
-    };
     int s_uses = 0, o_uses = 0;
     bool ok = true;
     PrefillTile t = {}, next;
@@ -678,18 +623,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int clear = p.causal ? first : t.len - 1;              // last key that every row sees
       float m = kPreNone, l = 0.f;
-      const float my_factor = q_factor;
-      float E = 0.f;
-      float2 power = make_float2(1.f, 0.f);  // E4M3: 2^a and b of this step's key tile
-      const float2* powers = p.powers + static_cast<long long>(t.row0) * p.n_kv + t.kvh;
-      if (FP8 && n > 0) {
-        power = __ldg(powers);
-        E = power.y + 2.f;
-      }
       for (int i = 0; i < n; ++i) {
-          float2 power_next = power;
-          if (FP8 && i + 1 < n) power_next = __ldg(powers + static_cast<long long>(i + 1) * kPreTile * p.n_kv);
-          const float f = FP8 ? my_factor * power.x : c;
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
@@ -713,17 +647,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               mx[h] = max3(mx[h], __uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1]));
 #pragma unroll
           for (int h = 0; h < 4; ++h) mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           const bool rise = top > m + kPreLazy;
-          if (__any_sync(~0u, rise) || (FP8 && power.y > E)) {
+          if (__any_sync(~0u, rise)) {
             const float up = rise ? top : m;
-            float down = ex2(m - up);
+            const float down = ex2(m - up);
             m = up;
             l *= down;
-            if (FP8 && power.y > E) {
-              down *= ex2(E - power.y - 2.f);
-              E = power.y + 2.f;
-            }
             if (i > 0) {  // O of the key tiles before is complete: S of this one was committed behind it
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -736,8 +666,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               }
             }
           }
-          const float lift = FP8 ? kPreLift + power.y - E : 0.f;  // weights are larger by 2^lift
-          const uint64_t f2f = f2(f, f), m2 = f2(lift - m, lift - m);
+          const uint64_t c2 = f2(c, c), m2 = f2(-m, -m);
           uint64_t l0 = 0, l1 = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -745,29 +674,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll
             for (int h = 0; h < 16; h += 2) {
               float a, b, d, e;
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), f2f, m2), a, b);
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), f2f, m2), d, e);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), c2, m2), a, b);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m2), d, e);
               a = ex2(a), b = ex2(b), d = ex2(d), e = ex2(e);
               l0 = f2_add(l0, f2(a, b)), l1 = f2_add(l1, f2(d, e));
-              w[h] = FP8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-              w[h + 1] = FP8 ? pack_f16x2(d, e) : pack_bf16x2(d, e);
+              w[h] = pack_bf16x2(a, b);
+              w[h + 1] = pack_bf16x2(d, e);
             }
             tmem_st16(s_tmem + j * 16, w);
           }
           float a, b, d, e;
           f2_split(l0, a, b);
           f2_split(l1, d, e);
-          l += FP8 ? ((a + b) + (d + e)) * ex2(-lift) : (a + b) + (d + e);
+          l += (a + b) + (d + e);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.p_full[s]);
-          power = power_next;
       }
       if (!ok) break;
       const bool have = __all_sync(~0u, get_tile(k + 1, next));
-      if (FP8 && have && !(ok = convert_queries(next))) break;  // before the output: the products behind it wait for them
-      const float inv = (FP8 ? ex2(E - kPreLift) : 1.f) / l;
+      const float inv = 1.f / l;
       if (n > 0) {
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
@@ -829,8 +756,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             float sum = 0.f;
 #pragma unroll 1
             for (int pos = bad_lo; pos <= min(bad_hi, lim); ++pos) {
-              const __nv_bfloat16 raw = v[static_cast<long long>(pos) * p.ldv + d];
-              const float y = FP8 ? __half2float(__ushort_as_half(__bfloat16_as_ushort(raw))) : __bfloat162float(raw);
+              const float y = __bfloat162float(v[static_cast<long long>(pos) * p.ldv + d]);
               if (!isfinite(y)) sum += y;
             }
             if (!isfinite(sum)) mine[d] = __float2bfloat16_rn(sum);
@@ -850,89 +776,54 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   if (threadIdx.x == 0 && bar.abort_flag != 0) record_failure(p.status, bar.abort_flag, 0);
 }
 
-// E4M3 codes and scales of K and V to fp16 for the kernel above.  One CTA takes a key tile (128 rows of a sequence,
-// from its first) of one kv head: the largest finite scale among them gives 2^a (K) or b (V), then each 16 codes of a
-// thread become code * (scale * 2^-a).  Bound by memory: 2 bytes in and 4 out for each K and V value.
-__global__ void __launch_bounds__(256) e4m3_tiles_to_f16_kernel(const uint8_t* K, const uint8_t* V, const float* ks,
-                                                               const float* vs, long long ld, long long lds, const int* cu,
-                                                               int batch, int seq_len, int M, int n_kv, __half* K16,
-                                                               __half* V16, float2* powers) {
+// E4M3 codes of K and V times their scales as bf16, for the kernel above.  Bound by memory: 1 byte in and 2 out for
+// each value, so nothing but independent loads: a CTA takes whole rows, a thread 16 codes at a time, eight loads of
+// codes on their way before the first is used.  Rows that lie behind every sequence are left out.
+constexpr int kCodesAtOnce = 1024;  // 16-byte pieces of a CTA's rows that are on their way together
+
+__global__ void __launch_bounds__(256) e4m3_rows_to_bf16_kernel(const uint8_t* K, const uint8_t* V, const float* ks,
+                                                                const float* vs, long long ld, long long lds,
+                                                                const int* cu, int batch, int M, int n_kv, int rows,
+                                                                __nv_bfloat16* K16, __nv_bfloat16* V16) {
+  const int tid = threadIdx.x, row0 = static_cast<int>(blockIdx.x) * rows;
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int found[2];  // first row and rows of this tile
-  __shared__ uint32_t top[2];
-  const int tid = threadIdx.x, lane = tid & 31, kvh = blockIdx.y;
-  if (tid == 0) found[1] = 0;
-  if (tid < 2) top[tid] = 0;
-  __syncthreads();
-  if (tid < 32) {  // the sequence that holds key tile blockIdx.x
-    int skip = static_cast<int>(blockIdx.x);
-    for (int b0 = 0; b0 < batch; b0 += 32) {
-      int first = 0, last = 0;
-      if (b0 + lane < batch) sequence_rows(cu, b0 + lane, seq_len, M, first, last);
-      const int have = last > first ? (last - first - 1) / kPreTile + 1 : 0;
-      int sum = have;
+  if (cu != nullptr) {
+    bool used = false;
+    for (int i = 1 + tid; i <= batch; i += 256) used |= cu[i] > row0;
+    if (!__syncthreads_or(used)) return;
+  }
+  const int per_row = n_kv * (kHeadDim / 16), pieces = min(rows, M - row0) * per_row;
+  for (int at = tid; at < pieces; at += kCodesAtOnce) {
+    uint4 codes[8];  // of four places K, then V
+    float scale[8];
+    long long to[4];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const unsigned who = __ballot_sync(~0u, sum > skip);
-      if (who != 0) {
-        if (lane == __ffs(who) - 1) {
-          found[0] = first + (skip - (sum - have)) * kPreTile;
-          found[1] = min(kPreTile, last - found[0]);
-        }
-        break;
-      }
-      skip -= __shfl_sync(~0u, sum, 31);
+    for (int i = 0; i < 4; ++i) {
+      const int piece = min(at + i * 256, pieces - 1), r = piece / per_row, c = piece - r * per_row;
+      const long long row = row0 + r;
+      to[i] = row * per_row + c;
+      codes[i] = __ldg(reinterpret_cast<const uint4*>(K + row * ld) + c);
+      codes[i + 4] = __ldg(reinterpret_cast<const uint4*>(V + row * ld) + c);
+      scale[i] = __ldg(ks + row * lds + c / (kHeadDim / 16));
+      scale[i + 4] = __ldg(vs + row * lds + c / (kHeadDim / 16));
     }
-  }
-  __syncthreads();
-  const int row0 = found[0], rows = found[1];
-  if (rows == 0) return;
-  uint4 codes[8];  // 32 rows at a time, 8 threads a row; K first, then V; on their way while the scales are compared
-  float scale[8];
-  const int c = (tid & 7) * 16;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = min((i & 3) * 32 + (tid >> 3), rows - 1);
-    codes[i] = __ldg(reinterpret_cast<const uint4*>((i >= 4 ? V : K) + (row0 + r) * ld + kvh * kHeadDim + c));
-    scale[i] = __ldg((i >= 4 ? vs : ks) + (row0 + r) * lds + kvh);
-  }
-  {  // threads 0 .. 127 the scales of K, 128 .. 255 those of V
-    const int r = tid & 127;
-    float x = r < rows ? fabsf((tid < 128 ? ks : vs)[static_cast<long long>(row0 + r) * lds + kvh]) : 0.f;
-    const uint32_t bits = __reduce_max_sync(~0u, x < INFINITY ? __float_as_uint(x) : 0u);
-    if (lane == 0) atomicMax(&top[tid >> 7], bits);
-  }
-  __syncthreads();
-  int e[2];  // 448 * scale * 2^-e is below 2^14
+    for (int i = 0; i < 8; ++i) {
+      if (at + (i & 3) * 256 >= pieces) continue;
+      const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+      uint32_t out[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) e[i] = top[i] == 0 ? 0 : min(max(static_cast<int>(top[i] >> 23) - 127 - 4, -120), 120);
-  if (tid == 0)
-    powers[static_cast<long long>(row0) * n_kv + kvh] =
-        make_float2(__uint_as_float(static_cast<uint32_t>(127 + e[0]) << 23), static_cast<float>(e[1]));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool second = i >= 4;
-    const int r = (i & 3) * 32 + (tid >> 3);
-    if (r >= rows) continue;
-    const long long row = row0 + r;
-    const float s = scale[i] * __uint_as_float(static_cast<uint32_t>(127 - e[second ? 1 : 0]) << 23);
-    const uint4 w = codes[i];
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t out[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(in[k >> 1] >> ((k & 1) * 16))));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      out[k] = pack_f16x2(f.x * s, f.y * s);
+      for (int k = 0; k < 8; ++k) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(in[k >> 1] >> ((k & 1) * 16))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        out[k] = pack_bf16x2(f.x * scale[i], f.y * scale[i]);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(i < 4 ? K16 : V16) + to[i & 3] * 2;
+      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
-    uint4* dst = reinterpret_cast<uint4*>((second ? V16 : K16) + (row * n_kv + kvh) * kHeadDim + c);
-    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }
 }
 

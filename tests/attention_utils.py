@@ -5,15 +5,14 @@ Notation: p_j = exp(x_j - max x), x_j = scale q.k_j, o = sum p_j v_j / sum p_j, 
 
 - The output is rounded to bf16 once: 2^-8 |o|.
 - Prefill rounds each weight p_j to bf16 for the tensor cores: each term moves by at most 2^-8 of itself, so o by
-  at most 2^-8 A.  With E4M3 keys and values it works in fp16 instead: weights and scaled values are each rounded
-  by at most 2^-11 (2^-10 A together), scaled keys too, which moves a logit by at most 2^-11 scale sum_d |q_d k_d|.
-  (fp16's range: values below 2^-26 of a key tile's largest, or weights below 2^-21, lose less than 2^-38 of the
-  largest.)  Decode rounds the weights to fp16 (E4M3 cache) or splits them into
-  two bf16 values (bf16 cache): 2^-11 A covers both (2^-16 for the split).
+  at most 2^-8 A.  Scaled E4M3 keys and values are rounded to bf16 first: held against the definition with these
+  rounded values the bound is the same; against the exact ones each value moves by 2^-8 of itself (another 2^-8 A)
+  and a logit by at most 2^-8 scale sum_d |q_d k_d|.  Decode rounds the weights to fp16 (E4M3 cache) or splits them
+  into two bf16 values (bf16 cache): 2^-11 A covers both (2^-16 for the split).
 - A logit is a sum of 128 exact products in fp32: |dx| <= 130 * 2^-24 * scale sum_d |q_d k_d| (the
   accumulation, the scaling and the multiplication by log2 e), plus 2^-21 for exp2 itself and 2^-24 |x_j - max|
-  for the rounding of its argument (|x_j - max| p_j < 1 for every j, so 2^-24 of the whole).  A relative error
-  d of every p_j moves o by at most 2 d A (numerator and denominator).
+  for the rounding of its argument (|x_j - max| p_j < 1 for every j, so 2^-24 of the whole).  Logits that move by
+  at most d move every p_j / sum p_j by a factor within exp(+-2d), so o by at most (exp(2d) - 1) A.
 - fp32 sums over n keys: n 2^-24 relative at most in each of numerator and denominator, 2 n 2^-24 A.
 """
 import torch
@@ -39,6 +38,11 @@ def values(codes, scale=None):
     return codes.view(torch.float8_e4m3fn).double() * scale.double()[..., None]
 
 
+def rounded(x):
+    """To bf16 by way of fp32, as the kernel does (a code times an fp32 scale is rounded to fp32 on the way)."""
+    return x.float().bfloat16().double()
+
+
 def attend(q, k, v, scale, weight_step, causal=False, key_step=0.0):
     """q [heads, n, 128]; k, v [kv heads, tokens, 128] (fp64).  Returns (o, tolerance), both [heads, n, 128]."""
     g = q.shape[0] // k.shape[0]
@@ -54,7 +58,7 @@ def attend(q, k, v, scale, weight_step, causal=False, key_step=0.0):
     p = torch.softmax(x, -1)
     o, a = p @ v, p @ v.abs()
     d = (130 * F32 + key_step) * mag.amax(-1, keepdim=True) + 2.0 ** -21 + F32
-    tol = BF16 * o.abs() + (weight_step + 2 * d + 2 * tokens * F32) * a
+    tol = BF16 * o.abs() + (weight_step + torch.expm1(2 * d) + 2 * tokens * F32) * a
     return o, tol * (1 + 2 * BF16) + 1e-30  # products of two of the errors
 
 
@@ -141,9 +145,13 @@ def check_prefill(q, k, v, ks, vs, lens, out, causal, scale=D ** -0.5, what=""):
             continue
         kk = values(k[rows].reshape(n, kv, D), None if ks is None else ks[rows]).transpose(0, 1)
         vv = values(v[rows].reshape(n, kv, D), None if vs is None else vs[rows]).transpose(0, 1)
-        steps = (BF16, causal) if ks is None else (2 * F16, causal, F16)
-        ref, tol = attend(q[rows].double().reshape(n, heads, D).transpose(0, 1), kk, vv, scale, *steps)
-        assert_within(out[rows].view(n, heads, D).transpose(0, 1), ref, tol, f"{what} sequence {b} of {n}")
+        qq, got = q[rows].double().reshape(n, heads, D).transpose(0, 1), out[rows].view(n, heads, D).transpose(0, 1)
+        if ks is not None:
+            ref, tol = attend(qq, kk, vv, scale, 2 * BF16, causal, BF16)
+            assert_within(got, ref, tol, f"{what} sequence {b} of {n}")
+            kk, vv = rounded(kk), rounded(vv)
+        ref, tol = attend(qq, kk, vv, scale, BF16, causal)
+        assert_within(got, ref, tol, f"{what} sequence {b} of {n}")
 
 
 def cu(lens):
