@@ -150,8 +150,9 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   p.work = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);
   p.timeout_ns = wait_timeout_ns();
   if (fp8) {
-    const int rows = std::max(kCodesAtOnce / (n_kv_heads * (kHeadDim / 16)), 1);  // of a CTA
-    if (!launch_dependent(e4m3_rows_to_bf16_kernel, dim3((M - 1) / rows + 1), 256, 0, s, static_cast<const uint8_t*>(K),
+    const int rows = std::max(kCodesAtOnce / (n_kv_heads * (kHeadDim / 8)), 1);  // of a CTA
+    const int grid = std::min((M - 1) / rows + 1, kCodesCtas * di.num_sms);
+    if (!launch_dependent(e4m3_rows_to_bf16_kernel, dim3(grid), 256, 0, s, static_cast<const uint8_t*>(K),
                           static_cast<const uint8_t*>(V), k_scale, v_scale, static_cast<long long>(ldkv),
                           static_cast<long long>(lds), cu_seqlens, p.batch, M, n_kv_heads, rows,
                           static_cast<__nv_bfloat16*>(const_cast<void*>(k16)),

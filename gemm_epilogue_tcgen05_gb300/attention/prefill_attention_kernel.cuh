@@ -34,7 +34,7 @@
 // E4M3: a first kernel writes codes times scales as bf16, 8 bits where the codes carry 4.  Measured for 4 x 2048
 // tokens, 32 query and 8 kv heads: 311 us with the scales in the softmax (two multiplications and two shared-memory
 // reads for each query and key, reads that the tensor cores need for themselves), 123 us with fp16 products (11 bits,
-// but powers of two for each key tile against fp16's range, and queries that become fp16, too); 109 us so.
+// but powers of two for each key tile against fp16's range, and queries that become fp16, too); 107 us so.
 #pragma once
 #include <climits>
 
@@ -777,52 +777,62 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 }
 
 // E4M3 codes of K and V times their scales as bf16, for the kernel above.  Bound by memory: 1 byte in and 2 out for
-// each value, so nothing but independent loads: a CTA takes whole rows, a thread 16 codes at a time, eight loads of
-// codes on their way before the first is used.  Rows that lie behind every sequence are left out.
-constexpr int kCodesAtOnce = 1024;  // 16-byte pieces of a CTA's rows that are on their way together
+// each value.  A CTA takes whole rows, a thread 8 codes at a time (16 bytes out; with 16 codes each
+// store left half sectors to the next one, 2 us more for 12400 rows of 8 heads), eight loads of codes on their way before
+// the first is used.  Rows that lie behind every sequence are left out.
+constexpr int kCodesAtOnce = 1024;  // 8-byte pieces of a CTA's rows, of K and V each, that are on their way together
+constexpr int kCodesCtas = 4;       // on an SM
 
-__global__ void __launch_bounds__(256) e4m3_rows_to_bf16_kernel(const uint8_t* K, const uint8_t* V, const float* ks,
-                                                                const float* vs, long long ld, long long lds,
-                                                                const int* cu, int batch, int M, int n_kv, int rows,
-                                                                __nv_bfloat16* K16, __nv_bfloat16* V16) {
-  const int tid = threadIdx.x, row0 = static_cast<int>(blockIdx.x) * rows;
+__global__ void __launch_bounds__(256, kCodesCtas) e4m3_rows_to_bf16_kernel(
+    const uint8_t* K, const uint8_t* V, const float* ks, const float* vs, long long ld, long long lds, const int* cu,
+    int batch, int M, int n_kv, int rows, __nv_bfloat16* K16, __nv_bfloat16* V16) {
+  __shared__ int top;
+  const int tid = threadIdx.x;
+  if (tid == 0) top = 0;
+  if (cu != nullptr && tid <= batch) asm volatile("prefetch.global.L2 [%0];" ::"l"(cu + tid));
   griddep_wait();
   griddep_launch_dependents();
+  int end = M;
   if (cu != nullptr) {
-    bool used = false;
-    for (int i = 1 + tid; i <= batch; i += 256) used |= cu[i] > row0;
-    if (!__syncthreads_or(used)) return;
+    int x = 0;
+    for (int i = 1 + tid; i <= batch; i += 256) x = max(x, cu[i]);
+    x = __reduce_max_sync(~0u, x);
+    __syncthreads();
+    if ((tid & 31) == 0 && x > 0) atomicMax(&top, x);
+    __syncthreads();
+    end = min(top, M);
   }
-  const int per_row = n_kv * (kHeadDim / 16), pieces = min(rows, M - row0) * per_row;
-  for (int at = tid; at < pieces; at += kCodesAtOnce) {
-    uint4 codes[8];  // of four places K, then V
-    float scale[8];
-    long long to[4];
+  const int per_row = n_kv * (kHeadDim / 8);
+  for (long long row0 = static_cast<long long>(blockIdx.x) * rows; row0 < end; row0 += static_cast<long long>(gridDim.x) * rows) {
+    const int pieces = static_cast<int>(min(static_cast<long long>(rows), end - row0)) * per_row;
+    for (int at = tid; at < pieces; at += kCodesAtOnce) {
+      uint2 codes[8];  // of four places K, then V
+      float scale[8];
+      long long to[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int piece = min(at + i * 256, pieces - 1), r = piece / per_row, c = piece - r * per_row;
-      const long long row = row0 + r;
-      to[i] = row * per_row + c;
-      codes[i] = __ldg(reinterpret_cast<const uint4*>(K + row * ld) + c);
-      codes[i + 4] = __ldg(reinterpret_cast<const uint4*>(V + row * ld) + c);
-      scale[i] = __ldg(ks + row * lds + c / (kHeadDim / 16));
-      scale[i + 4] = __ldg(vs + row * lds + c / (kHeadDim / 16));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (at + (i & 3) * 256 >= pieces) continue;
-      const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-      uint32_t out[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(in[k >> 1] >> ((k & 1) * 16))));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        out[k] = pack_bf16x2(f.x * scale[i], f.y * scale[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int piece = min(at + i * 256, pieces - 1), r = piece / per_row, c = piece - r * per_row;
+        const long long row = row0 + r;
+        to[i] = row * per_row + c;
+        codes[i] = __ldg(reinterpret_cast<const uint2*>(K + row * ld) + c);
+        codes[i + 4] = __ldg(reinterpret_cast<const uint2*>(V + row * ld) + c);
+        scale[i] = __ldg(ks + row * lds + c / (kHeadDim / 8));
+        scale[i + 4] = __ldg(vs + row * lds + c / (kHeadDim / 8));
       }
-      uint4* dst = reinterpret_cast<uint4*>(i < 4 ? K16 : V16) + to[i & 3] * 2;
-      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (at + (i & 3) * 256 >= pieces) continue;
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t two = (k < 2 ? codes[i].x : codes[i].y) >> ((k & 1) * 16);
+          uint32_t h;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          out[k] = pack_bf16x2(f.x * scale[i], f.y * scale[i]);
+        }
+        reinterpret_cast<uint4*>(i < 4 ? K16 : V16)[to[i & 3]] = make_uint4(out[0], out[1], out[2], out[3]);
+      }
     }
   }
 }
