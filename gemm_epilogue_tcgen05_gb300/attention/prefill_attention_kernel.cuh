@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int n = s ? t.n1 : t.n0, first = t.tok0 + s * p.tq;
       const int tok = first + row_tok;
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
-      const int clear = p.causal ? first : t.len - 1;              // last key that every row sees
+      const int lim_lo = __reduce_min_sync(~0u, lim);              // last key that every row of this warp sees
       float m = kPreNone, l = 0.f;
       for (int i = 0; i < n; ++i) {
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
@@ -631,11 +631,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmem_ld32(s_tmem + j * 32, x[j]);
           tmem_ld_wait();
-          if (i * kPreTile + kPreTile - 1 > clear) {
-            const int cols = lim - i * kPreTile;  // columns up to this one count
+          if (i * kPreTile + kPreTile - 1 > lim_lo) {
+            const int cols = lim - i * kPreTile, all = lim_lo - i * kPreTile;  // columns up to these count
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (j > cols) x[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+            for (int h = 0; h < 4; ++h)
+              if (h * 32 + 31 > all) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (h * 32 + j > cols) x[h][j] = __float_as_uint(-INFINITY);
+              }
           }
           float mx[4];
 #pragma unroll
