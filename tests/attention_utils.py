@@ -24,12 +24,14 @@ D = 128
 def quantise(y):
     """E4M3 bytes and scales of y [..., 128] (one scale per head of a token) in the library's fp32 arithmetic:
     s = max * fl(1/448), codes = e4m3(y * fl(448 / max)).  The quotient of two tensors is rounded once; with a
-    Python number on either side torch multiplies by a reciprocal instead."""
+    Python number on either side torch multiplies by a reciprocal instead.  Below 2^-100, where 448 / max leaves
+    fp32, y and max are both taken times 2^64 (exact) before."""
     y = y.double().float()
     m = y.abs().amax(-1)
     s = m * torch.tensor(1.0 / 448.0, dtype=torch.float32, device=y.device)
-    q = torch.where(m > 0, torch.full_like(m, 448.0) / torch.where(m > 0, m, 1.0), 0.0)
-    return (y * q[..., None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8), s
+    lift = torch.where(m < 2.0 ** -100, 2.0 ** 64, 1.0).to(m.dtype)
+    q = torch.where(m > 0, torch.full_like(m, 448.0) / torch.where(m > 0, m * lift, 1.0), 0.0)
+    return (y * lift[..., None] * q[..., None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8), s
 
 
 def values(codes, scale=None):

@@ -263,6 +263,25 @@ def test_decode_large_ragged_batch(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch", [32, 33, 128, 129, 257])
+def test_decode_batch_sizes(batch, fp8):
+    """Around a warp's and a block's share of the lengths; most of the last sequences are short or empty."""
+    lens = [300 if i % 31 == 0 else (i * 7) % 5 for i in range(batch - 1)] + [513]
+    c = Cache(lens, 3, 16, fp8, seed=batch)
+    q = randn(batch, 6 * D, seed=batch)
+    check_decode(q, c, fl.attention_decode(q, *c.args(), **c.scales()))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_wide_page_table(fp8):
+    """A table so wide that the units of all lengths it allows pass 31 bits, with ordinary sequences in it."""
+    lens, width = [700, 0, 65], 1 << 20
+    c = Cache(lens, 2, 16384, fp8, seed=7, max_pages=width)
+    q = randn(3, 4 * D, seed=7)
+    check_decode(q, c, fl.attention_decode(q, *c.args(), **c.scales()))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_decode_long_sequence(fp8):
     c = Cache([70001], 2, 64, fp8, seed=3)
     q = randn(1, 8 * D, seed=3)
@@ -461,6 +480,34 @@ def test_append_quantises_to_the_nearest_code(std):
         s = want.abs().amax(-1, keepdim=True) / 448.0
         tiny = 2.0 ** -149 * 448  # the scale itself may be subnormal
         assert_within(got, want, torch.maximum(want.abs() * 2.0 ** -4, s * 2.0 ** -10) * (1 + 2.0 ** -20) + tiny)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_append_quantises_rows_with_values_that_are_not_finite(bad):
+    """NaN stays NaN and leaves the other codes of its head alone; an infinity takes its head's scale with it.  Heads of
+    values near fp32's smallest beside ordinary ones keep their own factors."""
+    kv, page = 5, 16
+    c = Cache([40], kv, page, True, seed=50)
+    k, v = randn(40, kv * D, seed=51), randn(40, kv * D, seed=52)
+    k.view(40, kv, D)[::3, 1] *= 1e-36
+    v.view(40, kv, D)[1::3, 4] *= 1e-37
+    clean_k, clean_v = k.clone(), v.clone()
+    for t, clean, row, head, d in ((k, clean_k, 3, 0, 5), (v, clean_v, 17, 4, 127), (v, clean_v, 18, 0, 64)):
+        t.view(40, kv, D)[row, head, d] = bad
+        clean.view(40, kv, D)[row, head, d] = 0
+    fl.paged_kv_append(k, v, *c.args(), cu_seqlens=cu([40]), **c.scales())
+    pos = torch.arange(40, device="cuda")
+    for pages, scales, t, clean in ((c.k, c.ks, k, clean_k), (c.v, c.vs, v, clean_v)):
+        got, scale = place(c, 0, pos, pages), place(c, 0, pos, scales)
+        spoiled = ~t.view(40, kv, D).isfinite()
+        codes, want = quantise(clean.view(40, kv, D))
+        if bad != bad:
+            assert torch.equal(scale, want) and torch.equal(got[~spoiled], codes[~spoiled])
+            assert (got[spoiled] & 0x7F == 0x7F).all()
+        else:
+            heads = spoiled.any(-1)
+            assert (scale[heads] == INF).all() and torch.equal(scale[~heads], want[~heads])
+            assert torch.equal(got[~heads], codes[~heads])
 
 
 def test_append_one_token_each_with_strides():
