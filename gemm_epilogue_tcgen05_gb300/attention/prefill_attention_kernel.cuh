@@ -806,23 +806,25 @@ __global__ void __launch_bounds__(256, kCodesCtas) e4m3_rows_to_bf16_kernel(
     __syncthreads();
     end = min(top, M);
   }
-  const int per_row = n_kv * (kHeadDim / 8);
+  const int per_row = n_kv * (kHeadDim / 8), d_row = 256 / per_row, d_col = 256 - d_row * per_row;
   for (long long row0 = static_cast<long long>(blockIdx.x) * rows; row0 < end; row0 += static_cast<long long>(gridDim.x) * rows) {
     const int pieces = static_cast<int>(min(static_cast<long long>(rows), end - row0)) * per_row;
     for (int at = tid; at < pieces; at += kCodesAtOnce) {
       uint2 codes[8];  // of four places K, then V
       float scale[8];
-      long long to[4];
+      int r = at / per_row, c = at - r * per_row;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int piece = min(at + i * 256, pieces - 1), r = piece / per_row, c = piece - r * per_row;
+        if (at + i * 256 >= pieces) break;
         const long long row = row0 + r;
-        to[i] = row * per_row + c;
         codes[i] = __ldg(reinterpret_cast<const uint2*>(K + row * ld) + c);
         codes[i + 4] = __ldg(reinterpret_cast<const uint2*>(V + row * ld) + c);
         scale[i] = __ldg(ks + row * lds + c / (kHeadDim / 8));
         scale[i + 4] = __ldg(vs + row * lds + c / (kHeadDim / 8));
+        r += d_row, c += d_col;
+        if (c >= per_row) c -= per_row, ++r;
       }
+      const long long to = row0 * per_row + at;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (at + (i & 3) * 256 >= pieces) continue;
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(256, kCodesCtas) e4m3_rows_to_bf16_kernel(
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
           out[k] = pack_bf16x2(f.x * scale[i], f.y * scale[i]);
         }
-        reinterpret_cast<uint4*>(i < 4 ? K16 : V16)[to[i & 3]] = make_uint4(out[0], out[1], out[2], out[3]);
+        reinterpret_cast<uint4*>(i < 4 ? K16 : V16)[to + (i & 3) * 256] = make_uint4(out[0], out[1], out[2], out[3]);
       }
     }
   }
