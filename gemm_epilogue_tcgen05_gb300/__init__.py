@@ -578,7 +578,7 @@ def _on(dev, call, args, stream):
     """Runs call(*args, stream) on device `dev` (an index) and its current stream, or on the stream given."""
     if dev < 0:
         raise ValueError("expected CUDA tensors")
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     with torch.cuda.device(dev):
         return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
@@ -736,6 +736,10 @@ def attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale=Non
     """Attention of one new token per sequence, Q bf16 [batch, n_heads * 128], over the paged cache.
 
     scale: of the logits, 1 / sqrt(128) by default.  Returns O bf16 [batch, n_heads * 128]."""
+    if stream is not None and (O is None or workspace is None):  # what is made here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale, v_page_scale, scale, O,
+                                    workspace)
     dev = Q.get_device()
     rows, width, ldq = _query(Q, "Q", dev)
     batch, n_kv, page, n_pages, max_pages, ldt, pitch, spitch, dt = _cache(k_pages, v_pages, page_table, seq_lens,
@@ -773,6 +777,9 @@ def attention_prefill(Q, K, V, cu_seqlens=None, seq_len: int = 0, k_scale=None, 
     Sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; without cu_seqlens the rows are sequences of
     seq_len tokens laid end to end (0: one sequence).  Rows of O in no sequence stay as they were (zeros where O
     is allocated here).  scale: of the logits, 1 / sqrt(128) by default.  Returns O bf16 [M, n_heads * 128]."""
+    if stream is not None and (O is None or workspace is None):
+        with torch.cuda.stream(stream):
+            return attention_prefill(Q, K, V, cu_seqlens, seq_len, k_scale, v_scale, causal, scale, O, workspace)
     dev = Q.get_device()
     M, width, ldq = _query(Q, "Q", dev)
     rows, kv_width, ldkv, lds, dt = _kv_pair(K, V, k_scale, v_scale, dev)
@@ -791,7 +798,7 @@ def attention_prefill(Q, K, V, cu_seqlens=None, seq_len: int = 0, k_scale=None, 
         workspace = attention_prefill_workspace(M, n_kv, dt == FL_E4M3, Q.device)
     st = _on(dev, load().attention_prefill,
              (Q.data_ptr(), K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens),
-              O.data_ptr(), M, batch, width // HEAD_DIM, n_kv, HEAD_DIM, seq_len or max(M, 1), ldq, ldkv, lds, ldo,
+              O.data_ptr(), M, batch, width // HEAD_DIM, n_kv, HEAD_DIM, min(seq_len, M) or max(M, 1), ldq, ldkv, lds, ldo,
               HEAD_DIM ** -0.5 if scale is None else scale, 1 if causal else 0, dt, workspace.data_ptr(),
               _space(workspace, dev)), stream)
     if st:

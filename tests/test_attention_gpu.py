@@ -429,6 +429,26 @@ def test_calls_on_two_streams_at_once():
             check_prefill(*p[i], [600], f, True)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_stream_given_without_workspace_or_output(fp8):
+    """What a call makes itself belongs to the stream it is given: the current stream is busy, the other one is not."""
+    c = Cache([3000, 70], 2, 16, fp8, seed=60)
+    q = randn(2, 8 * D, seed=60)
+    p = prompt(500, 8, 2, fp8, seed=61)
+    offsets, other = cu([300, 200]), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(4):
+            junk = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")  # memory that is given out again
+            del junk
+            torch.cuda._sleep(2000000)
+            out = fl.attention_decode(q, *c.args(), **c.scales(), stream=other)
+            whole = fl.attention_prefill(p[0], p[1], p[2], cu_seqlens=offsets, k_scale=p[3], v_scale=p[4], stream=other)
+            other.synchronize()
+            check_decode(q, c, out)
+            check_prefill(*p, [300, 200], whole, True)
+
+
 # ---------------------------------------------------------------- append
 def place(cache, b, pos, pages):
     at, slot = cache.table[b].long()[pos // cache.page], pos % cache.page
