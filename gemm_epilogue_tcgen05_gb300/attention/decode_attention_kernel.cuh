@@ -67,8 +67,8 @@ struct DecodeTraits {
   static constexpr int kTile = kStep * kRowBytes;
   static constexpr int kStage = 2 * kTile + (FP8 ? 2 * kStep * 4 : 0);
   // CTAs on an SM and stages of a warp's ring.  Measured (64 sequences of 2048-8192 tokens, E4M3): 2 x 3 stages
-  // 106 us, 3 x 2 111 us; (24 sequences of 5-4096 tokens | 3 of 15000-32768, bf16): 2 x 3 29.7 | 87.6 us, 3 x 2
-  // 25.0 | 89.0 us.  Two column tiles need the registers of 3 CTAs.
+  // 104.7 us, 3 x 2 108.3 us; (24 sequences of 5-4096 tokens | 3 of 15000-32768, bf16): 2 x 3 25.2 | 87.9 us, 3 x 2
+  // 22.2 | 89.1 us.  Two column tiles need the registers of 3 CTAs.
   static constexpr int kCtas = !FP8 && NT == 1 ? 3 : 2;
   static constexpr int kStages = kCtas == 3 ? 2 : 3;
   static_assert(kStage >= NT * 8 * kHeadDim * 4, "a stage takes a warp's piece");

@@ -311,8 +311,8 @@ FL_API int fused_swiglu_bwd(const void* dO, const void* Wd, const void* G, const
  * page_size is any number >= 1 (a multiple of 8 streams best), offsets are 64-bit.  All of these live
  * on the device, so a captured graph can be replayed as the sequences grow.  head_dim must be 128
  * and head counts at most 65536 (FL_ERR_UNSUPPORTED otherwise).  Outputs may not overlap K, V or the
- * cache.  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes
- * them, with scales that are not negative.  Scale, table, length and offset pointers need 4-byte alignment, the others 16. */
+ * cache.  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes them, with scales that are
+ * not negative.  Scale, table, length and offset pointers need 4-byte alignment, the others 16. */
 
 /* Rows of keys and values into the cache.
  * K, V [T, n_kv_heads*128], pitch ldkv elements: bf16 (row_dtype FL_BF16) or E4M3 bytes (FL_E4M3) with
@@ -342,8 +342,8 @@ FL_API int paged_kv_append(const void* K, const void* V, const float* k_scale, c
  * fl_check_device_status(workspace) returns FL_ERR_INVALID_ARG once.  Nothing behind a sequence's
  * length is read into the result, whatever it holds.
  * workspace: fl_attention_decode_workspace_bytes() bytes, 256-byte aligned, its first 4096 bytes
- * zero-filled before first use; calls of any shape may follow one another with it, two calls that may overlap on the GPU need
- * one each. */
+ * zero-filled before first use; calls of any shape may follow one another with it, two calls that may
+ * overlap on the GPU need one each. */
 FL_API int attention_decode(const void* Q, const void* k_pages, const void* v_pages, const float* k_page_scale,
                             const float* v_page_scale, const int32_t* page_table, const int32_t* seq_lens, void* O,
                             int batch, int n_heads, int n_kv_heads, int head_dim, int page_size, int num_pages,
@@ -361,10 +361,8 @@ FL_API size_t fl_attention_decode_workspace_bytes(void);
  * decreasing, in [0, M]); cu_seqlens NULL: the rows are sequences of seq_len tokens laid end to end,
  * the last one possibly shorter (batch is ignored).  Rows of O in no sequence stay as they were.
  * Rows of another sequence, or masked ones of the own, never reach a result, whatever they hold.
- * Softmax state and sums are fp32; the weights p_ij are rounded to bf16 for the tensor cores.  With E4M3
- * keys and values the products run in fp16 instead: codes times scales and the weights are rounded to 11
- * bits, with a power of two of its own for each query row and for each 128 keys of a sequence and head
- * (what is below 2^-26 of the largest there loses bits).
+ * Softmax state and sums are fp32; the weights p_ij are rounded to bf16 for the tensor cores, and so
+ * are E4M3 codes times their scales before they are used.
  * workspace: fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype) bytes, 256-byte aligned, its
  * first 512 bytes zero-filled before first use (and again after FL_ERR_TIMEOUT); two calls that may
  * overlap on the GPU need one each.  One kernel; E4M3 runs a second one in front. */
