@@ -47,9 +47,10 @@ bool launch_dependent(Kernel* kernel, dim3 grid, int threads, int smem, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
+template <bool FP8>
 int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di, cudaStream_t s) {
   using T = PrefillTraits;
-  const void* fn = reinterpret_cast<const void*>(&attention_prefill_kernel);
+  const void* fn = reinterpret_cast<const void*>(&attention_prefill_kernel<FP8>);
   if (!ensure_smem_attr(fn, di.device, T::kSmem)) return FL_ERR_CUDA;
   // the warps share out the registers of the launch: with any other number of them the kernel would not start
   static std::atomic<int> regs{0};
@@ -60,7 +61,7 @@ int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di
   }
   if (regs.load() != kPreRegs) return FL_ERR_UNSUPPORTED;
   const int grid = tiles < di.num_sms ? static_cast<int>(tiles) : di.num_sms;
-  return launch_dependent(attention_prefill_kernel, grid, kPreThreads, T::kSmem, s, p) ? FL_OK : FL_ERR_CUDA;
+  return launch_dependent(attention_prefill_kernel<FP8>, grid, kPreThreads, T::kSmem, s, p) ? FL_OK : FL_ERR_CUDA;
 }
 
 }  // namespace
@@ -69,9 +70,10 @@ int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di
 extern "C" size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, int kv_dtype) {
   using namespace fl;
   if (M < 0 || n_kv_heads < 0) return 0;
-  // the status record and the work counters; for E4M3 also K and V as bf16
+  // the status record and the work counters; for E4M3 also K as bf16, V as fp16 and a power for each key tile (kept at
+  // its first row)
   const size_t rows = static_cast<size_t>(M) * n_kv_heads;
-  return 2 * kWsStatusBytes + (kv_dtype == FL_E4M3 ? rows * kHeadDim * 2 * sizeof(__nv_bfloat16) : 0);
+  return 2 * kWsStatusBytes + (kv_dtype == FL_E4M3 ? rows * (kHeadDim * (sizeof(__nv_bfloat16) + sizeof(__half)) + sizeof(float)) : 0);
 }
 
 extern "C" int attention_prefill(const void* Q, const void* K, const void* V, const float* k_scale,
@@ -130,7 +132,9 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   int64_t ld16 = ldkv;
   if (fp8) {
     __nv_bfloat16* kw = reinterpret_cast<__nv_bfloat16*>(ws + 2 * kWsStatusBytes);
-    k16 = kw, v16 = kw + static_cast<size_t>(M) * kv_width, ld16 = kv_width;
+    __half* vw = reinterpret_cast<__half*>(kw + static_cast<size_t>(M) * kv_width);
+    p.powers = reinterpret_cast<const float*>(vw + static_cast<size_t>(M) * kv_width);
+    k16 = kw, v16 = vw, ld16 = kv_width;
   }
   if (!encode_q(&p.map_q, Q, n_heads, M, ldq, p.hp, p.tq) ||
       !encode_2d(&p.map_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k16, kv_width, M, ld16, 64, kPreTile,
@@ -140,6 +144,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
     return FL_ERR_CUDA;
   p.V = static_cast<const __nv_bfloat16*>(v16);
   p.ldv = ld16;
+  p.n_kv = n_kv_heads;
   p.cu = cu_seqlens;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.ldo = ldo;
@@ -149,15 +154,18 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   p.status = reinterpret_cast<int*>(ws);
   p.work = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);
   p.timeout_ns = wait_timeout_ns();
-  if (fp8) {
-    const int rows = std::max(kCodesAtOnce / (n_kv_heads * (kHeadDim / 8)), 1);  // of a CTA
-    const int grid = std::min((M - 1) / rows + 1, kCodesCtas * di.num_sms);
-    if (!launch_dependent(e4m3_rows_to_bf16_kernel, dim3(grid), 256, 0, s, static_cast<const uint8_t*>(K),
-                          static_cast<const uint8_t*>(V), k_scale, v_scale, static_cast<long long>(ldkv),
-                          static_cast<long long>(lds), cu_seqlens, p.batch, M, n_kv_heads, rows,
-                          static_cast<__nv_bfloat16*>(const_cast<void*>(k16)),
-                          static_cast<__nv_bfloat16*>(const_cast<void*>(v16))))
-      return FL_ERR_CUDA;
-  }
-  return launch_prefill(p, blocks * p.pairs, di, s);
+  if (!fp8) return launch_prefill<false>(p, blocks * p.pairs, di, s);
+  const long long key_tiles =
+      cu_seqlens == nullptr
+          ? static_cast<long long>(M / seq_len) * ((seq_len - 1) / kPreTile + 1) + (M % seq_len + kPreTile - 1) / kPreTile
+          : std::min<long long>(static_cast<long long>(M) / kPreTile + batch, M);  // an upper bound
+  const long long items = key_tiles * ((n_kv_heads - 1) / kCodesHeads + 1) * (kPreTile / kCodesRows);
+  const int grid = static_cast<int>(std::min<long long>(items, kCodesCtas * di.num_sms));
+  if (!launch_dependent(e4m3_tiles_kernel, dim3(grid), 256, 0, s, static_cast<const uint8_t*>(K),
+                        static_cast<const uint8_t*>(V), k_scale, v_scale, static_cast<long long>(ldkv),
+                        static_cast<long long>(lds), cu_seqlens, p.batch, seq_len, M, n_kv_heads, key_tiles,
+                        static_cast<__nv_bfloat16*>(const_cast<void*>(k16)), static_cast<__half*>(const_cast<void*>(v16)),
+                        const_cast<float*>(p.powers)))
+    return FL_ERR_CUDA;
+  return launch_prefill<true>(p, blocks * p.pairs, di, s);
 }

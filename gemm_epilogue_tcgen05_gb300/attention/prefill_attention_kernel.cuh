@@ -53,6 +53,7 @@ constexpr int kPreRing = 3;                        // tile descriptors
 constexpr float kPreNone = -3e38f;                 // a maximum over nothing: any finite logit passes it
 constexpr float kPreLazy = 8.f;
 constexpr uint64_t kPreDrainNs = 1000000000;       // for copies and products in flight, whatever the limit of the waits
+constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted by 2^7 in fp16
 
 // Where a wait gave up (recorded in the workspace's status record).
 enum : int {
@@ -63,9 +64,11 @@ enum : int {
 struct alignas(128) PrefillParams {
   CUtensorMap map_q;  // Q [M][n_heads][128] bf16, box {64, hp, tq}
   CUtensorMap map_k;  // K [M][n_kv * 128] bf16, box {64, 128}
-  CUtensorMap map_v;
+  CUtensorMap map_v;  // the same, E4M3: fp16
   const __nv_bfloat16* V;  // the rows map_v covers
   long long ldv;
+  const float* powers;  // E4M3: [first row of a key tile][n_kv]: b of V * 2^-b
+  int n_kv;
   const int* cu;
   __nv_bfloat16* O;
   long long ldo;
@@ -186,9 +189,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 // Two values times zero, plus c: NaN for one that is not finite.
+template <bool F16>
 __device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t c) {
   uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
+  if (F16) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
+  else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 // Two fp32 lanes in one 64-bit register.
@@ -216,6 +226,7 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return r;
 }
 
+template <bool FP8>
 __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const __grid_constant__ PrefillParams p) {
   using T = PrefillTraits;
   extern __shared__ uint8_t smem_raw[];
@@ -427,7 +438,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   } else if (warp == 8) {
     // ================================================================ MMA issue
     // The whole warp walks the loop, so that descriptors stay in uniform registers, and one elected lane issues.
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile), idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true);
+    constexpr uint32_t kF16 = FP8 ? (1u << 7) | (1u << 10) : 0u;  // P and V: without these bits they are fp16
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreTile),
+                       idesc_pv = idesc_bf16_f32(kPreTile, kHeadDim, true) & ~kF16;
     constexpr uint32_t kStep16 = kPreTileBytes / 16;  // one tile in descriptor units
     const bool one = elect_one();
     const uint64_t q_desc = sdesc_k_sw128(q_smem), k_desc = sdesc_k_sw128(kv_smem + kPreTileBytes),
@@ -571,14 +584,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll 8
         for (int c = 0; c < kPreTileBytes / 512; ++c) {
           const uint4 w = ld_shared_v4(base + c * 512);
-          seen[0] = times_zero(w.x, seen[0]), seen[1] = times_zero(w.y, seen[1]);
-          seen[2] = times_zero(w.z, seen[2]), seen[3] = times_zero(w.w, seen[3]);
+          seen[0] = times_zero<FP8>(w.x, seen[0]), seen[1] = times_zero<FP8>(w.y, seen[1]);
+          seen[2] = times_zero<FP8>(w.z, seen[2]), seen[3] = times_zero<FP8>(w.w, seen[3]);
         }
         if (__any_sync(~0u, ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7FFF7FFFu) != 0)) {
           int lo = INT_MAX, hi = -1;
           bool bad_chunk = false;
           auto clean = [&](uint32_t w) {  // an exponent of all ones carries into the sign's place
-            constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+            constexpr uint32_t kExp = FP8 ? 0x7C007C00u : 0x7F807F80u, kOne = FP8 ? 0x04000400u : 0x00800080u;
             const uint32_t bad = ((w & kExp) + kOne) & 0x80008000u;
             bad_chunk |= bad != 0;
             return w & ~((bad >> 15) * 0xFFFFu);
@@ -623,7 +636,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int lim_lo = __reduce_min_sync(~0u, lim);              // last key that every row of this warp sees
       float m = kPreNone, l = 0.f;
+      float b = 0.f, E = 0.f;  // E4M3: this key tile's power of V, and that of O
+      const float* powers = p.powers + static_cast<long long>(t.row0) * p.n_kv + t.kvh;
+      if (FP8 && n > 0) {
+        b = __ldg(powers);
+        E = b + 2.f;
+      }
       for (int i = 0; i < n; ++i) {
+          float b_next = b;
+          if (FP8 && i + 1 < n) b_next = __ldg(powers + static_cast<long long>(i + 1) * kPreTile * p.n_kv);
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
@@ -653,11 +674,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           for (int h = 0; h < 4; ++h) mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           const bool rise = top > m + kPreLazy;
-          if (__any_sync(~0u, rise)) {
+          if (__any_sync(~0u, rise) || (FP8 && b > E)) {
             const float up = rise ? top : m;
-            const float down = ex2(m - up);
+            float down = ex2(m - up);
             m = up;
             l *= down;
+            if (FP8 && b > E) {
+              down *= ex2(E - b - 2.f);
+              E = b + 2.f;
+            }
             if (i > 0) {  // O of the key tiles before is complete: S of this one was committed behind it
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -670,27 +695,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               }
             }
           }
-          const uint64_t c2 = f2(c, c), m2 = f2(-m, -m);
+          const float lift = FP8 ? kPreLift + b - E : 0.f;  // weights are larger by 2^lift
+          const uint64_t c2 = f2(c, c), m2 = f2(lift - m, lift - m);
           uint64_t l0 = 0, l1 = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t w[16];
 #pragma unroll
             for (int h = 0; h < 16; h += 2) {
-              float a, b, d, e;
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), c2, m2), a, b);
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m2), d, e);
-              a = ex2(a), b = ex2(b), d = ex2(d), e = ex2(e);
-              l0 = f2_add(l0, f2(a, b)), l1 = f2_add(l1, f2(d, e));
-              w[h] = pack_bf16x2(a, b);
-              w[h + 1] = pack_bf16x2(d, e);
+              float w0, w1, w2, w3;
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), c2, m2), w0, w1);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m2), w2, w3);
+              w0 = ex2(w0), w1 = ex2(w1), w2 = ex2(w2), w3 = ex2(w3);
+              l0 = f2_add(l0, f2(w0, w1)), l1 = f2_add(l1, f2(w2, w3));
+              w[h] = FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
+              w[h + 1] = FP8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3);
             }
             tmem_st16(s_tmem + j * 16, w);
           }
-          float a, b, d, e;
-          f2_split(l0, a, b);
-          f2_split(l1, d, e);
-          l += (a + b) + (d + e);
+          float s0, s1, s2, s3;
+          f2_split(l0, s0, s1);
+          f2_split(l1, s2, s3);
+          l += FP8 ? ((s0 + s1) + (s2 + s3)) * ex2(-lift) : (s0 + s1) + (s2 + s3);
+          b = b_next;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -698,7 +725,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       }
       if (!ok) break;
       const bool have = __all_sync(~0u, get_tile(k + 1, next));
-      const float inv = 1.f / l;
+      const float inv = (FP8 ? ex2(E - kPreLift) : 1.f) / l;
       if (n > 0) {
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
@@ -760,7 +787,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             float sum = 0.f;
 #pragma unroll 1
             for (int pos = bad_lo; pos <= min(bad_hi, lim); ++pos) {
-              const float y = __bfloat162float(v[static_cast<long long>(pos) * p.ldv + d]);
+              const __nv_bfloat16 raw = v[static_cast<long long>(pos) * p.ldv + d];
+              const float y = FP8 ? __half2float(__ushort_as_half(__bfloat16_as_ushort(raw))) : __bfloat162float(raw);
               if (!isfinite(y)) sum += y;
             }
             if (!isfinite(sum)) mine[d] = __float2bfloat16_rn(sum);
@@ -780,66 +808,114 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   if (threadIdx.x == 0 && bar.abort_flag != 0) record_failure(p.status, bar.abort_flag, 0);
 }
 
-// E4M3 codes of K and V times their scales as bf16, for the kernel above.  Bound by memory: 1 byte in and 2 out for
-// each value.  A CTA takes whole rows, a thread 8 codes at a time (16 bytes out; with 16 codes each
-// store left half sectors to the next one, 2 us more for 12400 rows of 8 heads), eight loads of codes on their way before
-// the first is used.  Rows that lie behind every sequence are left out.
-constexpr int kCodesAtOnce = 1024;  // 8-byte pieces of a CTA's rows, of K and V each, that are on their way together
-constexpr int kCodesCtas = 4;       // on an SM
+// E4M3 codes of K and V times their scales, for the kernel above: K as bf16, V as fp16 times 2^-b, with b from V's
+// largest finite scale in the key tile (128 rows of a sequence, from its first) and head.  Bound by memory: 1 byte in
+// and 2 out for each value.  A CTA takes 16 rows of a key tile for up to 32 heads at a time, a thread 8 codes (16 bytes
+// out; with 16 codes each store left half sectors to the next one); the scales of the whole tile are read by each of
+// its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18 instead of
+// FIGURE us for 12400 rows of 8 heads: too few, too long).
+constexpr int kCodesRows = 16, kCodesHeads = 32;
+constexpr int kCodesCtas = 4;  // on an SM
 
-__global__ void __launch_bounds__(256, kCodesCtas) e4m3_rows_to_bf16_kernel(
+__global__ void __launch_bounds__(256, kCodesCtas) e4m3_tiles_kernel(
     const uint8_t* K, const uint8_t* V, const float* ks, const float* vs, long long ld, long long lds, const int* cu,
-    int batch, int M, int n_kv, int rows, __nv_bfloat16* K16, __nv_bfloat16* V16) {
-  __shared__ int top;
-  const int tid = threadIdx.x;
-  if (tid == 0) top = 0;
+    int batch, int seq_len, int M, int n_kv, long long tiles, __nv_bfloat16* K16, __half* V16, float* powers) {
+  __shared__ uint32_t tops[2][kCodesHeads];
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < kCodesHeads) tops[0][tid] = tops[1][tid] = 0;
   if (cu != nullptr && tid <= batch) asm volatile("prefetch.global.L2 [%0];" ::"l"(cu + tid));
   griddep_wait();
   griddep_launch_dependents();
-  int end = M;
-  if (cu != nullptr) {
-    int x = 0;
-    for (int i = 1 + tid; i <= batch; i += 256) x = max(x, cu[i]);
-    x = __reduce_max_sync(~0u, x);
-    __syncthreads();
-    if ((tid & 31) == 0 && x > 0) atomicMax(&top, x);
-    __syncthreads();
-    end = min(top, M);
-  }
-  const int per_row = n_kv * (kHeadDim / 8), d_row = 256 / per_row, d_col = 256 - d_row * per_row;
-  for (long long row0 = static_cast<long long>(blockIdx.x) * rows; row0 < end; row0 += static_cast<long long>(gridDim.x) * rows) {
-    const int pieces = static_cast<int>(min(static_cast<long long>(rows), end - row0)) * per_row;
-    for (int at = tid; at < pieces; at += kCodesAtOnce) {
-      uint2 codes[8];  // of four places K, then V
-      float scale[8];
-      int r = at / per_row, c = at - r * per_row;
+  __syncthreads();
+  constexpr int kParts = kPreTile / kCodesRows;
+  const int groups = (n_kv - 1) / kCodesHeads + 1;
+  const long long items = tiles * groups * kParts;
+  int turn = 0;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const long long of_tile = item / kParts;
+    const int part = static_cast<int>(item - of_tile * kParts), tile = static_cast<int>(of_tile / groups);
+    const int h0 = static_cast<int>(of_tile - static_cast<long long>(tile) * groups) * kCodesHeads;
+    const int heads = min(kCodesHeads, n_kv - h0);
+    int row0 = 0, rows = 0, skip = tile;
+    for (int b0 = 0; b0 < batch; b0 += 32) {  // the sequence that holds the tile: each warp looks for itself
+      int first = 0, last = 0;
+      if (b0 + lane < batch) sequence_rows(cu, b0 + lane, seq_len, M, first, last);
+      const int have = last > first ? (last - first - 1) / kPreTile + 1 : 0;
+      int sum = have;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (at + i * 256 >= pieces) break;
-        const long long row = row0 + r;
-        codes[i] = __ldg(reinterpret_cast<const uint2*>(K + row * ld) + c);
-        codes[i + 4] = __ldg(reinterpret_cast<const uint2*>(V + row * ld) + c);
-        scale[i] = __ldg(ks + row * lds + c / (kHeadDim / 8));
-        scale[i + 4] = __ldg(vs + row * lds + c / (kHeadDim / 8));
-        r += d_row, c += d_col;
-        if (c >= per_row) c -= per_row, ++r;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += y;
       }
-      const long long to = row0 * per_row + at;
+      const unsigned who = __ballot_sync(~0u, sum > skip);
+      if (who != 0) {
+        const int from = __ffs(who) - 1;
+        row0 = __shfl_sync(~0u, first + (skip - (sum - have)) * kPreTile, from);
+        rows = min(kPreTile, __shfl_sync(~0u, last, from) - row0);
+        break;
+      }
+      skip -= __shfl_sync(~0u, sum, 31);
+    }
+    if (rows == 0) return;  // fewer tiles than there might have been; the same for all threads
+    if (part * kCodesRows >= rows) continue;
+    const int r = part * kCodesRows + (tid >> 4), c = tid & 15;  // 16 threads a row and head
+    const bool there = r < rows;
+    const long long row = row0 + (there ? r : 0);
+    constexpr int kTogether = 4;
+    uint2 k[kTogether], v[kTogether];
+    float sk[kTogether], sv[kTogether];
+    auto fetch = [&](int j0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (at + (i & 3) * 256 >= pieces) continue;
-        uint32_t out[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t two = (k < 2 ? codes[i].x : codes[i].y) >> ((k & 1) * 16);
-          uint32_t h;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          out[k] = pack_bf16x2(f.x * scale[i], f.y * scale[i]);
+      for (int i = 0; i < kTogether; ++i) {
+        if (j0 + i >= heads) break;
+        const long long h = h0 + j0 + i;
+        k[i] = __ldg(reinterpret_cast<const uint2*>(K + row * ld + h * kHeadDim) + c);
+        v[i] = __ldg(reinterpret_cast<const uint2*>(V + row * ld + h * kHeadDim) + c);
+        sk[i] = __ldg(ks + row * lds + h);
+        sv[i] = __ldg(vs + row * lds + h);
+      }
+    };
+    fetch(0);
+    {
+      const int each = 256 / heads, j = tid % heads;
+      uint32_t largest = 0;
+      if (tid < each * heads)
+        for (int q = tid / heads; q < rows; q += each) {
+          const float x = fabsf(__ldg(vs + (row0 + q) * lds + h0 + j));
+          largest = max(largest, x < INFINITY ? __float_as_uint(x) : 0u);
         }
-        reinterpret_cast<uint4*>(i < 4 ? K16 : V16)[to + (i & 3) * 256] = make_uint4(out[0], out[1], out[2], out[3]);
+      if (largest != 0) atomicMax(&tops[turn][j], largest);
+    }
+    __syncthreads();
+    if (tid < kCodesHeads) tops[turn ^ 1][tid] = 0;  // for the next item, whose barrier lies behind
+    for (int j0 = 0; j0 < heads; j0 += kTogether) {
+      if (j0 > 0) fetch(j0);
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        if (j0 + i >= heads || !there) break;
+        auto codes = [](uint2 in, float scale, auto pack) {
+          uint32_t out[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t two;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>((e < 2 ? in.x : in.y) >> ((e & 1) * 16))));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+            out[e] = pack(f.x * scale, f.y * scale);
+          }
+          return make_uint4(out[0], out[1], out[2], out[3]);
+        };
+        const uint32_t bits = tops[turn][j0 + i];
+        // 448 * scale * 2^-b is below 2^14
+        const int b = bits == 0 ? 0 : min(max(static_cast<int>(bits >> 23) - 127 - 4, -120), 120);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - b) << 23);
+        const long long to = (row * n_kv + h0 + j0 + i) * (kHeadDim / 8) + c;
+        reinterpret_cast<uint4*>(K16)[to] = codes(k[i], sk[i], [](float x, float y) { return pack_bf16x2(x, y); });
+        reinterpret_cast<uint4*>(V16)[to] = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
+        if (part == 0 && tid == 0) powers[static_cast<long long>(row0) * n_kv + h0 + j0 + i] = static_cast<float>(b);
       }
     }
+    __syncthreads();
+    turn ^= 1;
   }
 }
 
