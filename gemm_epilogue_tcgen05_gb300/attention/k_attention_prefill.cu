@@ -159,11 +159,12 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
       cu_seqlens == nullptr
           ? static_cast<long long>(M / seq_len) * ((seq_len - 1) / kPreTile + 1) + (M % seq_len + kPreTile - 1) / kPreTile
           : std::min<long long>(static_cast<long long>(M) / kPreTile + batch, M);  // an upper bound
-  const long long items = key_tiles * ((n_kv_heads - 1) / kCodesHeads + 1) * (kPreTile / kCodesRows);
-  const int grid = static_cast<int>(std::min<long long>(items, kCodesCtas * di.num_sms));
-  if (!launch_dependent(e4m3_tiles_kernel, dim3(grid), 256, 0, s, static_cast<const uint8_t*>(K),
+  const long long parts = key_tiles * (kPreTile / kCodesRows);
+  if (parts > INT32_MAX) return FL_ERR_UNSUPPORTED;
+  if (!launch_dependent(e4m3_tiles_kernel, dim3(static_cast<unsigned>(parts), (n_kv_heads - 1) / kCodesHeads + 1), 256, 0, s,
+                        static_cast<const uint8_t*>(K),
                         static_cast<const uint8_t*>(V), k_scale, v_scale, static_cast<long long>(ldkv),
-                        static_cast<long long>(lds), cu_seqlens, p.batch, seq_len, M, n_kv_heads, key_tiles,
+                        static_cast<long long>(lds), cu_seqlens, p.batch, seq_len, M, n_kv_heads,
                         static_cast<__nv_bfloat16*>(const_cast<void*>(k16)), static_cast<__half*>(const_cast<void*>(v16)),
                         const_cast<float*>(p.powers)))
     return FL_ERR_CUDA;

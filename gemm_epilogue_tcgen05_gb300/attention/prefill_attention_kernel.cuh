@@ -31,10 +31,15 @@
 // Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
 //
-// E4M3: a first kernel writes codes times scales as bf16, 8 bits where the codes carry 4.  Measured for 4 x 2048
-// tokens, 32 query and 8 kv heads: 311 us with the scales in the softmax (two multiplications and two shared-memory
-// reads for each query and key, reads that the tensor cores need for themselves), 123 us with fp16 products (11 bits,
-// but powers of two for each key tile against fp16's range, and queries that become fp16, too); 107 us so.
+// E4M3: a first kernel writes K as bf16 (code times scale, 8 bits where the code carries 4) and V as fp16 times 2^-b,
+// b from the largest scale of 128 keys and a head, so that the largest possible value is in [2^12, 2^14).  The logits of
+// a key tile get b on top: weights are 2^(x + b - m + 7) in fp16, m the running maximum of x + b, and meet V 2^-b in O
+// at one common power whatever the tiles' scales are; the sum l takes each tile's weights times 2^-b.  (b counts from
+// the sequence's first tile, so that 2^-b stays in range.)  Measured for 4 x 2048 tokens, 32 query and 8 kv heads:
+// 311 us with scales inside the softmax (two multiplications and two shared-memory reads for each query and key, reads
+// that the tensor cores need for themselves), 123 us with fp16 keys (11 bits, but queries that have to become fp16,
+// too), FIGURE us so, 105 us with bf16 values and weights, whose roundings make the error 1.8 times that of a bf16
+// output alone instead of 1.4 times.
 #pragma once
 #include <climits>
 
@@ -53,7 +58,7 @@ constexpr int kPreRing = 3;                        // tile descriptors
 constexpr float kPreNone = -3e38f;                 // a maximum over nothing: any finite logit passes it
 constexpr float kPreLazy = 8.f;
 constexpr uint64_t kPreDrainNs = 1000000000;       // for copies and products in flight, whatever the limit of the waits
-constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted by 2^7 in fp16
+constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted by 2^7 in fp16 (2^8 more: kPreLazy)
 
 // Where a wait gave up (recorded in the workspace's status record).
 enum : int {
@@ -627,6 +632,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const uint32_t hp_inverse = 65536u / p.hp + 1;  // row / hp = row * hp_inverse >> 16 for rows below 128
     const int row_tok = row / p.hp;
     const float c = p.scale_log2;
+    auto load_powers = [&](const PrefillTile& t, int n, int i) {
+      const long long tile = i + lane;
+      return tile < n ? __ldg(p.powers + (t.row0 + tile * kPreTile) * p.n_kv + t.kvh) : 0.f;
+    };
+    float powers_next = 0.f;
     int s_uses = 0, o_uses = 0;
     bool ok = true;
     PrefillTile t = {}, next;
@@ -636,15 +646,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int lim_lo = __reduce_min_sync(~0u, lim);              // last key that every row of this warp sees
       float m = kPreNone, l = 0.f;
-      float b = 0.f, E = 0.f;  // E4M3: this key tile's power of V, and that of O
-      const float* powers = p.powers + static_cast<long long>(t.row0) * p.n_kv + t.kvh;
-      if (FP8 && n > 0) {
-        b = __ldg(powers);
-        E = b + 2.f;
-      }
+      float powers = powers_next;  // E4M3: of key tile i in lane i % 32
+      const float b0 = FP8 ? __shfl_sync(~0u, powers, 0) : 0.f;
       for (int i = 0; i < n; ++i) {
-          float b_next = b;
-          if (FP8 && i + 1 < n) b_next = __ldg(powers + static_cast<long long>(i + 1) * kPreTile * p.n_kv);
+          if (FP8 && i > 0 && (i & 31) == 0) powers = load_powers(t, n, i);
+          const float b = FP8 ? __shfl_sync(~0u, powers, i & 31) - b0 : 0.f;
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
@@ -672,17 +678,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               mx[h] = max3(mx[h], __uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1]));
 #pragma unroll
           for (int h = 0; h < 4; ++h) mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          if (FP8) top += b;
           const bool rise = top > m + kPreLazy;
-          if (__any_sync(~0u, rise) || (FP8 && b > E)) {
+          if (__any_sync(~0u, rise)) {
             const float up = rise ? top : m;
-            float down = ex2(m - up);
+            const float down = ex2(m - up);
             m = up;
             l *= down;
-            if (FP8 && b > E) {
-              down *= ex2(E - b - 2.f);
-              E = b + 2.f;
-            }
             if (i > 0) {  // O of the key tiles before is complete: S of this one was committed behind it
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -695,8 +698,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               }
             }
           }
-          const float lift = FP8 ? kPreLift + b - E : 0.f;  // weights are larger by 2^lift
-          const uint64_t c2 = f2(c, c), m2 = f2(lift - m, lift - m);
+          const float minus = FP8 ? (kPreLift + b) - m : -m;
+          const uint64_t c2 = f2(c, c), m2 = f2(minus, minus);
           uint64_t l0 = 0, l1 = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -716,8 +719,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           float s0, s1, s2, s3;
           f2_split(l0, s0, s1);
           f2_split(l1, s2, s3);
-          l += FP8 ? ((s0 + s1) + (s2 + s3)) * ex2(-lift) : (s0 + s1) + (s2 + s3);
-          b = b_next;
+          l += FP8 ? ((s0 + s1) + (s2 + s3)) * ex2(-b) : (s0 + s1) + (s2 + s3);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -725,7 +727,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       }
       if (!ok) break;
       const bool have = __all_sync(~0u, get_tile(k + 1, next));
-      const float inv = (FP8 ? ex2(E - kPreLift) : 1.f) / l;
+      if (FP8 && have) powers_next = load_powers(next, s ? next.n1 : next.n0, 0);
+      const float inv = (FP8 ? ex2(b0) : 1.f) / l;
       if (n > 0) {
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
@@ -815,107 +818,95 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 // its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18 instead of
 // FIGURE us for 12400 rows of 8 heads: too few, too long).
 constexpr int kCodesRows = 16, kCodesHeads = 32;
-constexpr int kCodesCtas = 4;  // on an SM
 
-__global__ void __launch_bounds__(256, kCodesCtas) e4m3_tiles_kernel(
+__global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
     const uint8_t* K, const uint8_t* V, const float* ks, const float* vs, long long ld, long long lds, const int* cu,
-    int batch, int seq_len, int M, int n_kv, long long tiles, __nv_bfloat16* K16, __half* V16, float* powers) {
-  __shared__ uint32_t tops[2][kCodesHeads];
+    int batch, int seq_len, int M, int n_kv, __nv_bfloat16* K16, __half* V16, float* powers) {
+  __shared__ uint32_t top[kCodesHeads];
   const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < kCodesHeads) tops[0][tid] = tops[1][tid] = 0;
+  if (tid < kCodesHeads) top[tid] = 0;
   if (cu != nullptr && tid <= batch) asm volatile("prefetch.global.L2 [%0];" ::"l"(cu + tid));
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
   constexpr int kParts = kPreTile / kCodesRows;
-  const int groups = (n_kv - 1) / kCodesHeads + 1;
-  const long long items = tiles * groups * kParts;
-  int turn = 0;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const long long of_tile = item / kParts;
-    const int part = static_cast<int>(item - of_tile * kParts), tile = static_cast<int>(of_tile / groups);
-    const int h0 = static_cast<int>(of_tile - static_cast<long long>(tile) * groups) * kCodesHeads;
-    const int heads = min(kCodesHeads, n_kv - h0);
-    int row0 = 0, rows = 0, skip = tile;
-    for (int b0 = 0; b0 < batch; b0 += 32) {  // the sequence that holds the tile: each warp looks for itself
-      int first = 0, last = 0;
-      if (b0 + lane < batch) sequence_rows(cu, b0 + lane, seq_len, M, first, last);
-      const int have = last > first ? (last - first - 1) / kPreTile + 1 : 0;
-      int sum = have;
+  const int tile = static_cast<int>(blockIdx.x / kParts), part = static_cast<int>(blockIdx.x % kParts);
+  const int h0 = static_cast<int>(blockIdx.y) * kCodesHeads, heads = min(kCodesHeads, n_kv - h0);
+  int row0 = 0, rows = 0, skip = tile;
+  for (int b0 = 0; b0 < batch; b0 += 32) {  // the sequence that holds the tile: each warp looks for itself
+    int first = 0, last = 0;
+    if (b0 + lane < batch) sequence_rows(cu, b0 + lane, seq_len, M, first, last);
+    const int have = last > first ? (last - first - 1) / kPreTile + 1 : 0;
+    int sum = have;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const unsigned who = __ballot_sync(~0u, sum > skip);
-      if (who != 0) {
-        const int from = __ffs(who) - 1;
-        row0 = __shfl_sync(~0u, first + (skip - (sum - have)) * kPreTile, from);
-        rows = min(kPreTile, __shfl_sync(~0u, last, from) - row0);
-        break;
-      }
-      skip -= __shfl_sync(~0u, sum, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, sum, o);
+      if (lane >= o) sum += y;
     }
-    if (rows == 0) return;  // fewer tiles than there might have been; the same for all threads
-    if (part * kCodesRows >= rows) continue;
-    const int r = part * kCodesRows + (tid >> 4), c = tid & 15;  // 16 threads a row and head
-    const bool there = r < rows;
-    const long long row = row0 + (there ? r : 0);
-    constexpr int kTogether = 4;
-    uint2 k[kTogether], v[kTogether];
-    float sk[kTogether], sv[kTogether];
-    auto fetch = [&](int j0) {
+    const unsigned who = __ballot_sync(~0u, sum > skip);
+    if (who != 0) {
+      const int from = __ffs(who) - 1;
+      row0 = __shfl_sync(~0u, first + (skip - (sum - have)) * kPreTile, from);
+      rows = min(kPreTile, __shfl_sync(~0u, last, from) - row0);
+      break;
+    }
+    skip -= __shfl_sync(~0u, sum, 31);
+  }
+  if (part * kCodesRows >= rows) return;  // the same for all threads
+  const int r = part * kCodesRows + (tid >> 4), c = tid & 15;  // 16 threads a row and head
+  const bool there = r < rows;
+  const long long row = row0 + (there ? r : 0);
+  constexpr int kTogether = 4;
+  uint2 k[kTogether], v[kTogether];
+  float sk[kTogether], sv[kTogether];
+  auto fetch = [&](int j0) {
 #pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        if (j0 + i >= heads) break;
-        const long long h = h0 + j0 + i;
-        k[i] = __ldg(reinterpret_cast<const uint2*>(K + row * ld + h * kHeadDim) + c);
-        v[i] = __ldg(reinterpret_cast<const uint2*>(V + row * ld + h * kHeadDim) + c);
-        sk[i] = __ldg(ks + row * lds + h);
-        sv[i] = __ldg(vs + row * lds + h);
+    for (int i = 0; i < kTogether; ++i) {
+      if (j0 + i >= heads) break;
+      const long long h = h0 + j0 + i;
+      k[i] = __ldg(reinterpret_cast<const uint2*>(K + row * ld + h * kHeadDim) + c);
+      v[i] = __ldg(reinterpret_cast<const uint2*>(V + row * ld + h * kHeadDim) + c);
+      sk[i] = __ldg(ks + row * lds + h);
+      sv[i] = __ldg(vs + row * lds + h);
+    }
+  };
+  fetch(0);
+  {
+    const int each = 256 / heads, j = tid % heads;
+    uint32_t largest = 0;
+    if (tid < each * heads)
+      for (int q = tid / heads; q < rows; q += each) {
+        const float x = fabsf(__ldg(vs + (row0 + q) * lds + h0 + j));
+        largest = max(largest, x < INFINITY ? __float_as_uint(x) : 0u);
       }
-    };
-    fetch(0);
-    {
-      const int each = 256 / heads, j = tid % heads;
-      uint32_t largest = 0;
-      if (tid < each * heads)
-        for (int q = tid / heads; q < rows; q += each) {
-          const float x = fabsf(__ldg(vs + (row0 + q) * lds + h0 + j));
-          largest = max(largest, x < INFINITY ? __float_as_uint(x) : 0u);
+    if (largest != 0) atomicMax(&top[j], largest);
+  }
+  __syncthreads();
+  for (int j0 = 0; j0 < heads; j0 += kTogether) {
+    if (j0 > 0) fetch(j0);
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) {
+      if (j0 + i >= heads || !there) break;
+      auto codes = [](uint2 in, float scale, auto pack) {
+        uint32_t out[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t two;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>((e < 2 ? in.x : in.y) >> ((e & 1) * 16))));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+          out[e] = pack(f.x * scale, f.y * scale);
         }
-      if (largest != 0) atomicMax(&tops[turn][j], largest);
+        return make_uint4(out[0], out[1], out[2], out[3]);
+      };
+      const uint32_t bits = top[j0 + i];
+      // 448 * scale * 2^-b is below 2^14
+      const int b = bits == 0 ? 0 : min(max(static_cast<int>(bits >> 23) - 127 - 4, -120), 120);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - b) << 23);
+      const long long to = (row * n_kv + h0 + j0 + i) * (kHeadDim / 8) + c;
+      reinterpret_cast<uint4*>(K16)[to] = codes(k[i], sk[i], [](float x, float y) { return pack_bf16x2(x, y); });
+      reinterpret_cast<uint4*>(V16)[to] = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
+      if (part == 0 && tid == 0) powers[static_cast<long long>(row0) * n_kv + h0 + j0 + i] = static_cast<float>(b);
     }
-    __syncthreads();
-    if (tid < kCodesHeads) tops[turn ^ 1][tid] = 0;  // for the next item, whose barrier lies behind
-    for (int j0 = 0; j0 < heads; j0 += kTogether) {
-      if (j0 > 0) fetch(j0);
-#pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        if (j0 + i >= heads || !there) break;
-        auto codes = [](uint2 in, float scale, auto pack) {
-          uint32_t out[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t two;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>((e < 2 ? in.x : in.y) >> ((e & 1) * 16))));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-            out[e] = pack(f.x * scale, f.y * scale);
-          }
-          return make_uint4(out[0], out[1], out[2], out[3]);
-        };
-        const uint32_t bits = tops[turn][j0 + i];
-        // 448 * scale * 2^-b is below 2^14
-        const int b = bits == 0 ? 0 : min(max(static_cast<int>(bits >> 23) - 127 - 4, -120), 120);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - b) << 23);
-        const long long to = (row * n_kv + h0 + j0 + i) * (kHeadDim / 8) + c;
-        reinterpret_cast<uint4*>(K16)[to] = codes(k[i], sk[i], [](float x, float y) { return pack_bf16x2(x, y); });
-        reinterpret_cast<uint4*>(V16)[to] = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
-        if (part == 0 && tid == 0) powers[static_cast<long long>(row0) * n_kv + h0 + j0 + i] = static_cast<float>(b);
-      }
-    }
-    __syncthreads();
-    turn ^= 1;
   }
 }
 
