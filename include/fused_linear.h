@@ -361,8 +361,10 @@ FL_API size_t fl_attention_decode_workspace_bytes(void);
  * decreasing, in [0, M]); cu_seqlens NULL: the rows are sequences of seq_len tokens laid end to end,
  * the last one possibly shorter (batch is ignored).  Rows of O in no sequence stay as they were.
  * Rows of another sequence, or masked ones of the own, never reach a result, whatever they hold.
- * Softmax state and sums are fp32; the weights p_ij are rounded to bf16 for the tensor cores, and so
- * are E4M3 codes times their scales before they are used.
+ * Softmax state and sums are fp32; the weights p_ij are rounded to bf16 for the tensor cores.  With E4M3
+ * rows, codes times scales become bf16 for K and fp16 for V, there with a power of two of its own for
+ * each 128 keys of a sequence and head (values below 2^-26 of the largest there lose bits), and the
+ * weights are rounded to fp16.
  * workspace: fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype) bytes, 256-byte aligned, its
  * first 512 bytes zero-filled before first use (and again after FL_ERR_TIMEOUT); two calls that may
  * overlap on the GPU need one each.  One kernel; E4M3 runs a second one in front. */

@@ -7,8 +7,11 @@ Notation: p_j = exp(x_j - max x), x_j = scale q.k_j, o = sum p_j v_j / sum p_j, 
 - Prefill rounds each weight p_j to bf16 for the tensor cores: each term moves by at most 2^-8 of itself, so o by
   at most 2^-8 A.  Scaled E4M3 keys are rounded to bf16 first: held against the definition with these rounded keys
   that adds nothing; against the exact ones a logit moves by at most 2^-8 scale sum_d |q_d k_d|.  With E4M3 the
-  weights and the scaled values become fp16: each is rounded by at most 2^-11 (2^-10 A together; fp16's range: values
-  below 2^-26 of a key tile's largest, or weights below 2^-21, lose less than 2^-38 of the largest).  Decode rounds the weights to fp16 (E4M3 cache) or splits them
+  weights and the scaled values become fp16: each is rounded by at most 2^-11 (2^-10 A together), or below fp16's
+  normal range by at most 2^-25.  Weights are 2^(7 + b_j - m) p_j there and values 2^-b_j v_j, b_j the power of the key's
+  tile and 2^m at most the largest 2^b_j p_j of the row: so a weight p_j moves by at most 2^-32 2^-b_j max 2^b p and the
+  output by 2^-32 (max 2^b p) sum_j 2^-b_j |v_j|, over the keys that the row sees; the values' part is
+  2^-25 sum_j 2^b_j p_j (p as a part of the row's sum in both).  Decode rounds the weights to fp16 (E4M3 cache) or splits them
   into two bf16 values (bf16 cache): 2^-11 A covers both (2^-16 for the split).
 - A logit is a sum of 128 exact products in fp32: |dx| <= 130 * 2^-24 * scale sum_d |q_d k_d| (the
   accumulation, the scaling and the multiplication by log2 e), plus 2^-21 for exp2 itself and 2^-24 |x_j - max|
@@ -46,22 +49,38 @@ def rounded(x):
     return x.float().bfloat16().double()
 
 
-def attend(q, k, v, scale, weight_step, causal=False, key_step=0.0):
+def tile_powers(scales):
+    """b of each key and head, [kv heads, tokens], from the scales [tokens, kv heads] of a sequence's values: two to the b
+    is 2^-4 of the largest scale's power of two in the key's tile of 128."""
+    n = scales.shape[0]
+    tiles = torch.nn.functional.pad(scales.double(), (0, 0, 0, -n % 128)).view(-1, 128, scales.shape[1]).amax(1)
+    b = torch.where(tiles > 0, torch.floor(torch.log2(tiles)) - 4, 0.0)
+    return b.repeat_interleave(128, 0)[:n].T
+
+
+def attend(q, k, v, scale, weight_step, causal=False, key_step=0.0, powers=None):
     """q [heads, n, 128]; k, v [kv heads, tokens, 128] (fp64).  Returns (o, tolerance), both [heads, n, 128]."""
     g = q.shape[0] // k.shape[0]
     k, v = k.repeat_interleave(g, 0), v.repeat_interleave(g, 0)
     n, tokens = q.shape[1], k.shape[1]
+    seen = torch.ones(n, tokens, dtype=torch.double, device=q.device)
     x = q @ k.transpose(1, 2) * scale
     mag = q.abs() @ k.abs().transpose(1, 2) * scale
     if causal:
         i = torch.arange(n, device=q.device)[:, None] + tokens - n
         hide = torch.arange(tokens, device=q.device)[None] > i
+        seen.masked_fill_(hide, 0.0)
         x = x.masked_fill(hide, float("-inf"))
         mag = mag.masked_fill(hide, 0.0)
     p = torch.softmax(x, -1)
     o, a = p @ v, p @ v.abs()
     d = (130 * F32 + key_step) * mag.amax(-1, keepdim=True) + 2.0 ** -21 + F32
     tol = BF16 * o.abs() + (weight_step + torch.expm1(2 * d) + 2 * tokens * F32) * a
+    if powers is not None:
+        two_b = torch.exp2(powers.repeat_interleave(g, 0))
+        heavy = p * two_b[:, None]
+        tol += 2.0 ** -32 * heavy.amax(-1, keepdim=True) * (seen @ (v.abs() / two_b[..., None]))
+        tol += 2.0 ** -25 * heavy.sum(-1, keepdim=True)
     return o, tol * (1 + 2 * BF16) + 1e-30  # products of two of the errors
 
 
@@ -150,10 +169,13 @@ def check_prefill(q, k, v, ks, vs, lens, out, causal, scale=D ** -0.5, what=""):
         vv = values(v[rows].reshape(n, kv, D), None if vs is None else vs[rows]).transpose(0, 1)
         qq, got = q[rows].double().reshape(n, heads, D).transpose(0, 1), out[rows].view(n, heads, D).transpose(0, 1)
         if ks is not None:
-            ref, tol = attend(qq, kk, vv, scale, 2 * F16, causal, BF16)
+            powers = tile_powers(vs[rows])
+            ref, tol = attend(qq, kk, vv, scale, 2 * F16, causal, BF16, powers)
             assert_within(got, ref, tol, f"{what} sequence {b} of {n}")
             kk = rounded(kk)
-        ref, tol = attend(qq, kk, vv, scale, BF16 if ks is None else 2 * F16, causal)
+            ref, tol = attend(qq, kk, vv, scale, 2 * F16, causal, powers=powers)
+        else:
+            ref, tol = attend(qq, kk, vv, scale, BF16, causal)
         assert_within(got, ref, tol, f"{what} sequence {b} of {n}")
 
 

@@ -165,6 +165,32 @@ def test_prefill_scale_and_strides():
     check_prefill(q, k8v, v8v, ksv, vsv, [n], out, True, scale=0.3)
 
 
+@pytest.mark.parametrize("shift", [-40, -20, 20, 40])
+def test_prefill_scales_far_apart(shift):
+    """Values of the first 128 keys 2^shift times as large as the others; every row looks at its own key or at one of
+    150 tokens before, by some 80 in the exponent, so both sides count for somebody and neither may swamp the other."""
+    n = 500
+    q, k, v, ks, vs = prompt(n, 2, 1, True, seed=70)
+    at = torch.arange(n, device="cuda")
+    at = torch.where(at % 2 == 0, at, (at - 150).clamp(min=0))
+    q = (8 * values(k.view(n, 1, D), ks).view(n, D)[at]).bfloat16().repeat(1, 2)
+    vs[:128] *= 2.0 ** shift
+    for causal in (True, False):
+        check_prefill(q, k, v, ks, vs, [n], fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs, causal=causal), causal)
+
+
+@pytest.mark.parametrize("shift", [-40, 40])
+def test_prefill_scales_along_a_long_sequence(shift):
+    """The same over more key tiles than a warp's lanes hold powers for, the scales growing or falling all the way."""
+    n = 4500
+    q, k, v, ks, vs = prompt(n, 1, 1, True, seed=71)
+    at = torch.arange(n, device="cuda")
+    at = torch.where(at % 2 == 0, at, (at - 2000).clamp(min=0))
+    q = (8 * values(k.view(n, 1, D), ks).view(n, D)[at]).bfloat16()
+    vs *= torch.exp2(torch.linspace(0, shift, n, device="cuda").round())[:, None]
+    check_prefill(q, k, v, ks, vs, [n], fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs), True)
+
+
 def test_prefill_zero_scales_and_codes():
     """Heads of zeros (scale 0) beside ordinary ones."""
     n = 150
