@@ -158,7 +158,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   const long long key_tiles =
       cu_seqlens == nullptr
           ? static_cast<long long>(M / seq_len) * ((seq_len - 1) / kPreTile + 1) + (M % seq_len + kPreTile - 1) / kPreTile
-          : std::min<long long>(static_cast<long long>(M) / kPreTile + batch, M);  // an upper bound
+          : static_cast<long long>(M) / kPreTile + batch;  // the numbers that tiles can have
   const long long parts = key_tiles * (kPreTile / kCodesRows);
   if (parts > INT32_MAX) return FL_ERR_UNSUPPORTED;
   if (!launch_dependent(e4m3_tiles_kernel, dim3(static_cast<unsigned>(parts), (n_kv_heads - 1) / kCodesHeads + 1), 256, 0, s,

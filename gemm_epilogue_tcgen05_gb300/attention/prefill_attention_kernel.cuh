@@ -832,26 +832,28 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
   constexpr int kParts = kPreTile / kCodesRows;
   const int tile = static_cast<int>(blockIdx.x / kParts), part = static_cast<int>(blockIdx.x % kParts);
   const int h0 = static_cast<int>(blockIdx.y) * kCodesHeads, heads = min(kCodesHeads, n_kv - h0);
-  int row0 = 0, rows = 0, skip = tile;
-  for (int b0 = 0; b0 < batch; b0 += 32) {  // the sequence that holds the tile: each warp looks for itself
-    int first = 0, last = 0;
-    if (b0 + lane < batch) sequence_rows(cu, b0 + lane, seq_len, M, first, last);
-    const int have = last > first ? (last - first - 1) / kPreTile + 1 : 0;
-    int sum = have;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(~0u, sum, o);
-      if (lane >= o) sum += y;
+  // Key tile j of sequence b has number cu[b] / 128 + b + j: no two have the same one, and each warp finds the sequence by
+  // itself, by 32 probes at a time for the last b whose number is not above the tile's.
+  int b = 0, at = tile;
+  auto number = [&](int b) { return min(max(cu[b], 0), M) / kPreTile + b; };
+  if (cu == nullptr) {
+    const int each = (seq_len - 1) / kPreTile + 1;
+    b = tile / each, at = tile - b * each;
+  } else {
+    for (int n = batch; n > 1;) {
+      const int step = (n + 31) / 32;
+      const unsigned below = __ballot_sync(~0u, lane * step < n && number(b + lane * step) <= tile);
+      const int past = (32 - __clz(below) - 1) * step;
+      if (below == 0) return;
+      b += past;
+      n = min(step, n - past);
     }
-    const unsigned who = __ballot_sync(~0u, sum > skip);
-    if (who != 0) {
-      const int from = __ffs(who) - 1;
-      row0 = __shfl_sync(~0u, first + (skip - (sum - have)) * kPreTile, from);
-      rows = min(kPreTile, __shfl_sync(~0u, last, from) - row0);
-      break;
-    }
-    skip -= __shfl_sync(~0u, sum, 31);
+    at -= number(b);
   }
+  int first, last;
+  sequence_rows(cu, b, seq_len, M, first, last);
+  if (at < 0 || at > (last - first - 1) / kPreTile) return;  // a number that nothing has; the same for all threads
+  const int row0 = first + at * kPreTile, rows = min(kPreTile, last - row0);
   if (part * kCodesRows >= rows) return;  // the same for all threads
   const int r = part * kCodesRows + (tid >> 4), c = tid & 15;  // 16 threads a row and head
   const bool there = r < rows;

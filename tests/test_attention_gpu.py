@@ -48,6 +48,33 @@ def test_prefill_many_sequences(fp8):
     check_prefill(q, k, v, ks, vs, lens, out, True)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_of_a_thousand_short_sequences(fp8):
+    """More sequences than a warp probes twice, empty ones and longer ones among them, rows behind the last."""
+    lens = [0 if i % 9 == 4 else 129 + i % 3 if i % 200 == 7 else 1 + i % 2 for i in range(1100)]
+    rows = sum(lens)
+    q, k, v, ks, vs = prompt(rows + 40, 2, 1, fp8, seed=72)
+    out = fl.attention_prefill(q, k, v, cu_seqlens=cu(lens), k_scale=ks, v_scale=vs)
+    long = [i for i, n in enumerate(lens) if n > 2]
+    first = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    for i in long + list(range(0, 1100, 29)):
+        r = slice(first[i], first[i + 1])
+        check_prefill(q[r], k[r], v[r], None if ks is None else ks[r], None if vs is None else vs[r], [lens[i]], out[r], True,
+                      what=f"of {i}:")
+    assert (out[rows:] == 0).all()
+    values_of = values(v[:rows].view(rows, 1, D), None if vs is None else vs[:rows]).view(rows, D)
+    alone = torch.tensor([first[i] for i, n in enumerate(lens) if n == 1], device="cuda")
+    ref = values_of[alone].repeat(1, 2)  # one key: its value, rounded to fp16 (E4M3) and bf16
+    assert ((out[alone].double() - ref).abs() <= (BF16 + 2 * F16) * ref.abs() * (1 + BF16) + 1e-6).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_of_more_sequences_than_rows(fp8):
+    lens = [0] * 700 + [3] + [0] * 60 + [1, 140] + [0] * 9
+    q, k, v, ks, vs = prompt(sum(lens), 4, 2, fp8, seed=73)
+    check_prefill(q, k, v, ks, vs, lens, fl.attention_prefill(q, k, v, cu_seqlens=cu(lens), k_scale=ks, v_scale=vs), True)
+
+
 def test_prefill_more_tiles_than_a_wave():
     lens = [700, 1, 333, 1025, 512, 90, 256, 255]
     q, k, v, _, _ = prompt(sum(lens), 32, 32, False, seed=6)
@@ -299,9 +326,9 @@ def test_decode_batch_sizes(batch, fp8):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_wide_page_table(fp8):
     """A table so wide that the units of all lengths it allows pass 31 bits, with ordinary sequences in it."""
-    lens, width = [700, 0, 65], 1 << 20
-    c = Cache(lens, 2, 16384, fp8, seed=7, max_pages=width)
-    q = randn(3, 4 * D, seed=7)
+    lens, width = [700, 0, 65], 1 << 21
+    c = Cache(lens, 32, 1024, fp8, seed=7, max_pages=width)
+    q = randn(3, 64 * D, seed=7)
     check_decode(q, c, fl.attention_decode(q, *c.args(), **c.scales()))
 
 
