@@ -22,9 +22,9 @@
 // all products before it), so no hand-over is needed.
 //
 // Work: tile (sequence, block of tokens, kv head) by falling block index, so the longest come first whatever the
-// sequences' lengths are (without the causal mask by falling length), each taken by the CTA that is free next
-// (an atomic counter, one tile ahead).  Neighbouring ranks are the heads of one
-// block: K and V are met again by every block of the sequence, and the keys and values of all heads of all
+// sequences' lengths are (without the causal mask by falling length; with many sequences one after the other, each from
+// its last block), each taken by the CTA that is free next (an atomic counter, one tile ahead).  Neighbouring ranks are
+// the heads of one block: K and V are met again by every block of the sequence, and the keys and values of all heads of all
 // sequences can be more than the L2 holds.  So the heads are worked off in groups whose keys and values are at
 // most 32 MB.
 //
@@ -77,7 +77,7 @@ struct alignas(128) PrefillParams {
   const int* cu;
   __nv_bfloat16* O;
   long long ldo;
-  int M, batch, seq_len, causal;
+  int M, batch, seq_len, causal, flat;
   int group, hp, tq;       // query heads of a kv head; heads and tokens of a query tile
   int pairs;               // head packs of a token block: n_kv * group / hp
   int pairs_at_once;       // of which this many are worked off before the next ones begin
@@ -284,7 +284,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const int tpc = 2 * p.tq;
     // Tiers: sequences have blocks [0, blocks) of tpc tokens.  Causal: block j costs about j, tier j is block j of
     // each sequence that has one.  Full mask: a block costs as much as its sequence has key tiles, tier j is all
-    // blocks of the sequences with j + 1 key tiles.
+    // blocks of the sequences with j + 1 key tiles.  Flat: all blocks are one tier in the order of the sequences, so
+    // that there is one walk over the sequences instead of one a tier.
     auto length_of = [&](int b) {
       int first, last;
       sequence_rows(p.cu, b, p.seq_len, p.M, first, last);
@@ -308,8 +309,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     }
     tiers = __reduce_max_sync(~0u, tiers);
     blocks = __reduce_add_sync(~0u, blocks);
+    if (p.flat) tiers = 1;
     int tier = tiers - 1;
-    unsigned above = 0;                                      // blocks of higher tiers
+    unsigned before = 0;                                     // blocks before sequence `from` of this tier
+    int from = 0;                                            // where the last block was found: ranks only rise
     int pair0 = 0, n_pairs = min(p.pairs, p.pairs_at_once);  // the group of heads
     unsigned rank0 = 0;                                      // its first rank (the launch keeps ranks below 2^30)
     bool more = true, long_before = false;
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         rank0 += blocks * n_pairs;
         pair0 += n_pairs;
         n_pairs = min(p.pairs - pair0, p.pairs_at_once);
-        tier = tiers - 1, above = 0;
+        tier = tiers - 1, before = 0, from = 0;
       }
       const unsigned block = (rank - rank0) / n_pairs;
       const int pair = pair0 + static_cast<int>(rank - rank0 - block * n_pairs);
@@ -334,28 +337,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       int seq = -1, in = 0;
 #pragma unroll 1
       while (tier >= 0) {
-        unsigned upto = above;
 #pragma unroll 1
-        for (int b0 = 0; b0 < p.batch && seq < 0; b0 += 32) {
+        for (; from < p.batch; from += 32) {
           int reach = my_reach, count = my_count;
-          if (b0 > 0) measure(b0 + lane, reach, count);
-          const unsigned have = p.causal ? reach > tier : reach == tier + 1 ? count : 0;
+          if (from > 0) measure(from + lane, reach, count);
+          const unsigned have = p.flat ? count : p.causal ? reach > tier : reach == tier + 1 ? count : 0;
           const unsigned all = __reduce_add_sync(~0u, have);
-          if (block < upto + all) {
+          if (block < before + all) {
             unsigned sum = have;  // inclusive sum over the lanes
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
               const unsigned y = __shfl_up_sync(~0u, sum, o);
               if (lane >= o) sum += y;
             }
-            const int src = __ffs(__ballot_sync(~0u, upto + sum > block)) - 1;
-            seq = b0 + src;
-            in = static_cast<int>(block - upto - __shfl_sync(~0u, sum - have, src));
+            const int src = __ffs(__ballot_sync(~0u, before + sum > block)) - 1;
+            seq = from + src;
+            in = static_cast<int>(block - before - __shfl_sync(~0u, sum - have, src));
+            break;
           }
-          upto += all;
+          before += all;
         }
         if (seq >= 0) break;
-        above = upto;
+        from = 0;
         --tier;
       }
       PrefillTile t = {};
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         sequence_rows(p.cu, seq, p.seq_len, p.M, first, last);
         t.row0 = first;
         t.len = last - first;
-        t.tok0 = (p.causal ? tier : in) * tpc;
+        t.tok0 = (!p.causal ? in : p.flat ? (t.len - 1) / tpc - in : tier) * tpc;
         const int packs = p.group / p.hp;
         t.kvh = pair / packs;
         t.head0 = t.kvh * p.group + (pair - t.kvh * packs) * p.hp;

@@ -75,6 +75,18 @@ def test_prefill_of_more_sequences_than_rows(fp8):
     check_prefill(q, k, v, ks, vs, lens, fl.attention_prefill(q, k, v, cu_seqlens=cu(lens), k_scale=ks, v_scale=vs), True)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("batch", [32, 33, 64, 65, 150])
+def test_prefill_order_of_the_tiles(batch, causal):
+    """Around the batches from which on the tiles come in another order; a long sequence last, first or in the middle."""
+    for at in (0, batch // 2, batch - 1):
+        lens = [1 + 37 * i % 150 for i in range(batch)]
+        lens[at] = 2100
+        q, k, v, _, _ = prompt(sum(lens), 4, 2, False, seed=batch)
+        out = fl.attention_prefill(q, k, v, cu_seqlens=cu(lens), causal=causal)
+        check_prefill(q, k, v, None, None, lens, out, causal)
+
+
 def test_prefill_more_tiles_than_a_wave():
     lens = [700, 1, 333, 1025, 512, 90, 256, 255]
     q, k, v, _, _ = prompt(sum(lens), 32, 32, False, seed=6)
