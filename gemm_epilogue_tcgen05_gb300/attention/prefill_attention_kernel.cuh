@@ -34,8 +34,10 @@
 // E4M3: a first kernel writes K as bf16 (code times scale, 8 bits where the code carries 4) and V as fp16 times 2^-b,
 // b from the largest scale of 128 keys and a head, so that the largest possible value is in [2^12, 2^14).  The logits of
 // a key tile get b on top: weights are 2^(x + b - m + 7) in fp16, m the running maximum of x + b, and meet V 2^-b in O
-// at one common power whatever the tiles' scales are; the sum l takes each tile's weights times 2^-b.  (b counts from
-// the sequence's first tile, so that 2^-b stays in range.)  Measured for 4 x 2048 tokens, 32 query and 8 kv heads:
+// at one common power whatever the tiles' scales are.  The sum l has a maximum mx of its own, of x alone: each tile's
+// weights come to it times 2^(m - b - 7 - mx).  A tile whose values are all zero has no power and leaves m as it is: with
+// any power of its own its logits would raise m, and push the weights of small values in other tiles below fp16's range
+// (128 such keys in front of values of 1e-5: relative error 0.2).  Measured for 4 x 2048 tokens, 32 query and 8 kv heads:
 // 311 us with scales inside the softmax (two multiplications and two shared-memory reads for each query and key, reads
 // that the tensor cores need for themselves), 123 us with fp16 keys (11 bits, but queries that have to become fp16,
 // too), 110.5 us so, 105 us with bf16 values and weights, whose roundings make the error 1.8 times that of a bf16
@@ -59,6 +61,7 @@ constexpr float kPreNone = -3e38f;                 // a maximum over nothing: an
 constexpr float kPreLazy = 8.f;
 constexpr uint64_t kPreDrainNs = 1000000000;       // for copies and products in flight, whatever the limit of the waits
 constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted by 2^7 in fp16 (2^8 more: kPreLazy)
+constexpr float kPreZero = -16384.f;               // E4M3: stands for the power of a key tile whose values are all zero
 
 // Where a wait gave up (recorded in the workspace's status record).
 enum : int {
@@ -649,11 +652,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int lim_lo = __reduce_min_sync(~0u, lim);              // last key that every row of this warp sees
       float m = kPreNone, l = 0.f;
+      float mx = kPreNone;         // E4M3: the maximum that l is held at (m is that of O)
       float powers = powers_next;  // E4M3: of key tile i in lane i % 32
-      const float b0 = FP8 ? __shfl_sync(~0u, powers, 0) : 0.f;
       for (int i = 0; i < n; ++i) {
           if (FP8 && i > 0 && (i & 31) == 0) powers = load_powers(t, n, i);
-          const float b = FP8 ? __shfl_sync(~0u, powers, i & 31) - b0 : 0.f;
+          const float b = FP8 ? __shfl_sync(~0u, powers, i & 31) : 0.f;
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
@@ -671,24 +674,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
                   if (h * 32 + j > cols) x[h][j] = __float_as_uint(-INFINITY);
               }
           }
-          float mx[4];
+          float t4[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(x[j][0]);
+          for (int j = 0; j < 4; ++j) t4[j] = __uint_as_float(x[j][0]);
 #pragma unroll
           for (int j = 1; j < 31; j += 2)
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-              mx[h] = max3(mx[h], __uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1]));
+              t4[h] = max3(t4[h], __uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1]));
 #pragma unroll
-          for (int h = 0; h < 4; ++h) mx[h] = fmaxf(mx[h], __uint_as_float(x[h][31]));
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          if (FP8) top += b;
-          const bool rise = top > m + kPreLazy;
-          if (__any_sync(~0u, rise)) {
-            const float up = rise ? top : m;
+          for (int h = 0; h < 4; ++h) t4[h] = fmaxf(t4[h], __uint_as_float(x[h][31]));
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c, lifted = FP8 ? top + b : top;
+          const bool rise = lifted > m + kPreLazy, rise_l = FP8 && top > mx + kPreLazy;
+          if (__any_sync(~0u, rise || rise_l)) {
+            const float up = rise ? lifted : m;
             const float down = ex2(m - up);
             m = up;
-            l *= down;
+            if (FP8) {
+              const float up_l = rise_l ? top : mx;
+              l *= ex2(mx - up_l);
+              mx = up_l;
+            } else {
+              l *= down;
+            }
             if (i > 0) {  // O of the key tiles before is complete: S of this one was committed behind it
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -701,7 +709,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               }
             }
           }
-          const float minus = FP8 ? (kPreLift + b) - m : -m;
+          const float at = FP8 && b == kPreZero ? mx : m - b;  // E4M3: what the tile's weights are held at, 2^7 above
+          const float minus = FP8 ? kPreLift - at : -m;
           const uint64_t c2 = f2(c, c), m2 = f2(minus, minus);
           uint64_t l0 = 0, l1 = 0;
 #pragma unroll
@@ -722,7 +731,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           float s0, s1, s2, s3;
           f2_split(l0, s0, s1);
           f2_split(l1, s2, s3);
-          l += FP8 ? ((s0 + s1) + (s2 + s3)) * ex2(-b) : (s0 + s1) + (s2 + s3);
+          l += FP8 ? ((s0 + s1) + (s2 + s3)) * ex2((at - kPreLift) - mx) : (s0 + s1) + (s2 + s3);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -731,7 +740,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       if (!ok) break;
       const bool have = __all_sync(~0u, get_tile(k + 1, next));
       if (FP8 && have) powers_next = load_powers(next, s ? next.n1 : next.n0, 0);
-      const float inv = (FP8 ? ex2(b0) : 1.f) / l;
+      const float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;
       if (n > 0) {
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
@@ -910,7 +919,8 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
       const long long to = (row * n_kv + h0 + j0 + i) * (kHeadDim / 8) + c;
       reinterpret_cast<uint4*>(K16)[to] = codes(k[i], sk[i], [](float x, float y) { return pack_bf16x2(x, y); });
       reinterpret_cast<uint4*>(V16)[to] = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
-      if (part == 0 && tid == 0) powers[static_cast<long long>(row0) * n_kv + h0 + j0 + i] = static_cast<float>(b);
+      if (part == 0 && tid == 0)
+        powers[static_cast<long long>(row0) * n_kv + h0 + j0 + i] = bits == 0 ? kPreZero : static_cast<float>(b);
     }
   }
 }
