@@ -78,7 +78,7 @@ extern "C" size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, in
   using namespace fl;
   if (M < 0 || n_kv_heads < 0) return 0;
   // the status record and the work counters; for E4M3 also K as bf16, V as fp16 and a power for each key tile (kept at
-  // its first row)
+  // its first row; where it has single keys, the other rows hold which)
   const size_t rows = static_cast<size_t>(M) * n_kv_heads;
   return 2 * kWsStatusBytes + (kv_dtype == FL_E4M3 ? rows * (kHeadDim * (sizeof(__nv_bfloat16) + sizeof(__half)) + sizeof(float)) : 0);
 }
@@ -142,6 +142,10 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
     __half* vw = reinterpret_cast<__half*>(kw + static_cast<size_t>(M) * kv_width);
     p.powers = reinterpret_cast<const float*>(vw + static_cast<size_t>(M) * kv_width);
     k16 = kw, v16 = vw, ld16 = kv_width;
+    p.codes = static_cast<const uint8_t*>(V);
+    p.v_scale = v_scale;
+    p.ld_codes = ldkv;
+    p.ld_scale = lds;
   }
   if (!encode_q(&p.map_q, Q, n_heads, M, ldq, p.hp, p.tq) ||
       !encode_2d(&p.map_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k16, kv_width, M, ld16, 64, kPreTile,

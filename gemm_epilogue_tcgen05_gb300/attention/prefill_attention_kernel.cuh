@@ -32,12 +32,20 @@
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
 //
 // E4M3: a first kernel writes K as bf16 (code times scale, 8 bits where the code carries 4) and V as fp16 times 2^-b,
-// b from the largest scale of 128 keys and a head, so that the largest possible value is in [2^12, 2^14).  The logits of
+// b from the largest scale of 128 keys and a head, so that the largest possible value is in [2^14, 2^16).  The logits of
 // a key tile get b on top: weights are 2^(x + b - m + 7) in fp16, m the running maximum of x + b, and meet V 2^-b in O
 // at one common power whatever the tiles' scales are.  The sum l has a maximum mx of its own, of x alone: each tile's
-// weights come to it times 2^(m - b - 7 - mx).  A tile whose values are all zero has no power and leaves m as it is: with
-// any power of its own its logits would raise m, and push the weights of small values in other tiles below fp16's range
-// (128 such keys in front of values of 1e-5: relative error 0.2).  Measured for 4 x 2048 tokens, 32 query and 8 kv heads:
+// weights come to it times 2^(m - b - 7 - mx).  A tile whose values are all zero gets a power of 2^-90, and its sum is
+// taken at mx: with an ordinary power its logits would raise m and push the weights of small values in other tiles below
+// fp16's range (128 such keys in front of values of 1e-5: relative error 0.2).
+//
+// b stands for the tile's ordinary keys, whose scales lie within kPreWindow powers of two, so that each value keeps its
+// bits whatever another key's scale is, be it later in the sequence.  What lies outside (attention sinks with tiny values,
+// outliers) are single keys: their V is zero in the tile, and the softmax warps take their columns out of S and add
+// p_j v_j in fp32 from the codes to O, which they begin with zeros.  (One power for all keys of a tile lost the bits of
+// the small ones: a later scale 2^32 times the others' put an error of 4 % on the rows before it, 2^40 all of them.)
+//
+// Measured for 4 x 2048 tokens, 32 query and 8 kv heads:
 // 311 us with scales inside the softmax (two multiplications and two shared-memory reads for each query and key, reads
 // that the tensor cores need for themselves), 123 us with fp16 keys (11 bits, but queries that have to become fp16,
 // too), 110.5 us so, 105 us with bf16 values and weights, whose roundings make the error 1.8 times that of a bf16
@@ -61,7 +69,14 @@ constexpr float kPreNone = -3e38f;                 // a maximum over nothing: an
 constexpr float kPreLazy = 8.f;
 constexpr uint64_t kPreDrainNs = 1000000000;       // for copies and products in flight, whatever the limit of the waits
 constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted by 2^7 in fp16 (2^8 more: kPreLazy)
-constexpr float kPreZero = -16384.f;               // E4M3: stands for the power of a key tile whose values are all zero
+// E4M3: the power of a key tile whose values are all zero, and of a single key of that kind: low enough to leave other
+// weights alone, high enough for 2^(m - mx) to stay in fp32's range, and no whole number, so that no other tile has it.
+constexpr float kPreZero = -90.5f;
+constexpr int kPreWindow = 13;                     // E4M3: powers of two that the scales of a tile's ordinary keys span
+constexpr int kPreRoom = 6;                        // E4M3: the largest of these scales times 2^-b is in [2^6, 2^7)
+// E4M3: what a tile's power carries on top, times kPreMark: it has single keys, and its first key is one.
+constexpr float kPreMark = 65536.f;
+enum : int { PRE_SINGLE = 1, PRE_SINGLE_FIRST = 2 };
 
 // Where a wait gave up (recorded in the workspace's status record).
 enum : int {
@@ -75,7 +90,10 @@ struct alignas(128) PrefillParams {
   CUtensorMap map_v;  // the same, E4M3: fp16
   const __nv_bfloat16* V;  // the rows map_v covers
   long long ldv;
-  const float* powers;  // E4M3: [first row of a key tile][n_kv]: b of V * 2^-b
+  const float* powers;  // E4M3: [first row of a key tile][n_kv]: b of V * 2^-b, and marks; other rows: 1 for a single key
+  const uint8_t* codes;  // E4M3: V and its scales as given, for single keys
+  const float* v_scale;
+  long long ld_codes, ld_scale;
   int n_kv;
   const int* cu;
   __nv_bfloat16* O;
@@ -142,6 +160,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  tmem_ld_wait();
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -487,12 +514,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       }
       __syncwarp();
     };
-    auto pv = [&](int s, int st, bool first, bool last) {  // O_s (+)= P_s V
+    auto pv = [&](int s, int st, bool first, bool last) {  // O_s (+)= P_s V; E4M3: += always, the softmax warps begin O
       if (one) {
         const uint64_t bd = v_desc + st * (2 * kStep16);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_bf16_ts(tmem + 256 + s * kHeadDim, tmem + s * kPreTile + k * 8, bd + k * 128, idesc_pv, !first || k != 0);
+          mma_bf16_ts(tmem + 256 + s * kHeadDim, tmem + s * kPreTile + k * 8, bd + k * 128, idesc_pv, FP8 || !first || k != 0);
         if (last) mma_commit(&bar.o_full[s]);
       }
       __syncwarp();
@@ -642,6 +669,68 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const long long tile = i + lane;
       return tile < n ? __ldg(p.powers + (t.row0 + tile * kPreTile) * p.n_kv + t.kvh) : 0.f;
     };
+    // E4M3: the single keys of a tile, in fp32 from their codes and scales: into l and O, and out of S.  O is complete: S
+    // of this tile was committed behind the products before.
+    auto single_keys = [&](const PrefillTile& t, int i, bool first_too, int lim, float& m, float& mx, float& l) {
+      const long long key0 = t.row0 + static_cast<long long>(i) * kPreTile;
+      const int keys = min(kPreTile, t.len - i * kPreTile);
+      uint32_t which[4], scales[4];  // of key 32 h + lane
+      float mark[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {  // all loads on their way together
+        const long long at = key0 + min(h * 32 + lane, keys - 1);
+        mark[h] = __ldcg(p.powers + at * p.n_kv + t.kvh);
+        scales[h] = __float_as_uint(__ldcg(p.v_scale + at * p.ld_scale + t.kvh));
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int j = h * 32 + lane;
+        which[h] = __ballot_sync(~0u, j == 0 ? first_too : j < keys && mark[h] != 0.f);
+      }
+      tmem_st_wait();  // O may have been begun just now
+#pragma unroll 1
+      for (int j = 0; j < kPreTile; ++j) {
+        const int h = j >> 5;
+        const uint32_t w = (h < 2 ? (h == 0 ? which[0] : which[1]) : (h == 2 ? which[2] : which[3])) >> (j & 31);
+        if (w == 0) j |= 31;
+        if ((w & 1u) == 0) continue;
+        const uint32_t bits = __shfl_sync(~0u, h < 2 ? (h == 0 ? scales[0] : scales[1]) : (h == 2 ? scales[2] : scales[3]), j & 31);
+        const int field = static_cast<int>(bits >> 23) & 255;
+        const uint8_t* from = p.codes + (key0 + j) * p.ld_codes + t.kvh * kHeadDim;
+        uint4 codes = *reinterpret_cast<const uint4*>(from);
+        const bool sees = i * kPreTile + j <= lim;
+        const float logit = tmem_ld1(s_tmem + j) * c, x = sees ? logit : -INFINITY;
+        tmem_st1(s_tmem + j, -INFINITY);
+        const int power = max(field - (127 + kPreRoom), -120);
+        const float up = fmaxf(m, x + (bits << 1 != 0 ? static_cast<float>(power) : kPreZero)), up_l = fmaxf(mx, x);
+        const float down = ex2(m - up);
+        l = l * ex2(mx - up_l) + ex2(x - up_l);
+        mx = up_l;
+        const float weight = ex2((x + static_cast<float>(power)) - (up - kPreLift));
+        const float scale = __uint_as_float(bits) * __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
+#pragma unroll 2
+        for (int d = 0; d < kHeadDim; d += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_tmem + d, o);
+          const uint32_t four[4] = {codes.x, codes.y, codes.z, codes.w};
+          if (d + 16 < kHeadDim) codes = *reinterpret_cast<const uint4*>(from + d + 16);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint32_t two;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>(four[e >> 1] >> ((e & 1) * 16))));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+            float y0 = __uint_as_float(o[e * 2]) * down, y1 = __uint_as_float(o[e * 2 + 1]) * down;
+            if (sees) y0 = fmaf(weight, f.x * scale, y0), y1 = fmaf(weight, f.y * scale, y1);  // a NaN only for who sees it
+            o[e * 2] = __float_as_uint(y0), o[e * 2 + 1] = __float_as_uint(y1);
+          }
+          tmem_st16(o_tmem + d, o);
+        }
+        tmem_st_wait();
+        m = up;
+      }
+      tmem_st_wait();
+    };
     float powers_next = 0.f;
     int s_uses = 0, o_uses = 0;
     bool ok = true;
@@ -654,9 +743,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       float m = kPreNone, l = 0.f;
       float mx = kPreNone;         // E4M3: the maximum that l is held at (m is that of O)
       float powers = powers_next;  // E4M3: of key tile i in lane i % 32
-      for (int i = 0; i < n; ++i) {
+      if (FP8 && n > 0) {  // O begins here, for what single keys bring to it ahead of the first product
+        uint32_t none[16] = {0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tmem_st16(o_tmem + j * 16, none);
+      }
+      int i = 0, single_done = -1;
+      bool begun = false;  // E4M3: single keys are in O before the first product
+      for (;;) {
+        for (; i < n; ++i) {
           if (FP8 && i > 0 && (i & 31) == 0) powers = load_powers(t, n, i);
-          const float b = FP8 ? __shfl_sync(~0u, powers, i & 31) : 0.f;
+          float b = FP8 ? __shfl_sync(~0u, powers, i & 31) : 0.f;
+          if (FP8 && b > kPreMark / 2) {
+            if (i != single_done) break;  // its single keys come first, behind this loop: in it they cost 3 % of the time
+            b -= rintf(b / kPreMark) * kPreMark;
+          }
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
@@ -697,7 +798,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             } else {
               l *= down;
             }
-            if (i > 0) {  // O of the key tiles before is complete: S of this one was committed behind it
+            if (i > 0 || (FP8 && begun)) {  // O of the key tiles before is complete: S of this one was committed behind it
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 uint32_t o[16];
@@ -736,15 +837,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.p_full[s]);
+        }
+        if (!FP8 || !ok || i >= n) break;
+        if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;  // the loop waits for the same phase again
+        tc_fence_after();
+        const int marks = __float2int_rn(__shfl_sync(~0u, powers, i & 31) / kPreMark);
+        single_keys(t, i, (marks & PRE_SINGLE_FIRST) != 0, lim, m, mx, l);
+        begun = true;
+        single_done = i;
       }
       if (!ok) break;
       const bool have = __all_sync(~0u, get_tile(k + 1, next));
       if (FP8 && have) powers_next = load_powers(next, s ? next.n1 : next.n0, 0);
-      const float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;
       if (n > 0) {
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
         tc_fence_after();
+        const float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;  // E4M3: O is held at m - 7, l at mx
         const volatile PrefillTile& said = bar.tile[k % kPreRing];
         const int bad_lo = said.bad_lo, bad_hi = said.bad_hi;
         // A thread has a row; lines of global memory want a few rows each, all of 128 bytes.  So 16-byte pieces go
@@ -823,8 +932,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   if (threadIdx.x == 0 && bar.abort_flag != 0) record_failure(p.status, bar.abort_flag, 0);
 }
 
-// E4M3 codes of K and V times their scales, for the kernel above: K as bf16, V as fp16 times 2^-b, with b from V's
-// largest finite scale in the key tile (128 rows of a sequence, from its first) and head.  Bound by memory: 1 byte in
+// E4M3 codes of K and V times their scales, for the kernel above: K as bf16, V as fp16 times 2^-b, with b for each key
+// tile (128 rows of a sequence, from its first) and head: from V's largest finite scale where the tile's scales lie
+// within kPreWindow powers of two, else from the window of that width that holds most of its keys.  The keys outside it
+// are written as zeros and marked as single keys.  Bound by memory: 1 byte in
 // and 2 out for each value.  A CTA takes 16 rows of a key tile for up to 32 heads at a time, a thread 8 codes (16 bytes
 // out; with 16 codes each store left half sectors to the next one); the scales of the whole tile are read by each of
 // its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18.5 instead of
@@ -834,9 +945,13 @@ constexpr int kCodesRows = 16, kCodesHeads = 32;
 __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
     const uint8_t* K, const uint8_t* V, const float* ks, const float* vs, long long ld, long long lds, const int* cu,
     int batch, int seq_len, int M, int n_kv, __nv_bfloat16* K16, __half* V16, float* powers) {
-  __shared__ uint32_t top[kCodesHeads];
+  __shared__ uint32_t top[kCodesHeads], low[kCodesHeads];  // largest and smallest finite scale of V, as bit patterns
+  __shared__ float power[kCodesHeads];
+  __shared__ int window[kCodesHeads];  // exponent field of its top, -1 where it holds all keys
+  __shared__ unsigned most;
+  __shared__ short fields[kPreTile];
   const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < kCodesHeads) top[tid] = 0;
+  if (tid < kCodesHeads) top[tid] = 0, low[tid] = ~0u;
   if (cu != nullptr && tid <= batch) asm volatile("prefetch.global.L2 [%0];" ::"l"(cu + tid));
   griddep_wait();
   griddep_launch_dependents();
@@ -887,15 +1002,46 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
   fetch(0);
   {
     const int each = 256 / heads, j = tid % heads;
-    uint32_t largest = 0;
+    uint32_t largest = 0, smallest = ~0u;
     if (tid < each * heads)
       for (int q = tid / heads; q < rows; q += each) {
         const float x = fabsf(__ldg(vs + (row0 + q) * lds + h0 + j));
-        largest = max(largest, x < INFINITY ? __float_as_uint(x) : 0u);
+        if (x < INFINITY) largest = max(largest, __float_as_uint(x)), smallest = min(smallest, __float_as_uint(x));
       }
-    if (largest != 0) atomicMax(&top[j], largest);
+    if (smallest != ~0u) atomicMax(&top[j], largest), atomicMin(&low[j], smallest);
   }
   __syncthreads();
+  bool wide = false;
+  if (tid < heads) {
+    const int field = static_cast<int>(top[tid] >> 23);
+    wide = top[tid] != 0 && field - static_cast<int>(low[tid] >> 23) >= kPreWindow;
+    power[tid] = top[tid] == 0 ? kPreZero : static_cast<float>(max(field - (127 + kPreRoom), -120));
+    window[tid] = wide ? field : -1;
+  }
+  if (__syncthreads_or(wide)) {
+#pragma unroll 1
+    for (int j = 0; j < heads; ++j) {
+      if (window[j] < 0) continue;  // the same for all threads
+      if (tid == 0) most = 0;
+      if (tid < kPreTile) {
+        const uint32_t bits = tid < rows ? __float_as_uint(fabsf(vs[(row0 + tid) * lds + h0 + j])) : 0u;
+        fields[tid] = bits == 0 || bits >= 0x7F800000u ? -1 : static_cast<short>(bits >> 23);
+      }
+      __syncthreads();
+      if (tid < rows && fields[tid] >= 0) {
+        const int mine = fields[tid];
+        unsigned n = 0;
+        for (int q = 0; q < rows; ++q) n += fields[q] >= max(mine - (kPreWindow - 1), 0) && fields[q] <= mine;
+        atomicMax(&most, n << 8 | mine);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        window[j] = static_cast<int>(most & 255u);
+        power[j] = static_cast<float>(max(window[j] - (127 + kPreRoom), -120));
+      }
+    }
+    __syncthreads();
+  }
   for (int j0 = 0; j0 < heads; j0 += kTogether) {
     if (j0 > 0) fetch(j0);
 #pragma unroll
@@ -912,15 +1058,22 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
         }
         return make_uint4(out[0], out[1], out[2], out[3]);
       };
-      const uint32_t bits = top[j0 + i];
-      // 448 * scale * 2^-b is below 2^14
-      const int b = bits == 0 ? 0 : min(max(static_cast<int>(bits >> 23) - 127 - 4, -120), 120);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - b) << 23);
+      const float b = power[j0 + i];
+      const int win = window[j0 + i];
+      const uint32_t bits = __float_as_uint(fabsf(sv[i]));
+      const int field = static_cast<int>(bits >> 23);
+      const bool single = win >= 0 && field < 255 && (bits == 0 || field > win || field <= win - kPreWindow);
+      // 448 * scale * 2^-b is below 2^16 * 0.875
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(b)) << 23);
       const long long to = (row * n_kv + h0 + j0 + i) * (kHeadDim / 8) + c;
       reinterpret_cast<uint4*>(K16)[to] = codes(k[i], sk[i], [](float x, float y) { return pack_bf16x2(x, y); });
-      reinterpret_cast<uint4*>(V16)[to] = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
-      if (part == 0 && tid == 0)
-        powers[static_cast<long long>(row0) * n_kv + h0 + j0 + i] = bits == 0 ? kPreZero : static_cast<float>(b);
+      uint4 v16 = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
+      if (single) v16 = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(V16)[to] = v16;
+      if (c == 0 && (r == 0 || win >= 0))
+        powers[row * n_kv + h0 + j0 + i] =
+            r == 0 ? b + kPreMark * ((win >= 0 ? PRE_SINGLE : 0) | (single ? PRE_SINGLE_FIRST : 0))
+                   : single ? 1.f : 0.f;
     }
   }
 }

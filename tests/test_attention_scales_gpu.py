@@ -2,21 +2,23 @@
 
 The tolerance is the definition's, it knows nothing of how the kernel groups keys.  With p_j the weights of a row (their
 sum 1), s_j the scales of V and c_j its codes:
-- the output is rounded to bf16 (2^-8 |o|), weights and values to fp16 (2^-11 each), logits and sums as attention_utils
-  derives them; the keys are taken as rounded to bf16;
-- a weight may also be lost below fp16's range, by half of its smallest step, 2^-25.  Weights carry a power of two of
-  their key's scale there: 2^b_j, 2^-4 <= s_j 2^-b_j < 2^7, and the largest of a row is held at 2^7 at least.  So a weight
-  moves by at most 2^-32 2^-b_j max_i(p_i 2^b_i) <= 2^-28 2^-b_j max_i(p_i s_i), and o by 2^-28 max_i(p_i s_i) times the
-  sum of |c_j| s_j 2^-b_j <= 2^7 |c_j| over the keys that the row sees: 2^-21 max_i(p_i s_i) sum_j |c_j|.
+- the output is rounded to bf16 (2^-8 |o|), logits and sums as attention_utils derives them; the keys are taken as rounded
+  to bf16;
+- values become fp16 times 2^-b_j with 2^-6 <= s_j 2^-b_j < 2^7: the smallest code, 2^-9, is 2^-15 at least there, and
+  half a step of fp16's smallest numbers, 2^-25, is 2^-10 of it; larger ones lose less;
+- weights become fp16: 2^-11 of each, or half a step of the smallest numbers, 2^-25.  They carry their key's 2^b_j there
+  and the largest of a row is held at 2^7 at least.  So the latter moves a weight by at most
+  2^-32 2^-b_j max_i(p_i 2^b_i) <= 2^-26 2^-b_j max_i(p_i s_i), and o by 2^-26 max_i(p_i s_i) times the sum of
+  |c_j| s_j 2^-b_j <= 2^7 |c_j| over the keys that the row sees: 2^-19 max_i(p_i s_i) sum_j |c_j|.
 """
 import pytest
 import torch
 
 import gemm_epilogue_tcgen05_gb300 as fl
-from attention_utils import D, F16, assert_within, attend, quantise, rounded, values
+from attention_utils import D, F16, assert_within, attend, cu, quantise, rounded, values
 
 pytestmark = pytest.mark.gpu
-INF = float("inf")
+INF, NAN = float("inf"), float("nan")
 
 
 def randn(*shape, seed=0, std=1.0):
@@ -43,7 +45,7 @@ def check(q, k, v, ks, vs, out, causal, rows=None, what=""):
     kk = rounded(values(k.reshape(n, kv, D), ks)).transpose(0, 1)
     vv = values(v.reshape(n, kv, D), vs).transpose(0, 1)
     qq = q.double().reshape(n, heads, D).transpose(0, 1)
-    ref, tol = attend(qq, kk, vv, D ** -0.5, 2 * F16, causal)
+    ref, tol = attend(qq, kk, vv, D ** -0.5, 3 * F16, causal)
     g = heads // kv
     codes = v.reshape(n, kv, D).view(torch.float8_e4m3fn).double()
     x = qq @ kk.repeat_interleave(g, 0).transpose(1, 2) * D ** -0.5
@@ -52,7 +54,7 @@ def check(q, k, v, ks, vs, out, causal, rows=None, what=""):
         seen = seen.tril()
         x = x.masked_fill(seen == 0, -INF)
     largest = (torch.softmax(x, -1) * vs.double().T.repeat_interleave(g, 0)[:, None]).amax(-1, keepdim=True)
-    tol += 2.0 ** -21 * largest * (seen @ codes.abs().transpose(0, 1).repeat_interleave(g, 0))
+    tol += 2.0 ** -19 * largest * (seen @ codes.abs().transpose(0, 1).repeat_interleave(g, 0))
     got = out.view(n, heads, D).transpose(0, 1)
     rows = slice(None) if rows is None else rows
     assert_within(got[:, rows], ref[:, rows], tol[:, rows], what)
@@ -85,3 +87,132 @@ def test_no_values_at_all():
     vs[:] = 0.0
     for causal in (True, False):
         assert (fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs, causal=causal) == 0).all()
+
+
+# ---------------------------------------------------------------- keys whose scale is far from the others' of their tile
+@pytest.mark.parametrize("factor", [2.0 ** 12, 2.0 ** 28, 2.0 ** 32, 2.0 ** 40, 1e30])
+@pytest.mark.parametrize("at", [5, 120, 127, 128, 200])
+def test_a_later_scale_reaches_no_earlier_row(at, factor):
+    """A huge scale of a key's values: rows before it are what they are without it, to the rounding."""
+    n = 260
+    q, k, v, ks, vs = prompt(n, 4, 2, seed=110)
+    vs[at, 0] *= factor
+    out = fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs)
+    c = slice(0, at)
+    check(q[c], k[c], v[c], ks[c], vs[c], out[c], True)
+    check(q, k, v, ks, vs, out, True)
+
+
+@pytest.mark.parametrize("factor", [2.0 ** -40, 2.0 ** -13, 2.0 ** -11, 0.0, 2.0 ** 11, 2.0 ** 13, 2.0 ** 16, 2.0 ** 40])
+@pytest.mark.parametrize("which", [[0], [0, 1, 127, 128], [130, 131, 255, 256], [299], list(range(0, 300, 3))])
+def test_single_keys_far_from_the_others(which, factor):
+    """Some keys' scales far above or below the rest of their tile, from one key to a third of all, around tile borders.
+    Every row looks at its own key or at one before it by some 80 in the exponent, or at nothing in particular, so each
+    kind of key counts for somebody."""
+    n = 300
+    q, k, v, ks, vs = prompt(n, 2, 2, seed=111)
+    vs[which] *= factor
+    if factor == 0.0:
+        v[which] = 0
+    i = torch.arange(n, device="cuda")
+    run_and_check(q, k, v, ks, vs, "even")
+    run_and_check(looks_at(k, ks, i), k, v, ks, vs, "own")
+    run_and_check(looks_at(k, ks, (i - 1 - i % 5).clamp(min=0)), k, v, ks, vs, "near")
+    run_and_check(looks_at(k, ks, (i // 2)), k, v, ks, vs, "far")
+
+
+def test_a_key_that_is_hardly_looked_at():
+    """One key whose scale is 2^40 times the others' and whose logit is far below; another key of its tile is looked at a
+    little less than the keys of the tile behind."""
+    n, big, other, main = 256, 60, 90, 200
+    q, k, v, ks, vs = prompt(n, 1, 1, seed=112)
+    vs[big] *= 2.0 ** 40
+    kk = values(k.view(n, 1, D), ks)[:, 0]
+    for part in (0.5, 0.8, 0.95):
+        mix = torch.linalg.lstsq(kk[[big, other, main]].cpu(),
+                                 torch.tensor([-300.0, part * 400.0, 400.0], dtype=torch.double, device="cpu"),
+                                 driver="gelsd").solution.cuda()
+        run_and_check(mix.bfloat16()[None].repeat(n, 1), k, v, ks, vs, f"part {part}")
+
+
+@pytest.mark.parametrize("heads,kv,n", [(1, 1, 1), (4, 4, 3), (5, 5, 130), (24, 4, 270), (70, 35, 140), (33, 33, 40)])
+def test_scales_over_many_orders_of_magnitude(heads, kv, n):
+    """Scales of V spread over some 2^+-25, different for every head, zeros among them; more heads than a block converts."""
+    q, k, v, ks, vs = prompt(n, heads, kv, seed=113)
+    vs *= torch.exp2(torch.randn(vs.shape, generator=torch.Generator().manual_seed(1)) * 8).cuda()
+    vs.view(-1)[::7] = 0.0
+    run_and_check(q, k, v, ks, vs)
+
+
+def test_many_sequences_with_scales_apart():
+    """Short and long sequences beside one another, wide tiles in some of them only, rows behind the last one."""
+    lens = [1, 128, 129, 0, 5, 400, 127, 2, 260, 64]
+    rows = sum(lens)
+    q, k, v, ks, vs = prompt(rows + 9, 4, 2, seed=114)
+    vs[0] *= 2.0 ** 30
+    vs[1:129:50, 1] *= 2.0 ** 30
+    vs[270:300] *= 2.0 ** -30
+    vs[rows - 64] = 0.0
+    vs[rows:] = NAN
+    for causal in (True, False):
+        out = fl.attention_prefill(q, k, v, cu_seqlens=cu(lens), k_scale=ks, v_scale=vs, causal=causal)
+        first = 0
+        for b, n in enumerate(lens):
+            r = slice(first, first + n)
+            if n:
+                check(q[r], k[r], v[r], ks[r], vs[r], out[r], causal, what=f"sequence {b} causal {causal}")
+            first += n
+        assert (out[rows:] == 0).all()
+
+
+def test_codes_that_are_not_a_number_under_scales_apart():
+    """NaN in a key whose scale is far from the others' reaches the rows that see it, in its dimension, and no other."""
+    n, at = 200, 70
+    for factor in (2.0 ** 30, 2.0 ** -30, 0.0):
+        q, k, v, ks, vs = prompt(n, 2, 1, seed=115)
+        vs[at] *= factor
+        v[at, 9] = 0x7F
+        out = fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs)
+        c = slice(0, at)
+        check(q[c], k[c], v[c], ks[c], vs[c], out[c], True)
+        assert out[at:].view(n - at, 2, D)[:, :, 9].isnan().all()
+        keep = [d for d in range(D) if d != 9]
+        assert out[at:].view(n - at, 2, D)[:, :, keep].isfinite().all()
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_scales_that_are_not_finite_beside_scales_apart(bad):
+    n, at = 200, 90
+    q, k, v, ks, vs = prompt(n, 2, 1, seed=116)
+    vs[30] *= 2.0 ** 25
+    vs[50] *= 2.0 ** -25
+    vs[at] = bad
+    out = fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs)
+    c = slice(0, at)
+    check(q[c], k[c], v[c], ks[c], vs[c], out[c], True)
+    assert not out[at:].isfinite().all(-1).any()
+
+
+def test_scales_apart_captured_and_replayed():
+    """One graph whose tiles turn wide and ordinary again between replays; strided codes and scales."""
+    n, heads, kv = 300, 4, 2
+    q, k, v, ks, vs = prompt(n, heads, kv, seed=117)
+    codes = torch.zeros(n, 2 * kv * D + 32, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n, 2 * kv + 1), NAN, device="cuda")
+    k8, v8, ks8, vs8 = codes[:, 16:16 + kv * D], codes[:, 32 + kv * D:], scales[:, :kv], scales[:, kv + 1:]
+    k8.copy_(k), v8.copy_(v), ks8.copy_(ks), vs8.copy_(vs)
+    ws = fl.attention_prefill_workspace(n, kv, True)
+    out = torch.empty_like(q)
+    call = dict(k_scale=ks8, v_scale=vs8, O=out, workspace=ws)
+    fl.attention_prefill(q, k8, v8, **call)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fl.attention_prefill(q, k8, v8, **call)
+    for rows, factor in (([], 1.0), ([3, 250], 2.0 ** 30), ([140], 2.0 ** -30), ([], 1.0), ([0], 0.0)):
+        vs8.copy_(vs)
+        vs8[rows] *= factor
+        for _ in range(2):
+            g.replay()
+        check(q, k8, v8, ks8, vs8, out, True)
+    assert fl.check_device_status(ws) == fl.FL_OK
