@@ -74,6 +74,9 @@ constexpr float kPreLift = 7.f;                    // E4M3: weights are lifted b
 constexpr float kPreZero = -90.5f;
 constexpr int kPreWindow = 13;                     // E4M3: powers of two that the scales of a tile's ordinary keys span
 constexpr int kPreRoom = 6;                        // E4M3: the largest of these scales times 2^-b is in [2^6, 2^7)
+// E4M3: b of any tile with ordinary keys.  m stays within 2^30 of mx then, and no weight that counts for l falls below
+// fp32's range: it is 2^(x - mx - 30 - 60 + 7 - 8) at least, 2^-126 for x = mx - 35.
+constexpr int kPrePowerMin = -60, kPrePowerMax = 30;
 // E4M3: what a tile's power carries on top, times kPreMark: it has single keys, and its first key is one.
 constexpr float kPreMark = 65536.f;
 enum : int { PRE_SINGLE = 1, PRE_SINGLE_FIRST = 2 };
@@ -702,7 +705,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         const float logit = tmem_ld1(s_tmem + j) * c, x = sees ? logit : -INFINITY;
         tmem_st1(s_tmem + j, -INFINITY);
         const int power = max(field - (127 + kPreRoom), -120);
-        const float up = fmaxf(m, x + (bits << 1 != 0 ? static_cast<float>(power) : kPreZero)), up_l = fmaxf(mx, x);
+        // m rises by 2^kPrePowerMax at most, for l's sake: fp32 has room for weights of 2^98 (and for 2^(m - mx) from 2^-125 on)
+        const float lift = bits << 1 != 0 ? static_cast<float>(min(max(power, -110), kPrePowerMax)) : kPreZero;
+        const float up = fmaxf(m, x + lift), up_l = fmaxf(mx, x);
         const float down = ex2(m - up);
         l = l * ex2(mx - up_l) + ex2(x - up_l);
         mx = up_l;
@@ -934,8 +939,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 
 // E4M3 codes of K and V times their scales, for the kernel above: K as bf16, V as fp16 times 2^-b, with b for each key
 // tile (128 rows of a sequence, from its first) and head: from V's largest finite scale where the tile's scales lie
-// within kPreWindow powers of two, else from the window of that width that holds most of its keys.  The keys outside it
-// are written as zeros and marked as single keys.  Bound by memory: 1 byte in
+// within kPreWindow powers of two, else from the window of that width that holds most of its keys; in either case not
+// beyond kPrePowerMin and kPrePowerMax.  The keys outside it are written as zeros and marked as single keys.  Bound by memory: 1 byte in
 // and 2 out for each value.  A CTA takes 16 rows of a key tile for up to 32 heads at a time, a thread 8 codes (16 bytes
 // out; with 16 codes each store left half sectors to the next one); the scales of the whole tile are read by each of
 // its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18.5 instead of
@@ -947,7 +952,7 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
     int batch, int seq_len, int M, int n_kv, __nv_bfloat16* K16, __half* V16, float* powers) {
   __shared__ uint32_t top[kCodesHeads], low[kCodesHeads];  // largest and smallest finite scale of V, as bit patterns
   __shared__ float power[kCodesHeads];
-  __shared__ int window[kCodesHeads];  // exponent field of its top, -1 where it holds all keys
+  __shared__ int window[kCodesHeads];  // exponent field of its top; -1: it holds all keys
   __shared__ unsigned most;
   __shared__ short fields[kPreTile];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -1011,11 +1016,12 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
     if (smallest != ~0u) atomicMax(&top[j], largest), atomicMin(&low[j], smallest);
   }
   __syncthreads();
+  constexpr int kFieldMin = 127 + kPreRoom + kPrePowerMin, kFieldMax = 127 + kPreRoom + kPrePowerMax;
   bool wide = false;
   if (tid < heads) {
     const int field = static_cast<int>(top[tid] >> 23);
-    wide = top[tid] != 0 && field - static_cast<int>(low[tid] >> 23) >= kPreWindow;
-    power[tid] = top[tid] == 0 ? kPreZero : static_cast<float>(max(field - (127 + kPreRoom), -120));
+    wide = top[tid] != 0 && (field - static_cast<int>(low[tid] >> 23) >= kPreWindow || field < kFieldMin || field > kFieldMax);
+    power[tid] = top[tid] == 0 ? kPreZero : static_cast<float>(field - (127 + kPreRoom));
     window[tid] = wide ? field : -1;
   }
   if (__syncthreads_or(wide)) {
@@ -1028,16 +1034,16 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
         fields[tid] = bits == 0 || bits >= 0x7F800000u ? -1 : static_cast<short>(bits >> 23);
       }
       __syncthreads();
-      if (tid < rows && fields[tid] >= 0) {
+      if (tid < rows && fields[tid] >= kFieldMin && fields[tid] <= kFieldMax) {
         const int mine = fields[tid];
         unsigned n = 0;
-        for (int q = 0; q < rows; ++q) n += fields[q] >= max(mine - (kPreWindow - 1), 0) && fields[q] <= mine;
+        for (int q = 0; q < rows; ++q) n += fields[q] > mine - kPreWindow && fields[q] <= mine;
         atomicMax(&most, n << 8 | mine);
       }
       __syncthreads();
       if (tid == 0) {
-        window[j] = static_cast<int>(most & 255u);
-        power[j] = static_cast<float>(max(window[j] - (127 + kPreRoom), -120));
+        window[j] = most != 0 ? static_cast<int>(most & 255u) : 512;  // 512: holds none
+        power[j] = most != 0 ? static_cast<float>(window[j] - (127 + kPreRoom)) : 0.f;
       }
     }
     __syncthreads();

@@ -365,8 +365,8 @@ FL_API size_t fl_attention_decode_workspace_bytes(void);
  * rows, codes times scales become bf16 for K and fp16 for V, there with a power of two of its own for
  * each 128 keys of a sequence and head, and the weights are rounded to fp16: a weight whose product with
  * its key's scale of V is below some 2^-20 of the row's largest loses bits.  Keys whose scale of V is zero
- * or more than 2^12 away from the others' of their 128 are taken one by one, in fp32 (1 to 4 us for each key
- * and block of query rows that meets it).
+ * or more than 2^12 away from the others' of their 128, and all whose scale is outside 2^-54 to 2^37, are taken
+ * one by one, in fp32 (1 to 4 us for each key and block of query rows that meets it).
  * workspace: fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype) bytes, 256-byte aligned, its
  * first 512 bytes zero-filled before first use (and again after FL_ERR_TIMEOUT); two calls that may
  * overlap on the GPU need one each.  One kernel; E4M3 runs a second one in front. */

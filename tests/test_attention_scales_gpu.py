@@ -216,3 +216,47 @@ def test_scales_apart_captured_and_replayed():
             g.replay()
         check(q, k8, v8, ks8, vs8, out, True)
     assert fl.check_device_status(ws) == fl.FL_OK
+
+
+# ---------------------------------------------------------------- tiles whose scales are far from one another
+@pytest.mark.parametrize("apart", [60, 100, 130, 160])
+@pytest.mark.parametrize("rising", [False, True])
+def test_neighbouring_tiles_far_apart(apart, rising):
+    """The scales of 128 keys and of those behind them 2^apart apart, around 1: both sides count for the rows that look at
+    them, by some 130 powers of two, and the smaller side for those that look past the other one."""
+    n = 300
+    q, k, v, ks, vs = prompt(n, 2, 2, seed=120)
+    step = torch.where(torch.arange(n, device="cuda") < 128, -1.0, 1.0) * (1 if rising else -1)
+    vs *= torch.exp2(step * (apart // 2))[:, None]
+    i = torch.arange(n, device="cuda")
+    run_and_check(q, k, v, ks, vs, "even")
+    run_and_check(looks_at(k, ks, i), k, v, ks, vs, "own")
+    run_and_check(looks_at(k, ks, (i - 140).clamp(min=0)), k, v, ks, vs, "before")
+    run_and_check(looks_at(k, ks, i, 2.0), k, v, ks, vs, "own, less so")
+
+
+@pytest.mark.parametrize("exponent", [-142, -120, -80, -53, -46, 37, 44, 60, 100])
+def test_scales_of_any_size(exponent):
+    """All values of one size, down to subnormal scales and up to where bf16 still holds the output; and some of them only."""
+    n = 200
+    q, k, v, ks, vs = prompt(n, 2, 1, seed=121)
+    big = vs * 2.0 ** exponent
+    small = vs.clone()
+    small[40:60] = big[40:60]
+    for scales in (big, small):
+        run_and_check(q, k, v, ks, scales, str(exponent))
+        out = fl.attention_prefill(q, k, v, k_scale=ks, v_scale=scales)
+        assert out.isfinite().all()
+
+
+def test_large_outlier_hardly_looked_at_keeps_the_sum():
+    """A key 2^100 times the others with weights from 2^-30 to 2^-200 of theirs: the sum of the weights is the others', the
+    output the key's or theirs."""
+    n, big = 256, 60
+    q, k, v, ks, vs = prompt(n, 1, 1, seed=122)
+    vs[big] *= 2.0 ** 100
+    kk = values(k.view(n, 1, D), ks)[:, 0]
+    u = kk[big] / kk[big].square().sum()
+    for down in (20.0, 40.0, 70.0, 100.0, 140.0):
+        row = (-(down / 1.4427) * D ** 0.5) * u
+        run_and_check(row.bfloat16()[None].repeat(n, 1), k, v, ks, vs, f"2^-{down}")
