@@ -776,7 +776,10 @@ def attention_prefill(Q, K, V, cu_seqlens=None, seq_len: int = 0, k_scale=None, 
 
     Sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; without cu_seqlens the rows are sequences of
     seq_len tokens laid end to end (0: one sequence).  Rows of O in no sequence stay as they were (zeros where O
-    is allocated here).  scale: of the logits, 1 / sqrt(128) by default.  Returns O bf16 [M, n_heads * 128]."""
+    is allocated here).  scale: of the logits, 1 / sqrt(128) by default.  Returns O bf16 [M, n_heads * 128].
+
+    A wait in the kernel that runs out (set_wait_timeout_ns) leaves O incomplete: check_device_status(workspace)
+    says so once, and the workspace serves the next call as it is."""
     if stream is not None and (O is None or workspace is None):
         with torch.cuda.stream(stream):
             return attention_prefill(Q, K, V, cu_seqlens, seq_len, k_scale, v_scale, causal, scale, O, workspace)

@@ -107,7 +107,7 @@ struct alignas(128) PrefillParams {
   int pairs_at_once;       // of which this many are worked off before the next ones begin
   float scale_log2;
   int* status;
-  unsigned* work;          // [0] ranks given out beyond the first of each CTA, [1] CTAs that found none left
+  unsigned* work;          // [0] ranks given out beyond the first of each CTA, [1] CTAs that take no more
   unsigned long long timeout_ns;
 };
 
@@ -411,15 +411,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
         t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
         long_before = max(t.n0, t.n1) >= 4;
-      } else if (lane == 0 && atomicAdd(p.work + 1, 1u) == static_cast<unsigned>(G) - 1) {
-        p.work[0] = 0;  // every CTA has come to the end: ready for the next launch
-        p.work[1] = 0;
       }
       if (lane == 0) {
         bar.tile[k % kPreRing] = t;
         mbar_arrive(&bar.tile_full[k % kPreRing]);
       }
       __syncwarp();
+    }
+    // Counted on every way out, also where a wait gave up, so that the next launch finds the counters at zero.
+    if (lane == 0 && atomicAdd(p.work + 1, 1u) == static_cast<unsigned>(G) - 1) {
+      p.work[0] = 0;  // every CTA has taken its last tile
+      p.work[1] = 0;
     }
   } else if (warp == 9) {
     // ================================================================ TMA loads

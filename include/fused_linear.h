@@ -368,8 +368,9 @@ FL_API size_t fl_attention_decode_workspace_bytes(void);
  * or more than 2^12 away from the others' of their 128, and all whose scale is outside 2^-54 to 2^37, are taken
  * one by one, in fp32 (1 to 4 us for each key and block of query rows that meets it).
  * workspace: fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype) bytes, 256-byte aligned, its
- * first 512 bytes zero-filled before first use (and again after FL_ERR_TIMEOUT); two calls that may
- * overlap on the GPU need one each.  One kernel; E4M3 runs a second one in front. */
+ * first 512 bytes zero-filled before first use; two calls that may overlap on the GPU need one each.  A wait
+ * that runs out ends the call with O incomplete; fl_check_device_status(workspace) returns FL_ERR_TIMEOUT
+ * once then, and the workspace serves the next call as it is.  One kernel; E4M3 runs a second one in front. */
 FL_API int attention_prefill(const void* Q, const void* K, const void* V, const float* k_scale,
                              const float* v_scale, const int32_t* cu_seqlens, void* O, int M, int batch,
                              int n_heads, int n_kv_heads, int head_dim, int seq_len, int64_t ldq, int64_t ldkv,

@@ -678,3 +678,29 @@ def test_projection_prompt_and_decode_steps(fp8):
             assert torch.equal(kk[:, -1], values(k[b].view(kv, D), None if ks is None else ks[b]))
             assert torch.equal(vv[:, -1], values(v[b].view(kv, D), None if vs is None else vs[b]))
     assert fl.check_device_status(ws) == fl.FL_OK and fl.device_status() == fl.FL_OK
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_workspace_serves_on_after_waits_that_ran_out(fp8):
+    """Calls that gave up leave nothing behind that the next one would trip over, though nobody zeroes the workspace: it
+    works off all of its tiles (more than there are CTAs)."""
+    n, m = 65536, 24000
+    q, k, v, ks, vs = prompt(n, 2, 2, fp8, seed=54)
+    ws = fl.attention_prefill_workspace(n, 2, fp8)
+    cut = (q[:m], k[:m], v[:m])
+    scales = dict(k_scale=ks[:m], v_scale=vs[:m]) if fp8 else {}
+    want = fl.attention_prefill(*cut, **scales)
+    for times in (1, 2):
+        try:
+            fl.set_wait_timeout_ns(1000)
+            for _ in range(times):
+                fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs, workspace=ws)
+            status = fl.check_device_status(ws)
+        finally:
+            fl.set_wait_timeout_ns(0)
+        assert status == fl.FL_ERR_TIMEOUT
+        for _ in range(2):
+            out = torch.full((m, 2 * D), 7.0, dtype=torch.bfloat16, device="cuda")
+            fl.attention_prefill(*cut, **scales, O=out, workspace=ws)
+            assert torch.equal(out, want)
+        assert fl.check_device_status(ws) == fl.FL_OK
