@@ -48,6 +48,10 @@ inline int check_cache(const void* k_pages, const void* v_pages, const void* ks,
 
 inline bool positive_finite(float x) { return x > 0.f && std::isfinite(x); }
 
+// The kernels are launched as dependents: they may begin while the kernel in front still writes what they read behind
+// griddep_wait.  So they read it by ordinary loads: the read-only path (ld.global.nc) asks for data that nobody writes
+// as long as the kernel lives.  Measured no difference in any case.
+
 // First and one-past-last row of sequence b: cu_seqlens clipped to [0, M] (a decreasing or out-of-range
 // entry gives an empty sequence, never a row outside the tensors), or runs of seq_len rows.
 __device__ __forceinline__ void sequence_rows(const int* cu, int b, int seq_len, int M, int& first, int& last) {

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
   if (p.small) {  // at most 128 sequences, all counts in 32 bits: each warp finds its way alone, without a barrier
     int len[4], mine[4], last[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) len[k] = k * 32 + lane < p.c.batch ? __ldg(p.c.lens + k * 32 + lane) : 0;
+    for (int k = 0; k < 4; ++k) len[k] = k * 32 + lane < p.c.batch ? p.c.lens[k * 32 + lane] : 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       last[k] = mine[k] = k * 32 + lane < p.c.batch ? decode_units<T::kUnit>(len[k], capacity, odd) : 0;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
     long long before;
     auto block_scan = [&](int b0) -> long long {  // of 128 sequences from b0
       const int b = b0 + tid;
-      mine = b < p.c.batch ? decode_units<T::kUnit>(__ldg(p.c.lens + b), capacity, odd) : 0;
+      mine = b < p.c.batch ? decode_units<T::kUnit>(p.c.lens[b], capacity, odd) : 0;
       long long x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
     }
     __syncthreads();
     seg.b = static_cast<int>(plan[8]);
-    seg.len = __ldg(p.c.lens + seg.b);
+    seg.len = p.c.lens[seg.b];
     const int n = decode_units<T::kUnit>(seg.len, capacity, odd);
     seg.h = static_cast<int>(plan[9] / n);
     tile = static_cast<int>(plan[9] - static_cast<long long>(seg.h) * n);
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
   };
   long long left = u1 - u0;
   auto begin_seg = [&](DecodeSeg& s, int tile, long long units_left) {
-    if (tile == 0 && s.h == 0) s.len = __ldg(p.c.lens + s.b);
+    if (tile == 0 && s.h == 0) s.len = p.c.lens[s.b];
     s.n_units = decode_units<T::kUnit>(s.len, capacity, s.bad);
     s.units = static_cast<int>(min(static_cast<long long>(s.n_units - tile), units_left));
     const int end = s.bad ? 0 : s.len;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
       if (lane < 2 * p.group) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + lane * 128));
     }
     const int pos = one_page ? pt : min(pt + (lane & (T::kStep - 1)), ps.t1 - 1);
-    entry = __ldg(p.c.table + ps.b * p.c.ldt + page_of(pos));
+    entry = p.c.table[ps.b * p.c.ldt + page_of(pos)];
   };
   const uint32_t ring = smem_u32(smem) + warp * T::kStages * T::kStage;
   auto issue = [&]() {
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
       for (int i = 0; i < 4; ++i) {
         const int d = FP8 ? ((i >> 1) * 4 + q) * 16 + (i & 1) * 8 : (i * 4 + q) * 8;
         uint4 w = make_uint4(0, 0, 0, 0);
-        if (has) w = __ldg(reinterpret_cast<const uint4*>(src + d));
+        if (has) w = *reinterpret_cast<const uint4*>(src + d);
         qf[nt][i * 4] = w.x, qf[nt][i * 4 + 1] = w.y, qf[nt][i * 4 + 2] = w.z, qf[nt][i * 4 + 3] = w.w;
       }
       float f = p.scale_log2;

@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const Appe
       const int h = first + i * kHeads + h0;
       k[i] = v[i] = make_uint4(0, 0, 0, 0);
       if (h < p.n_kv) {
-        k[i] = __ldg(reinterpret_cast<const uint4*>(k_src + h * (kHeadDim * kInBytes)));
-        v[i] = __ldg(reinterpret_cast<const uint4*>(v_src + h * (kHeadDim * kInBytes)));
+        k[i] = *reinterpret_cast<const uint4*>(k_src + h * (kHeadDim * kInBytes));
+        v[i] = *reinterpret_cast<const uint4*>(v_src + h * (kHeadDim * kInBytes));
       }
     }
   };

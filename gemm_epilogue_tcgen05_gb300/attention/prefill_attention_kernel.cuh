@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const float c = p.scale_log2;
     auto load_powers = [&](const PrefillTile& t, int n, int i) {
       const long long tile = i + lane;
-      return tile < n ? __ldg(p.powers + (t.row0 + tile * kPreTile) * p.n_kv + t.kvh) : 0.f;
+      return tile < n ? p.powers[(t.row0 + tile * kPreTile) * p.n_kv + t.kvh] : 0.f;
     };
     // E4M3: the single keys of a tile, in fp32 from their codes and scales: into l and O, and out of S.  O is complete: S
     // of this tile was committed behind the products before.
@@ -684,8 +684,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll
       for (int h = 0; h < 4; ++h) {  // all loads on their way together
         const long long at = key0 + min(h * 32 + lane, keys - 1);
-        mark[h] = __ldcg(p.powers + at * p.n_kv + t.kvh);
-        scales[h] = __float_as_uint(__ldcg(p.v_scale + at * p.ld_scale + t.kvh));
+        mark[h] = p.powers[at * p.n_kv + t.kvh];
+        scales[h] = __float_as_uint(p.v_scale[at * p.ld_scale + t.kvh]);
       }
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -1000,10 +1000,10 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
     for (int i = 0; i < kTogether; ++i) {
       if (j0 + i >= heads) break;
       const long long h = h0 + j0 + i;
-      k[i] = __ldg(reinterpret_cast<const uint2*>(K + row * ld + h * kHeadDim) + c);
-      v[i] = __ldg(reinterpret_cast<const uint2*>(V + row * ld + h * kHeadDim) + c);
-      sk[i] = __ldg(ks + row * lds + h);
-      sv[i] = __ldg(vs + row * lds + h);
+      k[i] = reinterpret_cast<const uint2*>(K + row * ld + h * kHeadDim)[c];
+      v[i] = reinterpret_cast<const uint2*>(V + row * ld + h * kHeadDim)[c];
+      sk[i] = ks[row * lds + h];
+      sv[i] = vs[row * lds + h];
     }
   };
   fetch(0);
@@ -1012,7 +1012,7 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
     uint32_t largest = 0, smallest = ~0u;
     if (tid < each * heads)
       for (int q = tid / heads; q < rows; q += each) {
-        const float x = fabsf(__ldg(vs + (row0 + q) * lds + h0 + j));
+        const float x = fabsf(vs[(row0 + q) * lds + h0 + j]);
         if (x < INFINITY) largest = max(largest, __float_as_uint(x)), smallest = min(smallest, __float_as_uint(x));
       }
     if (smallest != ~0u) atomicMax(&top[j], largest), atomicMin(&low[j], smallest);

@@ -1,6 +1,7 @@
 """The attention entry points on the host (no GPU needed): what they refuse before the device is touched,
 through the C ABI and through the binding."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -107,3 +108,15 @@ def test_binding_refuses_mixed_types_and_shapes():
         fl.paged_kv_append(t, t, c, c, table, lens)
     with pytest.raises(ValueError):
         fl.paged_kv_append(t, t, c, c, table, lens, k_scale=torch.zeros(4, 2))
+
+
+def test_kernels_launched_as_dependents_read_by_ordinary_loads():
+    """Every attention kernel begins while the kernel in front may still write its inputs, which rules out loads for data
+    that is read-only as long as the kernel lives: by intrinsic, in PTX, or by a pointer that promises it."""
+    files = [f for f in cuda_build._deps() if os.path.dirname(f) == cuda_build.ATTENTION]
+    assert len(files) >= 5
+    for f in files:
+        with open(f, encoding="utf-8") as src:
+            code = "".join(line.split("//")[0] + "\n" for line in src)
+        for word in ("__ldg", "ld.global.nc", "__restrict__", "ldu."):
+            assert word not in code, (f, word)
