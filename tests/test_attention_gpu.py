@@ -704,3 +704,24 @@ def test_workspace_serves_on_after_waits_that_ran_out(fp8):
             fl.attention_prefill(*cut, **scales, O=out, workspace=ws)
             assert torch.equal(out, want)
         assert fl.check_device_status(ws) == fl.FL_OK
+
+
+@pytest.mark.parametrize("heads,kv", [(4, 4), (8, 2), (24, 2)])
+def test_decode_weights_over_a_bf16_cache_keep_sixteen_bits(heads, kv):
+    """Sequences of two keys whose second value all but cancels the first one in the first head of each group: v_2 is
+    -p_1 v_1 / p_2 rounded to bf16, so |o| <= 2^-8 p_1 |v_1| and the output's rounding hides nothing.  Weights in two bf16
+    terms move o by 2^-16 A; in one, by up to 2^-8 A, forty times what is allowed here."""
+    batch, group = 64, heads // kv
+    c = Cache([2] * batch, kv, 16, False, seed=62)
+    q = randn(batch, heads * D, seed=63, std=0.25)
+    for b in range(batch):
+        k, v = c.sequence(b)
+        x = torch.einsum("hd,htd->ht", q[b].view(kv, group, D)[:, 0].double(), k) * D ** -0.5
+        p = torch.softmax(x, -1)
+        c.v[c.table[b, 0].long(), :, 1] = (-p[:, :1] * v[:, 0] / p[:, 1:]).bfloat16()
+    out = fl.attention_decode(q, *c.args())
+    for b in range(batch):
+        k, v = c.sequence(b)
+        ref, tol = attend(q[b].double().view(heads, 1, D), k, v, D ** -0.5, 2.0 ** -16)
+        assert_within(out[b].view(heads, 1, D)[::group], ref[::group], tol[::group], f"sequence {b}")
+        assert_within(out[b].view(heads, 1, D), ref, tol, f"sequence {b}, all heads")
