@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -41,6 +42,22 @@ def _deps():
         os.path.join(ROOT, "include", "fused_linear.h")]
 
 
+# Kernels whose warps share out the registers that they are launched with: with any other number than the one their
+# source counts on they would not start.  Source file: (kernel, file and name of the constant).
+REGISTERS = {"k_attention_prefill.cu": ("attention_prefill_kernel", "prefill_attention_kernel.cuh", "kPreRegs")}
+
+
+def check_registers(src: str, ptxas: str) -> None:
+    """Raises unless ptxas (its -v output) gave every instance of the source's kernel the registers it counts on."""
+    kernel, header, name = REGISTERS[os.path.basename(src)]
+    with open(os.path.join(os.path.dirname(src), header), encoding="utf-8") as f:
+        want = int(re.search(rf"\b{name} = (\d+)", f.read()).group(1))
+    got = [int(used) for function, used in
+           re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", ptxas, re.S) if kernel in function]
+    if not got or any(n != want for n in got):
+        raise RuntimeError(f"{kernel}: compiled for {got} registers a thread, {name} counts on {want}")
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB):
         return False
@@ -57,10 +74,13 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc] + flags + ["-c", src, "-o", obj]
+        counted = os.path.basename(src) in REGISTERS
+        cmd = [nvcc] + flags + (["-Xptxas", "-v"] if counted else []) + ["-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        if counted:
+            check_registers(src, r.stdout + r.stderr)
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
         return obj

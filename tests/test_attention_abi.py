@@ -120,3 +120,19 @@ def test_kernels_launched_as_dependents_read_by_ordinary_loads():
             code = "".join(line.split("//")[0] + "\n" for line in src)
         for word in ("__ldg", "ld.global.nc", "__restrict__", "ldu."):
             assert word not in code, (f, word)
+
+
+def test_build_refuses_another_register_count():
+    """The prefill kernel's warps share out the registers of its launch: a compiler that takes another number than the
+    source counts on ends the build, not the first call."""
+    src = os.path.join(cuda_build.ATTENTION, "k_attention_prefill.cu")
+    report = ("ptxas info    : Compiling entry function '_ZN2fl24attention_prefill_kernelILb{}EEEvNS_13PrefillParamsE' for "
+              "'sm_103a'\nptxas info    : Function properties for x\n    0 bytes stack frame\n"
+              "ptxas info    : Used {} registers, used 1 barriers\n")
+    other = "ptxas info    : Compiling entry function '_ZN2fl5otherEv' for 'sm_103a'\nptxas info    : Used 64 registers\n"
+    with open(os.path.join(cuda_build.ATTENTION, "prefill_attention_kernel.cuh"), encoding="utf-8") as f:
+        want = int(f.read().split("kPreRegs = ")[1].split(",")[0])
+    cuda_build.check_registers(src, report.format(0, want) + other + report.format(1, want))
+    for bad in (other, report.format(0, want) + report.format(1, want - 8), report.format(1, want + 8) + other, ""):
+        with pytest.raises(RuntimeError):
+            cuda_build.check_registers(src, bad)
