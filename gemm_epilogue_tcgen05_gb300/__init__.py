@@ -721,7 +721,7 @@ def paged_kv_append(K, V, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
 
 def _fresh(n: int, head: int, device) -> torch.Tensor:
     """A workspace of n bytes, its first `head` bytes (status and counters; the rest is written before it is read) zero."""
-    t = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    t = torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
     t[:head].zero_()
     return t
 

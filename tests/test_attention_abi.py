@@ -136,3 +136,13 @@ def test_build_refuses_another_register_count():
     for bad in (other, report.format(0, want) + report.format(1, want - 8), report.format(1, want + 8) + other, ""):
         with pytest.raises(RuntimeError):
             cuda_build.check_registers(src, bad)
+
+
+@pytest.mark.parametrize("device", [0, 1, "cuda:0", None])
+def test_workspaces_are_made_on_the_device_that_is_asked_for(lib, monkeypatch, device):
+    """An index of 0 is a device of its own, not the current one."""
+    made, empty = [], torch.empty
+    monkeypatch.setattr(fl.torch, "empty", lambda n, dtype, device: (made.append(device), empty(n, dtype=dtype))[1])
+    fl.attention_decode_workspace(device)
+    fl.attention_prefill_workspace(10, 2, True, device)
+    assert made == ["cuda" if device is None else device] * 2
