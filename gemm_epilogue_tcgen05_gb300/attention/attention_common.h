@@ -46,7 +46,11 @@ inline int check_cache(const void* k_pages, const void* v_pages, const void* ks,
   return FL_OK;
 }
 
-inline bool positive_finite(float x) { return x > 0.f && std::isfinite(x); }
+// The factor of the logits to base 2: positive and finite, or the scale is refused.
+inline bool scale_to_base_2(float scale, float* out) {
+  *out = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  return *out > 0.f && std::isfinite(*out);
+}
 
 // The kernels are launched as dependents: they may begin while the kernel in front still writes what they read behind
 // griddep_wait.  So they read it by ordinary loads: the read-only path (ld.global.nc) asks for data that nobody writes

@@ -47,7 +47,8 @@ extern "C" int attention_decode(const void* Q, const void* k_pages, const void* 
   if (batch < 0 || n_heads < 0 || n_kv_heads < 0 || page_size < 1 || num_pages < 0 || max_pages < 0)
     return FL_ERR_INVALID_ARG;
   const bool fp8 = cache_dtype == FL_E4M3;
-  if ((cache_dtype != FL_BF16 && !fp8) || !positive_finite(scale)) return FL_ERR_INVALID_ARG;
+  float scale_log2;
+  if ((cache_dtype != FL_BF16 && !fp8) || !scale_to_base_2(scale, &scale_log2)) return FL_ERR_INVALID_ARG;
   if (batch == 0 || n_heads == 0) return FL_OK;
   if (n_kv_heads == 0 || n_heads % n_kv_heads != 0) return FL_ERR_INVALID_ARG;
   if (head_dim != kHeadDim) return FL_ERR_UNSUPPORTED;
@@ -78,7 +79,7 @@ extern "C" int attention_decode(const void* Q, const void* k_pages, const void* 
   // units of all lengths that the table allows (64 tokens at least), for all heads
   const int64_t longest = std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, INT32_MAX) / 64 + 1;
   p.small = batch <= 128 && longest * batch < (int64_t{1} << 31) / (static_cast<int64_t>(n_kv_heads) * p.chunks);
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int*>(ws);
   p.counters = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);

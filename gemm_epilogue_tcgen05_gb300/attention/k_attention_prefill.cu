@@ -92,7 +92,8 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   if (M < 0 || n_heads < 0 || n_kv_heads < 0 || (cu_seqlens != nullptr ? batch < 0 : seq_len < 1))
     return FL_ERR_INVALID_ARG;
   const bool fp8 = kv_dtype == FL_E4M3;
-  if ((kv_dtype != FL_BF16 && !fp8) || !positive_finite(scale)) return FL_ERR_INVALID_ARG;
+  float scale_log2;
+  if ((kv_dtype != FL_BF16 && !fp8) || !scale_to_base_2(scale, &scale_log2)) return FL_ERR_INVALID_ARG;
   if (M == 0 || n_heads == 0 || (cu_seqlens != nullptr && batch == 0)) return FL_OK;
   if (n_kv_heads == 0 || n_heads % n_kv_heads != 0) return FL_ERR_INVALID_ARG;
   if (head_dim != kHeadDim) return FL_ERR_UNSUPPORTED;
@@ -162,7 +163,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   p.M = M;
   p.causal = causal != 0;
   p.flat = p.batch > (p.causal ? kTierBatch : kTierBatchFull);
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   p.status = reinterpret_cast<int*>(ws);
   p.work = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);
   p.timeout_ns = wait_timeout_ns();

@@ -336,7 +336,8 @@ FL_API int paged_kv_append(const void* K, const void* V, const float* k_scale, c
 /* Attention of one new token per sequence over the paged cache.
  *   O[b, h] = sum_j p_j V[j] / sum_j p_j,  p_j = exp(scale * Q[b, h] . K[j] - max),  j < seq_lens[b],
  * query head h reading kv head h / (n_heads / n_kv_heads).  Q, O [batch, n_heads*128] bf16 (Q already
- * rotated); n_heads a multiple of n_kv_heads; scale > 0.  Sums and the softmax's state are fp32.
+ * rotated); n_heads a multiple of n_kv_heads; scale > 0, and finite times log2 e.  Sums and the softmax's
+ * state are fp32.
  * A sequence of length 0 gets zeros.  A negative length, one beyond max_pages * page_size, or a page
  * outside [0, num_pages) among the entries in use: the sequence's rows are NaN and
  * fl_check_device_status(workspace) returns FL_ERR_INVALID_ARG once.  Nothing behind a sequence's

@@ -146,3 +146,11 @@ def test_workspaces_are_made_on_the_device_that_is_asked_for(lib, monkeypatch, d
     fl.attention_decode_workspace(device)
     fl.attention_prefill_workspace(10, 2, True, device)
     assert made == ["cuda" if device is None else device] * 2
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38])
+def test_scales_that_base_two_does_not_hold(lib, scale):
+    """The kernels work to base 2: a finite scale whose product with log2 e is not is refused, as an infinite one is."""
+    assert call(lib.attention_decode, DECODE, scale=F(scale)) == INVALID
+    assert call(lib.attention_prefill, PREFILL, scale=F(scale)) == INVALID
+    assert call(lib.attention_decode, DECODE, scale=F(2.3e38), ws=None) == WORKSPACE
