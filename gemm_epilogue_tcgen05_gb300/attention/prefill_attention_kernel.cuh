@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     };
     // E4M3: the single keys of a tile, in fp32 from their codes and scales: into l and O, and out of S.  O is complete: S
     // of this tile was committed behind the products before.
-    auto single_keys = [&](const PrefillTile& t, int i, bool first_too, int lim, float& m, float& mx, float& l) {
+    auto single_keys = [&](const PrefillTile& t, int i, bool first_too, int lim, float& m, float& mx, float& l, bool& begun) {
       const long long key0 = t.row0 + static_cast<long long>(i) * kPreTile;
       const int keys = min(kPreTile, t.len - i * kPreTile);
       uint32_t which[4], scales[4];  // of key 32 h + lane
@@ -693,26 +693,40 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         which[h] = __ballot_sync(~0u, j == 0 ? first_too : j < keys && mark[h] != 0.f);
       }
       tmem_st_wait();  // O may have been begun just now
+      float zero_top = -INFINITY;  // of the logits of keys whose values are zero: O learns of them once, behind the last key
 #pragma unroll 1
-      for (int j = 0; j < kPreTile; ++j) {
-        const int h = j >> 5;
-        const uint32_t w = (h < 2 ? (h == 0 ? which[0] : which[1]) : (h == 2 ? which[2] : which[3])) >> (j & 31);
-        if (w == 0) j |= 31;
-        if ((w & 1u) == 0) continue;
-        const uint32_t bits = __shfl_sync(~0u, h < 2 ? (h == 0 ? scales[0] : scales[1]) : (h == 2 ? scales[2] : scales[3]), j & 31);
-        const int field = static_cast<int>(bits >> 23) & 255;
-        const uint8_t* from = p.codes + (key0 + j) * p.ld_codes + t.kvh * kHeadDim;
+      for (int j = 0; j <= kPreTile; ++j) {
+        const bool end = j == kPreTile;
+        uint32_t bits = 0;
+        float x = zero_top;
+        bool sees = false;
+        if (end) {
+          if (!begun) m = fmaxf(m, zero_top + kPreZero);  // O is zero yet
+          if (!__any_sync(~0u, zero_top + kPreZero > m)) break;
+        } else {
+          const int h = j >> 5;
+          const uint32_t w = (h < 2 ? (h == 0 ? which[0] : which[1]) : (h == 2 ? which[2] : which[3])) >> (j & 31);
+          if (w == 0) j |= 31;
+          if ((w & 1u) == 0) continue;
+          bits = __shfl_sync(~0u, h < 2 ? (h == 0 ? scales[0] : scales[1]) : (h == 2 ? scales[2] : scales[3]), j & 31);
+          const float logit = tmem_ld1(s_tmem + j) * c;
+          tmem_st1(s_tmem + j, -INFINITY);
+          sees = i * kPreTile + j <= lim;
+          x = sees ? logit : -INFINITY;
+          const float up_l = fmaxf(mx, x);
+          l = l * ex2(mx - up_l) + ex2(x - up_l);
+          mx = up_l;
+          if (bits << 1 == 0) {
+            zero_top = fmaxf(zero_top, x);
+            continue;
+          }
+        }
+        const uint8_t* from = p.codes + (key0 + (end ? 0 : j)) * p.ld_codes + t.kvh * kHeadDim;
         uint4 codes = *reinterpret_cast<const uint4*>(from);
-        const bool sees = i * kPreTile + j <= lim;
-        const float logit = tmem_ld1(s_tmem + j) * c, x = sees ? logit : -INFINITY;
-        tmem_st1(s_tmem + j, -INFINITY);
-        const int power = max(field - (127 + kPreRoom), -120);
+        const int power = max((static_cast<int>(bits >> 23) & 255) - (127 + kPreRoom), -120);
         // m rises by 2^kPrePowerMax at most, for l's sake: fp32 has room for weights of 2^98 (and for 2^(m - mx) from 2^-125 on)
-        const float lift = bits << 1 != 0 ? static_cast<float>(min(max(power, -110), kPrePowerMax)) : kPreZero;
-        const float up = fmaxf(m, x + lift), up_l = fmaxf(mx, x);
-        const float down = ex2(m - up);
-        l = l * ex2(mx - up_l) + ex2(x - up_l);
-        mx = up_l;
+        const float lift = end ? kPreZero : static_cast<float>(min(max(power, -110), kPrePowerMax));
+        const float up = fmaxf(m, x + lift), down = ex2(m - up);
         const float weight = ex2((x + static_cast<float>(power)) - (up - kPreLift));
         const float scale = __uint_as_float(bits) * __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
 #pragma unroll 2
@@ -735,6 +749,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         }
         tmem_st_wait();
         m = up;
+        begun = true;
       }
       tmem_st_wait();
     };
@@ -756,7 +771,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         for (int j = 0; j < 8; ++j) tmem_st16(o_tmem + j * 16, none);
       }
       int i = 0, single_done = -1;
-      bool begun = false;  // E4M3: single keys are in O before the first product
+      bool begun = false;  // E4M3: single keys are in O (it may be before the first product)
       for (;;) {
         for (; i < n; ++i) {
           if (FP8 && i > 0 && (i & 31) == 0) powers = load_powers(t, n, i);
@@ -849,8 +864,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;  // the loop waits for the same phase again
         tc_fence_after();
         const int marks = __float2int_rn(__shfl_sync(~0u, powers, i & 31) / kPreMark);
-        single_keys(t, i, (marks & PRE_SINGLE_FIRST) != 0, lim, m, mx, l);
-        begun = true;
+        begun |= i > 0;
+        single_keys(t, i, (marks & PRE_SINGLE_FIRST) != 0, lim, m, mx, l, begun);
         single_done = i;
       }
       if (!ok) break;
@@ -1076,7 +1091,7 @@ __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
       const long long to = (row * n_kv + h0 + j0 + i) * (kHeadDim / 8) + c;
       reinterpret_cast<uint4*>(K16)[to] = codes(k[i], sk[i], [](float x, float y) { return pack_bf16x2(x, y); });
       uint4 v16 = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
-      if (single) v16 = make_uint4(0, 0, 0, 0);
+      if (single && bits != 0) v16 = make_uint4(0, 0, 0, 0);  // a scale of zero leaves zeros, and what is not a number
       reinterpret_cast<uint4*>(V16)[to] = v16;
       if (c == 0 && (r == 0 || win >= 0))
         powers[row * n_kv + h0 + j0 + i] =

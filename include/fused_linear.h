@@ -365,9 +365,10 @@ FL_API size_t fl_attention_decode_workspace_bytes(void);
  * Softmax state and sums are fp32; the weights p_ij are rounded to bf16 for the tensor cores.  With E4M3
  * rows, codes times scales become bf16 for K and fp16 for V, there with a power of two of its own for
  * each 128 keys of a sequence and head, and the weights are rounded to fp16: a weight whose product with
- * its key's scale of V is below some 2^-20 of the row's largest loses bits.  Keys whose scale of V is zero
- * or more than 2^12 away from the others' of their 128, and all whose scale is outside 2^-54 to 2^37, are taken
- * one by one, in fp32 (1 to 4 us for each key and block of query rows that meets it).
+ * its key's scale of V is below some 2^-20 of the row's largest loses bits.  Keys whose scale of V is
+ * more than 2^12 away from the others' of their 128, or outside 2^-54 to 2^37, are taken one by one, in fp32:
+ * 3 us for the first and 1.5 us for each other one that a block of query rows meets in 128 keys.  Keys whose
+ * scale is zero among others cost the same first 3 us and little more.
  * workspace: fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype) bytes, 256-byte aligned, its
  * first 512 bytes zero-filled before first use; two calls that may overlap on the GPU need one each.  A wait
  * that runs out ends the call with O incomplete; fl_check_device_status(workspace) returns FL_ERR_TIMEOUT
