@@ -45,11 +45,11 @@
 // p_j v_j in fp32 from the codes to O, which they begin with zeros.  (One power for all keys of a tile lost the bits of
 // the small ones: a later scale 2^32 times the others' put an error of 4 % on the rows before it, 2^40 all of them.)
 //
-// Measured for 4 x 2048 tokens, 32 query and 8 kv heads:
-// 311 us with scales inside the softmax (two multiplications and two shared-memory reads for each query and key, reads
-// that the tensor cores need for themselves), 123 us with fp16 keys (11 bits, but queries that have to become fp16,
-// too), 110.5 us so, 105 us with bf16 values and weights, whose roundings make the error 1.8 times that of a bf16
-// output alone instead of 1.4 times.
+// Measured for 4 x 2048 tokens, 32 query and 8 kv heads: 311 us with scales inside the softmax (two multiplications and
+// two shared-memory reads for each query and key, reads that the tensor cores need for themselves), 123 us with fp16
+// keys (11 bits, but queries that have to become fp16, too), 109 us with keys as bf16 and one power for all keys of a tile, 104 us with bf16 values and weights, whose
+// roundings make the error 1.8 times that of a bf16 output alone instead of 1.4 times; 110.5 us so.  Single keys take
+// 3 us for the first and 1.5 us for each other one that a unit of work meets in a tile, those of zeros 0.1 us.
 #pragma once
 #include <climits>
 

@@ -308,7 +308,7 @@ FL_API int fused_swiglu_bwd(const void* dO, const void* Wd, const void* G, const
  *                      may share pages (a common prefix); entries behind a sequence's length are not
  *                      used;
  *   seq_lens           int32 [batch], tokens in the cache.
- * page_size is any number >= 1 (a multiple of 8 streams best), offsets are 64-bit.  All of these live
+ * page_size is any number >= 1 (a multiple of 16, E4M3 of 32, streams best), offsets are 64-bit.  All of these live
  * on the device, so a captured graph can be replayed as the sequences grow.  head_dim must be 128
  * and head counts at most 65536 (FL_ERR_UNSUPPORTED otherwise).  Outputs may not overlap K, V or the
  * cache.  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes them, with scales that are

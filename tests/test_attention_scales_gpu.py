@@ -260,3 +260,66 @@ def test_large_outlier_hardly_looked_at_keeps_the_sum():
     for down in (20.0, 40.0, 70.0, 100.0, 140.0):
         row = (-(down / 1.4427) * D ** 0.5) * u
         run_and_check(row.bfloat16()[None].repeat(n, 1), k, v, ks, vs, f"2^-{down}")
+
+
+# ---------------------------------------------------------------- many units of work
+def test_single_keys_in_many_units():
+    """Several units of work for each CTA, single keys in some of their tiles; the same results every time."""
+    lens, heads, kv = [700, 650, 513, 700, 384, 699, 700, 640, 100, 700], 16, 4
+    rows = sum(lens)
+    q, k, v, ks, vs = prompt(rows, heads, kv, seed=130)
+    pick = torch.rand(vs.shape, generator=torch.Generator().manual_seed(2)).cuda()
+    vs[pick < 0.004] *= 2.0 ** 20
+    vs[(pick > 0.004) & (pick < 0.008)] *= 2.0 ** -20
+    vs[pick > 0.99] = 0.0
+    offsets = cu(lens)
+    for causal in (True, False):
+        out = fl.attention_prefill(q, k, v, cu_seqlens=offsets, k_scale=ks, v_scale=vs, causal=causal)
+        first = 0
+        for b, n in enumerate(lens):
+            r = slice(first, first + n)
+            check(q[r], k[r], v[r], ks[r], vs[r], out[r], causal, what=f"sequence {b} causal {causal}")
+            first += n
+        for _ in range(3):
+            assert torch.equal(out, fl.attention_prefill(q, k, v, cu_seqlens=offsets, k_scale=ks, v_scale=vs, causal=causal))
+
+
+def test_single_keys_of_a_long_sequence():
+    """Around the 32 key tiles whose powers a warp's lanes hold at a time."""
+    n = 4500
+    q, k, v, ks, vs = prompt(n, 1, 1, seed=131)
+    for at, factor in ((0, 2.0 ** -20), (4000, 2.0 ** 20), (4095, 0.0), (4096, 2.0 ** -20), (4097, 2.0 ** 25), (4223, 0.0),
+                       (4224, 2.0 ** 20), (4499, 2.0 ** -30)):
+        vs[at] *= factor
+    i = torch.arange(n, device="cuda")
+    for q in (q, looks_at(k, ks, torch.where(i % 3 == 0, i, (i - 300).clamp(min=0)))):
+        check(q, k, v, ks, vs, fl.attention_prefill(q, k, v, k_scale=ks, v_scale=vs), True)
+
+
+def test_padded_batch():
+    """Sequences of equal length that end in rows of zeros, the last one shorter."""
+    n, real, seq = 700, 140, 200
+    q, k, v, ks, vs = prompt(n, 8, 2, seed=132)
+    at = torch.arange(n, device="cuda") % seq
+    for t in (q, k, v, ks, vs):
+        t[at >= real] = 0
+    out = fl.attention_prefill(q, k, v, seq_len=seq, k_scale=ks, v_scale=vs)
+    for first in range(0, n, seq):
+        r = slice(first, min(first + seq, n))
+        check(q[r], k[r], v[r], ks[r], vs[r], out[r], True)
+        r = slice(first, min(first + real, n))
+        check(q[r], k[r], v[r], ks[r], vs[r], out[r], True)
+
+
+@pytest.mark.parametrize("apart", [1.0, 2.0 ** 20])
+def test_large_logits(apart):
+    """Logits of many hundreds, tiles of different powers, single keys: the maxima of O and of the sum move apart and on."""
+    n = 500
+    q, k, v, ks, vs = prompt(n, 2, 2, seed=133)
+    q = (q.float() * 60).bfloat16()
+    ks[400:] *= 3.0
+    vs[128:256] *= 2.0 ** -6
+    vs[300:310] *= apart
+    run_and_check(q, k, v, ks, vs)
+    rising = torch.linspace(0, 4, n, device="cuda")[:, None]
+    run_and_check(q.abs(), k & 0x7F, v, ks * rising, vs)
