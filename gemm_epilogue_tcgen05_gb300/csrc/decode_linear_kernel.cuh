@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, S == kLdStages ? 1 : 2)
       if constexpr (KIND == LD_ROWSCALE) {  // r of the item's token, from the step-1 sums (in order)
         float ssum = 0.f;
         if (in && t < p.M)
-          for (int q = 0; q < p.n_partials; ++q) ssum += __ldg(p.partials + static_cast<size_t>(q) * p.M + t);
+          for (int q = 0; q < p.n_partials; ++q) ssum += p.partials[static_cast<size_t>(q) * p.M + t];
         rr[it] = rsqrtf(ssum / static_cast<float>(p.n_norm) + p.eps);
       }
     }

@@ -216,10 +216,12 @@ __device__ __forceinline__ void unpack32(const uint4 (&w)[4], float (&v)[32]) {
   }
 }
 
-// Four bf16 values base[n .. n + 3] as floats; entries at or past `limit` read as zero.
+// Four bf16 values base[n .. n + 3] as floats; entries at or past `limit` read as zero.  An ordinary load: the decode
+// kernels begin while the kernel in front may still write what they read behind griddep_wait, which rules out the
+// read-only path (data that nobody writes as long as the kernel lives).
 __device__ __forceinline__ void load_bf16x4(const __nv_bfloat16* base, int n, int limit, float (&v)[4]) {
   if (n + 4 <= limit) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(base + n));
+    const uint2 u = *reinterpret_cast<const uint2*>(base + n);
     v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
   } else {
 #pragma unroll

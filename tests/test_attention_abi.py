@@ -154,3 +154,17 @@ def test_scales_that_base_two_does_not_hold(lib, scale):
     assert call(lib.attention_decode, DECODE, scale=F(scale)) == INVALID
     assert call(lib.attention_prefill, PREFILL, scale=F(scale)) == INVALID
     assert call(lib.attention_decode, DECODE, scale=F(2.3e38), ws=None) == WORKSPACE
+
+
+def test_decode_linear_kernels_read_by_ordinary_loads():
+    """The same for the decode kernels of the linear layers, and for the loader that they share with nobody else."""
+    def code(name):
+        with open(os.path.join(cuda_build.CSRC, name), encoding="utf-8") as src:
+            return "".join(line.split("//")[0] + "\n" for line in src)
+
+    loader = code("gemm_kernel.cuh").split("void load_bf16x4(")[1].split("__device__")[0]
+    kernels = [code(f) for f in os.listdir(cuda_build.CSRC) if "decode" in f and f.endswith(".cuh")]
+    assert len(kernels) >= 3 and any("griddep_wait();" in k for k in kernels)
+    for text in [loader] + kernels:
+        for word in ("__ldg", "ld.global.nc", "__restrict__", "ldu."):
+            assert word not in text
