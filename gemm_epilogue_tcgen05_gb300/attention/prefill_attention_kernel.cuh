@@ -47,9 +47,10 @@
 //
 // Measured for 4 x 2048 tokens, 32 query and 8 kv heads: 311 us with scales inside the softmax (two multiplications and
 // two shared-memory reads for each query and key, reads that the tensor cores need for themselves), 123 us with fp16
-// keys (11 bits, but queries that have to become fp16, too), 109 us with keys as bf16 and one power for all keys of a tile, 104 us with bf16 values and weights, whose
-// roundings make the error 1.8 times that of a bf16 output alone instead of 1.4 times; 110.5 us so.  Single keys take
-// 3 us for the first and 1.5 us for each other one that a unit of work meets in a tile, those of zeros 0.1 us.
+// keys (11 bits, but queries that have to become fp16, too), 110.5 us with keys as bf16 and one power for all keys of a
+// tile, 105 us with bf16 values and weights, whose roundings make the error 1.8 times that of a bf16 output alone
+// instead of 1.4 times.  Single keys cost 1.5 us where there are none (109.2 -> 110.6 in one run), else 3 us for the
+// first and 1.5 us for each other one that a unit of work meets in a tile, 0.1 us for those of zeros.
 #pragma once
 #include <climits>
 
@@ -724,7 +725,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         const uint8_t* from = p.codes + (key0 + (end ? 0 : j)) * p.ld_codes + t.kvh * kHeadDim;
         uint4 codes = *reinterpret_cast<const uint4*>(from);
         const int power = max((static_cast<int>(bits >> 23) & 255) - (127 + kPreRoom), -120);
-        // m rises by 2^kPrePowerMax at most, for l's sake: fp32 has room for weights of 2^98 (and for 2^(m - mx) from 2^-125 on)
+        // m rises by 2^kPrePowerMax at most, for l's sake: fp32 has room for weights of 2^98 (and for 2^(m - mx) from
+        // 2^-125 on)
         const float lift = end ? kPreZero : static_cast<float>(min(max(power, -110), kPrePowerMax));
         const float up = fmaxf(m, x + lift), down = ex2(m - up);
         const float weight = ex2((x + static_cast<float>(power)) - (up - kPreLift));
@@ -957,11 +959,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 // E4M3 codes of K and V times their scales, for the kernel above: K as bf16, V as fp16 times 2^-b, with b for each key
 // tile (128 rows of a sequence, from its first) and head: from V's largest finite scale where the tile's scales lie
 // within kPreWindow powers of two, else from the window of that width that holds most of its keys; in either case not
-// beyond kPrePowerMin and kPrePowerMax.  The keys outside it are written as zeros and marked as single keys.  Bound by memory: 1 byte in
-// and 2 out for each value.  A CTA takes 16 rows of a key tile for up to 32 heads at a time, a thread 8 codes (16 bytes
-// out; with 16 codes each store left half sectors to the next one); the scales of the whole tile are read by each of
-// its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18.5 instead of
-// 11.2 us for 12400 rows of 8 heads, caches cold: too few, too long).
+// beyond kPrePowerMin and kPrePowerMax.  The keys outside it are written as zeros and marked as single keys.  Bound by
+// memory: 1 byte in and 2 out for each value.  A CTA takes 16 rows of a key tile for up to 32 heads at a time, a thread
+// 8 codes (16 bytes out; with 16 codes each store left half sectors to the next one); the scales of the whole tile are
+// read by each of its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18.5
+// instead of 11.2 us for 12400 rows of 8 heads, caches cold: too few, too long).
 constexpr int kCodesRows = 16, kCodesHeads = 32;
 
 __global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(

@@ -311,8 +311,9 @@ FL_API int fused_swiglu_bwd(const void* dO, const void* Wd, const void* G, const
  * page_size is any number >= 1 (a multiple of 16, E4M3 of 32, streams best), offsets are 64-bit.  All of these live
  * on the device, so a captured graph can be replayed as the sequences grow.  head_dim must be 128
  * and head counts at most 65536 (FL_ERR_UNSUPPORTED otherwise).  Outputs may not overlap K, V or the
- * cache; O may be Q itself.  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes them, with scales that are
- * not negative.  Scale, table, length and offset pointers need 4-byte alignment, the others 16. */
+ * cache; O may be Q itself.  E4M3 entries stand for code * scale, as fused_qkv_rope_fp8kv writes them, with
+ * scales that are not negative.  Scale, table, length and offset pointers need 4-byte alignment, the others
+ * 16. */
 
 /* Rows of keys and values into the cache.
  * K, V [T, n_kv_heads*128], pitch ldkv elements: bf16 (row_dtype FL_BF16) or E4M3 bytes (FL_E4M3) with
