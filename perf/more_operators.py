@@ -391,9 +391,9 @@ def _int4_of(y):
     """The numbers, and the scales, that 4 bits hold of y [..., 128]."""
     y = y.double().view(*y.shape[:-1], HEAD_DIM // GROUP, GROUP)
     most = y.abs().max(-1).values
-    raw = most.clamp_min(2.0 ** -120) / 7
-    step = torch.pow(2.0, torch.floor(torch.log2(raw)) - 4)
-    s = torch.round(raw / step) * step * (most >= 2.0 ** -120)
+    part, power = torch.frexp(most.clamp_min(2.0 ** -120) / 7)  # part in [1/2, 1)
+    s = torch.ldexp(torch.round(part * 32), power - 5).to(torch.bfloat16).double()  # a power of two may be an ulp off
+    s = s * (most >= 2.0 ** -120)
     c = torch.round(y / s.clamp_min(1e-300)[..., None]) * (s > 0)[..., None]
     return (c * s[..., None]).flatten(-2), s
 
