@@ -16,7 +16,8 @@ the deferred-scale chain :func:`fused_linear_residual_gamma` and
 :func:`fused_linear_quant`, and the backward epilogues
 :func:`fused_dgrad_gelu` and :func:`fused_swiglu_bwd`; for the attention behind
 the QKV projections :func:`paged_kv_append`, :func:`attention_prefill` and
-:func:`attention_decode`.
+:func:`attention_decode`; for a cache held in 4 bits :func:`paged_kv_append_int4` and
+:func:`paged_kv_read` (which reads the others back, too).
 """
 from __future__ import annotations
 
@@ -33,7 +34,7 @@ HEADER = os.path.join(ROOT, "include", "fused_linear.h")
 
 FL_OK, FL_ERR_INVALID_ARG, FL_ERR_UNSUPPORTED, FL_ERR_ALIGNMENT, FL_ERR_WORKSPACE, FL_ERR_CUDA, \
     FL_ERR_TIMEOUT, FL_ERR_ARCH = range(8)
-FL_F32, FL_BF16, FL_E4M3 = 0, 1, 2
+FL_F32, FL_BF16, FL_E4M3, FL_INT4 = 0, 1, 2, 3
 FL_GELU_ERF, FL_GELU_TANH = 0, 1
 
 _lib = None
@@ -82,6 +83,10 @@ def load() -> ctypes.CDLL:
     lib.fused_linear_quant.restype = I
     lib.paged_kv_append.argtypes = [P] * 11 + [I] * 7 + [I64] * 5 + [I, I, P]
     lib.paged_kv_append.restype = I
+    lib.paged_kv_append_int4.argtypes = [P] * 9 + [I] * 7 + [I64] * 4 + [P]
+    lib.paged_kv_append_int4.restype = I
+    lib.paged_kv_read.argtypes = [P] * 9 + [I] * 7 + [I64] * 4 + [I, P]
+    lib.paged_kv_read.restype = I
     lib.attention_decode.argtypes = [P] * 8 + [I] * 7 + [I64] * 5 + [F, I, P, SZ, P]
     lib.attention_decode.restype = I
     lib.fl_attention_decode_workspace_bytes.argtypes = []
@@ -563,6 +568,7 @@ def fused_swiglu_bwd(dO, Wd, G, U, dGU=None, stream=None):
 
 
 HEAD_DIM = 128
+INT4_GROUP = 32  # columns of a 4-bit cache that share a scale
 _BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 
 # The attention calls are made once per layer and token, so their checks are written for few Python steps: a device
@@ -639,8 +645,8 @@ def _page_pitch(a, b, shape, per_page, what):
 
 
 def _cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
-    """Checks the paged cache; returns (batch, n_kv_heads, page_size, num_pages, max_pages, ldt, page_pitch,
-    scale_pitch, type)."""
+    """Checks the paged cache (bf16 or E4M3); returns (batch, max_pages, ldt, n_kv_heads, page_size,
+    num_pages, page_pitch, scale_pitch, type)."""
     shape, dt = k_pages.shape, k_pages.dtype
     if len(shape) != 4 or shape[3] != HEAD_DIM or v_pages.shape != shape or v_pages.dtype is not dt or \
             k_pages.get_device() != dev or v_pages.get_device() != dev:
@@ -662,6 +668,37 @@ def _cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
         raise ValueError("k_pages and v_pages: expected bf16 or uint8 (E4M3)")
     elif ks is not None or vs is not None:
         raise ValueError("a bf16 cache has no scales")
+    return (*_table(page_table, seq_lens, dev), n_kv, page, n_pages, pitch, spitch, kind)
+
+
+def _cache_int4(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
+    """The same for a 4-bit cache."""
+    shape = k_pages.shape
+    if k_pages.dtype is not _U8 or len(shape) != 4 or shape[3] != HEAD_DIM // 2 or v_pages.shape != shape or \
+            v_pages.dtype is not _U8 or k_pages.get_device() != dev or v_pages.get_device() != dev:
+        raise ValueError(f"k_pages and v_pages: expected two uint8 tensors [num_pages, n_kv_heads, page_size, "
+                         f"{HEAD_DIM // 2}] on the call's device")
+    if ks is None or vs is None:
+        raise ValueError("a 4-bit cache needs k_page_scale and v_page_scale")
+    groups = HEAD_DIM // INT4_GROUP
+    want = (*shape[:3], groups)
+    if ks.dtype is not _BF16 or vs.dtype is not _BF16 or ks.shape != want or vs.shape != want or \
+            ks.get_device() != dev or vs.get_device() != dev:
+        raise ValueError(f"k_page_scale and v_page_scale: expected bf16 [num_pages, n_kv_heads, page_size, {groups}] on "
+                         "the call's device")
+    n_pages, n_kv, page, _ = shape
+    pitch = _page_pitch(k_pages, v_pages, shape, n_kv * page * (HEAD_DIM // 2), "k_pages and v_pages")
+    spitch = _page_pitch(ks, vs, want, n_kv * page * groups, "k_page_scale and v_page_scale")
+    return (*_table(page_table, seq_lens, dev), n_kv, page, n_pages, pitch, spitch, FL_INT4)
+
+
+def _any_cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
+    four = k_pages.dtype is _U8 and k_pages.dim() == 4 and k_pages.shape[3] == HEAD_DIM // 2
+    return (_cache_int4 if four else _cache)(k_pages, v_pages, page_table, seq_lens, ks, vs, dev)
+
+
+def _table(page_table, seq_lens, dev):
+    """Checks the page table; returns (batch, max_pages, ldt)."""
     batch, t_shape = _ints(seq_lens, "seq_lens", dev), page_table.shape
     if page_table.dtype is not _I32 or len(t_shape) != 2 or t_shape[0] != batch or page_table.get_device() != dev:
         raise ValueError("page_table: expected int32 [batch, max_pages] on the call's device")
@@ -672,7 +709,7 @@ def _cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
             raise ValueError("page_table: expected unit column stride")
         if batch <= 1:
             ldt = max_pages
-    return batch, n_kv, page, n_pages, max_pages, ldt, pitch, spitch, kind
+    return batch, max_pages, ldt
 
 
 def _query(t, name, dev):
@@ -705,7 +742,7 @@ def paged_kv_append(K, V, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
     with k_scale and v_scale (as fused_qkv_rope_fp8kv returns them) go into an E4M3 cache as they are."""
     dev = K.get_device()
     T, width, ld, lds, rows_dt = _kv_pair(K, V, k_scale, v_scale, dev)
-    batch, n_kv, page, n_pages, max_pages, ldt, pitch, spitch, dt = _cache(k_pages, v_pages, page_table, seq_lens,
+    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _cache(k_pages, v_pages, page_table, seq_lens,
                                                                           k_page_scale, v_page_scale, dev)
     if width != n_kv * HEAD_DIM:
         raise ValueError("the rows must have the cache's n_kv_heads")
@@ -717,6 +754,67 @@ def paged_kv_append(K, V, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
               T, batch, n_kv, HEAD_DIM, page, n_pages, max_pages, ld, lds, ldt, pitch, spitch, rows_dt, dt), stream)
     if st:
         _check("paged_kv_append", st)
+
+
+def paged_kv_append_int4(K, V, k_pages, v_pages, k_page_scale, v_page_scale, page_table, seq_lens, cu_seqlens=None,
+                         stream=None):
+    """Puts bf16 K/V rows [T, n_kv_heads * 128] into the pages of a 4-bit cache.
+
+    Pages are uint8 [num_pages, n_kv_heads, page_size, 64] (codes in [-7, 7], column 2j of a head in the low half of byte
+    j), their scales bf16 [num_pages, n_kv_heads, page_size, 4], one for 32 columns: max / 7 rounded to five
+    significant bits, so that a code times its scale is a bf16 number.  Rows, offsets and lengths are those of
+    :func:`paged_kv_append`."""
+    dev = K.get_device()
+    T, width, ld, _, rows_dt = _kv_pair(K, V, None, None, dev)
+    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, _ = _cache_int4(k_pages, v_pages, page_table, seq_lens,
+                                                                              k_page_scale, v_page_scale, dev)
+    if width != n_kv * HEAD_DIM:
+        raise ValueError("the rows must have the cache's n_kv_heads")
+    if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", dev) != batch + 1:
+        raise ValueError("cu_seqlens must have batch + 1 entries")
+    st = _on(dev, load().paged_kv_append_int4,
+             (K.data_ptr(), V.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_page_scale.data_ptr(),
+              v_page_scale.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), T, batch, n_kv,
+              HEAD_DIM, page, n_pages, max_pages, ld, ldt, pitch, spitch), stream)
+    if st:
+        _check("paged_kv_append_int4", st)
+
+
+def paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, rows=None, k_page_scale=None,
+                  v_page_scale=None, K=None, V=None, stream=None):
+    """Tokens of a paged cache (bf16, E4M3 or 4 bits) back as bf16 rows [T, n_kv_heads * 128]; returns (K, V).
+
+    Rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 are the last of the first seq_lens[b] tokens of sequence b; without
+    cu_seqlens row b is the last one.  rows: how many to allocate where K and V are not given and cu_seqlens is (rows
+    in no sequence are zeros then; of given tensors they stay as they were).  A row whose position or page is outside
+    the table or the cache is NaN."""
+    if (K is None) != (V is None):
+        raise ValueError("K and V: expected both or neither")
+    if stream is not None and K is None:  # what is made here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens, rows, k_page_scale, v_page_scale)
+    dev = k_pages.get_device()
+    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _any_cache(k_pages, v_pages, page_table, seq_lens,
+                                                                              k_page_scale, v_page_scale, dev)
+    if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", dev) != batch + 1:
+        raise ValueError("cu_seqlens must have batch + 1 entries")
+    if K is None:
+        if rows is None and cu_seqlens is not None:
+            raise ValueError("rows: expected the number of rows, or K and V")
+        K, V = ((torch.empty if cu_seqlens is None else torch.zeros)(
+            (batch if rows is None else rows, n_kv * HEAD_DIM), dtype=_BF16, device=k_pages.device) for _ in range(2))
+    T, width, ld, _, _ = _kv_pair(K, V, None, None, dev)
+    if width != n_kv * HEAD_DIM:
+        raise ValueError("the rows must have the cache's n_kv_heads")
+    if rows is not None and rows != T:
+        raise ValueError("rows: not those of K and V")
+    st = _on(dev, load().paged_kv_read,
+             (k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale), page_table.data_ptr(),
+              seq_lens.data_ptr(), _addr(cu_seqlens), K.data_ptr(), V.data_ptr(), T, batch, n_kv, HEAD_DIM, page, n_pages,
+              max_pages, ld, ldt, pitch, spitch, dt), stream)
+    if st:
+        _check("paged_kv_read", st)
+    return K, V
 
 
 def _fresh(n: int, head: int, device) -> torch.Tensor:
@@ -742,7 +840,7 @@ def attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale=Non
                                     workspace)
     dev = Q.get_device()
     rows, width, ldq = _query(Q, "Q", dev)
-    batch, n_kv, page, n_pages, max_pages, ldt, pitch, spitch, dt = _cache(k_pages, v_pages, page_table, seq_lens,
+    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _cache(k_pages, v_pages, page_table, seq_lens,
                                                                           k_page_scale, v_page_scale, dev)
     if rows != batch:
         raise ValueError("Q: expected one row for each sequence")

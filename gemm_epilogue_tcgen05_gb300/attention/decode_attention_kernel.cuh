@@ -326,8 +326,8 @@ __global__ void __launch_bounds__(kDecThreads, DecodeTraits<FP8, NT>::kCtas) att
       if (FP8) {  // lane = row of the step
         const bool there = ok && lane < rows;
         const long long at = mypage * p.c.scale_pitch + cell + (one_page ? lane : 0);
-        cp_async_4_or_zero(dst + 2 * T::kTile + lane * 4, p.c.ks + at, there);
-        cp_async_4_or_zero(dst + 2 * T::kTile + 128 + lane * 4, p.c.vs + at, there);
+        cp_async_4_or_zero(dst + 2 * T::kTile + lane * 4, static_cast<const float*>(p.c.ks) + at, there);
+        cp_async_4_or_zero(dst + 2 * T::kTile + 128 + lane * 4, static_cast<const float*>(p.c.vs) + at, there);
       }
       pt += T::kUnit;
       settle();

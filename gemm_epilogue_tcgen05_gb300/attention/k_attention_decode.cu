@@ -56,8 +56,10 @@ extern "C" int attention_decode(const void* Q, const void* k_pages, const void* 
   if (Q == nullptr || O == nullptr) return FL_ERR_INVALID_ARG;
   const int64_t width = static_cast<int64_t>(n_heads) * kHeadDim;
   if (batch > 1 && (ldq < width || ldo < width)) return FL_ERR_INVALID_ARG;
+  CacheCell cell;
+  cache_cell(cache_dtype, &cell);
   int st = check_cache(k_pages, v_pages, k_page_scale, v_page_scale, page_table, seq_lens, batch, n_kv_heads,
-                       page_size, num_pages, max_pages, ldt, page_pitch, scale_pitch, fp8);
+                       page_size, num_pages, max_pages, ldt, page_pitch, scale_pitch, cell);
   if (st != FL_OK) return st;
   if (!aligned16(Q) || !aligned16(O) || (batch > 1 && (!pitch_ok(ldq, 2) || !pitch_ok(ldo, 2)))) return FL_ERR_ALIGNMENT;
   if (workspace == nullptr || workspace_bytes < fl_attention_decode_workspace_bytes()) return FL_ERR_WORKSPACE;

@@ -39,21 +39,6 @@ bool encode_q(CUtensorMap* map, const void* base, int heads, int rows, int64_t l
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class Kernel, class... Args>
-bool launch_dependent(Kernel* kernel, dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait in the kernels
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
-}
-
 template <bool FP8>
 int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di, cudaStream_t s) {
   using T = PrefillTraits;

@@ -34,18 +34,6 @@ struct AppendParams {
 
 enum AppendMode : int { APPEND_BF16 = 0, APPEND_FP8 = 1, APPEND_QUANT = 2 };
 
-// The sequence that row r belongs to: the last b with cu[b] <= r (sequences without rows are skipped);
-// -1 for rows before the first and behind the last sequence.
-__device__ __forceinline__ int sequence_of_row(const int* cu, int batch, int r) {
-  int lo = 0, hi = batch;  // cu[lo] <= r < cu[hi] once both ends are checked
-  if (r < cu[0] || r >= cu[batch]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= r) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -196,8 +184,10 @@ extern "C" int paged_kv_append(const void* K, const void* V, const float* k_scal
   if (K == nullptr || V == nullptr || (rows8 && (k_scale == nullptr || v_scale == nullptr))) return FL_ERR_INVALID_ARG;
   if (T > 1 && (ldkv < static_cast<int64_t>(n_kv_heads) * kHeadDim || (rows8 && lds < n_kv_heads)))
     return FL_ERR_INVALID_ARG;
+  CacheCell cell;
+  cache_cell(cache_dtype, &cell);
   int st = check_cache(k_pages, v_pages, k_page_scale, v_page_scale, page_table, seq_lens, batch, n_kv_heads,
-                       page_size, num_pages, max_pages, ldt, page_pitch, scale_pitch, cache8);
+                       page_size, num_pages, max_pages, ldt, page_pitch, scale_pitch, cell);
   if (st != FL_OK) return st;
   if (!aligned16(K) || !aligned16(V) || (T > 1 && !pitch_ok(ldkv, rows8 ? 1 : 2))) return FL_ERR_ALIGNMENT;
   if (((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) |

@@ -3,9 +3,9 @@
  * Every fused_* entry point computes a Linear layer Y = X W^T (+ b) on the tcgen05
  * tensor cores, keeps the fp32 accumulator tile in tensor memory, and applies
  * the memory-bound tail ("epilogue") to that tile before anything is written
- * to HBM; no intermediate tensor is materialised.  Three more (paged_kv_append,
- * attention_prefill, attention_decode) take what the QKV projections write: they
- * put keys and values into a paged cache and compute the attention over them.
+ * to HBM; no intermediate tensor is materialised.  The paged_kv_* and
+ * attention_* calls take what the QKV projections write: they put keys and values
+ * into a paged cache, read them back and compute the attention over them.
  *
  * Conventions shared by all entry points
  *   - Matrices are row-major.  X is [M, K] with leading dimension ldx (in
@@ -63,7 +63,7 @@ typedef enum fl_status {
     FL_ERR_ARCH = 7           /* the current device is not sm_103 */
 } fl_status;
 
-enum { FL_F32 = 0, FL_BF16 = 1, FL_E4M3 = 2 };
+enum { FL_F32 = 0, FL_BF16 = 1, FL_E4M3 = 2, FL_INT4 = 3 };
 enum { FL_GELU_ERF = 0, FL_GELU_TANH = 1 };
 
 /* Linear + bias + GELU.
@@ -380,6 +380,40 @@ FL_API int attention_prefill(const void* Q, const void* K, const void* V, const 
                              int64_t lds, int64_t ldo, float scale, int causal, int kv_dtype, void* workspace,
                              size_t workspace_bytes, void* stream);
 FL_API size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, int kv_dtype);
+
+/* ---------------------------------------------------------------- the 4-bit cache
+ * A paged cache as above of type FL_INT4, a bit more than a quarter of the bytes of bf16:
+ *   k_pages, v_pages   [num_pages] blocks `page_pitch` bytes apart, each [n_kv_heads][page_size][64]
+ *                      bytes: codes in [-7, 7] (two's complement), column 2j of a head in the low half
+ *                      of byte j;
+ *   k_page_scale, v_page_scale  [num_pages] blocks `scale_pitch` bf16 apart, each
+ *                      [n_kv_heads][page_size][4] bf16, one scale for 32 consecutive columns; 8-byte
+ *                      aligned, scale_pitch a multiple of 4.
+ * An entry stands for code * scale.  Scales that paged_kv_append_int4 writes have five significant bits,
+ * so that each entry is a bf16 number; the readers take any bf16 that is not negative. */
+
+/* bf16 rows of keys and values into a 4-bit cache; rows, offsets, lengths and what is ignored are those of
+ * paged_kv_append.  For 32 consecutive columns y of a head with a = max|y|:
+ *   s = a / 7 rounded to five significant bits, codes = y / s rounded to whole numbers (both nearest even);
+ * a below 2^-120: zero codes, s = 0; a NaN or an infinity among them: zero codes, s NaN. */
+FL_API int paged_kv_append_int4(const void* K, const void* V, void* k_pages, void* v_pages, void* k_page_scale,
+                                void* v_page_scale, const int32_t* page_table, const int32_t* seq_lens,
+                                const int32_t* cu_seqlens, int T, int batch, int n_kv_heads, int head_dim,
+                                int page_size, int num_pages, int max_pages, int64_t ldkv, int64_t ldt,
+                                int64_t page_pitch, int64_t scale_pitch, void* stream);
+
+/* Tokens of a paged cache (cache_dtype FL_BF16, FL_E4M3 with fp32 scales or FL_INT4) back as bf16 rows
+ * K, V [T, n_kv_heads*128], pitch ldkv elements: what the appends do, the other way round.  Rows
+ * cu_seqlens[b] .. cu_seqlens[b+1] - 1 are the last of the first seq_lens[b] tokens of sequence b (a
+ * smaller number than the sequence's length gives a part from its middle); cu_seqlens NULL: row b is the
+ * last one.  bf16 and 4-bit entries come back exactly, E4M3 entries rounded once.  Rows outside every
+ * sequence stay as they were; a row whose position or page is outside the table or the cache is NaN.  K
+ * and V must not overlap each other or the cache. */
+FL_API int paged_kv_read(const void* k_pages, const void* v_pages, const void* k_page_scale,
+                         const void* v_page_scale, const int32_t* page_table, const int32_t* seq_lens,
+                         const int32_t* cu_seqlens, void* K, void* V, int T, int batch, int n_kv_heads,
+                         int head_dim, int page_size, int num_pages, int max_pages, int64_t ldkv, int64_t ldt,
+                         int64_t page_pitch, int64_t scale_pitch, int cache_dtype, void* stream);
 
 /* fused_linear_gelu (bf16) on HOST buffers: copies in, GEMM + epilogue, copies out.
  *   X [M,K], W [N,K], b [N] (nullable) and Y [M,N] are contiguous bf16 arrays in host
