@@ -17,7 +17,8 @@ the deferred-scale chain :func:`fused_linear_residual_gamma` and
 :func:`fused_dgrad_gelu` and :func:`fused_swiglu_bwd`; for the attention behind
 the QKV projections :func:`paged_kv_append`, :func:`attention_prefill` and
 :func:`attention_decode`; for a cache held in 4 bits :func:`paged_kv_append_int4` and
-:func:`paged_kv_read` (which reads the others back, too).
+:func:`paged_kv_read` (which reads the others back, too), and over any cache, with a
+sliding window, :func:`attention_decode_window`.
 """
 from __future__ import annotations
 
@@ -89,6 +90,8 @@ def load() -> ctypes.CDLL:
     lib.paged_kv_read.restype = I
     lib.attention_decode.argtypes = [P] * 8 + [I] * 7 + [I64] * 5 + [F, I, P, SZ, P]
     lib.attention_decode.restype = I
+    lib.attention_decode_window.argtypes = [P] * 8 + [I] * 7 + [I64] * 5 + [F, I, I, I, P, SZ, P]
+    lib.attention_decode_window.restype = I
     lib.fl_attention_decode_workspace_bytes.argtypes = []
     lib.fl_attention_decode_workspace_bytes.restype = SZ
     lib.attention_prefill.argtypes = [P] * 7 + [I] * 6 + [I64] * 4 + [F, I, I, P, SZ, P]
@@ -858,6 +861,46 @@ def attention_decode(Q, k_pages, v_pages, page_table, seq_lens, k_page_scale=Non
               workspace.data_ptr(), _space(workspace, dev)), stream)
     if st:
         _check("attention_decode", st)
+    return O
+
+
+def _span(n, name):
+    """A number of tokens; what no sequence can have is as good as the longest one."""
+    if n < 0:
+        raise ValueError(f"{name}: expected a number of tokens, not {n}")
+    return min(n, 0x7FFFFFFF)
+
+
+def attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window=0, sinks=0, k_page_scale=None,
+                            v_page_scale=None, scale=None, O=None, workspace=None, stream=None):
+    """:func:`attention_decode` over a paged cache of bf16, E4M3 or 4 bits, each token seeing the last `window` tokens
+    of its sequence (itself among them) and its first `sinks` ones; a window of 0: all of them.
+
+    Pages in front of the window that hold no sinks are not looked at.  Workspaces are those of attention_decode."""
+    if stream is not None and (O is None or workspace is None):  # what is made here belongs to that stream, too
+        with torch.cuda.stream(stream):
+            return attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window, sinks, k_page_scale,
+                                           v_page_scale, scale, O, workspace)
+    dev = Q.get_device()
+    rows, width, ldq = _query(Q, "Q", dev)
+    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _any_cache(k_pages, v_pages, page_table, seq_lens,
+                                                                              k_page_scale, v_page_scale, dev)
+    if rows != batch:
+        raise ValueError("Q: expected one row for each sequence")
+    if O is None:
+        O = torch.empty((rows, width), dtype=_BF16, device=Q.device)
+    o_rows, o_width, ldo = _query(O, "O", dev)
+    if o_rows != rows or o_width != width:
+        raise ValueError("O must have Q's shape")
+    if workspace is None:
+        workspace = attention_decode_workspace(Q.device)
+    st = _on(dev, load().attention_decode_window,
+             (Q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale),
+              page_table.data_ptr(), seq_lens.data_ptr(), O.data_ptr(), batch, width // HEAD_DIM, n_kv, HEAD_DIM, page,
+              n_pages, max_pages, ldq, ldo, ldt, pitch, spitch, HEAD_DIM ** -0.5 if scale is None else scale,
+              _span(window, "window"), _span(sinks, "sinks"), dt, workspace.data_ptr(), _space(workspace, dev)), stream)
+    if st:
+        _check("attention_decode_window", st)
     return O
 
 

@@ -415,6 +415,22 @@ FL_API int paged_kv_read(const void* k_pages, const void* v_pages, const void* k
                          int head_dim, int page_size, int num_pages, int max_pages, int64_t ldkv, int64_t ldt,
                          int64_t page_pitch, int64_t scale_pitch, int cache_dtype, void* stream);
 
+/* attention_decode over a cache of any type (FL_BF16, FL_E4M3, FL_INT4), with a sliding window.
+ * The new token of sequence b is its last one, position i = seq_lens[b] - 1.  window > 0: it sees the
+ * positions j <= i with j > i - window or j < sinks (its own last `window` tokens, and the first `sinks` of
+ * the sequence); window 0: all.  window and sinks may be longer than a sequence; negative ones are
+ * FL_ERR_INVALID_ARG.  Tokens that are not seen are not read, and page table entries in front of the
+ * window (behind the sinks) need not be pages: a cache may have given them back.
+ * 4 bits: weights are rounded to fp16, and so is their product with the part of V's scale that is not a power
+ * of two common to the token's four; a scale of V that is not finite makes its 32 columns of the result NaN.
+ * Other arguments, the workspace and errors are those of attention_decode. */
+FL_API int attention_decode_window(const void* Q, const void* k_pages, const void* v_pages, const void* k_page_scale,
+                                   const void* v_page_scale, const int32_t* page_table, const int32_t* seq_lens,
+                                   void* O, int batch, int n_heads, int n_kv_heads, int head_dim, int page_size,
+                                   int num_pages, int max_pages, int64_t ldq, int64_t ldo, int64_t ldt,
+                                   int64_t page_pitch, int64_t scale_pitch, float scale, int window, int sinks,
+                                   int cache_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* fused_linear_gelu (bf16) on HOST buffers: copies in, GEMM + epilogue, copies out.
  *   X [M,K], W [N,K], b [N] (nullable) and Y [M,N] are contiguous bf16 arrays in host
  *   memory (page-locked for the copies to overlap; pageable memory works, serialised).
