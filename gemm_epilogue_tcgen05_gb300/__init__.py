@@ -17,8 +17,9 @@ the deferred-scale chain :func:`fused_linear_residual_gamma` and
 :func:`fused_dgrad_gelu` and :func:`fused_swiglu_bwd`; for the attention behind
 the QKV projections :func:`paged_kv_append`, :func:`attention_prefill` and
 :func:`attention_decode`; for a cache held in 4 bits :func:`paged_kv_append_int4` and
-:func:`paged_kv_read` (which reads the others back, too), and over any cache, with a
-sliding window, :func:`attention_decode_window`.
+:func:`paged_kv_read` (which reads the others back, too), and with a sliding window
+over any cache :func:`attention_decode_window` and over rows, which may be a prompt's next part
+behind cached ones, :func:`attention_prefill_window`.
 """
 from __future__ import annotations
 
@@ -96,6 +97,8 @@ def load() -> ctypes.CDLL:
     lib.fl_attention_decode_workspace_bytes.restype = SZ
     lib.attention_prefill.argtypes = [P] * 7 + [I] * 6 + [I64] * 4 + [F, I, I, P, SZ, P]
     lib.attention_prefill.restype = I
+    lib.attention_prefill_window.argtypes = [P] * 8 + [I] * 7 + [I64] * 4 + [F, I, I, I, P, SZ, P]
+    lib.attention_prefill_window.restype = I
     lib.fl_attention_prefill_workspace_bytes.argtypes = [I, I, I]
     lib.fl_attention_prefill_workspace_bytes.restype = SZ
     lib.fl_cross_entropy_workspace_bytes.argtypes = [I, I]
@@ -947,6 +950,48 @@ def attention_prefill(Q, K, V, cu_seqlens=None, seq_len: int = 0, k_scale=None, 
               _space(workspace, dev)), stream)
     if st:
         _check("attention_prefill", st)
+    return O
+
+
+def attention_prefill_window(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, seq_len: int = 0, window=0, sinks=0,
+                             k_scale=None, v_scale=None, scale=None, O=None, workspace=None, stream=None):
+    """Causal :func:`attention_prefill` in which a row sees the last `window` tokens of its sequence (itself among them)
+    and its first `sinks` ones; a window of 0: all of them.
+
+    cu_seqlens_k: offsets of the keys' rows, where the queries are the last rows of longer sequences (the next part of a
+    prompt behind rows that :func:`paged_kv_read` returns): sequence b has query rows cu_seqlens[b] .. and key rows
+    cu_seqlens_k[b] ..; a query in front of the first key gets zeros.  The workspace is that of attention_prefill for
+    K's rows."""
+    if stream is not None and (O is None or workspace is None):
+        with torch.cuda.stream(stream):
+            return attention_prefill_window(Q, K, V, cu_seqlens, cu_seqlens_k, seq_len, window, sinks, k_scale, v_scale,
+                                            scale, O, workspace)
+    dev = Q.get_device()
+    M, width, ldq = _query(Q, "Q", dev)
+    rows, kv_width, ldkv, lds, dt = _kv_pair(K, V, k_scale, v_scale, dev)
+    n_kv = kv_width // HEAD_DIM
+    batch = 0 if cu_seqlens is None else _ints(cu_seqlens, "cu_seqlens", dev) - 1
+    if batch < 0:
+        raise ValueError("cu_seqlens must have batch + 1 entries")
+    if cu_seqlens_k is None:
+        if rows != M:
+            raise ValueError("Q, K and V must have the same number of rows, or cu_seqlens_k be given")
+    elif cu_seqlens is None or _ints(cu_seqlens_k, "cu_seqlens_k", dev) != batch + 1:
+        raise ValueError("cu_seqlens_k: expected as many entries as cu_seqlens")
+    if O is None:
+        O = (torch.empty if cu_seqlens is None else torch.zeros)((M, width), dtype=_BF16, device=Q.device)
+    o_rows, o_width, ldo = _query(O, "O", dev)
+    if o_rows != M or o_width != width:
+        raise ValueError("O must have Q's shape")
+    if workspace is None:
+        workspace = attention_prefill_workspace(rows, n_kv, dt == FL_E4M3, Q.device)
+    st = _on(dev, load().attention_prefill_window,
+             (Q.data_ptr(), K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens),
+              _addr(cu_seqlens_k), O.data_ptr(), M, rows, batch, width // HEAD_DIM, n_kv, HEAD_DIM,
+              min(seq_len, M) or max(M, 1), ldq, ldkv, lds, ldo, HEAD_DIM ** -0.5 if scale is None else scale,
+              _span(window, "window"), _span(sinks, "sinks"), dt, workspace.data_ptr(), _space(workspace, dev)), stream)
+    if st:
+        _check("attention_prefill_window", st)
     return O
 
 

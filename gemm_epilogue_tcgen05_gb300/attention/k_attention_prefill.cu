@@ -1,11 +1,12 @@
-// attention_prefill: argument checks, tensor maps and launch (the kernel: prefill_attention_kernel.cuh).
+// attention_prefill and attention_prefill_window: argument checks, tensor maps and launch (the kernel:
+// prefill_attention_kernel.cuh).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 
-#include "prefill_attention_kernel.cuh"
+#include "e4m3_tiles_kernel.cuh"
+#include "prefill_attention_host.cuh"
 
 namespace fl {
 namespace {
@@ -39,23 +40,6 @@ bool encode_q(CUtensorMap* map, const void* base, int heads, int rows, int64_t l
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8>
-int launch_prefill(const PrefillParams& p, long long tiles, const DeviceInfo& di, cudaStream_t s) {
-  using T = PrefillTraits;
-  const void* fn = reinterpret_cast<const void*>(&attention_prefill_kernel<FP8>);
-  if (!ensure_smem_attr(fn, di.device, T::kSmem)) return FL_ERR_CUDA;
-  // the warps share out the registers of the launch: with any other number of them the kernel would not start
-  static std::atomic<int> regs{0};
-  if (regs.load() == 0) {
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, fn) != cudaSuccess) return FL_ERR_CUDA;
-    regs.store(a.numRegs);
-  }
-  if (regs.load() != kPreRegs) return FL_ERR_UNSUPPORTED;
-  const int grid = tiles < di.num_sms ? static_cast<int>(tiles) : di.num_sms;
-  return launch_dependent(attention_prefill_kernel<FP8>, grid, kPreThreads, T::kSmem, s, p) ? FL_OK : FL_ERR_CUDA;
-}
-
 }  // namespace
 }  // namespace fl
 
@@ -68,19 +52,22 @@ extern "C" size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, in
   return 2 * kWsStatusBytes + (kv_dtype == FL_E4M3 ? rows * (kHeadDim * (sizeof(__nv_bfloat16) + sizeof(__half)) + sizeof(float)) : 0);
 }
 
-extern "C" int attention_prefill(const void* Q, const void* K, const void* V, const float* k_scale,
-                                 const float* v_scale, const int32_t* cu_seqlens, void* O, int M, int batch,
-                                 int n_heads, int n_kv_heads, int head_dim, int seq_len, int64_t ldq, int64_t ldkv,
-                                 int64_t lds, int64_t ldo, float scale, int causal, int kv_dtype, void* workspace,
-                                 size_t workspace_bytes, void* stream) {
-  using namespace fl;
-  if (M < 0 || n_heads < 0 || n_kv_heads < 0 || (cu_seqlens != nullptr ? batch < 0 : seq_len < 1))
+namespace fl {
+namespace {
+
+int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_scale, const float* v_scale,
+                    const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, void* O, int M, int M_k, int batch, int n_heads,
+                    int n_kv_heads, int head_dim, int seq_len, int64_t ldq, int64_t ldkv, int64_t lds, int64_t ldo,
+                    float scale, int causal, int window, int sinks, int kv_dtype, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (M < 0 || M_k < 0 || n_heads < 0 || n_kv_heads < 0 || (cu_seqlens != nullptr ? batch < 0 : seq_len < 1))
     return FL_ERR_INVALID_ARG;
+  if (cu_seqlens_k != nullptr ? cu_seqlens == nullptr : M_k != M) return FL_ERR_INVALID_ARG;
   const bool fp8 = kv_dtype == FL_E4M3;
   float scale_log2;
   if ((kv_dtype != FL_BF16 && !fp8) || !scale_to_base_2(scale, &scale_log2)) return FL_ERR_INVALID_ARG;
   if (M == 0 || n_heads == 0 || (cu_seqlens != nullptr && batch == 0)) return FL_OK;
-  if (n_kv_heads == 0 || n_heads % n_kv_heads != 0) return FL_ERR_INVALID_ARG;
+  if (M_k == 0 || n_kv_heads == 0 || n_heads % n_kv_heads != 0) return FL_ERR_INVALID_ARG;
   if (head_dim != kHeadDim) return FL_ERR_UNSUPPORTED;
   if (n_heads > kMaxHeads) return FL_ERR_UNSUPPORTED;
   if (Q == nullptr || K == nullptr || V == nullptr || O == nullptr) return FL_ERR_INVALID_ARG;
@@ -90,9 +77,9 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return FL_ERR_ALIGNMENT;
   if (!pitch_ok(ldq, 2) || !pitch_ok(ldo, 2) || !pitch_ok(ldkv, fp8 ? 1 : 2)) return FL_ERR_ALIGNMENT;
   if (((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) |
-        reinterpret_cast<uintptr_t>(cu_seqlens)) & 3u) != 0)
+        reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(cu_seqlens_k)) & 3u) != 0)
     return FL_ERR_ALIGNMENT;
-  if (workspace == nullptr || workspace_bytes < fl_attention_prefill_workspace_bytes(M, n_kv_heads, kv_dtype))
+  if (workspace == nullptr || workspace_bytes < fl_attention_prefill_workspace_bytes(M_k, n_kv_heads, kv_dtype))
     return FL_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & (kWsStatusBytes - 1)) != 0) return FL_ERR_ALIGNMENT;
   DeviceInfo di;
@@ -108,7 +95,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   while (p.group % p.hp != 0) --p.hp;
   p.tq = kPreTile / p.hp;
   p.pairs = n_heads / p.hp;
-  const int64_t kv_bytes = static_cast<int64_t>(M) * kHeadDim * 4;  // of one kv head, as bf16
+  const int64_t kv_bytes = static_cast<int64_t>(M_k) * kHeadDim * 4;  // of one kv head, as bf16
   const int64_t at_once = std::max<int64_t>(kL2Share / kv_bytes, 1);
   const int64_t groups = (n_kv_heads + at_once - 1) / at_once;
   p.pairs_at_once = static_cast<int>((n_kv_heads + groups - 1) / groups) * (p.group / p.hp);
@@ -125,8 +112,8 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   int64_t ld16 = ldkv;
   if (fp8) {
     __nv_bfloat16* kw = reinterpret_cast<__nv_bfloat16*>(ws + 2 * kWsStatusBytes);
-    __half* vw = reinterpret_cast<__half*>(kw + static_cast<size_t>(M) * kv_width);
-    p.powers = reinterpret_cast<const float*>(vw + static_cast<size_t>(M) * kv_width);
+    __half* vw = reinterpret_cast<__half*>(kw + static_cast<size_t>(M_k) * kv_width);
+    p.powers = reinterpret_cast<const float*>(vw + static_cast<size_t>(M_k) * kv_width);
     k16 = kw, v16 = vw, ld16 = kv_width;
     p.codes = static_cast<const uint8_t*>(V);
     p.v_scale = v_scale;
@@ -134,9 +121,9 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
     p.ld_scale = lds;
   }
   if (!encode_q(&p.map_q, Q, n_heads, M, ldq, p.hp, p.tq) ||
-      !encode_2d(&p.map_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k16, kv_width, M, ld16, 64, kPreTile,
+      !encode_2d(&p.map_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k16, kv_width, M_k, ld16, 64, kPreTile,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&p.map_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, v16, kv_width, M, ld16, 64, kPreTile,
+      !encode_2d(&p.map_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, v16, kv_width, M_k, ld16, 64, kPreTile,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return FL_ERR_CUDA;
   p.V = static_cast<const __nv_bfloat16*>(v16);
@@ -147,24 +134,59 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
   p.ldo = ldo;
   p.M = M;
   p.causal = causal != 0;
-  p.flat = p.batch > (p.causal ? kTierBatch : kTierBatchFull);
+  // a window as long as the rows hides nothing
+  p.window = window < M_k ? window : 0;
+  p.sinks = sinks < M_k ? sinks : M_k;
+  p.cu_k = cu_seqlens_k;
+  p.M_k = M_k;
+  p.flat = p.window > 0 || p.batch > (p.causal ? kTierBatch : kTierBatchFull);
   p.scale_log2 = scale_log2;
   p.status = reinterpret_cast<int*>(ws);
   p.work = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);
   p.timeout_ns = wait_timeout_ns();
-  if (!fp8) return launch_prefill<false>(p, blocks * p.pairs, di, s);
+  const bool windowed = p.window > 0 || cu_seqlens_k != nullptr;
+  if (!fp8)
+    return windowed ? launch_prefill_window(p, false, blocks * p.pairs, di, s)
+                    : launch_prefill<false, false>(p, blocks * p.pairs, di, s);
+  const int32_t* cu_tiles = cu_seqlens_k != nullptr ? cu_seqlens_k : cu_seqlens;
   const long long key_tiles =
       cu_seqlens == nullptr
           ? static_cast<long long>(M / seq_len) * ((seq_len - 1) / kPreTile + 1) + (M % seq_len + kPreTile - 1) / kPreTile
-          : static_cast<long long>(M) / kPreTile + batch;  // the numbers that tiles can have
+          : static_cast<long long>(M_k) / kPreTile + batch;  // the numbers that tiles can have
   const long long parts = key_tiles * (kPreTile / kCodesRows);
   if (parts > INT32_MAX) return FL_ERR_UNSUPPORTED;
   if (!launch_dependent(e4m3_tiles_kernel, dim3(static_cast<unsigned>(parts), (n_kv_heads - 1) / kCodesHeads + 1), 256, 0, s,
                         static_cast<const uint8_t*>(K),
                         static_cast<const uint8_t*>(V), k_scale, v_scale, static_cast<long long>(ldkv),
-                        static_cast<long long>(lds), cu_seqlens, p.batch, seq_len, M, n_kv_heads,
+                        static_cast<long long>(lds), cu_tiles, p.batch, seq_len, M_k, n_kv_heads,
                         static_cast<__nv_bfloat16*>(const_cast<void*>(k16)), static_cast<__half*>(const_cast<void*>(v16)),
                         const_cast<float*>(p.powers)))
     return FL_ERR_CUDA;
-  return launch_prefill<true>(p, blocks * p.pairs, di, s);
+  return windowed ? launch_prefill_window(p, true, blocks * p.pairs, di, s)
+                  : launch_prefill<true, false>(p, blocks * p.pairs, di, s);
+}
+
+}  // namespace
+}  // namespace fl
+
+extern "C" int attention_prefill(const void* Q, const void* K, const void* V, const float* k_scale,
+                                 const float* v_scale, const int32_t* cu_seqlens, void* O, int M, int batch,
+                                 int n_heads, int n_kv_heads, int head_dim, int seq_len, int64_t ldq, int64_t ldkv,
+                                 int64_t lds, int64_t ldo, float scale, int causal, int kv_dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  return fl::enqueue_prefill(Q, K, V, k_scale, v_scale, cu_seqlens, nullptr, O, M, M, batch, n_heads, n_kv_heads, head_dim,
+                             seq_len, ldq, ldkv, lds, ldo, scale, causal, 0, 0, kv_dtype, workspace, workspace_bytes,
+                             stream);
+}
+
+extern "C" int attention_prefill_window(const void* Q, const void* K, const void* V, const float* k_scale,
+                                        const float* v_scale, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k,
+                                        void* O, int M, int M_k, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                        int seq_len, int64_t ldq, int64_t ldkv, int64_t lds, int64_t ldo, float scale,
+                                        int window, int sinks, int kv_dtype, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+  if (window < 0 || sinks < 0) return FL_ERR_INVALID_ARG;
+  return fl::enqueue_prefill(Q, K, V, k_scale, v_scale, cu_seqlens, cu_seqlens_k, O, M, M_k, batch, n_heads, n_kv_heads,
+                             head_dim, seq_len, ldq, ldkv, lds, ldo, scale, 1, window, sinks, kv_dtype, workspace,
+                             workspace_bytes, stream);
 }

@@ -28,6 +28,11 @@
 // sequences can be more than the L2 holds.  So the heads are worked off in groups whose keys and values are at
 // most 32 MB.
 //
+// Window (WIN, causal).  Queries are the last tokens of their sequence's keys, which have offsets of their own, and row i sees
+// the keys of the last `window` tokens and the first `sinks`.  A unit of work goes over the key tiles that hold the sinks and
+// then over those from the first key that its first row sees; any of them may be masked.  The blocks of a long prompt cost the
+// same then, so they come in the order of the sequences.
+//
 // Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
 //
@@ -100,6 +105,8 @@ struct alignas(128) PrefillParams {
   long long ld_codes, ld_scale;
   int n_kv;
   const int* cu;
+  const int* cu_k;         // WIN: offsets of the keys' rows, of which there are M_k; null: those of the queries
+  int M_k, window, sinks;  // WIN; a window of 0 hides nothing
   __nv_bfloat16* O;
   long long ldo;
   int M, batch, seq_len, causal, flat;
@@ -124,11 +131,13 @@ struct PrefillTraits {
 
 // One unit of work.
 struct PrefillTile {
-  int row0, len;   // the sequence's first row and length
-  int tok0;        // first token of query tile 0 (query tile 1: + tq)
+  int row0, len;   // the sequence's first row of keys, and their number (WIN: it may be none)
+  int tok0;        // first token of query tile 0 (query tile 1: + tq), as a position
   int n0, n1;      // key tiles that query tiles 0 and 1 meet
   int head0, kvh;
-  int bad_lo, bad_hi;  // set by warp 11: first and last key of masked tiles whose V is not finite (none: hi < 0)
+  int q_row0;            // row of position 0 (WIN: as if the queries began there; else row0)
+  int sink_tiles, jump;  // WIN: key tiles from sink_tiles on are `jump` further on
+  int bad_lo, bad_hi;    // set by warp 11: first and last key of masked tiles whose V is not finite (none: hi < 0)
 };
 
 struct PrefillBars {
@@ -265,7 +274,7 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const __grid_constant__ PrefillParams p) {
   using T = PrefillTraits;
   extern __shared__ uint8_t smem_raw[];
@@ -307,9 +316,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     if (!pre_wait(&bar.tile_full[k % kPreRing], (k / kPreRing) & 1, wc, W_PRE_TILE_FULL)) return false;
     const volatile PrefillTile& s = bar.tile[k % kPreRing];
     t.row0 = s.row0, t.len = s.len, t.tok0 = s.tok0, t.n0 = s.n0, t.n1 = s.n1, t.head0 = s.head0, t.kvh = s.kvh;
-    return t.len > 0;
+    if (WIN) t.q_row0 = s.q_row0, t.sink_tiles = s.sink_tiles, t.jump = s.jump;
+    return WIN ? t.n0 > 0 : t.len > 0;  // a tile of WIN may have no keys
   };
   auto first_masked = [&](const PrefillTile& t) { return p.causal ? (t.tok0 + 1) / kPreTile : t.len / kPreTile; };
+  // Which of the sequence's key tiles the i-th of a unit is, and whether all rows see all of it.
+  auto key_tile = [&](const PrefillTile& t, int i) { return WIN && i >= t.sink_tiles ? i + t.jump : i; };
+  auto plain_tile = [&](const PrefillTile& t, int i) {
+    const int k0 = key_tile(t, i) * kPreTile, last = k0 + kPreTile - 1;
+    return last <= t.tok0 && (p.window == 0 || last < p.sinks || k0 > t.tok0 + 2 * p.tq - 1 - p.window);
+  };
 
   if (warp >= 8) {
   fewer_registers<kPreRegsOther>();
@@ -404,13 +420,32 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         t.row0 = first;
         t.len = last - first;
         t.tok0 = (!p.causal ? in : p.flat ? (t.len - 1) / tpc - in : tier) * tpc;
+        int shift = 0;  // position of the first query
+        if (WIN) {
+          int first_k = first, last_k = last;
+          if (p.cu_k != nullptr) sequence_rows(p.cu_k, seq, 0, p.M_k, first_k, last_k);
+          shift = (last_k - first_k) - t.len;
+          t.row0 = first_k, t.len = last_k - first_k;
+          t.q_row0 = first - shift;
+          t.tok0 += shift;
+        }
         const int packs = p.group / p.hp;
         t.kvh = pair / packs;
         t.head0 = t.kvh * p.group + (pair - t.kvh * packs) * p.hp;
         const int all = (t.len - 1) / kPreTile + 1;
         // tokens [tok0, tok0 + tq) and [tok0 + tq, tok0 + 2 tq), cut off at the sequence's end
-        t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
-        t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
+        if (WIN) {  // queries in front of the first key (or without any) have a tile of masked keys
+          const int from = t.tok0 - p.window + 1;  // first key of the window of the first row
+          const int sink_tiles = static_cast<int>((static_cast<unsigned>(p.sinks) + kPreTile - 1) / kPreTile);
+          t.sink_tiles = 0, t.jump = 0;
+          if (p.window > 0 && from > 0 && from / kPreTile > sink_tiles)
+            t.sink_tiles = sink_tiles, t.jump = from / kPreTile - sink_tiles;
+          t.n0 = max((min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 - t.jump, 1);
+          t.n1 = t.tok0 + p.tq >= t.len ? 0 : max((min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 - t.jump, 1);
+        } else {
+          t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
+          t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
+        }
         long_before = max(t.n0, t.n1) >= 4;
       }
       if (lane == 0) {
@@ -443,8 +478,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!(ok = pre_wait(&bar.kv_empty[st], ((fills >> 1) & 1) ^ 1, wc, W_PRE_KV_EMPTY))) break;
         mbar_arrive_expect_tx(&bar.kv_full[st], (has_v + has_k) * kPreTileBytes);
         ++fills;
-        const int v_row = t.row0 + i * kPreTile, v_col = t.kvh * kHeadDim;
-        const int k_row = last ? next.row0 : v_row + kPreTile, k_col = last ? next.kvh * kHeadDim : v_col;
+        const int v_row = t.row0 + key_tile(t, i) * kPreTile, v_col = t.kvh * kHeadDim;
+        const int k_row = last ? next.row0 + key_tile(next, 0) * kPreTile : t.row0 + key_tile(t, i + 1) * kPreTile, k_col = last ? next.kvh * kHeadDim : v_col;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint8_t* to = smem + (2 + 2 * st) * kPreTileBytes + h * (kPreTileBytes / 2);
@@ -463,7 +498,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll 1
           for (int h = 0; h < 2; ++h)
             tma_load_3d(&p.map_q, &bar.q_full[s], q_smem + s * kPreTileBytes + h * (kPreTileBytes / 2), h * 64, next.head0,
-                        next.row0 + next.tok0 + s * p.tq);
+                        (WIN ? next.q_row0 : next.row0) + next.tok0 + s * p.tq);
         }
         mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
         t = next;
@@ -553,7 +588,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int plain = min(min(t.n0, t.n1) - 1, mask0);  // steps without a mask that both query tiles go on behind
       int i = 0;
 #pragma unroll 1
-      for (; i < plain; ++i) {
+      for (; !WIN && i < plain; ++i) {
         const int st = (uses - 1) & 1;
         p_wait(0);
         pv(0, st, i == 0, false);
@@ -575,7 +610,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         }
         const bool next = !last || more;  // another key tile, of this unit of work or the next
         const int st = (uses - 1) & 1;
-        if (i >= mask0) {
+        if (WIN ? !plain_tile(t, i) : i >= mask0) {
           wait(&bar.v_ok[st], (v_phase >> st) & 1, W_PRE_V);
           v_phase ^= 1u << st;
         }
@@ -619,7 +654,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       for (int i = 0; i < n; ++i, ++fills) {
         const int st = fills & 1;
         if (!(ok = warp_wait(&bar.kv_full[st], (fills >> 1) & 1, wc, W_PRE_KV_FULL))) break;
-        if (i < mask0) {
+        if (WIN ? plain_tile(t, i) : i < mask0) {
           if (lane == 0) mbar_arrive(&bar.kv_empty[st]);
           continue;
         }
@@ -645,7 +680,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             const uint4 w = ld_shared_v4(base + c * 512);
             bad_chunk = false;
             st_shared_v4(base + c * 512, clean(w.x), clean(w.y), clean(w.z), clean(w.w));
-            const int pos = i * kPreTile + (c & 31) * 4 + (lane >> 3);  // half a key's values are 128 bytes
+            const int pos = key_tile(t, i) * kPreTile + (c & 31) * 4 + (lane >> 3);  // half a key's values are 128 bytes
             if (bad_chunk && pos < t.len) lo = min(lo, pos), hi = max(hi, pos);
           }
           lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
@@ -672,12 +707,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const int row_tok = row / p.hp;
     const float c = p.scale_log2;
     auto load_powers = [&](const PrefillTile& t, int n, int i) {
-      const long long tile = i + lane;
-      return tile < n ? p.powers[(t.row0 + tile * kPreTile) * p.n_kv + t.kvh] : 0.f;
+      const long long tile = key_tile(t, i + lane);
+      return i + lane < n && (!WIN || tile * kPreTile < t.len) ? p.powers[(t.row0 + tile * kPreTile) * p.n_kv + t.kvh] : 0.f;
     };
     // E4M3: the single keys of a tile, in fp32 from their codes and scales: into l and O, and out of S.  O is complete: S
     // of this tile was committed behind the products before.
-    auto single_keys = [&](const PrefillTile& t, int i, bool first_too, int lim, float& m, float& mx, float& l, bool& begun) {
+    auto single_keys = [&](const PrefillTile& t, int i, bool first_too, int lim, int low, float& m, float& mx, float& l, bool& begun) {
       const long long key0 = t.row0 + static_cast<long long>(i) * kPreTile;
       const int keys = min(kPreTile, t.len - i * kPreTile);
       uint32_t which[4], scales[4];  // of key 32 h + lane
@@ -712,7 +747,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           bits = __shfl_sync(~0u, h < 2 ? (h == 0 ? scales[0] : scales[1]) : (h == 2 ? scales[2] : scales[3]), j & 31);
           const float logit = tmem_ld1(s_tmem + j) * c;
           tmem_st1(s_tmem + j, -INFINITY);
-          sees = i * kPreTile + j <= lim;
+          sees = i * kPreTile + j <= lim && (!WIN || i * kPreTile + j >= low || i * kPreTile + j < p.sinks);
           x = sees ? logit : -INFINITY;
           const float up_l = fmaxf(mx, x);
           l = l * ex2(mx - up_l) + ex2(x - up_l);
@@ -764,6 +799,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int tok = first + row_tok;
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int lim_lo = __reduce_min_sync(~0u, lim);              // last key that every row of this warp sees
+      const int low = WIN && p.window > 0 ? tok - p.window + 1 : INT_MIN;     // first key of this row's window
+      const int low_hi = WIN ? __reduce_max_sync(~0u, low) : INT_MIN;         // from here on every row sees (up to lim_lo)
       float m = kPreNone, l = 0.f;
       float mx = kPreNone;         // E4M3: the maximum that l is held at (m is that of O)
       float powers = powers_next;  // E4M3: of key tile i in lane i % 32
@@ -789,14 +826,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmem_ld32(s_tmem + j * 32, x[j]);
           tmem_ld_wait();
-          if (i * kPreTile + kPreTile - 1 > lim_lo) {
-            const int cols = lim - i * kPreTile, all = lim_lo - i * kPreTile;  // columns up to these count
+          const int key0 = key_tile(t, i) * kPreTile;
+          if (key0 + kPreTile - 1 > lim_lo) {
+            const int cols = lim - key0, all = lim_lo - key0;  // columns up to these count
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               if (h * 32 + 31 > all) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                   if (h * 32 + j > cols) x[h][j] = __float_as_uint(-INFINITY);
+              }
+          }
+          if (WIN && key0 < low_hi && key0 + kPreTile > p.sinks) {
+            const int from = low - key0, all = low_hi - key0, sinks = p.sinks - key0;  // columns below `sinks` and from `from` on count
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (h * 32 < all && h * 32 + 31 >= sinks) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (h * 32 + j < from && h * 32 + j >= sinks) x[h][j] = __float_as_uint(-INFINITY);
               }
           }
           float t4[4];
@@ -867,7 +915,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         tc_fence_after();
         const int marks = __float2int_rn(__shfl_sync(~0u, powers, i & 31) / kPreMark);
         begun |= i > 0;
-        single_keys(t, i, (marks & PRE_SINGLE_FIRST) != 0, lim, m, mx, l, begun);
+        single_keys(t, key_tile(t, i), (marks & PRE_SINGLE_FIRST) != 0, lim, low, m, mx, l, begun);
         single_done = i;
       }
       if (!ok) break;
@@ -877,7 +925,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
         tc_fence_after();
-        const float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;  // E4M3: O is held at m - 7, l at mx
+        float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;  // E4M3: O is held at m - 7, l at mx
+        if (WIN && l == 0.f) inv = 0.f;  // a row that sees nothing
         const volatile PrefillTile& said = bar.tile[k % kPreRing];
         const int bad_lo = said.bad_lo, bad_hi = said.bad_hi;
         // A thread has a row; lines of global memory want a few rows each, all of 128 bytes.  So 16-byte pieces go
@@ -892,7 +941,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         const int d_tok = kRowsPer / p.hp, d_head = kRowsPer - d_tok * p.hp;
         const long long d_off = d_tok * p.ldo + d_head * kHeadDim, d_wrap = p.ldo - static_cast<long long>(p.hp) * kHeadDim;
         const int toks = min(p.tq, t.len - first);
-        __nv_bfloat16* dst = p.O + static_cast<long long>(t.row0 + first + tok_first) * p.ldo +
+        const int row_zero = WIN ? t.q_row0 : t.row0;
+        __nv_bfloat16* dst = p.O + static_cast<long long>(row_zero + first + tok_first) * p.ldo +
                              static_cast<long long>(t.head0 + head_first) * kHeadDim + piece * 8;
 #pragma unroll 1
         for (int j = 0; j < kHeadDim; j += T::kOutCols) {
@@ -928,13 +978,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           // Values of V that are not finite were taken out for the rows that do not see them.  The others get their
           // sum (infinite or NaN), whatever the finite rest is.
           const __nv_bfloat16* v = p.V + static_cast<long long>(t.row0) * p.ldv + static_cast<long long>(t.kvh) * kHeadDim;
-          __nv_bfloat16* mine = p.O + static_cast<long long>(t.row0 + tok) * p.ldo +
+          __nv_bfloat16* mine = p.O + static_cast<long long>(row_zero + tok) * p.ldo +
                                 static_cast<long long>(t.head0 + row - row_tok * p.hp) * kHeadDim;
 #pragma unroll 1
           for (int d = 0; d < kHeadDim; ++d) {
             float sum = 0.f;
 #pragma unroll 1
             for (int pos = bad_lo; pos <= min(bad_hi, lim); ++pos) {
+              if (WIN && pos < low && pos >= p.sinks) {  // on to the window
+                pos = min(low, bad_hi + 1) - 1;
+                continue;
+              }
               const __nv_bfloat16 raw = v[static_cast<long long>(pos) * p.ldv + d];
               const float y = FP8 ? __half2float(__ushort_as_half(__bfloat16_as_ushort(raw))) : __bfloat162float(raw);
               if (!isfinite(y)) sum += y;
@@ -954,153 +1008,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && bar.abort_flag != 0) record_failure(p.status, bar.abort_flag, 0);
-}
-
-// E4M3 codes of K and V times their scales, for the kernel above: K as bf16, V as fp16 times 2^-b, with b for each key
-// tile (128 rows of a sequence, from its first) and head: from V's largest finite scale where the tile's scales lie
-// within kPreWindow powers of two, else from the window of that width that holds most of its keys; in either case not
-// beyond kPrePowerMin and kPrePowerMax.  The keys outside it are written as zeros and marked as single keys.  Bound by
-// memory: 1 byte in and 2 out for each value.  A CTA takes 16 rows of a key tile for up to 32 heads at a time, a thread
-// 8 codes (16 bytes out; with 16 codes each store left half sectors to the next one); the scales of the whole tile are
-// read by each of its eight CTAs (an eighth more to read, from L2) rather than one CTA turning a tile of one head (18.5
-// instead of 11.2 us for 12400 rows of 8 heads, caches cold: too few, too long).
-constexpr int kCodesRows = 16, kCodesHeads = 32;
-
-__global__ void __launch_bounds__(256, 4) e4m3_tiles_kernel(
-    const uint8_t* K, const uint8_t* V, const float* ks, const float* vs, long long ld, long long lds, const int* cu,
-    int batch, int seq_len, int M, int n_kv, __nv_bfloat16* K16, __half* V16, float* powers) {
-  __shared__ uint32_t top[kCodesHeads], low[kCodesHeads];  // largest and smallest finite scale of V, as bit patterns
-  __shared__ float power[kCodesHeads];
-  __shared__ int window[kCodesHeads];  // exponent field of its top; -1: it holds all keys
-  __shared__ unsigned most;
-  __shared__ short fields[kPreTile];
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < kCodesHeads) top[tid] = 0, low[tid] = ~0u;
-  if (cu != nullptr && tid <= batch) asm volatile("prefetch.global.L2 [%0];" ::"l"(cu + tid));
-  griddep_wait();
-  griddep_launch_dependents();
-  __syncthreads();
-  constexpr int kParts = kPreTile / kCodesRows;
-  const int tile = static_cast<int>(blockIdx.x / kParts), part = static_cast<int>(blockIdx.x % kParts);
-  const int h0 = static_cast<int>(blockIdx.y) * kCodesHeads, heads = min(kCodesHeads, n_kv - h0);
-  // Key tile j of sequence b has number cu[b] / 128 + b + j: no two have the same one, and each warp finds the sequence by
-  // itself, by 32 probes at a time for the last b whose number is not above the tile's.
-  int b = 0, at = tile;
-  auto number = [&](int b) { return min(max(cu[b], 0), M) / kPreTile + b; };
-  if (cu == nullptr) {
-    const int each = (seq_len - 1) / kPreTile + 1;
-    b = tile / each, at = tile - b * each;
-  } else {
-    for (int n = batch; n > 1;) {
-      const int step = (n + 31) / 32;
-      const unsigned below = __ballot_sync(~0u, lane * step < n && number(b + lane * step) <= tile);
-      const int past = (32 - __clz(below) - 1) * step;
-      if (below == 0) return;
-      b += past;
-      n = min(step, n - past);
-    }
-    at -= number(b);
-  }
-  int first, last;
-  sequence_rows(cu, b, seq_len, M, first, last);
-  if (at < 0 || at > (last - first - 1) / kPreTile) return;  // a number that nothing has; the same for all threads
-  const int row0 = first + at * kPreTile, rows = min(kPreTile, last - row0);
-  if (part * kCodesRows >= rows) return;  // the same for all threads
-  const int r = part * kCodesRows + (tid >> 4), c = tid & 15;  // 16 threads a row and head
-  const bool there = r < rows;
-  const long long row = row0 + (there ? r : 0);
-  constexpr int kTogether = 4;
-  uint2 k[kTogether], v[kTogether];
-  float sk[kTogether], sv[kTogether];
-  auto fetch = [&](int j0) {
-#pragma unroll
-    for (int i = 0; i < kTogether; ++i) {
-      if (j0 + i >= heads) break;
-      const long long h = h0 + j0 + i;
-      k[i] = reinterpret_cast<const uint2*>(K + row * ld + h * kHeadDim)[c];
-      v[i] = reinterpret_cast<const uint2*>(V + row * ld + h * kHeadDim)[c];
-      sk[i] = ks[row * lds + h];
-      sv[i] = vs[row * lds + h];
-    }
-  };
-  fetch(0);
-  {
-    const int each = 256 / heads, j = tid % heads;
-    uint32_t largest = 0, smallest = ~0u;
-    if (tid < each * heads)
-      for (int q = tid / heads; q < rows; q += each) {
-        const float x = fabsf(vs[(row0 + q) * lds + h0 + j]);
-        if (x < INFINITY) largest = max(largest, __float_as_uint(x)), smallest = min(smallest, __float_as_uint(x));
-      }
-    if (smallest != ~0u) atomicMax(&top[j], largest), atomicMin(&low[j], smallest);
-  }
-  __syncthreads();
-  constexpr int kFieldMin = 127 + kPreRoom + kPrePowerMin, kFieldMax = 127 + kPreRoom + kPrePowerMax;
-  bool wide = false;
-  if (tid < heads) {
-    const int field = static_cast<int>(top[tid] >> 23);
-    wide = top[tid] != 0 && (field - static_cast<int>(low[tid] >> 23) >= kPreWindow || field < kFieldMin || field > kFieldMax);
-    power[tid] = top[tid] == 0 ? kPreZero : static_cast<float>(field - (127 + kPreRoom));
-    window[tid] = wide ? field : -1;
-  }
-  if (__syncthreads_or(wide)) {
-#pragma unroll 1
-    for (int j = 0; j < heads; ++j) {
-      if (window[j] < 0) continue;  // the same for all threads
-      if (tid == 0) most = 0;
-      if (tid < kPreTile) {
-        const uint32_t bits = tid < rows ? __float_as_uint(fabsf(vs[(row0 + tid) * lds + h0 + j])) : 0u;
-        fields[tid] = bits == 0 || bits >= 0x7F800000u ? -1 : static_cast<short>(bits >> 23);
-      }
-      __syncthreads();
-      if (tid < rows && fields[tid] >= kFieldMin && fields[tid] <= kFieldMax) {
-        const int mine = fields[tid];
-        unsigned n = 0;
-        for (int q = 0; q < rows; ++q) n += fields[q] > mine - kPreWindow && fields[q] <= mine;
-        atomicMax(&most, n << 8 | mine);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        window[j] = most != 0 ? static_cast<int>(most & 255u) : 512;  // 512: holds none
-        power[j] = most != 0 ? static_cast<float>(window[j] - (127 + kPreRoom)) : 0.f;
-      }
-    }
-    __syncthreads();
-  }
-  for (int j0 = 0; j0 < heads; j0 += kTogether) {
-    if (j0 > 0) fetch(j0);
-#pragma unroll
-    for (int i = 0; i < kTogether; ++i) {
-      if (j0 + i >= heads || !there) break;
-      auto codes = [](uint2 in, float scale, auto pack) {
-        uint32_t out[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t two;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>((e < 2 ? in.x : in.y) >> ((e & 1) * 16))));
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-          out[e] = pack(f.x * scale, f.y * scale);
-        }
-        return make_uint4(out[0], out[1], out[2], out[3]);
-      };
-      const float b = power[j0 + i];
-      const int win = window[j0 + i];
-      const uint32_t bits = __float_as_uint(fabsf(sv[i]));
-      const int field = static_cast<int>(bits >> 23);
-      const bool single = win >= 0 && field < 255 && (bits == 0 || field > win || field <= win - kPreWindow);
-      // 448 * scale * 2^-b is below 2^16 * 0.875
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(b)) << 23);
-      const long long to = (row * n_kv + h0 + j0 + i) * (kHeadDim / 8) + c;
-      reinterpret_cast<uint4*>(K16)[to] = codes(k[i], sk[i], [](float x, float y) { return pack_bf16x2(x, y); });
-      uint4 v16 = codes(v[i], sv[i] * down, [](float x, float y) { return pack_f16x2(x, y); });
-      if (single && bits != 0) v16 = make_uint4(0, 0, 0, 0);  // a scale of zero leaves zeros, and what is not a number
-      reinterpret_cast<uint4*>(V16)[to] = v16;
-      if (c == 0 && (r == 0 || win >= 0))
-        powers[row * n_kv + h0 + j0 + i] =
-            r == 0 ? b + kPreMark * ((win >= 0 ? PRE_SINGLE : 0) | (single ? PRE_SINGLE_FIRST : 0))
-                   : single ? 1.f : 0.f;
-    }
-  }
 }
 
 }  // namespace fl

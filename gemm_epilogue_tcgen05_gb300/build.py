@@ -44,7 +44,8 @@ def _deps():
 
 # Kernels whose warps share out the registers that they are launched with: with any other number than the one their
 # source counts on they would not start.  Source file: (kernel, file and name of the constant).
-REGISTERS = {"k_attention_prefill.cu": ("attention_prefill_kernel", "prefill_attention_kernel.cuh", "kPreRegs")}
+REGISTERS = {f: ("attention_prefill_kernel", "prefill_attention_kernel.cuh", "kPreRegs")
+             for f in ("k_attention_prefill.cu", "k_attention_prefill_window.cu")}
 
 
 def check_registers(src: str, ptxas: str) -> None:

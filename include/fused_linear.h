@@ -431,6 +431,23 @@ FL_API int attention_decode_window(const void* Q, const void* k_pages, const voi
                                    int64_t page_pitch, int64_t scale_pitch, float scale, int window, int sinks,
                                    int cache_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* attention_prefill (causal) with a sliding window, and for a part of a prompt behind cached tokens.
+ * K and V have M_k rows and, where the queries are only the last rows of their sequences, offsets of their
+ * own: sequence b has query rows cu_seqlens[b] .. and key rows cu_seqlens_k[b] .. (int32 [batch + 1] each,
+ * cu_seqlens_k as cu_seqlens; NULL: the same offsets, M_k = M).  With len_q and len_k rows, query row r is
+ * at position i = len_k - len_q + r of the keys: the rows that paged_kv_read gives of a cache that the new
+ * tokens were appended to.  It sees the keys j <= i and, with window > 0, of these j > i - window or
+ * j < sinks.  A row that sees no key (i < 0) gets zeros.  window and sinks may be longer than any sequence;
+ * negative ones are FL_ERR_INVALID_ARG, and so are M_k == 0 with M > 0, cu_seqlens_k without cu_seqlens, and
+ * M_k != M without cu_seqlens_k.  The workspace is that of attention_prefill for M_k rows; other
+ * arguments, what may hold NaN, roundings and errors are those of attention_prefill. */
+FL_API int attention_prefill_window(const void* Q, const void* K, const void* V, const float* k_scale,
+                                    const float* v_scale, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k,
+                                    void* O, int M, int M_k, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                    int seq_len, int64_t ldq, int64_t ldkv, int64_t lds, int64_t ldo, float scale,
+                                    int window, int sinks, int kv_dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
 /* fused_linear_gelu (bf16) on HOST buffers: copies in, GEMM + epilogue, copies out.
  *   X [M,K], W [N,K], b [N] (nullable) and Y [M,N] are contiguous bf16 arrays in host
  *   memory (page-locked for the copies to overlap; pageable memory works, serialised).

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gemm_epilogue_tcgen05_gb300 as fl
-from attention_utils import D, F16, assert_within, cu
+from attention_utils import BF16, D, F16, assert_within, cu, quantise, rounded, tile_powers, values
 from window_utils import AnyCache, attend_window
 
 pytestmark = pytest.mark.gpu
@@ -320,3 +320,309 @@ def test_projection_append_and_decode_steps_over_4_bits():
                                          vv[rows].double().view(n, 4, D).transpose(0, 1), D ** -0.5, window, sinks, 2 * F16,
                                          scales=c.value_scales(b))
                 assert_within(out[b].view(4, 1, D), ref, tol, f"step {step}, sequence {b}")
+
+
+# ---------------------------------------------------------------- prefill
+def rows_of(n, heads, seed=0, std=1.0):
+    return randn(n, heads * D, seed=seed, std=std)
+
+
+def keys_of(rows, kv, fp8, seed=0):
+    k, v = randn(rows, kv, D, seed=seed + 1), randn(rows, kv, D, seed=seed + 2)
+    ks = vs = None
+    if fp8:
+        (k, ks), (v, vs) = quantise(k), quantise(v)
+    return k.view(rows, -1), v.view(rows, -1), ks, vs
+
+
+def check_prefill(q, k, v, ks, vs, lens, out, window=0, sinks=0, lens_k=None, scale=D ** -0.5, what="", first=0, first_k=0):
+    heads, kv = q.shape[1] // D, k.shape[1] // D
+    for b, (n, n_k) in enumerate(zip(lens, lens_k or lens)):
+        rows, keys = slice(first, first + n), slice(first_k, first_k + n_k)
+        first, first_k = first + n, first_k + n_k
+        if n == 0:
+            continue
+        got = out[rows].view(n, heads, D).transpose(0, 1)
+        if n_k == 0:
+            assert (got == 0).all(), f"{what}: sequence {b} has no keys"
+            continue
+        kk = values(k[keys].reshape(n_k, kv, D), None if ks is None else ks[keys]).transpose(0, 1)
+        vv = values(v[keys].reshape(n_k, kv, D), None if vs is None else vs[keys]).transpose(0, 1)
+        qq = q[rows].double().reshape(n, heads, D).transpose(0, 1)
+        if ks is not None:
+            kk = rounded(kk)
+            ref, tol = attend_window(qq, kk, vv, scale, window, sinks, 2 * F16, powers=tile_powers(vs[keys]))
+        else:
+            ref, tol = attend_window(qq, kk, vv, scale, window, sinks, BF16)
+        assert_within(got, ref, tol, f"{what} sequence {b} of {n} behind {n_k - n}")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (64, 0), (100, 4), (128, 128), (129, 1), (200, 200), (500, 64), (1000, 0)])
+@pytest.mark.parametrize("heads,kv", [(4, 1), (3, 3), (24, 2), (48, 1), (80, 1)])
+def test_prefill_window_matches_the_definition(heads, kv, window, sinks, fp8):
+    lens = [1, 700, 0, 130, 128, 333]
+    q = rows_of(sum(lens), heads, seed=40)
+    k, v, ks, vs = keys_of(sum(lens), kv, fp8, seed=41)
+    out = fl.attention_prefill_window(q, k, v, cu_seqlens=cu(lens), window=window, sinks=sinks, k_scale=ks, v_scale=vs)
+    check_prefill(q, k, v, ks, vs, lens, out, window, sinks)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3), (300, 150)])
+@pytest.mark.parametrize("heads,kv", [(8, 2), (16, 16), (20, 4)])
+def test_prefill_behind_cached_rows_matches_the_definition(heads, kv, window, sinks, fp8):
+    """Histories of every kind: none, shorter and longer than the new rows, with and without whole tiles."""
+    lens, lens_k = [1, 33, 128, 0, 200, 5, 300, 64], [900, 33, 129, 70, 328, 1200, 301, 192]
+    q = rows_of(sum(lens), heads, seed=42)
+    k, v, ks, vs = keys_of(sum(lens_k), kv, fp8, seed=43)
+    out = fl.attention_prefill_window(q, k, v, cu_seqlens=cu(lens), cu_seqlens_k=cu(lens_k), window=window, sinks=sinks,
+                                      k_scale=ks, v_scale=vs)
+    check_prefill(q, k, v, ks, vs, lens, out, window, sinks, lens_k)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_rows_in_front_of_the_first_key_are_zeros(fp8):
+    """More queries than keys, no keys at all; what lies in the rows of K there reaches nothing."""
+    lens, lens_k = [5, 300, 129, 40], [2, 0, 128, 41]
+    q = rows_of(sum(lens), 8, seed=44)
+    k, v, ks, vs = keys_of(sum(lens_k) + 200, 2, fp8, seed=45)
+    if fp8:
+        ks[sum(lens_k):], vs[sum(lens_k):] = NAN, INF
+    else:
+        k[sum(lens_k):], v[sum(lens_k):] = NAN, INF
+    for window, sinks in ((0, 0), (3, 1), (200, 7)):
+        out = torch.full((sum(lens), 8 * D), 5.0, dtype=torch.bfloat16, device="cuda")
+        fl.attention_prefill_window(q, k, v, cu_seqlens=cu(lens), cu_seqlens_k=cu(lens_k), window=window, sinks=sinks,
+                                    k_scale=ks, v_scale=vs, O=out)
+        check_prefill(q, k, v, ks, vs, lens, out, window, sinks, lens_k)
+        assert (out[:3] == 0).all() and (out[5:305] == 0).all() and (out[305] == 0).all()
+    # a query alone, without a key, in front of everything
+    out = fl.attention_prefill_window(q[:1], k, v, cu_seqlens=cu([1]), cu_seqlens_k=cu([0]), k_scale=ks, v_scale=vs)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_window_of_long_and_many_sequences(fp8):
+    lens = [3000, 20] + [(7 * i * i + 3) % 97 for i in range(150)] + [1100]
+    q = rows_of(sum(lens), 4, seed=46)
+    k, v, ks, vs = keys_of(sum(lens), 2, fp8, seed=47)
+    for window, sinks in ((256, 4), (1024, 64), (40, 500)):
+        out = fl.attention_prefill_window(q, k, v, cu_seqlens=cu(lens), window=window, sinks=sinks, k_scale=ks, v_scale=vs)
+        check_prefill(q, k, v, ks, vs, lens, out, window, sinks)
+
+
+@pytest.mark.parametrize("seq_len,rows", [(64, 256), (300, 1000), (0, 450)])
+def test_prefill_window_of_equal_sequences(seq_len, rows):
+    q = rows_of(rows, 8, seed=48)
+    k, v, _, _ = keys_of(rows, 4, False, seed=49)
+    n = seq_len or rows
+    lens = [n] * (rows // n) + ([rows % n] if rows % n else [])
+    out = fl.attention_prefill_window(q, k, v, seq_len=seq_len, window=150, sinks=2)
+    check_prefill(q, k, v, None, None, lens, out, 150, 2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_window_that_hides_nothing(fp8):
+    lens = [700, 3, 128]
+    q = rows_of(sum(lens), 8, seed=50)
+    k, v, ks, vs = keys_of(sum(lens), 2, fp8, seed=51)
+    call = dict(cu_seqlens=cu(lens), k_scale=ks, v_scale=vs)
+    want = fl.attention_prefill(q, k, v, **call)
+    for window, sinks in ((0, 0), (0, 5), (sum(lens), 0), (1 << 40, 1 << 33)):
+        assert torch.equal(want, fl.attention_prefill_window(q, k, v, window=window, sinks=sinks, **call))
+    for window, sinks in ((700, 0), (600, 100), (1, 830)):  # the windowed kernel
+        out = fl.attention_prefill_window(q, k, v, window=window, sinks=sinks, **call)
+        check_prefill(q, k, v, ks, vs, lens, out, window, sinks)
+    out = fl.attention_prefill_window(q, k, v, cu_seqlens_k=cu(lens), **call)
+    check_prefill(q, k, v, ks, vs, lens, out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(100, 3), (0, 0)])
+def test_prefill_window_leaves_other_rows_and_ignores_their_contents(fp8, window, sinks):
+    lens, lens_k, first, first_k = [150, 70], [400, 70], 20, 33
+    rows, rows_k = 300, 600
+    q = rows_of(rows, 8, seed=52)
+    k, v, ks, vs = keys_of(rows_k, 2, fp8, seed=53)
+    q[:first], q[first + 220:] = NAN, INF
+    for r in (slice(0, first_k), slice(first_k + 470, None)):
+        k[r], v[r] = (0x7F, 0x7F) if fp8 else (INF, NAN)
+        if fp8:
+            ks[r], vs[r] = NAN, INF
+    out = torch.full((rows, 8 * D), 3.0, dtype=torch.bfloat16, device="cuda")
+    fl.attention_prefill_window(q, k, v, cu_seqlens=cu(lens) + first, cu_seqlens_k=cu(lens_k) + first_k, window=window,
+                                sinks=sinks, k_scale=ks, v_scale=vs, O=out)
+    check_prefill(q, k, v, ks, vs, lens, out, window, sinks, lens_k, first=first, first_k=first_k)
+    assert (out[:first] == 3).all() and (out[first + 220:] == 3).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_prefill_window_values_that_are_not_finite_reach_only_who_sees_them(which, bad, fp8):
+    """In the sinks, in a window, and at keys that most rows do not see any more."""
+    n, window, sinks = 900, 130, 40
+    lens = [n, 64]
+    at = [7, 39, 300, 511, 512]
+    q = rows_of(sum(lens), 4, seed=54)
+    k, v, ks, vs = keys_of(sum(lens), 1, fp8, seed=55)
+    clean = [k.clone(), v.clone(), None if ks is None else ks.clone(), None if vs is None else vs.clone()]
+    for j in at[2:]:
+        if fp8:
+            (ks if which == "k" else vs)[j] = abs(bad)  # scales are not negative
+        else:
+            (k if which == "k" else v)[j, 5] = bad
+    call = dict(cu_seqlens=cu(lens), window=window, sinks=sinks)
+    out = fl.attention_prefill_window(q, k, v, k_scale=ks, v_scale=vs, **call)
+    i = torch.arange(n, device="cuda")
+    sees = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for j in at[2:]:
+        sees |= (i >= j) & (i < j + window)
+    hidden = torch.cat([~sees, torch.ones(64, dtype=torch.bool, device="cuda")])
+    assert torch.isfinite(out[hidden]).all()
+    ref = fl.attention_prefill_window(q, *clean[:2], k_scale=clean[2], v_scale=clean[3], **call)
+    if not fp8 or which == "k":
+        assert torch.equal(out[hidden], ref[hidden])
+    seen = out[:n][sees]
+    if which == "v" and not fp8:
+        assert (~torch.isfinite(seen.view(-1, 4, D)[..., 5])).all()
+        keep = torch.arange(D, device="cuda") != 5
+        assert torch.equal(seen.view(-1, 4, D)[..., keep], ref[:n][sees].view(-1, 4, D)[..., keep])
+    # in the sinks every row behind sees them
+    k, v, ks, vs = clean
+    for j in at[:2]:
+        if fp8:
+            (ks if which == "k" else vs)[j] = abs(bad)  # scales are not negative
+        else:
+            (k if which == "k" else v)[j, 5] = bad
+    out = fl.attention_prefill_window(q, k, v, k_scale=ks, v_scale=vs, **call)
+    assert torch.isfinite(out[:7]).all() and torch.isfinite(out[n:]).all()
+    if which == "v":
+        col = out[7:n].view(-1, 4, D)[..., 5]
+        assert (~torch.isfinite(col)).all()
+
+
+@pytest.mark.parametrize("shift", [2.0 ** 20, 2.0 ** 40, 2.0 ** -40, 0.0])
+def test_prefill_window_single_keys(shift):
+    """E4M3 keys whose scale of V lies far from the others', in the sinks, at the window's edges, and out of sight."""
+    lens, window, sinks = [800, 130], 200, 5
+    q = rows_of(sum(lens), 8, seed=56)
+    k, v, ks, vs = keys_of(sum(lens), 2, True, seed=57)
+    for j in (0, 3, 4, 6, 255, 256, 600, 799, 801):
+        vs[j] *= shift
+    out = fl.attention_prefill_window(q, k, v, cu_seqlens=cu(lens), window=window, sinks=sinks, k_scale=ks, v_scale=vs)
+    first = 0
+    for b, n in enumerate(lens):
+        r = slice(first, first + n)
+        first += n
+        kk = rounded(values(k[r].view(n, 2, D), ks[r]).transpose(0, 1))
+        vv = values(v[r].view(n, 2, D), vs[r]).transpose(0, 1)
+        ref, tol = attend_window(q[r].double().view(n, 8, D).transpose(0, 1), kk, vv, D ** -0.5, window, sinks, 2 * F16)
+        # a weight below fp16's range is off by 2^-32 of the row's largest weight times scale (attention_utils); 210 keys, and a
+        # value is below 2^9 of its scale's power: 2^-15 of that together
+        i = torch.arange(n, device="cuda")
+        seen = ((i[None] <= i[:, None]) & ((i[None] > i[:, None] - window) | (i[None] < sinks))).double()
+        x = (q[r].double().view(n, 8, D).transpose(0, 1) @ kk.repeat_interleave(4, 0).transpose(1, 2) * D ** -0.5)
+        p = torch.softmax(x.masked_fill(seen == 0, -INF), -1)
+        part = (p * vv.abs().amax(-1).repeat_interleave(4, 0)[:, None]).amax(-1, keepdim=True)
+        assert_within(out[r].view(n, 8, D).transpose(0, 1), ref, tol + 2.0 ** -14 * part, f"sequence {b}")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_window_strides_place_streams_and_repeats(fp8):
+    lens, lens_k = [300, 1, 64, 150], [700, 1, 200, 150]
+    q = rows_of(sum(lens), 12, seed=58)
+    k, v, ks, vs = keys_of(sum(lens_k), 4, fp8, seed=59)
+    call = dict(cu_seqlens=cu(lens), cu_seqlens_k=cu(lens_k), window=180, sinks=9, k_scale=ks, v_scale=vs, scale=0.11)
+    want = fl.attention_prefill_window(q, k, v, **call)
+    check_prefill(q, k, v, ks, vs, lens, want, 180, 9, lens_k, scale=0.11)
+
+    def wide(t, more):
+        room = torch.zeros((t.shape[0], t.shape[1] + more), dtype=t.dtype, device="cuda")
+        room[:, :t.shape[1]] = t
+        return room[:, :t.shape[1]]
+    out = wide(torch.zeros_like(q), 2 * D)
+    moved = dict(call, k_scale=None if ks is None else wide(ks, 3), v_scale=None if vs is None else wide(vs, 3))
+    fl.attention_prefill_window(wide(q, D), wide(k, 64), wide(v, 64), O=out, **moved)
+    assert torch.equal(out, want)
+    place = q.clone()
+    assert torch.equal(fl.attention_prefill_window(place, k, v, O=place, **call), want)
+    ws = fl.attention_prefill_workspace(sum(lens_k), 4, fp8)
+    for _ in range(5):
+        assert torch.equal(fl.attention_prefill_window(q, k, v, workspace=ws, **call), want)
+        fl.attention_prefill(q[:150], k[:150], v[:150], k_scale=ks if ks is None else ks[:150],
+                             v_scale=vs if vs is None else vs[:150], workspace=ws)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda._sleep(20000000)
+        got = fl.attention_prefill_window(q, k, v, **call, stream=other)
+        other.synchronize()
+    assert torch.equal(got, want) and fl.check_device_status(ws) == fl.FL_OK
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_window_captured_and_replayed_with_other_offsets(fp8):
+    rows, rows_k = 600, 1500
+    q = rows_of(rows, 8, seed=60)
+    k, v, ks, vs = keys_of(rows_k, 2, fp8, seed=61)
+    offsets, offsets_k = cu([300, 300]), cu([700, 800])
+    out = torch.zeros_like(q)
+    ws = fl.attention_prefill_workspace(rows_k, 2, fp8)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fl.attention_prefill_window(q, k, v, cu_seqlens=offsets, cu_seqlens_k=offsets_k, window=250, sinks=4, k_scale=ks,
+                                    v_scale=vs, O=out, workspace=ws)
+    for lens, lens_k in (([300, 300], [700, 800]), ([1, 599], [900, 600]), ([0, 64], [100, 1400]), ([600, 0], [600, 0])):
+        offsets.copy_(cu(lens)), offsets_k.copy_(cu(lens_k))
+        out.fill_(2)
+        g.replay()
+        check_prefill(q, k, v, ks, vs, lens, out, 250, 4, lens_k)
+        assert (out[sum(lens):] == 2).all()
+
+
+def test_prefill_window_bad_offsets_stay_inside():
+    """Offsets that fall or leave the rows give some rows or none, never a fault."""
+    q = rows_of(200, 4, seed=62)
+    k, v, _, _ = keys_of(300, 2, False, seed=63)
+    for a, b in (([0, 500, 100], [0, 300, 300]), ([-5, 50, 20], [10, 400, 350]), ([0, 100, 200], [300, 0, 900]),
+                 ([0, 100, 200], [-9, -4, -1]), ([200, 300, 400], [0, 100, 200])):
+        fl.attention_prefill_window(q, k, v, cu_seqlens=torch.tensor(a, dtype=torch.int32).cuda(),
+                                    cu_seqlens_k=torch.tensor(b, dtype=torch.int32).cuda(), window=40, sinks=2)
+    torch.cuda.synchronize()
+    assert fl.device_status() == fl.FL_OK
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 4)])
+def test_a_prompt_in_parts_over_a_4_bit_cache(window, sinks):
+    """The run as it is used: each part of two prompts is projected, appended, the context read back, and attended to; the
+    last token once more by decode.  Parts of another cut give the same bits in the cache and agree within the rounding."""
+    hidden, total = 256, [333, 64]
+    x = randn(sum(total), hidden, seed=64)
+    w = randn(3 * 4 * D, hidden, seed=65, std=hidden ** -0.5)
+    kept = None
+    for parts in ([(333, 64)], [(100, 64), (200, 0), (33, 0)], [(128, 1), (128, 62), (77, 1)]):
+        c = AnyCache(total, 4, 16, "int4", seed=66)
+        done, outs = [0, 0], [[], []]
+        for part in parts:
+            rows = torch.cat([x[sum(total[:b]) + done[b]:sum(total[:b]) + done[b] + part[b]] for b in range(2)])
+            pos = torch.cat([torch.arange(done[b], done[b] + part[b]) for b in range(2)]).int().cuda()
+            q, k, v = fl.fused_qkv_rope(rows, w, None, n_heads=4, positions=pos)
+            done = [done[b] + part[b] for b in range(2)]
+            held = torch.tensor(done, dtype=torch.int32).cuda()
+            fl.paged_kv_append_int4(k, v, c.k, c.v, c.ks, c.vs, c.table, held, cu_seqlens=cu(part))
+            kk, vv = fl.paged_kv_read(c.k, c.v, c.table, held, cu_seqlens=cu(done), rows=sum(done), **c.scales())
+            o = fl.attention_prefill_window(q, kk, vv, cu_seqlens=cu(part), cu_seqlens_k=cu(done), window=window, sinks=sinks)
+            check_prefill(q, kk, vv, None, None, part, o, window, sinks, done)
+            outs[0].append(o[:part[0]]), outs[1].append(o[part[0]:])
+            last = q[[part[0] - 1, part[0] + part[1] - 1]] if min(part) > 0 else None
+        if last is not None:
+            one = fl.attention_decode_window(last, c.k, c.v, c.table, c.seq_lens, window=window, sinks=sinks, **c.scales())
+            check_decode(last, c, one, window, sinks)
+        whole = torch.cat([torch.cat(o) for o in outs])
+        if kept is None:
+            kept = whole, kk, vv
+        assert torch.equal(kept[1], kk) and torch.equal(kept[2], vv)
+        # both are within 2^-8 |o| + 2^-8 A of one value, and A is at most the largest value
+        assert ((whole - kept[0]).double().abs() <= 2 * BF16 * (kept[0].double().abs() + vv.double().abs().max())).all()
