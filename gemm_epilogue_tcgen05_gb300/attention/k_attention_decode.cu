@@ -1,9 +1,10 @@
-// attention_decode and attention_decode_window: argument checks and dispatch (the kernel and its design:
-// decode_attention_kernel.cuh).
+// attention_decode and attention_decode_window: argument checks and dispatch (the kernels and their design:
+// decode_attention_kernel.cuh, decode_int4_kernel.cuh).
 #include <algorithm>
 #include <cstdint>
 
 #include "decode_attention_host.cuh"
+#include "decode_attention_kernel.cuh"
 
 namespace fl {
 namespace {
@@ -45,14 +46,22 @@ int enqueue_decode(const void* Q, const void* k_pages, const void* v_pages, cons
   p.ldq = ldq;
   p.ldo = ldo;
   p.group = n_heads / n_kv_heads;
-  p.chunks = (p.group + 15) / 16;
+  const int at_once = cache_dtype == FL_INT4 ? 8 : 16;  // query heads of one pass over the cache
+  p.chunks = (p.group + at_once - 1) / at_once;
   p.chunk_heads = (p.group + p.chunks - 1) / p.chunks;
-  p.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(page_size)) : -1;
+  // division by a product: with 2^bits the first power of two that page_size does not pass, page_mul = ceil(2^(31 + bits) /
+  // page_size) fits 32 bits and is less than 2^bits / page_size <= 1 part in 2^31 too large
+  const int bits = page_size == 1 ? 0 : 32 - __builtin_clz(static_cast<unsigned>(page_size) - 1);
+  p.page_shift = 31 + bits;
+  p.page_mul = static_cast<uint32_t>(((uint64_t{1} << p.page_shift) + page_size - 1) / page_size);
   // units of all lengths that the table allows (64 tokens at least), for all heads
   const int64_t longest = std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, INT32_MAX) / 64 + 1;
   p.small = batch <= 128 && longest * batch < (int64_t{1} << 31) / (static_cast<int64_t>(n_kv_heads) * p.chunks);
   p.window = window;
   p.sinks = sinks;
+  p.eights = 0x00080008u;
+  p.box = 0;
+  p.timeout_ns = wait_timeout_ns();
   p.scale_log2 = scale_log2;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int*>(ws);
@@ -62,9 +71,24 @@ int enqueue_decode(const void* Q, const void* k_pages, const void* v_pages, cons
   // a window that no sequence can pass hides nothing
   const bool windowed = window > 0 && static_cast<int64_t>(window) + sinks < static_cast<int64_t>(max_pages) * page_size;
   const bool fp8 = cache_dtype == FL_E4M3;
-  if (cache_dtype == FL_INT4) return launch_decode_int4(p, windowed, di, s);
+  if (cache_dtype == FL_INT4) {
+    // Tensor copies of 32, 16 or 8 tokens need whole boxes in a page, pages one behind the other (one index finds a row) and
+    // scales that begin on 16 bytes; other caches are copied by 16 bytes.
+    const int64_t rows = static_cast<int64_t>(num_pages) * n_kv_heads * page_size;
+    const int box = page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : page_size % 8 == 0 ? 8 : 0;
+    const bool packed = num_pages == 1 || (page_pitch == static_cast<int64_t>(n_kv_heads) * page_size * cell.elems &&
+                                           scale_pitch % 8 == 0);
+    p.box = packed && rows > 0 && rows <= INT32_MAX && aligned16(k_page_scale) && aligned16(v_page_scale) ? box : 0;
+    if (p.box > 0 && (!encode_2d(&p.map_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, k_pages, cell.elems, rows, cell.elems, cell.elems,
+                                 p.box, CU_TENSOR_MAP_SWIZZLE_64B) ||
+                      !encode_2d(&p.map_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v_pages, cell.elems, rows, cell.elems, cell.elems,
+                                 p.box, CU_TENSOR_MAP_SWIZZLE_64B)))
+      return FL_ERR_CUDA;
+    return launch_decode_int4(p, windowed, di, s);
+  }
   if (windowed) return launch_decode_window(p, fp8, di, s);
-  return fp8 ? launch_decode_tiles<FL_E4M3, false>(p, di, s) : launch_decode_tiles<FL_BF16, false>(p, di, s);
+  auto launch = [&](auto traits, auto* kernel) { return launch_decode<decltype(traits)>(kernel, p, di, s); };
+  return fp8 ? decode_tiles<true, false>(p, launch) : decode_tiles<false, false>(p, launch);
 }
 
 }  // namespace
