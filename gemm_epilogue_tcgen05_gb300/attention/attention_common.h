@@ -66,6 +66,21 @@ inline int check_cache(const void* k_pages, const void* v_pages, const void* ks,
   return FL_OK;
 }
 
+// Division by the page size as a product: pos / page_size = pos * mul >> shift for pos below 2^31.  With 2^bits the first power
+// of two that page_size does not pass, mul = ceil(2^(31 + bits) / page_size) fits 32 bits and is less than 2^bits / page_size
+// <= 1 part in 2^31 too large.
+struct PageDivisor {
+  uint32_t mul;
+  int shift;
+  __device__ __forceinline__ int operator()(int pos) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * mul >> shift);
+  }
+};
+inline PageDivisor page_divisor(int page_size) {
+  const int bits = page_size == 1 ? 0 : 32 - __builtin_clz(static_cast<unsigned>(page_size) - 1);
+  return {static_cast<uint32_t>(((uint64_t{1} << (31 + bits)) + page_size - 1) / page_size), 31 + bits};
+}
+
 // The factor of the logits to base 2: positive and finite, or the scale is refused.
 inline bool scale_to_base_2(float scale, float* out) {
   *out = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
@@ -116,6 +131,19 @@ __device__ __forceinline__ int sequence_of_row(const int* cu, int batch, int r) 
   return lo;
 }
 
+// The same by all lanes of a warp, 32 probes at a time: two loads one behind the other for up to 1000 sequences.
+__device__ __forceinline__ int sequence_of_row(const int* cu, int batch, int r, int lane) {
+  int lo = 0;
+  for (int n = batch + 1; n > 1;) {  // the last of cu[lo .. lo + n - 1] that is not above r
+    const int step = (n - 1) / 32 + 1;
+    const unsigned below = __ballot_sync(~0u, lane * step < n && cu[lo + lane * step] <= r);
+    if (below == 0) return -1;
+    const int past = (31 - __clz(below)) * step;
+    lo += past;
+    n = min(step, n - past);
+  }
+  return lo < batch ? lo : -1;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

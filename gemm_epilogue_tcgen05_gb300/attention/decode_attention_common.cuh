@@ -28,8 +28,7 @@ struct alignas(128) DecodeParams {
   __nv_bfloat16* O;
   long long ldq, ldo;
   int group, chunks, chunk_heads;  // query heads of a kv head, cut into `chunks` of `chunk_heads` (<= 8 NT)
-  uint32_t page_mul;               // pos / page_size = pos * page_mul >> page_shift for pos below 2^31
-  int page_shift;
+  PageDivisor page_of;
   bool small;                      // batch <= 128 and no count can pass 31 bits
   int window, sinks;               // of attention_decode_window
   uint32_t eights;                 // 4 bits: 0x00080008, which the compiler is not to know (int4_even)
@@ -126,9 +125,7 @@ struct DecodeWalk {
   __device__ __forceinline__ bool in_sight(const DecodeSeg& s, int pos) const {
     return !WIN || pos < p.sinks || pos >= s.len - p.window;
   }
-  __device__ __forceinline__ int page_of(int pos) const {
-    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.page_mul >> p.page_shift);
-  }
+  __device__ __forceinline__ int page_of(int pos) const { return p.page_of(pos); }
 };
 
 // Only hints go out before the kernel in front has finished: they bring the address translations (plan done after

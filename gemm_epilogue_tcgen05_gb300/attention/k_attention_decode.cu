@@ -49,11 +49,7 @@ int enqueue_decode(const void* Q, const void* k_pages, const void* v_pages, cons
   const int at_once = cache_dtype == FL_INT4 ? 8 : 16;  // query heads of one pass over the cache
   p.chunks = (p.group + at_once - 1) / at_once;
   p.chunk_heads = (p.group + p.chunks - 1) / p.chunks;
-  // division by a product: with 2^bits the first power of two that page_size does not pass, page_mul = ceil(2^(31 + bits) /
-  // page_size) fits 32 bits and is less than 2^bits / page_size <= 1 part in 2^31 too large
-  const int bits = page_size == 1 ? 0 : 32 - __builtin_clz(static_cast<unsigned>(page_size) - 1);
-  p.page_shift = 31 + bits;
-  p.page_mul = static_cast<uint32_t>(((uint64_t{1} << p.page_shift) + page_size - 1) / page_size);
+  p.page_of = page_divisor(page_size);
   // units of all lengths that the table allows (64 tokens at least), for all heads
   const int64_t longest = std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, INT32_MAX) / 64 + 1;
   p.small = batch <= 128 && longest * batch < (int64_t{1} << 31) / (static_cast<int64_t>(n_kv_heads) * p.chunks);

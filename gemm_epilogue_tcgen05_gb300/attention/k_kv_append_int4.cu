@@ -10,8 +10,8 @@
 // Both roundings are exact although no division is made.  a times fl(1/7) is a/7 itself where 7 divides a's
 // significand (fl(1/7) is 2^-26 off, less than half a step), else no closer than 2^-3 of a step to a border between
 // two values of s.  y / s has a denominator of at most 2 * 31 * 16 beside a power of two, so it is k + 1/2 exactly or
-// 2^-10 off: y * fl(1/s) + 768 in one rounding is its nearest multiple of 2^-14, and the next addition rounds that to
-// a whole number.
+// 2^-10 off: y times an approximate 1/s, plus 768, in one rounding is its nearest multiple of 2^-14, and the next addition
+// rounds that to a whole number.
 //
 // Bound by memory: 512 bytes in and 144 out for each head of a token.  One warp moves a row, all its heads, as in
 // paged_kv_append; a lane takes 8 values, four lanes a group.
@@ -32,6 +32,7 @@ struct AppendInt4Params {
   const int* cu;
   long long ldkv, ldt, page_pitch, scale_pitch;
   int T, batch, n_kv, page_size, num_pages, max_pages;
+  PageDivisor page_of;
 };
 
 __device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
@@ -49,22 +50,32 @@ __device__ __forceinline__ uint32_t magnitudes_nan(const uint4 k, const uint4 v)
 // s of a group from the bf16 bits of its largest magnitude, as an fp32 number: 0 for a group of zeros, NaN for one with
 // a value that is not finite.
 __device__ __forceinline__ float int4_scale(uint32_t largest) {
-  if (largest >= 0x7F80u) return NAN;
-  if (largest < (127u - 120u) << 7) return 0.f;
   const uint32_t b = __float_as_uint(__uint_as_float(largest << 16) * (1.f / 7.f));
-  return __uint_as_float((b + 0x3FFFFu + ((b >> 19) & 1u)) & 0xFFF80000u);
+  const uint32_t s = largest < (127u - 120u) << 7 ? 0u : (b + 0x3FFFFu + ((b >> 19) & 1u)) & 0xFFF80000u;
+  return __uint_as_float(largest >= 0x7F80u ? 0x7FFF0000u : s);
 }
-// 8 values times r = 1/s as codes, value i in bits 4 i; r of 0 or NaN gives zero codes.
-__device__ __forceinline__ uint32_t int4_codes(const uint4 raw, float r) {
+// 1/s to 2^-22 of itself, 0 for 0 and NaN: the fastest will do, for y * inverse(s) is off by 2^-19 at most.
+__device__ __forceinline__ float inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return s > 0.f ? r : 0.f;
+}
+// 8 values over s as codes, value i in bits 4 i; zeros for a group of zeros, and where s is NaN.
+__device__ __forceinline__ uint32_t int4_codes(const uint4 raw, float s) {
+  const float r = inverse(s);
   const float y[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y),
                       bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
-  if (!(r > 0.f)) return 0;
   // 3 * 2^22 + 8 + code: the last bits of the sum are code + 8, whose weighted sum has no carries
   constexpr uint32_t kBase = 0x4B400000u;
+  const uint64_t r2 = f2(r, r), part = f2(768.f, 768.f), whole = f2(12582912.f - 768.f + 8.f, 12582912.f - 768.f + 8.f);
   uint32_t word = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) word = word * 16 + __float_as_uint(fmaf(y[i], r, 768.f) + (12582912.f - 768.f + 8.f));
-  return (word - kBase * 0x11111111u) ^ 0x88888888u;
+  for (int i = 6; i >= 0; i -= 2) {
+    float a, b;
+    f2_split(f2_add(f2_fma(f2(y[i], y[i + 1]), r2, part), whole), a, b);
+    word = (word * 16 + __float_as_uint(b)) * 16 + __float_as_uint(a);
+  }
+  return s >= 0.f ? (word - kBase * 0x11111111u) ^ 0x88888888u : 0u;  // zeros where s is NaN
 }
 
 constexpr int kAppendWarps = 4;
@@ -95,20 +106,21 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_int4_kernel(const
     b = r;
     pos = p.lens[b] - 1;
   } else {
-    b = sequence_of_row(p.cu, p.batch, r);
+    b = sequence_of_row(p.cu, p.batch, r, lane);
     if (b < 0) return;
     const long long at = static_cast<long long>(p.lens[b]) - p.cu[b + 1] + r;
     pos = at > INT32_MAX ? -1 : static_cast<int>(max(at, -1ll));
   }
   if (pos < 0) return;
-  const int pi = pos / p.page_size, slot = pos - pi * p.page_size;
+  const int pi = p.page_of(pos), slot = pos - pi * p.page_size;
   if (pi >= p.max_pages) return;
   const int page = p.table[b * p.ldt + pi];
   if (page < 0 || page >= p.num_pages) return;
-  uint8_t* k_dst = p.kp + page * p.page_pitch + slot * (kHeadDim / 2) + part * 4;
-  uint8_t* v_dst = p.vp + page * p.page_pitch + slot * (kHeadDim / 2) + part * 4;
+  const long long head_step = static_cast<long long>(p.page_size) * (kHeadDim / 2);  // bytes; of the scales an eighth
+  const long long at = page * p.page_pitch + slot * (kHeadDim / 2) + part * 4 + h0 * head_step;
   // of each four lanes the first writes the scale of K, the second that of V
-  __nv_bfloat16* s_dst = ((lane & 1) != 0 ? p.vps : p.kps) + page * p.scale_pitch + slot * kInt4Groups + (part >> 2);
+  __nv_bfloat16* s_dst = ((lane & 1) != 0 ? p.vps : p.kps) + page * p.scale_pitch + slot * kInt4Groups + (part >> 2) +
+                         h0 * (head_step / 16);
   for (int first = 0; first < p.n_kv; first += kTogether * 2) {
     if (first > 0) fetch(first);
 #pragma unroll
@@ -117,11 +129,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_int4_kernel(const
       top = bf16x2_max_nan(top, __shfl_xor_sync(~0u, top, 1));
       top = bf16x2_max_nan(top, __shfl_xor_sync(~0u, top, 2));
       const float sk = int4_scale(top & 0xFFFFu), sv = int4_scale(top >> 16);
-      const long long cell = (first + i * 2 + h0) * static_cast<long long>(p.page_size);
       if (first + i * 2 + h0 >= p.n_kv) continue;
-      *reinterpret_cast<uint32_t*>(k_dst + cell * (kHeadDim / 2)) = int4_codes(k[i], sk > 0.f ? __frcp_rn(sk) : 0.f);
-      *reinterpret_cast<uint32_t*>(v_dst + cell * (kHeadDim / 2)) = int4_codes(v[i], sv > 0.f ? __frcp_rn(sv) : 0.f);
-      if ((lane & 2) == 0) s_dst[cell * kInt4Groups] = __float2bfloat16_rn((lane & 1) != 0 ? sv : sk);
+      const long long ahead = (first + i * 2) * head_step;
+      *reinterpret_cast<uint32_t*>(p.kp + at + ahead) = int4_codes(k[i], sk);
+      *reinterpret_cast<uint32_t*>(p.vp + at + ahead) = int4_codes(v[i], sv);
+      if ((lane & 2) == 0) s_dst[ahead / 16] = __float2bfloat16_rn((lane & 1) != 0 ? sv : sk);
     }
   }
 }
@@ -156,7 +168,7 @@ extern "C" int paged_kv_append_int4(const void* K, const void* V, void* k_pages,
                            static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages),
                            static_cast<__nv_bfloat16*>(k_page_scale), static_cast<__nv_bfloat16*>(v_page_scale),
                            page_table, seq_lens, cu_seqlens, ldkv, ldt, page_pitch, scale_pitch, T, batch, n_kv_heads,
-                           page_size, num_pages, max_pages};
+                           page_size, num_pages, max_pages, page_divisor(page_size)};
   return launch_dependent(kv_append_int4_kernel, dim3((T - 1) / kAppendWarps + 1), 32 * kAppendWarps, 0,
                           static_cast<cudaStream_t>(stream), p)
              ? FL_OK

@@ -18,6 +18,7 @@ struct ReadParams {
   __nv_bfloat16* V;
   long long ldkv;
   int T;
+  PageDivisor page_of;
 };
 
 enum ReadMode : int { READ_BF16 = 0, READ_E4M3 = 1, READ_INT4 = 2 };
@@ -73,14 +74,14 @@ struct Piece<READ_INT4> {
     s = reinterpret_cast<const unsigned short*>(scales)[cell * kInt4Groups + (part >> 2)];
   }
   __device__ __forceinline__ uint4 values() const {
-    const uint32_t ss = __byte_perm(s, s, 0x5410);
-    uint32_t out[4];
+    const uint32_t ss = __byte_perm(s, s, 0x5410), u = x ^ 0x88888888u;
+    const uint32_t even = u & 0x0F0F0F0Fu, odd = u >> 4 & 0x0F0F0F0Fu;
+    const uint32_t low = __byte_perm(even, odd, 0x5140), high = __byte_perm(even, odd, 0x7362);  // columns 0-3 | 4-7, a byte each
+    constexpr uint32_t k128 = 0x43434343u;  // with a byte u below it: 128 + u as bf16
+    uint32_t out[4] = {__byte_perm(low, k128, 0x4140), __byte_perm(low, k128, 0x4342), __byte_perm(high, k128, 0x4140),
+                       __byte_perm(high, k128, 0x4342)};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {  // columns 2e, 2e + 1: 128 + (code ^ 8) as bf16, minus 136 (all exact)
-      const uint32_t byte = x >> (8 * e);
-      const uint32_t u = (((byte & 0xFu) | (byte << 12 & 0xF0000u)) ^ 0x00080008u) | 0x43004300u;
-      out[e] = bf16x2_mul(bf16x2_sub(u, 0x43084308u), ss);
-    }
+    for (int e = 0; e < 4; ++e) out[e] = bf16x2_mul(bf16x2_sub(out[e], 0x43084308u), ss);  // less 136: exact, and so is the product
     return make_uint4(out[0], out[1], out[2], out[3]);
   }
 };
@@ -100,12 +101,12 @@ __global__ void __launch_bounds__(32 * kReadWarps) kv_read_kernel(const ReadPara
     b = r;
     pos = p.c.lens[b] - 1;
   } else {
-    b = sequence_of_row(p.cu, p.c.batch, r);
+    b = sequence_of_row(p.cu, p.c.batch, r, lane);
     if (b < 0) return;
     const long long at = static_cast<long long>(p.c.lens[b]) - p.cu[b + 1] + r;
     pos = at > INT32_MAX ? -1 : static_cast<int>(max(at, -1ll));
   }
-  const int pi = pos < 0 ? -1 : pos / p.c.page_size, slot = pos - pi * p.c.page_size;
+  const int pi = pos < 0 ? -1 : p.page_of(pos), slot = pos - pi * p.c.page_size;
   const int entry = pi < 0 || pi >= p.c.max_pages ? -1 : p.c.table[b * p.c.ldt + pi];
   const bool ok = entry >= 0 && entry < p.c.num_pages;
   const long long page = ok ? entry : 0;
@@ -172,7 +173,8 @@ extern "C" int paged_kv_read(const void* k_pages, const void* v_pages, const voi
   if (st != FL_OK) return st;
   const ReadParams p{CacheView{k_pages, v_pages, k_page_scale, v_page_scale, page_table, seq_lens, page_pitch,
                                scale_pitch, ldt, n_kv_heads, page_size, num_pages, max_pages, batch},
-                     cu_seqlens, static_cast<__nv_bfloat16*>(K), static_cast<__nv_bfloat16*>(V), ldkv, T};
+                     cu_seqlens, static_cast<__nv_bfloat16*>(K), static_cast<__nv_bfloat16*>(V), ldkv, T,
+                     page_divisor(page_size)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool done = cache_dtype == FL_BF16   ? launch_read<READ_BF16>(p, s)
                     : cache_dtype == FL_E4M3 ? launch_read<READ_E4M3>(p, s)
