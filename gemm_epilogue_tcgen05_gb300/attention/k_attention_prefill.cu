@@ -126,6 +126,12 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
       !encode_2d(&p.map_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, v16, kv_width, M_k, ld16, 64, kPreTile,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return FL_ERR_CUDA;
+  if ((window > 0 || cu_seqlens_k != nullptr) &&
+      (!encode_2d(&p.map_k32, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, k16, kv_width, M_k, ld16, 64, 32,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+       !encode_2d(&p.map_v32, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, v16, kv_width, M_k, ld16, 64, 32,
+                  CU_TENSOR_MAP_SWIZZLE_128B)))
+    return FL_ERR_CUDA;
   p.V = static_cast<const __nv_bfloat16*>(v16);
   p.ldv = ld16;
   p.n_kv = n_kv_heads;

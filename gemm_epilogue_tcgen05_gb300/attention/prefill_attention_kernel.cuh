@@ -29,9 +29,11 @@
 // most 32 MB.
 //
 // Window (WIN, causal).  Queries are the last tokens of their sequence's keys, which have offsets of their own, and row i sees
-// the keys of the last `window` tokens and the first `sinks`.  A unit of work goes over the key tiles that hold the sinks and
-// then over those from the first key that its first row sees; any of them may be masked.  The blocks of a long prompt cost the
-// same then, so they come in the order of the sequences.
+// the keys of the last `window` tokens and the first `sinks`.  A unit of work goes over a stream of keys: whole chunks of 32
+// that hold the sinks, then the keys from the chunk on that holds the first key its first row sees.  So a key tile is four
+// such chunks, loaded as one box where they follow one another and as four in the tile in which the sinks end.  (Tiles at multiples of
+// 128 keys, the sinks with one of their own: 116 us for 8192 tokens with a window of 1024 and 4 sinks, 32/8 heads.)  Any tile
+// may be masked.  The blocks of a long prompt cost the same, so they come in the order of the sequences.
 //
 // Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
@@ -105,8 +107,9 @@ struct alignas(128) PrefillParams {
   long long ld_codes, ld_scale;
   int n_kv;
   const int* cu;
-  const int* cu_k;         // WIN: offsets of the keys' rows, of which there are M_k; null: those of the queries
-  int M_k, window, sinks;  // WIN; a window of 0 hides nothing
+  CUtensorMap map_k32, map_v32;  // WIN: the same as map_k and map_v, box {64, 32}
+  const int* cu_k;               // WIN: offsets of the keys' rows, of which there are M_k; null: those of the queries
+  int M_k, window, sinks;        // WIN; a window of 0 hides nothing
   __nv_bfloat16* O;
   long long ldo;
   int M, batch, seq_len, causal, flat;
@@ -135,9 +138,9 @@ struct PrefillTile {
   int tok0;        // first token of query tile 0 (query tile 1: + tq), as a position
   int n0, n1;      // key tiles that query tiles 0 and 1 meet
   int head0, kvh;
-  int q_row0;            // row of position 0 (WIN: as if the queries began there; else row0)
-  int sink_tiles, jump;  // WIN: key tiles from sink_tiles on are `jump` further on
-  int bad_lo, bad_hi;    // set by warp 11: first and last key of masked tiles whose V is not finite (none: hi < 0)
+  int q_row0;          // WIN: row of position 0, as if the queries began there
+  int k0, sink_keys;   // WIN: place P of the stream is key P below sink_keys, else k0 + P - sink_keys
+  int bad_lo, bad_hi;  // set by warp 11: first and last key of masked tiles whose V is not finite (none: hi < 0)
 };
 
 struct PrefillBars {
@@ -231,6 +234,12 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
   return one != 0;
 }
+// The n lowest bits: none for n below 1, all for more than 31.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  uint32_t r;
+  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(32 - min(max(n, 0), 32)));  // a shift by 32 leaves nothing
+  return r;
+}
 // Two values times zero, plus c: NaN for one that is not finite.
 template <bool F16>
 __device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t c) {
@@ -281,15 +290,26 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     if (!pre_wait(&bar.tile_full[k % kPreRing], (k / kPreRing) & 1, wc, W_PRE_TILE_FULL)) return false;
     const volatile PrefillTile& s = bar.tile[k % kPreRing];
     t.row0 = s.row0, t.len = s.len, t.tok0 = s.tok0, t.n0 = s.n0, t.n1 = s.n1, t.head0 = s.head0, t.kvh = s.kvh;
-    if (WIN) t.q_row0 = s.q_row0, t.sink_tiles = s.sink_tiles, t.jump = s.jump;
-    return WIN ? t.n0 > 0 : t.len > 0;  // a tile of WIN may have no keys
+    if (WIN) {
+      t.q_row0 = s.q_row0, t.k0 = s.k0, t.sink_keys = s.sink_keys;
+      return t.n0 > 0;  // a tile may have no keys
+    }
+    return t.len > 0;
   };
   auto first_masked = [&](const PrefillTile& t) { return p.causal ? (t.tok0 + 1) / kPreTile : t.len / kPreTile; };
-  // Which of the sequence's key tiles the i-th of a unit is, and whether all rows see all of it.
-  auto key_tile = [&](const PrefillTile& t, int i) { return WIN && i >= t.sink_tiles ? i + t.jump : i; };
+  // First key of chunk h of a unit's i-th key tile; WIN: and whether all rows see all of the tile, a run of keys.
+  auto key_of = [&](const PrefillTile& t, int i, int h) {
+    if (!WIN) return i * kPreTile + h * 32;
+    const int place = i * kPreTile + h * 32;
+    return place < t.sink_keys ? place : place + t.k0 - t.sink_keys;
+  };
+  auto run_of_keys = [&](const PrefillTile& t, int i) {
+    const int place = i * kPreTile;
+    return !WIN || place >= t.sink_keys || place + kPreTile <= t.sink_keys;
+  };
   auto plain_tile = [&](const PrefillTile& t, int i) {
-    const int k0 = key_tile(t, i) * kPreTile, last = k0 + kPreTile - 1;
-    return last <= t.tok0 && (p.window == 0 || last < p.sinks || k0 > t.tok0 + 2 * p.tq - 1 - p.window);
+    const int first = key_of(t, i, 0), last = first + kPreTile - 1;
+    return run_of_keys(t, i) && last <= t.tok0 && (p.window == 0 || last < p.sinks || first > t.tok0 + 2 * p.tq - 1 - p.window);
   };
 
   if (warp >= 8) {
@@ -307,6 +327,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       return last - first;
     };
     const int tier_len = p.causal ? tpc : kPreTile;
+    // WIN: the stream of the block that begins at position tok0, of a sequence with len_k keys.
+    auto stream_of = [&](int tok0, int len_k, PrefillTile& t) {
+      const int from = (tok0 - p.window + 1) & ~31, sink_keys = static_cast<int>((static_cast<unsigned>(p.sinks) + 31u) & ~31u);
+      const bool gap = p.window > 0 && tok0 - p.window + 1 > 0 && from > sink_keys;
+      t.k0 = gap ? from : 0, t.sink_keys = gap ? sink_keys : 0;
+      // tiles that end at the last key of query tiles 0 and 1; rows in front of the first key (or without any) have one
+      auto tiles = [&](int end) { return max((t.sink_keys + min(end, len_k) - t.k0 - 1) / kPreTile + 1, 1); };
+      t.n0 = tiles(tok0 + p.tq);
+      t.n1 = tok0 + p.tq >= len_k ? 0 : tiles(tok0 + tpc);
+    };
     auto measure = [&](int b, int& reach, int& count) {  // tiers of a sequence, and its blocks
       const int len = b < p.batch ? length_of(b) : 0;
       reach = len > 0 ? (len - 1) / tier_len + 1 : 0;
@@ -385,29 +415,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         t.row0 = first;
         t.len = last - first;
         t.tok0 = (!p.causal ? in : p.flat ? (t.len - 1) / tpc - in : tier) * tpc;
-        int shift = 0;  // position of the first query
         if (WIN) {
           int first_k = first, last_k = last;
           if (p.cu_k != nullptr) sequence_rows(p.cu_k, seq, 0, p.M_k, first_k, last_k);
-          shift = (last_k - first_k) - t.len;
+          const int shift = (last_k - first_k) - t.len;  // position of the first query
           t.row0 = first_k, t.len = last_k - first_k;
           t.q_row0 = first - shift;
           t.tok0 += shift;
+          stream_of(t.tok0, t.len, t);
         }
         const int packs = p.group / p.hp;
         t.kvh = pair / packs;
         t.head0 = t.kvh * p.group + (pair - t.kvh * packs) * p.hp;
         const int all = (t.len - 1) / kPreTile + 1;
         // tokens [tok0, tok0 + tq) and [tok0 + tq, tok0 + 2 tq), cut off at the sequence's end
-        if (WIN) {  // queries in front of the first key (or without any) have a tile of masked keys
-          const int from = t.tok0 - p.window + 1;  // first key of the window of the first row
-          const int sink_tiles = static_cast<int>((static_cast<unsigned>(p.sinks) + kPreTile - 1) / kPreTile);
-          t.sink_tiles = 0, t.jump = 0;
-          if (p.window > 0 && from > 0 && from / kPreTile > sink_tiles)
-            t.sink_tiles = sink_tiles, t.jump = from / kPreTile - sink_tiles;
-          t.n0 = max((min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 - t.jump, 1);
-          t.n1 = t.tok0 + p.tq >= t.len ? 0 : max((min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 - t.jump, 1);
-        } else {
+        if (!WIN) {
           t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
           t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
         }
@@ -443,13 +465,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!(ok = pre_wait(&bar.kv_empty[st], ((fills >> 1) & 1) ^ 1, wc, W_PRE_KV_EMPTY))) break;
         mbar_arrive_expect_tx(&bar.kv_full[st], (has_v + has_k) * kPreTileBytes);
         ++fills;
-        const int v_row = t.row0 + key_tile(t, i) * kPreTile, v_col = t.kvh * kHeadDim;
-        const int k_row = last ? next.row0 + key_tile(next, 0) * kPreTile : t.row0 + key_tile(t, i + 1) * kPreTile, k_col = last ? next.kvh * kHeadDim : v_col;
+        const int v_col = t.kvh * kHeadDim, k_col = last ? next.kvh * kHeadDim : v_col;
+        if (WIN) {
+          auto load = [&](const CUtensorMap& whole, const CUtensorMap& part, const PrefillTile& from, int tile, int col, int at) {
+            const bool run = run_of_keys(from, tile);
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint8_t* to = smem + (2 + 2 * st) * kPreTileBytes + h * (kPreTileBytes / 2);
-          if (has_v) tma_load_2d(&p.map_v, &bar.kv_full[st], to, v_col + h * 64, v_row);
-          if (has_k) tma_load_2d(&p.map_k, &bar.kv_full[st], to + kPreTileBytes, k_col + h * 64, k_row);
+            for (int j = 0; j < (run ? 2 : 8); ++j) {  // halves of 64 dimensions, or their chunks of 32 keys
+              const int h = run ? j : j >> 2, c = run ? 0 : j & 3;
+              tma_load_2d(run ? &whole : &part, &bar.kv_full[st], smem + at + h * (kPreTileBytes / 2) + c * (32 * 128), col + h * 64,
+                          from.row0 + key_of(from, tile, c));
+            }
+          };
+          const int at = (2 + 2 * st) * kPreTileBytes;
+          if (has_v) load(p.map_v, p.map_v32, t, i, v_col, at);
+          if (has_k) load(p.map_k, p.map_k32, last ? next : t, last ? 0 : i + 1, k_col, at + kPreTileBytes);
+        } else {
+          const int v_row = t.row0 + i * kPreTile, k_row = last ? next.row0 : v_row + kPreTile;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint8_t* to = smem + (2 + 2 * st) * kPreTileBytes + h * (kPreTileBytes / 2);
+            if (has_v) tma_load_2d(&p.map_v, &bar.kv_full[st], to, v_col + h * 64, v_row);
+            if (has_k) tma_load_2d(&p.map_k, &bar.kv_full[st], to + kPreTileBytes, k_col + h * 64, k_row);
+          }
         }
         if (!last) continue;
         if (!more) break;
@@ -552,48 +589,52 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int n = max(t.n0, t.n1), mask0 = first_masked(t);
       const int plain = min(min(t.n0, t.n1) - 1, mask0);  // steps without a mask that both query tiles go on behind
       int i = 0;
+      for (;;) {
+        // steps that wait for no cleaned V (with a window bf16 gains 1.5 % by this loop, E4M3 loses 4 %)
 #pragma unroll 1
-      for (; !WIN && i < plain; ++i) {
-        const int st = (uses - 1) & 1;
-        p_wait(0);
-        pv(0, st, i == 0, false);
-        qk(0, st, i + 2 == t.n0);
-        p_wait(1);
-        pv(1, st, i == 0, false);
-        stage_wait();
-        qk(1, st, i + 2 == t.n1);
-        if (one) mma_commit(&bar.kv_empty[st]);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-      }
+        for (; WIN ? !FP8 && i < min(t.n0, t.n1) - 1 && plain_tile(t, i) : i < plain; ++i) {
+          const int st = (uses - 1) & 1;
+          p_wait(0);
+          pv(0, st, i == 0, false);
+          qk(0, st, i + 2 == t.n0);
+          p_wait(1);
+          pv(1, st, i == 0, false);
+          stage_wait();
+          qk(1, st, i + 2 == t.n1);
+          if (one) mma_commit(&bar.kv_empty[st]);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+        }
 #pragma unroll 1
-      for (; i < n && ok; ++i) {
-        const bool last = i == n - 1;
-        if (last) {
-          more = __all_sync(~0u, get_tile(k + 1, u));
-          if (more && one) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
-        }
-        const bool next = !last || more;  // another key tile, of this unit of work or the next
-        const int st = (uses - 1) & 1;
-        if (WIN ? !plain_tile(t, i) : i >= mask0) {
-          wait(&bar.v_ok[st], (v_phase >> st) & 1, W_PRE_V);
-          v_phase ^= 1u << st;
-        }
+        for (const int end = WIN && !FP8 ? min(i + 1, n) : n; i < end && ok; ++i) {
+          const bool last = i == n - 1;
+          if (last) {
+            more = __all_sync(~0u, get_tile(k + 1, u));
+            if (more && one) mbar_arrive(&bar.tile_empty[(k + 1) % kPreRing]);
+          }
+          const bool next = !last || more;  // another key tile, of this unit of work or the next
+          const int st = (uses - 1) & 1;
+          if (WIN ? !plain_tile(t, i) : i >= mask0) {
+            wait(&bar.v_ok[st], (v_phase >> st) & 1, W_PRE_V);
+            v_phase ^= 1u << st;
+          }
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int ns = s ? t.n1 : t.n0, un = s ? u.n1 : u.n0;
-          if (i < ns) {
-            p_wait(s);
-            pv(s, st, i == 0, i == ns - 1);
+          for (int s = 0; s < 2; ++s) {
+            const int ns = s ? t.n1 : t.n0, un = s ? u.n1 : u.n0;
+            if (i < ns) {
+              p_wait(s);
+              pv(s, st, i == 0, i == ns - 1);
+            }
+            if (s == 1 && next) stage_wait();
+            if (last ? more && un > 0 : i + 1 < ns) {
+              if (last) q_wait(s);
+              qk(s, st, last ? un == 1 : i + 1 == ns - 1);
+            }
           }
-          if (s == 1 && next) stage_wait();
-          if (last ? more && un > 0 : i + 1 < ns) {
-            if (last) q_wait(s);
-            qk(s, st, last ? un == 1 : i + 1 == ns - 1);
-          }
+          if (one) mma_commit(&bar.kv_empty[st]);
+          ok = __all_sync(~0u, ok);
         }
-        if (one) mma_commit(&bar.kv_empty[st]);
-        ok = __all_sync(~0u, ok);
+        if (i >= n || !ok) break;
       }
       t = u;
     }
@@ -645,7 +686,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             const uint4 w = ld_shared_v4(base + c * 512);
             bad_chunk = false;
             st_shared_v4(base + c * 512, clean(w.x), clean(w.y), clean(w.z), clean(w.w));
-            const int pos = key_tile(t, i) * kPreTile + (c & 31) * 4 + (lane >> 3);  // half a key's values are 128 bytes
+            const int pos = key_of(t, i, (c & 31) >> 3) + (c & 7) * 4 + (lane >> 3);  // half a key's values are 128 bytes
             if (bad_chunk && pos < t.len) lo = min(lo, pos), hi = max(hi, pos);
           }
           lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
@@ -671,27 +712,33 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     const uint32_t hp_inverse = 65536u / p.hp + 1;  // row / hp = row * hp_inverse >> 16 for rows below 128
     const int row_tok = row / p.hp;
     const float c = p.scale_log2;
+    // E4M3: of key tile i + lane, WIN: of chunk lane % 4 of key tile i + lane / 4; and how many tiles that is.
+    constexpr int kPowers = WIN ? 8 : 32;
     auto load_powers = [&](const PrefillTile& t, int n, int i) {
-      const long long tile = key_tile(t, i + lane);
-      return i + lane < n && (!WIN || tile * kPreTile < t.len) ? p.powers[(t.row0 + tile * kPreTile) * p.n_kv + t.kvh] : 0.f;
+      if (WIN) {
+        const int tile = i + (lane >> 2), key = key_of(t, tile, lane & 3) & ~(kPreTile - 1);
+        return tile < n && key < t.len ? p.powers[(t.row0 + static_cast<long long>(key)) * p.n_kv + t.kvh] : 0.f;
+      }
+      const long long tile = i + lane;
+      return tile < n ? p.powers[(t.row0 + tile * kPreTile) * p.n_kv + t.kvh] : 0.f;
     };
     // E4M3: the single keys of a tile, in fp32 from their codes and scales: into l and O, and out of S.  O is complete: S
     // of this tile was committed behind the products before.
-    auto single_keys = [&](const PrefillTile& t, int i, bool first_too, int lim, int low, float& m, float& mx, float& l, bool& begun) {
-      const long long key0 = t.row0 + static_cast<long long>(i) * kPreTile;
-      const int keys = min(kPreTile, t.len - i * kPreTile);
+    auto single_keys = [&](const PrefillTile& t, int i, float powers, int lim, int low, float& m, float& mx, float& l, bool& begun) {
       uint32_t which[4], scales[4];  // of key 32 h + lane
       float mark[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {  // all loads on their way together
-        const long long at = key0 + min(h * 32 + lane, keys - 1);
+        const long long at = t.row0 + static_cast<long long>(min(key_of(t, i, h) + lane, t.len - 1));
         mark[h] = p.powers[at * p.n_kv + t.kvh];
         scales[h] = __float_as_uint(p.v_scale[at * p.ld_scale + t.kvh]);
       }
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const int j = h * 32 + lane;
-        which[h] = __ballot_sync(~0u, j == 0 ? first_too : j < keys && mark[h] != 0.f);
+        const int key = key_of(t, i, h) + lane;
+        const int marks = __float2int_rn(__shfl_sync(~0u, powers, WIN ? (i % kPowers) * 4 + h : i & 31) / kPreMark);
+        const bool first = key % kPreTile == 0, single = first ? (marks & PRE_SINGLE_FIRST) != 0 : marks != 0 && mark[h] != 0.f;
+        which[h] = __ballot_sync(~0u, key < t.len && single);
       }
       tmem_st_wait();  // O may have been begun just now
       float zero_top = -INFINITY;  // of the logits of keys whose values are zero: O learns of them once, behind the last key
@@ -699,6 +746,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       for (int j = 0; j <= kPreTile; ++j) {
         const bool end = j == kPreTile;
         uint32_t bits = 0;
+        int from = key_of(t, i, 0);
         float x = zero_top;
         bool sees = false;
         if (end) {
@@ -712,7 +760,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           bits = __shfl_sync(~0u, h < 2 ? (h == 0 ? scales[0] : scales[1]) : (h == 2 ? scales[2] : scales[3]), j & 31);
           const float logit = tmem_ld1(s_tmem + j) * c;
           tmem_st1(s_tmem + j, -INFINITY);
-          sees = i * kPreTile + j <= lim && (!WIN || i * kPreTile + j >= low || i * kPreTile + j < p.sinks);
+          const int key = key_of(t, i, h) + (j & 31);
+          sees = key <= lim && (!WIN || key >= low || key < p.sinks);
+          from = key;
           x = sees ? logit : -INFINITY;
           const float up_l = fmaxf(mx, x);
           l = l * ex2(mx - up_l) + ex2(x - up_l);
@@ -722,8 +772,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             continue;
           }
         }
-        const uint8_t* from = p.codes + (key0 + (end ? 0 : j)) * p.ld_codes + t.kvh * kHeadDim;
-        uint4 codes = *reinterpret_cast<const uint4*>(from);
+        const uint8_t* codes_at = p.codes + (t.row0 + static_cast<long long>(from)) * p.ld_codes + t.kvh * kHeadDim;
+        uint4 codes = *reinterpret_cast<const uint4*>(codes_at);
         const int power = max((static_cast<int>(bits >> 23) & 255) - (127 + kPreRoom), -120);
         // m rises by 2^kPrePowerMax at most, for l's sake: fp32 has room for weights of 2^98 (and for 2^(m - mx) from
         // 2^-125 on)
@@ -736,7 +786,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           uint32_t o[16];
           tmem_ld16(o_tmem + d, o);
           const uint32_t four[4] = {codes.x, codes.y, codes.z, codes.w};
-          if (d + 16 < kHeadDim) codes = *reinterpret_cast<const uint4*>(from + d + 16);
+          if (d + 16 < kHeadDim) codes = *reinterpret_cast<const uint4*>(codes_at + d + 16);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -764,8 +814,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int tok = first + row_tok;
       const int lim = p.causal ? min(tok, t.len - 1) : t.len - 1;  // last key this row sees
       const int lim_lo = __reduce_min_sync(~0u, lim);              // last key that every row of this warp sees
-      const int low = WIN && p.window > 0 ? tok - p.window + 1 : INT_MIN;     // first key of this row's window
-      const int low_hi = WIN ? __reduce_max_sync(~0u, low) : INT_MIN;         // from here on every row sees (up to lim_lo)
+      const int low = WIN && p.window > 0 ? tok - p.window + 1 : 0;  // first key of this row's window
+      const int low_hi = WIN ? __reduce_max_sync(~0u, low) : 0;     // from here on every row sees (up to lim_lo)
       float m = kPreNone, l = 0.f;
       float mx = kPreNone;         // E4M3: the maximum that l is held at (m is that of O)
       float powers = powers_next;  // E4M3: of key tile i in lane i % 32
@@ -778,38 +828,63 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       bool begun = false;  // E4M3: single keys are in O (it may be before the first product)
       for (;;) {
         for (; i < n; ++i) {
-          if (FP8 && i > 0 && (i & 31) == 0) powers = load_powers(t, n, i);
-          float b = FP8 ? __shfl_sync(~0u, powers, i & 31) : 0.f;
-          if (FP8 && b > kPreMark / 2) {
+          if (FP8 && i > 0 && i % kPowers == 0) powers = load_powers(t, n, i);
+          float b = FP8 && !WIN ? __shfl_sync(~0u, powers, i & 31) : 0.f;
+          float b4[4] = {b, b, b, b};  // WIN: of each chunk
+          if (FP8 && WIN) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) b4[h] = __shfl_sync(~0u, powers, (i % kPowers) * 4 + h);
+            if (fmaxf(fmaxf(b4[0], b4[1]), fmaxf(b4[2], b4[3])) > kPreMark / 2) {
+              if (i != single_done) break;
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                if (b4[h] > kPreMark / 2) b4[h] -= rintf(b4[h] / kPreMark) * kPreMark;
+            }
+          }
+          if (FP8 && !WIN && b > kPreMark / 2) {
             if (i != single_done) break;  // its single keys come first, behind this loop: in it they cost 3 % of the time
             b -= rintf(b / kPreMark) * kPreMark;
           }
           if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;
           ++s_uses;
           tc_fence_after();
+          if (WIN) {
+            // Where a row does not see all of a chunk, S gets its -inf in tensor memory: few chunks do.  (Masks of the registers
+            // below cost more, taken or not: 118-180 us for 107, by how their branches are written.)
+            const int first_key = key_of(t, i, 0), last_key = key_of(t, i, 3) + 31;
+            if (last_key > lim_lo || (first_key < low_hi && last_key >= p.sinks)) {
+#pragma unroll 1
+              for (int h = 0; h < 4; ++h) {
+                const int key0 = key_of(t, i, h);
+                if (key0 + 31 <= lim_lo && (key0 >= low_hi || key0 + 31 < p.sinks)) continue;
+                const uint32_t seen = bits_below(lim + 1 - key0) & (~bits_below(low - key0) | bits_below(p.sinks - key0));
+                uint32_t y[2][16];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) tmem_ld16(s_tmem + h * 32 + q * 16, y[q]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    if ((seen & (1u << (q * 16 + j))) == 0) y[q][j] = __float_as_uint(-INFINITY);
+                  tmem_st16(s_tmem + h * 32 + q * 16, y[q]);
+                }
+              }
+              tmem_st_wait();
+            }
+          }
           uint32_t x[4][32];
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmem_ld32(s_tmem + j * 32, x[j]);
           tmem_ld_wait();
-          const int key0 = key_tile(t, i) * kPreTile;
-          if (key0 + kPreTile - 1 > lim_lo) {
-            const int cols = lim - key0, all = lim_lo - key0;  // columns up to these count
+          if (!WIN && i * kPreTile + kPreTile - 1 > lim_lo) {
+            const int cols = lim - i * kPreTile, all = lim_lo - i * kPreTile;  // columns up to these count
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               if (h * 32 + 31 > all) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                   if (h * 32 + j > cols) x[h][j] = __float_as_uint(-INFINITY);
-              }
-          }
-          if (WIN && key0 < low_hi && key0 + kPreTile > p.sinks) {
-            const int from = low - key0, all = low_hi - key0, sinks = p.sinks - key0;  // columns below `sinks` and from `from` on count
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-              if (h * 32 < all && h * 32 + 31 >= sinks) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (h * 32 + j < from && h * 32 + j >= sinks) x[h][j] = __float_as_uint(-INFINITY);
               }
           }
           float t4[4];
@@ -822,7 +897,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               t4[h] = max3(t4[h], __uint_as_float(x[h][j]), __uint_as_float(x[h][j + 1]));
 #pragma unroll
           for (int h = 0; h < 4; ++h) t4[h] = fmaxf(t4[h], __uint_as_float(x[h][31]));
-          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c, lifted = FP8 ? top + b : top;
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c;
+          float lifted = FP8 ? top + b : top;
+          if (FP8 && WIN)
+            lifted = fmaxf(fmaxf(fmaf(t4[0], c, b4[0]), fmaf(t4[1], c, b4[1])), fmaxf(fmaf(t4[2], c, b4[2]), fmaf(t4[3], c, b4[3])));
           const bool rise = lifted > m + kPreLazy, rise_l = FP8 && top > mx + kPreLazy;
           if (__any_sync(~0u, rise || rise_l)) {
             const float up = rise ? lifted : m;
@@ -847,29 +925,42 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               }
             }
           }
-          const float at = FP8 && b == kPreZero ? mx : m - b;  // E4M3: what the tile's weights are held at, 2^7 above
+          // E4M3: what the tile's (WIN: a chunk's) weights are held at, 2^7 above
+          auto held_at = [&](float power) { return FP8 && power == kPreZero ? mx : m - power; };
+          const float at = held_at(b);
           const float minus = FP8 ? kPreLift - at : -m;
           const uint64_t c2 = f2(c, c), m2 = f2(minus, minus);
           uint64_t l0 = 0, l1 = 0;
+          float chunks = 0.f;  // E4M3, WIN: their sums
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t w[16];
+            const float at4 = held_at(b4[j]);
+            const uint64_t m4 = FP8 && WIN ? f2(kPreLift - at4, kPreLift - at4) : m2;
+            if (FP8 && WIN) l0 = l1 = 0;
 #pragma unroll
             for (int h = 0; h < 16; h += 2) {
               float w0, w1, w2, w3;
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), c2, m2), w0, w1);
-              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m2), w2, w3);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2]), __uint_as_float(x[j][h * 2 + 1])), c2, m4), w0, w1);
+              f2_split(f2_fma(f2(__uint_as_float(x[j][h * 2 + 2]), __uint_as_float(x[j][h * 2 + 3])), c2, m4), w2, w3);
               w0 = ex2(w0), w1 = ex2(w1), w2 = ex2(w2), w3 = ex2(w3);
               l0 = f2_add(l0, f2(w0, w1)), l1 = f2_add(l1, f2(w2, w3));
               w[h] = FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
               w[h + 1] = FP8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3);
             }
             tmem_st16(s_tmem + j * 16, w);
+            if (FP8 && WIN) {
+              float s0, s1, s2, s3;
+              f2_split(l0, s0, s1);
+              f2_split(l1, s2, s3);
+              chunks += ((s0 + s1) + (s2 + s3)) * ex2((at4 - kPreLift) - mx);
+            }
           }
           float s0, s1, s2, s3;
           f2_split(l0, s0, s1);
           f2_split(l1, s2, s3);
-          l += FP8 ? ((s0 + s1) + (s2 + s3)) * ex2((at - kPreLift) - mx) : (s0 + s1) + (s2 + s3);
+          if (FP8 && WIN) l += chunks;
+          else l += FP8 ? ((s0 + s1) + (s2 + s3)) * ex2((at - kPreLift) - mx) : (s0 + s1) + (s2 + s3);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -878,9 +969,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!FP8 || !ok || i >= n) break;
         if (!(ok = warp_wait(&bar.s_full[s], s_uses & 1, wc, W_PRE_S))) break;  // the loop waits for the same phase again
         tc_fence_after();
-        const int marks = __float2int_rn(__shfl_sync(~0u, powers, i & 31) / kPreMark);
         begun |= i > 0;
-        single_keys(t, key_tile(t, i), (marks & PRE_SINGLE_FIRST) != 0, lim, low, m, mx, l, begun);
+        single_keys(t, i, powers, lim, low, m, mx, l, begun);
         single_done = i;
       }
       if (!ok) break;
@@ -890,10 +980,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         if (!(ok = warp_wait(&bar.o_full[s], o_uses & 1, wc, W_PRE_O))) break;
         ++o_uses;
         tc_fence_after();
-        float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;  // E4M3: O is held at m - 7, l at mx
-        if (WIN && l == 0.f) inv = 0.f;  // a row that sees nothing
         const volatile PrefillTile& said = bar.tile[k % kPreRing];
         const int bad_lo = said.bad_lo, bad_hi = said.bad_hi;
+        float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;  // E4M3: O is held at m - 7, l at mx
+        if (WIN && l == 0.f) inv = 0.f;  // a row that sees nothing
         // A thread has a row; lines of global memory want a few rows each, all of 128 bytes.  So 16-byte pieces go
         // through shared memory, piece j of row r at place j ^ (r's low bits).  (Stored straight from the row's
         // thread, each instruction touched 32 lines: 4000 cycles a tile.)
