@@ -76,8 +76,10 @@ struct DecodeSeg {
 };
 
 // How segments follow one another, and which of their tokens count.
-template <int UNIT, bool WIN>
+// OVER: units that the beginning of a (sequence, head) counts as in the split, 0 or 1; they hold no tokens and stand in front.
+template <int UNIT, bool WIN, int OVER = 0>
 struct DecodeWalk {
+  static constexpr int kOver = OVER;
   const DecodeParams& p;
   const int heads_v;         // independent (kv head, chunk) pairs of a sequence
   const long long capacity;  // tokens that the table has room for
@@ -99,15 +101,15 @@ struct DecodeWalk {
   __device__ __forceinline__ int units_of(int len) const {
     bool bad;
     int at, jump;
-    return span(len, bad, at, jump);
+    return span(len, bad, at, jump) + OVER;
   }
   __device__ __forceinline__ void begin(DecodeSeg& s, int tile, long long units_left) const {
     if (tile == 0 && s.h == 0) s.len = p.c.lens[s.b];
-    s.n_units = span(s.len, s.bad, s.jump_at, s.jump);
+    s.n_units = span(s.len, s.bad, s.jump_at, s.jump) + OVER;
     s.units = static_cast<int>(min(static_cast<long long>(s.n_units - tile), units_left));
     const int end = s.bad ? 0 : s.len - s.jump;
-    s.t0 = tile * UNIT;
-    s.t1 = static_cast<int>(min(static_cast<long long>(end), (static_cast<long long>(tile) + s.units) * UNIT));
+    s.t0 = max(tile - OVER, 0) * UNIT;
+    s.t1 = static_cast<int>(min(static_cast<long long>(end), (static_cast<long long>(tile) + s.units - OVER) * UNIT));
   }
   __device__ __forceinline__ void next(DecodeSeg& s, long long units_left) const {
     ++s.h;
@@ -239,7 +241,7 @@ __device__ __forceinline__ bool decode_plan(const DecodeParams& p, const Walk& w
   seg.kvh = seg.h / p.chunks;
   seg.chunk = seg.h - seg.kvh * p.chunks;
   walk.begin(seg, tile, own.u1 - own.u0);
-  return true;
+  return tile >= Walk::kOver || own.u1 - own.u0 > Walk::kOver;  // more than a beginning
 }
 
 // The CTAs that share a (sequence, head).
@@ -248,13 +250,15 @@ struct DecodeOwners {
   int first, last;
   float* part;  // where this CTA's piece goes if not whole
 };
+template <int OVER = 0>
 __device__ __forceinline__ DecodeOwners decode_owners(const DecodeParams& p, const DecodeShare& own, const DecodeSeg& seg) {
   const int cta = blockIdx.x;
+  const long long first = own.seg_first + OVER;  // unit with tokens
   DecodeOwners w;
-  w.whole = own.seg_first >= own.u0 && own.seg_first + seg.n_units <= own.u1;
+  w.whole = first >= own.u0 && own.seg_first + seg.n_units <= own.u1;
   w.first = w.last = cta;
   if (!w.whole) {
-    if (own.seg_first < own.u0) w.first = own.cta_of(own.seg_first);
+    if (first < own.u0) w.first = own.cta_of(first);
     if (own.seg_first + seg.n_units > own.u1) w.last = own.cta_of(own.seg_first + seg.n_units - 1);
   }
   w.part = p.parts + (static_cast<long long>(cta) * 2 + (cta == w.first ? 1 : 0)) * kDecPartFloats;
@@ -312,11 +316,13 @@ template <int WARPS, class Sync>
 __device__ __forceinline__ void decode_join(const DecodeParams& p, const DecodeCuts& cuts, long long* plan, Sync&& sync) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   sync();
-  if (tid < 2) {
-    __threadfence();  // for the whole CTA: the others' stores are behind the barrier
+  if (tid < 2) {  // release: for the whole CTA, the others' stores are behind the barrier; acquire: those of the others that came
     plan[tid] = 0;
     const int first = tid == 0 ? cuts.first[0] : cuts.first[1], last = tid == 0 ? cuts.last[0] : cuts.last[1];
-    if (first >= 0 && atomicAdd(p.counters + first, 1u) == static_cast<unsigned>(last - first)) {
+    unsigned came = 0;
+    if (first >= 0)
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(came) : "l"(p.counters + first) : "memory");
+    if (first >= 0 && came == static_cast<unsigned>(last - first)) {
       p.counters[first] = 0;
       plan[tid] = 1;
     }
@@ -325,7 +331,6 @@ __device__ __forceinline__ void decode_join(const DecodeParams& p, const DecodeC
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (plan[k] == 0) continue;
-    __threadfence();
     const int c_first = cuts.first[k], c_last = cuts.last[k];
     const int kvh = cuts.h[k] / p.chunks, chunk = cuts.h[k] - kvh * p.chunks;
     const int head0 = kvh * p.group + chunk * p.chunk_heads;

@@ -4,7 +4,8 @@
 //
 // What bounds it: the cache is read once, 144 bytes for a token and kv head, at the memory's rate if the instructions for
 // these 256 codes are few enough: a logic instruction takes two cycles of a scheduler, and an SM has some 25 cycles of each
-// of its four for a token and head.
+// of its four for a token and head.  64 sequences of 2048-8192 tokens, 32/8 heads: 80 us, 4500 GB/s; some 345 instructions for
+// 16 tokens and a head, 0.55 of them in a cycle of a scheduler.
 //
 // Codes.  A code xor 8, u = code + 8, is an fp16 number u 2^-24 (a denormal one) as it stands in the low bits of a half, and
 // 16 u 2^-24 four bits further up: one logic instruction gives two, and the factor 16 lies in the query's fragments for K, in
@@ -26,11 +27,21 @@
 // warp walks ahead and fills the stages by tensor copies, one for each 32, 16 or 8 tokens of a page and tensor (the codes with
 // the 64-byte swizzle, so that eight rows of a chunk meet in no bank), and bulk copies for the scales; caches that these
 // do not fit are copied by 16 bytes.  With a ring of its own for each warp, filled by itself, finding the pages and issuing the
-// copies took 112 of 400 instructions for 16 tokens and a head: 105.7 us for 64 sequences of 2048-8192 tokens (32/8 heads).
+// copies took 112 of 400 instructions for 16 tokens and a head: 105.7 us for these 64 sequences, 91 with the fifth warp.  In the
+// split the beginning of a (sequence, head) counts as a unit: its queries and the join of its pieces take as long (24 sequences
+// with a window of 1024: 16.4 us without).
 #pragma once
 #include "decode_attention_common.cuh"
 
 namespace fl {
+
+// What the warps that compute only look at between segments; in registers it cost spills (90 us for 80).
+struct DecodeKept {
+  DecodeShare own;
+  DecodeSeg seg;
+  long long left;  // units
+  DecodeCuts cuts;
+};
 
 struct DecodeInt4Traits {
   static constexpr int kWarps = 4;  // that compute
@@ -45,10 +56,13 @@ struct DecodeInt4Traits {
   // twice, [group or power][g][tokens g + 8 r].  Its piece of a segment's result comes to the same place.
   static constexpr int kParts = kInt4Groups * kStep * 2, kPairs = kStep * 8, kTables = kParts + (kInt4Groups + 1) * kPairs;
   static constexpr int kPiece = 8 * kHeadDim * 4, kOwn = kPiece > kTables ? kPiece : kTables;
-  // The segment's queries, for all warps: fragments of each group, [group][lane], and -8 sum q, [group][head].
-  static constexpr int kQuery = kInt4Groups * (32 * 16 + 8 * 4);
+  // The segment's queries, for all warps: fragments of each group, [group][lane], -8 sum q, [group][head], and the
+  // logits' factor in two parts, [q][part][head 2 q, 2 q + 1].
+  static constexpr int kQuery = kInt4Groups * (32 * 16 + 8 * 4) + 4 * 16;
+  static constexpr int kOver = 1;  // units that the beginning of a (sequence, head) counts as
   static constexpr int kCtas = 3, kStages = 3;
-  static constexpr int kSmem = 512 /*alignment*/ + kStages * kStage + kWarps * (kOwn + 8 * 16) + kQuery + 128 + 2 * kStages * 8 + 64;
+  static constexpr int kSmem = 512 /*alignment*/ + kStages * kStage + kWarps * (kOwn + 8 * 16) + kQuery + 128 + 2 * kStages * 8 + 16 +
+                               sizeof(DecodeKept);
 };
 
 template <bool TRANS>
@@ -143,8 +157,10 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
   uint64_t* const empty = full + T::kStages;
   int* const stage_bad = reinterpret_cast<int*>(empty + T::kStages);  // the unit in the stage meets a bad table entry
   int* const abort_flag = stage_bad + T::kStages;
+  DecodeKept* const kept = reinterpret_cast<DecodeKept*>(plan + 16 + 2 * T::kStages + 2);
+  static_assert((T::kStages + 1) * 4 <= 16, "two words");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const DecodeWalk<T::kUnit, WIN> walk(p);
+  const DecodeWalk<T::kUnit, WIN, T::kOver> walk(p);
   decode_hints(p, tid);
   if (tid == 0) {
     for (int i = 0; i < T::kStages; ++i) mbar_init(&full[i], p.box > 0 ? 1 : 33), mbar_init(&empty[i], T::kWarps);
@@ -155,10 +171,14 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
   __syncthreads();
   griddep_wait();  // launched as a dependent: nothing is read before the kernel in front has finished
   griddep_launch_dependents();
-  DecodeShare own;
   DecodeSeg seg;
-  if (!decode_plan<T::kThreads>(p, walk, plan, own, seg)) return;
-  long long left = own.u1 - own.u0;
+  long long left;
+  {
+    DecodeShare own;
+    if (!decode_plan<T::kThreads>(p, walk, plan, own, seg)) return;
+    left = own.u1 - own.u0;
+    if (tid == 0) kept->own = own, kept->seg = seg, kept->left = left, kept->cuts = DecodeCuts();
+  }
 
   if (warp == T::kWarps) {
     // ================================================================ the ring is filled
@@ -167,7 +187,7 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
     auto advance = [&]() -> bool {  // on to the next unit that has tokens
       while (pt >= seg.t1) {
         left -= seg.units;
-        if (left <= 0) return false;
+        if (left <= T::kOver) return false;
         walk.next(seg, left);
         pt = seg.t0;
         const char* row = reinterpret_cast<const char*>(p.Q + seg.b * p.ldq + static_cast<long long>(seg.kvh) * p.group * kHeadDim);
@@ -275,17 +295,17 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
   const uint32_t ld_at = (lane >> 1) * 128 + (((lane & 1) << 2 ^ (lane >> 1 & 3)) << 4);
   const uint32_t flip = p.eights, flip16 = flip << 4;
   auto sync = [] { named_bar_sync(1, 32 * T::kWarps); };
-  DecodeCuts cuts;
   int stage = 0;
   uint32_t parity = 0;
-  bool failed = false;  // a wait ran out
+  constexpr uint32_t kSpread = 16, kBad = 32, kFailed = 64;
+  uint32_t said = 0;  // kFailed: a wait ran out
 
   for (;;) {
     // ---- this segment's query fragments (B operand: head g of the column tile, dimensions in the codes' order)
-    const int head0 = seg.kvh * p.group + seg.chunk * p.chunk_heads;
-    const int n_heads = min(p.chunk_heads, p.group - seg.chunk * p.chunk_heads);
-    uint64_t fac, fac_code;  // the logits' factor of heads 2q, 2q + 1, in two parts
+    auto first_head = [&] { return seg.kvh * p.group + seg.chunk * p.chunk_heads; };
+    auto heads_here = [&] { return min(p.chunk_heads, p.group - seg.chunk * p.chunk_heads); };
     {
+      const int head0 = first_head(), n_heads = heads_here();
       uint4 own_group = make_uint4(0, 0, 0, 0);
       float a = 0.f;
 #pragma unroll
@@ -322,35 +342,33 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
       if (warp < kInt4Groups && q == 0) reinterpret_cast<float*>(query + kInt4Groups * 512)[warp * 8 + g] = sum * (-8.f / kDecCode);
       // f times 2^24, as two factors the first of which neither overflows nor, where it matters, underflows
       const float f0 = f > 1.f ? kDecCode : f, f1 = f > 1.f ? f : kDecCode;
-      fac = f2(__shfl_sync(~0u, f0, q * 8), __shfl_sync(~0u, f0, q * 8 + 4));
-      fac_code = f2(__shfl_sync(~0u, f1, q * 8), __shfl_sync(~0u, f1, q * 8 + 4));
+      // [q]: of heads 2q and 2q + 1 the first, then the second
+      if (warp == 0 && q < 2) reinterpret_cast<float*>(query + kInt4Groups * (512 + 32))[(g >> 1) * 4 + q * 2 + (g & 1)] = q == 0 ? f0 : f1;
       sync();
     }
-    bool bad = seg.bad;
-    bool spread = false;     // the scales of some token of this segment lie far apart
-    uint32_t no_number = 0;  // groups of columns in which this lane met a scale of V that is not finite
+    // Of this segment: the table or the length is bad; the scales of some token lie far apart (kSpread); in bits 0-3 the groups of
+    // columns in which this lane met a scale of V that is not finite.
+    said = (said & kFailed) | (seg.bad ? kBad : 0u);
     float o[8][4];
     uint64_t eights[kInt4Groups];  // 8 sum w of a group, heads 2q and 2q + 1, in the units of o
     float m[2], mv[2];
     uint64_t l;
-    {
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
+    for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+      for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < kInt4Groups; ++c) eights[c] = 0;
-      m[0] = m[1] = mv[0] = mv[1] = kDecNone;
-      l = 0;
-    }
+    for (int c = 0; c < kInt4Groups; ++c) eights[c] = 0;
+    m[0] = m[1] = mv[0] = mv[1] = kDecNone;
+    l = 0;
 
     for (int unit = seg.t0; unit < seg.t1; unit += T::kUnit) {
-      if (!failed && !decode_wait(&full[stage], parity, abort_flag, p.timeout_ns)) {
-        failed = true;
+      if ((said & kFailed) == 0 && !decode_wait(&full[stage], parity, abort_flag, p.timeout_ns)) {
+        said |= kFailed;
         record_failure(p.status, W_DEC_FULL, stage);
       }
       __syncwarp();
-      bad |= stage_bad[stage] != 0;
+      if (stage_bad[stage] != 0) said |= kBad;
       const int t = unit + warp * T::kStep;
       if (t < seg.t1) {
         const uint32_t kb = smem_u32(smem) + stage * T::kStage + warp * (T::kStep * T::kRowBytes), vb = kb + T::kTile;
@@ -378,10 +396,10 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           uint32_t four[4] = {sv.x & 0xFFFFu, sv.x >> 16, sv.y & 0xFFFFu, sv.y >> 16};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (four[c] >= 0x7F80u) four[c] = 0, no_number |= 1u << c;  // reaches its own columns only, at the segment's end
+            if (four[c] >= 0x7F80u) four[c] = 0, said |= 1u << c;  // reaches its own columns only, at the segment's end
           sv = make_uint2(four[0] | four[1] << 16, four[2] | four[3] << 16);
           ends();
-          spread |= __any_sync(~0u, far());
+          if (__any_sync(~0u, far())) said |= kSpread;
         }
         const float power = __uint_as_float(0x4B000000u + (top >> 7)) - (8388608.f + 126.f);
         uint8_t* const pairs = parts + T::kParts;
@@ -393,7 +411,7 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           for (int c = 0; c < kInt4Groups; ++c) *reinterpret_cast<float2*>(to + c * T::kPairs) = make_float2(k[c], k[c]);
           *reinterpret_cast<float2*>(to + kInt4Groups * T::kPairs) = make_float2(power, power);
         }
-        if (!spread) {
+        if ((said & kSpread) == 0) {
           const uint32_t base = (max(top >> 7, 14u) - 14u) * 0x00800080u;
           const uint32_t p01 = (u16x2_max(sv.x, base) - base) << 3, p23 = (u16x2_max(sv.y, base) - base) << 3;
           const bool second = (lane & 1) != 0;  // of a pair of tokens: writes groups 2 and 3, the first one 0 and 1
@@ -431,8 +449,9 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
             }
           }
         }
+        const ulonglong2 fac = *reinterpret_cast<const ulonglong2*>(query + kInt4Groups * (512 + 32) + q * 16);
 #pragma unroll
-        for (int r = 0; r < T::kSubs * 2; ++r) f2_split(f2_mul(f2_mul(sum[r], fac), fac_code), x[r * 2], x[r * 2 + 1]);
+        for (int r = 0; r < T::kSubs * 2; ++r) f2_split(f2_mul(f2_mul(sum[r], fac.x), fac.y), x[r * 2], x[r * 2 + 1]);
         // ---- softmax
         if (cut) {
 #pragma unroll
@@ -489,7 +508,7 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           f2_split(f2_add(f2(y[r * 2], y[r * 2 + 1]), minus_mv), e0, e1);
           y[r * 2] = ex2(e0), y[r * 2 + 1] = ex2(e1);
         }
-        if (!spread) {
+        if ((said & kSpread) == 0) {
           uint32_t pf[T::kSubs][2];  // P^T (B operand: tokens 2q, 2q + 1 | + 8 of head g)
 #pragma unroll
           for (int r = 0; r < T::kSubs * 2; ++r) pf[r >> 1][r & 1] = transpose8x8(pack_f16x2(y[r * 2], y[r * 2 + 1]));
@@ -549,11 +568,13 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
     }
 
     // ---- the CTA's four pieces become one: finished here, or a part of a cut (sequence, head)
-    const DecodeOwners owners = decode_owners(p, own, seg);
-    const bool spoiled = __any_sync(~0u, bad || failed);
+    DecodeShare own = kept->own;
+    seg = kept->seg, left = kept->left;
+    const DecodeOwners owners = decode_owners<T::kOver>(p, own, seg);
+    const bool spoiled = __any_sync(~0u, (said & (kBad | kFailed)) != 0);
     if (spoiled && lane == 0 && atomicCAS(p.status + ST_CODE, 0, static_cast<int>(FL_ERR_INVALID_ARG)) == 0)
       p.status[ST_DETAIL] = seg.b;
-    no_number = __reduce_or_sync(~0u, no_number);
+    const uint32_t no_number = __reduce_or_sync(~0u, said);  // bits 0-3
     // o[t][i] with t = 2 group + odd: head 2q + (i & 1), dimension 32 group + 4 g + odd + 2 (i >> 1), still with 8 sum w in
     // it, odd dimensions times 16.  Chunks of 4 dimensions, permuted by 2 q against bank conflicts.
     {
@@ -581,15 +602,17 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
       }
     }
     sync();
-    decode_merge<T::kWarps, 8, 2>(p, smem, stats, warp, lane, seg, head0, n_heads, owners);
+    decode_merge<T::kWarps, 8, 2>(p, smem, stats, warp, lane, seg, first_head(), heads_here(), owners);
     sync();
-    if (!owners.whole) cuts.add(seg, owners);
+    if (!owners.whole && tid == 0) kept->cuts.add(seg, owners);
     left -= seg.units;
-    if (left <= 0) break;
+    if (left <= T::kOver) break;  // another beginning at most
     own.seg_first += seg.n_units;
     walk.next(seg, left);
+    if (tid == 0) kept->own.seg_first = own.seg_first, kept->seg = seg, kept->left = left;
   }
-  if (cuts.any()) decode_join<T::kWarps>(p, cuts, plan, sync);
+  sync();
+  if (kept->cuts.any()) decode_join<T::kWarps>(p, kept->cuts, plan, sync);
 }
 
 }  // namespace fl

@@ -51,7 +51,7 @@ int enqueue_decode(const void* Q, const void* k_pages, const void* v_pages, cons
   p.chunk_heads = (p.group + p.chunks - 1) / p.chunks;
   p.page_of = page_divisor(page_size);
   // units of all lengths that the table allows (64 tokens at least), for all heads
-  const int64_t longest = std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, INT32_MAX) / 64 + 1;
+  const int64_t longest = std::min<int64_t>(static_cast<int64_t>(max_pages) * page_size, INT32_MAX) / 64 + 2;
   p.small = batch <= 128 && longest * batch < (int64_t{1} << 31) / (static_cast<int64_t>(n_kv_heads) * p.chunks);
   p.window = window;
   p.sinks = sinks;
