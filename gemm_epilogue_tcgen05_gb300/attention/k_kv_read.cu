@@ -1,8 +1,8 @@
 // paged_kv_read: tokens of a cache back as bf16 rows of keys and values.
 //
 // Row r of sequence b is position seq_lens[b] - n_b + (r - first row of b), with n_b the rows that b gets: the
-// counterpart of the appends.  bf16 entries are moved as they are, E4M3 codes times their scale are rounded once, 4-bit
-// codes times theirs are bf16 numbers (three and five significant bits).
+// counterpart of the appends.  bf16 entries are moved as they are, E4M3 codes are multiplied by their scale in fp32 and
+// rounded, 4-bit codes times theirs are bf16 numbers (three and five significant bits).
 //
 // Bound by memory: a row is written once, its entries read once.  One warp does one row, all its heads; a lane writes
 // 16 bytes.

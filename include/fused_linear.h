@@ -406,7 +406,7 @@ FL_API int paged_kv_append_int4(const void* K, const void* V, void* k_pages, voi
  * K, V [T, n_kv_heads*128], pitch ldkv elements: what the appends do, the other way round.  Rows
  * cu_seqlens[b] .. cu_seqlens[b+1] - 1 are the last of the first seq_lens[b] tokens of sequence b (a
  * smaller number than the sequence's length gives a part from its middle); cu_seqlens NULL: row b is the
- * last one.  bf16 and 4-bit entries come back exactly, E4M3 entries rounded once.  Rows outside every
+ * last one.  bf16 and 4-bit entries come back exactly, E4M3 entries as code times scale in fp32, rounded.  Rows outside every
  * sequence stay as they were; a row whose position or page is outside the table or the cache is NaN.  K
  * and V must not overlap each other or the cache. */
 FL_API int paged_kv_read(const void* k_pages, const void* v_pages, const void* k_page_scale,
