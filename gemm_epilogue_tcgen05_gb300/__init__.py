@@ -596,6 +596,18 @@ def _on(dev, call, args, stream):
         return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
+def _elsewhere(dev):
+    """Whether `dev` (an index) is another device than the current one."""
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    return torch._C._cuda_getDevice() != dev
+
+
+def _raw(dev, stream):
+    """The handle of a given stream, or of the current one of device `dev`."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _pitch(a, b, rows, width, what):
     """The shared leading dimension of two [rows, width] tensors with unit column stride."""
     if a.is_contiguous() and b.is_contiguous():
@@ -687,19 +699,22 @@ def _cache_int4(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
     if ks is None or vs is None:
         raise ValueError("a 4-bit cache needs k_page_scale and v_page_scale")
     groups = HEAD_DIM // INT4_GROUP
-    want = (*shape[:3], groups)
+    n_pages, n_kv, page, _ = shape
+    want = (n_pages, n_kv, page, groups)
     if ks.dtype is not _BF16 or vs.dtype is not _BF16 or ks.shape != want or vs.shape != want or \
             ks.get_device() != dev or vs.get_device() != dev:
         raise ValueError(f"k_page_scale and v_page_scale: expected bf16 [num_pages, n_kv_heads, page_size, {groups}] on "
                          "the call's device")
-    n_pages, n_kv, page, _ = shape
-    pitch = _page_pitch(k_pages, v_pages, shape, n_kv * page * (HEAD_DIM // 2), "k_pages and v_pages")
-    spitch = _page_pitch(ks, vs, want, n_kv * page * groups, "k_page_scale and v_page_scale")
-    return (*_table(page_table, seq_lens, dev), n_kv, page, n_pages, pitch, spitch, FL_INT4)
+    pitch, spitch = n_kv * page * (HEAD_DIM // 2), n_kv * page * groups
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        pitch = _page_pitch(k_pages, v_pages, shape, pitch, "k_pages and v_pages")
+        spitch = _page_pitch(ks, vs, want, spitch, "k_page_scale and v_page_scale")
+    batch, max_pages, ldt = _table(page_table, seq_lens, dev)
+    return batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, FL_INT4
 
 
 def _any_cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
-    four = k_pages.dtype is _U8 and k_pages.dim() == 4 and k_pages.shape[3] == HEAD_DIM // 2
+    four = ks is not None and ks.dtype is _BF16  # no other cache has such scales
     return (_cache_int4 if four else _cache)(k_pages, v_pages, page_table, seq_lens, ks, vs, dev)
 
 
@@ -771,17 +786,21 @@ def paged_kv_append_int4(K, V, k_pages, v_pages, k_page_scale, v_page_scale, pag
     significant bits, so that a code times its scale is a bf16 number.  Rows, offsets and lengths are those of
     :func:`paged_kv_append`."""
     dev = K.get_device()
-    T, width, ld, _, rows_dt = _kv_pair(K, V, None, None, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_append_int4(K, V, k_pages, v_pages, k_page_scale, v_page_scale, page_table, seq_lens, cu_seqlens,
+                                        stream)
+    T, width, ld, _, _ = _kv_pair(K, V, None, None, dev)
     batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, _ = _cache_int4(k_pages, v_pages, page_table, seq_lens,
                                                                               k_page_scale, v_page_scale, dev)
     if width != n_kv * HEAD_DIM:
         raise ValueError("the rows must have the cache's n_kv_heads")
     if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", dev) != batch + 1:
         raise ValueError("cu_seqlens must have batch + 1 entries")
-    st = _on(dev, load().paged_kv_append_int4,
-             (K.data_ptr(), V.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_page_scale.data_ptr(),
-              v_page_scale.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), T, batch, n_kv,
-              HEAD_DIM, page, n_pages, max_pages, ld, ldt, pitch, spitch), stream)
+    st = load().paged_kv_append_int4(
+        K.data_ptr(), V.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_page_scale.data_ptr(), v_page_scale.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), T, batch, n_kv, HEAD_DIM, page, n_pages, max_pages, ld,
+        ldt, pitch, spitch, _raw(dev, stream))
     if st:
         _check("paged_kv_append_int4", st)
 
@@ -800,6 +819,10 @@ def paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, rows=
         with torch.cuda.stream(stream):
             return paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens, rows, k_page_scale, v_page_scale)
     dev = k_pages.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens, rows, k_page_scale, v_page_scale, K, V,
+                                 stream)
     batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _any_cache(k_pages, v_pages, page_table, seq_lens,
                                                                               k_page_scale, v_page_scale, dev)
     if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", dev) != batch + 1:
@@ -814,10 +837,10 @@ def paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, rows=
         raise ValueError("the rows must have the cache's n_kv_heads")
     if rows is not None and rows != T:
         raise ValueError("rows: not those of K and V")
-    st = _on(dev, load().paged_kv_read,
-             (k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale), page_table.data_ptr(),
-              seq_lens.data_ptr(), _addr(cu_seqlens), K.data_ptr(), V.data_ptr(), T, batch, n_kv, HEAD_DIM, page, n_pages,
-              max_pages, ld, ldt, pitch, spitch, dt), stream)
+    st = load().paged_kv_read(
+        k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale), page_table.data_ptr(),
+        seq_lens.data_ptr(), _addr(cu_seqlens), K.data_ptr(), V.data_ptr(), T, batch, n_kv, HEAD_DIM, page, n_pages,
+        max_pages, ld, ldt, pitch, spitch, dt, _raw(dev, stream))
     if st:
         _check("paged_kv_read", st)
     return K, V
@@ -885,6 +908,10 @@ def attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window=0,
             return attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window, sinks, k_page_scale,
                                            v_page_scale, scale, O, workspace)
     dev = Q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window, sinks, k_page_scale,
+                                           v_page_scale, scale, O, workspace, stream)
     rows, width, ldq = _query(Q, "Q", dev)
     batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _any_cache(k_pages, v_pages, page_table, seq_lens,
                                                                               k_page_scale, v_page_scale, dev)
@@ -897,11 +924,11 @@ def attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window=0,
         raise ValueError("O must have Q's shape")
     if workspace is None:
         workspace = attention_decode_workspace(Q.device)
-    st = _on(dev, load().attention_decode_window,
-             (Q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale),
-              page_table.data_ptr(), seq_lens.data_ptr(), O.data_ptr(), batch, width // HEAD_DIM, n_kv, HEAD_DIM, page,
-              n_pages, max_pages, ldq, ldo, ldt, pitch, spitch, HEAD_DIM ** -0.5 if scale is None else scale,
-              _span(window, "window"), _span(sinks, "sinks"), dt, workspace.data_ptr(), _space(workspace, dev)), stream)
+    st = load().attention_decode_window(
+        Q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale),
+        page_table.data_ptr(), seq_lens.data_ptr(), O.data_ptr(), batch, width // HEAD_DIM, n_kv, HEAD_DIM, page, n_pages,
+        max_pages, ldq, ldo, ldt, pitch, spitch, HEAD_DIM ** -0.5 if scale is None else scale, _span(window, "window"),
+        _span(sinks, "sinks"), dt, workspace.data_ptr(), _space(workspace, dev), _raw(dev, stream))
     if st:
         _check("attention_decode_window", st)
     return O
@@ -967,6 +994,10 @@ def attention_prefill_window(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, seq_le
             return attention_prefill_window(Q, K, V, cu_seqlens, cu_seqlens_k, seq_len, window, sinks, k_scale, v_scale,
                                             scale, O, workspace)
     dev = Q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return attention_prefill_window(Q, K, V, cu_seqlens, cu_seqlens_k, seq_len, window, sinks, k_scale, v_scale,
+                                            scale, O, workspace, stream)
     M, width, ldq = _query(Q, "Q", dev)
     rows, kv_width, ldkv, lds, dt = _kv_pair(K, V, k_scale, v_scale, dev)
     n_kv = kv_width // HEAD_DIM
@@ -985,11 +1016,11 @@ def attention_prefill_window(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, seq_le
         raise ValueError("O must have Q's shape")
     if workspace is None:
         workspace = attention_prefill_workspace(rows, n_kv, dt == FL_E4M3, Q.device)
-    st = _on(dev, load().attention_prefill_window,
-             (Q.data_ptr(), K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens),
-              _addr(cu_seqlens_k), O.data_ptr(), M, rows, batch, width // HEAD_DIM, n_kv, HEAD_DIM,
-              min(seq_len, M) or max(M, 1), ldq, ldkv, lds, ldo, HEAD_DIM ** -0.5 if scale is None else scale,
-              _span(window, "window"), _span(sinks, "sinks"), dt, workspace.data_ptr(), _space(workspace, dev)), stream)
+    st = load().attention_prefill_window(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens), _addr(cu_seqlens_k),
+        O.data_ptr(), M, rows, batch, width // HEAD_DIM, n_kv, HEAD_DIM, min(seq_len, M) or max(M, 1), ldq, ldkv, lds, ldo,
+        HEAD_DIM ** -0.5 if scale is None else scale, _span(window, "window"), _span(sinks, "sinks"), dt,
+        workspace.data_ptr(), _space(workspace, dev), _raw(dev, stream))
     if st:
         _check("attention_prefill_window", st)
     return O
