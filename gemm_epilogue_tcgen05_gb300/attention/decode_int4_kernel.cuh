@@ -23,8 +23,8 @@
 // a group in the N columns; of larger groups each 8 read the cache).  V^T comes by ldmatrix: a group's 16 bytes are 8 columns of
 // 16 bits, 4 codes each.  The maxima m and m' rise only when a logit passes them by more than 8.
 //
-// Work.  Units (decode_attention_common.cuh) are 128 tokens, a stage of the CTA's ring; each of four warps takes 32 of them.  A fifth
-// warp walks ahead and fills the stages by tensor copies, one for each 32, 16 or 8 tokens of a page and tensor (the codes with
+// Work.  Units (decode_attention_common.cuh) are 128 tokens, a stage of the CTA's ring; each of four warps takes 32 of them.  A
+// fifth warp walks ahead and fills the stages by tensor copies, one for each 32, 16 or 8 tokens of a page and tensor (the codes with
 // the 64-byte swizzle, so that eight rows of a chunk meet in no bank), and bulk copies for the scales; caches that these
 // do not fit are copied by 16 bytes.  With a ring of its own for each warp, filled by itself, finding the pages and issuing the
 // copies took 112 of 400 instructions for 16 tokens and a head: 105.7 us for these 64 sequences, 91 with the fifth warp.  In the
@@ -61,8 +61,8 @@ struct DecodeInt4Traits {
   static constexpr int kQuery = kInt4Groups * (32 * 16 + 8 * 4) + 4 * 16;
   static constexpr int kOver = 1;  // units that the beginning of a (sequence, head) counts as
   static constexpr int kCtas = 3, kStages = 3;
-  static constexpr int kSmem = 512 /*alignment*/ + kStages * kStage + kWarps * (kOwn + 8 * 16) + kQuery + 128 + 2 * kStages * 8 + 16 +
-                               sizeof(DecodeKept);
+  static constexpr int kSmem = 512 /*alignment*/ + kStages * kStage + kWarps * (kOwn + 8 * 16) + kQuery + 128 + 2 * kStages * 8 +
+                               16 + sizeof(DecodeKept);
 };
 
 template <bool TRANS>
@@ -108,7 +108,8 @@ __device__ __forceinline__ bool decode_wait(uint64_t* bar, uint32_t parity, int*
 }
 // d = a b.
 template <bool F16>
-__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
   if (F16)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -150,7 +151,8 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
   using T = DecodeInt4Traits;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((512u - (smem_u32(smem_raw) & 511u)) & 511u);
-  float4* const stats = reinterpret_cast<float4*>(smem + T::kStages * T::kStage + T::kWarps * T::kOwn);  // [warp][head]: m, m', l, place
+  // [warp][head]: m, m', l, place
+  float4* const stats = reinterpret_cast<float4*>(smem + T::kStages * T::kStage + T::kWarps * T::kOwn);
   uint8_t* const query = reinterpret_cast<uint8_t*>(stats + T::kWarps * 8);
   long long* const plan = reinterpret_cast<long long*>(query + T::kQuery);
   uint64_t* const full = reinterpret_cast<uint64_t*>(plan + 16);
@@ -259,15 +261,17 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           bad |= !there;
           if (!there) continue;
           const long long cell = static_cast<long long>(seg.kvh) * p.c.page_size + (pos - page * p.c.page_size);
-          const long long code = entry * p.c.page_pitch + cell * T::kRowBytes, scale = (entry * p.c.scale_pitch + cell * kInt4Groups) * 2;
+          const long long code = entry * p.c.page_pitch + cell * T::kRowBytes,
+                          scale = (entry * p.c.scale_pitch + cell * kInt4Groups) * 2;
 #pragma unroll
           for (int c = 0; c < T::kRowBytes / 16; ++c) {
             const uint32_t at = to + (row >> 1) * 128 + ((((row & 1) << 2 | c) ^ (row >> 1 & 3)) << 4);  // as the tensor copies do
             cp_async_16_or_zero(at, static_cast<const uint8_t*>(p.c.k) + code + c * 16, true);
             cp_async_16_or_zero(at + T::kTile, static_cast<const uint8_t*>(p.c.v) + code + c * 16, true);
           }
-          cp_async_8_or_zero(to + 2 * T::kTile + row * T::kScaleBytes, static_cast<const uint8_t*>(p.c.ks) + scale, true);
-          cp_async_8_or_zero(to + 2 * T::kTile + T::kScales + row * T::kScaleBytes, static_cast<const uint8_t*>(p.c.vs) + scale, true);
+          const uint32_t scales = to + 2 * T::kTile + row * T::kScaleBytes;
+          cp_async_8_or_zero(scales, static_cast<const uint8_t*>(p.c.ks) + scale, true);
+          cp_async_8_or_zero(scales + T::kScales, static_cast<const uint8_t*>(p.c.vs) + scale, true);
         }
         bad = __any_sync(~0u, bad);
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[stage])) : "memory");
@@ -312,7 +316,8 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
       for (int c = 0; c < kInt4Groups; ++c) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if (g < n_heads)
-          w = *reinterpret_cast<const uint4*>(p.Q + seg.b * p.ldq + static_cast<long long>(head0 + g) * kHeadDim + c * kInt4Group + q * 8);
+          w = *reinterpret_cast<const uint4*>(p.Q + seg.b * p.ldq + static_cast<long long>(head0 + g) * kHeadDim + c * kInt4Group +
+                                              q * 8);
         if (c == warp) own_group = w;
         const uint32_t four[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -338,12 +343,14 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
       }
       sum += __shfl_xor_sync(~0u, sum, 1);
       sum += __shfl_xor_sync(~0u, sum, 2);
-      if (warp < kInt4Groups) *reinterpret_cast<uint4*>(query + (warp * 32 + lane) * 16) = make_uint4(two[0], two[1], two[2], two[3]);
+      if (warp < kInt4Groups)
+        *reinterpret_cast<uint4*>(query + (warp * 32 + lane) * 16) = make_uint4(two[0], two[1], two[2], two[3]);
       if (warp < kInt4Groups && q == 0) reinterpret_cast<float*>(query + kInt4Groups * 512)[warp * 8 + g] = sum * (-8.f / kDecCode);
       // f times 2^24, as two factors the first of which neither overflows nor, where it matters, underflows
       const float f0 = f > 1.f ? kDecCode : f, f1 = f > 1.f ? f : kDecCode;
       // [q]: of heads 2q and 2q + 1 the first, then the second
-      if (warp == 0 && q < 2) reinterpret_cast<float*>(query + kInt4Groups * (512 + 32))[(g >> 1) * 4 + q * 2 + (g & 1)] = q == 0 ? f0 : f1;
+      if (warp == 0 && q < 2)
+        reinterpret_cast<float*>(query + kInt4Groups * (512 + 32))[(g >> 1) * 4 + q * 2 + (g & 1)] = q == 0 ? f0 : f1;
       sync();
     }
     // Of this segment: the table or the length is bad; the scales of some token lie far apart (kSpread); in bits 0-3 the groups of
@@ -534,9 +541,9 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           }
         } else {
 #pragma unroll
-          for (int r = 0; r < T::kSubs * 2; ++r) {  // tokens g + 8 r: eight at a time, the other eight of a product with weights of zero
+          for (int r = 0; r < T::kSubs * 2; ++r) {  // tokens g + 8 r: eight at a time, the other eight with weights of zero
             uint2 raw = *reinterpret_cast<const uint2*>(v_scales + (g + r * 8) * 8);
-            if (t + g + r * 8 >= seg.t1 || !walk.in_sight(seg, pos0 + g + r * 8)) raw = make_uint2(0, 0);  // a row that may hold anything
+            if (t + g + r * 8 >= seg.t1 || !walk.in_sight(seg, pos0 + g + r * 8)) raw = make_uint2(0, 0);  // it may hold anything
             const uint32_t four[4] = {raw.x & 0xFFFFu, raw.x >> 16, raw.y & 0xFFFFu, raw.y >> 16};
             uint32_t largest = 0;
 #pragma unroll
@@ -598,7 +605,8 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           *reinterpret_cast<float4*>(row + (((c * 8 + g) ^ (q * 2)) << 2)) = four;
         }
         if (g == 0)
-          stats[warp * 8 + h] = make_float4(m[i], mv[i] - kDecLift, spoiled ? NAN : sum, __int_as_float(static_cast<int>(mine - smem)));
+          stats[warp * 8 + h] =
+              make_float4(m[i], mv[i] - kDecLift, spoiled ? NAN : sum, __int_as_float(static_cast<int>(mine - smem)));
       }
     }
     sync();

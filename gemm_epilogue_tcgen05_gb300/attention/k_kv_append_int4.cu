@@ -14,7 +14,8 @@
 // rounds that to a whole number.
 //
 // Bound by memory: 512 bytes in and 144 out for each head of a token.  One warp moves a row, all its heads, as in
-// paged_kv_append; a lane takes 8 values, four lanes a group.
+// paged_kv_append; a lane takes 8 values, four lanes a group.  10075 rows of 8 heads: 13.1 us, 4.0 TB/s: a chain of loads (offsets,
+// length, table entry) behind a row's own, and the ramp of a short kernel.  (Several rows a warp: 16.5 us and more.)
 #include "attention_common.h"
 
 namespace fl {
