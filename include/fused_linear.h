@@ -423,6 +423,8 @@ FL_API int paged_kv_read(const void* k_pages, const void* v_pages, const void* k
  * window (behind the sinks) need not be pages: a cache may have given them back.
  * 4 bits: weights are rounded to fp16, and so is their product with the part of V's scale that is not a power
  * of two common to the token's four; a scale of V that is not finite makes its 32 columns of the result NaN.
+ * The kernel over 4 bits waits for its copies; a wait that runs out gives NaN rows and FL_ERR_TIMEOUT from
+ * fl_check_device_status(workspace).
  * Other arguments, the workspace and errors are those of attention_decode. */
 FL_API int attention_decode_window(const void* Q, const void* k_pages, const void* v_pages, const void* k_page_scale,
                                    const void* v_page_scale, const int32_t* page_table, const int32_t* seq_lens,
