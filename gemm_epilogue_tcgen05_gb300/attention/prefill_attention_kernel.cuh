@@ -988,6 +988,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         const int bad_lo = said.bad_lo, bad_hi = said.bad_hi;
         float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;  // E4M3: O is held at m - 7, l at mx
         if (WIN && l == 0.f) inv = 0.f;  // a row that sees nothing
+        const uint64_t inv2 = f2(inv, inv);
         // A thread has a row; lines of global memory want a few rows each, all of 128 bytes.  So 16-byte pieces go
         // through shared memory, piece j of row r at place j ^ (r's low bits).  (Stored straight from the row's
         // thread, each instruction touched 32 lines: 4000 cycles a tile.)
@@ -1014,8 +1015,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
             for (int q = 0; q < 4; ++q) {
               uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(o[q * 8 + e * 2]) * inv, __uint_as_float(o[q * 8 + e * 2 + 1]) * inv);
+              for (int e = 0; e < 4; ++e) {
+                float a, b;
+                f2_split(f2_mul(f2(__uint_as_float(o[q * 8 + e * 2]), __uint_as_float(o[q * 8 + e * 2 + 1])), inv2), a, b);
+                w[e] = pack_bf16x2(a, b);
+              }
               st_shared_v4(out + lane * (T::kOutCols * 2) + (((h >> 3) + q) ^ (lane & kSwizzle)) * 16, w[0], w[1], w[2], w[3]);
             }
           }
