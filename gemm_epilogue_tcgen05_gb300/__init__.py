@@ -574,6 +574,7 @@ def fused_swiglu_bwd(dO, Wd, G, U, dGU=None, stream=None):
 
 
 HEAD_DIM = 128
+_LONGEST = 0x7FFFFFFF  # tokens
 INT4_GROUP = 32  # columns of a 4-bit cache that share a scale
 _BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 
@@ -713,17 +714,15 @@ def _cache_int4(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
     return batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, FL_INT4
 
 
-def _any_cache(k_pages, v_pages, page_table, seq_lens, ks, vs, dev):
-    four = ks is not None and ks.dtype is _BF16  # no other cache has such scales
-    return (_cache_int4 if four else _cache)(k_pages, v_pages, page_table, seq_lens, ks, vs, dev)
-
-
 def _table(page_table, seq_lens, dev):
     """Checks the page table; returns (batch, max_pages, ldt)."""
-    batch, t_shape = _ints(seq_lens, "seq_lens", dev), page_table.shape
-    if page_table.dtype is not _I32 or len(t_shape) != 2 or t_shape[0] != batch or page_table.get_device() != dev:
+    shape = page_table.shape
+    if page_table.dtype is not _I32 or len(shape) != 2 or page_table.get_device() != dev:
         raise ValueError("page_table: expected int32 [batch, max_pages] on the call's device")
-    ldt = max_pages = t_shape[1]
+    batch, max_pages = shape
+    if seq_lens.dtype is not _I32 or seq_lens.shape != (batch,) or seq_lens.get_device() != dev or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens: expected a contiguous int32 vector on the call's device, one for each row of page_table")
+    ldt = max_pages
     if not page_table.is_contiguous():
         ldt, one = page_table.stride()
         if one != 1 and max_pages > 1:
@@ -745,6 +744,13 @@ def _query(t, name, dev):
     if one != 1 and width > 1:
         raise ValueError(f"{name}: expected unit column stride")
     return rows, width, ld if rows > 1 else width
+
+
+def _like_query(O, rows, width, dev):
+    """Checks O, which has Q's shape; returns its leading dimension."""
+    if O.dtype is not _BF16 or O.shape != (rows, width) or O.get_device() != dev:
+        raise ValueError("O must have Q's shape, bf16 on the call's device")
+    return width if O.is_contiguous() else _query(O, "O", dev)[2]
 
 
 def _space(t, dev):
@@ -823,8 +829,9 @@ def paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, rows=
         with torch.cuda.device(dev):
             return paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens, rows, k_page_scale, v_page_scale, K, V,
                                  stream)
-    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _any_cache(k_pages, v_pages, page_table, seq_lens,
-                                                                              k_page_scale, v_page_scale, dev)
+    check = _cache_int4 if k_page_scale is not None and k_page_scale.dtype is _BF16 else _cache  # only 4 bits have such scales
+    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = check(k_pages, v_pages, page_table, seq_lens, k_page_scale,
+                                                                         v_page_scale, dev)
     if cu_seqlens is not None and _ints(cu_seqlens, "cu_seqlens", dev) != batch + 1:
         raise ValueError("cu_seqlens must have batch + 1 entries")
     if K is None:
@@ -894,7 +901,7 @@ def _span(n, name):
     """A number of tokens; what no sequence can have is as good as the longest one."""
     if n < 0:
         raise ValueError(f"{name}: expected a number of tokens, not {n}")
-    return min(n, 0x7FFFFFFF)
+    return min(n, _LONGEST)
 
 
 def attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window=0, sinks=0, k_page_scale=None,
@@ -913,22 +920,23 @@ def attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window=0,
             return attention_decode_window(Q, k_pages, v_pages, page_table, seq_lens, window, sinks, k_page_scale,
                                            v_page_scale, scale, O, workspace, stream)
     rows, width, ldq = _query(Q, "Q", dev)
-    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = _any_cache(k_pages, v_pages, page_table, seq_lens,
-                                                                              k_page_scale, v_page_scale, dev)
+    check = _cache_int4 if k_page_scale is not None and k_page_scale.dtype is _BF16 else _cache  # only 4 bits have such scales
+    batch, max_pages, ldt, n_kv, page, n_pages, pitch, spitch, dt = check(k_pages, v_pages, page_table, seq_lens, k_page_scale,
+                                                                         v_page_scale, dev)
     if rows != batch:
         raise ValueError("Q: expected one row for each sequence")
     if O is None:
         O = torch.empty((rows, width), dtype=_BF16, device=Q.device)
-    o_rows, o_width, ldo = _query(O, "O", dev)
-    if o_rows != rows or o_width != width:
-        raise ValueError("O must have Q's shape")
+    ldo = _like_query(O, rows, width, dev)
     if workspace is None:
         workspace = attention_decode_workspace(Q.device)
+    if not (0 <= window <= _LONGEST and 0 <= sinks <= _LONGEST):
+        window, sinks = _span(window, "window"), _span(sinks, "sinks")
     st = load().attention_decode_window(
         Q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_page_scale), _addr(v_page_scale),
         page_table.data_ptr(), seq_lens.data_ptr(), O.data_ptr(), batch, width // HEAD_DIM, n_kv, HEAD_DIM, page, n_pages,
-        max_pages, ldq, ldo, ldt, pitch, spitch, HEAD_DIM ** -0.5 if scale is None else scale, _span(window, "window"),
-        _span(sinks, "sinks"), dt, workspace.data_ptr(), _space(workspace, dev), _raw(dev, stream))
+        max_pages, ldq, ldo, ldt, pitch, spitch, HEAD_DIM ** -0.5 if scale is None else scale, window,
+        sinks, dt, workspace.data_ptr(), _space(workspace, dev), _raw(dev, stream))
     if st:
         _check("attention_decode_window", st)
     return O
@@ -1011,15 +1019,15 @@ def attention_prefill_window(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, seq_le
         raise ValueError("cu_seqlens_k: expected as many entries as cu_seqlens")
     if O is None:
         O = (torch.empty if cu_seqlens is None else torch.zeros)((M, width), dtype=_BF16, device=Q.device)
-    o_rows, o_width, ldo = _query(O, "O", dev)
-    if o_rows != M or o_width != width:
-        raise ValueError("O must have Q's shape")
+    ldo = _like_query(O, M, width, dev)
     if workspace is None:
         workspace = attention_prefill_workspace(rows, n_kv, dt == FL_E4M3, Q.device)
+    if not (0 <= window <= _LONGEST and 0 <= sinks <= _LONGEST):
+        window, sinks = _span(window, "window"), _span(sinks, "sinks")
     st = load().attention_prefill_window(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens), _addr(cu_seqlens_k),
         O.data_ptr(), M, rows, batch, width // HEAD_DIM, n_kv, HEAD_DIM, min(seq_len, M) or max(M, 1), ldq, ldkv, lds, ldo,
-        HEAD_DIM ** -0.5 if scale is None else scale, _span(window, "window"), _span(sinks, "sinks"), dt,
+        HEAD_DIM ** -0.5 if scale is None else scale, window, sinks, dt,
         workspace.data_ptr(), _space(workspace, dev), _raw(dev, stream))
     if st:
         _check("attention_prefill_window", st)
