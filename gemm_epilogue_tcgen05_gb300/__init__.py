@@ -97,8 +97,10 @@ def load() -> ctypes.CDLL:
     lib.fl_attention_decode_workspace_bytes.restype = SZ
     lib.attention_prefill.argtypes = [P] * 7 + [I] * 6 + [I64] * 4 + [F, I, I, P, SZ, P]
     lib.attention_prefill.restype = I
-    lib.attention_prefill_window.argtypes = [P] * 8 + [I] * 7 + [I64] * 4 + [F, I, I, I, P, SZ, P]
+    lib.attention_prefill_window.argtypes = [P] * 8 + [I] * 7 + [I64] * 4 + [F, I, I, I, P, SZ, P, SZ, P]
     lib.attention_prefill_window.restype = I
+    lib.fl_attention_prefill_window_scratch_bytes.argtypes = [I] * 7
+    lib.fl_attention_prefill_window_scratch_bytes.restype = SZ
     lib.fl_attention_prefill_workspace_bytes.argtypes = [I, I, I]
     lib.fl_attention_prefill_workspace_bytes.restype = SZ
     lib.fl_cross_entropy_workspace_bytes.argtypes = [I, I]
@@ -575,6 +577,7 @@ def fused_swiglu_bwd(dO, Wd, G, U, dGU=None, stream=None):
 
 HEAD_DIM = 128
 _LONGEST = 0x7FFFFFFF  # tokens
+_FEW_ROWS = 1 << 22  # elements of Q that some hundred units of prefill hold
 INT4_GROUP = 32  # columns of a 4-bit cache that share a scale
 _BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 
@@ -996,7 +999,7 @@ def attention_prefill_window(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, seq_le
     cu_seqlens_k: offsets of the keys' rows, where the queries are the last rows of longer sequences (the next part of a
     prompt behind rows that :func:`paged_kv_read` returns): sequence b has query rows cu_seqlens[b] .. and key rows
     cu_seqlens_k[b] ..; a query in front of the first key gets zeros.  The workspace is that of attention_prefill for
-    K's rows."""
+    K's rows.  Few queries behind many keys take up to 20 MB of torch's memory, too, while the call runs."""
     if stream is not None and (O is None or workspace is None):
         with torch.cuda.stream(stream):
             return attention_prefill_window(Q, K, V, cu_seqlens, cu_seqlens_k, seq_len, window, sinks, k_scale, v_scale,
@@ -1024,11 +1027,19 @@ def attention_prefill_window(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, seq_le
         workspace = attention_prefill_workspace(rows, n_kv, dt == FL_E4M3, Q.device)
     if not (0 <= window <= _LONGEST and 0 <= sinks <= _LONGEST):
         window, sinks = _span(window, "window"), _span(sinks, "sinks")
+    scratch, space = None, 0
+    if cu_seqlens_k is not None and M * width <= _FEW_ROWS and rows > 1536:  # few units over many keys: cut along these, perhaps
+        space = load().fl_attention_prefill_window_scratch_bytes(M, rows, batch, width // HEAD_DIM, n_kv, window, sinks)
+        if space and stream is None:  # memory of this call's own, on its stream
+            scratch = torch.empty(space, dtype=_U8, device=Q.device)
+        elif space:
+            with torch.cuda.stream(stream):
+                scratch = torch.empty(space, dtype=_U8, device=Q.device)
     st = load().attention_prefill_window(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), _addr(k_scale), _addr(v_scale), _addr(cu_seqlens), _addr(cu_seqlens_k),
         O.data_ptr(), M, rows, batch, width // HEAD_DIM, n_kv, HEAD_DIM, min(seq_len, M) or max(M, 1), ldq, ldkv, lds, ldo,
         HEAD_DIM ** -0.5 if scale is None else scale, window, sinks, dt,
-        workspace.data_ptr(), _space(workspace, dev), _raw(dev, stream))
+        workspace.data_ptr(), _space(workspace, dev), _addr(scratch), space, _raw(dev, stream))
     if st:
         _check("attention_prefill_window", st)
     return O

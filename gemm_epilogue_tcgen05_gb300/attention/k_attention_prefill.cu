@@ -40,8 +40,46 @@ bool encode_q(CUtensorMap* map, const void* base, int heads, int rows, int64_t l
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Query heads of a tile: the largest part of a group that leaves room for two tokens.
+int heads_of_tile(int group) {
+  int hp = group < 64 ? group : 64;
+  while (group % hp != 0) --hp;
+  return hp;
+}
+// Blocks of per_cta tokens, at most: the lengths are on the device.
+long long packed_blocks(int M, int batch, long long per_cta) { return M / per_cta + batch; }
+
+// Parts that each unit may be cut into where few units go over many keys, 1: none.  A part costs a unit's output, 128 KB into the
+// scratch buffer and out of it, and a second kernel joins them, so they pay where SMs would be idle and units be long.  Measured,
+// whole units -> parts, 32/8 heads, bf16: 33 tokens behind 5000 58.1 -> 24.8 us, 128 behind 8000 92.9 -> 35.5, 512 behind 8000 96.7
+// -> 62.1, 16 behind 1500 (two parts) 20.9 -> 18.1, which the second launch costs the host; E4M3, 33 behind 5000 70.1 -> 34.4; 144
+// units of up to 33 tiles, cut all the same, 55 -> 62.
+int parts_of_units(long long units, int M_k, int window, int sinks, long long per_cta, int num_sms) {
+  long long keys = M_k;
+  if (window > 0) keys = std::min(keys, static_cast<long long>(window) + sinks + 61 + per_cta);
+  const long long longest = (keys - 1) / kPreTile / kPrePartTiles + 1;
+  if (longest < 3) return 1;
+  return static_cast<int>(std::max<long long>(std::min(longest, num_sms / units), 1));
+}
+size_t scratch_of(long long numbers) {
+  return numbers * kPrePartFloats * sizeof(float) + (numbers + 1) * sizeof(PrefillCut);
+}
+
 }  // namespace
 }  // namespace fl
+
+extern "C" size_t fl_attention_prefill_window_scratch_bytes(int M, int M_k, int batch, int n_heads, int n_kv_heads, int window,
+                                                            int sinks) {
+  using namespace fl;
+  DeviceInfo di;
+  if (M <= 0 || M_k <= 0 || batch <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 || window < 0 ||
+      sinks < 0 || current_device(&di) != FL_OK)
+    return 0;
+  const int hp = heads_of_tile(n_heads / n_kv_heads);
+  const long long per_cta = 2 * (kPreTile / hp), units = packed_blocks(M, batch, per_cta) * (n_heads / hp);
+  const int parts = parts_of_units(units, M_k, window, sinks, per_cta, di.num_sms);
+  return parts > 1 ? scratch_of(units * parts) : 0;
+}
 
 extern "C" size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, int kv_dtype) {
   using namespace fl;
@@ -59,7 +97,7 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
                     const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, void* O, int M, int M_k, int batch, int n_heads,
                     int n_kv_heads, int head_dim, int seq_len, int64_t ldq, int64_t ldkv, int64_t lds, int64_t ldo,
                     float scale, int causal, int window, int sinks, int kv_dtype, void* workspace,
-                    size_t workspace_bytes, void* stream) {
+                    size_t workspace_bytes, void* scratch, size_t scratch_bytes, void* stream) {
   if (M < 0 || M_k < 0 || n_heads < 0 || n_kv_heads < 0 || (cu_seqlens != nullptr ? batch < 0 : seq_len < 1))
     return FL_ERR_INVALID_ARG;
   if (cu_seqlens_k != nullptr ? cu_seqlens == nullptr : M_k != M) return FL_ERR_INVALID_ARG;
@@ -81,7 +119,7 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
     return FL_ERR_ALIGNMENT;
   if (workspace == nullptr || workspace_bytes < fl_attention_prefill_workspace_bytes(M_k, n_kv_heads, kv_dtype))
     return FL_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(workspace) & (kWsStatusBytes - 1)) != 0) return FL_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(workspace) & (kWsStatusBytes - 1)) != 0 || !aligned16(scratch)) return FL_ERR_ALIGNMENT;
   DeviceInfo di;
   const int st = current_device(&di);
   if (st != FL_OK) return st;
@@ -90,9 +128,7 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
   PrefillParams p;
   std::memset(&p, 0, sizeof(p));
   p.group = n_heads / n_kv_heads;
-  // heads of a tile: the largest part of the group that leaves room for two tokens
-  p.hp = p.group < 64 ? p.group : 64;
-  while (p.group % p.hp != 0) --p.hp;
+  p.hp = heads_of_tile(p.group);
   p.tq = kPreTile / p.hp;
   p.pairs = n_heads / p.hp;
   const int64_t kv_bytes = static_cast<int64_t>(M_k) * kHeadDim * 4;  // of one kv head, as bf16
@@ -104,7 +140,7 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
   const long long per_cta = 2 * p.tq;
   const long long blocks = cu_seqlens == nullptr
                                ? (M / seq_len) * ((seq_len - 1) / per_cta + 1) + (M % seq_len + per_cta - 1) / per_cta
-                               : M / per_cta + batch;  // an upper bound: the lengths are on the device
+                               : packed_blocks(M, batch, per_cta);
   if (blocks * p.pairs > (1ll << 30)) return FL_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const void* k16 = K;
@@ -151,6 +187,16 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
   p.work = reinterpret_cast<unsigned*>(ws + kWsStatusBytes);
   p.timeout_ns = wait_timeout_ns();
   const bool windowed = p.window > 0 || cu_seqlens_k != nullptr;
+  const long long units = blocks * p.pairs;
+  const int most_parts = cu_seqlens_k == nullptr ? 1 : parts_of_units(units, M_k, p.window, p.sinks, per_cta, di.num_sms);
+  const bool cut = most_parts > 1 && scratch != nullptr && scratch_bytes >= scratch_of(units * most_parts);
+  if (cut) {
+    p.flat = 1;
+    p.most_parts = most_parts;
+    p.cuts = static_cast<PrefillCut*>(scratch);
+    p.parts = reinterpret_cast<float*>(p.cuts + 1 + units * most_parts);
+  }
+  if (!fp8 && cut) return launch_prefill_parts(p, false, units * most_parts, di, s);
   if (!fp8)
     return windowed ? launch_prefill_window(p, false, blocks * p.pairs, di, s)
                     : launch_prefill<false, false>(p, blocks * p.pairs, di, s);
@@ -168,6 +214,7 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
                         static_cast<__nv_bfloat16*>(const_cast<void*>(k16)), static_cast<__half*>(const_cast<void*>(v16)),
                         const_cast<float*>(p.powers)))
     return FL_ERR_CUDA;
+  if (cut) return launch_prefill_parts(p, true, units * most_parts, di, s);
   return windowed ? launch_prefill_window(p, true, blocks * p.pairs, di, s)
                   : launch_prefill<true, false>(p, blocks * p.pairs, di, s);
 }
@@ -182,7 +229,7 @@ extern "C" int attention_prefill(const void* Q, const void* K, const void* V, co
                                  size_t workspace_bytes, void* stream) {
   return fl::enqueue_prefill(Q, K, V, k_scale, v_scale, cu_seqlens, nullptr, O, M, M, batch, n_heads, n_kv_heads, head_dim,
                              seq_len, ldq, ldkv, lds, ldo, scale, causal, 0, 0, kv_dtype, workspace, workspace_bytes,
-                             stream);
+                             nullptr, 0, stream);
 }
 
 extern "C" int attention_prefill_window(const void* Q, const void* K, const void* V, const float* k_scale,
@@ -190,9 +237,9 @@ extern "C" int attention_prefill_window(const void* Q, const void* K, const void
                                         void* O, int M, int M_k, int batch, int n_heads, int n_kv_heads, int head_dim,
                                         int seq_len, int64_t ldq, int64_t ldkv, int64_t lds, int64_t ldo, float scale,
                                         int window, int sinks, int kv_dtype, void* workspace, size_t workspace_bytes,
-                                        void* stream) {
+                                        void* scratch, size_t scratch_bytes, void* stream) {
   if (window < 0 || sinks < 0) return FL_ERR_INVALID_ARG;
   return fl::enqueue_prefill(Q, K, V, k_scale, v_scale, cu_seqlens, cu_seqlens_k, O, M, M_k, batch, n_heads, n_kv_heads,
                              head_dim, seq_len, ldq, ldkv, lds, ldo, scale, 1, window, sinks, kv_dtype, workspace,
-                             workspace_bytes, stream);
+                             workspace_bytes, scratch, scratch_bytes, stream);
 }

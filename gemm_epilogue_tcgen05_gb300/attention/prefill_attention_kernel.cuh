@@ -37,6 +37,10 @@
 // key tiles for 64 tokens at the tensor cores' pace and 1.7 us between units.  (Tiles at multiples of 128 keys, the sinks with
 // one of their own: 116 us.)
 //
+// Parts (CUT, WIN).  Few units over many keys (a prompt's next part behind thousands of tokens) leave SMs idle: then a unit's
+// stream is cut into parts of 6 key tiles and more, each a unit for itself, whose O, m and l go to a scratch buffer as they are,
+// and a second kernel joins them in their order.  A kernel of its own: the mere presence of this code cost E4M3 6 %.
+//
 // Masked columns have weight zero, but 0 * NaN is NaN: in tiles where some row masks some key, warp 11 replaces
 // values of V that are not finite by zero before the product; rows that do see such a key add it at the end.
 //
@@ -75,6 +79,9 @@ static_assert(kPreThreads * kPreRegs == 256 * kPreRegsSoftmax + 128 * kPreRegsOt
 constexpr int kPreTile = 128;                      // query rows of a tile, and keys of a tile
 constexpr int kPreTileBytes = kPreTile * kHeadDim * 2;
 constexpr int kPreRing = 3;                        // tile descriptors
+constexpr int kPrePartTiles = 6;                   // CUT: key tiles of a part, at least
+// A part: of query tiles 0 and 1 O [32 float4][128 rows], then m, mx and l of each row.
+constexpr int kPrePartRows = kPreTile * (kHeadDim + 3), kPrePartFloats = 2 * kPrePartRows;
 constexpr float kPreNone = -3e38f;                 // a maximum over nothing: any finite logit passes it
 constexpr float kPreLazy = 8.f;
 constexpr uint64_t kPreDrainNs = 1000000000;       // for copies and products in flight, whatever the limit of the waits
@@ -97,6 +104,13 @@ enum : int {
   W_PRE_KV_FULL = 25, W_PRE_S = 26, W_PRE_P = 27, W_PRE_O = 28, W_PRE_V = 29
 };
 
+// Of a unit's first part: what the join needs; `parts` 0 in the others and where nothing is to be joined.
+struct alignas(16) PrefillCut {
+  int parts[2], step;  // of query tiles 0 and 1, and how far apart their numbers are
+  int row, tokens;     // row of the first token, and how many there are
+  int head0, unused[2];
+};
+
 struct alignas(128) PrefillParams {
   CUtensorMap map_q;  // Q [M][n_heads][128] bf16, box {64, hp, tq}
   CUtensorMap map_k;  // K [M][n_kv * 128] bf16, box {64, 128}
@@ -112,6 +126,9 @@ struct alignas(128) PrefillParams {
   CUtensorMap map_k32, map_v32;  // WIN: the same as map_k and map_v, box {64, 32}
   const int* cu_k;               // WIN: offsets of the keys' rows, of which there are M_k; null: those of the queries
   int M_k, window, sinks;        // WIN; a window of 0 hides nothing
+  int most_parts;                // CUT: numbers that a unit has
+  float* parts;                  // CUT: [numbers][kPrePartFloats]
+  PrefillCut* cuts;              // CUT: [numbers], and in front of them one whose `step` says how many there are
   __nv_bfloat16* O;
   long long ldo;
   int M, batch, seq_len, causal, flat;
@@ -122,6 +139,14 @@ struct alignas(128) PrefillParams {
   int* status;
   unsigned* work;          // [0] ranks given out beyond the first of each CTA, [1] CTAs that take no more
   unsigned long long timeout_ns;
+};
+
+struct PrefillJoinParams {
+  const float* parts;
+  const PrefillCut* cuts;
+  int hp, tq;
+  __nv_bfloat16* O;
+  long long ldo;
 };
 
 struct PrefillTraits {
@@ -142,6 +167,7 @@ struct PrefillTile {
   int head0, kvh;
   int q_row0;          // WIN: row of position 0, as if the queries began there
   int k0, sink_keys;   // WIN: place P of the stream is key P below sink_keys, else k0 + P - sink_keys
+  int place0, part;    // CUT: where in the stream the part begins, and its number, -1 for a whole unit
   int bad_lo, bad_hi;  // set by warp 11: first and last key of masked tiles whose V is not finite (none: hi < 0)
 };
 
@@ -250,7 +276,7 @@ __device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t c) {
   else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0), "r"(c));
   return r;
 }
-template <bool FP8, bool WIN>
+template <bool FP8, bool WIN, bool CUT = false>
 __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const __grid_constant__ PrefillParams p) {
   using T = PrefillTraits;
   extern __shared__ uint8_t smem_raw[];
@@ -294,7 +320,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     t.row0 = s.row0, t.len = s.len, t.tok0 = s.tok0, t.n0 = s.n0, t.n1 = s.n1, t.head0 = s.head0, t.kvh = s.kvh;
     if (WIN) {
       t.q_row0 = s.q_row0, t.k0 = s.k0, t.sink_keys = s.sink_keys;
-      return t.n0 > 0;  // a tile may have no keys
+      if (CUT) t.place0 = s.place0;
+      return CUT ? max(t.n0, t.n1) > 0 : t.n0 > 0;  // a tile may have no keys
     }
     return t.len > 0;
   };
@@ -302,11 +329,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   // First key of chunk h of a unit's i-th key tile; WIN: and whether all rows see all of the tile, a run of keys.
   auto key_of = [&](const PrefillTile& t, int i, int h) {
     if (!WIN) return i * kPreTile + h * 32;
-    const int place = i * kPreTile + h * 32;
+    const int place = (CUT ? t.place0 : 0) + i * kPreTile + h * 32;
     return place < t.sink_keys ? place : place + t.k0 - t.sink_keys;
   };
   auto run_of_keys = [&](const PrefillTile& t, int i) {
-    const int place = i * kPreTile;
+    const int place = (CUT ? t.place0 : 0) + i * kPreTile;
     return !WIN || place >= t.sink_keys || place + kPreTile <= t.sink_keys;
   };
   auto plain_tile = [&](const PrefillTile& t, int i) {
@@ -343,6 +370,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       const int len = b < p.batch ? length_of(b) : 0;
       reach = len > 0 ? (len - 1) / tier_len + 1 : 0;
       count = len > 0 ? (len - 1) / tpc + 1 : 0;
+      if (CUT) count *= p.most_parts;
     };
     int my_reach = 0, my_count = 0, tiers = 0;  // of sequence `lane`
     unsigned blocks = 0;
@@ -362,16 +390,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     int from = 0;                                            // where the last block was found: ranks only rise
     int pair0 = 0, n_pairs = min(p.pairs, p.pairs_at_once);  // the group of heads
     unsigned rank0 = 0;                                      // its first rank (the launch keeps ranks below 2^30)
-    bool more = true, long_before = false;
+    bool more = true, long_before = false, ok = true, again = false;  // again, CUT: a number that stands for nothing
+    if (CUT && cta == 0 && lane == 0) p.cuts[0].step = static_cast<int>(blocks * p.pairs);
     for (int k = 0; more; ++k) {
-      if (!warp_wait(&bar.tile_empty[k % kPreRing], ((k / kPreRing) & 1) ^ 1, wc, W_PRE_TILE_EMPTY)) break;
+      ok = ok && warp_wait(&bar.tile_empty[k % kPreRing], ((k / kPreRing) & 1) ^ 1, wc, W_PRE_TILE_EMPTY);
       // behind a long tile the next one is only taken once the tile before it is done: it goes to who is free
-      if (k >= 2 && long_before &&
-          !warp_wait(&bar.tile_empty[(k - 2) % kPreRing], ((k - 2) / kPreRing) & 1, wc, W_PRE_TILE_EMPTY))
-        break;
+      if (k >= 2 && long_before)
+        ok = ok && warp_wait(&bar.tile_empty[(k - 2) % kPreRing], ((k - 2) / kPreRing) & 1, wc, W_PRE_TILE_EMPTY);
+      if (!CUT && !ok) break;  // CUT: all numbers are taken, so that the join knows what each is
       unsigned taken = 0;
-      if (k > 0 && lane == 0) taken = atomicAdd(p.work, 1u);
-      const unsigned rank = k == 0 ? cta : G + __shfl_sync(~0u, taken, 0);
+      if ((k > 0 || again) && lane == 0) taken = atomicAdd(p.work, 1u);
+      const unsigned rank = k == 0 && !again ? cta : G + __shfl_sync(~0u, taken, 0);
       while (rank >= rank0 + blocks * n_pairs && pair0 + n_pairs < p.pairs) {  // on to the next group
         rank0 += blocks * n_pairs;
         pair0 += n_pairs;
@@ -409,13 +438,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         --tier;
       }
       PrefillTile t = {};
+      PrefillCut cut = {};
       t.bad_lo = INT_MAX, t.bad_hi = -1;
       more = seq >= 0;
+      again = false;
       if (more) {
         int first, last;
         sequence_rows(p.cu, seq, p.seq_len, p.M, first, last);
         t.row0 = first;
         t.len = last - first;
+        const int part = CUT ? in % p.most_parts : 0;
+        if (CUT) in /= p.most_parts;
         t.tok0 = (!p.causal ? in : p.flat ? (t.len - 1) / tpc - in : tier) * tpc;
         if (WIN) {
           int first_k = first, last_k = last;
@@ -426,6 +459,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           t.tok0 += shift;
           stream_of(t.tok0, t.len, t);
         }
+        if (CUT) {
+          // part i of c: tiles n i / c .. n (i + 1) / c - 1; query tile s takes part in those that begin before its last key
+          const int n = max(t.n0, t.n1), c = min(p.most_parts, (n - 1) / kPrePartTiles + 1);
+          const int begin = static_cast<int>(static_cast<long long>(n) * part / c),
+                    end = static_cast<int>(static_cast<long long>(n) * (part + 1) / c);
+          auto taking_part = [&](int own) { return own > 0 ? static_cast<int>((static_cast<long long>(own) * c - 1) / n) + 1 : 0; };
+          again = part >= c;
+          t.place0 = begin * kPreTile;
+          t.part = c > 1 ? static_cast<int>(rank) : -1;
+          if (c > 1 && part == 0) {
+            cut.parts[0] = taking_part(t.n0), cut.parts[1] = taking_part(t.n1), cut.step = n_pairs;
+            cut.row = t.q_row0 + t.tok0, cut.tokens = t.len - t.tok0;
+          }
+          t.n0 = min(max(t.n0 - begin, 0), end - begin), t.n1 = min(max(t.n1 - begin, 0), end - begin);
+        }
         const int packs = p.group / p.hp;
         t.kvh = pair / packs;
         t.head0 = t.kvh * p.group + (pair - t.kvh * packs) * p.hp;
@@ -435,9 +483,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
           t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
         }
+        if (CUT && lane == 0) {
+          cut.head0 = t.head0;
+          p.cuts[1 + rank] = cut;
+        }
+        if (CUT && again) {
+          --k;  // the next number in its place
+          continue;
+        }
         long_before = max(t.n0, t.n1) >= 4;
       }
-      if (lane == 0) {
+      if (ok && lane == 0) {
         bar.tile[k % kPreRing] = t;
         mbar_arrive(&bar.tile_full[k % kPreRing]);
       }
@@ -986,6 +1042,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         tc_fence_after();
         const volatile PrefillTile& said = bar.tile[k % kPreRing];
         const int bad_lo = said.bad_lo, bad_hi = said.bad_hi;
+        const int number = CUT ? said.part : -1;
+        float* own_part = nullptr;  // CUT: where this row's columns go as they are
+        if (CUT && number >= 0) {
+          float* at = p.parts + static_cast<long long>(number) * kPrePartFloats + s * kPrePartRows;
+          own_part = at + row * 4;
+          at += kPreTile * kHeadDim + row;
+          at[0] = m, at[kPreTile] = mx, at[2 * kPreTile] = l;
+#pragma unroll 1
+          for (int d = 0; d < kHeadDim; d += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_tmem + d, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 16; h += 4)
+              *reinterpret_cast<uint4*>(own_part + (d + h) * kPreTile) = make_uint4(o[h], o[h + 1], o[h + 2], o[h + 3]);
+          }
+        }
         float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;  // E4M3: O is held at m - 7, l at mx
         if (WIN && l == 0.f) inv = 0.f;  // a row that sees nothing
         const uint64_t inv2 = f2(inv, inv);
@@ -1005,7 +1078,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         __nv_bfloat16* dst = p.O + static_cast<long long>(row_zero + first + tok_first) * p.ldo +
                              static_cast<long long>(t.head0 + head_first) * kHeadDim + piece * 8;
 #pragma unroll 1
-        for (int j = 0; j < kHeadDim; j += T::kOutCols) {
+        for (int j = CUT && number >= 0 ? kHeadDim : 0; j < kHeadDim; j += T::kOutCols) {
 #pragma unroll
           for (int h = 0; h < T::kOutCols; h += 32) {
             uint32_t o[32];
@@ -1056,7 +1129,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
               const float y = FP8 ? __half2float(__ushort_as_half(__bfloat16_as_ushort(raw))) : __bfloat162float(raw);
               if (!isfinite(y)) sum += y;
             }
-            if (!isfinite(sum)) mine[d] = __float2bfloat16_rn(sum);
+            if (isfinite(sum)) continue;
+            if (CUT && number >= 0) own_part[(d >> 2) * (4 * kPreTile) + (d & 3)] = sum;
+            else mine[d] = __float2bfloat16_rn(sum);
           }
         }
       }
@@ -1071,6 +1146,55 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && bar.abort_flag != 0) record_failure(p.status, bar.abort_flag, 0);
+}
+
+// The parts of units, in their order: blocks (number, query tile, quarter of the columns) of a thread for each row.  A value that
+// is not finite counts as it is, whatever the weight of its part.
+template <bool FP8>
+__global__ void __launch_bounds__(kPreTile) attention_prefill_join_kernel(const __grid_constant__ PrefillJoinParams p) {
+  griddep_wait();
+  const int number = blockIdx.x, s = blockIdx.y, d0 = blockIdx.z * 32, row = threadIdx.x;
+  if (number >= p.cuts[0].step) return;
+  const PrefillCut cut = p.cuts[1 + number];
+  const int parts = cut.parts[s], row_tok = row / p.hp, tok = s * p.tq + row_tok;
+  if (parts == 0 || row_tok >= p.tq || tok >= cut.tokens) return;
+  const float* first = p.parts + static_cast<long long>(number) * kPrePartFloats + s * kPrePartRows;
+  const long long apart = static_cast<long long>(cut.step) * kPrePartFloats;
+  float m = kPreNone, mx = kPreNone, l = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float* at = first + i * apart + kPreTile * kHeadDim + row;
+    m = fmaxf(m, at[0]);
+    if (FP8) mx = fmaxf(mx, at[kPreTile]);
+  }
+  float o[32];
+#pragma unroll
+  for (int h = 0; h < 32; ++h) o[h] = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < parts; ++i) {
+    const float* at = first + i * apart;
+    const float* own = at + kPreTile * kHeadDim + row;
+    const float down = ex2(own[0] - m);
+    l += own[2 * kPreTile] * (FP8 ? ex2(own[kPreTile] - mx) : down);
+    float4 v[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) v[h] = *reinterpret_cast<const float4*>(at + (d0 + h * 4) * kPreTile + row * 4);
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      o[h * 4] = isfinite(v[h].x) ? fmaf(v[h].x, down, o[h * 4]) : o[h * 4] + v[h].x;
+      o[h * 4 + 1] = isfinite(v[h].y) ? fmaf(v[h].y, down, o[h * 4 + 1]) : o[h * 4 + 1] + v[h].y;
+      o[h * 4 + 2] = isfinite(v[h].z) ? fmaf(v[h].z, down, o[h * 4 + 2]) : o[h * 4 + 2] + v[h].z;
+      o[h * 4 + 3] = isfinite(v[h].w) ? fmaf(v[h].w, down, o[h * 4 + 3]) : o[h * 4 + 3] + v[h].w;
+    }
+  }
+  float inv = (FP8 ? ex2((m - kPreLift) - mx) : 1.f) / l;
+  if (l == 0.f) inv = 0.f;  // a row that sees nothing
+  __nv_bfloat16* to = p.O + static_cast<long long>(cut.row + tok) * p.ldo +
+                      static_cast<long long>(cut.head0 + row - row_tok * p.hp) * kHeadDim + d0;
+#pragma unroll
+  for (int h = 0; h < 32; h += 8)
+    *reinterpret_cast<uint4*>(to + h) =
+        make_uint4(pack_bf16x2(o[h] * inv, o[h + 1] * inv), pack_bf16x2(o[h + 2] * inv, o[h + 3] * inv),
+                   pack_bf16x2(o[h + 4] * inv, o[h + 5] * inv), pack_bf16x2(o[h + 6] * inv, o[h + 7] * inv));
 }
 
 }  // namespace fl

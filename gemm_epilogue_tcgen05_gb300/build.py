@@ -45,7 +45,7 @@ def _deps():
 # Kernels whose warps share out the registers that they are launched with: with any other number than the one their
 # source counts on they would not start.  Source file: (kernel, file and name of the constant).
 REGISTERS = {f: ("attention_prefill_kernel", "prefill_attention_kernel.cuh", "kPreRegs")
-             for f in ("k_attention_prefill.cu", "k_attention_prefill_window.cu")}
+             for f in ("k_attention_prefill.cu", "k_attention_prefill_window.cu", "k_attention_prefill_parts.cu")}
 
 
 def check_registers(src: str, ptxas: str) -> None:

@@ -442,12 +442,19 @@ FL_API int attention_decode_window(const void* Q, const void* k_pages, const voi
  * j < sinks.  A row that sees no key (i < 0) gets zeros.  window and sinks may be longer than any sequence;
  * negative ones are FL_ERR_INVALID_ARG, and so are M_k == 0 with M > 0, cu_seqlens_k without cu_seqlens, and
  * M_k != M without cu_seqlens_k.  The workspace is that of attention_prefill for M_k rows; other
- * arguments, what may hold NaN, roundings and errors are those of attention_prefill. */
+ * arguments, what may hold NaN, roundings and errors are those of attention_prefill.
+ * scratch (may be NULL; 16-byte aligned, any contents): with cu_seqlens_k, where few tokens meet many keys, their
+ * attention is cut along the keys, and the parts lie here while the call runs: it takes
+ * fl_attention_prefill_window_scratch_bytes of the same arguments (0: not worth it); with less nothing is cut.  Two calls
+ * that may overlap on the GPU need one each. */
+FL_API size_t fl_attention_prefill_window_scratch_bytes(int M, int M_k, int batch, int n_heads, int n_kv_heads, int window,
+                                                        int sinks);
 FL_API int attention_prefill_window(const void* Q, const void* K, const void* V, const float* k_scale,
                                     const float* v_scale, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k,
                                     void* O, int M, int M_k, int batch, int n_heads, int n_kv_heads, int head_dim,
                                     int seq_len, int64_t ldq, int64_t ldkv, int64_t lds, int64_t ldo, float scale,
                                     int window, int sinks, int kv_dtype, void* workspace, size_t workspace_bytes,
+                                    void* scratch, size_t scratch_bytes,
                                     void* stream);
 
 /* fused_linear_gelu (bf16) on HOST buffers: copies in, GEMM + epilogue, copies out.

@@ -32,7 +32,7 @@ DECODE = dict(Q=A, kp=A, vp=A, kps=A, vps=A, table=A, lens=A, O=A, batch=4, head
               ws=A, bytes=1 << 30, stream=None)
 PREFILL = dict(Q=A, K=A, V=A, ks=None, vs=None, cu=A, cu_k=A, O=A, M=10, M_k=30, batch=2, heads=8, n_kv=2, head_dim=128,
                seq_len=0, ldq=1024, ldkv=256, lds=0, ldo=1024, scale=F(0.1), window=10, sinks=2, kv=1, ws=A, bytes=1 << 30,
-               stream=None)
+               scratch=None, scratch_bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("status,changes", [
@@ -62,6 +62,7 @@ def test_decode_checks(lib, status, changes):
     (INVALID, dict(kv=2, ks=A, vs=A, lds=1)), (ALIGNMENT, dict(Q=P(0x10008))), (ALIGNMENT, dict(ldkv=260)),
     (ALIGNMENT, dict(cu_k=P(0x10002))), (ALIGNMENT, dict(ws=P(0x10020))), (WORKSPACE, dict(ws=None)),
     (WORKSPACE, dict(bytes=100)), (WORKSPACE, dict(kv=2, ks=A, vs=A, lds=2, bytes=512 + 10 * 2 * 516)),
+    (ALIGNMENT, dict(scratch=P(0x10008), scratch_bytes=1 << 20)),
     (OK, dict(M=0, Q=None)), (OK, dict(heads=0)), (OK, dict(batch=0))])
 def test_prefill_checks(lib, status, changes):
     assert call(lib.attention_prefill_window, PREFILL, **changes) == status

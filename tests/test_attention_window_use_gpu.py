@@ -174,6 +174,113 @@ def test_prefill_window_serves_on_after_waits_that_ran_out(fp8):
         assert fl.check_device_status(ws) == fl.FL_OK
 
 
+# ---------------------------------------------------------------- few queries behind many keys, cut along these
+LONG = [([33], [5000]), ([1], [1700]), ([70, 1, 0, 64], [3000, 1, 900, 2500]), ([5, 300], [4000, 200]), ([200], [130 * 128])]
+
+
+def space_of(q, k, lens, window, sinks):
+    return fl.load().fl_attention_prefill_window_scratch_bytes(q.shape[0], k.shape[0], len(lens), q.shape[1] // D, k.shape[1] // D,
+                                                               window, sinks)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2100, 100), (1000, 0)])
+@pytest.mark.parametrize("heads,kv", [(8, 2), (4, 4), (48, 1)])
+@pytest.mark.parametrize("lens,lens_k", LONG, ids=lambda x: "-".join(map(str, x)))
+def test_prefill_parts_match_the_definition(lens, lens_k, heads, kv, window, sinks, fp8):
+    """Also queries in front of the first key (5 of 300 behind 200), a sequence without rows, a key tile that ends inside."""
+    q = rows_of(sum(lens) + 3, heads, seed=121)
+    k, v, ks, vs = keys_of(sum(lens_k) + 5, kv, fp8, seed=122)
+    assert space_of(q, k, lens, window, sinks) > 0 or heads == 48 or 0 < window < 2000 or sum(lens) > 300
+    out = torch.full_like(q, 7.0)
+    call = dict(cu_seqlens=cu(lens), cu_seqlens_k=cu(lens_k), window=window, sinks=sinks, k_scale=ks, v_scale=vs)
+    ws = fl.attention_prefill_workspace(k.shape[0], kv, fp8)
+    for _ in range(2):
+        fl.attention_prefill_window(q, k, v, O=out, workspace=ws, **call)
+        check_prefill(q, k, v, ks, vs, lens, out, window, sinks, lens_k)
+        assert (out[sum(lens):] == 7.0).all()
+    assert torch.equal(fl.attention_prefill_window(q, k, v, **call)[:sum(lens)], out[:sum(lens)])
+
+
+def test_prefill_parts_are_used():
+    """What the cases above count on; one window as long as a few tiles, and many units, stay whole."""
+    def space(m, m_k, batch, heads, kv, window=0, sinks=0):
+        return fl.load().fl_attention_prefill_window_scratch_bytes(m, m_k, batch, heads, kv, window, sinks)
+    assert space(33, 5000, 1, 8, 2) > 0 and space(1, 2000, 1, 8, 2) > 0 and space(512, 5000, 1, 4, 4, 3000, 10) > 0
+    assert space(33, 5000, 1, 8, 2, 500, 4) == 0 and space(4096, 8000, 2, 32, 8) == 0 and space(33, 1500, 1, 8, 2) == 0
+    assert space(0, 10, 1, 8, 2) == 0 and space(10, 0, 1, 8, 2) == 0 and space(10, 10, 0, 8, 2) == 0 and space(9, 9, 1, 8, 3) == 0
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 30, 2.0 ** -30])
+def test_prefill_parts_of_very_different_scales(scale):
+    """E4M3: a part whose values are far larger or smaller than the others', and one of zeros."""
+    q = rows_of(40, 8, seed=123)
+    k, v, ks, vs = keys_of(5000, 2, True, seed=124)
+    vs[1000:2000] *= scale
+    vs[2500:3700] = 0
+    out = fl.attention_prefill_window(q, k, v, cu_seqlens=cu([40]), cu_seqlens_k=cu([5000]), k_scale=ks, v_scale=vs)
+    check_prefill(q, k, v, ks, vs, [40], out, lens_k=[5000])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_prefill_parts_values_that_are_not_finite(bad, fp8):
+    """In a value that all rows see, in one that the last rows see, and behind them all."""
+    q = rows_of(60, 8, seed=125)
+    k, v, ks, vs = keys_of(5000, 2, fp8, seed=126)
+    call = dict(cu_seqlens=cu([60]), cu_seqlens_k=cu([4960]))
+    want = fl.attention_prefill_window(q, k, v, k_scale=ks, v_scale=vs, **call)
+    for at, seen in ((1234, 0), (4950, 50), (4965, 60)):  # key 4900 + r is row r's own
+        if fp8:
+            scales = vs.clone()
+            scales[at, 1] = bad
+            got = fl.attention_prefill_window(q, k, v, k_scale=ks, v_scale=scales, **call)
+        else:
+            values = v.clone()
+            values[at, D + 5] = bad
+            got = fl.attention_prefill_window(q, k, values, **call)
+        first = got.view(60, 8, D)[:, :4]
+        assert torch.equal(first, want.view(60, 8, D)[:, :4])  # the other kv head's
+        mine = got.view(60, 8, D)[:, 4:]
+        assert torch.isfinite(mine[:seen]).all()
+        assert seen == 60 or (~torch.isfinite(mine[seen:, :, 5])).all()
+        if not fp8 and seen < 60:
+            assert torch.isfinite(mine[seen:, :, :5]).all() and torch.isfinite(mine[seen:, :, 6:]).all()
+            assert torch.isnan(mine[seen:, :, 5]).all() if bad != bad else (mine[seen:, :, 5] == bad).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_parts_captured_and_replayed_with_other_offsets(fp8):
+    q = rows_of(100, 8, seed=127)
+    k, v, ks, vs = keys_of(6000, 2, fp8, seed=128)
+    offsets, offsets_k = cu([40, 60]), cu([3000, 3000])
+    out = torch.empty_like(q)
+    ws = fl.attention_prefill_workspace(6000, 2, fp8)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fl.attention_prefill_window(q, k, v, cu_seqlens=offsets, cu_seqlens_k=offsets_k, k_scale=ks, v_scale=vs, O=out, workspace=ws)
+    for lens, lens_k in (([40, 60], [3000, 3000]), ([1, 99], [5800, 200]), ([100, 0], [100, 5000]), ([64, 36], [10, 5990])):
+        offsets.copy_(cu(lens)), offsets_k.copy_(cu(lens_k))
+        out.fill_(3)
+        g.replay()
+        check_prefill(q, k, v, ks, vs, lens, out, lens_k=lens_k)
+
+
+def test_prefill_parts_of_two_calls_at_once():
+    q = rows_of(60, 8, seed=131)
+    k, v, _, _ = keys_of(5000, 2, False, seed=132)
+    calls = [dict(cu_seqlens=cu([60]), cu_seqlens_k=cu([n])) for n in (5000, 3000)]
+    wants = [fl.attention_prefill_window(q, k, v, **c) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate(calls):
+            got[i].append(fl.attention_prefill_window(q, k, v, stream=streams[i], **c))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for outs, w in zip(got, wants) for o in outs)
+
+
 # ---------------------------------------------------------------- the first calls of a process
 FIRST = """
 import sys
