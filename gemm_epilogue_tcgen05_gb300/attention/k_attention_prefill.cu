@@ -46,8 +46,11 @@ int heads_of_tile(int group) {
   while (group % hp != 0) --hp;
   return hp;
 }
-// Blocks of per_cta tokens, at most: the lengths are on the device.
-long long packed_blocks(int M, int batch, long long per_cta) { return M / per_cta + batch; }
+// Blocks of per_cta tokens, at most (the lengths are on the device): a sequence of n has (n - 1) / per_cta + 1.
+long long packed_blocks(int M, int batch, long long per_cta) {
+  const int some = std::min(M, batch);
+  return (M - some) / per_cta + some;
+}
 
 // Parts that each unit may be cut into where few units go over many keys, 1: none.  A part costs a unit's output, 128 KB into the
 // scratch buffer and out of it, and a second kernel joins them, so they pay where SMs would be idle and units be long.  Measured,
@@ -193,6 +196,7 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
   if (cut) {
     p.flat = 1;
     p.most_parts = most_parts;
+    p.numbers = static_cast<int>(units * most_parts);
     p.cuts = static_cast<PrefillCut*>(scratch);
     p.parts = reinterpret_cast<float*>(p.cuts + 1 + units * most_parts);
   }

@@ -126,7 +126,7 @@ struct alignas(128) PrefillParams {
   CUtensorMap map_k32, map_v32;  // WIN: the same as map_k and map_v, box {64, 32}
   const int* cu_k;               // WIN: offsets of the keys' rows, of which there are M_k; null: those of the queries
   int M_k, window, sinks;        // WIN; a window of 0 hides nothing
-  int most_parts;                // CUT: numbers that a unit has
+  int most_parts, numbers;       // CUT: numbers that a unit has, and how many there is room for
   float* parts;                  // CUT: [numbers][kPrePartFloats]
   PrefillCut* cuts;              // CUT: [numbers], and in front of them one whose `step` says how many there are
   __nv_bfloat16* O;
@@ -366,11 +366,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
       t.n0 = tiles(tok0 + p.tq);
       t.n1 = tok0 + p.tq >= len_k ? 0 : tiles(tok0 + tpc);
     };
+    int parts_here = CUT ? p.most_parts : 1;
     auto measure = [&](int b, int& reach, int& count) {  // tiers of a sequence, and its blocks
       const int len = b < p.batch ? length_of(b) : 0;
       reach = len > 0 ? (len - 1) / tier_len + 1 : 0;
       count = len > 0 ? (len - 1) / tpc + 1 : 0;
-      if (CUT) count *= p.most_parts;
+      if (CUT) count *= parts_here;
     };
     int my_reach = 0, my_count = 0, tiers = 0;  // of sequence `lane`
     unsigned blocks = 0;
@@ -384,6 +385,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     }
     tiers = __reduce_max_sync(~0u, tiers);
     blocks = __reduce_add_sync(~0u, blocks);
+    if (CUT && static_cast<unsigned long long>(blocks) * p.pairs > static_cast<unsigned>(p.numbers)) {
+      // offsets that give rows to several sequences: more units than rows can make, and they stay whole
+      blocks /= parts_here, my_count /= parts_here;
+      parts_here = 1;
+    }
     if (p.flat) tiers = 1;
     int tier = tiers - 1;
     unsigned before = 0;                                     // blocks before sequence `from` of this tier
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
     int pair0 = 0, n_pairs = min(p.pairs, p.pairs_at_once);  // the group of heads
     unsigned rank0 = 0;                                      // its first rank (the launch keeps ranks below 2^30)
     bool more = true, long_before = false, ok = true, again = false;  // again, CUT: a number that stands for nothing
-    if (CUT && cta == 0 && lane == 0) p.cuts[0].step = static_cast<int>(blocks * p.pairs);
+    if (CUT && cta == 0 && lane == 0) p.cuts[0].step = parts_here > 1 ? static_cast<int>(blocks * p.pairs) : 0;
     for (int k = 0; more; ++k) {
       ok = ok && warp_wait(&bar.tile_empty[k % kPreRing], ((k / kPreRing) & 1) ^ 1, wc, W_PRE_TILE_EMPTY);
       // behind a long tile the next one is only taken once the tile before it is done: it goes to who is free
@@ -447,8 +453,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         sequence_rows(p.cu, seq, p.seq_len, p.M, first, last);
         t.row0 = first;
         t.len = last - first;
-        const int part = CUT ? in % p.most_parts : 0;
-        if (CUT) in /= p.most_parts;
+        const int part = CUT ? in % parts_here : 0;
+        if (CUT) in /= parts_here;
         t.tok0 = (!p.causal ? in : p.flat ? (t.len - 1) / tpc - in : tier) * tpc;
         if (WIN) {
           int first_k = first, last_k = last;
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
         }
         if (CUT) {
           // part i of c: tiles n i / c .. n (i + 1) / c - 1; query tile s takes part in those that begin before its last key
-          const int n = max(t.n0, t.n1), c = min(p.most_parts, (n - 1) / kPrePartTiles + 1);
+          const int n = max(t.n0, t.n1), c = min(parts_here, (n - 1) / kPrePartTiles + 1);
           const int begin = static_cast<int>(static_cast<long long>(n) * part / c),
                     end = static_cast<int>(static_cast<long long>(n) * (part + 1) / c);
           auto taking_part = [&](int own) { return own > 0 ? static_cast<int>((static_cast<long long>(own) * c - 1) / n) + 1 : 0; };
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) attention_prefill_kernel(const
           t.n0 = p.causal ? (min(t.tok0 + p.tq, t.len) - 1) / kPreTile + 1 : all;
           t.n1 = t.tok0 + p.tq >= t.len ? 0 : p.causal ? (min(t.tok0 + tpc, t.len) - 1) / kPreTile + 1 : all;
         }
-        if (CUT && lane == 0) {
+        if (CUT && parts_here > 1 && lane == 0) {
           cut.head0 = t.head0;
           p.cuts[1 + rank] = cut;
         }

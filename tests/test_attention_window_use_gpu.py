@@ -266,6 +266,33 @@ def test_prefill_parts_captured_and_replayed_with_other_offsets(fp8):
         check_prefill(q, k, v, ks, vs, lens, out, lens_k=lens_k)
 
 
+def test_prefill_parts_bad_offsets_stay_inside():
+    """Offsets that give the same rows to many sequences make more units than there is room for: they stay whole, and nothing
+    behind the scratch buffer or outside the rows is written."""
+    heads, kv, m, m_k, batch = 8, 2, 60, 5000, 9
+    q = rows_of(m, heads, seed=133)
+    k, v, _, _ = keys_of(m_k, kv, False, seed=134)
+    ws = fl.attention_prefill_workspace(m_k, kv, False)
+    size = fl.load().fl_attention_prefill_window_scratch_bytes(m, m_k, batch, heads, kv, 0, 0)
+    assert size > 0
+    scratch = torch.full((size + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((m + 8, heads * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    for rows in ([0, 60] * 5, [0, 60, 0, 60, -5, 70, 3, 1 << 30, 0, 60], [0, 1, 2, 3, 4, 5, 6, 7, 8, 60]):
+        for keys in ([0, 5000] * 5, [0, 5000, -9, 5000, 0, 1 << 30, 7, 5000, 0, 4000]):
+            offsets, offsets_k = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (rows, keys))
+            st = fl.load().attention_prefill_window(
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, offsets.data_ptr(), offsets_k.data_ptr(), out.data_ptr(), m,
+                m_k, batch, heads, kv, D, 1, heads * D, kv * D, 0, heads * D, D ** -0.5, 0, 0, fl.FL_BF16, ws.data_ptr(),
+                ws.numel(), scratch.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+            assert st == fl.FL_OK
+            torch.cuda.synchronize()
+            assert (scratch[size:] == 0x5A).all() and (out[m:] == 7.0).all()
+    # the workspace serves on, with the scratch buffer as it is
+    offsets, offsets_k = cu([60]), cu([5000])
+    want = fl.attention_prefill_window(q, k, v, cu_seqlens=offsets, cu_seqlens_k=offsets_k)
+    assert torch.equal(fl.attention_prefill_window(q, k, v, cu_seqlens=offsets, cu_seqlens_k=offsets_k, workspace=ws), want)
+
+
 def test_prefill_parts_of_two_calls_at_once():
     q = rows_of(60, 8, seed=131)
     k, v, _, _ = keys_of(5000, 2, False, seed=132)
