@@ -4,7 +4,7 @@
 //
 // What bounds it: the cache is read once, 144 bytes for a token and kv head, at the memory's rate if the instructions for
 // these 256 codes are few enough: a logic instruction takes two cycles of a scheduler, and an SM has some 25 cycles of each
-// of its four for a token and head.  64 sequences of 2048-8192 tokens, 32/8 heads: 80 us, 4500 GB/s; some 345 instructions for
+// of its four for a token and head.  64 sequences of 2048-8192 tokens, 32/8 heads: 81 us, 4450 GB/s; some 345 instructions for
 // 16 tokens and a head, 0.55 of them in a cycle of a scheduler.
 //
 // Codes.  A code xor 8, u = code + 8, is an fp16 number u 2^-24 (a denormal one) as it stands in the low bits of a half, and
@@ -12,7 +12,11 @@
 // the output's odd dimensions for V.
 //   q . k = sum_g s_g (sum_d q_d u_d - 8 sum_d q_d): products of 32 columns with a scale of their own.
 //   o_d = sum_j w_j u_jd - 8 sum_j w_j: weights with the scale of the value's group in them, w_j = p_j s_jg, and eight times
-//   their sum by one more product for each group, of eights.
+//   their sum by one more product for each group, of eights: in its even rows as the even dimensions' codes stand, in its odd ones
+//   as the odd dimensions'.  A product of denormal numbers is aligned by the exponent of their format, so sums of these codes keep
+//   2^-14 (even) and 2^-18 (odd) of the largest weight, not fp32's 2^-24, and much of what they drop leaves with eights that are
+//   aligned alike (one sum of eights for both: 2^-12.6 of the weights' sum where the heavy tokens' codes are zero, now 2^-13.8;
+//   a register pair for each group, 1 % of the time).
 // A query head is scaled by a power of two to fp16's upper range, where its bf16 values are exact down to 2^-25 of the largest.
 // p_j is 2^(x_j + e_j - m'), 2^e_j next above the token's largest scale and m' the running maximum of that exponent; it is
 // rounded to fp16, and its product with s_jg 2^-e_j (at most 1) again.  Where the four scales of a token lie 2^12 and more
@@ -24,7 +28,7 @@
 // 16 bits, 4 codes each.  The maxima m and m' rise only when a logit passes them by more than 8.
 //
 // Work.  Units (decode_attention_common.cuh) are 128 tokens, a stage of the CTA's ring; each of four warps takes 32 of them.  A
-// fifth warp walks ahead and fills the stages by tensor copies, one for each 32, 16 or 8 tokens of a page and tensor (the codes with
+// fifth warp walks ahead and fills the stages by tensor copies, one for each 32, 16 or 8 tokens of a page and tensor (codes with
 // the 64-byte swizzle, so that eight rows of a chunk meet in no bank), and bulk copies for the scales; caches that these
 // do not fit are copied by 16 bytes.  With a ring of its own for each warp, filled by itself, finding the pages and issuing the
 // copies took 112 of 400 instructions for 16 tokens and a head: 105.7 us for these 64 sequences, 91 with the fifth warp.  In the
@@ -357,7 +361,8 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
     // columns in which this lane met a scale of V that is not finite.
     said = (said & kFailed) | (seg.bad ? kBad : 0u);
     float o[8][4];
-    uint64_t eights[kInt4Groups];  // 8 sum w of a group, heads 2q and 2q + 1, in the units of o
+    // 8 sum w of a group, heads 2q and 2q + 1, in the units of o's even dimensions and in those of its odd ones
+    uint64_t eights[kInt4Groups], eights16[kInt4Groups];
     float m[2], mv[2];
     uint64_t l;
 #pragma unroll
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < kInt4Groups; ++c) eights[c] = 0;
+    for (int c = 0; c < kInt4Groups; ++c) eights[c] = eights16[c] = 0;
     m[0] = m[1] = mv[0] = mv[1] = kDecNone;
     l = 0;
 
@@ -503,7 +508,10 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           }
           l = f2_mul(l, f2(down[0], down[1]));
 #pragma unroll
-          for (int c = 0; c < kInt4Groups; ++c) eights[c] = f2_mul(eights[c], f2(down_o[0], down_o[1]));
+          for (int c = 0; c < kInt4Groups; ++c) {
+            eights[c] = f2_mul(eights[c], f2(down_o[0], down_o[1]));
+            eights16[c] = f2_mul(eights16[c], f2(down_o[0], down_o[1]));
+          }
         }
         // ---- weights, and O^T += V^T P^T, of a group of 32: dimensions 4 g and 4 g + 2, then 4 g + 1 and 4 g + 3
         const uint64_t minus_m = f2(-m[0], -m[1]), minus_mv = f2(kDecLift - mv[0], kDecLift - mv[1]);
@@ -535,9 +543,10 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
                               int4_odd(hi >> 8, flip16), b0, b1);
             }
             float d[4];
-            mma_16816_first<true>(d, flip, flip, flip, flip, b[0], b[1]);
-            mma_16816<true>(d, flip, flip, flip, flip, b[2], b[3]);
+            mma_16816_first<true>(d, flip, flip16, flip, flip16, b[0], b[1]);
+            mma_16816<true>(d, flip, flip16, flip, flip16, b[2], b[3]);
             eights[c] = f2_add(eights[c], f2(d[0], d[1]));
+            eights16[c] = f2_add(eights16[c], f2(d[2], d[3]));
           }
         } else {
 #pragma unroll
@@ -557,9 +566,10 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
               const uint32_t top = pack_bf16x2(w0, w1);
               const uint32_t b[2] = {transpose8x8(top), transpose8x8(pack_bf16x2(w0 - bf16_lo(top), w1 - bf16_hi(top)))};
               float d[4];
-              mma_16816_first<false>(d, flip, flip, flip, flip, b[0], 0u);
-              mma_16816<false>(d, flip, flip, flip, flip, b[1], 0u);
+              mma_16816_first<false>(d, flip, flip16, flip, flip16, b[0], 0u);
+              mma_16816<false>(d, flip, flip16, flip, flip16, b[1], 0u);
               eights[c] = f2_add(eights[c], f2(d[0], d[1]));
+              eights16[c] = f2_add(eights16[c], f2(d[2], d[3]));
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 mma_16816<false>(o[c * 2], int4_even(v[r], flip), int4_even(v[r] >> 8, flip), 0u, 0u, b[k], 0u);
@@ -596,11 +606,12 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
         float* row = reinterpret_cast<float*>(mine) + h * kHeadDim;
 #pragma unroll
         for (int c = 0; c < kInt4Groups; ++c) {
-          float e[2];
+          float e[2], e16[2];
           f2_split(eights[c], e[0], e[1]);
-          const float less = e[i];
-          float4 four = make_float4((o[c * 2][i] - less) * kDecCode, fmaf(o[c * 2 + 1][i], 0.0625f, -less) * kDecCode,
-                                    (o[c * 2][i + 2] - less) * kDecCode, fmaf(o[c * 2 + 1][i + 2], 0.0625f, -less) * kDecCode);
+          f2_split(eights16[c], e16[0], e16[1]);
+          constexpr float kOdd = kDecCode / 16.f;
+          float4 four = make_float4((o[c * 2][i] - e[i]) * kDecCode, (o[c * 2 + 1][i] - e16[i]) * kOdd,
+                                    (o[c * 2][i + 2] - e[i]) * kDecCode, (o[c * 2 + 1][i + 2] - e16[i]) * kOdd);
           if ((no_number >> c & 1u) != 0) four = make_float4(NAN, NAN, NAN, NAN);
           *reinterpret_cast<float4*>(row + (((c * 8 + g) ^ (q * 2)) << 2)) = four;
         }

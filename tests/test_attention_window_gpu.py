@@ -103,6 +103,16 @@ def test_decode_over_4_bits_peaked_flat_and_large():
     check_decode(q, c, fl.attention_decode_window(q, *c.args(), **c.scales()))
 
 
+@pytest.mark.parametrize("std", [2.0, 4.0, 8.0])
+def test_decode_over_4_bits_heavy_tokens_with_small_codes(std):
+    """A few tokens have all the weight, and in many columns codes of zero: what is left of their codes + 8 and the eights."""
+    for seed in range(12):
+        c = AnyCache([16, 40, 100, 7, 33, 300, 12, 20, 2, 1], 1, 16, "int4", seed=140 + seed)
+        q = randn(10, 8 * D, seed=160 + seed, std=std)
+        out = fl.attention_decode_window(q, *c.args(), **c.scales())
+        check_decode(q, c, out)
+
+
 def test_decode_over_4_bits_entries_that_are_not_finite():
     """A value's group reaches its own 32 columns only, a key's the whole of its heads; other heads and sequences neither."""
     c = AnyCache([300, 300, 300], 2, 16, "int4", seed=14)

@@ -8,6 +8,8 @@ Attention: the allowances of attention_utils, of the keys that a row sees.  The 
 rounded to fp16, and its product with a group's scale again (2 * 2^-11 A, the second one at most 2^-25 2^7 of the largest
 weight times scale below fp16's normal range); its sums hold codes + 8, which are at most 15 where the code is 1 at least or
 stands for nothing, less 8 times the sum of the weights: fp32 sums over n keys, n 2^-24 * (15 + 8) sum_j p_j s_j each.
+Sums of products with codes, which are denormal numbers to the tensor cores, keep 2^-14 of the largest weight times
+scale (measured 2^-13.8 of their sum); the allowance for weights below fp16's range, 15 * 2^-17 of the largest, holds that.
 A logit's sums are over (code + 8) q: 130 * 2^-24 * (15 + 8) * scale sum_d |q_d| s_d.
 """
 import torch
