@@ -288,11 +288,10 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
         more = advance();
       }
     }
-    if (!ok) {
-      if (lane == 0) record_failure(p.status, W_DEC_EMPTY, stage);
-      for (int i = 0; i < T::kStages; ++i)  // leave no copy in flight: each stage's last one
-        if (round > 0 || i < stage) mbar_wait_quiet(&full[i], (i < stage ? round : round - 1) & 1, 1000000000);
-    }
+    if (!ok && lane == 0) record_failure(p.status, W_DEC_EMPTY, stage);
+    // Leave no copy in flight, each stage's last one: a warp that gave up waiting for it ends without it.
+    for (int i = 0; i < T::kStages; ++i)
+      if (round > 0 || i < stage) mbar_wait_quiet(&full[i], (i < stage ? round : round - 1) & 1, 1000000000);
     return;
   }
 
