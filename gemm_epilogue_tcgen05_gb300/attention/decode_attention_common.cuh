@@ -267,6 +267,13 @@ __device__ __forceinline__ DecodeOwners decode_owners(const DecodeParams& p, con
   return w;
 }
 
+// acc 2^(mv - m) / l as bf16.  mv - m is the power of V's scales, down to 2^-149: below 2^-100 it comes as two factors, for one
+// below 2^-126 would be flushed to zero, and the quotient lose bits before that.
+__device__ __forceinline__ uint2 decode_output(const float4& acc, float m, float mv, float l) {
+  const float e = mv - m, r = ex2(fmaxf(e, -100.f)) / l, rest = ex2(fminf(e + 100.f, 0.f));
+  return make_uint2(pack_bf16x2(acc.x * r * rest, acc.y * r * rest), pack_bf16x2(acc.z * r * rest, acc.w * r * rest));
+}
+
 // The pieces of a CTA's warps become one: finished, or a part of a cut (sequence, head).  stats [warp][head]: m, m', l and where
 // in shared memory the warp's piece is: o[head][128], chunks of 4 permuted by SWIZZLE times the head's pair.
 template <int WARPS, int HEADS, int SWIZZLE>
@@ -290,10 +297,7 @@ __device__ __forceinline__ void decode_merge(const DecodeParams& p, const uint8_
       acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
     if (w.whole) {
-      const float r = ex2(MV - M) / L;
-      uint2 out;
-      out.x = pack_bf16x2(acc.x * r, acc.y * r);
-      out.y = pack_bf16x2(acc.z * r, acc.w * r);
+      uint2 out = decode_output(acc, M, MV, L);
       if (seg.len == 0) out = make_uint2(0, 0);
       *reinterpret_cast<uint2*>(p.O + seg.b * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + lane * 4) = out;
     } else {
@@ -377,10 +381,7 @@ __device__ __forceinline__ void decode_join(const DecodeParams& p, const DecodeC
           }
         }
       }
-      const float r = ex2(MV - M) / L;
-      uint2 out;
-      out.x = pack_bf16x2(acc.x * r, acc.y * r);
-      out.y = pack_bf16x2(acc.z * r, acc.w * r);
+      uint2 out = decode_output(acc, M, MV, L);
       *reinterpret_cast<uint2*>(p.O + cuts.b[k] * p.ldo + static_cast<long long>(head0 + h) * kHeadDim + lane * 4) = out;
     }
   }
