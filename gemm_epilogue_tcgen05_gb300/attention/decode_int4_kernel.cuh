@@ -16,7 +16,9 @@
 //   as the odd dimensions'.  A product of denormal numbers is aligned by the exponent of their format, so sums of these codes keep
 //   2^-14 (even) and 2^-18 (odd) of the largest weight, not fp32's 2^-24, and much of what they drop leaves with eights that are
 //   aligned alike (one sum of eights for both: 2^-12.6 of the weights' sum where the heavy tokens' codes are zero, now 2^-13.8;
-//   a register pair for each group, 1 % of the time).
+//   1 % of the time).  The eights are taken off every 32 tokens: the tensor cores truncate a running sum, and the sum of u, 8 or so
+//   times the weights', would lose more with every product than the eights, rounded to nearest, take off (400000 tokens with
+//   like weights in one CTA: an error of 2.3 % of the output, now 0.16 %, its rounding).
 // A query head is scaled by a power of two to fp16's upper range, where its bf16 values are exact down to 2^-25 of the largest.
 // p_j is 2^(x_j + e_j - m'), 2^e_j next above the token's largest scale and m' the running maximum of that exponent; it is
 // rounded to fp16, and its product with s_jg 2^-e_j (at most 1) again.  Where the four scales of a token lie 2^12 and more
@@ -360,16 +362,12 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
     // columns in which this lane met a scale of V that is not finite.
     said = (said & kFailed) | (seg.bad ? kBad : 0u);
     float o[8][4];
-    // 8 sum w of a group, heads 2q and 2q + 1, in the units of o's even dimensions and in those of its odd ones
-    uint64_t eights[kInt4Groups], eights16[kInt4Groups];
     float m[2], mv[2];
     uint64_t l;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < kInt4Groups; ++c) eights[c] = eights16[c] = 0;
     m[0] = m[1] = mv[0] = mv[1] = kDecNone;
     l = 0;
 
@@ -506,13 +504,17 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
             for (int d = 0; d < 8; ++d) o[d][i] *= down_o[i], o[d][i + 2] *= down_o[i];
           }
           l = f2_mul(l, f2(down[0], down[1]));
-#pragma unroll
-          for (int c = 0; c < kInt4Groups; ++c) {
-            eights[c] = f2_mul(eights[c], f2(down_o[0], down_o[1]));
-            eights16[c] = f2_mul(eights16[c], f2(down_o[0], down_o[1]));
-          }
         }
         // ---- weights, and O^T += V^T P^T, of a group of 32: dimensions 4 g and 4 g + 2, then 4 g + 1 and 4 g + 3
+        // -8 sum w, heads 2q and 2q + 1: d in the units of o's even dimensions, then in those of its odd ones
+        const uint32_t less = flip ^ 0x80008000u, less16 = flip16 ^ 0x80008000u;
+        auto take_off = [](float (&even)[4], float (&odd)[4], const float (&d)[4]) {
+          const uint64_t d2 = f2(d[0], d[1]), d16 = f2(d[2], d[3]);
+          f2_split(f2_add(f2(even[0], even[1]), d2), even[0], even[1]);
+          f2_split(f2_add(f2(even[2], even[3]), d2), even[2], even[3]);
+          f2_split(f2_add(f2(odd[0], odd[1]), d16), odd[0], odd[1]);
+          f2_split(f2_add(f2(odd[2], odd[3]), d16), odd[2], odd[3]);
+        };
         const uint64_t minus_m = f2(-m[0], -m[1]), minus_mv = f2(kDecLift - mv[0], kDecLift - mv[1]);
 #pragma unroll
         for (int r = 0; r < T::kSubs * 2; ++r) {
@@ -542,10 +544,9 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
                               int4_odd(hi >> 8, flip16), b0, b1);
             }
             float d[4];
-            mma_16816_first<true>(d, flip, flip16, flip, flip16, b[0], b[1]);
-            mma_16816<true>(d, flip, flip16, flip, flip16, b[2], b[3]);
-            eights[c] = f2_add(eights[c], f2(d[0], d[1]));
-            eights16[c] = f2_add(eights16[c], f2(d[2], d[3]));
+            mma_16816_first<true>(d, less, less16, less, less16, b[0], b[1]);
+            mma_16816<true>(d, less, less16, less, less16, b[2], b[3]);
+            take_off(o[c * 2], o[c * 2 + 1], d);
           }
         } else {
 #pragma unroll
@@ -564,16 +565,15 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
               const float w0 = y[r * 2] * part, w1 = y[r * 2 + 1] * part;
               const uint32_t top = pack_bf16x2(w0, w1);
               const uint32_t b[2] = {transpose8x8(top), transpose8x8(pack_bf16x2(w0 - bf16_lo(top), w1 - bf16_hi(top)))};
-              float d[4];
-              mma_16816_first<false>(d, flip, flip16, flip, flip16, b[0], 0u);
-              mma_16816<false>(d, flip, flip16, flip, flip16, b[1], 0u);
-              eights[c] = f2_add(eights[c], f2(d[0], d[1]));
-              eights16[c] = f2_add(eights16[c], f2(d[2], d[3]));
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 mma_16816<false>(o[c * 2], int4_even(v[r], flip), int4_even(v[r] >> 8, flip), 0u, 0u, b[k], 0u);
                 mma_16816<false>(o[c * 2 + 1], int4_odd(v[r], flip16), int4_odd(v[r] >> 8, flip16), 0u, 0u, b[k], 0u);
               }
+              float d[4];
+              mma_16816_first<false>(d, less, less16, less, less16, b[0], 0u);
+              mma_16816<false>(d, less, less16, less, less16, b[1], 0u);
+              take_off(o[c * 2], o[c * 2 + 1], d);
             }
           }
         }
@@ -591,8 +591,7 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
     if (spoiled && lane == 0 && atomicCAS(p.status + ST_CODE, 0, static_cast<int>(FL_ERR_INVALID_ARG)) == 0)
       p.status[ST_DETAIL] = seg.b;
     const uint32_t no_number = __reduce_or_sync(~0u, said);  // bits 0-3
-    // o[t][i] with t = 2 group + odd: head 2q + (i & 1), dimension 32 group + 4 g + odd + 2 (i >> 1), still with 8 sum w in
-    // it, odd dimensions times 16.  Chunks of 4 dimensions, permuted by 2 q against bank conflicts.
+    // o[t][i] with t = 2 group + odd: head 2q + (i & 1), dimension 32 group + 4 g + odd + 2 (i >> 1), odd ones times 16.  Chunks of 4 dimensions, permuted by 2 q against bank conflicts.
     {
       float sums[2];
       f2_split(l, sums[0], sums[1]);
@@ -605,12 +604,9 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
         float* row = reinterpret_cast<float*>(mine) + h * kHeadDim;
 #pragma unroll
         for (int c = 0; c < kInt4Groups; ++c) {
-          float e[2], e16[2];
-          f2_split(eights[c], e[0], e[1]);
-          f2_split(eights16[c], e16[0], e16[1]);
           constexpr float kOdd = kDecCode / 16.f;
-          float4 four = make_float4((o[c * 2][i] - e[i]) * kDecCode, (o[c * 2 + 1][i] - e16[i]) * kOdd,
-                                    (o[c * 2][i + 2] - e[i]) * kDecCode, (o[c * 2 + 1][i + 2] - e16[i]) * kOdd);
+          float4 four = make_float4(o[c * 2][i] * kDecCode, o[c * 2 + 1][i] * kOdd, o[c * 2][i + 2] * kDecCode,
+                                    o[c * 2 + 1][i + 2] * kOdd);
           if ((no_number >> c & 1u) != 0) four = make_float4(NAN, NAN, NAN, NAN);
           *reinterpret_cast<float4*>(row + (((c * 8 + g) ^ (q * 2)) << 2)) = four;
         }

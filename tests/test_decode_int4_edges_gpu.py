@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gemm_epilogue_tcgen05_gb300 as fl
-from attention_utils import D, assert_within
+from attention_utils import BF16, D, assert_within
 from test_attention_window_gpu import STEP, check_decode, randn
 from window_utils import AnyCache, attend_window
 
@@ -81,3 +81,42 @@ def test_decode_over_e4m3_of_the_smallest_scales(power, lens):
     q = randn(len(lens), 12 * D, seed=11)
     check_small_values(q, c, fl.attention_decode_window(q, *c.args(), **c.scales()), -power)
     check_small_values(q, c, fl.attention_decode(q, *c.args(), **c.scales()), -power)
+
+
+# ---------------------------------------------------------------- long sums
+def shared(cache, batch):
+    """Many sequences with the tokens of one: each CTA walks most of a (sequence, head) by itself."""
+    return (cache.k, cache.v, cache.table.expand(batch, -1).contiguous(), cache.seq_lens.expand(batch).contiguous())
+
+
+def test_decode_over_4_bits_flat_attention_over_many_tokens():
+    """All weights are alike: these, and their products with the scales, are exact.  A sum of 16 products with a running sum r is
+    truncated to 2^-23 of the larger of |r| and what it adds, 16 * 15 weights times scale for the codes + 8 of one product,
+    and the sum of the eights is taken off once in two products (2^-24).  So a warp that walks a quarter of n tokens leaves
+    (n / 64) 1.25 2^-23 (max |r| + 480 s), 2^-27 1.25 (max |r| + 480 s) of the output for all four; values are random signs of
+    some 1, so |r| stays below 5 sqrt(n / 4).  (With all eights taken off at the end: 2 % of the output.)"""
+    n, kv, batch = 400000, 8, 64
+    c = AnyCache([n], kv, 64, "int4", seed=21)
+    q = torch.zeros(batch, 2 * kv * D, dtype=torch.bfloat16, device="cuda")
+    out = fl.attention_decode_window(q, *shared(c, batch), **c.scales()).view(batch, kv, 2, D).double()
+    ref = c.sequence(0)[1].mean(1)
+    s = c.value_scales(0)[1].amax(1)
+    tol = BF16 * ref.abs() + 1.25 * 2.0 ** -27 * (5 * (n / 4) ** 0.5 + 480 * s) + 2.0 ** -20 * ref.abs()
+    err = (out - ref[:, None]).abs()
+    assert (err <= tol[:, None]).all(), f"worst {(err / tol[:, None]).max():.3f} of the allowance"
+
+
+@pytest.mark.parametrize("n", [9000, 40000])
+def test_decode_over_4_bits_nearly_flat_attention_over_many_tokens(n):
+    """Over all elements: the output's rounding is 2^-8 / sqrt(3) of them at most, the two of the weights and their products with
+    scales 2^-11 each of values that average out as they do (a quarter of 2^-8), and what 16 products drop, 2^-14 of a weight
+    times scale, 2^-18 of the sum p s, and again for the running sums."""
+    kv, batch = 8, 64
+    c = AnyCache([n], kv, 64, "int4", seed=22)
+    q = randn(1, 2 * kv * D, seed=23, std=0.05).expand(batch, -1).contiguous()
+    out = fl.attention_decode_window(q, *shared(c, batch), **c.scales()).view(batch, 2 * kv, 1, D).double()
+    k, v = c.sequence(0)
+    ref = attend_window(q[0].double().view(2 * kv, 1, D), k, v, D ** -0.5, 0, 0, 0.0)[0]
+    s = c.value_scales(0)[1].mean()
+    err = (out - ref).square().mean().sqrt()
+    assert err <= BF16 * ref.square().mean().sqrt() + 2.0 ** -17 * s, f"{err:.3e} of outputs of {ref.square().mean().sqrt():.3e}"
