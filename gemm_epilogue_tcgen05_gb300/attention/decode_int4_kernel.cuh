@@ -405,7 +405,10 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
           uint32_t four[4] = {sv.x & 0xFFFFu, sv.x >> 16, sv.y & 0xFFFFu, sv.y >> 16};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (four[c] >= 0x7F80u) four[c] = 0, said |= 1u << c;  // reaches its own columns only, at the segment's end
+            if (four[c] >= 0x7F80u) {  // reaches its own columns only, at the segment's end; -0 is a zero
+              if (four[c] != 0x8000u) said |= 1u << c;
+              four[c] = 0;
+            }
           sv = make_uint2(four[0] | four[1] << 16, four[2] | four[3] << 16);
           ends();
           if (__any_sync(~0u, far())) said |= kSpread;

@@ -120,3 +120,20 @@ def test_decode_over_4_bits_nearly_flat_attention_over_many_tokens(n):
     s = c.value_scales(0)[1].mean()
     err = (out - ref).square().mean().sqrt()
     assert err <= BF16 * ref.square().mean().sqrt() + 2.0 ** -17 * s, f"{err:.3e} of outputs of {ref.square().mean().sqrt():.3e}"
+
+
+# ---------------------------------------------------------------- scales of -0
+def test_scales_of_minus_zero_are_zeros():
+    for spread in (False, True):
+        c = AnyCache([300, 700], 2, 16, "int4", seed=31)
+        g = torch.Generator().manual_seed(32)
+        if spread:
+            c.vs *= torch.exp2(torch.randint(-30, 31, c.vs.shape, generator=g).float().cuda()).bfloat16()
+        for s in (c.ks, c.vs):
+            s[torch.rand(s.shape, generator=g).cuda() < 0.2] = 0.0
+        q = randn(2, 8 * D, seed=33)
+        want = fl.attention_decode_window(q, *c.args(), **c.scales())
+        check_decode(q, c, want)
+        for s in (c.ks, c.vs):
+            s[s == 0] = -0.0
+        assert torch.equal(fl.attention_decode_window(q, *c.args(), **c.scales()), want)
