@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_int4_kernel(const
     pos = at > INT32_MAX ? -1 : static_cast<int>(max(at, -1ll));
   }
   if (pos < 0) return;
-  const int pi = p.page_of(pos), slot = pos - pi * p.page_size;
+  const int pi = p.page_of(pos);
+  const long long slot = pos - pi * p.page_size;  // its bytes may pass 32 bits
   if (pi >= p.max_pages) return;
   const int page = p.table[b * p.ldt + pi];
   if (page < 0 || page >= p.num_pages) return;

@@ -4,9 +4,9 @@ import pytest
 import torch
 
 import gemm_epilogue_tcgen05_gb300 as fl
-from attention_utils import BF16, D, assert_within
+from attention_utils import BF16, D, assert_within, cu
 from test_attention_window_gpu import STEP, check_decode, randn
-from window_utils import AnyCache, attend_window
+from window_utils import AnyCache, attend_window, quantise_int4, values_int4
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +137,29 @@ def test_scales_of_minus_zero_are_zeros():
         for s in (c.ks, c.vs):
             s[s == 0] = -0.0
         assert torch.equal(fl.attention_decode_window(q, *c.args(), **c.scales()), want)
+
+
+# ---------------------------------------------------------------- pages of many tokens
+@pytest.mark.parametrize("last", [1, 6])
+def test_a_page_whose_bytes_pass_32_bits(last):
+    """One page of 2^25 tokens and some more: rows behind 2^31 bytes of codes come back, are attended to, and nothing else is written."""
+    page, n = (1 << 25) + 64, 9
+    k, v = (torch.zeros(1, 1, page, D // 2, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(1, 1, page, 4, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    seq_lens = torch.tensor([page - last], dtype=torch.int32, device="cuda")
+    y, z = randn(n, D, seed=41), randn(n, D, seed=42)
+    fl.paged_kv_append_int4(y, z, k, v, ks, vs, table, seq_lens, cu_seqlens=cu([n]))
+    scales = dict(k_page_scale=ks, v_page_scale=vs)
+    back = fl.paged_kv_read(k, v, table, seq_lens, cu_seqlens=cu([n]), rows=n, **scales)
+    end = page - last
+    for out, x, codes, s in zip(back, (y, z), (k, v), (ks, vs)):
+        want, ws = quantise_int4(x)
+        assert torch.equal(out.double(), values_int4(want, ws))
+        assert torch.equal(codes[0, 0, end - n:end], want) and torch.equal(s[0, 0, end - n:end], ws)
+        assert not codes[0, 0, :end - n].any() and not codes[0, 0, end:].any() and not s[0, 0, :end - n].any()
+    q = randn(1, 2 * D, seed=43)
+    out = fl.attention_decode_window(q, k, v, table, seq_lens, window=n, **scales)
+    ref, tol = attend_window(q.double().view(2, 1, D), *(t.double()[None] for t in back), D ** -0.5, 0, 0, STEP["int4"],
+                             scales=[s[0, 0, end - n:end].double().repeat_interleave(32, -1)[None] for s in (ks, vs)])
+    assert_within(out.view(2, 1, D), ref, tol, "decode")
