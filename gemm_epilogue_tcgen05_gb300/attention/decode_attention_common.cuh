@@ -18,6 +18,7 @@ namespace fl {
 
 constexpr int kDecMaxCtas = 640;
 constexpr int kDecPartFloats = 16 * (kHeadDim + 4);  // o[16][128], then (m, m', l, 0) of up to 16 heads
+constexpr long long kDecLongest = 0x7FFFFC00;  // tokens of a sequence: a warp looks up to 1000 ahead of the last one, in 32 bits
 constexpr float kDecNone = -3e38f;             // a maximum over nothing: any finite logit passes it
 constexpr float kDecLazy = 8.f;
 constexpr float kDecLift = 7.f;                // E4M3 and 4 bits: weights are lifted by 2^7 in fp16
@@ -83,10 +84,10 @@ struct DecodeWalk {
   static constexpr int kOver = OVER;
   const DecodeParams& p;
   const int heads_v;         // independent (kv head, chunk) pairs of a sequence
-  const long long capacity;  // tokens that the table has room for
+  const long long capacity;  // tokens that the table has room for, kDecLongest at most
 
   __device__ __forceinline__ explicit DecodeWalk(const DecodeParams& p)
-      : p(p), heads_v(p.c.n_kv * p.chunks), capacity(static_cast<long long>(p.c.max_pages) * p.c.page_size) {}
+      : p(p), heads_v(p.c.n_kv * p.chunks), capacity(min(static_cast<long long>(p.c.max_pages) * p.c.page_size, kDecLongest)) {}
   // Units of a sequence, and where its virtual tokens jump.
   __device__ __forceinline__ int span(int len, bool& bad, int& jump_at, int& jump) const {
     bad = len < 0 || len > capacity;

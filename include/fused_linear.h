@@ -339,7 +339,7 @@ FL_API int paged_kv_append(const void* K, const void* V, const float* k_scale, c
  * query head h reading kv head h / (n_heads / n_kv_heads).  Q, O [batch, n_heads*128] bf16 (Q already
  * rotated); n_heads a multiple of n_kv_heads; scale > 0, and finite times log2 e.  Sums and the softmax's
  * state are fp32.
- * A sequence of length 0 gets zeros.  A negative length, one beyond max_pages * page_size, or a page
+ * A sequence of length 0 gets zeros.  A negative length, one beyond max_pages * page_size or 2^31 - 1024, or a page
  * outside [0, num_pages) among the entries in use: the sequence's rows are NaN and
  * fl_check_device_status(workspace) returns FL_ERR_INVALID_ARG once.  Nothing behind a sequence's
  * length is read into the result, whatever it holds.

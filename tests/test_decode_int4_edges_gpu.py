@@ -5,7 +5,7 @@ import torch
 
 import gemm_epilogue_tcgen05_gb300 as fl
 from attention_utils import BF16, D, assert_within, cu
-from test_attention_window_gpu import STEP, check_decode, randn
+from test_attention_window_gpu import KINDS, STEP, check_decode, randn
 from window_utils import AnyCache, attend_window, quantise_int4, values_int4
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +163,45 @@ def test_a_page_whose_bytes_pass_32_bits(last):
     ref, tol = attend_window(q.double().view(2, 1, D), *(t.double()[None] for t in back), D ** -0.5, 0, 0, STEP["int4"],
                              scales=[s[0, 0, end - n:end].double().repeat_interleave(32, -1)[None] for s in (ks, vs)])
     assert_within(out.view(2, 1, D), ref, tol, "decode")
+
+
+# ---------------------------------------------------------------- lengths up to 2^31
+@pytest.mark.parametrize("kind", KINDS)
+def test_lengths_next_to_the_end_of_32_bits(kind):
+    """A table with room for 2^31 tokens (its entries are all one page): up to 2^31 - 1024 of them a sequence is served, longer
+    ones are refused like those that pass the table."""
+    page, window, sinks, longest = 1 << 20, 100, 5, (1 << 31) - 1024
+    lens = [longest, (1 << 31) - 1, 300, longest + 1]
+    small = AnyCache([window + sinks, 300], 2, 400, kind, seed=51)  # the tokens that are seen, of sequence 0 and of sequence 2
+
+    def paged(x):
+        if x is None:
+            return None
+        big = torch.zeros((1, x.shape[1], page) + x.shape[3:], dtype=x.dtype, device="cuda")
+        first, second = (x[small.table[b, 0].long()] for b in (0, 1))
+        big[0, :, :300] = second[:, :300]
+        end = longest % page
+        big[0, :, end - window:end] = first[:, sinks:sinks + window]
+        return big
+
+    k, v, ks, vs = (paged(x) for x in (small.k, small.v, small.ks, small.vs))
+    for x, y in ((small.k, k), (small.v, v), (small.ks, ks), (small.vs, vs)):
+        if x is not None:
+            x[small.table[0, 0].long(), :, :sinks] = y[0, :, :sinks]  # the sinks are the other sequence's first tokens
+    table = torch.zeros(4, 2048, dtype=torch.int32, device="cuda")
+    seq_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = randn(4, 8 * D, seed=52)
+    ws = fl.attention_decode_workspace()
+    scales = dict(k_page_scale=ks, v_page_scale=vs)
+    out = fl.attention_decode_window(q, k, v, table, seq_lens, window=window, sinks=sinks, workspace=ws, **scales)
+    assert fl.check_device_status(ws) == fl.FL_ERR_INVALID_ARG
+    assert torch.isnan(out[[1, 3]]).all()
+    check_decode(q[[0, 2]], small, out[[0, 2]], window + sinks, 0, what="sequence 0 with its tokens side by side", skip=(1,))
+    check_decode(q[[0, 2]], small, out[[0, 2]], window, sinks, skip=(0,))
+    if kind != "int4":
+        out = fl.attention_decode(q[1:3], k, v, table[1:3], seq_lens[1:3], workspace=ws, **scales)
+    else:
+        out = fl.attention_decode_window(q[1:3], k, v, table[1:3], seq_lens[1:3], workspace=ws, **scales)
+    assert fl.check_device_status(ws) == fl.FL_ERR_INVALID_ARG
+    assert torch.isnan(out[0]).all()
+    check_decode(q[1:3], small, out, skip=(0,))
