@@ -1028,7 +1028,8 @@ def attention_prefill_window(Q, K, V, cu_seqlens=None, cu_seqlens_k=None, seq_le
     if not (0 <= window <= _LONGEST and 0 <= sinks <= _LONGEST):
         window, sinks = _span(window, "window"), _span(sinks, "sinks")
     scratch, space = None, 0
-    if cu_seqlens_k is not None and M * width <= _FEW_ROWS and rows > 1536:  # few units over many keys: cut along these, perhaps
+    if cu_seqlens_k is not None and M * width <= _FEW_ROWS and rows > 1536 and rows >= 500 * (batch + 1):
+        # few units over many keys: cut along these, perhaps
         space = load().fl_attention_prefill_window_scratch_bytes(M, rows, batch, width // HEAD_DIM, n_kv, window, sinks)
         if space and stream is None:  # memory of this call's own, on its stream
             scratch = torch.empty(space, dtype=_U8, device=Q.device)

@@ -55,9 +55,17 @@ long long packed_blocks(int M, int batch, long long per_cta) {
 // Parts that each unit may be cut into where few units go over many keys, 1: none.  A part costs a unit's output, 128 KB into the
 // scratch buffer and out of it, and a second kernel joins them, so they pay where SMs would be idle and units be long.  Measured,
 // whole units -> parts, 32/8 heads, bf16: 33 tokens behind 5000 58.1 -> 24.8 us, 128 behind 8000 92.9 -> 35.5, 512 behind 8000 96.7
-// -> 62.1, 16 behind 1500 (two parts) 20.9 -> 18.1, which the second launch costs the host; E4M3, 33 behind 5000 70.1 -> 34.4; 144
-// units of up to 33 tiles, cut all the same, 55 -> 62.
-int parts_of_units(long long units, int M_k, int window, int sinks, long long per_cta, int num_sms) {
+// -> 62.1, 16 behind 1500 (two parts) 20.9 -> 18.1, which the second launch costs the host; E4M3, 33 behind 5000 70.1 -> 34.4.  From
+// half as many units as SMs on a part for each is none to spare: 576 behind 8000 93.8 -> 60.2, 577 stay whole with 94.9 (a batch
+// of 144 units of up to 33 tiles, all of them cut, 55 -> 62).
+// The lengths are on the device: of several sequences the longest is taken to be what it is where they are spread evenly from
+// none on, 2 M_k / (batch + 1), and where that is short nothing is cut, for the binding's pass and the kernel, 4 x 20 behind 480
+// tokens: 20.3 -> 10.8 us, 13.0 -> 10.5 (16/2 heads, 16 x 20 behind 480: 19.8 -> 11.6, 13.8 -> 11.2).  Above, what even
+// lengths lose, 4 x 20 behind 980 16.2 -> 20.2, 15.8 -> 17.0, is less than what uneven ones gain, 60, 60, 60 and 3000 keys: 37.1 ->
+// 23.6, 36.9 -> 23.3, fifteen times 250 and once 6000: 67.2 -> 34.6, 66.8 -> 34.3.
+constexpr int kCutKeys = 1000;
+int parts_of_units(long long units, int M_k, int batch, int window, int sinks, long long per_cta, int num_sms) {
+  if (2ll * M_k < kCutKeys * (batch + 1ll)) return 1;
   long long keys = M_k;
   if (window > 0) keys = std::min(keys, static_cast<long long>(window) + sinks + 61 + per_cta);
   const long long longest = (keys - 1) / kPreTile / kPrePartTiles + 1;
@@ -80,7 +88,7 @@ extern "C" size_t fl_attention_prefill_window_scratch_bytes(int M, int M_k, int 
     return 0;
   const int hp = heads_of_tile(n_heads / n_kv_heads);
   const long long per_cta = 2 * (kPreTile / hp), units = packed_blocks(M, batch, per_cta) * (n_heads / hp);
-  const int parts = parts_of_units(units, M_k, window, sinks, per_cta, di.num_sms);
+  const int parts = parts_of_units(units, M_k, batch, window, sinks, per_cta, di.num_sms);
   return parts > 1 ? scratch_of(units * parts) : 0;
 }
 
@@ -191,7 +199,7 @@ int enqueue_prefill(const void* Q, const void* K, const void* V, const float* k_
   p.timeout_ns = wait_timeout_ns();
   const bool windowed = p.window > 0 || cu_seqlens_k != nullptr;
   const long long units = blocks * p.pairs;
-  const int most_parts = cu_seqlens_k == nullptr ? 1 : parts_of_units(units, M_k, p.window, p.sinks, per_cta, di.num_sms);
+  const int most_parts = cu_seqlens_k == nullptr ? 1 : parts_of_units(units, M_k, batch, p.window, p.sinks, per_cta, di.num_sms);
   const bool cut = most_parts > 1 && scratch != nullptr && scratch_bytes >= scratch_of(units * most_parts);
   if (cut) {
     p.flat = 1;
