@@ -144,16 +144,11 @@ __device__ __forceinline__ int sequence_of_row(const int* cu, int batch, int r, 
   }
   return lo < batch ? lo : -1;
 }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
-  uint32_t h;
-  asm("{\n\t.reg .b32 t;\n\tcvt.rn.f16x2.e4m3x2 t, %1;\n\tmov.b32 %0, t;\n\t}" : "=r"(h) : "h"(static_cast<uint16_t>(code)));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

@@ -57,7 +57,7 @@ struct DecodeInt4Traits {
   static constexpr int kTile = kUnit * kRowBytes, kScales = kUnit * kScaleBytes;
   static constexpr int kStage = 2 * (kTile + kScales);  // K, V, K's scales, V's
   static_assert(kStage % 512 == 0, "the swizzle's pattern");
-  static_assert(kWarps >= kInt4Groups, "a warp prepares a group of the queries");
+  static_assert(kWarps == kInt4Groups, "a warp prepares a group of the queries");
   // A warp's tables: parts of V's scales as fp16, [group][q][pairs of tokens 2 q + 8 j]; K's scales and the power of V's, each
   // twice, [group or power][g][tokens g + 8 r].  Its piece of a segment's result comes to the same place.
   static constexpr int kParts = kInt4Groups * kStep * 2, kPairs = kStep * 8, kTables = kParts + (kInt4Groups + 1) * kPairs;
@@ -144,11 +144,6 @@ __device__ __forceinline__ float int4_part(uint32_t bits, int field) {
   const float down = __uint_as_float(static_cast<uint32_t>(253 - min(field, 252)) << 23);
   const float more = field > 252 ? (field == 253 ? 0.5f : 0.25f) : 1.f;
   return bits < 0x7F80u ? __uint_as_float(bits << 16) * down * more : 0.f;
-}
-__device__ __forceinline__ float power_of(uint64_t twice) {
-  float a, b;
-  f2_split(twice, a, b);
-  return a;
 }
 
 template <bool WIN>
@@ -348,9 +343,8 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
       }
       sum += __shfl_xor_sync(~0u, sum, 1);
       sum += __shfl_xor_sync(~0u, sum, 2);
-      if (warp < kInt4Groups)
-        *reinterpret_cast<uint4*>(query + (warp * 32 + lane) * 16) = make_uint4(two[0], two[1], two[2], two[3]);
-      if (warp < kInt4Groups && q == 0) reinterpret_cast<float*>(query + kInt4Groups * 512)[warp * 8 + g] = sum * (-8.f / kDecCode);
+      *reinterpret_cast<uint4*>(query + (warp * 32 + lane) * 16) = make_uint4(two[0], two[1], two[2], two[3]);
+      if (q == 0) reinterpret_cast<float*>(query + kInt4Groups * 512)[warp * 8 + g] = sum * (-8.f / kDecCode);
       // f times 2^24, as two factors the first of which neither overflows nor, where it matters, underflows
       const float f0 = f > 1.f ? kDecCode : f, f1 = f > 1.f ? f : kDecCode;
       // [q]: of heads 2q and 2q + 1 the first, then the second

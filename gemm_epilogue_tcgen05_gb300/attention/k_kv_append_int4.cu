@@ -7,11 +7,12 @@
 // group whose largest magnitude is below 2^-120 becomes zeros (no denormal number has to be dealt with, here or where
 // the cache is read), a group with a value that is not finite gets a NaN for s and zero codes.
 //
-// Both roundings are exact although no division is made.  a times fl(1/7) is a/7 itself where 7 divides a's
-// significand (fl(1/7) is 2^-26 off, less than half a step), else no closer than 2^-3 of a step to a border between
-// two values of s.  y / s has a denominator of at most 2 * 31 * 16 beside a power of two, so it is k + 1/2 exactly or
-// 2^-10 off: y times an approximate 1/s, plus 768, in one rounding is its nearest multiple of 2^-14, and the next addition
-// rounds that to a whole number.
+// Both roundings are exact although no division is made.  a / 7 is half way between two five-bit numbers only for significands
+// 231 and 245 (33 and 35 times 7; of the other multiples of 7 the quotients are five-bit numbers themselves), whose product
+// with fl(1/7) is the quotient exactly; else it is 1/14 of a step or more from there, and the product is off by 2^-18 of one at
+// most (fl(1/7) is off by 2^-24.4 of itself, its rounding 2^-24).  y / s has a denominator of at most 2 * 31 * 16 beside a power of
+// two, so it is k + 1/2 exactly or 2^-10 off: y times an approximate 1/s, plus 768, in one rounding is its nearest multiple of 2^-14,
+// and the next addition rounds that to a whole number.
 //
 // Bound by memory: 512 bytes in and 144 out for each head of a token.  One warp moves a row, all its heads, as in
 // paged_kv_append; a lane takes 8 values, four lanes a group.  10075 rows of 8 heads: 13.1 us, 4.0 TB/s: a chain of loads (offsets,
