@@ -820,8 +820,8 @@ def paged_kv_read(k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, rows=
 
     Rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 are the last of the first seq_lens[b] tokens of sequence b; without
     cu_seqlens row b is the last one.  rows: how many to allocate where K and V are not given and cu_seqlens is (rows
-    in no sequence are zeros then; of given tensors they stay as they were).  A row whose position or page is outside
-    the table or the cache is NaN."""
+    in no sequence are zeros then, which takes longer than the call itself; of given tensors they stay as they were).
+    A row whose position or page is outside the table or the cache is NaN."""
     if (K is None) != (V is None):
         raise ValueError("K and V: expected both or neither")
     if stream is not None and K is None:  # what is made here belongs to that stream, too

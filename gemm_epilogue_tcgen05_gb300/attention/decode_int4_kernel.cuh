@@ -4,8 +4,8 @@
 //
 // What bounds it: the cache is read once, 144 bytes for a token and kv head, at the memory's rate if the instructions for
 // these 256 codes are few enough: a logic instruction takes two cycles of a scheduler, and an SM has some 25 cycles of each
-// of its four for a token and head.  64 sequences of 2048-8192 tokens, 32/8 heads: 81 us, 4450 GB/s; some 345 instructions for
-// 16 tokens and a head, 0.55 of them in a cycle of a scheduler.
+// of its four for a token and head.  64 sequences of 2048-8192 tokens, 32/8 heads: 81 us, 4440 GB/s; some 350 instructions for
+// 16 tokens and a head, 0.53 of them in a cycle of a scheduler.
 //
 // Codes.  A code xor 8, u = code + 8, is an fp16 number u 2^-24 (a denormal one) as it stands in the low bits of a half, and
 // 16 u 2^-24 four bits further up: one logic instruction gives two, and the factor 16 lies in the query's fragments for K, in

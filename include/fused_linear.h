@@ -390,7 +390,8 @@ FL_API size_t fl_attention_prefill_workspace_bytes(int M, int n_kv_heads, int kv
  *                      [n_kv_heads][page_size][4] bf16, one scale for 32 consecutive columns; 8-byte
  *                      aligned, scale_pitch a multiple of 4.
  * An entry stands for code * scale.  Scales that paged_kv_append_int4 writes have five significant bits,
- * so that each entry is a bf16 number; the readers take any bf16 that is not below zero (-0 is a zero). */
+ * so that each entry is a bf16 number; the readers take any bf16 that is not below zero (-0 is a zero).
+ * Pages one behind the other (page_pitch n_kv_heads * page_size * 64) of a multiple of 32 tokens stream best. */
 
 /* bf16 rows of keys and values into a 4-bit cache; rows, offsets, lengths and what is ignored are those of
  * paged_kv_append.  For 32 consecutive columns y of a head with a = max|y|:
