@@ -588,7 +588,8 @@ __global__ void __launch_bounds__(DecodeInt4Traits::kThreads, DecodeInt4Traits::
     if (spoiled && lane == 0 && atomicCAS(p.status + ST_CODE, 0, static_cast<int>(FL_ERR_INVALID_ARG)) == 0)
       p.status[ST_DETAIL] = seg.b;
     const uint32_t no_number = __reduce_or_sync(~0u, said);  // bits 0-3
-    // o[t][i] with t = 2 group + odd: head 2q + (i & 1), dimension 32 group + 4 g + odd + 2 (i >> 1), odd ones times 16.  Chunks of 4 dimensions, permuted by 2 q against bank conflicts.
+    // o[t][i] with t = 2 group + odd: head 2q + (i & 1), dimension 32 group + 4 g + odd + 2 (i >> 1), odd ones times 16.  Chunks of
+    // 4 dimensions, permuted by 2 q against bank conflicts.
     {
       float sums[2];
       f2_split(l, sums[0], sums[1]);
